@@ -355,11 +355,11 @@ def _select(s):
     has, parent = parents >= 0, parents.clamp(min=0)
     j = torch.arange(wide, device="cuda")
     length = torch.where(has, lengths[parent], 0)
-    earlier = torch.tril(parents[:, None] == parents[None, :], diagonal=-1).any(1)
     old, total = (length + page - 1) // page, (length + s["grow"] + page - 1) // page
+    fits = total <= wide
+    earlier = torch.tril((parents[:, None] == parents[None, :]) & fits, diagonal=-1).any(1)
     split = has & earlier & (length % page != 0)  # a later child of a page in progress gets a copy of it
     keep = old - split.long()
-    fits = total <= wide
     need = torch.where(fits, total - keep, 0)
     base = torch.cumsum(need, 0) - need
     # pages that nothing holds once the old rows are gone and the new ones hold what they keep
