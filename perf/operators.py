@@ -334,7 +334,7 @@ def _attend(s):
     p = torch.exp(scores - top)
     total = p.sum(-1, keepdim=True)
     o = torch.matmul(p, torch.where(seen[:, :, None, None], v, 0.0).transpose(1, 2))
-    o = torch.where(total > 0, o / total, 0.0)
+    o = torch.where(total == 0, 0.0, o / total)
     lse = (top + torch.log(total)).reshape(rows, -1)
     return {"out": o.reshape(rows, -1, dim).to(s["q"].dtype), "lse": lse}
 
