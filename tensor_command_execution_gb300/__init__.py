@@ -469,3 +469,9 @@ def command_from_spec(spec: dict):
 
 def spec_scalars(spec: dict, tags: dict) -> dict:
     return {tags[op[1]]: op[3] for op in spec["ops"] if op[0] == "scalar"}
+
+
+# ---- operators of a paged key-value cache (include/cmd_cache.h) ------------------
+
+from .cache import (attention_decode, attention_workspace, cache_append, cache_compact, cache_select,  # noqa: E402
+                    cache_status, rope, rope_backward, rope_turns)

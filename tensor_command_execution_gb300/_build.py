@@ -41,9 +41,11 @@ CU_SOURCES = [("exec_tile2d.cu", _objs((2,), (0, 1))), ("exec_generic.cu", _objs
               ("exec_contig.cu", [dict(CMDX_TIER=1, CMDX_EXT=0, CMDX_HALF16=1)]),
               ("exec_tile2d.cu", _objs((1, 0), (0, 1))),
               ("exec_generic.cu", _objs((4, 3, 1, 0))), ("exec_contig.cu", _objs((4, 3, 1, 0))),
-              ("static_scratch.cu", [{}])]
-CPP_SOURCES = ["cmd_api.cpp", "cmd_yaml.cpp", "exec_host.cpp"]
-HEADERS = ["cmd_internal.h", "exec_common.cuh", "exec_pipe.cuh", "exec_tile2d.h", "interp_asm.cuh", "gen_interp.py"]
+              ("static_scratch.cu", [{}]),
+              ("cache_attend.cu", [{}]), ("cache_rope.cu", [{}]), ("cache_pages.cu", [{}])]
+CPP_SOURCES = ["cmd_api.cpp", "cmd_yaml.cpp", "exec_host.cpp", "cache_api.cpp"]
+HEADERS = ["cmd_internal.h", "exec_common.cuh", "exec_launch.cuh", "exec_pipe.cuh", "exec_tile2d.h", "interp_asm.cuh",
+           "gen_interp.py", "cache_internal.h", "cache_common.cuh", "cache_attend.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -59,7 +61,7 @@ def cuda_home() -> str:
 
 def _sources():
     return ([os.path.join(CSRC, s) for s in sorted({c for c, _ in CU_SOURCES}) + CPP_SOURCES + HEADERS]
-            + [os.path.join(ROOT, "include", "cmd.h"), os.path.abspath(__file__)])
+            + [os.path.join(ROOT, "include", h) for h in ("cmd.h", "cmd_cache.h")] + [os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:

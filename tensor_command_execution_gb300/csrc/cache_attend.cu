@@ -1,0 +1,219 @@
+// cache_attend.cu - attention of one new token per sequence over a paged
+// cache, on the general-purpose units: 32-bit numbers, and 16-bit ones whose
+// rows are not 16-byte vectors (cache_attend_mma.cu takes the others).
+//
+// out = sum_t exp(s_t - lse) v_t, s_t = scale q . k_t, one pass over the
+// tokens with a running maximum. Bound by memory: each key and value is read
+// once for all query heads that share it. A warp takes kStep tokens at a
+// time, a lane VEC elements of the head dim, straight from memory to
+// registers; the kStep * GT dot products (GT query heads) are summed over the
+// lanes by a transposing butterfly that leaves each lane one finished score
+// (31 shuffles for 32 scores rather than 5 each), where scaling, the cap, the
+// mask and the exponential are then done once.
+#include "cache_attend.cuh"
+
+namespace cmdx {
+
+namespace {
+
+constexpr int kWarps = 8;
+
+// VEC elements of a row for this lane (element 4 lane + 128 j + i for VEC 4
+// and 8, 2 lane + i for VEC 2), zero past dim.
+template <class T, int VEC>
+__device__ __forceinline__ int lane_element(int lane, int i) {
+  return VEC == 2 ? 2 * lane + i : (i / 4) * 128 + 4 * lane + i % 4;
+}
+template <class T, int VEC>
+__device__ __forceinline__ void load_row(float (&x)[VEC], const T* row, int lane, int dim, bool vec) {
+  constexpr int W = VEC == 2 ? 2 : 4;
+#pragma unroll
+  for (int i = 0; i < VEC; i += W) {
+    const int e = lane_element<T, VEC>(lane, i);
+    if (vec && e + W <= dim) {
+      struct alignas(W * sizeof(T)) Pack { T v[W]; };
+      const Pack t = *reinterpret_cast<const Pack*>(row + e);
+#pragma unroll
+      for (int j = 0; j < W; ++j) x[i + j] = to_float(t.v[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < W; ++j) x[i + j] = e + j < dim ? to_float(row[e + j]) : 0.0f;
+    }
+  }
+}
+
+template <class T, int GT, int VEC>
+__global__ void __launch_bounds__(kWarps * 32) attend_simt_kernel(const __grid_constant__ AttendParams p) {
+  constexpr int kStep = VEC == 8 && GT == 8 ? 2 : 4;  // tokens at once
+  constexpr int NV = kStep * GT;
+  constexpr int kDup = 32 / NV;  // lanes that end up with the same score
+  constexpr int kPitch = 32 * VEC + 2;
+  extern __shared__ __align__(16) unsigned char s_mem[];
+  AttendSpan& s_span = *reinterpret_cast<AttendSpan*>(s_mem);
+  float(*s_state)[GT][kPitch] = reinterpret_cast<float(*)[GT][kPitch]>(s_mem + sizeof(AttendSpan));
+  __shared__ int s_last;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int hw = p.heads_per_cta, phases = kWarps / hw;
+  const int tile = kAttendTile * phases;
+  pdl_wait();
+  pdl_trigger();
+  attend_spans(p, s_span, tile);
+  attend_empty_rows<T>(p, s_span);
+  const AttendShare share = attend_share(p, s_span);
+  const T* kp = static_cast<const T*>(p.k);
+  const T* vp = static_cast<const T*>(p.v);
+  for (int64_t u = share.begin; u < share.end;) {
+    const AttendSegment g = attend_segment(p, s_span, share, u, tile);
+    const int head = g.head0 + warp % hw, phase = warp / hw;
+    const int gh = min(p.block_heads, p.group - g.qblock * p.block_heads);
+    float q[GT][VEC], o[GT][VEC];
+#pragma unroll
+    for (int h = 0; h < GT; ++h) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) q[h][i] = o[h][i] = 0.0f;
+      if (h < gh) {
+        const T* row = static_cast<const T*>(p.q) + g.row * p.q_st[0] +
+                       (head * p.group + g.qblock * p.block_heads + h) * p.q_st[1];
+        load_row<T, VEC>(q[h], row, lane, p.dim, false);
+      }
+    }
+    // this lane's score is that of token lane / kDup / GT and head lane / kDup % GT of a step
+    const int my_token = lane / kDup / GT;
+    float m = -CUDART_INF_F, l = 0.0f;
+    for (int i = 0; i < g.tiles; ++i) {
+      const int t0 = (g.tile0 + i) * tile + phase * kAttendTile;
+      for (int t = max(t0, g.lo / kStep * kStep); t < min(t0 + kAttendTile, g.n); t += kStep) {
+        float k[kStep][VEC], v[kStep][VEC];
+        bool bad = false;
+        bool seen[kStep];
+#pragma unroll
+        for (int j = 0; j < kStep; ++j) {
+          const int token = t + j;
+          seen[j] = token >= g.lo && token < g.n;
+          const uint32_t column = fast_div32(p.page, (uint32_t)token);
+          int page = 0;
+          if (seen[j]) {
+            page = p.tables[g.row * p.table_st[0] + column * p.table_st[1]];
+            if (page < 0 || page >= p.n_pages) {
+              seen[j] = false;
+              bad = true;
+            }
+          }
+          if (seen[j]) {
+            const int64_t in_page = token - (int64_t)column * p.page.d;
+            load_row<T, VEC>(k[j], kp + page * p.k_st[0] + in_page * p.k_st[1] + head * p.k_st[2], lane, p.dim, p.vec);
+            load_row<T, VEC>(v[j], vp + page * p.v_st[0] + in_page * p.v_st[1] + head * p.v_st[2], lane, p.dim, p.vec);
+          } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) k[j][e] = v[j][e] = 0.0f;
+          }
+        }
+        if (bad && lane == 0) report(p.status, CMD_CACHE_BAD_PAGE);
+        float s[NV];
+#pragma unroll
+        for (int j = 0; j < kStep; ++j)
+#pragma unroll
+          for (int h = 0; h < GT; ++h) {
+            float x = q[h][0] * k[j][0];
+#pragma unroll
+            for (int e = 1; e < VEC; ++e) x = fmaf(q[h][e], k[j][e], x);
+            s[j * GT + h] = x;
+          }
+        // after each round a lane keeps half of its sums, the upper half
+        // where its bit of the round is set
+        int n = NV;
+#pragma unroll
+        for (int b = 16; b > 0; b >>= 1) {
+          if (n > 1) {
+            n >>= 1;
+            const bool upper = lane & b;
+#pragma unroll
+            for (int e = 0; e < NV / 2; ++e)
+              if (e < n) {
+                const float give = upper ? s[e] : s[e + n], keep = upper ? s[e + n] : s[e];
+                s[e] = keep + __shfl_xor_sync(~0u, give, b);
+              }
+          } else {
+            s[0] += __shfl_xor_sync(~0u, s[0], b);
+          }
+        }
+        bool mine = seen[0];
+#pragma unroll
+        for (int j = 1; j < kStep; ++j) mine = my_token == j ? seen[j] : mine;
+        const float score = mine ? attend_score(p, s[0]) : -CUDART_INF_F;
+        float top = score;  // over the step's tokens: the lane bits above a head's
+#pragma unroll
+        for (int b = kDup * GT; b < 32; b <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, b));
+        const float up = fmaxf(m, top);
+        if (__any_sync(~0u, up != m)) {
+          const float c = m == -CUDART_INF_F ? 0.0f : exp2f(m - up);
+          l *= c;
+          m = up;
+#pragma unroll
+          for (int h = 0; h < GT; ++h) {
+            const float ch = __shfl_sync(~0u, c, h * kDup);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) o[h][e] *= ch;
+          }
+        }
+        const float w = score == -CUDART_INF_F ? 0.0f : exp2f(score - m);
+        l += w;
+#pragma unroll
+        for (int j = 0; j < kStep; ++j)
+#pragma unroll
+          for (int h = 0; h < GT; ++h) {
+            const float x = __shfl_sync(~0u, w, (j * GT + h) * kDup);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) o[h][e] = fmaf(x, v[j][e], o[h][e]);
+          }
+      }
+    }
+#pragma unroll
+    for (int b = kDup * GT; b < 32; b <<= 1) l += __shfl_xor_sync(~0u, l, b);
+#pragma unroll
+    for (int h = 0; h < GT; ++h) {
+      if (lane == h * kDup) {
+        s_state[warp][h][0] = m;
+        s_state[warp][h][1] = l;
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) s_state[warp][h][2 + lane_element<T, VEC>(lane, e)] = o[h][e];
+    }
+    attend_finish<T>(p, share, g, &s_state[0][0][0], GT * kPitch, kPitch, &s_last);
+    u += g.tiles;
+  }
+}
+
+template <class T, int GT, int VEC>
+cudaError_t launch(const AttendParams& p, cudaStream_t stream) {
+  constexpr int smem = sizeof(AttendSpan) + kWarps * GT * (32 * VEC + 2) * (int)sizeof(float);
+  static DeviceCache ready;  // (static storage: zero before first use)
+  const cudaError_t e = allow_smem(attend_simt_kernel<T, GT, VEC>, smem, ready);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attend_simt_kernel<T, GT, VEC>, p.max_ctas, kWarps * 32, smem, stream, p);
+}
+
+template <class T, int GT>
+cudaError_t launch_dim(const AttendParams& p, cudaStream_t stream) {
+  if (p.dim <= 64) return launch<T, GT, 2>(p, stream);
+  return p.dim <= 128 ? launch<T, GT, 4>(p, stream) : launch<T, GT, 8>(p, stream);
+}
+
+template <class T>
+cudaError_t launch_type(const AttendParams& p, cudaStream_t stream) {
+  if (p.block_heads == 1) return launch_dim<T, 1>(p, stream);
+  return p.block_heads <= 4 ? launch_dim<T, 4>(p, stream) : launch_dim<T, 8>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t attend_simt_launch(int dtype, const AttendParams& p, cudaStream_t stream) {
+  switch (dtype) {
+    case CMD_F32: return launch_type<float>(p, stream);
+    case CMD_F16: return launch_type<__half>(p, stream);
+    case CMD_BF16: return launch_type<__nv_bfloat16>(p, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace cmdx

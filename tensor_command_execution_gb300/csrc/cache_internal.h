@@ -1,0 +1,123 @@
+// cache_internal.h - launch parameters of the cache operators' kernels, shared
+// by their host side (cache_api.cpp) and the CUDA sources (cache_*.cu). Not
+// public.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "../../include/cmd_cache.h"
+
+namespace cmdx {
+
+// Unsigned 32-bit division by an invariant divisor with a multiply-high
+// (Granlund and Montgomery, PLDI 1994, section 4, as FastDiv in
+// cmd_internal.h): l = 0 marks a divisor of 1.
+struct FastDiv32 {
+  uint32_t m, l, d;
+};
+
+// ---- rotation and append (cache_rope.cu) --------------------------------------
+// What a tensor of the launch is: rotated or copied, into a tensor or into a
+// cache's pages.
+struct RopeStream {
+  const void* in;
+  void* out;           // a tensor's first element, or the pool's
+  int64_t in_st[3];    // batch, token, head strides (elements)
+  int64_t out_st[3];   // the same of a tensor; page, slot, head of a pool
+  int32_t heads;
+  uint8_t rotate, cache;
+};
+
+struct RopeParams {
+  RopeStream s[3];
+  int32_t n_streams;
+  int32_t heads;       // of all streams together
+  const int32_t* positions;
+  int64_t pos_st[2];   // batch, token
+  const uint64_t* turns;
+  int32_t n_pairs;
+  int32_t dim;
+  float scale, sine_scale;  // of the cosine; of the sine (negative: backward)
+  int64_t tokens;      // per batch
+  int32_t batch;
+  // the cache (append)
+  const int32_t* tables;
+  const int32_t* rows;
+  int64_t table_st[2], rows_st;
+  int32_t n_rows, columns, n_pages;  // (columns -1: no cache)
+  FastDiv32 page;
+  int32_t* status;
+};
+
+// vec: every row of every stream may be accessed in 16-byte vectors
+cudaError_t rope_launch(int dtype, int layout, bool vec, const RopeParams& p, cudaStream_t stream);
+
+// ---- attention of one token (cache_attend*.cu) --------------------------------
+constexpr int kAttendMaxCtas = 304;   // two for each of 152 SMs; bounds the workspace
+constexpr int kAttendRows = 2048;     // rows of one launch (the host splits larger calls)
+constexpr int kAttendHeads = 8;       // kv heads a CTA works on at once, at most
+constexpr int kAttendTile = 16;       // tokens a warp takes at a time
+
+struct AttendParams {
+  const void* q;
+  void* out;
+  float* lse;
+  const void* k;
+  const void* v;
+  const int32_t* tables;
+  const int32_t* lengths;
+  int64_t q_st[2], out_st[2], lse_st[2];  // row, head
+  int64_t k_st[3], v_st[3];               // page, slot, head
+  int64_t table_st[2], len_st;
+  int32_t rows, kv_heads, group, dim;
+  int32_t n_pages, columns;
+  FastDiv32 page;
+  float scale_log2;    // scale * log2 e: scores are kept in powers of two
+  float cap_in, cap_out;  // scale / softcap, softcap * log2 e (cap_out 0: none)
+  int32_t window;
+  int32_t heads_per_cta;  // kv heads a CTA works on at once (divides kv_heads and the warps)
+  int32_t blocks;      // blocks of query heads of one kv head
+  int32_t block_heads; // query heads of a block (the last may have fewer)
+  int32_t max_ctas;
+  float* parts;        // partial results, [2 max_ctas][heads_per_cta * block_heads][dim + 2]
+  int32_t* arrived;    // [rows][head groups]: parts written so far, 0 between launches
+  int32_t* status;
+  uint8_t q_pairs;     // q rows may be read two 16-bit elements at a time
+  uint8_t vec;         // cache rows may be read in vectors
+};
+
+cudaError_t attend_simt_launch(int dtype, const AttendParams& p, cudaStream_t stream);
+
+// ---- pages (cache_pages.cu) -----------------------------------------------------
+struct PoolList {
+  uint8_t* ptr[CMD_CACHE_MAX_POOLS];
+  int64_t stride[CMD_CACHE_MAX_POOLS];
+  int64_t bytes[CMD_CACHE_MAX_POOLS];
+  int32_t n;
+  int32_t unit;        // bytes of one access: every address and size is a multiple of it
+};
+
+struct SelectParams {
+  const int32_t *tables, *lengths, *refs, *parents, *grow;
+  int32_t *tables_out, *lengths_out, *refs_out;
+  int64_t table_st, table_out_st;  // rows; a row's entries are dense
+  int32_t old_rows, new_rows, columns, pages, page_size;
+  int32_t *first, *children, *keep, *base, *free_list, *copy_src, *copy_dst, *head;  // workspace
+  int32_t* status;
+};
+
+struct CompactParams {
+  const int32_t *tables, *lengths, *refs;
+  int32_t *tables_out, *refs_out, *map_out;
+  int64_t table_st, table_out_st;
+  int32_t rows, columns, pages, page_size;
+  int32_t *holes, *movers, *head;  // workspace
+  int32_t* status;
+};
+
+cudaError_t select_launch(const SelectParams& p, const PoolList& pools, cudaStream_t stream);
+cudaError_t compact_launch(const CompactParams& p, const PoolList& pools, cudaStream_t stream);
+
+}  // namespace cmdx
