@@ -142,10 +142,10 @@ cmd_status cmd_cache_append(const cmd_append_args* args, void* cuda_stream);
  * hold there (infinities and NaN included).
  *
  * The work is split over the sequences' lengths in equal parts and joined
- * through workspace: cmd_attention_workspace bytes of device memory, 256-byte
- * aligned, zeroed once before its first use (every launch leaves the zeros
- * it needs) and used by one launch at a time (streams that overlap need one
- * each). Results do not depend on the timing of the parts. */
+ * through workspace: cmd_attention_workspace bytes of device memory, 16-byte
+ * aligned, of any contents, used by one call at a time (streams that overlap
+ * need one each). Results do not depend on the timing of the parts. A 16-bit
+ * value of infinity inside a row makes its element of out NaN or infinite. */
 typedef struct cmd_attention_args {
   cmd_operand q, out;           /* [rows, q_heads, dim], dim <= CMD_CACHE_MAX_DIM */
   cmd_operand lse;              /* optional: f32 [rows, q_heads] */

@@ -473,5 +473,5 @@ def spec_scalars(spec: dict, tags: dict) -> dict:
 
 # ---- operators of a paged key-value cache (include/cmd_cache.h) ------------------
 
-from .cache import (attention_decode, attention_workspace, cache_append, cache_compact, cache_select,  # noqa: E402
-                    cache_status, rope, rope_backward, rope_turns)
+from .cache import (attention_decode, cache_append, cache_compact, cache_select, cache_status,  # noqa: E402
+                    rope, rope_backward, rope_turns)

@@ -215,31 +215,12 @@ def cmd_attention_workspace(q_heads: int, kv_heads: int, dim: int) -> int:
     return n.value
 
 
-def attention_workspace(q_heads: int, kv_heads: int, dim: int, device="cuda"):
-    """A zeroed workspace for attention_decode, for one launch at a time: for calls that are captured in a graph."""
-    import torch
-    return torch.zeros(cmd_attention_workspace(q_heads, kv_heads, dim), dtype=torch.uint8, device=device)
-
-
-_workspaces: dict = {}  # (device, stream, heads, dim) -> workspace of that stream's calls
-
-
-def _attention_workspace(s, q_heads, kv_heads, dim):
-    key = (s.device.index, s.handle, q_heads, kv_heads, dim)
-    w = _workspaces.get(key)
-    if w is None:
-        import torch
-        if torch.cuda.is_current_stream_capturing():
-            raise ValueError("a captured attention_decode needs a workspace of its own (see attention_workspace)")
-        w = _workspaces[key] = s.empty(cmd_attention_workspace(q_heads, kv_heads, dim), torch.uint8, zero=True)
-    return w
-
-
 def attention_decode(q, k_cache, v_cache, tables, lengths, *, scale: float | None = None, softcap: float = 0.0,
                      window: int = 0, out=None, lse=None, return_lse: bool = False, workspace=None, status=None,
                      stream=None):
     """Attention of one new token per row: q [rows, q_heads, dim] over the first lengths[r] tokens of row r. Returns
-    out, or (out, lse) with return_lse. scale: dim ** -0.5 unless given."""
+    out, or (out, lse) with return_lse. scale: dim ** -0.5 unless given. workspace: cmd_attention_workspace bytes
+    (allocated where None)."""
     s = _Stream(stream, q)
     if q.dim() != 3 or k_cache.dim() != 4:
         raise ValueError("q has rank 3 and the caches have rank 4")
@@ -250,8 +231,10 @@ def attention_decode(q, k_cache, v_cache, tables, lengths, *, scale: float | Non
         import torch
         lse = s.empty((rows, heads), torch.float32)
     kv = k_cache.shape[2]
-    if workspace is None and rows and heads and kv:
-        workspace = _attention_workspace(s, heads, kv, dim)
+    n = cmd_attention_workspace(heads, kv, dim) if rows and heads and kv and heads % kv == 0 else 0
+    if workspace is None and n:
+        import torch
+        workspace = s.empty(n, torch.uint8)
     w = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     args = _attention_args.pack(*_operand(q, "q"), *_operand(out, "out"), *_optional(lse, "lse"),
                                 *_operand(k_cache, "k_cache"), *_operand(v_cache, "v_cache"),

@@ -471,22 +471,20 @@ extern "C" cmd_status cmd_cache_append(const cmd_append_args* args, void* cuda_s
 
 namespace {
 
-// kv heads a CTA works on at once: the most of 8, 4, 2 that divides them.
-int heads_at_once(int64_t kv_heads, int most) {
-  for (int h = most; h > 1; h /= 2)
-    if (kv_heads % h == 0) return h;
-  return 1;
-}
-constexpr int kBlockHeads = 16;  // query heads of one block, at most
-
 int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
-int64_t counters_bytes(int64_t q_heads) { return round_up(cmdx::kAttendRows * q_heads * 4, 256); }
+void check_workspace(const void* ws, int64_t bytes, int64_t want) {
+  need(ws, CMD_ERR_NULL, "workspace is NULL");
+  need(reinterpret_cast<uintptr_t>(ws) % 16 == 0, CMD_ERR_ALIGN, "workspace is not 16-byte aligned");
+  need(bytes >= want, CMD_ERR_LIMIT, "workspace has " + std::to_string(bytes) + " bytes, not " + std::to_string(want));
+}
+
+constexpr int64_t kSplitBytes = cmdx::kAttendMaxCtas * sizeof(cmdx::AttendSplit);
+static_assert(kSplitBytes % 16 == 0, "the parts are aligned");
 
 int64_t attention_workspace(int64_t q_heads, int64_t kv_heads, int64_t dim) {
-  const int64_t group = q_heads / kv_heads;
-  const int64_t heads = std::min<int64_t>(kv_heads, cmdx::kAttendHeads) * std::min<int64_t>(group, kBlockHeads);
-  return counters_bytes(q_heads) + 2 * (int64_t)cmdx::kAttendMaxCtas * heads * (dim + 2) * 4;
+  const int64_t heads = std::min<int64_t>(q_heads / kv_heads, cmdx::kAttendMmaHeads);
+  return kSplitBytes + 2 * (int64_t)cmdx::kAttendMaxCtas * heads * (round_up(dim, 4) + 4) * 4;
 }
 
 }  // namespace
@@ -537,11 +535,7 @@ extern "C" cmd_status cmd_attention_decode(const cmd_attention_args* args, void*
     need(a.window >= 0, CMD_ERR_ARG, "window must be positive, or 0 for none");
     need(a.reserved == 0, CMD_ERR_ARG, "reserved must be 0");
     if (rows == 0 || heads == 0) return CMD_OK;
-    need(a.workspace, CMD_ERR_NULL, "workspace is NULL");
-    need(reinterpret_cast<uintptr_t>(a.workspace) % 256 == 0, CMD_ERR_ALIGN, "workspace is not 256-byte aligned");
-    const int64_t want = attention_workspace(heads, kv, dim);
-    need(a.workspace_bytes >= want, CMD_ERR_LIMIT, "workspace has " + std::to_string(a.workspace_bytes) + " bytes, not " +
-                                                       std::to_string(want));
+    check_workspace(a.workspace, a.workspace_bytes, attention_workspace(heads, kv, dim));
     cmdx::AttendParams p;
     std::memset(&p, 0, sizeof p);
     p.kv_heads = (int32_t)kv;
@@ -568,16 +562,18 @@ extern "C" cmd_status cmd_attention_decode(const cmd_attention_args* args, void*
     p.len_st = a.lengths.strides[0];
     p.k = a.k_cache.ptr;
     p.v = a.v_cache.ptr;
-    p.arrived = static_cast<int32_t*>(a.workspace);
-    p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + counters_bytes(heads));
+    p.splits = static_cast<cmdx::AttendSplit*>(a.workspace);
+    p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kSplitBytes);
     p.status = a.status;
     const int es = elem_size(a.q.dtype);
-    p.max_ctas = cmdx::kAttendMaxCtas;
-    const int most = 8;  // query heads of a block
+    // the tensor units take 16-bit caches whose rows are whole 16-byte vectors
+    const bool mma = es == 2 && dim > 0 && dim % 8 == 0 && vector_rows(a.k_cache, 16) && vector_rows(a.v_cache, 16);
+    const int most = mma ? cmdx::kAttendMmaHeads : cmdx::kAttendSimtHeads;
     p.blocks = (p.group + most - 1) / most;
     p.block_heads = (p.group + p.blocks - 1) / p.blocks;
-    p.heads_per_cta = heads_at_once(kv, cmdx::kAttendHeads);
-    p.vec = vector_rows(a.k_cache, (dim <= 64 ? 2 : 4) * es) && vector_rows(a.v_cache, (dim <= 64 ? 2 : 4) * es);
+    p.q_pairs = vector_rows(a.q, 4);
+    const int few = (dim <= 64 ? 2 : 4) * es;
+    p.vec = vector_rows(a.k_cache, few) && vector_rows(a.v_cache, few);
     for (int64_t r = 0; r < rows; r += cmdx::kAttendRows) {
       p.rows = (int32_t)std::min<int64_t>(cmdx::kAttendRows, rows - r);
       p.q = static_cast<const uint8_t*>(a.q.ptr) + r * a.q.strides[0] * es;
@@ -585,7 +581,8 @@ extern "C" cmd_status cmd_attention_decode(const cmd_attention_args* args, void*
       p.lse = a.lse.ptr ? static_cast<float*>(a.lse.ptr) + r * a.lse.strides[0] : nullptr;
       p.tables = static_cast<const int32_t*>(a.tables.ptr) + r * a.tables.strides[0];
       p.lengths = static_cast<const int32_t*>(a.lengths.ptr) + r * a.lengths.strides[0];
-      const cudaError_t e = cmdx::attend_simt_launch(a.q.dtype, p, static_cast<cudaStream_t>(cuda_stream));
+      const cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+      const cudaError_t e = mma ? cmdx::attend_mma_launch(a.q.dtype, p, stream) : cmdx::attend_simt_launch(a.q.dtype, p, stream);
       if (e != cudaSuccess) return launched(e);
     }
     return CMD_OK;
@@ -648,12 +645,6 @@ void check_pools(const cmdx::PoolList& l, int64_t pages) {
       }
       need(ok, CMD_ERR_ALIAS, "two pools overlap");
     }
-}
-
-void check_workspace(const void* ws, int64_t bytes, int64_t want) {
-  need(ws, CMD_ERR_NULL, "workspace is NULL");
-  need(reinterpret_cast<uintptr_t>(ws) % 16 == 0, CMD_ERR_ALIGN, "workspace is not 16-byte aligned");
-  need(bytes >= want, CMD_ERR_LIMIT, "workspace has " + std::to_string(bytes) + " bytes, not " + std::to_string(want));
 }
 
 constexpr int64_t kHeadWords = 16;

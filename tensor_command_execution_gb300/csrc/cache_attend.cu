@@ -17,6 +17,7 @@ namespace cmdx {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kRowsBytes = (sizeof(AttendRows) + 15) / 16 * 16;
 
 // VEC elements of a row for this lane (element 4 lane + 128 j + i for VEC 4
 // and 8, 2 lane + i for VEC 2), zero past dim.
@@ -47,33 +48,28 @@ __global__ void __launch_bounds__(kWarps * 32) attend_simt_kernel(const __grid_c
   constexpr int kStep = VEC == 8 && GT == 8 ? 2 : 4;  // tokens at once
   constexpr int NV = kStep * GT;
   constexpr int kDup = 32 / NV;  // lanes that end up with the same score
-  constexpr int kPitch = 32 * VEC + 2;
+  constexpr int kPitch = attend_pitch(32 * VEC);
   extern __shared__ __align__(16) unsigned char s_mem[];
-  AttendSpan& s_span = *reinterpret_cast<AttendSpan*>(s_mem);
-  float(*s_state)[GT][kPitch] = reinterpret_cast<float(*)[GT][kPitch]>(s_mem + sizeof(AttendSpan));
-  __shared__ int s_last;
+  AttendRows& s_rows = *reinterpret_cast<AttendRows*>(s_mem);
+  float(*s_state)[GT][kPitch] = reinterpret_cast<float(*)[GT][kPitch]>(s_mem + kRowsBytes);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int hw = p.heads_per_cta, phases = kWarps / hw;
-  const int tile = kAttendTile * phases;
+  constexpr int tile = kAttendTile * kWarps;
   pdl_wait();
   pdl_trigger();
-  attend_spans(p, s_span, tile);
-  attend_empty_rows<T>(p, s_span);
-  const AttendShare share = attend_share(p, s_span);
+  AttendShare share;
+  if (!attend_begin<T>(p, s_rows, tile, &share)) return;
   const T* kp = static_cast<const T*>(p.k);
   const T* vp = static_cast<const T*>(p.v);
-  for (int64_t u = share.begin; u < share.end;) {
-    const AttendSegment g = attend_segment(p, s_span, share, u, tile);
-    const int head = g.head0 + warp % hw, phase = warp / hw;
-    const int gh = min(p.block_heads, p.group - g.qblock * p.block_heads);
+  int64_t u = share.begin;
+  for (AttendSegment g = attend_first(p, s_rows, share, tile);; g = attend_next(p, s_rows, share, g, u, tile)) {
+    const AttendHeads heads = attend_heads(p, g.group);
     float q[GT][VEC], o[GT][VEC];
 #pragma unroll
     for (int h = 0; h < GT; ++h) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) q[h][i] = o[h][i] = 0.0f;
-      if (h < gh) {
-        const T* row = static_cast<const T*>(p.q) + g.row * p.q_st[0] +
-                       (head * p.group + g.qblock * p.block_heads + h) * p.q_st[1];
+      if (h < heads.heads) {
+        const T* row = static_cast<const T*>(p.q) + g.row * p.q_st[0] + (heads.head0 + h) * p.q_st[1];
         load_row<T, VEC>(q[h], row, lane, p.dim, false);
       }
     }
@@ -81,7 +77,7 @@ __global__ void __launch_bounds__(kWarps * 32) attend_simt_kernel(const __grid_c
     const int my_token = lane / kDup / GT;
     float m = -CUDART_INF_F, l = 0.0f;
     for (int i = 0; i < g.tiles; ++i) {
-      const int t0 = (g.tile0 + i) * tile + phase * kAttendTile;
+      const int t0 = (g.tile0 + i) * tile + warp * kAttendTile;
       for (int t = max(t0, g.lo / kStep * kStep); t < min(t0 + kAttendTile, g.n); t += kStep) {
         float k[kStep][VEC], v[kStep][VEC];
         bool bad = false;
@@ -101,8 +97,8 @@ __global__ void __launch_bounds__(kWarps * 32) attend_simt_kernel(const __grid_c
           }
           if (seen[j]) {
             const int64_t in_page = token - (int64_t)column * p.page.d;
-            load_row<T, VEC>(k[j], kp + page * p.k_st[0] + in_page * p.k_st[1] + head * p.k_st[2], lane, p.dim, p.vec);
-            load_row<T, VEC>(v[j], vp + page * p.v_st[0] + in_page * p.v_st[1] + head * p.v_st[2], lane, p.dim, p.vec);
+            load_row<T, VEC>(k[j], kp + page * p.k_st[0] + in_page * p.k_st[1] + heads.kv * p.k_st[2], lane, p.dim, p.vec);
+            load_row<T, VEC>(v[j], vp + page * p.v_st[0] + in_page * p.v_st[1] + heads.kv * p.v_st[2], lane, p.dim, p.vec);
           } else {
 #pragma unroll
             for (int e = 0; e < VEC; ++e) k[j][e] = v[j][e] = 0.0f;
@@ -173,24 +169,25 @@ __global__ void __launch_bounds__(kWarps * 32) attend_simt_kernel(const __grid_c
 #pragma unroll
     for (int h = 0; h < GT; ++h) {
       if (lane == h * kDup) {
-        s_state[warp][h][0] = m;
-        s_state[warp][h][1] = l;
+        s_state[warp][h][kPitch - 4] = m;
+        s_state[warp][h][kPitch - 3] = l;
       }
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) s_state[warp][h][2 + lane_element<T, VEC>(lane, e)] = o[h][e];
+      for (int e = 0; e < VEC; ++e) s_state[warp][h][lane_element<T, VEC>(lane, e)] = o[h][e];
     }
-    attend_finish<T>(p, share, g, &s_state[0][0][0], GT * kPitch, kPitch, &s_last);
+    attend_finish<T, kWarps>(p, share, g, heads, &s_state[0][0][0], GT * kPitch, kPitch);
     u += g.tiles;
+    if (u == share.end) break;
   }
 }
 
 template <class T, int GT, int VEC>
 cudaError_t launch(const AttendParams& p, cudaStream_t stream) {
-  constexpr int smem = sizeof(AttendSpan) + kWarps * GT * (32 * VEC + 2) * (int)sizeof(float);
+  constexpr int smem = kRowsBytes + kWarps * GT * attend_pitch(32 * VEC) * (int)sizeof(float);
   static DeviceCache ready;  // (static storage: zero before first use)
   const cudaError_t e = allow_smem(attend_simt_kernel<T, GT, VEC>, smem, ready);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attend_simt_kernel<T, GT, VEC>, p.max_ctas, kWarps * 32, smem, stream, p);
+  return attend_launch<T>(attend_simt_kernel<T, GT, VEC>, p, 2 * 152, kWarps * 32, smem, kAttendTile * kWarps, stream);
 }
 
 template <class T, int GT>

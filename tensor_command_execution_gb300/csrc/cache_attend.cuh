@@ -1,16 +1,17 @@
 // cache_attend.cuh - how the one-token attention's work is split and joined,
 // shared by its kernels.
 //
-// A unit of work is a tile of tokens of one row and one group of heads. The
-// units of a launch, ordered by row, then head group, then token, are cut
-// into equal runs, one for each CTA, whatever the rows' lengths: no CTA waits
-// for a long row. A CTA whose run holds all of a row's tiles writes the
-// result; one that holds some writes a partial result (running maximum, sum
-// and weighted values) to the workspace, and the CTA that arrives last at a
-// row's counter joins the row's parts, in their order, so that the result does
-// not depend on which CTA that was. At most two of a CTA's segments are
-// partial (its first and its last), so the workspace does not grow with the
-// rows.
+// A unit of work is a tile of tokens of one row, for one kv head and a block
+// of the query heads that share it; a CTA's warps take 16 tokens of it each.
+// The units of a launch, ordered by row, then head, then token, are cut into
+// equal runs, one for each CTA, whatever the rows' lengths: no CTA waits for a
+// long row. A CTA whose run holds all of a row's tiles writes the result; one
+// that holds some writes a part (maximum, sum and weighted values) to the
+// workspace, and a second, small launch joins the parts of each split row in
+// their order, so that the result does not depend on timing. At most two of a
+// CTA's segments are parts (its first and its last), so the workspace does not
+// grow with the rows, and at most one row that is split begins in a CTA, so
+// neither does the list of them.
 #pragma once
 
 #include <math_constants.h>
@@ -19,35 +20,34 @@
 
 namespace cmdx {
 
-// Where each row's units begin (in units of one head group), in shared memory.
-struct AttendSpan {
+// The rows of a launch, in shared memory: where each row's units begin (in
+// units of one kv head and block of query heads), and its tokens [lo, n) that
+// are attended to.
+struct AttendRows {
   int64_t at[kAttendRows + 1];
+  int32_t n[kAttendRows];
+  __device__ __forceinline__ int lo(const AttendParams& p, int r) const {
+    return p.window > 0 && n[r] > p.window ? n[r] - p.window : 0;
+  }
 };
 
-// Row r's tokens [lo, n) that are attended to.
-__device__ __forceinline__ void attend_range(const AttendParams& p, int r, int* lo, int* n) {
-  int64_t len = p.lengths[r * p.len_st];
-  const int64_t most = (int64_t)p.columns * p.page.d;
-  if (len < 0 || len > most) {
-    if (blockIdx.x == 0) report(p.status, CMD_CACHE_BAD_INDEX);
-    len = len < 0 ? 0 : most;
-  }
-  *n = (int)len;
-  *lo = p.window > 0 && len > p.window ? (int)(len - p.window) : 0;
-}
-
-// The rows' first units for tiles of `tile` tokens (aligned to the row's
-// start), by all threads of the CTA (256 of them or fewer).
-__device__ __forceinline__ void attend_spans(const AttendParams& p, AttendSpan& s, int tile) {
+// Fills s for tiles of `tile` tokens (aligned to the row's start); all
+// threads of the CTA call it.
+__device__ __forceinline__ void attend_rows(const AttendParams& p, AttendRows& s, int tile) {
   __shared__ int64_t s_warp[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int run = (p.rows + blockDim.x - 1) / blockDim.x;
   const int r0 = min(tid * run, p.rows), r1 = min(r0 + run, p.rows);
+  const int64_t most = (int64_t)p.columns * p.page.d;
   int64_t sum = 0;
   for (int r = r0; r < r1; ++r) {
-    int lo, n;
-    attend_range(p, r, &lo, &n);
-    s.at[r + 1] = n > lo ? (n + tile - 1) / tile - lo / tile : 0;
+    int64_t len = p.lengths[r * p.len_st];
+    if (len < 0 || len > most) {
+      if (blockIdx.x == 0) report(p.status, CMD_CACHE_BAD_INDEX);
+      len = len < 0 ? 0 : most;
+    }
+    const int n = s.n[r] = (int)len;
+    s.at[r + 1] = n > 0 ? (n + tile - 1) / tile - s.lo(p, r) / tile : 0;
     sum += s.at[r + 1];
   }
   int64_t incl = sum;
@@ -68,13 +68,15 @@ __device__ __forceinline__ void attend_spans(const AttendParams& p, AttendSpan& 
   __syncthreads();
 }
 
-// A CTA's share of a launch.
+// A CTA's share of a launch: units [begin, end).
 struct AttendShare {
   int64_t units, ctas, begin, end;
+  int groups;  // kv heads times blocks of query heads
 };
-__device__ __forceinline__ AttendShare attend_share(const AttendParams& p, const AttendSpan& s) {
+__device__ __forceinline__ AttendShare attend_share(const AttendParams& p, const AttendRows& s) {
   AttendShare w;
-  w.units = s.at[p.rows] * ((p.kv_heads / p.heads_per_cta) * p.blocks);
+  w.groups = p.kv_heads * p.blocks;
+  w.units = s.at[p.rows] * w.groups;
   w.ctas = w.units < gridDim.x ? w.units : gridDim.x;
   w.begin = w.ctas ? blockIdx.x * w.units / w.ctas : 0;
   w.end = blockIdx.x < w.ctas ? (blockIdx.x + 1) * w.units / w.ctas : w.begin;
@@ -85,47 +87,157 @@ __device__ __forceinline__ int attend_owner(const AttendShare& w, int64_t u) {
   return (int)(((u + 1) * w.ctas - 1) / w.units);
 }
 
-// A stretch of one row's tiles for one head group.
+// A stretch of one row's tiles for one kv head and block of query heads.
 struct AttendSegment {
-  int row, head0, qblock;   // first kv head, block of query heads
+  int row, group;           // group = kv head * blocks + block
   int lo, n;                // the row's tokens
   int tile0, tiles;         // this stretch, in tiles from the row's start
-  int64_t first, last;      // the first and last unit of the row and head group
-  int64_t unit;             // the stretch's first unit
-  bool whole;
+  int64_t first;            // the first unit of the row and group
+  int row_tiles;            // and their number
+  __device__ __forceinline__ bool whole() const { return tiles == row_tiles; }
 };
-__device__ __forceinline__ AttendSegment attend_segment(const AttendParams& p, const AttendSpan& s, const AttendShare& w,
-                                                        int64_t u, int tile) {
-  const int groups = (p.kv_heads / p.heads_per_cta) * p.blocks;
-  const int64_t x = u / groups;
+// The stretch that begins at unit u: of row `row` and group `group`, `t` tiles in.
+__device__ __forceinline__ AttendSegment attend_stretch(const AttendParams& p, const AttendRows& s, const AttendShare& w,
+                                                        int64_t u, int row, int group, int t, int tile) {
+  AttendSegment g;
+  g.row = row;
+  g.group = group;
+  g.n = s.n[row];
+  g.lo = s.lo(p, row);
+  g.row_tiles = (int)(s.at[row + 1] - s.at[row]);
+  g.tile0 = g.lo / tile + t;
+  const int64_t left = w.end - u;
+  g.tiles = g.row_tiles - t < left ? g.row_tiles - t : (int)left;
+  g.first = u - t;
+  return g;
+}
+__device__ __forceinline__ AttendSegment attend_first(const AttendParams& p, const AttendRows& s, const AttendShare& w,
+                                                      int tile) {
+  const int64_t x = w.begin / w.groups;
   int a = 0, b = p.rows;  // the last row that begins at or before x
   while (b - a > 1) {
     const int m = (a + b) >> 1;
     if (s.at[m] <= x) a = m; else b = m;
   }
-  AttendSegment g;
-  g.row = a;
+  const int64_t in_row = w.begin - s.at[a] * w.groups;
   const int64_t row_tiles = s.at[a + 1] - s.at[a];
-  const int64_t in_row = u - s.at[a] * groups;
   const int group = (int)(in_row / row_tiles);
-  const int64_t t = in_row - group * row_tiles;
-  g.head0 = group / p.blocks * p.heads_per_cta;
-  g.qblock = group % p.blocks;
-  attend_range(p, a, &g.lo, &g.n);
-  g.tile0 = (int)(g.lo / tile + t);
-  const int64_t left = w.end - u;
-  g.tiles = (int)(row_tiles - t < left ? row_tiles - t : left);
-  g.unit = u;
-  g.first = u - t;
-  g.last = g.first + row_tiles - 1;
-  g.whole = g.tiles == row_tiles;
-  return g;
+  return attend_stretch(p, s, w, w.begin, a, group, (int)(in_row - group * row_tiles), tile);
+}
+// The one after g, beginning at unit u.
+__device__ __forceinline__ AttendSegment attend_next(const AttendParams& p, const AttendRows& s, const AttendShare& w,
+                                                     const AttendSegment& g, int64_t u, int tile) {
+  int row = g.row, group = g.group + 1;
+  if (group == w.groups) {
+    group = 0;
+    do ++row;
+    while (s.at[row + 1] == s.at[row]);
+  }
+  return attend_stretch(p, s, w, u, row, group, 0, tile);
 }
 
-// Rows with no tokens: zeros, and a log-sum of -infinity.
+// The state of a query head over some of its tokens: the maximum m of the
+// scores (in powers of two), the sum l of exp2(score - m) and the values
+// weighted by the same, o[dim]. -infinity, zero and zeros for no token. In
+// memory: o, then m and l at attend_pitch - 4 and - 3, all aligned to 16
+// bytes.
+__host__ __device__ constexpr int attend_pitch(int dim) { return (dim + 3) / 4 * 4 + 4; }
+
+// What a state with maximum m weighs in one with maximum top.
+__device__ __forceinline__ float attend_weight(float m, float top) {
+  return m == -CUDART_INF_F ? 0.0f : exp2f(m - top);
+}
+
+__device__ __forceinline__ void add_scaled(float4& o, const float4& x, float c) {
+  o.x = fmaf(x.x, c, o.x);
+  o.y = fmaf(x.y, c, o.y);
+  o.z = fmaf(x.z, c, o.z);
+  o.w = fmaf(x.w, c, o.w);
+}
+__device__ __forceinline__ void scale_by(float4& o, float c) {
+  o.x *= c;
+  o.y *= c;
+  o.z *= c;
+  o.w *= c;
+}
+
+// Writes elements d .. d + 3 (those below dim) of a finished head.
 template <class T>
-__device__ __forceinline__ void attend_empty_rows(const AttendParams& p, const AttendSpan& s) {
-  const int heads = p.kv_heads * p.group;
+__device__ __forceinline__ void attend_write(const AttendParams& p, int row, int h, int d, float top, float l, float4 o) {
+  T* out = static_cast<T*>(p.out) + row * p.out_st[0] + h * p.out_st[1] + d;
+  const float r = l == 0.0f ? 0.0f : 1.0f / l;
+  if (l == 0.0f) o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const float x[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (d + i < p.dim) out[i] = from_float<T>(x[i] * r);
+  if (d == 0 && p.lse) p.lse[row * p.lse_st[0] + h * p.lse_st[1]] = l == 0.0f ? -CUDART_INF_F : (top + log2f(l)) * CUDART_LN2_F;
+}
+
+// A segment's kv head and its query heads [head0, head0 + heads).
+struct AttendHeads {
+  int kv, head0, heads;
+};
+__device__ __forceinline__ AttendHeads attend_heads(const AttendParams& p, int group) {
+  AttendHeads h;
+  h.kv = group / p.blocks;
+  h.head0 = h.kv * p.group + (group - h.kv * p.blocks) * p.block_heads;
+  h.heads = min(p.block_heads, (h.kv + 1) * p.group - h.head0);
+  return h;
+}
+
+// Ends a segment. The warps' states lie in shared memory, query head q of
+// warp w at state + w * warp_pitch + q * pitch (pitch = attend_pitch of
+// something at least dim). All threads call it, once their states are
+// written.
+template <class T, int WARPS>
+__device__ __forceinline__ void attend_finish(const AttendParams& p, const AttendShare& w, const AttendSegment& g,
+                                              const AttendHeads& h, const float* state, int warp_pitch, int pitch) {
+  const int part_pitch = attend_pitch(p.dim), quads = part_pitch / 4 - 1;
+  const int slot = 2 * blockIdx.x + (g.first <= w.begin ? 0 : 1);
+  float* part = g.whole() ? nullptr : p.parts + (int64_t)slot * p.block_heads * part_pitch;
+  if (threadIdx.x == 0 && g.first >= w.begin) {
+    // the row begins here: say where its parts are
+    AttendSplit split = {g.row, g.group, slot, 0};
+    if (part) split.parts = attend_owner(w, g.first + g.row_tiles - 1) - (int)blockIdx.x + 1;
+    if (p.split_by_row) p.splits[g.row * w.groups + g.group] = split;
+    else if (part) p.splits[blockIdx.x] = split;
+  }
+  __syncthreads();  // the warps' states are complete
+  for (int i = threadIdx.x; i < h.heads * quads; i += WARPS * 32) {
+    const int q = i / quads, d = 4 * (i - q * quads);
+    const float* s = state + q * pitch;
+    float m[WARPS], top = -CUDART_INF_F, l = 0.0f;
+#pragma unroll
+    for (int t = 0; t < WARPS; ++t) top = fmaxf(top, m[t] = s[t * warp_pitch + pitch - 4]);
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int t = 0; t < WARPS; ++t) {
+      const float* x = s + t * warp_pitch;
+      const float c = attend_weight(m[t], top);
+      l = fmaf(x[pitch - 3], c, l);
+      add_scaled(o, *reinterpret_cast<const float4*>(x + d), c);
+    }
+    if (part) {
+      float* x = part + q * part_pitch;
+      if (d == 0) {
+        x[part_pitch - 4] = top;
+        x[part_pitch - 3] = l;
+      }
+      *reinterpret_cast<float4*>(x + d) = o;
+    } else {
+      attend_write<T>(p, g.row, h.head0 + q, d, top, l, o);
+    }
+  }
+  __syncthreads();  // the states may be overwritten
+}
+
+// What a CTA does before its first segment: the rows, those of them that are
+// empty (zeros, and a log-sum of -infinity), and its share. False: no work.
+template <class T>
+__device__ __forceinline__ bool attend_begin(const AttendParams& p, AttendRows& s, int tile, AttendShare* w) {
+  attend_rows(p, s, tile);
+  const int heads = p.kv_heads * p.group, groups = p.kv_heads * p.blocks;
   for (int r = blockIdx.x; r < p.rows; r += gridDim.x) {
     if (s.at[r + 1] != s.at[r]) continue;
     for (int i = threadIdx.x; i < heads * p.dim; i += blockDim.x) {
@@ -134,100 +246,111 @@ __device__ __forceinline__ void attend_empty_rows(const AttendParams& p, const A
     }
     if (p.lse)
       for (int h = threadIdx.x; h < heads; h += blockDim.x) p.lse[r * p.lse_st[0] + h * p.lse_st[1]] = -CUDART_INF_F;
+    if (p.split_by_row)
+      for (int i = threadIdx.x; i < groups; i += blockDim.x) p.splits[r * groups + i].parts = 0;
   }
+  *w = attend_share(p, s);
+  if (!p.split_by_row && threadIdx.x == 0) p.splits[blockIdx.x].parts = 0;  // (unless a row is split here, below)
+  return w->begin != w->end;
 }
 
-// The merged state of one query head over the warps that shared its tokens.
-// o[] of a warp: unnormalised, relative to its maximum m (in powers of two;
-// -infinity where it saw no token, with l and o zero).
-__device__ __forceinline__ float attend_weight(float m, float top) {
-  return m == -CUDART_INF_F ? 0.0f : exp2f(m - top);
-}
-
-// Writes the result of (row, kv head, query head g of its block), element d.
-template <class T>
-__device__ __forceinline__ void attend_write(const AttendParams& p, int row, int kv_head, int qblock, int g, int d,
-                                             float top, float l, float o) {
-  const int h = kv_head * p.group + qblock * p.block_heads + g;
-  static_cast<T*>(p.out)[row * p.out_st[0] + h * p.out_st[1] + d] = from_float<T>(l == 0.0f ? 0.0f : o / l);
-  if (d == 0 && p.lse)
-    p.lse[row * p.lse_st[0] + h * p.lse_st[1]] = l == 0.0f ? -CUDART_INF_F : (top + log2f(l)) * CUDART_LN2_F;
-}
-
-// Ends a segment. The warps' states lie in shared memory: query head g of warp
-// w has its m, its l and its o[dim] at state + w * warp_pitch + g * pitch. Warp
-// w worked on kv head head0 + w % heads_per_cta and every (warps /
-// heads_per_cta)-th tile. All threads call it.
-template <class T>
-__device__ __forceinline__ void attend_finish(const AttendParams& p, const AttendShare& w, const AttendSegment& g,
-                                              const float* state, int warp_pitch, int pitch, int* s_last) {
-  const int hw = p.heads_per_cta, phases = (int)(blockDim.x >> 5) / hw;
-  const int gh = min(p.block_heads, p.group - g.qblock * p.block_heads);
-  const int heads = hw * gh, dim = p.dim;
-  const int part_pitch = dim + 2;
-  const int64_t part_size = (int64_t)hw * p.block_heads * part_pitch;
-  __syncthreads();  // the warps' states are complete
-  float* part = nullptr;
-  if (!g.whole) part = p.parts + (2 * (int64_t)blockIdx.x + (g.unit == w.begin ? 0 : 1)) * part_size;
-  for (int i = threadIdx.x; i < heads * dim; i += blockDim.x) {
-    const int hg = i / dim, d = i - hg * dim, hh = hg / gh, q = hg - hh * gh;
-    const float* s = state + hh * warp_pitch + q * pitch;
-    float top = -CUDART_INF_F;
-    for (int t = 0; t < phases; ++t) top = fmaxf(top, s[t * hw * warp_pitch]);
-    float l = 0.0f, o = 0.0f;
-    for (int t = 0; t < phases; ++t) {
-      const float* x = s + t * hw * warp_pitch;
-      const float c = attend_weight(x[0], top);
-      l = fmaf(x[1], c, l);
-      o = fmaf(x[2 + d], c, o);
-    }
-    if (part) {
-      float* x = part + (hh * p.block_heads + q) * part_pitch;
-      if (d == 0) {
-        x[0] = top;
-        x[1] = l;
-      }
-      x[2 + d] = o;
-    } else {
-      attend_write<T>(p, g.row, g.head0 + hh, g.qblock, q, d, top, l, o);
-    }
-  }
-  if (part) {
-    const int c0 = attend_owner(w, g.first), c1 = attend_owner(w, g.last);
-    const int groups = (p.kv_heads / hw) * p.blocks;
-    int32_t* arrived = p.arrived + (int64_t)g.row * groups + g.head0 / hw * p.blocks + g.qblock;
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      const int seen = atomicAdd(arrived, 1);
-      *s_last = seen == c1 - c0;
-      if (seen == c1 - c0) *arrived = 0;  // for the next launch
-    }
-    __syncthreads();
-    if (*s_last) {
-      __threadfence();
-      // the first part is the second of its CTA unless that CTA's run begins with this row
-      const int64_t begin0 = c0 * w.units / w.ctas;
-      const float* first = p.parts + (2 * (int64_t)c0 + (begin0 == g.first ? 0 : 1)) * part_size;
-      for (int i = threadIdx.x; i < heads * dim; i += blockDim.x) {
-        const int hg = i / dim, d = i - hg * dim, hh = hg / gh, q = hg - hh * gh;
-        const int64_t off = (hh * p.block_heads + q) * part_pitch;
-        float top = __ldcg(first + off);
-        float l = __ldcg(first + off + 1), o = __ldcg(first + off + 2 + d);
-        for (int c = c0 + 1; c <= c1; ++c) {
-          const float* x = p.parts + 2 * (int64_t)c * part_size + off;
-          const float m = __ldcg(x), pl = __ldcg(x + 1), po = __ldcg(x + 2 + d);
-          const float up = fmaxf(top, m);
-          const float a = attend_weight(top, up), b = attend_weight(m, up);
-          l = fmaf(l, a, pl * b);
-          o = fmaf(o, a, po * b);
-          top = up;
+// Joins the parts of query head q of a split row: WARPS warps take every
+// WARPS-th run of 8 parts, a lane 4 elements of the head (and 128 further).
+template <class T, int WARPS>
+__device__ __forceinline__ void attend_join(const AttendParams& p, int task, float (*s_state)[CMD_CACHE_MAX_DIM + 4]) {
+  constexpr int kAtOnce = 8;
+  const int lane = threadIdx.x & 31, warp = WARPS == 1 ? 0 : threadIdx.x >> 5;
+  const AttendSplit split = p.splits[task / p.block_heads];
+  const int q = task % p.block_heads;
+  if (split.parts == 0) return;
+  const AttendHeads h = attend_heads(p, split.group);
+  if (q >= h.heads) return;
+  const int pitch = attend_pitch(p.dim);
+  const int64_t size = (int64_t)p.block_heads * pitch;
+  const float* base = p.parts + (int64_t)q * pitch;
+  for (int d = 4 * lane; d < pitch - 4 || WARPS > 1; d += 128) {
+    if (WARPS > 1 && d - 4 * lane >= pitch - 4) break;  // (the same for all of the CTA)
+    const bool mine = d < pitch - 4;
+    float top = -CUDART_INF_F, l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int c = warp * kAtOnce; c < split.parts; c += WARPS * kAtOnce) {
+      float m[kAtOnce], pl[kAtOnce];
+      float4 po[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const float* x = base + (c + k == 0 ? split.first : (split.first & ~1) + 2 * (int64_t)(c + k)) * size;
+        m[k] = -CUDART_INF_F;
+        if (c + k < split.parts && mine) {
+          m[k] = x[pitch - 4];
+          pl[k] = x[pitch - 3];
+          po[k] = *reinterpret_cast<const float4*>(x + d);
         }
-        attend_write<T>(p, g.row, g.head0 + hh, g.qblock, q, d, top, l, o);
       }
+      float up = top;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) up = fmaxf(up, m[k]);
+      const float a = attend_weight(top, up);
+      l *= a;
+      scale_by(o, a);
+      top = up;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k)
+        if (c + k < split.parts && mine) {
+          const float b = attend_weight(m[k], up);
+          l = fmaf(pl[k], b, l);
+          add_scaled(o, po[k], b);
+        }
     }
+    if constexpr (WARPS > 1) {
+      if (mine) {
+        *reinterpret_cast<float4*>(&s_state[warp][d]) = o;
+        if (d == 0) {
+          s_state[warp][CMD_CACHE_MAX_DIM] = top;
+          s_state[warp][CMD_CACHE_MAX_DIM + 1] = l;
+        }
+      }
+      __syncthreads();
+      if (warp == 0 && mine) {
+        top = -CUDART_INF_F;
+#pragma unroll
+        for (int t = 0; t < WARPS; ++t) top = fmaxf(top, s_state[t][CMD_CACHE_MAX_DIM]);
+        l = 0.0f;
+        o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int t = 0; t < WARPS; ++t) {
+          const float c = attend_weight(s_state[t][CMD_CACHE_MAX_DIM], top);
+          l = fmaf(s_state[t][CMD_CACHE_MAX_DIM + 1], c, l);
+          add_scaled(o, *reinterpret_cast<const float4*>(&s_state[t][d]), c);
+        }
+      }
+      // (a second run of dims reads the m and l that the first wrote, unchanged)
+    }
+    if (warp == 0 && mine) attend_write<T>(p, split.row, h.head0 + q, d, top, l, o);
   }
-  __syncthreads();  // the states may be overwritten
+}
+
+template <class T, int WARPS>
+__global__ void __launch_bounds__(WARPS == 1 ? 256 : WARPS * 32) attend_join_kernel(const __grid_constant__ AttendParams p) {
+  __shared__ __align__(16) float s_state[WARPS == 1 ? 1 : WARPS][CMD_CACHE_MAX_DIM + 4];
+  pdl_wait();
+  pdl_trigger();
+  const int task = WARPS == 1 ? blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
+  if (task < p.tasks) attend_join<T, WARPS>(p, task, s_state);
+}
+
+// Launches a kernel of `ctas` CTAs of `threads` threads that splits its work
+// as above in tiles of `tile` tokens, and the join. The joining warps: 16 to a
+// head where few rows can have many parts each, one where each has few.
+template <class T, class K>
+cudaError_t attend_launch(K kernel, AttendParams p, int ctas, int threads, int smem, int tile, cudaStream_t stream) {
+  const int64_t rows = (int64_t)p.rows * p.kv_heads * p.blocks;
+  p.split_by_row = rows <= ctas;
+  const int lists = p.split_by_row ? (int)rows : ctas;
+  p.tasks = lists * p.block_heads;
+  cudaError_t e = launch_pdl(kernel, ctas, threads, (size_t)smem, stream, p);
+  if (e != cudaSuccess || (int64_t)p.columns * p.page.d <= tile) return e;  // (a row of one tile is never split)
+  if (lists * 16 <= ctas) return launch_pdl(attend_join_kernel<T, 16>, p.tasks, 512, 0, stream, p);
+  return launch_pdl(attend_join_kernel<T, 1>, (p.tasks + 7) / 8, 256, 0, stream, p);
 }
 
 // A score in powers of two from a dot product.

@@ -1,0 +1,361 @@
+// cache_attend_mma.cu - attention of one new token per sequence over a paged
+// cache of 16-bit numbers, on the tensor units.
+//
+// Scores and weighted values are kept transposed: S^T = K q^T is a product of
+// 16 tokens by 16 dims with 16 dims by 8 query heads, O^T = V^T P^T one of 16
+// dims by 16 tokens with 16 tokens by 8 heads (mma.sync m16n8k16), so the 16
+// wide side is always the cache's and up to 8 query heads that share a kv head
+// cost no padding beyond 8. The bound is memory: each key and value crosses
+// from HBM once, and 24 such products for 8 KB at dim 128 leave the tensor
+// units mostly idle, so the warp-level instruction, whose operands come from
+// the registers and shared memory of one warp, serves better here than a
+// CTA-wide one: every warp streams tiles of 16 tokens of its own through its
+// own ring of shared memory (asynchronous 16-byte copies, rows padded by 16
+// bytes against bank conflicts) and keeps its own running maximum, sum and
+// O^T, and no barrier is met until a row ends.
+//
+// A weight p is held as the sum of two 16-bit numbers, hi + lo, multiplied
+// apart: rounding p itself to 16 bits would add an error as large as the
+// output's own rounding. Tokens outside the row are filled with zeros as they
+// are copied, whatever their slots hold.
+#include "cache_attend.cuh"
+
+namespace cmdx {
+
+namespace {
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+// 16 bytes to shared memory, or 16 zero bytes where !take
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void load4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void load4_transposed(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+template <class T>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma<__half>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma<__nv_bfloat16>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// x and y rounded to T, and what the rounding leaves of each, rounded again.
+template <class T>
+__device__ __forceinline__ void split(float x, float y, uint32_t* hi, uint32_t* lo) {
+  T h[2] = {from_float<T>(x), from_float<T>(y)};
+  T l[2] = {from_float<T>(x - to_float(h[0])), from_float<T>(y - to_float(h[1]))};
+  *hi = *reinterpret_cast<uint32_t*>(h);
+  *lo = *reinterpret_cast<uint32_t*>(l);
+}
+
+// 2^x for x <= 0 (a result below 2^-126 is 0)
+__device__ __forceinline__ float power_of_two(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Warps of a CTA, stages of each warp's ring, and CTAs of an SM, for heads of
+// up to DP dims.
+template <int DP, int NT>
+struct Shape {
+  static constexpr int kWarps = 4;
+  static constexpr int kStages = DP == 64 ? 3 : 2;
+  static constexpr int kCtas = DP == 256 ? 1 : NT == 2 ? 2 : 3;
+  static constexpr int kPitch = DP * 2 + 16;                   // bytes of a row: an odd number of 16
+  static constexpr int kStage = 2 * kAttendTile * kPitch;      // keys, then values
+  static constexpr int kRing = kStages * kStage;
+  static constexpr int kSmem = kWarps * kRing + (int)sizeof(AttendRows);
+};
+
+template <class T, int DP, int NT>
+__global__ void __launch_bounds__(Shape<DP, NT>::kWarps * 32, Shape<DP, NT>::kCtas) attend_mma_kernel(const __grid_constant__ AttendParams p) {
+  using S = Shape<DP, NT>;
+  constexpr int kChunks = DP / 8;              // 16-byte pieces of a row
+  constexpr int kRowsAtOnce = 32 / kChunks;    // rows that one copy of the warp covers
+  constexpr int KS = DP / 16;
+  extern __shared__ __align__(16) unsigned char s_mem[];
+  AttendRows& s_rows = *reinterpret_cast<AttendRows*>(s_mem + S::kWarps * S::kRing);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int tile = kAttendTile * S::kWarps;
+  unsigned char* ring = s_mem + warp * S::kRing;
+  const uint32_t ring_at = smem_addr(ring);
+  // this lane's places: its chunk and first row in a copy; its row and chunk
+  // in the two kinds of fragment loads; its row g and columns 2 t, 2 t + 1 in
+  // an 8 by 8 block
+  const int chunk = lane % kChunks, copy_row = lane / kChunks;
+  const uint32_t key_at = (lane & 15) * S::kPitch + (lane >> 4) * 16;
+  const uint32_t value_at = ((lane >> 4) * 8 + (lane & 7)) * S::kPitch + ((lane >> 3) & 1) * 16 + kAttendTile * S::kPitch;
+  const int gr = lane >> 2, tc = (lane & 3) * 2;
+
+  pdl_wait();
+  pdl_trigger();
+  AttendShare share;
+  if (!attend_begin<T>(p, s_rows, tile, &share)) return;
+  const T* kp = static_cast<const T*>(p.k) + chunk * 8;
+  const T* vp = static_cast<const T*>(p.v) + chunk * 8;
+  const bool in_dim = chunk * 8 < p.dim;
+  const bool one_page = p.page.d % kAttendTile == 0;  // a tile lies in one page
+
+  int64_t u = share.begin;
+  for (AttendSegment g = attend_first(p, s_rows, share, tile);; g = attend_next(p, s_rows, share, g, u, tile)) {
+    const AttendHeads heads = attend_heads(p, g.group);
+    const int32_t* table = p.tables + g.row * p.table_st[0];
+    const T* kh = kp + heads.kv * p.k_st[2];
+    const T* vh = vp + heads.kv * p.v_st[2];
+    // this warp's i-th tile begins at token first + i * tile
+    const int first = g.tile0 * tile + warp * kAttendTile;
+
+    // the page of this lane's token (lane % 16) of tile i, -1 for none
+    auto look_up = [&](int i) {
+      const int token = first + i * tile + (lane & 15);
+      if (i >= g.tiles || token < g.lo || token >= g.n) return -1;
+      const int page = __ldg(table + fast_div32(p.page, (uint32_t)token) * p.table_st[1]);
+      if (page < 0 || page >= p.n_pages) {
+        report(p.status, CMD_CACHE_BAD_PAGE);
+        return -1;
+      }
+      return page;
+    };
+    // copies tile i into its stage; page: look_up(i). Returns which of its
+    // tokens have a page, a bit each.
+    auto copy_tile = [&](int i, int page) {
+      const uint32_t known = __ballot_sync(~0u, page >= 0) & 0xffffu;
+      if (known) {
+        const int token = first + i * tile + (lane & 15);
+        const uint32_t dst = ring_at + i % S::kStages * S::kStage + copy_row * S::kPitch + chunk * 16;
+        const int slot = token - (int)(fast_div32(p.page, (uint32_t)token) * p.page.d);
+        if (one_page) {
+          const int64_t pg = __shfl_sync(~0u, page, __ffs(known) - 1);
+          const int64_t slot0 = __shfl_sync(~0u, slot, 0) + copy_row;
+          const T* k = kh + pg * p.k_st[0] + slot0 * p.k_st[1];
+          const T* v = vh + pg * p.v_st[0] + slot0 * p.v_st[1];
+#pragma unroll
+          for (int r = 0; r < kAttendTile; r += kRowsAtOnce) {
+            const bool take = in_dim && (known >> (r + copy_row) & 1);
+            copy16(dst + r * S::kPitch, take ? k + r * p.k_st[1] : p.k, take);
+            copy16(dst + (r + kAttendTile) * S::kPitch, take ? v + r * p.v_st[1] : p.v, take);
+          }
+        } else {
+#pragma unroll
+          for (int r = 0; r < kAttendTile; r += kRowsAtOnce) {
+            const int64_t pg = __shfl_sync(~0u, page, r + copy_row);
+            const int64_t sl = __shfl_sync(~0u, slot, r + copy_row);
+            const bool take = in_dim && pg >= 0;
+            copy16(dst + r * S::kPitch, take ? kh + pg * p.k_st[0] + sl * p.k_st[1] : p.k, take);
+            copy16(dst + (r + kAttendTile) * S::kPitch, take ? vh + pg * p.v_st[0] + sl * p.v_st[1] : p.v, take);
+          }
+        }
+      }
+      copy_commit();
+      return known;
+    };
+
+    uint32_t known[S::kStages];  // of the tiles on their way, the next one first
+    int next = look_up(0);
+#pragma unroll
+    for (int i = 0; i < S::kStages - 1; ++i) {
+      const int page = next;
+      next = look_up(i + 1);
+      known[i] = copy_tile(i, page);
+    }
+
+    // the query heads of this block, as the right side of K q^T
+    uint32_t q[NT][KS][2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int h = j * 8 + gr;
+      const T* row = static_cast<const T*>(p.q) + g.row * p.q_st[0] + (heads.head0 + min(h, heads.heads - 1)) * p.q_st[1];
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const int d = 16 * s + 8 * b + tc;
+          uint32_t x = 0;
+          if (h < heads.heads && d < p.dim) {
+            if (p.q_pairs) {
+              x = *reinterpret_cast<const uint32_t*>(row + d);
+            } else {
+              T e[2] = {row[d], row[d + 1]};
+              x = *reinterpret_cast<uint32_t*>(e);
+            }
+          }
+          q[j][s][b] = x;
+        }
+    }
+
+    float o[NT][KS][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][s][e] = 0.0f;
+      m[j][0] = m[j][1] = -CUDART_INF_F;
+      l[j][0] = l[j][1] = 0.0f;
+    }
+
+    for (int i = 0; i < g.tiles; ++i) {
+      copy_wait<S::kStages - 2>();
+      __syncwarp();
+      const int page = next;
+      next = look_up(i + S::kStages);
+      known[S::kStages - 1] = copy_tile(i + S::kStages - 1, page);
+      const uint32_t here = known[0];
+#pragma unroll
+      for (int j = 0; j < S::kStages - 1; ++j) known[j] = known[j + 1];
+      if (!here) continue;
+      const uint32_t stage = ring_at + i % S::kStages * S::kStage;
+      // scores: tokens gr, gr + 8, heads tc, tc + 1; two chains of products
+      float s[NT][2][4];
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[j][0][e] = s[j][1][e] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        uint32_t a[4];
+        load4(a, stage + key_at + k * 32);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) mma<T>(s[j][k & 1], a, q[j][k][0], q[j][k][1]);
+      }
+      const bool in0 = here >> gr & 1, in1 = here >> (gr + 8) & 1;
+      uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          x[e] = (e < 2 ? in0 : in1) ? attend_score(p, s[j][0][e] + s[j][1][e]) : -CUDART_INF_F;
+        float up[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
+#pragma unroll
+        for (int b = 4; b < 32; b <<= 1) {
+          up[0] = fmaxf(up[0], __shfl_xor_sync(~0u, up[0], b));
+          up[1] = fmaxf(up[1], __shfl_xor_sync(~0u, up[1], b));
+        }
+        up[0] = fmaxf(up[0], m[j][0]);
+        up[1] = fmaxf(up[1], m[j][1]);
+        if (__any_sync(~0u, up[0] != m[j][0] || up[1] != m[j][1])) {
+          const float c0 = m[j][0] == -CUDART_INF_F ? 0.0f : power_of_two(m[j][0] - up[0]);
+          const float c1 = m[j][1] == -CUDART_INF_F ? 0.0f : power_of_two(m[j][1] - up[1]);
+          l[j][0] *= c0;
+          l[j][1] *= c1;
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            o[j][k][0] *= c0;
+            o[j][k][1] *= c1;
+            o[j][k][2] *= c0;
+            o[j][k][3] *= c1;
+          }
+          m[j][0] = up[0];
+          m[j][1] = up[1];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[e] = x[e] == -CUDART_INF_F ? 0.0f : power_of_two(x[e] - m[j][e & 1]);
+          l[j][e & 1] += x[e];
+        }
+        split<T>(x[0], x[1], &hi[j][0], &lo[j][0]);
+        split<T>(x[2], x[3], &hi[j][1], &lo[j][1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          hi[j][e] = transposed(hi[j][e]);
+          lo[j][e] = transposed(lo[j][e]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        uint32_t a[4];
+        load4_transposed(a, stage + value_at + k * 32);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          mma<T>(o[j][k], a, hi[j][0], hi[j][1]);
+          mma<T>(o[j][k], a, lo[j][0], lo[j][1]);
+        }
+      }
+    }
+
+    // the warp's state into its ring, whose copies have all landed
+    copy_wait<0>();
+    __syncwarp();
+    float* state = reinterpret_cast<float*>(ring);
+    constexpr int kStatePitch = attend_pitch(DP);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+      for (int b = 4; b < 32; b <<= 1) {
+        l[j][0] += __shfl_xor_sync(~0u, l[j][0], b);
+        l[j][1] += __shfl_xor_sync(~0u, l[j][1], b);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float* x = state + (j * 8 + tc + e) * kStatePitch;
+        if (gr == 0) {
+          x[kStatePitch - 4] = m[j][e];
+          x[kStatePitch - 3] = l[j][e];
+        }
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          x[16 * k + gr] = o[j][k][e];
+          x[16 * k + gr + 8] = o[j][k][2 + e];
+        }
+      }
+    }
+    attend_finish<T, S::kWarps>(p, share, g, heads, reinterpret_cast<float*>(s_mem), S::kRing / 4, kStatePitch);
+    u += g.tiles;
+    if (u == share.end) break;
+  }
+}
+
+template <class T, int DP, int NT>
+cudaError_t launch(const AttendParams& p, cudaStream_t stream) {
+  using S = Shape<DP, NT>;
+  static_assert(NT * 8 * attend_pitch(DP) * 4 <= S::kRing, "a warp's state fits its ring");
+  static DeviceCache ready;  // (static storage: zero before first use)
+  const cudaError_t e = allow_smem(attend_mma_kernel<T, DP, NT>, S::kSmem, ready);
+  if (e != cudaSuccess) return e;
+  return attend_launch<T>(attend_mma_kernel<T, DP, NT>, p, 152 * S::kCtas, S::kWarps * 32, S::kSmem, kAttendTile * S::kWarps,
+                          stream);
+}
+
+template <class T>
+cudaError_t launch_type(const AttendParams& p, cudaStream_t stream) {
+  const bool two = p.block_heads > 8;
+  if (p.dim <= 64) return two ? launch<T, 64, 2>(p, stream) : launch<T, 64, 1>(p, stream);
+  if (p.dim <= 128) return two ? launch<T, 128, 2>(p, stream) : launch<T, 128, 1>(p, stream);
+  return two ? launch<T, 256, 2>(p, stream) : launch<T, 256, 1>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t attend_mma_launch(int dtype, const AttendParams& p, cudaStream_t stream) {
+  return dtype == CMD_F16 ? launch_type<__half>(p, stream) : launch_type<__nv_bfloat16>(p, stream);
+}
+
+}  // namespace cmdx

@@ -55,10 +55,16 @@ struct RopeParams {
 cudaError_t rope_launch(int dtype, int layout, bool vec, const RopeParams& p, cudaStream_t stream);
 
 // ---- attention of one token (cache_attend*.cu) --------------------------------
-constexpr int kAttendMaxCtas = 304;   // two for each of 152 SMs; bounds the workspace
-constexpr int kAttendRows = 2048;     // rows of one launch (the host splits larger calls)
-constexpr int kAttendHeads = 8;       // kv heads a CTA works on at once, at most
-constexpr int kAttendTile = 16;       // tokens a warp takes at a time
+constexpr int kAttendMaxCtas = 152 * 4;  // bounds the workspace
+constexpr int kAttendRows = 512;         // rows of one launch (the host splits larger calls)
+constexpr int kAttendTile = 16;          // tokens a warp takes at a time
+
+// A row (for one kv head and block of query heads) whose tiles went to several
+// CTAs: part k lies at index `first` for k = 0, (first & ~1) + 2 k after.
+struct AttendSplit {
+  int32_t row, group, first;
+  int32_t parts;  // 0: none
+};
 
 struct AttendParams {
   const void* q;
@@ -77,18 +83,22 @@ struct AttendParams {
   float scale_log2;    // scale * log2 e: scores are kept in powers of two
   float cap_in, cap_out;  // scale / softcap, softcap * log2 e (cap_out 0: none)
   int32_t window;
-  int32_t heads_per_cta;  // kv heads a CTA works on at once (divides kv_heads and the warps)
   int32_t blocks;      // blocks of query heads of one kv head
   int32_t block_heads; // query heads of a block (the last may have fewer)
-  int32_t max_ctas;
-  float* parts;        // partial results, [2 max_ctas][heads_per_cta * block_heads][dim + 2]
-  int32_t* arrived;    // [rows][head groups]: parts written so far, 0 between launches
+  float* parts;        // partial results, [2 CTAs][block_heads][attend_pitch(dim)]
+  AttendSplit* splits; // one for each CTA, or for each row and group
+  int32_t tasks;       // of the join
+  uint8_t split_by_row;
   int32_t* status;
   uint8_t q_pairs;     // q rows may be read two 16-bit elements at a time
-  uint8_t vec;         // cache rows may be read in vectors
+  uint8_t vec;         // cache rows may be read in vectors (of 2 or 4 elements)
 };
 
+// any types, alignment and strides; at most 8 query heads of a block
 cudaError_t attend_simt_launch(int dtype, const AttendParams& p, cudaStream_t stream);
+// 16-bit types whose cache rows are whole 16-byte vectors; at most 16 query heads of a block
+cudaError_t attend_mma_launch(int dtype, const AttendParams& p, cudaStream_t stream);
+constexpr int kAttendSimtHeads = 8, kAttendMmaHeads = 16;
 
 // ---- pages (cache_pages.cu) -----------------------------------------------------
 struct PoolList {

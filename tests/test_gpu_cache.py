@@ -9,6 +9,7 @@ import torch
 
 import tensor_command_execution_gb300 as T
 import cacheutil as U
+from tensor_command_execution_gb300.cache import cmd_attention_workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -317,8 +318,8 @@ def test_attention_on_streams_and_in_a_graph():
     got = [T.attention_decode(q, c.k, c.v, c.tables, c.lengths, stream=s) for s in side for _ in range(3)]
     torch.cuda.synchronize()
     assert all(_same_bits(x, want) for x in got)
-    ws, out = T.attention_workspace(8, 2, 128), torch.empty_like(q)
-    lengths = c.lengths.clone()
+    out, lengths = torch.empty_like(q), c.lengths.clone()
+    ws = torch.full((cmd_attention_workspace(8, 2, 128),), 255, dtype=torch.uint8, device="cuda")  # (any contents)
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         T.attention_decode(q, c.k, c.v, c.tables, lengths, out=out, workspace=ws)
@@ -330,9 +331,6 @@ def test_attention_on_streams_and_in_a_graph():
     g.replay()
     torch.cuda.synchronize()
     assert _same_bits(out, T.attention_decode(q, c.k, c.v, c.tables, lengths))
-    with torch.cuda.graph(torch.cuda.CUDAGraph()):
-        with pytest.raises(ValueError, match="workspace"):
-            T.attention_decode(q, c.k, c.v, c.tables, lengths, out=out)
 
 
 # ---- pages -----------------------------------------------------------------------------------------------------------
