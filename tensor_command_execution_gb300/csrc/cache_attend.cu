@@ -60,8 +60,7 @@ __global__ void __launch_bounds__(kWarps * 32) attend_simt_kernel(const __grid_c
   if (!attend_begin<T>(p, s_rows, tile, &share)) return;
   const T* kp = static_cast<const T*>(p.k);
   const T* vp = static_cast<const T*>(p.v);
-  int64_t u = share.begin;
-  for (AttendSegment g = attend_first(p, s_rows, share, tile);; g = attend_next(p, s_rows, share, g, u, tile)) {
+  for (AttendSegment g = attend_first(p, s_rows, share, tile); g.tiles; g = attend_next(p, s_rows, share, g, tile)) {
     const AttendHeads heads = attend_heads(p, g.group);
     float q[GT][VEC], o[GT][VEC];
 #pragma unroll
@@ -176,8 +175,6 @@ __global__ void __launch_bounds__(kWarps * 32) attend_simt_kernel(const __grid_c
       for (int e = 0; e < VEC; ++e) s_state[warp][h][lane_element<T, VEC>(lane, e)] = o[h][e];
     }
     attend_finish<T, kWarps>(p, share, g, heads, &s_state[0][0][0], GT * kPitch, kPitch);
-    u += g.tiles;
-    if (u == share.end) break;
   }
 }
 
@@ -187,7 +184,7 @@ cudaError_t launch(const AttendParams& p, cudaStream_t stream) {
   static DeviceCache ready;  // (static storage: zero before first use)
   const cudaError_t e = allow_smem(attend_simt_kernel<T, GT, VEC>, smem, ready);
   if (e != cudaSuccess) return e;
-  return attend_launch<T>(attend_simt_kernel<T, GT, VEC>, p, 2 * 152, kWarps * 32, smem, kAttendTile * kWarps, stream);
+  return attend_launch<T>(attend_simt_kernel<T, GT, VEC>, p, 0, 2 * 152, kWarps * 32, smem, kAttendTile * kWarps, stream);
 }
 
 template <class T, int GT>

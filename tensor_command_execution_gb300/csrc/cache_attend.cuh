@@ -5,7 +5,9 @@
 // of the query heads that share it; a CTA's warps take 16 tokens of it each.
 // The units of a launch, ordered by row, then head, then token, are cut into
 // equal runs, one for each CTA, whatever the rows' lengths: no CTA waits for a
-// long row. A CTA whose run holds all of a row's tiles writes the result; one
+// long row. The beginning of a row counts as start_units more units (before
+// its first tile; a CTA whose run ends with them does nothing for the row),
+// since fetching queries and writing a result take as long as some tiles. A CTA whose run holds all of a row's tiles writes the result; one
 // that holds some writes a part (maximum, sum and weighted values) to the
 // workspace, and a second, small launch joins the parts of each split row in
 // their order, so that the result does not depend on timing. At most two of a
@@ -47,7 +49,7 @@ __device__ __forceinline__ void attend_rows(const AttendParams& p, AttendRows& s
       len = len < 0 ? 0 : most;
     }
     const int n = s.n[r] = (int)len;
-    s.at[r + 1] = n > 0 ? (n + tile - 1) / tile - s.lo(p, r) / tile : 0;
+    s.at[r + 1] = n > 0 ? (n + tile - 1) / tile - s.lo(p, r) / tile + p.start_units : 0;
     sum += s.at[r + 1];
   }
   int64_t incl = sum;
@@ -91,24 +93,25 @@ __device__ __forceinline__ int attend_owner(const AttendShare& w, int64_t u) {
 struct AttendSegment {
   int row, group;           // group = kv head * blocks + block
   int lo, n;                // the row's tokens
-  int tile0, tiles;         // this stretch, in tiles from the row's start
-  int64_t first;            // the first unit of the row and group
+  int tile0, tiles;         // this stretch, in tiles from the row's start; no tiles: the share has ended
+  int64_t first;            // the unit of the row's and group's first tile
   int row_tiles;            // and their number
   __device__ __forceinline__ bool whole() const { return tiles == row_tiles; }
 };
-// The stretch that begins at unit u: of row `row` and group `group`, `t` tiles in.
+// The stretch of row `row` and group `group`, whose first unit is u, that lies in the share.
 __device__ __forceinline__ AttendSegment attend_stretch(const AttendParams& p, const AttendRows& s, const AttendShare& w,
-                                                        int64_t u, int row, int group, int t, int tile) {
+                                                        int64_t u, int row, int group, int tile) {
   AttendSegment g;
   g.row = row;
   g.group = group;
   g.n = s.n[row];
   g.lo = s.lo(p, row);
-  g.row_tiles = (int)(s.at[row + 1] - s.at[row]);
-  g.tile0 = g.lo / tile + t;
-  const int64_t left = w.end - u;
-  g.tiles = g.row_tiles - t < left ? g.row_tiles - t : (int)left;
-  g.first = u - t;
+  g.row_tiles = (int)(s.at[row + 1] - s.at[row]) - p.start_units;
+  g.first = u + p.start_units;
+  const int64_t from = w.begin > g.first ? w.begin : g.first;
+  const int64_t to = w.end < g.first + g.row_tiles ? w.end : g.first + g.row_tiles;
+  g.tile0 = g.lo / tile + (int)(from - g.first);
+  g.tiles = to > from ? (int)(to - from) : 0;
   return g;
 }
 __device__ __forceinline__ AttendSegment attend_first(const AttendParams& p, const AttendRows& s, const AttendShare& w,
@@ -119,21 +122,26 @@ __device__ __forceinline__ AttendSegment attend_first(const AttendParams& p, con
     const int m = (a + b) >> 1;
     if (s.at[m] <= x) a = m; else b = m;
   }
-  const int64_t in_row = w.begin - s.at[a] * w.groups;
-  const int64_t row_tiles = s.at[a + 1] - s.at[a];
-  const int group = (int)(in_row / row_tiles);
-  return attend_stretch(p, s, w, w.begin, a, group, (int)(in_row - group * row_tiles), tile);
+  const int64_t row_units = s.at[a + 1] - s.at[a];
+  const int group = (int)((w.begin - s.at[a] * w.groups) / row_units);
+  return attend_stretch(p, s, w, s.at[a] * w.groups + group * row_units, a, group, tile);
 }
-// The one after g, beginning at unit u.
+// The one after g (no tiles: there is none).
 __device__ __forceinline__ AttendSegment attend_next(const AttendParams& p, const AttendRows& s, const AttendShare& w,
-                                                     const AttendSegment& g, int64_t u, int tile) {
+                                                     const AttendSegment& g, int tile) {
+  const int64_t u = g.first + g.row_tiles;
   int row = g.row, group = g.group + 1;
+  if (u >= w.end) {
+    AttendSegment none = g;
+    none.tiles = 0;
+    return none;
+  }
   if (group == w.groups) {
     group = 0;
     do ++row;
     while (s.at[row + 1] == s.at[row]);
   }
-  return attend_stretch(p, s, w, u, row, group, 0, tile);
+  return attend_stretch(p, s, w, u, row, group, tile);
 }
 
 // The state of a query head over some of its tokens: the maximum m of the
@@ -342,7 +350,9 @@ __global__ void __launch_bounds__(WARPS == 1 ? 256 : WARPS * 32) attend_join_ker
 // as above in tiles of `tile` tokens, and the join. The joining warps: 16 to a
 // head where few rows can have many parts each, one where each has few.
 template <class T, class K>
-cudaError_t attend_launch(K kernel, AttendParams p, int ctas, int threads, int smem, int tile, cudaStream_t stream) {
+cudaError_t attend_launch(K kernel, AttendParams p, int start_units, int ctas, int threads, int smem, int tile,
+                          cudaStream_t stream) {
+  p.start_units = start_units;
   const int64_t rows = (int64_t)p.rows * p.kv_heads * p.blocks;
   p.split_by_row = rows <= ctas;
   const int lists = p.split_by_row ? (int)rows : ctas;

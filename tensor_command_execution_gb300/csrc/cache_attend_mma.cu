@@ -118,74 +118,85 @@ __global__ void __launch_bounds__(Shape<DP, NT>::kWarps * 32, Shape<DP, NT>::kCt
   pdl_trigger();
   AttendShare share;
   if (!attend_begin<T>(p, s_rows, tile, &share)) return;
-  const T* kp = static_cast<const T*>(p.k) + chunk * 8;
-  const T* vp = static_cast<const T*>(p.v) + chunk * 8;
   const bool in_dim = chunk * 8 < p.dim;
   const bool one_page = p.page.d % kAttendTile == 0;  // a tile lies in one page
 
-  int64_t u = share.begin;
-  for (AttendSegment g = attend_first(p, s_rows, share, tile);; g = attend_next(p, s_rows, share, g, u, tile)) {
-    const AttendHeads heads = attend_heads(p, g.group);
-    const int32_t* table = p.tables + g.row * p.table_st[0];
-    const T* kh = kp + heads.kv * p.k_st[2];
-    const T* vh = vp + heads.kv * p.v_st[2];
-    // this warp's i-th tile begins at token first + i * tile
-    const int first = g.tile0 * tile + warp * kAttendTile;
-
-    // the page of this lane's token (lane % 16) of tile i, -1 for none
-    auto look_up = [&](int i) {
-      const int token = first + i * tile + (lane & 15);
-      if (i >= g.tiles || token < g.lo || token >= g.n) return -1;
-      const int page = __ldg(table + fast_div32(p.page, (uint32_t)token) * p.table_st[1]);
-      if (page < 0 || page >= p.n_pages) {
-        report(p.status, CMD_CACHE_BAD_PAGE);
-        return -1;
-      }
-      return page;
-    };
-    // copies tile i into its stage; page: look_up(i). Returns which of its
-    // tokens have a page, a bit each.
-    auto copy_tile = [&](int i, int page) {
-      const uint32_t known = __ballot_sync(~0u, page >= 0) & 0xffffu;
-      if (known) {
-        const int token = first + i * tile + (lane & 15);
-        const uint32_t dst = ring_at + i % S::kStages * S::kStage + copy_row * S::kPitch + chunk * 16;
-        const int slot = token - (int)(fast_div32(p.page, (uint32_t)token) * p.page.d);
-        if (one_page) {
-          const int64_t pg = __shfl_sync(~0u, page, __ffs(known) - 1);
-          const int64_t slot0 = __shfl_sync(~0u, slot, 0) + copy_row;
-          const T* k = kh + pg * p.k_st[0] + slot0 * p.k_st[1];
-          const T* v = vh + pg * p.v_st[0] + slot0 * p.v_st[1];
+  // The copies run ahead of the products, across the ends of segments: `next`
+  // is the tile to copy next (the page and slot of this lane's token lane %
+  // 16, -1 for none, and the head's keys and values), whose table entry was
+  // read a tile earlier; `look` is the segment of the one after.
+  AttendSegment g = attend_first(p, s_rows, share, tile);
+  AttendSegment look = g;
+  int look_at = -1;
+  const int32_t* table = nullptr;
+  struct {
+    int page, slot;
+    const T *k, *v;
+  } next = {-1, 0, nullptr, nullptr};
+  auto look_up = [&]() {
+    next.page = -1;
+    if (look_at < 0 || look_at == look.tiles) {
+      if (look_at > 0) look = attend_next(p, s_rows, share, look, tile);
+      look_at = 0;
+      if (look.tiles == 0) return;
+      table = p.tables + look.row * p.table_st[0];
+      const int head = look.group / p.blocks;
+      next.k = static_cast<const T*>(p.k) + chunk * 8 + head * p.k_st[2];
+      next.v = static_cast<const T*>(p.v) + chunk * 8 + head * p.v_st[2];
+    }
+    const int token = (look.tile0 + look_at) * tile + warp * kAttendTile + (lane & 15);
+    const uint32_t column = fast_div32(p.page, (uint32_t)token);
+    next.slot = token - (int)(column * p.page.d);
+    if (token >= look.lo && token < look.n) {
+      const int page = __ldg(table + column * p.table_st[1]);
+      if (page < 0 || page >= p.n_pages) report(p.status, CMD_CACHE_BAD_PAGE);
+      else next.page = page;
+    }
+    ++look_at;
+  };
+  // Copies the next tile into a stage. Returns which of its tokens have a
+  // page, a bit each.
+  auto copy_next = [&](int stage) {
+    const uint32_t known = __ballot_sync(~0u, next.page >= 0) & 0xffffu;
+    if (known) {
+      const uint32_t dst = ring_at + stage * S::kStage + copy_row * S::kPitch + chunk * 16;
+      if (one_page) {
+        const int64_t page = __shfl_sync(~0u, next.page, __ffs(known) - 1);
+        const int64_t slot = __shfl_sync(~0u, next.slot, 0) + copy_row;
+        const T* k = next.k + page * p.k_st[0] + slot * p.k_st[1];
+        const T* v = next.v + page * p.v_st[0] + slot * p.v_st[1];
 #pragma unroll
-          for (int r = 0; r < kAttendTile; r += kRowsAtOnce) {
-            const bool take = in_dim && (known >> (r + copy_row) & 1);
-            copy16(dst + r * S::kPitch, take ? k + r * p.k_st[1] : p.k, take);
-            copy16(dst + (r + kAttendTile) * S::kPitch, take ? v + r * p.v_st[1] : p.v, take);
-          }
-        } else {
+        for (int r = 0; r < kAttendTile; r += kRowsAtOnce) {
+          const bool take = in_dim && (known >> (r + copy_row) & 1);
+          copy16(dst + r * S::kPitch, take ? k + r * p.k_st[1] : p.k, take);
+          copy16(dst + (r + kAttendTile) * S::kPitch, take ? v + r * p.v_st[1] : p.v, take);
+        }
+      } else {
 #pragma unroll
-          for (int r = 0; r < kAttendTile; r += kRowsAtOnce) {
-            const int64_t pg = __shfl_sync(~0u, page, r + copy_row);
-            const int64_t sl = __shfl_sync(~0u, slot, r + copy_row);
-            const bool take = in_dim && pg >= 0;
-            copy16(dst + r * S::kPitch, take ? kh + pg * p.k_st[0] + sl * p.k_st[1] : p.k, take);
-            copy16(dst + (r + kAttendTile) * S::kPitch, take ? vh + pg * p.v_st[0] + sl * p.v_st[1] : p.v, take);
-          }
+        for (int r = 0; r < kAttendTile; r += kRowsAtOnce) {
+          const int64_t page = __shfl_sync(~0u, next.page, r + copy_row);
+          const int64_t slot = __shfl_sync(~0u, next.slot, r + copy_row);
+          const bool take = in_dim && page >= 0;
+          copy16(dst + r * S::kPitch, take ? next.k + page * p.k_st[0] + slot * p.k_st[1] : p.k, take);
+          copy16(dst + (r + kAttendTile) * S::kPitch, take ? next.v + page * p.v_st[0] + slot * p.v_st[1] : p.v, take);
         }
       }
-      copy_commit();
-      return known;
-    };
-
-    uint32_t known[S::kStages];  // of the tiles on their way, the next one first
-    int next = look_up(0);
-#pragma unroll
-    for (int i = 0; i < S::kStages - 1; ++i) {
-      const int page = next;
-      next = look_up(i + 1);
-      known[i] = copy_tile(i, page);
     }
+    copy_commit();
+    return known;
+  };
 
+  uint32_t known[S::kStages];  // of the tiles on their way, the nearest first
+  look_up();
+#pragma unroll
+  for (int i = 0; i < S::kStages - 1; ++i) {
+    known[i] = copy_next(i);
+    look_up();
+  }
+
+  int stage = 0;
+  for (; g.tiles; g = attend_next(p, s_rows, share, g, tile)) {
+    const AttendHeads heads = attend_heads(p, g.group);
     // the query heads of this block, as the right side of K q^T
     uint32_t q[NT][KS][2];
 #pragma unroll
@@ -224,14 +235,14 @@ __global__ void __launch_bounds__(Shape<DP, NT>::kWarps * 32, Shape<DP, NT>::kCt
     for (int i = 0; i < g.tiles; ++i) {
       copy_wait<S::kStages - 2>();
       __syncwarp();
-      const int page = next;
-      next = look_up(i + S::kStages);
-      known[S::kStages - 1] = copy_tile(i + S::kStages - 1, page);
+      known[S::kStages - 1] = copy_next(stage == 0 ? S::kStages - 1 : stage - 1);
+      look_up();
       const uint32_t here = known[0];
 #pragma unroll
       for (int j = 0; j < S::kStages - 1; ++j) known[j] = known[j + 1];
+      const uint32_t at = ring_at + stage * S::kStage;
+      stage = stage == S::kStages - 1 ? 0 : stage + 1;
       if (!here) continue;
-      const uint32_t stage = ring_at + i % S::kStages * S::kStage;
       // scores: tokens gr, gr + 8, heads tc, tc + 1; two chains of products
       float s[NT][2][4];
 #pragma unroll
@@ -241,7 +252,7 @@ __global__ void __launch_bounds__(Shape<DP, NT>::kWarps * 32, Shape<DP, NT>::kCt
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         uint32_t a[4];
-        load4(a, stage + key_at + k * 32);
+        load4(a, at + key_at + k * 32);
 #pragma unroll
         for (int j = 0; j < NT; ++j) mma<T>(s[j][k & 1], a, q[j][k][0], q[j][k][1]);
       }
@@ -292,7 +303,7 @@ __global__ void __launch_bounds__(Shape<DP, NT>::kWarps * 32, Shape<DP, NT>::kCt
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         uint32_t a[4];
-        load4_transposed(a, stage + value_at + k * 32);
+        load4_transposed(a, at + value_at + k * 32);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           mma<T>(o[j][k], a, hi[j][0], hi[j][1]);
@@ -301,10 +312,11 @@ __global__ void __launch_bounds__(Shape<DP, NT>::kWarps * 32, Shape<DP, NT>::kCt
       }
     }
 
-    // the warp's state into its ring, whose copies have all landed
-    copy_wait<0>();
+    // the warp's state into the stage read last, which is copied to again only
+    // with the next tile
     __syncwarp();
-    float* state = reinterpret_cast<float*>(ring);
+    const int last = (stage == 0 ? S::kStages : stage) - 1;
+    float* state = reinterpret_cast<float*>(ring + last * S::kStage);
     constexpr int kStatePitch = attend_pitch(DP);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
@@ -327,21 +339,24 @@ __global__ void __launch_bounds__(Shape<DP, NT>::kWarps * 32, Shape<DP, NT>::kCt
         }
       }
     }
-    attend_finish<T, S::kWarps>(p, share, g, heads, reinterpret_cast<float*>(s_mem), S::kRing / 4, kStatePitch);
-    u += g.tiles;
-    if (u == share.end) break;
+    attend_finish<T, S::kWarps>(p, share, g, heads, reinterpret_cast<float*>(s_mem + last * S::kStage), S::kRing / 4,
+                                kStatePitch);
   }
 }
 
 template <class T, int DP, int NT>
 cudaError_t launch(const AttendParams& p, cudaStream_t stream) {
   using S = Shape<DP, NT>;
-  static_assert(NT * 8 * attend_pitch(DP) * 4 <= S::kRing, "a warp's state fits its ring");
+  static_assert(NT * 8 * attend_pitch(DP) * 4 <= S::kStage, "a warp's state fits a stage");
   static DeviceCache ready;  // (static storage: zero before first use)
   const cudaError_t e = allow_smem(attend_mma_kernel<T, DP, NT>, S::kSmem, ready);
   if (e != cudaSuccess) return e;
-  return attend_launch<T>(attend_mma_kernel<T, DP, NT>, p, 152 * S::kCtas, S::kWarps * 32, S::kSmem, kAttendTile * S::kWarps,
-                          stream);
+  // The beginning of a row as two tiles of 64 tokens. Measured on 64 rows of 0
+  // to 8192 tokens (their logarithms even; bf16, dim 128): counted as 0, 66.6
+  // us; 1, 49.9; 2, 48.9; 3, 48.6; with 16 query heads to a kv head 120, 74,
+  // 58 and 59. On 64 rows of 4096 tokens it costs nothing beyond the noise.
+  return attend_launch<T>(attend_mma_kernel<T, DP, NT>, p, 2, 152 * S::kCtas, S::kWarps * 32, S::kSmem,
+                          kAttendTile * S::kWarps, stream);
 }
 
 template <class T>

@@ -88,6 +88,7 @@ struct AttendParams {
   float* parts;        // partial results, [2 CTAs][block_heads][attend_pitch(dim)]
   AttendSplit* splits; // one for each CTA, or for each row and group
   int32_t tasks;       // of the join
+  int32_t start_units; // what the beginning of a row counts, in tiles
   uint8_t split_by_row;
   int32_t* status;
   uint8_t q_pairs;     // q rows may be read two 16-bit elements at a time
