@@ -1,4 +1,4 @@
-"""Build the CUDA executor library (libcmdexec.so) in-tree.
+"""Build the CUDA executor library (libcmdexec.so) in-tree, and the module that hands torch tensors to it.
 
 Each executor source compiles once per tier and op-set variant
 (CMDX_TIER, CMDX_EXT; the tile executor also per view variant, CMDX_ND):
@@ -10,9 +10,12 @@ fast-math, so denormals are kept and every add/sub/mul rounds once.
 """
 from __future__ import annotations
 
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +24,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 OBJ_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libcmdexec.so")
+# (torch's C++ interface holds for one version of it)
+TORCH_PATH = os.path.join(OUT_DIR, f"_cache_torch-{importlib.metadata.version('torch')}.so")
 
 # (source, the defines of each object built from it), longest compiles first
 def _objs(tiers, nds=(None,)):
@@ -44,6 +49,7 @@ CU_SOURCES = [("exec_tile2d.cu", _objs((2,), (0, 1))), ("exec_generic.cu", _objs
               ("static_scratch.cu", [{}]),
               ("cache_attend.cu", [{}]), ("cache_attend_mma.cu", [{}]), ("cache_rope.cu", [{}]), ("cache_pages.cu", [{}])]
 CPP_SOURCES = ["cmd_api.cpp", "cmd_yaml.cpp", "exec_host.cpp", "cache_api.cpp"]
+TORCH_SOURCE = "cache_torch.cpp"
 HEADERS = ["cmd_internal.h", "exec_common.cuh", "exec_launch.cuh", "exec_pipe.cuh", "exec_tile2d.h", "interp_asm.cuh",
            "gen_interp.py", "cache_internal.h", "cache_common.cuh", "cache_attend.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -60,14 +66,14 @@ def cuda_home() -> str:
 
 
 def _sources():
-    return ([os.path.join(CSRC, s) for s in sorted({c for c, _ in CU_SOURCES}) + CPP_SOURCES + HEADERS]
+    return ([os.path.join(CSRC, s) for s in sorted({c for c, _ in CU_SOURCES}) + CPP_SOURCES + [TORCH_SOURCE] + HEADERS]
             + [os.path.join(ROOT, "include", h) for h in ("cmd.h", "cmd_cache.h")] + [os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(TORCH_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(TORCH_PATH))
     return all(os.path.getmtime(s) <= t for s in _sources())
 
 
@@ -100,6 +106,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
         cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-Wno-unused-parameter",
                "-c", os.path.join(CSRC, s), "-o", obj] + inc
         jobs.append((cmd, obj, None))
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch_obj = os.path.join(OBJ_DIR, TORCH_SOURCE + ".o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c", os.path.join(CSRC, TORCH_SOURCE), "-o", torch_obj,
+           "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(torch_dir, "include"), "-isystem",
+           os.path.join(torch_dir, "include", "torch", "csrc", "api", "include")] + inc
+    jobs.append((cmd, torch_obj, None))
 
     def run(job):
         cmd, obj, log = job
@@ -114,13 +126,20 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     with ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
-        objs = list(ex.map(run, jobs))
+        objs = [o for o in ex.map(run, jobs) if o != torch_obj]
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     link = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcudart_static", "-lrt", "-lpthread", "-ldl"]
     r = subprocess.run(link, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed: {' '.join(link)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    tmp = TORCH_PATH + f".tmp{os.getpid()}"
+    link = (["g++", "-shared", "-o", tmp, torch_obj, "-L" + os.path.join(torch_dir, "lib"), "-L" + OUT_DIR]
+            + ["-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-l:libcmdexec.so", "-Wl,-rpath,$ORIGIN"])
+    r = subprocess.run(link, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed: {' '.join(link)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TORCH_PATH)
     return LIB_PATH
 
 
