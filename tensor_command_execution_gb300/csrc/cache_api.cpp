@@ -566,9 +566,8 @@ extern "C" cmd_status cmd_attention_decode(const cmd_attention_args* args, void*
     p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kSplitBytes);
     p.status = a.status;
     const int es = elem_size(a.q.dtype);
-    // the tensor units take 16-bit caches whose rows are whole 16-byte vectors
-    const bool mma = es == 2 && dim > 0 && dim % 8 == 0 && vector_rows(a.k_cache, 16) && vector_rows(a.v_cache, 16);
-    const int most = mma ? cmdx::kAttendMmaHeads : cmdx::kAttendSimtHeads;
+    const bool vectors = dim > 0 && dim * es % 16 == 0 && vector_rows(a.k_cache, 16) && vector_rows(a.v_cache, 16);
+    const int most = vectors && es == 2 ? cmdx::kAttendMmaHeads : cmdx::kAttendHeads;
     p.blocks = (p.group + most - 1) / most;
     p.block_heads = (p.group + p.blocks - 1) / p.blocks;
     p.q_pairs = vector_rows(a.q, 4);
@@ -582,7 +581,9 @@ extern "C" cmd_status cmd_attention_decode(const cmd_attention_args* args, void*
       p.tables = static_cast<const int32_t*>(a.tables.ptr) + r * a.tables.strides[0];
       p.lengths = static_cast<const int32_t*>(a.lengths.ptr) + r * a.lengths.strides[0];
       const cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
-      const cudaError_t e = mma ? cmdx::attend_mma_launch(a.q.dtype, p, stream) : cmdx::attend_simt_launch(a.q.dtype, p, stream);
+      const cudaError_t e = !vectors  ? cmdx::attend_simt_launch(a.q.dtype, p, stream)
+                            : es == 2 ? cmdx::attend_mma_launch(a.q.dtype, p, stream)
+                                      : cmdx::attend_f32_launch(p, stream);
       if (e != cudaSuccess) return launched(e);
     }
     return CMD_OK;

@@ -1,15 +1,15 @@
 // cache_attend.cu - attention of one new token per sequence over a paged
-// cache, on the general-purpose units: 32-bit numbers, and 16-bit ones whose
-// rows are not 16-byte vectors (cache_attend_mma.cu takes the others).
+// cache of any alignment, strides and head dim: what cache_attend_mma.cu and
+// cache_attend_f32.cu, which copy rows in 16-byte pieces, cannot take.
 //
 // out = sum_t exp(s_t - lse) v_t, s_t = scale q . k_t, one pass over the
-// tokens with a running maximum. Bound by memory: each key and value is read
-// once for all query heads that share it. A warp takes kStep tokens at a
-// time, a lane VEC elements of the head dim, straight from memory to
-// registers; the kStep * GT dot products (GT query heads) are summed over the
-// lanes by a transposing butterfly that leaves each lane one finished score
-// (31 shuffles for 32 scores rather than 5 each), where scaling, the cap, the
-// mask and the exponential are then done once.
+// tokens with a running maximum. A warp takes kStep tokens at a time, a lane
+// VEC elements of the head dim, straight from memory to registers; the kStep *
+// GT dot products (GT query heads) are summed over the lanes by a transposing
+// butterfly that leaves each lane one finished score (31 shuffles for 32
+// scores rather than 5 each), where scaling, the cap, the mask and the
+// exponential are then done once. Bound by the latency of its loads, element
+// by element or (where rows allow it) 2 or 4 at a time.
 #include "cache_attend.cuh"
 
 namespace cmdx {
@@ -17,6 +17,7 @@ namespace cmdx {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kTokens = 16;  // of a warp's tile
 constexpr int kRowsBytes = (sizeof(AttendRows) + 15) / 16 * 16;
 
 // VEC elements of a row for this lane (element 4 lane + 128 j + i for VEC 4
@@ -53,7 +54,7 @@ __global__ void __launch_bounds__(kWarps * 32) attend_simt_kernel(const __grid_c
   AttendRows& s_rows = *reinterpret_cast<AttendRows*>(s_mem);
   float(*s_state)[GT][kPitch] = reinterpret_cast<float(*)[GT][kPitch]>(s_mem + kRowsBytes);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int tile = kAttendTile * kWarps;
+  constexpr int tile = kTokens * kWarps;
   pdl_wait();
   pdl_trigger();
   AttendShare share;
@@ -76,8 +77,8 @@ __global__ void __launch_bounds__(kWarps * 32) attend_simt_kernel(const __grid_c
     const int my_token = lane / kDup / GT;
     float m = -CUDART_INF_F, l = 0.0f;
     for (int i = 0; i < g.tiles; ++i) {
-      const int t0 = (g.tile0 + i) * tile + warp * kAttendTile;
-      for (int t = max(t0, g.lo / kStep * kStep); t < min(t0 + kAttendTile, g.n); t += kStep) {
+      const int t0 = (g.tile0 + i) * tile + warp * kTokens;
+      for (int t = max(t0, g.lo / kStep * kStep); t < min(t0 + kTokens, g.n); t += kStep) {
         float k[kStep][VEC], v[kStep][VEC];
         bool bad = false;
         bool seen[kStep];
@@ -184,7 +185,7 @@ cudaError_t launch(const AttendParams& p, cudaStream_t stream) {
   static DeviceCache ready;  // (static storage: zero before first use)
   const cudaError_t e = allow_smem(attend_simt_kernel<T, GT, VEC>, smem, ready);
   if (e != cudaSuccess) return e;
-  return attend_launch<T>(attend_simt_kernel<T, GT, VEC>, p, 0, 2 * 152, kWarps * 32, smem, kAttendTile * kWarps, stream);
+  return attend_launch<T>(attend_simt_kernel<T, GT, VEC>, p, 0, 2 * 152, kWarps * 32, smem, kTokens * kWarps, stream);
 }
 
 template <class T, int GT>
@@ -195,8 +196,7 @@ cudaError_t launch_dim(const AttendParams& p, cudaStream_t stream) {
 
 template <class T>
 cudaError_t launch_type(const AttendParams& p, cudaStream_t stream) {
-  if (p.block_heads == 1) return launch_dim<T, 1>(p, stream);
-  return p.block_heads <= 4 ? launch_dim<T, 4>(p, stream) : launch_dim<T, 8>(p, stream);
+  return p.block_heads == 1 ? launch_dim<T, 1>(p, stream) : launch_dim<T, 8>(p, stream);
 }
 
 }  // namespace

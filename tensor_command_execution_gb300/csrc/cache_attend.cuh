@@ -2,7 +2,7 @@
 // shared by its kernels.
 //
 // A unit of work is a tile of tokens of one row, for one kv head and a block
-// of the query heads that share it; a CTA's warps take 16 tokens of it each.
+// of the query heads that share it; a CTA's warps share its tokens.
 // The units of a launch, ordered by row, then head, then token, are cut into
 // equal runs, one for each CTA, whatever the rows' lengths: no CTA waits for a
 // long row. The beginning of a row counts as start_units more units (before

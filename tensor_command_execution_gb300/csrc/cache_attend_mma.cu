@@ -18,23 +18,11 @@
 // apart: rounding p itself to 16 bits would add an error as large as the
 // output's own rounding. Tokens outside the row are filled with zeros as they
 // are copied, whatever their slots hold.
-#include "cache_attend.cuh"
+#include "cache_attend_ring.cuh"
 
 namespace cmdx {
 
 namespace {
-
-__device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
-
-// 16 bytes to shared memory, or 16 zero bytes where !take
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool take) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 __device__ __forceinline__ void load4(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -74,128 +62,40 @@ __device__ __forceinline__ void split(float x, float y, uint32_t* hi, uint32_t* 
   *lo = *reinterpret_cast<uint32_t*>(l);
 }
 
-// 2^x for x <= 0 (a result below 2^-126 is 0)
-__device__ __forceinline__ float power_of_two(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
+constexpr int kTokens = 16;  // of a warp's tile
+constexpr int kWarps = 4;
 
-// Warps of a CTA, stages of each warp's ring, and CTAs of an SM, for heads of
-// up to DP dims.
-template <int DP, int NT>
+// Stages of each warp's ring, and CTAs of an SM, for heads of up to DP dims.
+template <class T, int DP, int NT>
 struct Shape {
-  static constexpr int kWarps = 4;
   static constexpr int kStages = DP == 64 ? 3 : 2;
   static constexpr int kCtas = DP == 256 ? 1 : NT == 2 ? 2 : 3;
   static constexpr int kPitch = DP * 2 + 16;                   // bytes of a row: an odd number of 16
-  static constexpr int kStage = 2 * kAttendTile * kPitch;      // keys, then values
-  static constexpr int kRing = kStages * kStage;
-  static constexpr int kSmem = kWarps * kRing + (int)sizeof(AttendRows);
+  using Ring = AttendRing<T, kTokens, DP / 8, kPitch, kStages, kWarps>;
+  static constexpr int kSmem = kWarps * Ring::kBytes + (int)sizeof(AttendRows);
 };
 
 template <class T, int DP, int NT>
-__global__ void __launch_bounds__(Shape<DP, NT>::kWarps * 32, Shape<DP, NT>::kCtas) attend_mma_kernel(const __grid_constant__ AttendParams p) {
-  using S = Shape<DP, NT>;
-  constexpr int kChunks = DP / 8;              // 16-byte pieces of a row
-  constexpr int kRowsAtOnce = 32 / kChunks;    // rows that one copy of the warp covers
+__global__ void __launch_bounds__(kWarps * 32, Shape<T, DP, NT>::kCtas) attend_mma_kernel(const __grid_constant__ AttendParams p) {
+  using S = Shape<T, DP, NT>;
+  using Ring = typename S::Ring;
   constexpr int KS = DP / 16;
   extern __shared__ __align__(16) unsigned char s_mem[];
-  AttendRows& s_rows = *reinterpret_cast<AttendRows*>(s_mem + S::kWarps * S::kRing);
+  AttendRows& s_rows = *reinterpret_cast<AttendRows*>(s_mem + kWarps * Ring::kBytes);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int tile = kAttendTile * S::kWarps;
-  unsigned char* ring = s_mem + warp * S::kRing;
-  const uint32_t ring_at = smem_addr(ring);
-  // this lane's places: its chunk and first row in a copy; its row and chunk
-  // in the two kinds of fragment loads; its row g and columns 2 t, 2 t + 1 in
-  // an 8 by 8 block
-  const int chunk = lane % kChunks, copy_row = lane / kChunks;
+  // this lane's row and 16-byte piece in the two kinds of fragment loads; its
+  // row gr and columns tc, tc + 1 in an 8 by 8 block
   const uint32_t key_at = (lane & 15) * S::kPitch + (lane >> 4) * 16;
-  const uint32_t value_at = ((lane >> 4) * 8 + (lane & 7)) * S::kPitch + ((lane >> 3) & 1) * 16 + kAttendTile * S::kPitch;
+  const uint32_t value_at = ((lane >> 4) * 8 + (lane & 7)) * S::kPitch + ((lane >> 3) & 1) * 16 + Ring::kKeys;
   const int gr = lane >> 2, tc = (lane & 3) * 2;
 
   pdl_wait();
   pdl_trigger();
   AttendShare share;
-  if (!attend_begin<T>(p, s_rows, tile, &share)) return;
-  const bool in_dim = chunk * 8 < p.dim;
-  const bool one_page = p.page.d % kAttendTile == 0;  // a tile lies in one page
-
-  // The copies run ahead of the products, across the ends of segments: `next`
-  // is the tile to copy next (the page and slot of this lane's token lane %
-  // 16, -1 for none, and the head's keys and values), whose table entry was
-  // read a tile earlier; `look` is the segment of the one after.
-  AttendSegment g = attend_first(p, s_rows, share, tile);
-  AttendSegment look = g;
-  int look_at = -1;
-  const int32_t* table = nullptr;
-  struct {
-    int page, slot;
-    const T *k, *v;
-  } next = {-1, 0, nullptr, nullptr};
-  auto look_up = [&]() {
-    next.page = -1;
-    if (look_at < 0 || look_at == look.tiles) {
-      if (look_at > 0) look = attend_next(p, s_rows, share, look, tile);
-      look_at = 0;
-      if (look.tiles == 0) return;
-      table = p.tables + look.row * p.table_st[0];
-      const int head = look.group / p.blocks;
-      next.k = static_cast<const T*>(p.k) + chunk * 8 + head * p.k_st[2];
-      next.v = static_cast<const T*>(p.v) + chunk * 8 + head * p.v_st[2];
-    }
-    const int token = (look.tile0 + look_at) * tile + warp * kAttendTile + (lane & 15);
-    const uint32_t column = fast_div32(p.page, (uint32_t)token);
-    next.slot = token - (int)(column * p.page.d);
-    if (token >= look.lo && token < look.n) {
-      const int page = __ldg(table + column * p.table_st[1]);
-      if (page < 0 || page >= p.n_pages) report(p.status, CMD_CACHE_BAD_PAGE);
-      else next.page = page;
-    }
-    ++look_at;
-  };
-  // Copies the next tile into a stage. Returns which of its tokens have a
-  // page, a bit each.
-  auto copy_next = [&](int stage) {
-    const uint32_t known = __ballot_sync(~0u, next.page >= 0) & 0xffffu;
-    if (known) {
-      const uint32_t dst = ring_at + stage * S::kStage + copy_row * S::kPitch + chunk * 16;
-      if (one_page) {
-        const int64_t page = __shfl_sync(~0u, next.page, __ffs(known) - 1);
-        const int64_t slot = __shfl_sync(~0u, next.slot, 0) + copy_row;
-        const T* k = next.k + page * p.k_st[0] + slot * p.k_st[1];
-        const T* v = next.v + page * p.v_st[0] + slot * p.v_st[1];
-#pragma unroll
-        for (int r = 0; r < kAttendTile; r += kRowsAtOnce) {
-          const bool take = in_dim && (known >> (r + copy_row) & 1);
-          copy16(dst + r * S::kPitch, take ? k + r * p.k_st[1] : p.k, take);
-          copy16(dst + (r + kAttendTile) * S::kPitch, take ? v + r * p.v_st[1] : p.v, take);
-        }
-      } else {
-#pragma unroll
-        for (int r = 0; r < kAttendTile; r += kRowsAtOnce) {
-          const int64_t page = __shfl_sync(~0u, next.page, r + copy_row);
-          const int64_t slot = __shfl_sync(~0u, next.slot, r + copy_row);
-          const bool take = in_dim && page >= 0;
-          copy16(dst + r * S::kPitch, take ? next.k + page * p.k_st[0] + slot * p.k_st[1] : p.k, take);
-          copy16(dst + (r + kAttendTile) * S::kPitch, take ? next.v + page * p.v_st[0] + slot * p.v_st[1] : p.v, take);
-        }
-      }
-    }
-    copy_commit();
-    return known;
-  };
-
-  uint32_t known[S::kStages];  // of the tiles on their way, the nearest first
-  look_up();
-#pragma unroll
-  for (int i = 0; i < S::kStages - 1; ++i) {
-    known[i] = copy_next(i);
-    look_up();
-  }
-
-  int stage = 0;
-  for (; g.tiles; g = attend_next(p, s_rows, share, g, tile)) {
+  if (!attend_begin<T>(p, s_rows, Ring::kTile, &share)) return;
+  AttendSegment g = attend_first(p, s_rows, share, Ring::kTile);
+  Ring ring(p, s_rows, share, g, s_mem + warp * Ring::kBytes);
+  for (; g.tiles; g = attend_next(p, s_rows, share, g, Ring::kTile)) {
     const AttendHeads heads = attend_heads(p, g.group);
     // the query heads of this block, as the right side of K q^T
     uint32_t q[NT][KS][2];
@@ -233,16 +133,10 @@ __global__ void __launch_bounds__(Shape<DP, NT>::kWarps * 32, Shape<DP, NT>::kCt
     }
 
     for (int i = 0; i < g.tiles; ++i) {
-      copy_wait<S::kStages - 2>();
-      __syncwarp();
-      known[S::kStages - 1] = copy_next(stage == 0 ? S::kStages - 1 : stage - 1);
-      look_up();
-      const uint32_t here = known[0];
-#pragma unroll
-      for (int j = 0; j < S::kStages - 1; ++j) known[j] = known[j + 1];
-      const uint32_t at = ring_at + stage * S::kStage;
-      stage = stage == S::kStages - 1 ? 0 : stage + 1;
+      int index;
+      const uint32_t here = ring.next_tile(&index);
       if (!here) continue;
+      const uint32_t at = ring.at + index * Ring::kStage;
       // scores: tokens gr, gr + 8, heads tc, tc + 1; two chains of products
       float s[NT][2][4];
 #pragma unroll
@@ -315,8 +209,8 @@ __global__ void __launch_bounds__(Shape<DP, NT>::kWarps * 32, Shape<DP, NT>::kCt
     // the warp's state into the stage read last, which is copied to again only
     // with the next tile
     __syncwarp();
-    const int last = (stage == 0 ? S::kStages : stage) - 1;
-    float* state = reinterpret_cast<float*>(ring + last * S::kStage);
+    unsigned char* states = s_mem + ring.free_stage() * Ring::kStage;
+    float* state = reinterpret_cast<float*>(states + warp * Ring::kBytes);
     constexpr int kStatePitch = attend_pitch(DP);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
@@ -339,15 +233,14 @@ __global__ void __launch_bounds__(Shape<DP, NT>::kWarps * 32, Shape<DP, NT>::kCt
         }
       }
     }
-    attend_finish<T, S::kWarps>(p, share, g, heads, reinterpret_cast<float*>(s_mem + last * S::kStage), S::kRing / 4,
-                                kStatePitch);
+    attend_finish<T, kWarps>(p, share, g, heads, reinterpret_cast<float*>(states), Ring::kBytes / 4, kStatePitch);
   }
 }
 
 template <class T, int DP, int NT>
 cudaError_t launch(const AttendParams& p, cudaStream_t stream) {
-  using S = Shape<DP, NT>;
-  static_assert(NT * 8 * attend_pitch(DP) * 4 <= S::kStage, "a warp's state fits a stage");
+  using S = Shape<T, DP, NT>;
+  static_assert(NT * 8 * attend_pitch(DP) * 4 <= S::Ring::kStage, "a warp's state fits a stage");
   static DeviceCache ready;  // (static storage: zero before first use)
   const cudaError_t e = allow_smem(attend_mma_kernel<T, DP, NT>, S::kSmem, ready);
   if (e != cudaSuccess) return e;
@@ -355,8 +248,7 @@ cudaError_t launch(const AttendParams& p, cudaStream_t stream) {
   // to 8192 tokens (their logarithms even; bf16, dim 128): counted as 0, 66.6
   // us; 1, 49.9; 2, 48.9; 3, 48.6; with 16 query heads to a kv head 120, 74,
   // 58 and 59. On 64 rows of 4096 tokens it costs nothing beyond the noise.
-  return attend_launch<T>(attend_mma_kernel<T, DP, NT>, p, 2, 152 * S::kCtas, S::kWarps * 32, S::kSmem,
-                          kAttendTile * S::kWarps, stream);
+  return attend_launch<T>(attend_mma_kernel<T, DP, NT>, p, 2, 152 * S::kCtas, kWarps * 32, S::kSmem, S::Ring::kTile, stream);
 }
 
 template <class T>

@@ -57,7 +57,6 @@ cudaError_t rope_launch(int dtype, int layout, bool vec, const RopeParams& p, cu
 // ---- attention of one token (cache_attend*.cu) --------------------------------
 constexpr int kAttendMaxCtas = 152 * 4;  // bounds the workspace
 constexpr int kAttendRows = 512;         // rows of one launch (the host splits larger calls)
-constexpr int kAttendTile = 16;          // tokens a warp takes at a time
 
 // A row (for one kv head and block of query heads) whose tiles went to several
 // CTAs: part k lies at index `first` for k = 0, (first & ~1) + 2 k after.
@@ -97,9 +96,11 @@ struct AttendParams {
 
 // any types, alignment and strides; at most 8 query heads of a block
 cudaError_t attend_simt_launch(int dtype, const AttendParams& p, cudaStream_t stream);
-// 16-bit types whose cache rows are whole 16-byte vectors; at most 16 query heads of a block
+// types whose cache rows are whole 16-byte vectors: 32-bit, at most 8 query
+// heads of a block; 16-bit, at most 16
+cudaError_t attend_f32_launch(const AttendParams& p, cudaStream_t stream);
 cudaError_t attend_mma_launch(int dtype, const AttendParams& p, cudaStream_t stream);
-constexpr int kAttendSimtHeads = 8, kAttendMmaHeads = 16;
+constexpr int kAttendHeads = 8, kAttendMmaHeads = 16;
 
 // ---- pages (cache_pages.cu) -----------------------------------------------------
 struct PoolList {
