@@ -26,9 +26,11 @@ struct Failure {
   cmd_status status;
   std::string message;
 };
-void need(bool ok, cmd_status s, const std::string& msg) {
-  if (!ok) throw Failure{s, msg};
-}
+// (a macro: the message is put together only when the check fails)
+#define NEED(ok, status, msg) \
+  do {                        \
+    if (!(ok)) throw Failure{status, msg}; \
+  } while (0)
 
 // Runs f, turning failures (and anything else thrown) into a status.
 template <class F>
@@ -57,7 +59,7 @@ int64_t last_offset(const cmd_operand& o, const char* name) {
     if (o.sizes[d] == 0) return -1;
     last += (__int128)(o.sizes[d] - 1) * o.strides[d];
   }
-  need(last < ((__int128)1 << 60), CMD_ERR_SHAPE, std::string(name) + " extends past the address space");
+  NEED(last < ((__int128)1 << 60), CMD_ERR_SHAPE, std::string(name) + " extends past the address space");
   return (int64_t)last;
 }
 
@@ -69,28 +71,28 @@ bool empty(const cmd_operand& o) {
 
 // Checks that hold for every operand: rank, sizes, strides, pointer.
 void check(const cmd_operand& o, const char* name, int rank, bool has_dim = false) {
-  need(o.rank == rank, CMD_ERR_SHAPE, std::string(name) + " has rank " + std::to_string(o.rank) + ", not " +
+  NEED(o.rank == rank, CMD_ERR_SHAPE, std::string(name) + " has rank " + std::to_string(o.rank) + ", not " +
                                           std::to_string(rank));
   for (int d = 0; d < rank; ++d) {
-    need(o.sizes[d] >= 0, CMD_ERR_SHAPE, std::string(name) + " has a negative size");
-    need(o.strides[d] >= 0, CMD_ERR_SHAPE, std::string(name) + " has a negative stride (strides must be >= 0)");
+    NEED(o.sizes[d] >= 0, CMD_ERR_SHAPE, std::string(name) + " has a negative size");
+    NEED(o.strides[d] >= 0, CMD_ERR_SHAPE, std::string(name) + " has a negative stride (strides must be >= 0)");
   }
-  need(o.ptr || empty(o), CMD_ERR_NULL, std::string(name) + " is NULL");
-  need(reinterpret_cast<uintptr_t>(o.ptr) % elem_size(o.dtype) == 0, CMD_ERR_ALIGN,
+  NEED(o.ptr || empty(o), CMD_ERR_NULL, std::string(name) + " is NULL");
+  NEED(reinterpret_cast<uintptr_t>(o.ptr) % elem_size(o.dtype) == 0, CMD_ERR_ALIGN,
        std::string(name) + " is not aligned to its element size");
   if (has_dim)
-    need(o.sizes[rank - 1] <= 1 || o.strides[rank - 1] == 1, CMD_ERR_SHAPE,
+    NEED(o.sizes[rank - 1] <= 1 || o.strides[rank - 1] == 1, CMD_ERR_SHAPE,
          std::string(name) + " needs a unit stride along its last dim");
   last_offset(o, name);
 }
 
 void check_type(const cmd_operand& o, const char* name, int dtype) {
-  need(o.dtype == dtype, CMD_ERR_TYPE, std::string(name) + " has another element type than its call needs");
+  NEED(o.dtype == dtype, CMD_ERR_TYPE, std::string(name) + " has another element type than its call needs");
 }
 
 void check_sizes(const cmd_operand& o, const char* name, const int64_t* sizes) {
   for (int d = 0; d < o.rank; ++d)
-    need(o.sizes[d] == sizes[d], CMD_ERR_SHAPE, std::string(name) + " has size " + std::to_string(o.sizes[d]) +
+    NEED(o.sizes[d] == sizes[d], CMD_ERR_SHAPE, std::string(name) + " has size " + std::to_string(o.sizes[d]) +
                                                     " in dim " + std::to_string(d) + ", not " + std::to_string(sizes[d]));
 }
 
@@ -113,7 +115,7 @@ void check_distinct(const cmd_operand& o, const char* name) {
   int64_t reach = 0;
   for (int i = 0; i < n; ++i) {
     const int d = order[i];
-    need(o.strides[d] > reach, CMD_ERR_ALIAS, std::string(name) + " is written and overlaps itself");
+    NEED(o.strides[d] > reach, CMD_ERR_ALIAS, std::string(name) + " is written and overlaps itself");
     reach += (o.sizes[d] - 1) * o.strides[d];
   }
 }
@@ -203,12 +205,12 @@ bool vector_rows(const cmd_operand& o, int bytes) {
 }
 
 void check_rope(const cmd_rope_spec& r, int64_t dim) {
-  need(r.layout == CMD_ROPE_HALF || r.layout == CMD_ROPE_INTERLEAVED, CMD_ERR_ARG, "unknown rope layout");
-  need(r.n_pairs >= 0 && 2 * (int64_t)r.n_pairs <= dim, CMD_ERR_SHAPE, "more rotated elements than the head has");
-  need(std::isfinite(r.scale), CMD_ERR_ARG, "the rope scale is not finite");
+  NEED(r.layout == CMD_ROPE_HALF || r.layout == CMD_ROPE_INTERLEAVED, CMD_ERR_ARG, "unknown rope layout");
+  NEED(r.n_pairs >= 0 && 2 * (int64_t)r.n_pairs <= dim, CMD_ERR_SHAPE, "more rotated elements than the head has");
+  NEED(std::isfinite(r.scale), CMD_ERR_ARG, "the rope scale is not finite");
   if (r.n_pairs > 0) {
-    need(r.turns != nullptr, CMD_ERR_NULL, "turns is NULL");
-    need(reinterpret_cast<uintptr_t>(r.turns) % 8 == 0, CMD_ERR_ALIGN, "turns is not 8-byte aligned");
+    NEED(r.turns != nullptr, CMD_ERR_NULL, "turns is NULL");
+    NEED(reinterpret_cast<uintptr_t>(r.turns) % 8 == 0, CMD_ERR_ALIGN, "turns is not 8-byte aligned");
   }
 }
 
@@ -257,25 +259,25 @@ void rope_common(cmdx::RopeParams& p, const cmd_rope_spec& r, int64_t dim) {
   p.n_streams = n;
 }
 
-void check_heads(int64_t heads) { need(heads <= 65536, CMD_ERR_LIMIT, "more than 65536 heads"); }
+void check_heads(int64_t heads) { NEED(heads <= 65536, CMD_ERR_LIMIT, "more than 65536 heads"); }
 
 }  // namespace
 
 extern "C" cmd_status cmd_rope_turns(int32_t n_pairs, double base, int32_t scaling, double factor,
                                      double original_length, double beta_fast, double beta_slow, uint64_t* turns) {
   return guarded([&]() -> cmd_status {
-    need(n_pairs >= 0, CMD_ERR_SHAPE, "negative number of pairs");
-    need(turns || n_pairs == 0, CMD_ERR_NULL, "turns is NULL");
-    need(std::isfinite(base) && (base > 1.0 || (base >= 1.0 && n_pairs <= 1)), CMD_ERR_ARG, "the base must be above 1");
-    need(scaling >= CMD_ROPE_SCALING_NONE && scaling <= CMD_ROPE_SCALING_PARTS, CMD_ERR_ARG, "unknown scaling");
+    NEED(n_pairs >= 0, CMD_ERR_SHAPE, "negative number of pairs");
+    NEED(turns || n_pairs == 0, CMD_ERR_NULL, "turns is NULL");
+    NEED(std::isfinite(base) && (base > 1.0 || (base >= 1.0 && n_pairs <= 1)), CMD_ERR_ARG, "the base must be above 1");
+    NEED(scaling >= CMD_ROPE_SCALING_NONE && scaling <= CMD_ROPE_SCALING_PARTS, CMD_ERR_ARG, "unknown scaling");
     if (scaling != CMD_ROPE_SCALING_NONE)
-      need(std::isfinite(factor) && factor >= 1.0, CMD_ERR_ARG, "the scaling factor must be at least 1");
+      NEED(std::isfinite(factor) && factor >= 1.0, CMD_ERR_ARG, "the scaling factor must be at least 1");
     const double two_pi = 6.283185307179586476925;
     double lo = 0.0, hi = 0.0;
     if (scaling == CMD_ROPE_SCALING_BASE)
       base *= n_pairs > 1 ? std::pow(factor, (double)n_pairs / (n_pairs - 1)) : factor;
     if (scaling == CMD_ROPE_SCALING_PARTS) {
-      need(std::isfinite(original_length) && original_length > 0 && std::isfinite(beta_fast) && beta_slow > 0 &&
+      NEED(std::isfinite(original_length) && original_length > 0 && std::isfinite(beta_fast) && beta_slow > 0 &&
                beta_fast > beta_slow,
            CMD_ERR_ARG, "scaling by parts needs original_length > 0 and beta_fast > beta_slow > 0");
       // the pair that makes `beta` turns over original_length: a real index
@@ -303,7 +305,7 @@ extern "C" cmd_status cmd_rope(const cmd_operand* q, const cmd_operand* q_out, c
                                const cmd_operand* k_out, const cmd_operand* positions, const cmd_rope_spec* rope,
                                void* cuda_stream) {
   return guarded([&]() -> cmd_status {
-    need(positions && rope, CMD_ERR_NULL, "positions or rope is NULL");
+    NEED(positions && rope, CMD_ERR_NULL, "positions or rope is NULL");
     cmdx::RopeParams p;
     std::memset(&p, 0, sizeof p);
     const cmd_operand* ins[2] = {q, k};
@@ -314,20 +316,20 @@ extern "C" cmd_status cmd_rope(const cmd_operand* q, const cmd_operand* q_out, c
     for (int j = 0; j < 2; ++j) {
       if (!ins[j]) continue;
       const cmd_operand& in = *ins[j];
-      need(outs[j], CMD_ERR_NULL, std::string(names[j][1]) + " is NULL");
+      NEED(outs[j], CMD_ERR_NULL, std::string(names[j][1]) + " is NULL");
       const cmd_operand& out = *outs[j];
-      need(in.rank == 3 || in.rank == 4, CMD_ERR_SHAPE, std::string(names[j][0]) + " needs rank 3 or 4");
+      NEED(in.rank == 3 || in.rank == 4, CMD_ERR_SHAPE, std::string(names[j][0]) + " needs rank 3 or 4");
       check(in, names[j][0], in.rank, true);
       check(out, names[j][1], in.rank, true);
-      need(is_float(in.dtype), CMD_ERR_TYPE, std::string(names[j][0]) + " is no float tensor");
+      NEED(is_float(in.dtype), CMD_ERR_TYPE, std::string(names[j][0]) + " is no float tensor");
       check_type(out, names[j][1], in.dtype);
       check_sizes(out, names[j][1], in.sizes);
       check_distinct(out, names[j][1]);
       if (like) {
         check_type(in, names[j][0], like->dtype);
-        need(in.rank == like->rank, CMD_ERR_SHAPE, "q and k differ in rank");
+        NEED(in.rank == like->rank, CMD_ERR_SHAPE, "q and k differ in rank");
         for (int d = 0; d < in.rank; ++d)
-          need(d == in.rank - 2 || in.sizes[d] == like->sizes[d], CMD_ERR_SHAPE, "q and k differ in tokens or dim");
+          NEED(d == in.rank - 2 || in.sizes[d] == like->sizes[d], CMD_ERR_SHAPE, "q and k differ in tokens or dim");
       }
       like = &in;
       check_apart(out, names[j][1], in, names[j][0], true);
@@ -337,7 +339,7 @@ extern "C" cmd_status cmd_rope(const cmd_operand* q, const cmd_operand* q_out, c
       vec = vec && vector_rows(in, 16) && vector_rows(out, 16);
       p.s[p.n_streams++] = rope_stream(in, out, true, false);
     }
-    need(like, CMD_ERR_NULL, "q and k are both absent");
+    NEED(like, CMD_ERR_NULL, "q and k are both absent");
     if (q && k) {
       check_apart(*q_out, "q_out", *k, "k");
       check_apart(*k_out, "k_out", *q, "q");
@@ -348,15 +350,15 @@ extern "C" cmd_status cmd_rope(const cmd_operand* q, const cmd_operand* q_out, c
     check_type(*positions, "positions", CMD_I32);
     check_sizes(*positions, "positions", like->sizes);
     const int64_t dim = like->sizes[like->rank - 1];
-    need(dim <= CMD_CACHE_MAX_DIM, CMD_ERR_LIMIT, "a head dim above 256");
+    NEED(dim <= CMD_CACHE_MAX_DIM, CMD_ERR_LIMIT, "a head dim above 256");
     check_rope(*rope, dim);
     p.batch = 1;
     p.tokens = like->sizes[like->rank - 3];
     if (like->rank == 4) {
-      need(like->sizes[0] <= 0x7fffffff, CMD_ERR_LIMIT, "batch above 2^31");
+      NEED(like->sizes[0] <= 0x7fffffff, CMD_ERR_LIMIT, "batch above 2^31");
       p.batch = (int32_t)like->sizes[0];
     }
-    need((__int128)p.batch * p.tokens <= 0x7fffffff, CMD_ERR_LIMIT, "more than 2^31 - 1 tokens");
+    NEED((__int128)p.batch * p.tokens <= 0x7fffffff, CMD_ERR_LIMIT, "more than 2^31 - 1 tokens");
     p.positions = static_cast<const int32_t*>(positions->ptr);
     p.pos_st[0] = lead == 2 ? positions->strides[0] : 0;
     p.pos_st[1] = positions->strides[lead - 1];
@@ -374,17 +376,17 @@ namespace {
 void check_cache(const cmd_operand& k_cache, const cmd_operand& v_cache, const cmd_operand& tables) {
   check(k_cache, "k_cache", 4, true);
   check(v_cache, "v_cache", 4, true);
-  need(is_float(k_cache.dtype), CMD_ERR_TYPE, "k_cache is no float tensor");
+  NEED(is_float(k_cache.dtype), CMD_ERR_TYPE, "k_cache is no float tensor");
   check_type(v_cache, "v_cache", k_cache.dtype);
   check_sizes(v_cache, "v_cache", k_cache.sizes);
-  need(k_cache.sizes[0] <= 0x7fffffff, CMD_ERR_LIMIT, "more than 2^31 - 1 pages");
-  need(k_cache.sizes[1] >= 1, CMD_ERR_SHAPE, "a page holds no token");
-  need(k_cache.sizes[3] <= CMD_CACHE_MAX_DIM, CMD_ERR_LIMIT, "a head dim above 256");
+  NEED(k_cache.sizes[0] <= 0x7fffffff, CMD_ERR_LIMIT, "more than 2^31 - 1 pages");
+  NEED(k_cache.sizes[1] >= 1, CMD_ERR_SHAPE, "a page holds no token");
+  NEED(k_cache.sizes[3] <= CMD_CACHE_MAX_DIM, CMD_ERR_LIMIT, "a head dim above 256");
   check_heads(k_cache.sizes[2]);
   check(tables, "tables", 2);
   check_type(tables, "tables", CMD_I32);
-  need(tables.sizes[0] <= 0x7fffffff, CMD_ERR_LIMIT, "more than 2^31 - 1 table rows");
-  need((__int128)tables.sizes[1] * k_cache.sizes[1] <= 0x7fff0000, CMD_ERR_LIMIT,
+  NEED(tables.sizes[0] <= 0x7fffffff, CMD_ERR_LIMIT, "more than 2^31 - 1 table rows");
+  NEED((__int128)tables.sizes[1] * k_cache.sizes[1] <= 0x7fff0000, CMD_ERR_LIMIT,
        "table rows that reach past 2^31 - 2^16 tokens");
 }
 
@@ -392,7 +394,7 @@ void check_cache(const cmd_operand& k_cache, const cmd_operand& v_cache, const c
 
 extern "C" cmd_status cmd_cache_append(const cmd_append_args* args, void* cuda_stream) {
   return guarded([&]() -> cmd_status {
-    need(args, CMD_ERR_NULL, "args is NULL");
+    NEED(args, CMD_ERR_NULL, "args is NULL");
     const cmd_append_args& a = *args;
     check(a.k, "k", 3, true);
     check(a.v, "v", 3, true);
@@ -400,10 +402,10 @@ extern "C" cmd_status cmd_cache_append(const cmd_append_args* args, void* cuda_s
     check_type(a.k, "k", a.k_cache.dtype);
     check_type(a.v, "v", a.k_cache.dtype);
     check_sizes(a.v, "v", a.k.sizes);
-    need(a.k.sizes[1] == a.k_cache.sizes[2] && a.k.sizes[2] == a.k_cache.sizes[3], CMD_ERR_SHAPE,
+    NEED(a.k.sizes[1] == a.k_cache.sizes[2] && a.k.sizes[2] == a.k_cache.sizes[3], CMD_ERR_SHAPE,
          "k and k_cache differ in heads or dim");
     const int64_t tokens = a.k.sizes[0], dim = a.k.sizes[2];
-    need(tokens <= 0x7fffffff, CMD_ERR_LIMIT, "more than 2^31 - 1 tokens");
+    NEED(tokens <= 0x7fffffff, CMD_ERR_LIMIT, "more than 2^31 - 1 tokens");
     check(a.positions, "positions", 1);
     check_type(a.positions, "positions", CMD_I32);
     check_sizes(a.positions, "positions", &tokens);
@@ -413,7 +415,7 @@ extern "C" cmd_status cmd_cache_append(const cmd_append_args* args, void* cuda_s
       check_type(a.rows, "rows", CMD_I32);
       check_sizes(a.rows, "rows", &tokens);
     } else {
-      need(a.tables.sizes[0] == tokens, CMD_ERR_SHAPE, "rows may be absent only where each token has its own table row");
+      NEED(a.tables.sizes[0] == tokens, CMD_ERR_SHAPE, "rows may be absent only where each token has its own table row");
     }
     check_rope(a.rope, dim);
     check_distinct(a.k_cache, "k_cache");
@@ -433,10 +435,10 @@ extern "C" cmd_status cmd_cache_append(const cmd_append_args* args, void* cuda_s
     if (has_q) {
       check(a.q, "q", 3, true);
       check(a.q_out, "q_out", 3, true);
-      need(a.rope.n_pairs > 0, CMD_ERR_ARG, "q is given and nothing rotates it");
+      NEED(a.rope.n_pairs > 0, CMD_ERR_ARG, "q is given and nothing rotates it");
       check_type(a.q, "q", a.k.dtype);
       check_type(a.q_out, "q_out", a.k.dtype);
-      need(a.q.sizes[0] == tokens && a.q.sizes[2] == dim, CMD_ERR_SHAPE, "q and k differ in tokens or dim");
+      NEED(a.q.sizes[0] == tokens && a.q.sizes[2] == dim, CMD_ERR_SHAPE, "q and k differ in tokens or dim");
       check_sizes(a.q_out, "q_out", a.q.sizes);
       check_distinct(a.q_out, "q_out");
       check_heads(a.q.sizes[1]);
@@ -474,9 +476,9 @@ namespace {
 int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
 void check_workspace(const void* ws, int64_t bytes, int64_t want) {
-  need(ws, CMD_ERR_NULL, "workspace is NULL");
-  need(reinterpret_cast<uintptr_t>(ws) % 16 == 0, CMD_ERR_ALIGN, "workspace is not 16-byte aligned");
-  need(bytes >= want, CMD_ERR_LIMIT, "workspace has " + std::to_string(bytes) + " bytes, not " + std::to_string(want));
+  NEED(ws, CMD_ERR_NULL, "workspace is NULL");
+  NEED(reinterpret_cast<uintptr_t>(ws) % 16 == 0, CMD_ERR_ALIGN, "workspace is not 16-byte aligned");
+  NEED(bytes >= want, CMD_ERR_LIMIT, "workspace has " + std::to_string(bytes) + " bytes, not " + std::to_string(want));
 }
 
 constexpr int64_t kSplitBytes = cmdx::kAttendMaxCtas * sizeof(cmdx::AttendSplit);
@@ -491,10 +493,10 @@ int64_t attention_workspace(int64_t q_heads, int64_t kv_heads, int64_t dim) {
 
 extern "C" cmd_status cmd_attention_workspace(int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t* bytes) {
   return guarded([&]() -> cmd_status {
-    need(bytes, CMD_ERR_NULL, "bytes is NULL");
-    need(kv_heads >= 1 && q_heads >= 1 && q_heads % kv_heads == 0, CMD_ERR_SHAPE, "kv_heads must divide q_heads");
+    NEED(bytes, CMD_ERR_NULL, "bytes is NULL");
+    NEED(kv_heads >= 1 && q_heads >= 1 && q_heads % kv_heads == 0, CMD_ERR_SHAPE, "kv_heads must divide q_heads");
     check_heads(q_heads);
-    need(dim >= 0 && dim <= CMD_CACHE_MAX_DIM, CMD_ERR_LIMIT, "a head dim above 256");
+    NEED(dim >= 0 && dim <= CMD_CACHE_MAX_DIM, CMD_ERR_LIMIT, "a head dim above 256");
     *bytes = attention_workspace(q_heads, kv_heads, dim);
     return CMD_OK;
   });
@@ -502,7 +504,7 @@ extern "C" cmd_status cmd_attention_workspace(int32_t q_heads, int32_t kv_heads,
 
 extern "C" cmd_status cmd_attention_decode(const cmd_attention_args* args, void* cuda_stream) {
   return guarded([&]() -> cmd_status {
-    need(args, CMD_ERR_NULL, "args is NULL");
+    NEED(args, CMD_ERR_NULL, "args is NULL");
     const cmd_attention_args& a = *args;
     check(a.q, "q", 3, true);
     check(a.out, "out", 3, true);
@@ -512,10 +514,10 @@ extern "C" cmd_status cmd_attention_decode(const cmd_attention_args* args, void*
     check_sizes(a.out, "out", a.q.sizes);
     check_distinct(a.out, "out");
     const int64_t rows = a.q.sizes[0], heads = a.q.sizes[1], dim = a.q.sizes[2], kv = a.k_cache.sizes[2];
-    need(dim == a.k_cache.sizes[3], CMD_ERR_SHAPE, "q and k_cache differ in dim");
-    need(kv >= 1 ? heads % kv == 0 : heads == 0, CMD_ERR_SHAPE, "the cache's heads must divide q's");
+    NEED(dim == a.k_cache.sizes[3], CMD_ERR_SHAPE, "q and k_cache differ in dim");
+    NEED(kv >= 1 ? heads % kv == 0 : heads == 0, CMD_ERR_SHAPE, "the cache's heads must divide q's");
     check_heads(heads);
-    need(rows == a.tables.sizes[0], CMD_ERR_SHAPE, "q and tables differ in rows");
+    NEED(rows == a.tables.sizes[0], CMD_ERR_SHAPE, "q and tables differ in rows");
     check(a.lengths, "lengths", 1);
     check_type(a.lengths, "lengths", CMD_I32);
     check_sizes(a.lengths, "lengths", &rows);
@@ -530,10 +532,10 @@ extern "C" cmd_status cmd_attention_decode(const cmd_attention_args* args, void*
       check_apart(a.lse, "lse", a.out, "out");
     }
     for (int i = 0; i < 5; ++i) check_apart(a.out, "out", *ins[i], names[i]);
-    need(std::isfinite(a.scale) && a.scale > 0.0f, CMD_ERR_ARG, "scale must be positive");
-    need(std::isfinite(a.softcap) && a.softcap >= 0.0f, CMD_ERR_ARG, "softcap must be positive, or 0 for none");
-    need(a.window >= 0, CMD_ERR_ARG, "window must be positive, or 0 for none");
-    need(a.reserved == 0, CMD_ERR_ARG, "reserved must be 0");
+    NEED(std::isfinite(a.scale) && a.scale > 0.0f, CMD_ERR_ARG, "scale must be positive");
+    NEED(std::isfinite(a.softcap) && a.softcap >= 0.0f, CMD_ERR_ARG, "softcap must be positive, or 0 for none");
+    NEED(a.window >= 0, CMD_ERR_ARG, "window must be positive, or 0 for none");
+    NEED(a.reserved == 0, CMD_ERR_ARG, "reserved must be 0");
     if (rows == 0 || heads == 0) return CMD_OK;
     check_workspace(a.workspace, a.workspace_bytes, attention_workspace(heads, kv, dim));
     cmdx::AttendParams p;
@@ -596,22 +598,22 @@ namespace {
 void check_ints(const cmd_operand& o, const char* name, int rank) {
   check(o, name, rank, true);
   check_type(o, name, CMD_I32);
-  for (int d = 0; d < rank; ++d) need(o.sizes[d] <= 0x7fffffff, CMD_ERR_LIMIT, std::string(name) + " is too long");
+  for (int d = 0; d < rank; ++d) NEED(o.sizes[d] <= 0x7fffffff, CMD_ERR_LIMIT, std::string(name) + " is too long");
 }
 
 // The pools of a call, and the largest access that suits them all.
 cmdx::PoolList pool_list(const cmd_pool* pools, int32_t n, int64_t pages) {
-  need(n >= 0 && n <= CMD_CACHE_MAX_POOLS, CMD_ERR_LIMIT, "more than 64 pools");
-  need(pools || n == 0, CMD_ERR_NULL, "pools is NULL");
+  NEED(n >= 0 && n <= CMD_CACHE_MAX_POOLS, CMD_ERR_LIMIT, "more than 64 pools");
+  NEED(pools || n == 0, CMD_ERR_NULL, "pools is NULL");
   cmdx::PoolList l;
   std::memset(&l, 0, sizeof l);
   uint64_t bits = 16;
   for (int i = 0; i < n; ++i) {
-    need(pools[i].page_bytes >= 0 && pools[i].page_stride >= pools[i].page_bytes, CMD_ERR_SHAPE,
+    NEED(pools[i].page_bytes >= 0 && pools[i].page_stride >= pools[i].page_bytes, CMD_ERR_SHAPE,
          "a pool's pages overlap (page_stride below page_bytes)");
-    need(pools[i].page_stride < ((int64_t)1 << 40), CMD_ERR_LIMIT, "a page stride above 2^40 bytes");
+    NEED(pools[i].page_stride < ((int64_t)1 << 40), CMD_ERR_LIMIT, "a page stride above 2^40 bytes");
     if (pools[i].page_bytes == 0 || pages == 0) continue;
-    need(pools[i].ptr, CMD_ERR_NULL, "a pool's pointer is NULL");
+    NEED(pools[i].ptr, CMD_ERR_NULL, "a pool's pointer is NULL");
     l.ptr[l.n] = static_cast<uint8_t*>(pools[i].ptr);
     l.stride[l.n] = pools[i].page_stride;
     l.bytes[l.n] = pools[i].page_bytes;
@@ -625,7 +627,7 @@ cmdx::PoolList pool_list(const cmd_pool* pools, int32_t n, int64_t pages) {
 void check_pools_apart(const cmd_operand& o, const char* name, const cmdx::PoolList& l, int64_t pages) {
   for (int i = 0; i < l.n; ++i) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(l.ptr[i]);
-    need(!meet(range_of(o), {a, a + (uintptr_t)((pages - 1) * l.stride[i] + l.bytes[i])}), CMD_ERR_ALIAS,
+    NEED(!meet(range_of(o), {a, a + (uintptr_t)((pages - 1) * l.stride[i] + l.bytes[i])}), CMD_ERR_ALIAS,
          std::string(name) + " overlaps a pool");
   }
 }
@@ -644,7 +646,7 @@ void check_pools(const cmdx::PoolList& l, int64_t pages) {
         const int64_t first = a > b ? l.bytes[j] : l.bytes[i], second = a > b ? l.bytes[i] : l.bytes[j];
         ok = (int64_t)d >= first && (int64_t)d + second <= l.stride[i];
       }
-      need(ok, CMD_ERR_ALIAS, "two pools overlap");
+      NEED(ok, CMD_ERR_ALIAS, "two pools overlap");
     }
 }
 
@@ -668,8 +670,8 @@ struct Words {
 
 extern "C" cmd_status cmd_select_workspace(int64_t old_rows, int64_t new_rows, int64_t pages, int64_t* bytes) {
   return guarded([&]() -> cmd_status {
-    need(bytes, CMD_ERR_NULL, "bytes is NULL");
-    need(old_rows >= 0 && new_rows >= 0 && pages >= 0 && old_rows <= 0x7fffffff && new_rows <= 0x7fffffff &&
+    NEED(bytes, CMD_ERR_NULL, "bytes is NULL");
+    NEED(old_rows >= 0 && new_rows >= 0 && pages >= 0 && old_rows <= 0x7fffffff && new_rows <= 0x7fffffff &&
              pages <= 0x7fffffff,
          CMD_ERR_SHAPE, "negative size, or one above 2^31 - 1");
     *bytes = 4 * select_words(old_rows, new_rows, pages);
@@ -679,12 +681,12 @@ extern "C" cmd_status cmd_select_workspace(int64_t old_rows, int64_t new_rows, i
 
 extern "C" cmd_status cmd_cache_select(const cmd_select_args* args, void* cuda_stream) {
   return guarded([&]() -> cmd_status {
-    need(args, CMD_ERR_NULL, "args is NULL");
+    NEED(args, CMD_ERR_NULL, "args is NULL");
     const cmd_select_args& a = *args;
     check_ints(a.tables, "tables", 2);
     check_ints(a.tables_out, "tables_out", 2);
     const int64_t old_rows = a.tables.sizes[0], new_rows = a.tables_out.sizes[0], columns = a.tables.sizes[1];
-    need(a.tables_out.sizes[1] == columns, CMD_ERR_SHAPE, "tables and tables_out differ in columns");
+    NEED(a.tables_out.sizes[1] == columns, CMD_ERR_SHAPE, "tables and tables_out differ in columns");
     check_distinct(a.tables_out, "tables_out");
     check_ints(a.lengths, "lengths", 1);
     check_sizes(a.lengths, "lengths", &old_rows);
@@ -700,8 +702,8 @@ extern "C" cmd_status cmd_cache_select(const cmd_select_args* args, void* cuda_s
     const int64_t pages = a.refs.sizes[0];
     check_ints(a.refs_out, "refs_out", 1);
     check_sizes(a.refs_out, "refs_out", &pages);
-    need(a.page_size >= 1, CMD_ERR_SHAPE, "a page holds no token");
-    need((__int128)columns * a.page_size <= 0x7fff0000, CMD_ERR_LIMIT, "table rows that reach past 2^31 - 2^16 tokens");
+    NEED(a.page_size >= 1, CMD_ERR_SHAPE, "a page holds no token");
+    NEED((__int128)columns * a.page_size <= 0x7fff0000, CMD_ERR_LIMIT, "table rows that reach past 2^31 - 2^16 tokens");
     const cmdx::PoolList pools = pool_list(a.pools, a.n_pools, pages);
     check_pools(pools, pages);
     const cmd_operand* ins[] = {&a.tables, &a.lengths, &a.refs, &a.parents, &a.grow};
@@ -732,7 +734,7 @@ extern "C" cmd_status cmd_cache_select(const cmd_select_args* args, void* cuda_s
     p.new_rows = (int32_t)new_rows;
     p.columns = (int32_t)columns;
     p.pages = (int32_t)pages;
-    p.page_size = a.page_size;
+    p.page = fast_div32((uint32_t)a.page_size);
     p.status = a.status;
     Words w = {static_cast<int32_t*>(a.workspace)};
     p.head = w.take(kHeadWords);
@@ -749,8 +751,8 @@ extern "C" cmd_status cmd_cache_select(const cmd_select_args* args, void* cuda_s
 
 extern "C" cmd_status cmd_compact_workspace(int64_t pages, int64_t* bytes) {
   return guarded([&]() -> cmd_status {
-    need(bytes, CMD_ERR_NULL, "bytes is NULL");
-    need(pages >= 0 && pages <= 0x7fffffff, CMD_ERR_SHAPE, "negative number of pages, or one above 2^31 - 1");
+    NEED(bytes, CMD_ERR_NULL, "bytes is NULL");
+    NEED(pages >= 0 && pages <= 0x7fffffff, CMD_ERR_SHAPE, "negative number of pages, or one above 2^31 - 1");
     *bytes = 4 * compact_words(pages);
     return CMD_OK;
   });
@@ -758,7 +760,7 @@ extern "C" cmd_status cmd_compact_workspace(int64_t pages, int64_t* bytes) {
 
 extern "C" cmd_status cmd_cache_compact(const cmd_compact_args* args, void* cuda_stream) {
   return guarded([&]() -> cmd_status {
-    need(args, CMD_ERR_NULL, "args is NULL");
+    NEED(args, CMD_ERR_NULL, "args is NULL");
     const cmd_compact_args& a = *args;
     check_ints(a.tables, "tables", 2);
     check_ints(a.tables_out, "tables_out", 2);
@@ -772,8 +774,8 @@ extern "C" cmd_status cmd_cache_compact(const cmd_compact_args* args, void* cuda
     check_sizes(a.refs_out, "refs_out", &pages);
     check_ints(a.page_map_out, "page_map_out", 1);
     check_sizes(a.page_map_out, "page_map_out", &pages);
-    need(a.page_size >= 1, CMD_ERR_SHAPE, "a page holds no token");
-    need((__int128)columns * a.page_size <= 0x7fff0000, CMD_ERR_LIMIT, "table rows that reach past 2^31 - 2^16 tokens");
+    NEED(a.page_size >= 1, CMD_ERR_SHAPE, "a page holds no token");
+    NEED((__int128)columns * a.page_size <= 0x7fff0000, CMD_ERR_LIMIT, "table rows that reach past 2^31 - 2^16 tokens");
     const cmdx::PoolList pools = pool_list(a.pools, a.n_pools, pages);
     check_pools(pools, pages);
     const cmd_operand* ins[] = {&a.tables, &a.lengths, &a.refs};
@@ -801,7 +803,7 @@ extern "C" cmd_status cmd_cache_compact(const cmd_compact_args* args, void* cuda
     p.rows = (int32_t)a.tables.sizes[0];
     p.columns = (int32_t)columns;
     p.pages = (int32_t)pages;
-    p.page_size = a.page_size;
+    p.page = fast_div32((uint32_t)a.page_size);
     p.status = a.status;
     Words w = {static_cast<int32_t*>(a.workspace)};
     p.head = w.take(kHeadWords);
@@ -813,7 +815,7 @@ extern "C" cmd_status cmd_cache_compact(const cmd_compact_args* args, void* cuda
 
 extern "C" cmd_status cmd_cache_status(int32_t* status, int32_t* bits, void* cuda_stream) {
   return guarded([&]() -> cmd_status {
-    need(status, CMD_ERR_NULL, "status is NULL");
+    NEED(status, CMD_ERR_NULL, "status is NULL");
     const cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
     int32_t word = 0;
     cudaError_t e = cudaMemcpyAsync(&word, status, sizeof word, cudaMemcpyDeviceToHost, stream);

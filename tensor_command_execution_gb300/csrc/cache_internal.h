@@ -103,19 +103,24 @@ cudaError_t attend_mma_launch(int dtype, const AttendParams& p, cudaStream_t str
 constexpr int kAttendHeads = 8, kAttendMmaHeads = 16;
 
 // ---- pages (cache_pages.cu) -----------------------------------------------------
-struct PoolList {
-  uint8_t* ptr[CMD_CACHE_MAX_POOLS];
-  int64_t stride[CMD_CACHE_MAX_POOLS];
-  int64_t bytes[CMD_CACHE_MAX_POOLS];
+// The pools of a call; MAX of them at most (a launch's parameters are copied
+// to the device with it, so few pools go in a short list).
+template <int MAX>
+struct PoolListOf {
+  uint8_t* ptr[MAX];
+  int64_t stride[MAX];
+  int64_t bytes[MAX];
   int32_t n;
   int32_t unit;        // bytes of one access: every address and size is a multiple of it
 };
+using PoolList = PoolListOf<CMD_CACHE_MAX_POOLS>;
 
 struct SelectParams {
   const int32_t *tables, *lengths, *refs, *parents, *grow;
   int32_t *tables_out, *lengths_out, *refs_out;
   int64_t table_st, table_out_st;  // rows; a row's entries are dense
-  int32_t old_rows, new_rows, columns, pages, page_size;
+  int32_t old_rows, new_rows, columns, pages;
+  FastDiv32 page;
   int32_t *first, *children, *keep, *base, *free_list, *copy_src, *copy_dst, *head;  // workspace
   int32_t* status;
 };
@@ -124,7 +129,8 @@ struct CompactParams {
   const int32_t *tables, *lengths, *refs;
   int32_t *tables_out, *refs_out, *map_out;
   int64_t table_st, table_out_st;
-  int32_t rows, columns, pages, page_size;
+  int32_t rows, columns, pages;
+  FastDiv32 page;
   int32_t *holes, *movers, *head;  // workspace
   int32_t* status;
 };
