@@ -359,6 +359,7 @@ extern "C" cmd_status cmd_rope(const cmd_operand* q, const cmd_operand* q_out, c
       p.batch = (int32_t)like->sizes[0];
     }
     NEED((__int128)p.batch * p.tokens <= 0x7fffffff, CMD_ERR_LIMIT, "more than 2^31 - 1 tokens");
+    p.per_batch = fast_div32((uint32_t)p.tokens);
     p.positions = static_cast<const int32_t*>(positions->ptr);
     p.pos_st[0] = lead == 2 ? positions->strides[0] : 0;
     p.pos_st[1] = positions->strides[lead - 1];
@@ -452,6 +453,7 @@ extern "C" cmd_status cmd_cache_append(const cmd_append_args* args, void* cuda_s
     p.s[p.n_streams++] = rope_stream(a.v, a.v_cache, false, true);
     p.batch = 1;
     p.tokens = tokens;
+    p.per_batch = fast_div32((uint32_t)tokens);
     p.positions = static_cast<const int32_t*>(a.positions.ptr);
     p.pos_st[1] = a.positions.strides[0];
     p.tables = static_cast<const int32_t*>(a.tables.ptr);

@@ -41,6 +41,7 @@ struct RopeParams {
   int32_t dim;
   float scale, sine_scale;  // of the cosine; of the sine (negative: backward)
   int64_t tokens;      // per batch
+  FastDiv32 per_batch; // by that number
   int32_t batch;
   // the cache (append)
   const int32_t* tables;

@@ -8,107 +8,237 @@
 // rotation, t negated.
 //
 // Bound by memory: every element is read and written once, at about two
-// fused multiply-adds each. One CTA takes one token and all of its heads
-// (queries, keys, values), so a token's angles are computed once, by n_pairs
-// of its threads, into shared memory, while the token's elements are already
-// on their way: each thread issues its loads first. A thread keeps one place
-// within the head (a vector of 16 bytes, in the half layout with its partner
-// n_pairs further) and goes over heads, so its cosines stay in registers.
+// fused multiply-adds each. A CTA takes a token, or several where heads are
+// few, and all of their heads (queries, keys, values), so that an angle is
+// computed once, into shared memory, while the elements are already on their
+// way: each thread issues its loads first. A thread keeps two 16-byte places
+// within the head (in the half layout's rotated part, elements and their
+// partners n_pairs further) and goes over heads.
 #include "cache_common.cuh"
 
 namespace cmdx {
 
 namespace {
 
-constexpr int kRopeLoads = 4;  // heads a thread has in flight
+// Heads a thread has in flight. Measured on 4 x 4096 tokens of 40 heads of 128
+// (bf16): 2, 56.2 us (half), 56.9 (interleaved); 3, 55.7 and 55.3; 4, 61.5 and
+// 61.4. A copy of as many bytes by the library takes 54.0.
+constexpr int kRopeLoads = 3;
 
-// VE elements at p, in one 16-byte access when VEC, else the first n of them one by one.
+// Two 16-bit numbers of a word, and back.
+template <class T>
+__device__ __forceinline__ float2 unpack(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack<__half>(uint32_t w) { return __half22float2(*reinterpret_cast<__half2*>(&w)); }
+template <>
+__device__ __forceinline__ float2 unpack<__nv_bfloat16>(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <class T>
+__device__ __forceinline__ uint32_t pack(float x, float y);
+template <>
+__device__ __forceinline__ uint32_t pack<__half>(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack<__nv_bfloat16>(float x, float y) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The pair (a, b) turned: (a c - b s, b c + a s).
+__device__ __forceinline__ float2 turned(float a, float b, float2 t) {
+  return make_float2(fmaf(a, t.x, -(b * t.y)), fmaf(b, t.x, a * t.y));
+}
+
+// Where pair i's cosine and sine lie among the n_pairs of a token, which
+// threads read NP at a time: 16 bytes each, next to the other threads' (groups
+// = n_pairs / NP of them), so that no two meet in a bank.
+template <int NP>
+__device__ __forceinline__ int turn_at(int i, int groups) {
+  if (NP == 1) return i;
+  const int k = i % NP;
+  return (k / 2 * groups + i / NP) * 2 + k % 2;
+}
+
+// The cosines and sines of one place: pairs 2 i and 2 i + 1 of its NP.
+template <int NP>
+struct Turns {
+  const float2* of_token;
+  int group, groups;
+  __device__ __forceinline__ float4 two(int i) const {
+    return *reinterpret_cast<const float4*>(of_token + turn_at<NP>(group * NP + 2 * i, groups));
+  }
+  __device__ __forceinline__ float2 one() const { return of_token[group]; }
+};
+
+// VE elements of a head: a 16-byte vector when VEC, else up to VE of them one
+// by one.
 template <class T, int VE, bool VEC>
 struct Chunk {
   T x[VE];
   __device__ __forceinline__ void load(const T* p, int n) {
-    if constexpr (VEC) {
-      *reinterpret_cast<uint4*>(x) = __ldcs(reinterpret_cast<const uint4*>(p));
-    } else {
 #pragma unroll
-      for (int i = 0; i < VE; ++i)
-        if (i < n) x[i] = p[i];
-    }
+    for (int i = 0; i < VE; ++i)
+      if (i < n) x[i] = p[i];
   }
   __device__ __forceinline__ void store(T* p, int n) const {
-    if constexpr (VEC) {
-      __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(x));
-    } else {
 #pragma unroll
-      for (int i = 0; i < VE; ++i)
-        if (i < n) p[i] = x[i];
+    for (int i = 0; i < VE; ++i)
+      if (i < n) p[i] = x[i];
+  }
+  // this chunk's element paired with another's (VE 1)
+  __device__ __forceinline__ void turn_with(Chunk& o, const Turns<1>& t) {
+    const float2 y = turned(to_float(x[0]), to_float(o.x[0]), t.one());
+    x[0] = from_float<T>(y.x);
+    o.x[0] = from_float<T>(y.y);
+  }
+  // neighbours paired (VE 2)
+  __device__ __forceinline__ void turn(const Turns<1>& t) {
+    const float2 y = turned(to_float(x[0]), to_float(x[VE - 1]), t.one());
+    x[0] = from_float<T>(y.x);
+    x[VE - 1] = from_float<T>(y.y);
+  }
+};
+template <class T, int VE>
+struct Chunk<T, VE, true> {
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const T* p, int) {
+    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+  }
+  __device__ __forceinline__ void store(T* p, int) const {
+    __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
+  }
+  __device__ __forceinline__ void turn_with(Chunk& o, const Turns<VE>& t) {
+#pragma unroll
+    for (int i = 0; i < 4; i += VE == 4 ? 2 : 1) {
+      if constexpr (VE == 4) {
+        const float4 c = t.two(i / 2);
+        const float2 y = turned(__uint_as_float(w[i]), __uint_as_float(o.w[i]), make_float2(c.x, c.y));
+        const float2 z = turned(__uint_as_float(w[i + 1]), __uint_as_float(o.w[i + 1]), make_float2(c.z, c.w));
+        w[i] = __float_as_uint(y.x);
+        o.w[i] = __float_as_uint(y.y);
+        w[i + 1] = __float_as_uint(z.x);
+        o.w[i + 1] = __float_as_uint(z.y);
+      } else {
+        const float4 c = t.two(i);
+        const float2 a = unpack<T>(w[i]), b = unpack<T>(o.w[i]);
+        const float2 y = turned(a.x, b.x, make_float2(c.x, c.y)), z = turned(a.y, b.y, make_float2(c.z, c.w));
+        w[i] = pack<T>(y.x, z.x);
+        o.w[i] = pack<T>(y.y, z.y);
+      }
+    }
+  }
+  __device__ __forceinline__ void turn(const Turns<VE / 2>& t) {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      if constexpr (VE == 4) {
+        const float4 c = t.two(0);
+        const float2 y = turned(__uint_as_float(w[i]), __uint_as_float(w[i + 1]),
+                                i == 0 ? make_float2(c.x, c.y) : make_float2(c.z, c.w));
+        w[i] = __float_as_uint(y.x);
+        w[i + 1] = __float_as_uint(y.y);
+      } else {
+        const float4 c = t.two(i / 2);
+        const float2 a = unpack<T>(w[i]), b = unpack<T>(w[i + 1]);
+        const float2 y = turned(a.x, a.y, make_float2(c.x, c.y)), z = turned(b.x, b.y, make_float2(c.z, c.w));
+        w[i] = pack<T>(y.x, y.y);
+        w[i + 1] = pack<T>(z.x, z.y);
+      }
     }
   }
 };
 
+// How a launch's CTAs are made up: `units` threads to a head, `slots` heads at
+// once, `tokens` tokens.
+struct RopeShape {
+  int units, slots, tokens;
+};
+
 template <class T, int VE, bool VEC, bool HALF>
-__global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeParams p, int units, int head_slots) {
-  __shared__ float2 s_turn[CMD_CACHE_MAX_DIM / 2];
+__global__ void __launch_bounds__(512, 2) rope_kernel(const __grid_constant__ RopeParams p, const RopeShape shape) {
+  constexpr int NP = HALF ? VE : VE / 2;  // pairs of a thread's place
+  extern __shared__ __align__(16) float2 s_turn[];  // [tokens][n_pairs]: cosine and sine
   const int tid = threadIdx.x;
-  const int unit = tid % units, slot = tid / units;
-  const bool works = slot < head_slots;
-  const int rot = 2 * p.n_pairs;
-  // the thread's place in a head: its first element, and whether it has a
-  // partner n_pairs further (half layout, rotated part)
-  const int rot_units = (HALF ? p.n_pairs : rot) / VE;
-  const bool in_rot = unit < rot_units;
-  const int e0 = in_rot ? unit * VE : rot + (unit - rot_units) * VE;
-  const int pair0 = HALF ? e0 : e0 / 2;
-  const int count = p.dim - e0 < VE ? p.dim - e0 : VE;  // (a head's odd last element)
+  const int unit = tid % shape.units, slot = tid / shape.units % shape.slots, mine = tid / (shape.units * shape.slots);
+  const int rot = 2 * p.n_pairs, groups = p.n_pairs / NP;
+  // the thread's two places in a head: their first elements, the elements
+  // they have (fewer at an odd head's end, 0 for none), and whether they are
+  // rotated (in the half layout: with one another)
+  int e[2], count[2];
+  bool turn[2];
+  const int halves = HALF ? p.n_pairs / VE : 0;
+  if (HALF && unit < halves) {
+    e[0] = unit * VE;
+    e[1] = e[0] + p.n_pairs;
+    turn[0] = turn[1] = true;
+  } else {
+    const int from = HALF ? rot : 0, chunks = (p.dim - from + VE - 1) / VE;
+    e[0] = from + (unit - halves) * VE;
+    e[1] = e[0] + (chunks + 1) / 2 * VE;
+    turn[0] = e[0] < rot;
+    turn[1] = e[1] < rot;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) count[i] = max(0, min(VE, p.dim - e[i]));
 
   pdl_wait();
   pdl_trigger();
 
-  const int64_t token = blockIdx.x;
-  const int64_t b = p.batch == 1 ? 0 : token / p.tokens;
+  const int64_t first = (int64_t)blockIdx.x * shape.tokens;
+  const int64_t all = p.batch * p.tokens;
+  // the CTA's angles, one to a thread: their position and turns are read now
+  const auto angle_position = [&](int i) {
+    const uint32_t at = (uint32_t)(first + i / p.n_pairs);
+    const int64_t ob = fast_div32(p.per_batch, at);
+    return at < all ? p.positions[ob * p.pos_st[0] + (at - ob * p.tokens) * p.pos_st[1]] : 0;
+  };
+  const int angles = shape.tokens * p.n_pairs;
+  int32_t angle_at = 0;
+  uint64_t angle_turns = 0;
+  if (tid < angles) {
+    angle_at = angle_position(tid);
+    angle_turns = p.turns[tid % p.n_pairs];
+  }
+  const bool works = mine < shape.tokens && first + mine < all;
+  const uint32_t token = works ? (uint32_t)(first + mine) : 0;
+  const int64_t b = fast_div32(p.per_batch, token);
   const int64_t t = token - b * p.tokens;
-  const int32_t position = p.positions[b * p.pos_st[0] + t * p.pos_st[1]];
 
-  // where the cache takes the token: the offset's page and slot, or none
+  // where the cache takes the token: the page and slot, or none
   int32_t page = -1, page_slot = 0;
-  if (p.columns >= 0) {
+  if (p.columns >= 0 && works) {
+    const int32_t position = p.positions[b * p.pos_st[0] + t * p.pos_st[1]];
     const int32_t row = p.rows ? p.rows[t * p.rows_st] : (int32_t)t;
     if (position >= 0) {
       const uint32_t column = fast_div32(p.page, (uint32_t)position);
       page_slot = position - (int32_t)(column * p.page.d);
       if (row < 0 || row >= p.n_rows || column >= (uint32_t)p.columns) {
-        if (tid == 0) report(p.status, CMD_CACHE_BAD_INDEX);
+        if (unit == 0) report(p.status, CMD_CACHE_BAD_INDEX);
       } else {
         page = p.tables[row * p.table_st[0] + column * p.table_st[1]];
         if (page < 0 || page >= p.n_pages) {
           page = -1;
-          if (tid == 0) report(p.status, CMD_CACHE_BAD_PAGE);
+          if (unit == 0) report(p.status, CMD_CACHE_BAD_PAGE);
         }
       }
     }
   }
 
-  auto turn_angles = [&]() {
-    for (int i = tid; i < p.n_pairs; i += blockDim.x) {
-      const uint64_t phase = (uint64_t)(int64_t)position * p.turns[i];
-      float s, c;
-      sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &c);
-      s_turn[i] = make_float2(c * p.scale, s * p.sine_scale);
-    }
-    __syncthreads();
-  };
-
-  constexpr int NP = HALF ? VE : VE / 2;  // pairs of one thread
-  float cs[NP], sn[NP];
-  for (int h0 = 0; h0 < p.heads; h0 += kRopeLoads * head_slots) {
-    Chunk<T, VE, VEC> a[kRopeLoads], c[kRopeLoads];
+  for (int h0 = 0; h0 < p.heads; h0 += kRopeLoads * shape.slots) {
+    Chunk<T, VE, VEC> x[kRopeLoads][2];
     T* dst[kRopeLoads];
-    bool turn[kRopeLoads];
+    bool rotate[kRopeLoads];
 #pragma unroll
     for (int i = 0; i < kRopeLoads; ++i) {
-      int h = h0 + i * head_slots + slot;
+      int h = h0 + i * shape.slots + slot;
       dst[i] = nullptr;
-      turn[i] = false;
+      rotate[i] = false;
       if (!works || h >= p.heads) continue;
       int j = 0;
       while (h >= p.s[j].heads) h -= p.s[j++].heads;
@@ -120,57 +250,61 @@ __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeP
       } else {
         dst[i] = static_cast<T*>(s.out) + b * s.out_st[0] + t * s.out_st[1] + h * s.out_st[2];
       }
-      turn[i] = s.rotate;
-      a[i].load(src + e0, count);
-      if (HALF && in_rot) c[i].load(src + e0 + p.n_pairs, count);
+      rotate[i] = s.rotate;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (count[k]) x[i][k].load(src + e[k], count[k]);
     }
     if (h0 == 0) {
-      turn_angles();
-      if (in_rot) {
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          const float2 w = s_turn[pair0 + i];
-          cs[i] = w.x;
-          sn[i] = w.y;
+      for (int i = tid; i < angles; i += blockDim.x) {
+        if (i != tid) {
+          angle_at = angle_position(i);
+          angle_turns = p.turns[i % p.n_pairs];
         }
+        const uint64_t phase = (uint64_t)(int64_t)angle_at * angle_turns;
+        float s, c;
+        sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &c);
+        const int k = i / p.n_pairs;
+        s_turn[k * p.n_pairs + turn_at<NP>(i - k * p.n_pairs, groups)] = make_float2(c * p.scale, s * p.sine_scale);
       }
+      __syncthreads();
     }
+    // (a thread without a token has no place here, and no dst)
+    const float2* turns = s_turn + mine * p.n_pairs;
 #pragma unroll
     for (int i = 0; i < kRopeLoads; ++i) {
       if (!dst[i]) continue;
-      if (turn[i] && in_rot) {
+      if constexpr (HALF) {
+        if (rotate[i] && turn[0]) x[i][0].turn_with(x[i][1], Turns<NP>{turns, e[0] / VE, groups});
+      } else {
 #pragma unroll
-        for (int k = 0; k < NP; ++k) {
-          const float x = to_float(HALF ? a[i].x[k] : a[i].x[(2 * k) % VE]);
-          const float y = to_float(HALF ? c[i].x[k] : a[i].x[(2 * k + 1) % VE]);
-          const T u = from_float<T>(fmaf(x, cs[k], -(y * sn[k])));
-          const T w = from_float<T>(fmaf(y, cs[k], x * sn[k]));
-          if (HALF) {
-            a[i].x[k] = u;
-            c[i].x[k] = w;
-          } else {
-            a[i].x[(2 * k) % VE] = u;
-            a[i].x[(2 * k + 1) % VE] = w;
-          }
-        }
+        for (int k = 0; k < 2; ++k)
+          if (rotate[i] && turn[k]) x[i][k].turn(Turns<NP>{turns, e[k] / VE, groups});
       }
-      a[i].store(dst[i] + e0, count);
-      if (HALF && in_rot) c[i].store(dst[i] + e0 + p.n_pairs, count);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (count[k]) x[i][k].store(dst[i] + e[k], count[k]);
     }
   }
 }
 
 template <class T, int VE, bool VEC, bool HALF>
 cudaError_t launch(const RopeParams& p, cudaStream_t stream) {
-  const int rot = 2 * p.n_pairs;
-  const int units = (HALF ? p.n_pairs : rot) / VE + (p.dim - rot + VE - 1) / VE;
-  // threads: as many heads at once as leave every thread kRopeLoads of them or fewer, within 512 threads
-  int slots = 512 / units;
-  if (slots < 1) slots = 1;
-  const int rounds = (p.heads + slots * kRopeLoads - 1) / (slots * kRopeLoads);
-  slots = (p.heads + rounds * kRopeLoads - 1) / (rounds * kRopeLoads);
-  const int threads = (units * slots + 31) / 32 * 32;
-  return launch_pdl(rope_kernel<T, VE, VEC, HALF>, (int)(p.tokens * p.batch), threads, 0, stream, p, units, slots);
+  RopeShape s;
+  const int halves = HALF ? p.n_pairs / VE : 0, chunks = (p.dim - (HALF ? 2 * p.n_pairs : 0) + VE - 1) / VE;
+  s.units = halves + (chunks + 1) / 2;
+  // as many heads at once as leave every thread kRopeLoads of them, or fewer, within 512 threads
+  s.slots = 512 / s.units;
+  const int rounds = (p.heads + s.slots * kRopeLoads - 1) / (s.slots * kRopeLoads);
+  s.slots = (p.heads + rounds * kRopeLoads - 1) / (rounds * kRopeLoads);
+  // CTAs of about 128 threads, where there are tokens enough to give every SM eight
+  const int64_t all = p.batch * p.tokens, each = all / (152 * 8);
+  s.tokens = 128 / (s.units * s.slots);
+  if (s.tokens > each) s.tokens = (int)each;
+  if (s.tokens < 1) s.tokens = 1;
+  const int threads = (s.units * s.slots * s.tokens + 31) / 32 * 32;
+  return launch_pdl(rope_kernel<T, VE, VEC, HALF>, (int)((all + s.tokens - 1) / s.tokens), threads,
+                    (size_t)s.tokens * p.n_pairs * sizeof(float2), stream, p, s);
 }
 
 template <class T>
