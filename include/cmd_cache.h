@@ -144,7 +144,8 @@ cmd_status cmd_cache_append(const cmd_append_args* args, void* cuda_stream);
  * The work is split over the sequences' lengths in equal parts and joined
  * through workspace: cmd_attention_workspace bytes of device memory, 16-byte
  * aligned, of any contents, used by one call at a time (streams that overlap
- * need one each). Results do not depend on the timing of the parts. A 16-bit
+ * need one each). Results do not depend on the timing of the parts. columns *
+ * page_size * kv_heads stays below 2^35. A 16-bit
  * value of infinity inside a row makes its element of out NaN or infinite. */
 typedef struct cmd_attention_args {
   cmd_operand q, out;           /* [rows, q_heads, dim], dim <= CMD_CACHE_MAX_DIM */

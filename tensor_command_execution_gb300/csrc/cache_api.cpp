@@ -577,8 +577,13 @@ extern "C" cmd_status cmd_attention_decode(const cmd_attention_args* args, void*
     p.q_pairs = vector_rows(a.q, 4);
     const int few = (dim <= 64 ? 2 : 4) * es;
     p.vec = vector_rows(a.k_cache, few) && vector_rows(a.v_cache, few);
-    for (int64_t r = 0; r < rows; r += cmdx::kAttendRows) {
-      p.rows = (int32_t)std::min<int64_t>(cmdx::kAttendRows, rows - r);
+    // a launch's units (tiles of rows that fill their tables, for each head) stay below 2^31
+    const int64_t row_units = (int64_t)p.kv_heads * p.blocks *
+                              (p.columns * a.k_cache.sizes[1] / cmdx::kAttendLeastTile + 2 + cmdx::kAttendMostStart);
+    NEED(row_units < 0x7fffffff, CMD_ERR_LIMIT, "a table row's tokens times the heads pass 2^31 tiles of 32");
+    const int64_t at_once = std::min<int64_t>(cmdx::kAttendRows, 0x7fffffff / row_units);
+    for (int64_t r = 0; r < rows; r += at_once) {
+      p.rows = (int32_t)std::min<int64_t>(at_once, rows - r);
       p.q = static_cast<const uint8_t*>(a.q.ptr) + r * a.q.strides[0] * es;
       p.out = static_cast<uint8_t*>(a.out.ptr) + r * a.out.strides[0] * es;
       p.lse = a.lse.ptr ? static_cast<float*>(a.lse.ptr) + r * a.lse.strides[0] : nullptr;

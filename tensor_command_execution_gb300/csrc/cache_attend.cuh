@@ -23,10 +23,9 @@
 namespace cmdx {
 
 // The rows of a launch, in shared memory: where each row's units begin (in
-// units of one kv head and block of query heads), and its tokens [lo, n) that
-// are attended to.
+// units of one kv head and block of query heads), and the row's length.
 struct AttendRows {
-  int64_t at[kAttendRows + 1];
+  int32_t at[kAttendRows + 4];  // (one more than the rows, and a multiple of 16 bytes)
   int32_t n[kAttendRows];
   __device__ __forceinline__ int lo(const AttendParams& p, int r) const {
     return p.window > 0 && n[r] > p.window ? n[r] - p.window : 0;
@@ -34,33 +33,34 @@ struct AttendRows {
 };
 
 // Fills s for tiles of `tile` tokens (aligned to the row's start); all
-// threads of the CTA call it.
+// threads of the CTA call it. (The host sees to it that the units of a launch,
+// of all heads, are below 2^31.)
 __device__ __forceinline__ void attend_rows(const AttendParams& p, AttendRows& s, int tile) {
-  __shared__ int64_t s_warp[32];
+  __shared__ int32_t s_warp[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int run = (p.rows + blockDim.x - 1) / blockDim.x;
   const int r0 = min(tid * run, p.rows), r1 = min(r0 + run, p.rows);
-  const int64_t most = (int64_t)p.columns * p.page.d;
-  int64_t sum = 0;
+  const int most = p.columns * (int)p.page.d;
+  int sum = 0;
   for (int r = r0; r < r1; ++r) {
-    int64_t len = p.lengths[r * p.len_st];
-    if (len < 0 || len > most) {
+    int n = p.lengths[r * p.len_st];
+    if (n < 0 || n > most) {
       if (blockIdx.x == 0) report(p.status, CMD_CACHE_BAD_INDEX);
-      len = len < 0 ? 0 : most;
+      n = n < 0 ? 0 : most;
     }
-    const int n = s.n[r] = (int)len;
+    s.n[r] = n;
     s.at[r + 1] = n > 0 ? (n + tile - 1) / tile - s.lo(p, r) / tile + p.start_units : 0;
     sum += s.at[r + 1];
   }
-  int64_t incl = sum;
+  int incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(~0u, incl, o);
+    const int y = __shfl_up_sync(~0u, incl, o);
     if (lane >= o) incl += y;
   }
   if (lane == 31) s_warp[warp] = incl;
   __syncthreads();
-  int64_t at = incl - sum;
+  int at = incl - sum;
   for (int w = 0; w < warp; ++w) at += s_warp[w];
   if (tid == 0) s.at[0] = 0;
   for (int r = r0; r < r1; ++r) {
@@ -72,21 +72,27 @@ __device__ __forceinline__ void attend_rows(const AttendParams& p, AttendRows& s
 
 // A CTA's share of a launch: units [begin, end).
 struct AttendShare {
-  int64_t units, ctas, begin, end;
+  int units, ctas, begin, end;
   int groups;  // kv heads times blocks of query heads
+  // the first unit of CTA c: c * units / ctas (each < 2^31; the product of c and the remainder is small)
+  __device__ __forceinline__ int begin_of(int c) const {
+    const int each = units / ctas;
+    return c * each + c * (units - each * ctas) / ctas;
+  }
+  // the CTA that works on unit u
+  __device__ __forceinline__ int owner(int u) const { return (int)((((int64_t)u + 1) * ctas - 1) / units); }
 };
 __device__ __forceinline__ AttendShare attend_share(const AttendParams& p, const AttendRows& s) {
   AttendShare w;
   w.groups = p.kv_heads * p.blocks;
   w.units = s.at[p.rows] * w.groups;
-  w.ctas = w.units < gridDim.x ? w.units : gridDim.x;
-  w.begin = w.ctas ? blockIdx.x * w.units / w.ctas : 0;
-  w.end = blockIdx.x < w.ctas ? (blockIdx.x + 1) * w.units / w.ctas : w.begin;
+  w.ctas = min(w.units, (int)gridDim.x);
+  w.begin = w.end = 0;
+  if ((int)blockIdx.x < w.ctas) {
+    w.begin = w.begin_of(blockIdx.x);
+    w.end = w.begin_of(blockIdx.x + 1);
+  }
   return w;
-}
-// The CTA that works on unit u.
-__device__ __forceinline__ int attend_owner(const AttendShare& w, int64_t u) {
-  return (int)(((u + 1) * w.ctas - 1) / w.units);
 }
 
 // A stretch of one row's tiles for one kv head and block of query heads.
@@ -94,42 +100,41 @@ struct AttendSegment {
   int row, group;           // group = kv head * blocks + block
   int lo, n;                // the row's tokens
   int tile0, tiles;         // this stretch, in tiles from the row's start; no tiles: the share has ended
-  int64_t first;            // the unit of the row's and group's first tile
+  int first;                // the unit of the row's and group's first tile
   int row_tiles;            // and their number
   __device__ __forceinline__ bool whole() const { return tiles == row_tiles; }
 };
 // The stretch of row `row` and group `group`, whose first unit is u, that lies in the share.
 __device__ __forceinline__ AttendSegment attend_stretch(const AttendParams& p, const AttendRows& s, const AttendShare& w,
-                                                        int64_t u, int row, int group, int tile) {
+                                                        int u, int row, int group, int tile) {
   AttendSegment g;
   g.row = row;
   g.group = group;
   g.n = s.n[row];
   g.lo = s.lo(p, row);
-  g.row_tiles = (int)(s.at[row + 1] - s.at[row]) - p.start_units;
+  g.row_tiles = s.at[row + 1] - s.at[row] - p.start_units;
   g.first = u + p.start_units;
-  const int64_t from = w.begin > g.first ? w.begin : g.first;
-  const int64_t to = w.end < g.first + g.row_tiles ? w.end : g.first + g.row_tiles;
-  g.tile0 = g.lo / tile + (int)(from - g.first);
-  g.tiles = to > from ? (int)(to - from) : 0;
+  const int from = max(w.begin, g.first), to = min(w.end, g.first + g.row_tiles);
+  g.tile0 = g.lo / tile + from - g.first;
+  g.tiles = max(to - from, 0);
   return g;
 }
 __device__ __forceinline__ AttendSegment attend_first(const AttendParams& p, const AttendRows& s, const AttendShare& w,
                                                       int tile) {
-  const int64_t x = w.begin / w.groups;
+  const int x = w.begin / w.groups;
   int a = 0, b = p.rows;  // the last row that begins at or before x
   while (b - a > 1) {
     const int m = (a + b) >> 1;
     if (s.at[m] <= x) a = m; else b = m;
   }
-  const int64_t row_units = s.at[a + 1] - s.at[a];
-  const int group = (int)((w.begin - s.at[a] * w.groups) / row_units);
-  return attend_stretch(p, s, w, s.at[a] * w.groups + group * row_units, a, group, tile);
+  const int row_units = s.at[a + 1] - s.at[a], row0 = s.at[a] * w.groups;
+  const int group = (w.begin - row0) / row_units;
+  return attend_stretch(p, s, w, row0 + group * row_units, a, group, tile);
 }
 // The one after g (no tiles: there is none).
 __device__ __forceinline__ AttendSegment attend_next(const AttendParams& p, const AttendRows& s, const AttendShare& w,
                                                      const AttendSegment& g, int tile) {
-  const int64_t u = g.first + g.row_tiles;
+  const int u = g.first + g.row_tiles;
   int row = g.row, group = g.group + 1;
   if (u >= w.end) {
     AttendSegment none = g;
@@ -207,7 +212,7 @@ __device__ __forceinline__ void attend_finish(const AttendParams& p, const Atten
   if (threadIdx.x == 0 && g.first >= w.begin) {
     // the row begins here: say where its parts are
     AttendSplit split = {g.row, g.group, slot, 0};
-    if (part) split.parts = attend_owner(w, g.first + g.row_tiles - 1) - (int)blockIdx.x + 1;
+    if (part) split.parts = w.owner(g.first + g.row_tiles - 1) - (int)blockIdx.x + 1;
     if (p.split_by_row) p.splits[g.row * w.groups + g.group] = split;
     else if (part) p.splits[blockIdx.x] = split;
   }

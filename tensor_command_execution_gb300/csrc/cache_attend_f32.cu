@@ -2,14 +2,15 @@
 // cache of 32-bit numbers whose rows are whole 16-byte vectors.
 //
 // Products and sums stay in binary32 (the tensor units' 32-bit type holds 11
-// bits of a factor). Bound by memory up to about 8 query heads to a kv head:
-// each pair of elements takes 2 multiply-adds a query head, and the SM's 128
-// lanes do 128 in the cycle that brings 24 bytes. Each warp streams tiles of
-// 8 tokens through a ring of its own; scores are computed with a lane to a
-// quarter of a token's key (rows are an odd number of 16 bytes apart, so 8
-// tokens are read without bank conflicts), weighted values with a lane to 4
-// elements of the head dim (dims up to 64: the half-warps take every other
-// token). Queries and weights are read from shared memory as broadcasts.
+// bits of a factor). Bound by memory for few query heads to a kv head. Each
+// warp streams tiles of 8 tokens through a ring of its own. Scores: a lane
+// takes an eighth of the head dim of two tokens' keys, so that a query read
+// (shared by all lanes of the eighth) serves both, and the sums over the eight
+// lanes go by a transposing butterfly that leaves each lane a few finished
+// scores. Weighted values: a lane takes 4 elements of the head dim (dims up to
+// 64: the half-warps take every other token), the weights being read back from
+// shared memory. Rows lie 32 bytes past a multiple of 128 apart: the lanes of
+// 4 tokens and 2 neighbouring pieces meet in no bank.
 #include "cache_attend_ring.cuh"
 
 namespace cmdx {
@@ -24,8 +25,8 @@ constexpr int kWarps = 4;
 template <int DP, int GT>
 struct Shape {
   static constexpr int kStages = DP == 64 ? 3 : 2;
-  static constexpr int kCtas = DP == 256 ? 1 : DP == 64 ? 3 : GT == 8 ? 2 : 3;
-  static constexpr int kPitch = DP * 4 + 16;  // bytes of a row: an odd number of 16
+  static constexpr int kCtas = DP == 256 ? 1 : DP == 64 || GT < 8 ? 3 : 2;
+  static constexpr int kPitch = DP * 4 + 32;  // bytes of a row
   using Ring = AttendRing<float, kTokens, DP / 4, kPitch, kStages, kWarps>;
   static constexpr int kQueries = GT * DP * 4;              // bytes of a block's queries
   static constexpr int kWeights = kWarps * kTokens * GT * 4;  // and of the warps' weights
@@ -36,7 +37,8 @@ template <int DP, int GT>
 __global__ void __launch_bounds__(kWarps * 32, Shape<DP, GT>::kCtas) attend_f32_kernel(const __grid_constant__ AttendParams p) {
   using S = Shape<DP, GT>;
   using Ring = typename S::Ring;
-  constexpr int kHeld = GT > 4 ? GT / 4 : 1;           // heads whose softmax a lane keeps
+  constexpr int kScores = 2 * GT;                      // of a lane's two tokens
+  constexpr int kHeld = GT > 4 ? GT / 4 : 1;           // finished scores (and heads) of a lane
   constexpr int kQuads = DP > 128 ? DP / 128 : 1;      // groups of 4 dims of a lane
   constexpr int kApart = DP == 64 ? 2 : 1;             // tokens taken at once by the warp's halves
   extern __shared__ __align__(16) unsigned char s_mem[];
@@ -44,7 +46,11 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<DP, GT>::kCtas) attend_f32_
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float* s_w = s_q + GT * DP + warp * kTokens * GT;    // [token][head]
   AttendRows& s_rows = *reinterpret_cast<AttendRows*>(s_mem + kWarps * Ring::kBytes + S::kQueries + S::kWeights);
-  const int token = lane & 7, part = lane >> 3;        // in the scores
+  // in the scores: tokens token and token + 4, eighth `part`; finished scores
+  // are of token `done` and heads held, held + 1
+  const int token = lane & 3, part = lane >> 2;
+  const int done = token + (part & 4), held = GT == 1 ? 0 : (part & 3) * kHeld;
+
   const int quad = DP == 64 ? lane & 15 : lane, half = DP == 64 ? lane >> 4 : 0;  // in the values
 
   pdl_wait();
@@ -63,8 +69,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<DP, GT>::kCtas) attend_f32_
     }
     __syncthreads();
 
-    // the softmax of head part + 4 i lies with lanes of that part (one query
-    // head: with all lanes); o of this lane's dims
+    // the softmax of heads held + i, and o of this lane's dims
     float m[kHeld], l[kHeld];
     float4 o[GT][kQuads];
 #pragma unroll
@@ -82,52 +87,65 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<DP, GT>::kCtas) attend_f32_
       const uint32_t here = ring.next_tile(&index);
       if (!here) continue;
       const unsigned char* keys = s_mem + warp * Ring::kBytes + index * Ring::kStage;
-      float s[GT];
+      float s[kScores];
 #pragma unroll
-      for (int h = 0; h < GT; ++h) s[h] = 0.0f;
-#pragma unroll 4
-      for (int c = 0; c < DP / 16; ++c) {
-        if (16 * c >= p.dim) break;
-        const float4 x = *reinterpret_cast<const float4*>(keys + token * S::kPitch + (4 * c + part) * 16);
+      for (int h = 0; h < kScores; ++h) s[h] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < DP / 32; ++c) {
+        if (32 * c >= p.dim) break;
+        const float4 x = *reinterpret_cast<const float4*>(keys + token * S::kPitch + (8 * c + part) * 16);
+        const float4 y = *reinterpret_cast<const float4*>(keys + (token + 4) * S::kPitch + (8 * c + part) * 16);
 #pragma unroll
         for (int h = 0; h < GT; ++h) {
-          const float4 q = *reinterpret_cast<const float4*>(s_q + h * DP + (4 * c + part) * 4);
+          const float4 q = *reinterpret_cast<const float4*>(s_q + h * DP + (8 * c + part) * 4);
           s[h] = fmaf(x.x, q.x, s[h]);
           s[h] = fmaf(x.y, q.y, s[h]);
           s[h] = fmaf(x.z, q.z, s[h]);
           s[h] = fmaf(x.w, q.w, s[h]);
+          s[GT + h] = fmaf(y.x, q.x, s[GT + h]);
+          s[GT + h] = fmaf(y.y, q.y, s[GT + h]);
+          s[GT + h] = fmaf(y.z, q.z, s[GT + h]);
+          s[GT + h] = fmaf(y.w, q.w, s[GT + h]);
         }
       }
+      // over the eight lanes of a token: after each round a lane keeps half of
+      // its sums, the upper half where its bit of the round is set
 #pragma unroll
-      for (int h = 0; h < GT; ++h) {
-        s[h] += __shfl_xor_sync(~0u, s[h], 8);
-        s[h] += __shfl_xor_sync(~0u, s[h], 16);
+      for (int b = 16, n = kScores; b >= 4; b >>= 1) {
+        if (n > 1) {
+          n >>= 1;
+          const bool upper = lane & b;
+#pragma unroll
+          for (int e = 0; e < kScores / 2; ++e)
+            if (e < n) {
+              const float give = upper ? s[e] : s[e + n], keep = upper ? s[e + n] : s[e];
+              s[e] = keep + __shfl_xor_sync(~0u, give, b);
+            }
+        } else {
+          s[0] += __shfl_xor_sync(~0u, s[0], b);
+        }
       }
-      const bool in = here >> token & 1;
+      const bool in = here >> done & 1;
       float c[kHeld];
       bool moved = false;
 #pragma unroll
       for (int j = 0; j < kHeld; ++j) {
-        float x = s[0];
-#pragma unroll
-        for (int h = 0; h < GT; ++h)
-          if (GT > 1 && h / 4 == j) x = part == h % 4 ? s[h] : x;
-        x = in ? attend_score(p, x) : -CUDART_INF_F;
-        float up = x;
-#pragma unroll
-        for (int b = 1; b < 8; b <<= 1) up = fmaxf(up, __shfl_xor_sync(~0u, up, b));
+        const float x = in ? attend_score(p, s[j]) : -CUDART_INF_F;
+        float up = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
+        up = fmaxf(up, __shfl_xor_sync(~0u, up, 2));
+        up = fmaxf(up, __shfl_xor_sync(~0u, up, 16));
         up = fmaxf(up, m[j]);
         c[j] = m[j] == -CUDART_INF_F ? 0.0f : power_of_two(m[j] - up);
         moved = moved || up != m[j];
         m[j] = up;
         const float w = x == -CUDART_INF_F ? 0.0f : power_of_two(x - up);
         l[j] = fmaf(l[j], c[j], w);
-        if (GT > 1 || part == 0) s_w[token * GT + (GT > 1 ? part + 4 * j : 0)] = w;
+        s_w[done * GT + held + j] = w;
       }
       if (__any_sync(~0u, moved)) {
 #pragma unroll
         for (int h = 0; h < GT; ++h) {
-          const float ch = __shfl_sync(~0u, c[h / 4], (h % 4) * 8);
+          const float ch = __shfl_sync(~0u, c[h % kHeld], h / kHeld * 4);
 #pragma unroll
           for (int e = 0; e < kQuads; ++e) scale_by(o[h][e], ch);
         }
@@ -161,10 +179,11 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<DP, GT>::kCtas) attend_f32_
     constexpr int kStatePitch = attend_pitch(DP);
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
-#pragma unroll
-      for (int b = 1; b < 8; b <<= 1) l[j] += __shfl_xor_sync(~0u, l[j], b);
-      if (token == 0 && (GT > 1 || part == 0)) {
-        float* x = state + (GT > 1 ? part + 4 * j : 0) * kStatePitch;
+      l[j] += __shfl_xor_sync(~0u, l[j], 1);
+      l[j] += __shfl_xor_sync(~0u, l[j], 2);
+      l[j] += __shfl_xor_sync(~0u, l[j], 16);
+      if (done == 0) {
+        float* x = state + (held + j) * kStatePitch;
         x[kStatePitch - 4] = m[j];
         x[kStatePitch - 3] = l[j];
       }

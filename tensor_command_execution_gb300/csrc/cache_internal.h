@@ -57,7 +57,9 @@ cudaError_t rope_launch(int dtype, int layout, bool vec, const RopeParams& p, cu
 
 // ---- attention of one token (cache_attend*.cu) --------------------------------
 constexpr int kAttendMaxCtas = 152 * 4;  // bounds the workspace
-constexpr int kAttendRows = 512;         // rows of one launch (the host splits larger calls)
+constexpr int kAttendRows = 512;         // rows of one launch, at most (the host splits larger calls)
+constexpr int kAttendLeastTile = 32;     // tokens of a CTA's tile, at least, and
+constexpr int kAttendMostStart = 4;      // units of a row's beginning, at most: they bound a launch's units
 
 // A row (for one kv head and block of query heads) whose tiles went to several
 // CTAs: part k lies at index `first` for k = 0, (first & ~1) + 2 k after.
