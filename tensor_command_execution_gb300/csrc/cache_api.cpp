@@ -709,6 +709,7 @@ extern "C" cmd_status cmd_cache_select(const cmd_select_args* args, void* cuda_s
     const int64_t pages = a.refs.sizes[0];
     check_ints(a.refs_out, "refs_out", 1);
     check_sizes(a.refs_out, "refs_out", &pages);
+    NEED(pages <= 0x40000000, CMD_ERR_LIMIT, "more than 2^30 pages");
     NEED(a.page_size >= 1, CMD_ERR_SHAPE, "a page holds no token");
     NEED((__int128)columns * a.page_size <= 0x7fff0000, CMD_ERR_LIMIT, "table rows that reach past 2^31 - 2^16 tokens");
     const cmdx::PoolList pools = pool_list(a.pools, a.n_pools, pages);
@@ -781,6 +782,7 @@ extern "C" cmd_status cmd_cache_compact(const cmd_compact_args* args, void* cuda
     check_sizes(a.refs_out, "refs_out", &pages);
     check_ints(a.page_map_out, "page_map_out", 1);
     check_sizes(a.page_map_out, "page_map_out", &pages);
+    NEED(pages <= 0x40000000, CMD_ERR_LIMIT, "more than 2^30 pages");
     NEED(a.page_size >= 1, CMD_ERR_SHAPE, "a page holds no token");
     NEED((__int128)columns * a.page_size <= 0x7fff0000, CMD_ERR_LIMIT, "table rows that reach past 2^31 - 2^16 tokens");
     const cmdx::PoolList pools = pool_list(a.pools, a.n_pools, pages);

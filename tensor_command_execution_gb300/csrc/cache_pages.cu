@@ -33,7 +33,7 @@ enum { kCopies = 0, kUsedBefore = 1 };
 template <int CTAS>
 struct Team {
   static constexpr int kThreads = CTAS * kTeamThreads;
-  const int me = blockIdx.x * kTeamThreads + threadIdx.x;
+  const int me = (CTAS == 1 ? 0 : (int)blockIdx.x * kTeamThreads) + threadIdx.x;
 
   // (orders global memory among the team's threads)
   __device__ __forceinline__ void sync() const {
@@ -43,37 +43,38 @@ struct Team {
 
   // The sum of x over the threads before this one, and over all in *all.
   // Every thread of the team calls it.
-  __device__ __forceinline__ int before(int x, int* all) const {
-    __shared__ int s_warp[kTeamThreads / 32];
-    __shared__ int s_cta;
+  template <class N>
+  __device__ __forceinline__ N before(N x, N* all) const {
+    __shared__ N s_warp[kTeamThreads / 32];
+    __shared__ N s_cta;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int incl = x;
+    N incl = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(~0u, incl, o);
+      const N y = __shfl_up_sync(~0u, incl, o);
       if (lane >= o) incl += y;
     }
     if (lane == 31) s_warp[warp] = incl;
     __syncthreads();
     if (warp == 0) {
-      int w = s_warp[lane];
+      N w = s_warp[lane];
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(~0u, w, o);
+        const N y = __shfl_up_sync(~0u, w, o);
         if (lane >= o) w += y;
       }
       s_warp[lane] = w;
       if (lane == 31) s_cta = w;
     }
     sync();
-    int sum = incl - x + (warp ? s_warp[warp - 1] : 0);
+    N sum = incl - x + (warp ? s_warp[warp - 1] : 0);
     if constexpr (CTAS == 1) {
       *all = s_cta;
     } else {
-      int total = 0;
+      N total = 0;
 #pragma unroll
       for (int c = 0; c < CTAS; ++c) {
-        const int v = *cg::this_cluster().map_shared_rank(&s_cta, c);
+        const N v = *cg::this_cluster().map_shared_rank(&s_cta, c);
         if (c < (int)blockIdx.x) sum += v;
         total += v;
       }
@@ -134,120 +135,169 @@ __device__ __forceinline__ int row_length(const SelectParams& p, int row) {
   return (int)n;
 }
 
-// What becomes of new row i: its parent (-1: none), its length, the pages it
-// shares and the pages it has in all. A row that its table is too short for
-// has all = columns + 1. first[] is read unless the caller is filling it.
+// What becomes of new row i: its parent (-1: none), its length and its pages
+// (where its table has room), the parent's pages, and whether the last of
+// those is in progress.
 struct Plan {
-  int parent, length, keep, all;
-  bool split, fits;
+  int parent, length, all, old;
+  bool fits, partial;
+  // pages it shares, when `first` is the first of its parent's children that fits
+  __device__ __forceinline__ int keep(bool first) const { return old - (partial && !first); }
 };
-__device__ __forceinline__ Plan plan_row(const SelectParams& p, int i, bool with_first = true) {
+__device__ __forceinline__ Plan plan_row(const SelectParams& p, int i) {
   Plan r;
   r.parent = p.parents[i];
   int grow = p.grow ? p.grow[i] : 0;
   if (r.parent < -1 || r.parent >= p.old_rows || grow < 0) {
-    if (with_first) report(p.status, CMD_CACHE_BAD_INDEX);
-    if (grow < 0) grow = 0;
-    if (r.parent >= p.old_rows) r.parent = -1;
-    if (r.parent < -1) r.parent = -1;
+    report(p.status, CMD_CACHE_BAD_INDEX);
+    grow = max(grow, 0);
+    if (r.parent >= p.old_rows || r.parent < -1) r.parent = -1;
   }
   const int n = r.parent >= 0 ? row_length(p, r.parent) : 0;
-  const int old = pages_of(n, p.page);
   const int64_t length = (int64_t)n + grow;
+  r.old = pages_of(n, p.page);
+  r.partial = n != r.old * (int)p.page.d;
   r.fits = length <= (int64_t)p.columns * p.page.d;
+  if (!r.fits) report(p.status, CMD_CACHE_FULL_TABLE);
   r.length = r.fits ? (int)length : 0;
-  r.all = r.fits ? pages_of(r.length, p.page) : p.columns + 1;
-  r.split = with_first && r.parent >= 0 && n != old * (int)p.page.d && p.first[r.parent] != i;
-  r.keep = old - (r.split ? 1 : 0);
+  r.all = r.fits ? pages_of(r.length, p.page) : 0;
   return r;
 }
 
-template <int CTAS>
-__device__ __forceinline__ void select_plan(const SelectParams& p) {
-  using All = Team<CTAS>;
-  const All team;
-  const int me = team.me;
-  pdl_wait();
-  pdl_trigger();
-  // counts start from refs, families empty
-  for (int i = me; i < p.pages; i += All::kThreads) p.refs_out[i] = p.refs[i];
-  for (int i = me; i < p.old_rows; i += All::kThreads) {
-    p.first[i] = 0x7fffffff;
-    p.children[i] = 0;
-  }
-  if (me == 0) p.head[kCopies] = 0;
-  team.sync();
-  for (int i = me; i < p.new_rows; i += All::kThreads) {
-    const Plan r = plan_row(p, i, false);
-    if (r.parent >= 0 && r.fits) atomicMin(&p.first[r.parent], i);
-  }
-  team.sync();
-  // pages each new row needs, summed in row order; children that fit
-  const int run = (p.new_rows + All::kThreads - 1) / All::kThreads;
-  const int i0 = min(me * run, p.new_rows), i1 = min(i0 + run, p.new_rows);
-  int need = 0, all_need;
-  for (int i = i0; i < i1; ++i) {
-    const Plan r = plan_row(p, i);
-    p.keep[i] = r.keep;
-    if (!r.fits) {
-      report(p.status, CMD_CACHE_FULL_TABLE);
+constexpr int kNobody = 0x7fffffff;  // as a row's first child
+
+// Counts of the pages of old row r, by a warp: each changes hands from the row
+// to its children (those that fit), the page in progress to the first of them.
+__device__ __forceinline__ void hand_over(const SelectParams& p, int r, int kids) {
+  const int n = row_length(p, r), old = pages_of(n, p.page);
+  const bool partial = n != old * (int)p.page.d;
+  const int last = partial ? min(kids, 1) : kids;
+  if (kids == 1) return;
+  for (int j = threadIdx.x & 31; j < old; j += 32) {
+    const int page = p.tables[r * p.table_st + j];
+    if (page < 0 || page >= p.pages) {
+      report(p.status, CMD_CACHE_BAD_PAGE);
       continue;
     }
-    need += r.all - r.keep;
-    if (r.parent >= 0) atomicAdd(&p.children[r.parent], 1);
+    const int change = (j == old - 1 ? last : kids) - 1;
+    if (change) atomicAdd(&p.refs_out[page], change);
   }
-  int base = team.before(need, &all_need);
-  for (int i = i0; i < i1; ++i) {
-    const Plan r = plan_row(p, i);
-    p.base[i] = r.fits ? base : -1;
-    if (r.fits) base += r.all - r.keep;
-  }
-  team.sync();  // (children complete, base of every row written)
-  // counts: each page of an old row changes hands from one row to its
-  // children; the page in progress to the first child alone. A warp per row.
-  const int lane = threadIdx.x & 31;
-  for (int r = me >> 5; r < p.old_rows; r += All::kThreads / 32) {
-    const int n = row_length(p, r), old = pages_of(n, p.page), kids = p.children[r];
-    const bool partial = n != old * (int)p.page.d;
-    const int last = partial ? (kids ? 1 : 0) : kids;
-    if (kids == 1 && last == 1) continue;
-    for (int j = lane; j < old; j += 32) {
-      const int page = p.tables[r * p.table_st + j];
-      if (page < 0 || page >= p.pages) {
-        report(p.status, CMD_CACHE_BAD_PAGE);
-        continue;
-      }
-      const int change = (j == old - 1 ? last : kids) - 1;
-      if (change) atomicAdd(&p.refs_out[page], change);
+}
+
+// New row i, whose new pages begin at the base-th free one: its length, and
+// the page to copy. Returns the base, or what stands for none: -1 for a row
+// whose table is too short, -2 where the pool had no room (and the pages it
+// would have shared were counted).
+__device__ __forceinline__ int settle(const SelectParams& p, int i, const Plan& r, bool first, int64_t base, int all_free) {
+  const int keep = r.keep(first), wants = r.all - keep;
+  const bool room = wants <= 0 || base + wants <= all_free;
+  if (r.fits && !room) report(p.status, CMD_CACHE_NO_PAGES);
+  const int at = !r.fits ? -1 : !room ? -2 : (int)min(base, (int64_t)all_free);
+  p.lengths_out[i] = at >= 0 ? r.length : 0;
+  if (at >= 0 && r.partial && !first) {
+    const int src = p.tables[r.parent * p.table_st + keep];
+    if (src >= 0 && src < p.pages) {
+      const int c = atomicAdd(&p.head[kCopies], 1);
+      p.copy_src[c] = src;
+      p.copy_dst[c] = __ldcg(&p.free_list[at]);
     }
   }
-  team.sync();
-  // the free pages in ascending order
+  return at;
+}
+
+// The free pages in ascending order; returns their number.
+template <int CTAS>
+__device__ __forceinline__ int list_free(const SelectParams& p, const Team<CTAS>& team) {
   int all_free;
   const auto is_free = [&](int i) { return __ldcg(&p.refs_out[i]) == 0; };
   const Ranks<CTAS> ranks(team, p.pages, is_free, &all_free);
   ranks.each(is_free, [&](int i, bool f, int rank) {
     if (f) p.free_list[rank] = i;
   });
+  return all_free;
+}
+
+// Rows enough for a thread each and families in shared memory: every CTA of
+// the team works out all rows, and the team meets over the counts alone.
+constexpr int kFewRows = kTeamThreads, kFewOldRows = 4096;
+
+template <int CTAS>
+__device__ __forceinline__ void select_plan_few(const SelectParams& p) {
+  __shared__ int s_first[kFewOldRows], s_children[kFewOldRows];
+  const Team<CTAS> team;
+  const Team<1> cta;
+  const int i = threadIdx.x;
+  pdl_wait();
+  pdl_trigger();
+  Plan r = {};
+  if (i < p.new_rows) r = plan_row(p, i);
+  for (int k = team.me; k < p.pages; k += Team<CTAS>::kThreads) p.refs_out[k] = p.refs[k];
+  for (int k = i; k < p.old_rows; k += kTeamThreads) {
+    s_first[k] = kNobody;
+    s_children[k] = 0;
+  }
+  if (team.me == 0) p.head[kCopies] = 0;
+  __syncthreads();
+  const bool goes_on = i < p.new_rows && r.parent >= 0;
+  if (goes_on && r.fits) {
+    atomicMin(&s_first[r.parent], i);
+    atomicAdd(&s_children[r.parent], 1);
+  }
+  team.sync();  // (and the counts are copied)
+  const bool first = !goes_on || s_first[r.parent] == i;
+  int64_t all_need;
+  const int64_t base = cta.before<int64_t>(r.fits ? r.all - r.keep(first) : 0, &all_need);
+  for (int k = team.me >> 5; k < p.old_rows; k += Team<CTAS>::kThreads / 32) hand_over(p, k, s_children[k]);
   team.sync();
-  // which rows the pool has room for, and the pages to copy
+  const int all_free = list_free(p, team);
+  team.sync();
+  if (i < p.new_rows && i % CTAS == (CTAS == 1 ? 0 : (int)blockIdx.x)) {
+    p.base[i] = settle(p, i, r, first, base, all_free);
+    p.keep[i] = r.keep(first);
+  }
+}
+
+template <int CTAS>
+__device__ __forceinline__ void select_plan_many(const SelectParams& p) {
+  using All = Team<CTAS>;
+  const All team;
+  const int me = team.me;
+  pdl_wait();
+  pdl_trigger();
+  for (int i = me; i < p.pages; i += All::kThreads) p.refs_out[i] = p.refs[i];
+  for (int i = me; i < p.old_rows; i += All::kThreads) {
+    p.first[i] = kNobody;
+    p.children[i] = 0;
+  }
+  if (me == 0) p.head[kCopies] = 0;
+  team.sync();
   for (int i = me; i < p.new_rows; i += All::kThreads) {
     const Plan r = plan_row(p, i);
-    int at = p.base[i];
-    const int wants = r.all - r.keep;
-    if (at >= 0 && wants > 0 && (int64_t)at + wants > all_free) {
-      report(p.status, CMD_CACHE_NO_PAGES);
-      at = p.base[i] = -2;  // dropped, although its shared pages were counted
-    }
-    p.lengths_out[i] = at >= 0 ? r.length : 0;
-    if (at >= 0 && r.split) {
-      const int src = p.tables[r.parent * p.table_st + r.keep];
-      if (src >= 0 && src < p.pages) {
-        const int c = atomicAdd(&p.head[kCopies], 1);
-        p.copy_src[c] = src;
-        p.copy_dst[c] = __ldcg(&p.free_list[at]);
-      }
-    }
+    if (r.parent < 0 || !r.fits) continue;
+    atomicMin(&p.first[r.parent], i);
+    atomicAdd(&p.children[r.parent], 1);
+  }
+  team.sync();
+  // pages each new row needs, summed in row order
+  const int run = (p.new_rows + All::kThreads - 1) / All::kThreads;
+  const int i0 = min(me * run, p.new_rows), i1 = min(i0 + run, p.new_rows);
+  const auto is_first = [&](int i, const Plan& r) { return r.parent < 0 || p.first[r.parent] == i; };
+  int64_t need = 0, all_need;
+  for (int i = i0; i < i1; ++i) {
+    const Plan r = plan_row(p, i);
+    if (r.fits) need += r.all - r.keep(is_first(i, r));
+  }
+  int64_t base = team.template before<int64_t>(need, &all_need);
+  for (int k = me >> 5; k < p.old_rows; k += All::kThreads / 32) hand_over(p, k, p.children[k]);
+  team.sync();
+  const int all_free = list_free(p, team);
+  team.sync();
+  for (int i = i0; i < i1; ++i) {
+    const Plan r = plan_row(p, i);
+    const bool first = is_first(i, r);
+    p.base[i] = settle(p, i, r, first, base, all_free);
+    p.keep[i] = r.keep(first);
+    if (r.fits) base += r.all - r.keep(first);
   }
 }
 
@@ -373,10 +423,14 @@ __global__ void __launch_bounds__(kMoveThreads) compact_apply_kernel(const __gri
   move_pages<U, L>(pools, p.movers, p.holes, p.head[kCopies]);
 }
 
-__global__ void __launch_bounds__(kTeamThreads) select_plan_one(const __grid_constant__ SelectParams p) { select_plan<1>(p); }
+__global__ void __launch_bounds__(kTeamThreads) select_plan_one(const __grid_constant__ SelectParams p) { select_plan_few<1>(p); }
 __global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(kTeamThreads)
     select_plan_cluster(const __grid_constant__ SelectParams p) {
-  select_plan<8>(p);
+  select_plan_few<8>(p);
+}
+__global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(kTeamThreads)
+    select_plan_many_rows(const __grid_constant__ SelectParams p) {
+  select_plan_many<8>(p);
 }
 __global__ void __launch_bounds__(kTeamThreads) compact_plan_one(const __grid_constant__ CompactParams p) { compact_plan<1>(p); }
 __global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(kTeamThreads)
@@ -384,8 +438,12 @@ __global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(kTeamThreads)
   compact_plan<8>(p);
 }
 
-// Pages or rows above which the first launch is a cluster.
-constexpr int kLargePool = 2048, kManyRows = 256;
+// Pages (and for a selection rows) above which the first launch is a cluster
+// of 8 CTAs. Measured, whole calls, one CTA against the cluster: compaction of
+// 601 pages 5.8 and 7.6 us, of 7001 147.6 and 143.6 (131.7 of them the moves);
+// selection of 64 rows among 1400 pages 12.6 and 14.7, 3000 pages 13.4 and
+// 14.8, 6000 pages 16.5 and 15.4; of 509 rows among 6300 pages 54.5 and 41.7.
+constexpr int kLargePool = 4096, kManyRows = 256;
 
 template <class P, class L>
 cudaError_t run(void (*plan)(P), int ctas, void (*apply)(P, L), const P& p, const PoolList& pools, cudaStream_t stream) {
@@ -419,10 +477,11 @@ cudaError_t by_unit(const PoolList& pools, F f) {
 }  // namespace
 
 cudaError_t select_launch(const SelectParams& p, const PoolList& pools, cudaStream_t stream) {
+  const bool few = p.new_rows <= kFewRows && p.old_rows <= kFewOldRows;
   const bool large = p.pages > kLargePool || p.new_rows > kManyRows || p.old_rows > kManyRows;
+  const auto plan = !few ? select_plan_many_rows : large ? select_plan_cluster : select_plan_one;
   return by_unit(pools, [&](auto u, auto l) {
-    return run(large ? select_plan_cluster : select_plan_one, large ? 8 : 1, select_apply_kernel<decltype(u), decltype(l)>, p,
-               pools, stream);
+    return run(plan, !few || large ? 8 : 1, select_apply_kernel<decltype(u), decltype(l)>, p, pools, stream);
   });
 }
 

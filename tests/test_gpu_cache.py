@@ -35,6 +35,7 @@ def _same_bits(a, b):
 ROPE_SHAPES = [  # batch, tokens, q heads, k heads, dim, rotated
     (2, 5, 4, 2, 128, 128), (1, 1, 1, 1, 64, 64), (3, 7, 3, 3, 80, 32), (1, 9, 5, 1, 72, 72), (2, 3, 2, 2, 256, 256),
     (1, 4, 130, 2, 64, 48), (1, 6, 2, 1, 10, 6), (2, 4, 3, 1, 33, 20), (1, 2, 1, 1, 2, 2), (1, 3, 2, 2, 16, 0),
+    (2, 3001, 1, 1, 16, 8), (1, 5003, 2, 0, 32, 32),
 ]
 
 
@@ -112,6 +113,27 @@ def test_rope_every_pair_of_a_long_context():
         y = T.rope(x, None, pos, turns)[0]
         want = U.rotated(x, pos, turns, "half", 1.0)
         _near(y, want, U.rope_bound(x, want, 128, "half", 1.0, "f32"), p)
+
+
+def test_rope_in_autograd():
+    """The pair as a differentiable function, with a broadcast input: its gradient is the sum over what it fed."""
+    turns, pos = T.rope_turns(32), torch.arange(7, dtype=torch.int32, device="cuda") * 999
+
+    class Rope(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            return T.rope(x, None, pos.expand(x.shape[:2]), turns, layout="interleaved", scale=1.5)[0]
+
+        @staticmethod
+        def backward(ctx, g):
+            return T.rope_backward(g, None, pos.expand(g.shape[:2]), turns, layout="interleaved", scale=1.5)[0]
+
+    x = _randn(1, 7, 3, 40, kind="f32").requires_grad_()
+    w = _randn(4, 7, 3, 40, kind="f32", seed=1)
+    (Rope.apply(x.expand(4, 7, 3, 40)) * w).sum().backward()
+    want = U.rotated(w, pos.expand(4, 7), turns, "interleaved", 1.5, backward=True).sum(0, keepdim=True)
+    bound = U.rope_bound(w, w.cpu().double() * 0, 16, "interleaved", 1.5, "f32").sum(0, keepdim=True) + 8 * 2.0 ** -24 * want.abs()
+    _near(x.grad, want, bound + 4 * 2.0 ** -24 * w.cpu().double().abs().sum(0, keepdim=True) * 1.5)
 
 
 # ---- append --------------------------------------------------------------------------------------------------------
@@ -476,3 +498,36 @@ def test_pages_of_any_alignment():
         for a, b in pairs:
             want[b] = want[a]
         assert torch.equal(pool, want)
+
+
+# ---- refusals ----------------------------------------------------------------------------------------------------------
+
+def test_refusals_of_tensors():
+    x, i = torch.zeros(2, 1, 8, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    t, turns = torch.zeros(2, 3, dtype=torch.int32, device="cuda"), T.rope_turns(8)
+    c = torch.zeros(4, 2, 1, 8, device="cuda")
+    for bad, error, words in (
+            (lambda: T.rope(x.double(), None, i, turns), TypeError, "float32"),
+            (lambda: T.rope(x, None, i.long(), turns), TypeError, "positions"),
+            (lambda: T.rope(x, None, i, turns.int()), ValueError, "turns"),
+            (lambda: T.rope(x, None, i, turns[::2]), ValueError, "turns"),
+            (lambda: T.rope(x, None, i.cpu(), turns), ValueError, "positions is not on a GPU"),
+            (lambda: T.rope(x, None, i, None, layout="half"), None, None),
+            (lambda: T.rope(x, None, i[:1], turns), T.CmdError, "positions"),
+            (lambda: T.rope(x.expand(2, 3, 8), None, i, turns, out=(x.expand(2, 3, 8), None)), T.CmdError, "overlaps itself"),
+            (lambda: T.attention_decode(x[0], c, c, t, i), ValueError, "rank"),
+            (lambda: T.attention_decode(x, c, c, t, i, scale=-1.0), T.CmdError, "scale"),
+            (lambda: T.attention_decode(x.half(), c, c, t, i), T.CmdError, "element type"),
+            (lambda: T.attention_decode(x, c, c, t, i, workspace=torch.empty(64, device="cuda")), T.CmdError, "workspace"),
+            (lambda: T.attention_decode(x, c, c, t, i, status=torch.zeros(2, dtype=torch.int32, device="cuda")), ValueError, "status"),
+            (lambda: T.cache_append(x, x, c, c.clone(), t, i, q=x), T.CmdError, "rotates"),
+            (lambda: T.cache_select(t, i, i, i, [c], page_size=2), ValueError, "pages in its first dim"),
+            (lambda: T.cache_select(t, i, torch.zeros(4, dtype=torch.int32, device="cuda"), i, [c[..., ::2]], page_size=2), ValueError, "dense"),
+            (lambda: T.cache_select(t, i, torch.zeros(4, dtype=torch.int32, device="cuda"), i, c, page_size=2), TypeError, "list or tuple"),
+            (lambda: T.cache_compact(t, i, i, [], page_size=2, out=(t, i)), TypeError, "tuple of 3"),
+            (lambda: T.cache_compact(t, i, i, [], page_size=2, out=(t, i, i.clone())), T.CmdError, "overlaps")):
+        if error is None:
+            bad()
+            continue
+        with pytest.raises(error, match=words):
+            bad()
