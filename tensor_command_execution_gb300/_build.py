@@ -137,7 +137,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.replace(tmp, LIB_PATH)
     tmp = TORCH_PATH + f".tmp{os.getpid()}"
     link = (["g++", "-shared", "-o", tmp, torch_obj, "-L" + os.path.join(torch_dir, "lib"), "-L" + OUT_DIR]
-            + ["-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-l:libcmdexec.so", "-Wl,-rpath,$ORIGIN"])
+            + ["-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-l:libcmdexec.so", "-Wl,-rpath,$ORIGIN"])
     r = subprocess.run(link, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed: {' '.join(link)}\n{r.stdout}\n{r.stderr}")

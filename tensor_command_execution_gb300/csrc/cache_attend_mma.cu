@@ -68,8 +68,8 @@ constexpr int kWarps = 4;
 // Stages of each warp's ring, and CTAs of an SM, for heads of up to DP dims.
 template <class T, int DP, int NT>
 struct Shape {
-  static constexpr int kStages = DP == 64 ? 3 : 2;
-  static constexpr int kCtas = DP == 256 ? 1 : NT == 2 ? 2 : 3;
+  static constexpr int kStages = 2;
+  static constexpr int kCtas = DP == 256 ? 1 : NT == 2 ? 2 : DP == 64 ? 4 : 3;
   static constexpr int kPitch = DP * 2 + 16;                   // bytes of a row: an odd number of 16
   using Ring = AttendRing<T, kTokens, DP / 8, kPitch, kStages, kWarps>;
   static constexpr int kSmem = kWarps * Ring::kBytes + (int)sizeof(AttendRows);

@@ -6,7 +6,8 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -104,11 +105,14 @@ int32_t integer(PyObject* o, const char* name) {
 // The device of a call's tensors, made current, and its current stream.
 struct Where {
   c10::cuda::CUDAGuard guard;
-  at::TensorOptions options;
   void* stream;
   explicit Where(const at::Tensor& t)
-      : guard(t.device()), options(t.options()), stream(c10::cuda::getCurrentCUDAStream(t.device().index()).stream()) {}
-  at::Tensor empty(at::IntArrayRef sizes, at::ScalarType type) const { return at::empty(sizes, options.dtype(type)); }
+      : guard(t.device()), stream(c10::cuda::getCurrentCUDAStream(t.device().index()).stream()) {}
+  at::Tensor empty(at::IntArrayRef sizes, at::ScalarType type) const {
+    return at::detail::empty_cuda(sizes, type, guard.current_device(), std::nullopt);
+  }
+  // memory for the current stream, given back (for work after the call's on that stream) when the result goes
+  c10::DataPtr scratch(int64_t bytes) const { return c10::cuda::CUDACachingAllocator::get()->allocate((size_t)bytes); }
 };
 
 void same_device(const Where& w, PyObject* o, const char* name) {
@@ -230,7 +234,8 @@ PyObject* py_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     x.scale = (float)(a[5] != Py_None ? number(a[5]) : dim > 0 ? 1.0 / std::sqrt((double)dim) : 1.0);
     x.softcap = (float)number(a[6]);
     x.window = integer(a[7], "window");
-    at::Tensor out, lse, workspace;
+    at::Tensor out, lse;
+    c10::DataPtr workspace;
     x.out = a[8] == Py_None ? describe(out = w.empty(q.sizes(), q.scalar_type()), "out") : operand(a[8], "out");
     const bool with_lse = PyObject_IsTrue(a[10]);
     if (a[9] != Py_None) x.lse = operand(a[9], "lse");
@@ -243,8 +248,8 @@ PyObject* py_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
       x.workspace_bytes = (int64_t)t.nbytes();
     } else if (heads > 0 && kv > 0 && heads % kv == 0 && heads <= INT32_MAX && dim <= CMD_CACHE_MAX_DIM) {
       check(cmd_attention_workspace((int32_t)heads, (int32_t)kv, (int32_t)dim, &x.workspace_bytes), "cmd_attention_workspace");
-      workspace = w.empty({x.workspace_bytes}, at::kByte);
-      x.workspace = workspace.data_ptr();
+      workspace = w.scratch(x.workspace_bytes);
+      x.workspace = workspace.get();
     }
     x.status = status_word(a[12]);
     const char* names[] = {"q", "k_cache", "v_cache", "tables", "lengths"};
@@ -320,7 +325,8 @@ PyObject* py_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (x.tables.rank != 2 || x.refs.rank != 1 || x.parents.rank != 1)
       raise(PyExc_ValueError, "tables has rank 2, refs and parents have rank 1");
     const int64_t rows = x.parents.sizes[0], pages = x.refs.sizes[0];
-    at::Tensor made[3], workspace;
+    at::Tensor made[3];
+    c10::DataPtr workspace;
     PyObject* out[3] = {item(a[7], 0, 3), item(a[7], 1, 3), item(a[7], 2, 3)};
     x.tables_out = output(out[0], w, {rows, x.tables.sizes[1]}, &made[0], "tables_out");
     x.lengths_out = output(out[1], w, {rows}, &made[1], "lengths_out");
@@ -330,8 +336,8 @@ PyObject* py_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
     x.n_pools = pools(a[4], pages, w, list);
     x.page_size = integer(a[5], "page_size");
     check(cmd_select_workspace(x.tables.sizes[0], rows, pages, &x.workspace_bytes), "cmd_select_workspace");
-    workspace = w.empty({x.workspace_bytes}, at::kByte);
-    x.workspace = workspace.data_ptr();
+    workspace = w.scratch(x.workspace_bytes);
+    x.workspace = workspace.get();
     x.status = status_word(a[8]);
     const char* names[] = {"tables", "lengths", "refs", "parents"};
     for (int i = 0; i < 4; ++i) same_device(w, a[i], names[i]);
@@ -352,7 +358,8 @@ PyObject* py_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
     x.refs = operand(a[2], "refs");
     if (x.tables.rank != 2 || x.refs.rank != 1) raise(PyExc_ValueError, "tables has rank 2 and refs has rank 1");
     const int64_t pages = x.refs.sizes[0];
-    at::Tensor made[3], workspace;
+    at::Tensor made[3];
+    c10::DataPtr workspace;
     PyObject* out[3] = {item(a[5], 0, 3), item(a[5], 1, 3), item(a[5], 2, 3)};
     x.tables_out = output(out[0], w, {x.tables.sizes[0], x.tables.sizes[1]}, &made[0], "tables_out");
     x.refs_out = output(out[1], w, {pages}, &made[1], "refs_out");
@@ -362,8 +369,8 @@ PyObject* py_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
     x.n_pools = pools(a[3], pages, w, list);
     x.page_size = integer(a[4], "page_size");
     check(cmd_compact_workspace(pages, &x.workspace_bytes), "cmd_compact_workspace");
-    workspace = w.empty({x.workspace_bytes}, at::kByte);
-    x.workspace = workspace.data_ptr();
+    workspace = w.scratch(x.workspace_bytes);
+    x.workspace = workspace.get();
     x.status = status_word(a[6]);
     const char* names[] = {"tables", "lengths", "refs"};
     for (int i = 0; i < 3; ++i) same_device(w, a[i], names[i]);

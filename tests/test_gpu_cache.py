@@ -355,6 +355,39 @@ def test_attention_on_streams_and_in_a_graph():
     assert _same_bits(out, T.attention_decode(q, c.k, c.v, c.tables, lengths))
 
 
+def test_a_whole_step_in_a_graph():
+    """Selection, append and attention captured without buffers of their own; replayed, they do what the calls do."""
+    c = U.Cache("bf16", [33, 16, 5], 2, 64, 16, spare=12, columns=4)
+    refs = torch.zeros(c.pages, dtype=torch.int32, device="cuda")
+    for r, n in enumerate(c.need):
+        refs[c.tables[r, :n].long()] += 1
+    parents, one = torch.tensor([1, 0, 0], dtype=torch.int32, device="cuda"), torch.ones(3, dtype=torch.int32, device="cuda")
+    q, k, v = (_randn(3, h, 64, kind="bf16", seed=h) for h in (8, 2, 2))
+    turns, pools = T.rope_turns(64), [c.k, c.v]
+
+    def step():
+        t, n, r = T.cache_select(c.tables, c.lengths, refs, parents, pools, page_size=16, grow=one)
+        x = T.cache_append(k, v, c.k, c.v, t, n - 1, q=q, turns=turns)
+        return t, n, r, T.attention_decode(x, c.k, c.v, t, n)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        want = [x.clone() for x in step()]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        got = step()
+    for new in ([1, 0, 0], [1, 0, 0], [2, 2, -1]):  # (the last takes the pages of rows 0 and 1)
+        parents.copy_(torch.tensor(new))
+        g.replay()
+        torch.cuda.synchronize()
+        if new[2] == 0:
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+        else:
+            assert got[1].tolist() == [6, 6, 1] and int((got[2] > 0).sum()) == 3
+
+
 # ---- pages -----------------------------------------------------------------------------------------------------------
 
 def _select_case(seed, rows, new_rows, page, columns, spare, longest, grow, dim=16, heads=2, kind="bf16", order="slots"):
