@@ -187,14 +187,6 @@ void check_apart(const cmd_operand& out, const char* out_name, const cmd_operand
   throw Failure{CMD_ERR_ALIAS, std::string(out_name) + " overlaps " + in_name};
 }
 
-cmdx::FastDiv32 fast_div32(uint32_t d) {
-  cmdx::FastDiv32 f = {0, 0, d};
-  if (d < 2) return f;
-  while ((uint64_t(1) << f.l) < d) ++f.l;
-  f.m = (uint32_t)(((uint64_t(1) << 32) * ((uint64_t(1) << f.l) - d)) / d + 1);
-  return f;
-}
-
 // Whether rows of a view may be accessed `bytes` at a time.
 bool vector_rows(const cmd_operand& o, int bytes) {
   const int es = elem_size(o.dtype);
@@ -212,6 +204,13 @@ void check_rope(const cmd_rope_spec& r, int64_t dim) {
     NEED(r.turns != nullptr, CMD_ERR_NULL, "turns is NULL");
     NEED(reinterpret_cast<uintptr_t>(r.turns) % 8 == 0, CMD_ERR_ALIGN, "turns is not 8-byte aligned");
   }
+}
+
+// Whether a view's rows are whole 16-byte vectors, and its strides below 2^31.
+bool rope_rows(const cmd_operand& o) {
+  for (int d = 0; d < o.rank; ++d)
+    if (o.sizes[d] > 1 && o.strides[d] > 0x7fffffff) return false;
+  return vector_rows(o, 16);
 }
 
 // Whether every chunk of 16 bytes of a head lies wholly in the rotated part
@@ -336,7 +335,7 @@ extern "C" cmd_status cmd_rope(const cmd_operand* q, const cmd_operand* q_out, c
       check_apart(out, names[j][1], *positions, "positions");
       check_heads(in.sizes[in.rank - 2]);
       nothing = nothing || in.sizes[in.rank - 3] == 0 || in.sizes[in.rank - 1] == 0 || in.sizes[0] == 0;
-      vec = vec && vector_rows(in, 16) && vector_rows(out, 16);
+      vec = vec && rope_rows(in) && rope_rows(out);
       p.s[p.n_streams++] = rope_stream(in, out, true, false);
     }
     NEED(like, CMD_ERR_NULL, "q and k are both absent");
@@ -359,7 +358,7 @@ extern "C" cmd_status cmd_rope(const cmd_operand* q, const cmd_operand* q_out, c
       p.batch = (int32_t)like->sizes[0];
     }
     NEED((__int128)p.batch * p.tokens <= 0x7fffffff, CMD_ERR_LIMIT, "more than 2^31 - 1 tokens");
-    p.per_batch = fast_div32((uint32_t)p.tokens);
+    p.per_batch = cmdx::fast_div_by((uint32_t)p.tokens);
     p.positions = static_cast<const int32_t*>(positions->ptr);
     p.pos_st[0] = lead == 2 ? positions->strides[0] : 0;
     p.pos_st[1] = positions->strides[lead - 1];
@@ -432,7 +431,7 @@ extern "C" cmd_status cmd_cache_append(const cmd_append_args* args, void* cuda_s
     check_apart(a.k_cache, "k_cache", a.v_cache, "v_cache");
     cmdx::RopeParams p;
     std::memset(&p, 0, sizeof p);
-    bool vec = vector_rows(a.k, 16) && vector_rows(a.v, 16) && vector_rows(a.k_cache, 16) && vector_rows(a.v_cache, 16);
+    bool vec = rope_rows(a.k) && rope_rows(a.v) && rope_rows(a.k_cache) && rope_rows(a.v_cache);
     if (has_q) {
       check(a.q, "q", 3, true);
       check(a.q_out, "q_out", 3, true);
@@ -446,14 +445,14 @@ extern "C" cmd_status cmd_cache_append(const cmd_append_args* args, void* cuda_s
       for (const auto& r : reads) check_apart(a.q_out, "q_out", *r.o, r.name, r.o == &a.q);
       check_apart(a.q_out, "q_out", a.k_cache, "k_cache");
       check_apart(a.q_out, "q_out", a.v_cache, "v_cache");
-      vec = vec && vector_rows(a.q, 16) && vector_rows(a.q_out, 16);
+      vec = vec && rope_rows(a.q) && rope_rows(a.q_out);
       p.s[p.n_streams++] = rope_stream(a.q, a.q_out, true, false);
     }
     p.s[p.n_streams++] = rope_stream(a.k, a.k_cache, true, true);
     p.s[p.n_streams++] = rope_stream(a.v, a.v_cache, false, true);
     p.batch = 1;
     p.tokens = tokens;
-    p.per_batch = fast_div32((uint32_t)tokens);
+    p.per_batch = cmdx::fast_div_by((uint32_t)tokens);
     p.positions = static_cast<const int32_t*>(a.positions.ptr);
     p.pos_st[1] = a.positions.strides[0];
     p.tables = static_cast<const int32_t*>(a.tables.ptr);
@@ -464,7 +463,7 @@ extern "C" cmd_status cmd_cache_append(const cmd_append_args* args, void* cuda_s
     p.n_rows = (int32_t)a.tables.sizes[0];
     p.columns = (int32_t)a.tables.sizes[1];
     p.n_pages = (int32_t)a.k_cache.sizes[0];
-    p.page = fast_div32((uint32_t)a.k_cache.sizes[1]);
+    p.page = cmdx::fast_div_by((uint32_t)a.k_cache.sizes[1]);
     p.status = a.status;
     rope_common(p, a.rope, dim);
     if (tokens == 0 || dim == 0 || p.heads == 0) return CMD_OK;
@@ -547,7 +546,7 @@ extern "C" cmd_status cmd_attention_decode(const cmd_attention_args* args, void*
     p.dim = (int32_t)dim;
     p.n_pages = (int32_t)a.k_cache.sizes[0];
     p.columns = (int32_t)a.tables.sizes[1];
-    p.page = fast_div32((uint32_t)a.k_cache.sizes[1]);
+    p.page = cmdx::fast_div_by((uint32_t)a.k_cache.sizes[1]);
     const double log2e = 1.4426950408889634074;
     p.scale_log2 = (float)(a.scale * log2e);
     p.cap_in = a.softcap > 0.0f ? (float)((double)a.scale / a.softcap) : 0.0f;
@@ -742,7 +741,7 @@ extern "C" cmd_status cmd_cache_select(const cmd_select_args* args, void* cuda_s
     p.new_rows = (int32_t)new_rows;
     p.columns = (int32_t)columns;
     p.pages = (int32_t)pages;
-    p.page = fast_div32((uint32_t)a.page_size);
+    p.page = cmdx::fast_div_by((uint32_t)a.page_size);
     p.status = a.status;
     Words w = {static_cast<int32_t*>(a.workspace)};
     p.head = w.take(kHeadWords);
@@ -812,7 +811,7 @@ extern "C" cmd_status cmd_cache_compact(const cmd_compact_args* args, void* cuda
     p.rows = (int32_t)a.tables.sizes[0];
     p.columns = (int32_t)columns;
     p.pages = (int32_t)pages;
-    p.page = fast_div32((uint32_t)a.page_size);
+    p.page = cmdx::fast_div_by((uint32_t)a.page_size);
     p.status = a.status;
     Words w = {static_cast<int32_t*>(a.workspace)};
     p.head = w.take(kHeadWords);

@@ -17,6 +17,13 @@ namespace cmdx {
 struct FastDiv32 {
   uint32_t m, l, d;
 };
+inline FastDiv32 fast_div_by(uint32_t d) {
+  FastDiv32 f = {0, 0, d};
+  if (d < 2) return f;
+  while ((uint64_t(1) << f.l) < d) ++f.l;
+  f.m = (uint32_t)(((uint64_t(1) << 32) * ((uint64_t(1) << f.l) - d)) / d + 1);
+  return f;
+}
 
 // ---- rotation and append (cache_rope.cu) --------------------------------------
 // What a tensor of the launch is: rotated or copied, into a tensor or into a
@@ -52,7 +59,8 @@ struct RopeParams {
   int32_t* status;
 };
 
-// vec: every row of every stream may be accessed in 16-byte vectors
+// vec: every row of every stream may be accessed in 16-byte vectors, and every
+// stride is below 2^31
 cudaError_t rope_launch(int dtype, int layout, bool vec, const RopeParams& p, cudaStream_t stream);
 
 // ---- attention of one token (cache_attend*.cu) --------------------------------

@@ -158,14 +158,23 @@ struct Chunk<T, VE, true> {
 // once, `tokens` tokens.
 struct RopeShape {
   int units, slots, tokens;
+  FastDiv32 by_units, by_slots, by_pairs;
 };
+
+// An index times a stride: strides of the vector kernels are below 2^31 (see
+// rope_launch's vec), which makes it one instruction.
+template <bool NARROW>
+__device__ __forceinline__ int64_t stride_of(int64_t index, int64_t stride) {
+  return NARROW ? (int64_t)(int32_t)index * (int32_t)stride : index * stride;
+}
 
 template <class T, int VE, bool VEC, bool HALF>
 __global__ void __launch_bounds__(512, 2) rope_kernel(const __grid_constant__ RopeParams p, const RopeShape shape) {
   constexpr int NP = HALF ? VE : VE / 2;  // pairs of a thread's place
   extern __shared__ __align__(16) float2 s_turn[];  // [tokens][n_pairs]: cosine and sine
   const int tid = threadIdx.x;
-  const int unit = tid % shape.units, slot = tid / shape.units % shape.slots, mine = tid / (shape.units * shape.slots);
+  const int column = (int)fast_div32(shape.by_units, tid), unit = tid - column * shape.units;
+  const int mine = (int)fast_div32(shape.by_slots, column), slot = column - mine * shape.slots;
   const int rot = 2 * p.n_pairs, groups = p.n_pairs / NP;
   // the thread's two places in a head: their first elements, the elements
   // they have (fewer at an odd head's end, 0 for none), and whether they are
@@ -194,7 +203,7 @@ __global__ void __launch_bounds__(512, 2) rope_kernel(const __grid_constant__ Ro
   const int64_t all = p.batch * p.tokens;
   // the CTA's angles, one to a thread: their position and turns are read now
   const auto angle_position = [&](int i) {
-    const uint32_t at = (uint32_t)(first + i / p.n_pairs);
+    const uint32_t at = (uint32_t)first + fast_div32(shape.by_pairs, i);
     const int64_t ob = fast_div32(p.per_batch, at);
     return at < all ? p.positions[ob * p.pos_st[0] + (at - ob * p.tokens) * p.pos_st[1]] : 0;
   };
@@ -203,7 +212,7 @@ __global__ void __launch_bounds__(512, 2) rope_kernel(const __grid_constant__ Ro
   uint64_t angle_turns = 0;
   if (tid < angles) {
     angle_at = angle_position(tid);
-    angle_turns = p.turns[tid % p.n_pairs];
+    angle_turns = p.turns[tid - fast_div32(shape.by_pairs, tid) * p.n_pairs];
   }
   const bool works = mine < shape.tokens && first + mine < all;
   const uint32_t token = works ? (uint32_t)(first + mine) : 0;
@@ -243,12 +252,14 @@ __global__ void __launch_bounds__(512, 2) rope_kernel(const __grid_constant__ Ro
       int j = 0;
       while (h >= p.s[j].heads) h -= p.s[j++].heads;
       const RopeStream& s = p.s[j];
-      const T* src = static_cast<const T*>(s.in) + b * s.in_st[0] + t * s.in_st[1] + h * s.in_st[2];
+      const T* src = static_cast<const T*>(s.in) + stride_of<VEC>(b, s.in_st[0]) + stride_of<VEC>(t, s.in_st[1]) + stride_of<VEC>(h, s.in_st[2]);
       if (s.cache) {
         if (page < 0) continue;
-        dst[i] = static_cast<T*>(s.out) + page * s.out_st[0] + page_slot * s.out_st[1] + h * s.out_st[2];
+        dst[i] = static_cast<T*>(s.out) + stride_of<VEC>(page, s.out_st[0]) + stride_of<VEC>(page_slot, s.out_st[1]) +
+                 stride_of<VEC>(h, s.out_st[2]);
       } else {
-        dst[i] = static_cast<T*>(s.out) + b * s.out_st[0] + t * s.out_st[1] + h * s.out_st[2];
+        dst[i] = static_cast<T*>(s.out) + stride_of<VEC>(b, s.out_st[0]) + stride_of<VEC>(t, s.out_st[1]) +
+                 stride_of<VEC>(h, s.out_st[2]);
       }
       rotate[i] = s.rotate;
 #pragma unroll
@@ -259,12 +270,12 @@ __global__ void __launch_bounds__(512, 2) rope_kernel(const __grid_constant__ Ro
       for (int i = tid; i < angles; i += blockDim.x) {
         if (i != tid) {
           angle_at = angle_position(i);
-          angle_turns = p.turns[i % p.n_pairs];
+          angle_turns = p.turns[i - fast_div32(shape.by_pairs, i) * p.n_pairs];
         }
         const uint64_t phase = (uint64_t)(int64_t)angle_at * angle_turns;
         float s, c;
         sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &c);
-        const int k = i / p.n_pairs;
+        const int k = (int)fast_div32(shape.by_pairs, i);
         s_turn[k * p.n_pairs + turn_at<NP>(i - k * p.n_pairs, groups)] = make_float2(c * p.scale, s * p.sine_scale);
       }
       __syncthreads();
@@ -303,6 +314,9 @@ cudaError_t launch(const RopeParams& p, cudaStream_t stream) {
   if (s.tokens > each) s.tokens = (int)each;
   if (s.tokens < 1) s.tokens = 1;
   const int threads = (s.units * s.slots * s.tokens + 31) / 32 * 32;
+  s.by_units = fast_div_by(s.units);
+  s.by_slots = fast_div_by(s.slots);
+  s.by_pairs = fast_div_by(p.n_pairs);
   return launch_pdl(rope_kernel<T, VE, VEC, HALF>, (int)((all + s.tokens - 1) / s.tokens), threads,
                     (size_t)s.tokens * p.n_pairs * sizeof(float2), stream, p, s);
 }
