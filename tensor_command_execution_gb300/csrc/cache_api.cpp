@@ -516,6 +516,7 @@ extern "C" cmd_status cmd_attention_decode(const cmd_attention_args* args, void*
     check_distinct(a.out, "out");
     const int64_t rows = a.q.sizes[0], heads = a.q.sizes[1], dim = a.q.sizes[2], kv = a.k_cache.sizes[2];
     NEED(dim == a.k_cache.sizes[3], CMD_ERR_SHAPE, "q and k_cache differ in dim");
+    NEED(dim >= 1, CMD_ERR_SHAPE, "a head has no elements");
     NEED(kv >= 1 ? heads % kv == 0 : heads == 0, CMD_ERR_SHAPE, "the cache's heads must divide q's");
     check_heads(heads);
     NEED(rows == a.tables.sizes[0], CMD_ERR_SHAPE, "q and tables differ in rows");
@@ -617,7 +618,7 @@ cmdx::PoolList pool_list(const cmd_pool* pools, int32_t n, int64_t pages) {
   for (int i = 0; i < n; ++i) {
     NEED(pools[i].page_bytes >= 0 && pools[i].page_stride >= pools[i].page_bytes, CMD_ERR_SHAPE,
          "a pool's pages overlap (page_stride below page_bytes)");
-    NEED(pools[i].page_stride < ((int64_t)1 << 40), CMD_ERR_LIMIT, "a page stride above 2^40 bytes");
+    NEED((__int128)pools[i].page_stride * pages < ((__int128)1 << 60), CMD_ERR_LIMIT, "a pool extends past the address space");
     if (pools[i].page_bytes == 0 || pages == 0) continue;
     NEED(pools[i].ptr, CMD_ERR_NULL, "a pool's pointer is NULL");
     l.ptr[l.n] = static_cast<uint8_t*>(pools[i].ptr);

@@ -235,6 +235,7 @@ def test_attention_refusals():
     refuses("cmd_attention_decode", (None, None), "CMD_ERR_NULL")
     bad("CMD_ERR_SHAPE", "heads must divide", q=op(3, 5, 16), out=op(3, 5, 16))
     bad("CMD_ERR_SHAPE", "dim", q=op(3, 4, 8), out=op(3, 4, 8))
+    bad("CMD_ERR_SHAPE", "no elements", **{n: op(*s) for n, s in (("q", (3, 4, 0)), ("out", (3, 4, 0)), ("k_cache", (9, 4, 2, 0)), ("v_cache", (9, 4, 2, 0)))})
     bad("CMD_ERR_SHAPE", "rows", tables=op(4, 5, dtype=I32))
     bad("CMD_ERR_SHAPE", "lengths", lengths=op(2, dtype=I32))
     bad("CMD_ERR_TYPE", "lse", lse=op(3, 4, dtype=F16))
@@ -307,6 +308,7 @@ def test_select_and_compact_refusals():
         bad("CMD_ERR_LIMIT", "2.31", page_size=1 << 30)
         bad("CMD_ERR_SHAPE", "overlap", pools=(C.cmd_pool * 2)(_pool(stride=512), _pool()))
         bad("CMD_ERR_NULL", "pool", pools=(C.cmd_pool * 2)(_pool(ptr=0), _pool()))
+        bad("CMD_ERR_LIMIT", "address space", pools=(C.cmd_pool * 2)(_pool(stride=1 << 60), _pool()))
         p = _pool()
         bad("CMD_ERR_ALIAS", "two pools", pools=(C.cmd_pool * 2)(p, p))
         bad("CMD_ERR_ALIAS", "two pools", pools=(C.cmd_pool * 2)(p, _pool(stride=2048, ptr=p.ptr + 1024)))

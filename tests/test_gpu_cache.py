@@ -533,6 +533,40 @@ def test_pages_of_any_alignment():
         assert torch.equal(pool, want)
 
 
+@pytest.mark.parametrize("kind,dim", [("bf16", 256), ("f32", 256), ("bf16", 255)])
+def test_a_pool_past_32_bits(kind, dim):
+    """Pages at element offsets above 2^32: appended to, attended to, copied by a selection and moved by a compaction
+    as the same values in a small pool are."""
+    pages, page, heads = (1 << 32) // (16 * 16 * dim) + 40, 16, 16
+    big = [torch.empty(pages, page, heads, dim, device="cuda", dtype=U.TYPES[kind]) for _ in range(2)]
+    assert big[0].stride(0) * (pages - 9) > 1 << 32
+    small = U.Cache(kind, [40, 20], heads, dim, page)
+    where = {p: pages - 9 + p for p in range(small.pages)}
+    assert small.pages <= 9
+    for a, b in zip(big, (small.k, small.v)):
+        a[pages - 9: pages - 9 + small.pages] = b
+    tables = torch.tensor([[where[p] if p < small.pages else -1 for p in row] for row in small.tables.tolist()],
+                          dtype=torch.int32, device="cuda")
+    q, k, v = (_randn(2, h, dim, kind=kind, seed=h) for h in (32, heads, heads))
+    pos, turns = small.lengths - 1, T.rope_turns(dim // 2 * 2)
+    a = T.cache_append(k, v, big[0], big[1], tables, pos, q=q, turns=turns)
+    b = T.cache_append(k, v, small.k, small.v, small.tables, pos, q=q, turns=turns)
+    assert _same_bits(a, b)
+    want = T.attention_decode(b, small.k, small.v, small.tables, small.lengths)
+    assert _same_bits(T.attention_decode(a, big[0], big[1], tables, small.lengths), want)
+    refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    refs[tables[0, :3].long()] = 1
+    refs[tables[1, :2].long()] = 1
+    parents = torch.tensor([0, 0, 1], dtype=torch.int32, device="cuda")
+    t, n, refs = T.cache_select(tables, small.lengths, refs, parents, big, page_size=page)
+    assert int(t[1, 2]) == 0  # (the copy went to the front of the pool)
+    t, refs, _ = T.cache_compact(t, n, refs, big, page_size=page)
+    assert int(t.max()) == 5 and int((refs > 0).sum()) == 6
+    got = T.attention_decode(a[parents.long()], big[0], big[1], t, n)
+    at = parents.long()
+    assert _same_bits(got, T.attention_decode(b[at], small.k, small.v, small.tables[at], small.lengths[at]))
+
+
 # ---- refusals ----------------------------------------------------------------------------------------------------------
 
 def test_refusals_of_tensors():
