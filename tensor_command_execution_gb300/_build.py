@@ -51,7 +51,7 @@ CU_SOURCES = [("exec_tile2d.cu", _objs((2,), (0, 1))), ("exec_generic.cu", _objs
               ("cache_attend_f32.cu", [{}]), ("cache_rope.cu", [{}]), ("cache_pages.cu", [{}])]
 CPP_SOURCES = ["cmd_api.cpp", "cmd_yaml.cpp", "exec_host.cpp", "cache_api.cpp"]
 TORCH_SOURCE = "cache_torch.cpp"
-HEADERS = ["cmd_internal.h", "exec_common.cuh", "exec_launch.cuh", "exec_pipe.cuh", "exec_tile2d.h", "interp_asm.cuh",
+HEADERS = ["cmd_internal.h", "exec_common.cuh", "exec_pipe.cuh", "exec_tile2d.h", "interp_asm.cuh",
            "gen_interp.py", "cache_internal.h", "cache_common.cuh", "cache_attend.cuh",
            "cache_attend_ring.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -55,8 +55,8 @@ __global__ void __launch_bounds__(kWarps * 32) attend_simt_kernel(const __grid_c
   float(*s_state)[GT][kPitch] = reinterpret_cast<float(*)[GT][kPitch]>(s_mem + kRowsBytes);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int tile = kTokens * kWarps;
-  pdl_wait();
-  pdl_trigger();
+  wait_for_previous();
+  let_next_start();
   AttendShare share;
   if (!attend_begin<T>(p, s_rows, tile, &share)) return;
   const T* kp = static_cast<const T*>(p.k);
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kWarps * 32) attend_simt_kernel(const __grid_c
 template <class T, int GT, int VEC>
 cudaError_t launch(const AttendParams& p, cudaStream_t stream) {
   constexpr int smem = kRowsBytes + kWarps * GT * attend_pitch(32 * VEC) * (int)sizeof(float);
-  static DeviceCache ready;  // (static storage: zero before first use)
+  static PerDevice ready;  // (static storage: zero before first use)
   const cudaError_t e = allow_smem(attend_simt_kernel<T, GT, VEC>, smem, ready);
   if (e != cudaSuccess) return e;
   return attend_launch<T>(attend_simt_kernel<T, GT, VEC>, p, 0, 2 * 152, kWarps * 32, smem, kTokens * kWarps, stream);

@@ -345,8 +345,8 @@ __device__ __forceinline__ void attend_join(const AttendParams& p, int task, flo
 template <class T, int WARPS>
 __global__ void __launch_bounds__(WARPS == 1 ? 256 : WARPS * 32) attend_join_kernel(const __grid_constant__ AttendParams p) {
   __shared__ __align__(16) float s_state[WARPS == 1 ? 1 : WARPS][CMD_CACHE_MAX_DIM + 4];
-  pdl_wait();
-  pdl_trigger();
+  wait_for_previous();
+  let_next_start();
   const int task = WARPS == 1 ? blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
   if (task < p.tasks) attend_join<T, WARPS>(p, task, s_state);
 }
@@ -362,10 +362,10 @@ cudaError_t attend_launch(K kernel, AttendParams p, int start_units, int ctas, i
   p.split_by_row = rows <= ctas;
   const int lists = p.split_by_row ? (int)rows : ctas;
   p.tasks = lists * p.block_heads;
-  cudaError_t e = launch_pdl(kernel, ctas, threads, (size_t)smem, stream, p);
+  cudaError_t e = launch_chained(kernel, ctas, threads, (size_t)smem, stream, p);
   if (e != cudaSuccess || (int64_t)p.columns * p.page.d <= tile) return e;  // (a row of one tile is never split)
-  if (lists * 16 <= ctas) return launch_pdl(attend_join_kernel<T, 16>, p.tasks, 512, 0, stream, p);
-  return launch_pdl(attend_join_kernel<T, 1>, (p.tasks + 7) / 8, 256, 0, stream, p);
+  if (lists * 16 <= ctas) return launch_chained(attend_join_kernel<T, 16>, p.tasks, 512, 0, stream, p);
+  return launch_chained(attend_join_kernel<T, 1>, (p.tasks + 7) / 8, 256, 0, stream, p);
 }
 
 // A score in powers of two from a dot product.

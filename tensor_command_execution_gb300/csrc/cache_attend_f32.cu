@@ -53,8 +53,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<DP, GT>::kCtas) attend_f32_
 
   const int quad = DP == 64 ? lane & 15 : lane, half = DP == 64 ? lane >> 4 : 0;  // in the values
 
-  pdl_wait();
-  pdl_trigger();
+  wait_for_previous();
+  let_next_start();
   AttendShare share;
   if (!attend_begin<float>(p, s_rows, Ring::kTile, &share)) return;
   AttendSegment g = attend_first(p, s_rows, share, Ring::kTile);
@@ -209,7 +209,7 @@ template <int DP, int GT>
 cudaError_t launch(const AttendParams& p, cudaStream_t stream) {
   using S = Shape<DP, GT>;
   static_assert(GT * attend_pitch(DP) * 4 <= S::Ring::kStage, "a warp's state fits a stage");
-  static DeviceCache ready;  // (static storage: zero before first use)
+  static PerDevice ready;  // (static storage: zero before first use)
   const cudaError_t e = allow_smem(attend_f32_kernel<DP, GT>, S::kSmem, ready);
   if (e != cudaSuccess) return e;
   return attend_launch<float>(attend_f32_kernel<DP, GT>, p, 2, 152 * S::kCtas, kWarps * 32, S::kSmem, S::Ring::kTile, stream);

@@ -89,8 +89,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<T, DP, NT>::kCtas) attend_m
   const uint32_t value_at = ((lane >> 4) * 8 + (lane & 7)) * S::kPitch + ((lane >> 3) & 1) * 16 + Ring::kKeys;
   const int gr = lane >> 2, tc = (lane & 3) * 2;
 
-  pdl_wait();
-  pdl_trigger();
+  wait_for_previous();
+  let_next_start();
   AttendShare share;
   if (!attend_begin<T>(p, s_rows, Ring::kTile, &share)) return;
   AttendSegment g = attend_first(p, s_rows, share, Ring::kTile);
@@ -241,7 +241,7 @@ template <class T, int DP, int NT>
 cudaError_t launch(const AttendParams& p, cudaStream_t stream) {
   using S = Shape<T, DP, NT>;
   static_assert(NT * 8 * attend_pitch(DP) * 4 <= S::Ring::kStage, "a warp's state fits a stage");
-  static DeviceCache ready;  // (static storage: zero before first use)
+  static PerDevice ready;  // (static storage: zero before first use)
   const cudaError_t e = allow_smem(attend_mma_kernel<T, DP, NT>, S::kSmem, ready);
   if (e != cudaSuccess) return e;
   // The beginning of a row as two tiles of 64 tokens. Measured on 64 rows of 0

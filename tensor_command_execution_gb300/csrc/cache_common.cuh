@@ -1,13 +1,57 @@
 // cache_common.cuh - device helpers of the cache operators' kernels.
 #pragma once
 
+#include <atomic>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "cache_internal.h"
-#include "exec_launch.cuh"
 
 namespace cmdx {
+
+// ---- launches ------------------------------------------------------------------
+// As the executors' launches, these may begin while the previous kernel on
+// their stream still runs (programmatic dependent launch): each CTA waits for
+// it before its first access to memory, and lets the next launch start.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <class K, class... P>
+inline cudaError_t launch_chained(K kernel, int grid, int block, size_t smem, cudaStream_t stream, const P&... params) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, params...);
+}
+
+// Whether something was done once for a device (relaxed atomics: a race only
+// repeats it). Static storage: no, before first use.
+struct PerDevice {
+  static constexpr int kDevices = 64;
+  std::atomic<bool> done[kDevices];
+};
+
+// Lets a kernel use smem bytes of dynamic shared memory, once per device.
+template <class K>
+inline cudaError_t allow_smem(K kernel, int smem, PerDevice& ready) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const bool listed = dev >= 0 && dev < PerDevice::kDevices;
+  if (listed && ready.done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && listed) ready.done[dev].store(true, std::memory_order_relaxed);
+  return e;
+}
+
+// ---- numbers ---------------------------------------------------------------------
 
 __device__ __forceinline__ uint32_t fast_div32(const FastDiv32& f, uint32_t n) {
   if (f.l == 0) return n;

@@ -227,8 +227,8 @@ __device__ __forceinline__ void select_plan_few(const SelectParams& p) {
   const Team<CTAS> team;
   const Team<1> cta;
   const int i = threadIdx.x;
-  pdl_wait();
-  pdl_trigger();
+  wait_for_previous();
+  let_next_start();
   Plan r = {};
   if (i < p.new_rows) r = plan_row(p, i);
   for (int k = team.me; k < p.pages; k += Team<CTAS>::kThreads) p.refs_out[k] = p.refs[k];
@@ -262,8 +262,8 @@ __device__ __forceinline__ void select_plan_many(const SelectParams& p) {
   using All = Team<CTAS>;
   const All team;
   const int me = team.me;
-  pdl_wait();
-  pdl_trigger();
+  wait_for_previous();
+  let_next_start();
   for (int i = me; i < p.pages; i += All::kThreads) p.refs_out[i] = p.refs[i];
   for (int i = me; i < p.old_rows; i += All::kThreads) {
     p.first[i] = kNobody;
@@ -335,8 +335,8 @@ constexpr int kMoveThreads = 256;
 
 template <class U, class L>
 __global__ void __launch_bounds__(kMoveThreads) select_apply_kernel(const __grid_constant__ SelectParams p, const __grid_constant__ L pools) {
-  pdl_wait();
-  pdl_trigger();
+  wait_for_previous();
+  let_next_start();
   const int lane = threadIdx.x & 31, warps = gridDim.x * (kMoveThreads / 32);
   for (int i = blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5); i < p.new_rows; i += warps) {
     const int base = p.base[i], keep = p.keep[i], parent = p.parents[i];
@@ -366,8 +366,8 @@ template <int CTAS>
 __device__ __forceinline__ void compact_plan(const CompactParams& p) {
   const Team<CTAS> team;
   const int me = team.me;
-  pdl_wait();
-  pdl_trigger();
+  wait_for_previous();
+  let_next_start();
   int n;
   const auto is_used = [&](int i) { return p.refs[i] > 0; };
   const Ranks<CTAS> ranks(team, p.pages, is_used, &n);
@@ -399,8 +399,8 @@ __device__ __forceinline__ void compact_plan(const CompactParams& p) {
 
 template <class U, class L>
 __global__ void __launch_bounds__(kMoveThreads) compact_apply_kernel(const __grid_constant__ CompactParams p, const __grid_constant__ L pools) {
-  pdl_wait();
-  pdl_trigger();
+  wait_for_previous();
+  let_next_start();
   const int lane = threadIdx.x & 31, warps = gridDim.x * (kMoveThreads / 32);
   for (int i = blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5); i < p.rows; i += warps) {
     int64_t n = p.lengths[i];
@@ -447,7 +447,7 @@ constexpr int kLargePool = 4096, kManyRows = 256;
 
 template <class P, class L>
 cudaError_t run(void (*plan)(P), int ctas, void (*apply)(P, L), const P& p, const PoolList& pools, cudaStream_t stream) {
-  cudaError_t e = launch_pdl(plan, ctas, kTeamThreads, 0, stream, p);
+  cudaError_t e = launch_chained(plan, ctas, kTeamThreads, 0, stream, p);
   if (e != cudaSuccess) return e;
   L l;
   constexpr int most = sizeof l.ptr / sizeof l.ptr[0];
@@ -458,7 +458,7 @@ cudaError_t run(void (*plan)(P), int ctas, void (*apply)(P, L), const P& p, cons
   }
   l.n = pools.n;
   l.unit = pools.unit;
-  return launch_pdl(apply, 152 * 8, kMoveThreads, 0, stream, p, l);
+  return launch_chained(apply, 152 * 8, kMoveThreads, 0, stream, p, l);
 }
 
 // calls f with a value of the pools' access type, and an empty list that holds them

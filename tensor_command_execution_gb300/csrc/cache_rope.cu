@@ -196,8 +196,8 @@ __global__ void __launch_bounds__(512, 2) rope_kernel(const __grid_constant__ Ro
 #pragma unroll
   for (int i = 0; i < 2; ++i) count[i] = max(0, min(VE, p.dim - e[i]));
 
-  pdl_wait();
-  pdl_trigger();
+  wait_for_previous();
+  let_next_start();
 
   const int64_t first = (int64_t)blockIdx.x * shape.tokens;
   const int64_t all = p.batch * p.tokens;
@@ -321,7 +321,7 @@ cudaError_t launch(const RopeParams& p, cudaStream_t stream) {
   s.by_units = fast_div_by(s.units);
   s.by_slots = fast_div_by(s.slots);
   s.by_pairs = fast_div_by(p.n_pairs);
-  return launch_pdl(rope_kernel<T, VE, VEC, HALF>, (int)((all + s.tokens - 1) / s.tokens), threads,
+  return launch_chained(rope_kernel<T, VE, VEC, HALF>, (int)((all + s.tokens - 1) / s.tokens), threads,
                     (size_t)s.tokens * p.n_pairs * sizeof(float2), stream, p, s);
 }
 
