@@ -47,8 +47,9 @@ CU_SOURCES = [("exec_tile2d.cu", _objs((2,), (0, 1))), ("exec_generic.cu", _objs
               ("exec_tile2d.cu", _objs((1, 0), (0, 1))),
               ("exec_generic.cu", _objs((4, 3, 1, 0))), ("exec_contig.cu", _objs((4, 3, 1, 0))),
               ("static_scratch.cu", [{}]),
-              ("cache_attend.cu", [{}]), ("cache_attend_mma.cu", [{}]),
-              ("cache_attend_f32.cu", [{}]), ("cache_rope.cu", [{}]), ("cache_pages.cu", [{}])]
+              ("cache_attend.cu", [{}]),
+              ("cache_attend_mma.cu", [dict(CMDX_COPY=16), dict(CMDX_COPY=4)]),
+              ("cache_attend_f32.cu", [dict(CMDX_COPY=16), dict(CMDX_COPY=4)]), ("cache_rope.cu", [{}]), ("cache_pages.cu", [{}])]
 CPP_SOURCES = ["cmd_api.cpp", "cmd_yaml.cpp", "exec_host.cpp", "cache_api.cpp"]
 TORCH_SOURCE = "cache_torch.cpp"
 HEADERS = ["cmd_internal.h", "exec_common.cuh", "exec_pipe.cuh", "exec_tile2d.h", "interp_asm.cuh",

@@ -570,13 +570,13 @@ extern "C" cmd_status cmd_attention_decode(const cmd_attention_args* args, void*
     p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kSplitBytes);
     p.status = a.status;
     const int es = elem_size(a.q.dtype);
-    const bool vectors = dim > 0 && dim * es % 16 == 0 && vector_rows(a.k_cache, 16) && vector_rows(a.v_cache, 16);
-    const int most = vectors && es == 2 ? cmdx::kAttendMmaHeads : cmdx::kAttendHeads;
+    // bytes of a copy that suit every row of the cache: 16, 4, or fewer
+    const auto pieces = [&](int n) { return dim * es % n == 0 && vector_rows(a.k_cache, n) && vector_rows(a.v_cache, n); };
+    const int copy = pieces(16) ? 16 : pieces(4) ? 4 : 0;
+    const int most = copy && es == 2 ? cmdx::kAttendMmaHeads : cmdx::kAttendHeads;
     p.blocks = (p.group + most - 1) / most;
     p.block_heads = (p.group + p.blocks - 1) / p.blocks;
     p.q_pairs = vector_rows(a.q, 4);
-    const int few = (dim <= 64 ? 2 : 4) * es;
-    p.vec = vector_rows(a.k_cache, few) && vector_rows(a.v_cache, few);
     // a launch's units (tiles of rows that fill their tables, for each head) stay below 2^31
     const int64_t row_units = (int64_t)p.kv_heads * p.blocks *
                               (p.columns * a.k_cache.sizes[1] / cmdx::kAttendLeastTile + 2 + cmdx::kAttendMostStart);
@@ -590,9 +590,9 @@ extern "C" cmd_status cmd_attention_decode(const cmd_attention_args* args, void*
       p.tables = static_cast<const int32_t*>(a.tables.ptr) + r * a.tables.strides[0];
       p.lengths = static_cast<const int32_t*>(a.lengths.ptr) + r * a.lengths.strides[0];
       const cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
-      const cudaError_t e = !vectors  ? cmdx::attend_simt_launch(a.q.dtype, p, stream)
-                            : es == 2 ? cmdx::attend_mma_launch(a.q.dtype, p, stream)
-                                      : cmdx::attend_f32_launch(p, stream);
+      const cudaError_t e = !copy       ? cmdx::attend_simt_launch(a.q.dtype, p, stream)
+                            : es == 4   ? (copy == 16 ? cmdx::attend_f32_launch16 : cmdx::attend_f32_launch4)(p, stream)
+                                        : (copy == 16 ? cmdx::attend_mma_launch16 : cmdx::attend_mma_launch4)(a.q.dtype, p, stream);
       if (e != cudaSuccess) return launched(e);
     }
     return CMD_OK;

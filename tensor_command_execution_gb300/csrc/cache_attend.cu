@@ -1,6 +1,7 @@
 // cache_attend.cu - attention of one new token per sequence over a paged
-// cache of any alignment, strides and head dim: what cache_attend_mma.cu and
-// cache_attend_f32.cu, which copy rows in 16-byte pieces, cannot take.
+// cache of 16-bit numbers whose rows are not whole 4-byte words (an odd head
+// dim, base or stride): what cache_attend_mma.cu, which copies rows in pieces,
+// cannot take.
 //
 // out = sum_t exp(s_t - lse) v_t, s_t = scale q . k_t, one pass over the
 // tokens with a running maximum. A warp takes kStep tokens at a time, a lane
@@ -9,7 +10,7 @@
 // butterfly that leaves each lane one finished score (31 shuffles for 32
 // scores rather than 5 each), where scaling, the cap, the mask and the
 // exponential are then done once. Bound by the latency of its loads, element
-// by element or (where rows allow it) 2 or 4 at a time.
+// by element.
 #include "cache_attend.cuh"
 
 namespace cmdx {
@@ -20,27 +21,13 @@ constexpr int kWarps = 8;
 constexpr int kTokens = 16;  // of a warp's tile
 constexpr int kRowsBytes = (sizeof(AttendRows) + 15) / 16 * 16;
 
-// VEC elements of a row for this lane (element 4 lane + 128 j + i for VEC 4
-// and 8, 2 lane + i for VEC 2), zero past dim.
+// VEC elements of a row for this lane (element 32 i + lane), zero past dim.
 template <class T, int VEC>
-__device__ __forceinline__ int lane_element(int lane, int i) {
-  return VEC == 2 ? 2 * lane + i : (i / 4) * 128 + 4 * lane + i % 4;
-}
-template <class T, int VEC>
-__device__ __forceinline__ void load_row(float (&x)[VEC], const T* row, int lane, int dim, bool vec) {
-  constexpr int W = VEC == 2 ? 2 : 4;
+__device__ __forceinline__ void load_row(float (&x)[VEC], const T* row, int lane, int dim) {
 #pragma unroll
-  for (int i = 0; i < VEC; i += W) {
-    const int e = lane_element<T, VEC>(lane, i);
-    if (vec && e + W <= dim) {
-      struct alignas(W * sizeof(T)) Pack { T v[W]; };
-      const Pack t = *reinterpret_cast<const Pack*>(row + e);
-#pragma unroll
-      for (int j = 0; j < W; ++j) x[i + j] = to_float(t.v[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < W; ++j) x[i + j] = e + j < dim ? to_float(row[e + j]) : 0.0f;
-    }
+  for (int i = 0; i < VEC; ++i) {
+    const int e = 32 * i + lane;
+    x[i] = e < dim ? to_float(row[e]) : 0.0f;
   }
 }
 
@@ -70,7 +57,7 @@ __global__ void __launch_bounds__(kWarps * 32) attend_simt_kernel(const __grid_c
       for (int i = 0; i < VEC; ++i) q[h][i] = o[h][i] = 0.0f;
       if (h < heads.heads) {
         const T* row = static_cast<const T*>(p.q) + g.row * p.q_st[0] + (heads.head0 + h) * p.q_st[1];
-        load_row<T, VEC>(q[h], row, lane, p.dim, false);
+        load_row<T, VEC>(q[h], row, lane, p.dim);
       }
     }
     // this lane's score is that of token lane / kDup / GT and head lane / kDup % GT of a step
@@ -97,8 +84,8 @@ __global__ void __launch_bounds__(kWarps * 32) attend_simt_kernel(const __grid_c
           }
           if (seen[j]) {
             const int64_t in_page = token - (int64_t)column * p.page.d;
-            load_row<T, VEC>(k[j], kp + page * p.k_st[0] + in_page * p.k_st[1] + heads.kv * p.k_st[2], lane, p.dim, p.vec);
-            load_row<T, VEC>(v[j], vp + page * p.v_st[0] + in_page * p.v_st[1] + heads.kv * p.v_st[2], lane, p.dim, p.vec);
+            load_row<T, VEC>(k[j], kp + page * p.k_st[0] + in_page * p.k_st[1] + heads.kv * p.k_st[2], lane, p.dim);
+            load_row<T, VEC>(v[j], vp + page * p.v_st[0] + in_page * p.v_st[1] + heads.kv * p.v_st[2], lane, p.dim);
           } else {
 #pragma unroll
             for (int e = 0; e < VEC; ++e) k[j][e] = v[j][e] = 0.0f;
@@ -173,7 +160,7 @@ __global__ void __launch_bounds__(kWarps * 32) attend_simt_kernel(const __grid_c
         s_state[warp][h][kPitch - 3] = l;
       }
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) s_state[warp][h][lane_element<T, VEC>(lane, e)] = o[h][e];
+      for (int e = 0; e < VEC; ++e) s_state[warp][h][32 * e + lane] = o[h][e];
     }
     attend_finish<T, kWarps>(p, share, g, heads, &s_state[0][0][0], GT * kPitch, kPitch);
   }
@@ -203,7 +190,6 @@ cudaError_t launch_type(const AttendParams& p, cudaStream_t stream) {
 
 cudaError_t attend_simt_launch(int dtype, const AttendParams& p, cudaStream_t stream) {
   switch (dtype) {
-    case CMD_F32: return launch_type<float>(p, stream);
     case CMD_F16: return launch_type<__half>(p, stream);
     case CMD_BF16: return launch_type<__nv_bfloat16>(p, stream);
   }

@@ -1,5 +1,5 @@
 // cache_attend_f32.cu - attention of one new token per sequence over a paged
-// cache of 32-bit numbers whose rows are whole 16-byte vectors.
+// cache of 32-bit numbers.
 //
 // Products and sums stay in binary32 (the tensor units' 32-bit type holds 11
 // bits of a factor). Bound by memory for few query heads to a kv head. Each
@@ -12,6 +12,10 @@
 // shared memory. Rows lie 32 bytes past a multiple of 128 apart: the lanes of
 // 4 tokens and 2 neighbouring pieces meet in no bank.
 #include "cache_attend_ring.cuh"
+
+#ifndef CMDX_COPY
+#error "cache_attend_f32.cu is compiled for each copy size, with -DCMDX_COPY=<16|4>"
+#endif
 
 namespace cmdx {
 
@@ -27,7 +31,7 @@ struct Shape {
   static constexpr int kStages = DP == 64 ? 3 : 2;
   static constexpr int kCtas = DP == 256 ? 1 : DP == 64 || GT < 8 ? 3 : 2;
   static constexpr int kPitch = DP * 4 + 32;  // bytes of a row
-  using Ring = AttendRing<float, kTokens, DP / 4, kPitch, kStages, kWarps>;
+  using Ring = AttendRing<float, DP, CMDX_COPY, kTokens, kPitch, kStages, kWarps>;
   static constexpr int kQueries = GT * DP * 4;              // bytes of a block's queries
   static constexpr int kWeights = kWarps * kTokens * GT * 4;  // and of the warps' weights
   static constexpr int kSmem = kWarps * Ring::kBytes + kQueries + kWeights + (int)sizeof(AttendRows);
@@ -223,7 +227,7 @@ cudaError_t launch_dim(const AttendParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t attend_f32_launch(const AttendParams& p, cudaStream_t stream) {
+cudaError_t CMDX_COPY_NAME(attend_f32_launch)(const AttendParams& p, cudaStream_t stream) {
   if (p.dim <= 64) return launch_dim<64>(p, stream);
   return p.dim <= 128 ? launch_dim<128>(p, stream) : launch_dim<256>(p, stream);
 }

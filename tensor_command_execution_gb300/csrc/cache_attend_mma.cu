@@ -20,6 +20,10 @@
 // are copied, whatever their slots hold.
 #include "cache_attend_ring.cuh"
 
+#ifndef CMDX_COPY
+#error "cache_attend_mma.cu is compiled for each copy size, with -DCMDX_COPY=<16|4>"
+#endif
+
 namespace cmdx {
 
 namespace {
@@ -71,7 +75,7 @@ struct Shape {
   static constexpr int kStages = 2;
   static constexpr int kCtas = DP == 256 ? 1 : NT == 2 ? 2 : DP == 64 ? 4 : 3;
   static constexpr int kPitch = DP * 2 + 16;                   // bytes of a row: an odd number of 16
-  using Ring = AttendRing<T, kTokens, DP / 8, kPitch, kStages, kWarps>;
+  using Ring = AttendRing<T, DP, CMDX_COPY, kTokens, kPitch, kStages, kWarps>;
   static constexpr int kSmem = kWarps * Ring::kBytes + (int)sizeof(AttendRows);
 };
 
@@ -261,7 +265,7 @@ cudaError_t launch_type(const AttendParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t attend_mma_launch(int dtype, const AttendParams& p, cudaStream_t stream) {
+cudaError_t CMDX_COPY_NAME(attend_mma_launch)(int dtype, const AttendParams& p, cudaStream_t stream) {
   return dtype == CMD_F16 ? launch_type<__half>(p, stream) : launch_type<__nv_bfloat16>(p, stream);
 }
 

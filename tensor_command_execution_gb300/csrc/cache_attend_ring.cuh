@@ -1,8 +1,9 @@
 // cache_attend_ring.cuh - how a warp of the attention kernels streams its tiles
 // of keys and values from the cache's pages into shared memory.
 //
-// Each warp has a ring of stages of its own, filled by asynchronous 16-byte
-// copies, and waits for no other warp. The copies run ahead of the arithmetic
+// Each warp has a ring of stages of its own, filled by asynchronous copies (of
+// 16 bytes, or of 4 where the rows are no whole 16-byte vectors), and waits
+// for no other warp. The copies run ahead of the arithmetic
 // across the ends of rows, and the table entry of a tile is read one tile
 // before its copies need it. Tokens outside the row, and elements past the head
 // dim, are filled with zeros, whatever their slots hold.
@@ -14,9 +15,13 @@ namespace cmdx {
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
-// 16 bytes to shared memory, or 16 zero bytes where !take
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool take) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+// N bytes to shared memory, or as many zeros where !take
+template <int N>
+__device__ __forceinline__ void copy_bytes(uint32_t dst, const void* src, bool take) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(take ? 4 : 0) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -31,10 +36,12 @@ __device__ __forceinline__ float power_of_two(float x) {
   return y;
 }
 
-// TOKENS tokens to a tile, CHUNKS 16-byte pieces to a row (in PITCH bytes),
-// STAGES stages, WARPS warps to a CTA; the elements are of type T.
-template <class T, int TOKENS, int CHUNKS, int PITCH, int STAGES, int WARPS>
+// Tiles of TOKENS rows of up to DP elements of type T, PITCH bytes apart,
+// copied COPY bytes at a time; STAGES stages, WARPS warps to a CTA.
+template <class T, int DP, int COPY, int TOKENS, int PITCH, int STAGES, int WARPS>
 struct AttendRing {
+  static constexpr int CHUNKS = DP * (int)sizeof(T) / COPY;
+  static constexpr int kEach = COPY / (int)sizeof(T);             // elements of a copy
   static constexpr int kKeys = TOKENS * PITCH;  // bytes of a stage's keys; the values follow
   static constexpr int kStage = 2 * kKeys;
   static constexpr int kBytes = STAGES * kStage;
@@ -63,7 +70,7 @@ struct AttendRing {
   __device__ __forceinline__ AttendRing(const AttendParams& p_, const AttendRows& r, const AttendShare& s,
                                         const AttendSegment& first, const void* ring)
       : p(p_), rows(r), share(s), lane(threadIdx.x & 31), warp(threadIdx.x >> 5), at(smem_addr(ring)),
-        copy_row(lane / CHUNKS), chunk(lane % CHUNKS), chunks(p_.dim * (int)sizeof(T) / 16),
+        copy_row(lane / CHUNKS), chunk(lane % CHUNKS), chunks(p_.dim / kEach),
         one_page(p_.page.d % TOKENS == 0), look(first) {
     look_up();
 #pragma unroll
@@ -81,8 +88,8 @@ struct AttendRing {
       if (look.tiles == 0) return;
       table = p.tables + look.row * p.table_st[0];
       const int head = look.group / p.blocks;
-      k = static_cast<const T*>(p.k) + chunk * (16 / (int)sizeof(T)) + head * p.k_st[2];
-      v = static_cast<const T*>(p.v) + chunk * (16 / (int)sizeof(T)) + head * p.v_st[2];
+      k = static_cast<const T*>(p.k) + chunk * kEach + head * p.k_st[2];
+      v = static_cast<const T*>(p.v) + chunk * kEach + head * p.v_st[2];
     }
     const int token = (look.tile0 + look_at) * kTile + warp * TOKENS + lane % TOKENS;
     const uint32_t column = fast_div32(p.page, (uint32_t)token);
@@ -101,7 +108,7 @@ struct AttendRing {
   __device__ __forceinline__ uint32_t copy(int into) {
     const uint32_t has = __ballot_sync(~0u, page >= 0) & ((1u << TOKENS) - 1u);
     if (has) {
-      const uint32_t dst = at + into * kStage + copy_row * PITCH + chunk * 16;
+      const uint32_t dst = at + into * kStage + copy_row * PITCH + chunk * COPY;
       const int64_t one = __shfl_sync(~0u, page, __ffs(has) - 1);
       const int64_t first = __shfl_sync(~0u, slot, 0) + copy_row;
       const T* k0 = k + one * p.k_st[0] + first * p.k_st[1];
@@ -118,9 +125,9 @@ struct AttendRing {
 #pragma unroll
         for (int c = 0; c < kPieces; ++c) {
           const bool take = in && chunk + 32 * c < chunks;
-          const int e = 32 * c * (16 / (int)sizeof(T));
-          copy16(dst + r * PITCH + 512 * c, take ? static_cast<const void*>(ks + e) : p.k, take);
-          copy16(dst + r * PITCH + 512 * c + kKeys, take ? static_cast<const void*>(vs + e) : p.v, take);
+          const int e = 32 * c * kEach, to = r * PITCH + 32 * c * COPY;
+          copy_bytes<COPY>(dst + to, take ? static_cast<const void*>(ks + e) : p.k, take);
+          copy_bytes<COPY>(dst + to + kKeys, take ? static_cast<const void*>(vs + e) : p.v, take);
         }
       }
     }

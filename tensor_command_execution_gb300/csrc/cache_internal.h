@@ -102,15 +102,20 @@ struct AttendParams {
   uint8_t split_by_row;
   int32_t* status;
   uint8_t q_pairs;     // q rows may be read two 16-bit elements at a time
-  uint8_t vec;         // cache rows may be read in vectors (of 2 or 4 elements)
 };
 
-// any types, alignment and strides; at most 8 query heads of a block
+// 16-bit types whose cache rows are not whole 4-byte words; at most 8 query
+// heads of a block
 cudaError_t attend_simt_launch(int dtype, const AttendParams& p, cudaStream_t stream);
-// types whose cache rows are whole 16-byte vectors: 32-bit, at most 8 query
-// heads of a block; 16-bit, at most 16
-cudaError_t attend_f32_launch(const AttendParams& p, cudaStream_t stream);
-cudaError_t attend_mma_launch(int dtype, const AttendParams& p, cudaStream_t stream);
+// the others, with rows of whole 16-byte or 4-byte pieces: 32-bit, at most 8
+// query heads of a block; 16-bit, at most 16
+#define CMDX_COPY_NAME_(f, n) f##n
+#define CMDX_COPY_NAME__(f, n) CMDX_COPY_NAME_(f, n)
+#define CMDX_COPY_NAME(f) CMDX_COPY_NAME__(f, CMDX_COPY)
+cudaError_t attend_f32_launch16(const AttendParams& p, cudaStream_t stream);
+cudaError_t attend_f32_launch4(const AttendParams& p, cudaStream_t stream);
+cudaError_t attend_mma_launch16(int dtype, const AttendParams& p, cudaStream_t stream);
+cudaError_t attend_mma_launch4(int dtype, const AttendParams& p, cudaStream_t stream);
 constexpr int kAttendHeads = 8, kAttendMmaHeads = 16;
 
 // ---- pages (cache_pages.cu) -----------------------------------------------------
