@@ -570,7 +570,8 @@ extern "C" cmd_status cmd_attention_decode(const cmd_attention_args* args, void*
     p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kSplitBytes);
     p.status = a.status;
     const int es = elem_size(a.q.dtype);
-    // bytes of a copy that suit every row of the cache: 16, 4, or fewer
+    // bytes of a copy that suit every row of the cache: 16, 4, or fewer. (On rows that suit both, 64 of 4096 tokens, 8 kv
+    // heads of 128: bf16 180 us with 16, 217 with 4; 24 f32 ones of 2999 tokens and 16 kv heads 180 and 226.)
     const auto pieces = [&](int n) { return dim * es % n == 0 && vector_rows(a.k_cache, n) && vector_rows(a.v_cache, n); };
     const int copy = pieces(16) ? 16 : pieces(4) ? 4 : 0;
     const int most = copy && es == 2 ? cmdx::kAttendMmaHeads : cmdx::kAttendHeads;

@@ -354,6 +354,9 @@ __global__ void __launch_bounds__(WARPS == 1 ? 256 : WARPS * 32) attend_join_ker
 // Launches a kernel of `ctas` CTAs of `threads` threads that splits its work
 // as above in tiles of `tile` tokens, and the join. The joining warps: 16 to a
 // head where few rows can have many parts each, one where each has few.
+// Measured, one against 16, whole calls: one row of 393217 tokens and one kv
+// head (456 parts) 116 and 47.7 us; one of 32768 and 8 kv heads 39.3 and 30.2;
+// four of those 93.5 and 94.5; 64 rows of 4096 tokens 179 and 227.
 template <class T, class K>
 cudaError_t attend_launch(K kernel, AttendParams p, int start_units, int ctas, int threads, int smem, int tile,
                           cudaStream_t stream) {

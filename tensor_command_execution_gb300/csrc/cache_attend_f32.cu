@@ -11,6 +11,12 @@
 // 64: the half-warps take every other token), the weights being read back from
 // shared memory. Rows lie 32 bytes past a multiple of 128 apart: the lanes of
 // 4 tokens and 2 neighbouring pieces meet in no bank.
+//
+// Measured: 24 rows of 2999 tokens, 16 kv heads of 128, one query head each
+// 177 us, 6.65 TB/s, 98% of the copy peak; 8 query heads to each of 2 kv heads,
+// 96 rows, 118 us, 74%, bound by the multiply-adds and the reads of queries; 24
+// rows of 1 to 1100 tokens (16 heads of 80, capped, windowed) 20.2 us, 49%,
+// 8 of it the fixed part of two launches.
 #include "cache_attend_ring.cuh"
 
 #ifndef CMDX_COPY
@@ -216,6 +222,9 @@ cudaError_t launch(const AttendParams& p, cudaStream_t stream) {
   static PerDevice ready;  // (static storage: zero before first use)
   const cudaError_t e = allow_smem(attend_f32_kernel<DP, GT>, S::kSmem, ready);
   if (e != cudaSuccess) return e;
+  // (a row's beginning as two tiles of 32 tokens: 24 short rows of 16 heads took
+  // 28.2 us counted as 0, 20.7 as 1, 21.2 as 2; 64 longer ones of 4 heads with 4
+  // query heads each 64.5, 48.4 and 42.2)
   return attend_launch<float>(attend_f32_kernel<DP, GT>, p, 2, 152 * S::kCtas, kWarps * 32, S::kSmem, S::Ring::kTile, stream);
 }
 
