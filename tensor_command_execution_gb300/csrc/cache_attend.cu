@@ -173,7 +173,8 @@ cudaError_t launch(const AttendParams& p, cudaStream_t stream) {
   static PerDevice ready;  // (static storage: zero before first use)
   const cudaError_t e = allow_smem(attend_simt_kernel<T, GT, VEC>, smem, ready);
   if (e != cudaSuccess) return e;
-  return attend_launch<T>(attend_simt_kernel<T, GT, VEC>, p, 0, 2 * 152, kWarps * 32, smem, kTokens * kWarps, stream);
+  return attend_launch<T>(attend_simt_kernel<T, GT, VEC>, p, 0, 2 * 152, kWarps * 32, smem, kTokens * kWarps, stream,
+                          false);
 }
 
 template <class T, int GT>

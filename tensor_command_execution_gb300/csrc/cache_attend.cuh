@@ -14,8 +14,17 @@
 // CTA's segments are parts (its first and its last), so the workspace does not
 // grow with the rows, and at most one row that is split begins in a CTA, so
 // neither does the list of them.
+//
+// A few short rows are not worth that: there a cluster of CTAs (a team) takes
+// each row and group and joins its parts through distributed shared memory,
+// in the same launch and without the workspace.
+//
+// A few short rows are not worth that: there a cluster of CTAs (a team) takes
+// each row and group and joins its parts through distributed shared memory,
+// in the same launch and with no workspace.
 #pragma once
 
+#include <cooperative_groups.h>
 #include <math_constants.h>
 
 #include "cache_common.cuh"
@@ -32,6 +41,14 @@ struct AttendRows {
   }
 };
 
+// Row r's length, held to its table.
+__device__ __forceinline__ int attend_length(const AttendParams& p, int r) {
+  const int n = p.lengths[r * p.len_st], most = p.columns * (int)p.page.d;
+  if (n >= 0 && n <= most) return n;
+  report(p.status, CMD_CACHE_BAD_INDEX);
+  return n < 0 ? 0 : most;
+}
+
 // Fills s for tiles of `tile` tokens (aligned to the row's start); all
 // threads of the CTA call it. (The host sees to it that the units of a launch,
 // of all heads, are below 2^31.)
@@ -40,15 +57,9 @@ __device__ __forceinline__ void attend_rows(const AttendParams& p, AttendRows& s
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int run = (p.rows + blockDim.x - 1) / blockDim.x;
   const int r0 = min(tid * run, p.rows), r1 = min(r0 + run, p.rows);
-  const int most = p.columns * (int)p.page.d;
   int sum = 0;
   for (int r = r0; r < r1; ++r) {
-    int n = p.lengths[r * p.len_st];
-    if (n < 0 || n > most) {
-      if (blockIdx.x == 0) report(p.status, CMD_CACHE_BAD_INDEX);
-      n = n < 0 ? 0 : most;
-    }
-    s.n[r] = n;
+    const int n = s.n[r] = attend_length(p, r);
     s.at[r + 1] = n > 0 ? (n + tile - 1) / tile - s.lo(p, r) / tile + p.start_units : 0;
     sum += s.at[r + 1];
   }
@@ -199,6 +210,26 @@ __device__ __forceinline__ AttendHeads attend_heads(const AttendParams& p, int g
   return h;
 }
 
+// Elements d .. d + 3 of a head over the warps' states of it, WARPS of them
+// warp_pitch apart; the maximum and sum in *top and *l.
+template <int WARPS>
+__device__ __forceinline__ float4 attend_merged(const float* s, int warp_pitch, int pitch, int d, float* top, float* l) {
+  float m[WARPS];
+  *top = -CUDART_INF_F;
+  *l = 0.0f;
+#pragma unroll
+  for (int t = 0; t < WARPS; ++t) *top = fmaxf(*top, m[t] = s[t * warp_pitch + pitch - 4]);
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int t = 0; t < WARPS; ++t) {
+    const float* x = s + t * warp_pitch;
+    const float c = attend_weight(m[t], *top);
+    *l = fmaf(x[pitch - 3], c, *l);
+    add_scaled(o, *reinterpret_cast<const float4*>(x + d), c);
+  }
+  return o;
+}
+
 // Ends a segment. The warps' states lie in shared memory, query head q of
 // warp w at state + w * warp_pitch + q * pitch (pitch = attend_pitch of
 // something at least dim). All threads call it, once their states are
@@ -219,18 +250,8 @@ __device__ __forceinline__ void attend_finish(const AttendParams& p, const Atten
   __syncthreads();  // the warps' states are complete
   for (int i = threadIdx.x; i < h.heads * quads; i += WARPS * 32) {
     const int q = i / quads, d = 4 * (i - q * quads);
-    const float* s = state + q * pitch;
-    float m[WARPS], top = -CUDART_INF_F, l = 0.0f;
-#pragma unroll
-    for (int t = 0; t < WARPS; ++t) top = fmaxf(top, m[t] = s[t * warp_pitch + pitch - 4]);
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-    for (int t = 0; t < WARPS; ++t) {
-      const float* x = s + t * warp_pitch;
-      const float c = attend_weight(m[t], top);
-      l = fmaf(x[pitch - 3], c, l);
-      add_scaled(o, *reinterpret_cast<const float4*>(x + d), c);
-    }
+    float top, l;
+    const float4 o = attend_merged<WARPS>(state + q * pitch, warp_pitch, pitch, d, &top, &l);
     if (part) {
       float* x = part + q * part_pitch;
       if (d == 0) {
@@ -265,6 +286,77 @@ __device__ __forceinline__ bool attend_begin(const AttendParams& p, AttendRows& 
   *w = attend_share(p, s);
   if (!p.split_by_row && threadIdx.x == 0) p.splits[blockIdx.x].parts = 0;  // (unless a row is split here, below)
   return w->begin != w->end;
+}
+
+// A team's CTA: its stretch of the team's row and group (no tiles where the row
+// is short), and a share that ends with it.
+__device__ __forceinline__ AttendSegment attend_team(const AttendParams& p, int tile, AttendShare* w) {
+  const int team = blockIdx.x / p.team, rank = blockIdx.x - team * p.team;
+  w->groups = p.kv_heads * p.blocks;
+  w->units = w->ctas = w->begin = w->end = 0;
+  AttendSegment g;
+  g.row = team / w->groups;
+  g.group = team - g.row * w->groups;
+  g.n = attend_length(p, g.row);
+  g.lo = p.window > 0 && g.n > p.window ? g.n - p.window : 0;
+  const int all = g.n > 0 ? (g.n + tile - 1) / tile - g.lo / tile : 0;
+  const int each = all / p.team, more = all - each * p.team;  // the first `more` CTAs take one more
+  g.tile0 = g.lo / tile + rank * each + min(rank, more);
+  g.tiles = each + (rank < more);
+  g.first = 0;
+  g.row_tiles = 0;
+  return g;
+}
+
+// Ends a team's row: the warps' states (as in attend_finish) go to `part` of
+// each CTA, and the CTAs of the team write the result, a run of elements each.
+// Every thread of the team calls it.
+template <class T, int WARPS>
+__device__ __forceinline__ void attend_finish_team(const AttendParams& p, const AttendSegment& g, const AttendHeads& h,
+                                                   const float* state, int warp_pitch, int pitch, float* part) {
+  namespace cg = cooperative_groups;
+  const cg::cluster_group team = cg::this_cluster();
+  const int part_pitch = attend_pitch(p.dim), quads = part_pitch / 4 - 1;
+  __syncthreads();  // the warps' states are complete
+  for (int i = threadIdx.x; i < h.heads * quads; i += WARPS * 32) {
+    const int q = i / quads, d = 4 * (i - q * quads);
+    float top, l;
+    const float4 o = attend_merged<WARPS>(state + q * pitch, warp_pitch, pitch, d, &top, &l);
+    float* x = part + q * part_pitch;
+    if (d == 0) {
+      x[part_pitch - 4] = top;
+      x[part_pitch - 3] = l;
+    }
+    *reinterpret_cast<float4*>(x + d) = o;
+  }
+  team.sync();
+  constexpr int kMost = 8;
+  const int rank = blockIdx.x % p.team;
+  for (int i = rank * WARPS * 32 + threadIdx.x; i < h.heads * quads; i += p.team * WARPS * 32) {
+    const int q = i / quads, d = 4 * (i - q * quads);
+    float m[kMost], pl[kMost], top = -CUDART_INF_F, l = 0.0f;
+    float4 po[kMost], o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < kMost; ++k) {
+      m[k] = -CUDART_INF_F;
+      if (k < p.team) {
+        const float* x = team.map_shared_rank(part, k) + q * part_pitch;
+        m[k] = x[part_pitch - 4];
+        pl[k] = x[part_pitch - 3];
+        po[k] = *reinterpret_cast<const float4*>(x + d);
+      }
+      top = fmaxf(top, m[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kMost; ++k)
+      if (k < p.team) {
+        const float c = attend_weight(m[k], top);
+        l = fmaf(pl[k], c, l);
+        add_scaled(o, po[k], c);
+      }
+    attend_write<T>(p, g.row, h.head0 + q, d, top, l, o);
+  }
+  team.sync();  // nobody leaves while its part is read
 }
 
 // Joins the parts of query head q of a split row: WARPS warps take every
@@ -351,16 +443,39 @@ __global__ void __launch_bounds__(WARPS == 1 ? 256 : WARPS * 32) attend_join_ker
   if (task < p.tasks) attend_join<T, WARPS>(p, task, s_state);
 }
 
+// CTAs of the teams of a launch of tiles of `tile` tokens, 0 for none: up to 8
+// for each row and group, where a CTA has four tiles at most and the teams
+// leave a third of the device's places (`ctas`) free. Measured against units
+// dealt out evenly, bf16, 8 kv heads of 128, 64 tokens to a tile: one row of 64
+// tokens 4.3 and 5.1 us, 700 6.6 and 8.3, 2000 (4 tiles) 8.4 and 9.3, 4000 (8
+// tiles) 12.3 and 10.8; 4 rows of 1000 (256 CTAs of 456) 8.8 and 11.9, 14 of
+// 250 (448) 10.8 and 10.5, 7 of 2000 (448) 22.1 and 18.1; dim 256, 2 rows of
+// 900 (128 of 152) 16.5 and 14.4.
+constexpr int kTeamTiles = 4;
+
+inline int attend_team_size(const AttendParams& p, int ctas, int tile) {
+  int64_t most = (int64_t)p.columns * p.page.d;
+  if (p.window > 0) most = most < p.window ? most : p.window;
+  const int64_t tiles = (most + tile - 1) / tile + (p.window > 0);  // (a window may begin inside a tile)
+  int team = 1;
+  while (team < 8 && team < tiles) team *= 2;
+  return tiles <= team * kTeamTiles && (int64_t)p.rows * p.kv_heads * p.blocks * team * 3 <= ctas * 2 ? team : 0;
+}
+
 // Launches a kernel of `ctas` CTAs of `threads` threads that splits its work
-// as above in tiles of `tile` tokens, and the join. The joining warps: 16 to a
+// as above in tiles of `tile` tokens (teams: it can also work in teams), and
+// the join. The joining warps: 16 to a
 // head where few rows can have many parts each, one where each has few.
 // Measured, one against 16, whole calls: one row of 393217 tokens and one kv
 // head (456 parts) 116 and 47.7 us; one of 32768 and 8 kv heads 39.3 and 30.2;
 // four of those 93.5 and 94.5; 64 rows of 4096 tokens 179 and 227.
 template <class T, class K>
 cudaError_t attend_launch(K kernel, AttendParams p, int start_units, int ctas, int threads, int smem, int tile,
-                          cudaStream_t stream) {
+                          cudaStream_t stream, bool teams = true) {
   p.start_units = start_units;
+  p.team = teams ? attend_team_size(p, ctas, tile) : 0;
+  if (p.team)
+    return launch_clusters(kernel, p.team, p.rows * p.kv_heads * p.blocks * p.team, threads, (size_t)smem, stream, p);
   const int64_t rows = (int64_t)p.rows * p.kv_heads * p.blocks;
   p.split_by_row = rows <= ctas;
   const int lists = p.split_by_row ? (int)rows : ctas;

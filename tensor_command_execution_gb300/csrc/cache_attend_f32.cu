@@ -66,10 +66,15 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<DP, GT>::kCtas) attend_f32_
   wait_for_previous();
   let_next_start();
   AttendShare share;
-  if (!attend_begin<float>(p, s_rows, Ring::kTile, &share)) return;
-  AttendSegment g = attend_first(p, s_rows, share, Ring::kTile);
+  AttendSegment g;
+  if (p.team) {
+    g = attend_team(p, Ring::kTile, &share);
+  } else {
+    if (!attend_begin<float>(p, s_rows, Ring::kTile, &share)) return;
+    g = attend_first(p, s_rows, share, Ring::kTile);
+  }
   Ring ring(p, s_rows, share, g, s_mem + warp * Ring::kBytes);
-  for (; g.tiles; g = attend_next(p, s_rows, share, g, Ring::kTile)) {
+  for (; p.team || g.tiles; g = attend_next(p, s_rows, share, g, Ring::kTile)) {
     const AttendHeads heads = attend_heads(p, g.group);
     for (int i = threadIdx.x; i < GT * DP; i += kWarps * 32) {
       const int h = i / DP, d = i % DP;
@@ -183,8 +188,9 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<DP, GT>::kCtas) attend_f32_
     }
 
     // the warp's state into the stage read last, which is copied to again only
-    // with the next tile
-    unsigned char* states = s_mem + ring.free_stage() * Ring::kStage;
+    // with the next tile (a team has no next one: its states go to the first
+    // stage, and its CTAs' parts to the second of the first warp)
+    unsigned char* states = s_mem + (p.team ? 0 : ring.free_stage()) * Ring::kStage;
     float* state = reinterpret_cast<float*>(states + warp * Ring::kBytes);
     constexpr int kStatePitch = attend_pitch(DP);
 #pragma unroll
@@ -211,6 +217,11 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<DP, GT>::kCtas) attend_f32_
         }
         if (half == 0) *reinterpret_cast<float4*>(state + h * kStatePitch + (quad + 32 * e) * 4) = x;
       }
+    if (p.team) {
+      attend_finish_team<float, kWarps>(p, g, heads, reinterpret_cast<float*>(states), Ring::kBytes / 4, kStatePitch,
+                                  reinterpret_cast<float*>(s_mem + Ring::kStage));
+      break;
+    }
     attend_finish<float, kWarps>(p, share, g, heads, reinterpret_cast<float*>(states), Ring::kBytes / 4, kStatePitch);
   }
 }

@@ -23,7 +23,7 @@
 // 177 us, 6.08 TB/s, 90% of the copy peak (the launch alone 169; its slowest
 // SM ran 8% longer than the mean); 64 rows of 0 to 8192 tokens 47 us, 75%; two
 // rows of 393217 and 262147 tokens of 2 kv heads (f16) 112.5 us, 88%; one row
-// of 700, 8.4 us, the fixed part of two launches. Tensor units 14% busy, issue
+// of 700, 6.5 us, the latency of one launch. Tensor units 14% busy, issue
 // slots 31%. Rows copied in pieces of 4 bytes: 64 rows of 4096 tokens of dim
 // 100, 263 us, 47%, bound by the number of copies.
 #include "cache_attend_ring.cuh"
@@ -104,10 +104,15 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<T, DP, NT>::kCtas) attend_m
   wait_for_previous();
   let_next_start();
   AttendShare share;
-  if (!attend_begin<T>(p, s_rows, Ring::kTile, &share)) return;
-  AttendSegment g = attend_first(p, s_rows, share, Ring::kTile);
+  AttendSegment g;
+  if (p.team) {
+    g = attend_team(p, Ring::kTile, &share);
+  } else {
+    if (!attend_begin<T>(p, s_rows, Ring::kTile, &share)) return;
+    g = attend_first(p, s_rows, share, Ring::kTile);
+  }
   Ring ring(p, s_rows, share, g, s_mem + warp * Ring::kBytes);
-  for (; g.tiles; g = attend_next(p, s_rows, share, g, Ring::kTile)) {
+  for (; p.team || g.tiles; g = attend_next(p, s_rows, share, g, Ring::kTile)) {
     const AttendHeads heads = attend_heads(p, g.group);
     // the query heads of this block, as the right side of K q^T
     uint32_t q[NT][KS][2];
@@ -219,9 +224,10 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<T, DP, NT>::kCtas) attend_m
     }
 
     // the warp's state into the stage read last, which is copied to again only
-    // with the next tile
+    // with the next tile (a team has no next one: its states go to the first
+    // stage, and its CTAs' parts to the second of the first warp)
     __syncwarp();
-    unsigned char* states = s_mem + ring.free_stage() * Ring::kStage;
+    unsigned char* states = s_mem + (p.team ? 0 : ring.free_stage()) * Ring::kStage;
     float* state = reinterpret_cast<float*>(states + warp * Ring::kBytes);
     constexpr int kStatePitch = attend_pitch(DP);
 #pragma unroll
@@ -244,6 +250,11 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<T, DP, NT>::kCtas) attend_m
           x[16 * k + gr + 8] = o[j][k][2 + e];
         }
       }
+    }
+    if (p.team) {
+      attend_finish_team<T, kWarps>(p, g, heads, reinterpret_cast<float*>(states), Ring::kBytes / 4, kStatePitch,
+                                  reinterpret_cast<float*>(s_mem + Ring::kStage));
+      break;
     }
     attend_finish<T, kWarps>(p, share, g, heads, reinterpret_cast<float*>(states), Ring::kBytes / 4, kStatePitch);
   }

@@ -17,19 +17,28 @@ namespace cmdx {
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// (with cluster > 1: in clusters of that many CTAs)
 template <class K, class... P>
-inline cudaError_t launch_chained(K kernel, int grid, int block, size_t smem, cudaStream_t stream, const P&... params) {
+inline cudaError_t launch_clusters(K kernel, int cluster, int grid, int block, size_t smem, cudaStream_t stream,
+                                   const P&... params) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3((unsigned)block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, params...);
+}
+template <class K, class... P>
+inline cudaError_t launch_chained(K kernel, int grid, int block, size_t smem, cudaStream_t stream, const P&... params) {
+  return launch_clusters(kernel, 1, grid, block, smem, stream, params...);
 }
 
 // Whether something was done once for a device (relaxed atomics: a race only

@@ -99,6 +99,7 @@ struct AttendParams {
   AttendSplit* splits; // one for each CTA, or for each row and group
   int32_t tasks;       // of the join
   int32_t start_units; // what the beginning of a row counts, in tiles
+  int32_t team;        // CTAs of a cluster that takes one row and group; 0: units are dealt out evenly
   uint8_t split_by_row;
   int32_t* status;
   uint8_t q_pairs;     // q rows may be read two 16-bit elements at a time

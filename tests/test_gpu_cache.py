@@ -208,22 +208,33 @@ def test_append_reports_what_it_cannot_store():
 
 def _attend(kind, lengths, hq, hk, dim, page, order="slots", softcap=0.0, window=0, seed=0, junk=math.nan, pad=0, scale=None,
             q=None):
-    c = U.Cache(kind, lengths, hk, dim, page, order, seed=seed, junk=junk, pad=pad)
+    """Both ways of dealing out the work: with tables as long as the rows (few short rows go to teams of CTAs), and with
+    tables that could hold far more tokens."""
     q = 2 * _randn(len(lengths), hq, dim, kind=kind, seed=seed + 1) if q is None else q
-    status = torch.zeros(1, dtype=torch.int32, device="cuda")
-    out, lse = T.attention_decode(q, c.k, c.v, c.tables, c.lengths, softcap=softcap, window=window, scale=scale,
-                                  return_lse=True, status=status)
-    T.cache_status(status)
-    want, want_lse, bound, lse_bound = U.attended(q, c, lengths, dim ** -0.5 if scale is None else scale, softcap, window)
-    # the weights of 16-bit caches are held as two 16-bit numbers: 2^-16 of each (bf16), 2^-21 (f16)
-    split = {"f32": 0.0, "f16": 2.0 ** -21, "bf16": 2.0 ** -16}[kind]
-    top = torch.stack([c.rows(r, n)[1].abs().amax() if n else torch.zeros(()).double() for r, n in enumerate(lengths)])
-    bound = bound + split * top[:, None, None] + U.ROUND[kind] * want.abs() * (1 + 2.0 ** -10) + U.TINY[kind]
-    _near(out, want, bound, "out")
-    empty = torch.isinf(want_lse)
-    assert torch.equal(torch.isinf(lse.cpu()) & (lse.cpu() < 0), empty)
-    _near(torch.where(empty.cuda(), 0.0, lse), torch.where(empty, 0.0, want_lse), lse_bound, "lse")
-    return out, lse, c, q
+    most = -(-max(lengths) // page)
+    for columns in (max(most, 1), most + 5000 // page):
+        c = U.Cache(kind, lengths, hk, dim, page, order, seed=seed, junk=junk, pad=pad, columns=columns)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, lse = T.attention_decode(q, c.k, c.v, c.tables, c.lengths, softcap=softcap, window=window, scale=scale,
+                                      return_lse=True, status=status)
+        T.cache_status(status)
+        want, want_lse, bound, lse_bound = U.attended(q, c, lengths, dim ** -0.5 if scale is None else scale, softcap, window)
+        # the weights of 16-bit caches are held as two 16-bit numbers: 2^-16 of each (bf16), 2^-21 (f16)
+        split = {"f32": 0.0, "f16": 2.0 ** -21, "bf16": 2.0 ** -16}[kind]
+        top = torch.stack([c.rows(r, n)[1].abs().amax() if n else torch.zeros(()).double() for r, n in enumerate(lengths)])
+        bound = bound + split * top[:, None, None] + U.ROUND[kind] * want.abs() * (1 + 2.0 ** -10) + U.TINY[kind]
+        _near(out, want, bound, "out")
+        empty = torch.isinf(want_lse)
+        assert torch.equal(torch.isinf(lse.cpu()) & (lse.cpu() < 0), empty)
+        _near(torch.where(empty.cuda(), 0.0, lse), torch.where(empty, 0.0, want_lse), lse_bound, "lse")
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("lengths", [[1], [64], [65], [700], [1500], [2048], [0], [33, 2000], [512, 0, 1, 900]], ids=str)
+@pytest.mark.parametrize("window", [0, 150])
+def test_attention_few_short_rows(kind, lengths, window):
+    """Teams of one, two, four and eight CTAs, with no, one and several tiles to a CTA."""
+    _attend(kind, lengths, 6, 2, 80, 16, window=window)
 
 
 @pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
