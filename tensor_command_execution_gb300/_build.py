@@ -24,8 +24,9 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 OBJ_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libcmdexec.so")
-# (torch's C++ interface holds for one version of it)
-TORCH_PATH = os.path.join(OUT_DIR, f"_cache_torch-{importlib.metadata.version('torch')}.so")
+# (torch's C++ interface holds for one version of it; without torch the module is not built)
+TORCH = importlib.util.find_spec("torch") is not None
+TORCH_PATH = os.path.join(OUT_DIR, f"_cache_torch-{importlib.metadata.version('torch') if TORCH else 'none'}.so")
 
 # (source, the defines of each object built from it), longest compiles first
 def _objs(tiers, nds=(None,)):
@@ -74,9 +75,10 @@ def _sources():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(TORCH_PATH):
+    made = [LIB_PATH] + [TORCH_PATH] * TORCH
+    if not all(os.path.exists(m) for m in made):
         return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(TORCH_PATH))
+    t = min(os.path.getmtime(m) for m in made)
     return all(os.path.getmtime(s) <= t for s in _sources())
 
 
@@ -109,12 +111,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
         cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-Wno-unused-parameter",
                "-c", os.path.join(CSRC, s), "-o", obj] + inc
         jobs.append((cmd, obj, None))
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
     torch_obj = os.path.join(OBJ_DIR, TORCH_SOURCE + ".o")
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c", os.path.join(CSRC, TORCH_SOURCE), "-o", torch_obj,
-           "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(torch_dir, "include"), "-isystem",
-           os.path.join(torch_dir, "include", "torch", "csrc", "api", "include")] + inc
-    jobs.append((cmd, torch_obj, None))
+    if TORCH:
+        torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c", os.path.join(CSRC, TORCH_SOURCE), "-o",
+               torch_obj, "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(torch_dir, "include"),
+               "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include")] + inc
+        jobs.append((cmd, torch_obj, None))
 
     def run(job):
         cmd, obj, log = job
@@ -136,6 +139,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed: {' '.join(link)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    if not TORCH:
+        return LIB_PATH
     tmp = TORCH_PATH + f".tmp{os.getpid()}"
     link = (["g++", "-shared", "-o", tmp, torch_obj, "-L" + os.path.join(torch_dir, "lib"), "-L" + OUT_DIR]
             + ["-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-l:libcmdexec.so", "-Wl,-rpath,$ORIGIN"])

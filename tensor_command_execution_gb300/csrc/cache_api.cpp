@@ -593,7 +593,8 @@ extern "C" cmd_status cmd_attention_decode(const cmd_attention_args* args, void*
       const cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
       const cudaError_t e = !copy       ? cmdx::attend_simt_launch(a.q.dtype, p, stream)
                             : es == 4   ? (copy == 16 ? cmdx::attend_f32_launch16 : cmdx::attend_f32_launch4)(p, stream)
-                                        : (copy == 16 ? cmdx::attend_mma_launch16 : cmdx::attend_mma_launch4)(a.q.dtype, p, stream);
+                                        : (copy == 16 ? cmdx::attend_mma_launch16
+                                                      : cmdx::attend_mma_launch4)(a.q.dtype, p, stream);
       if (e != cudaSuccess) return launched(e);
     }
     return CMD_OK;

@@ -2,26 +2,23 @@
 // shared by its kernels.
 //
 // A unit of work is a tile of tokens of one row, for one kv head and a block
-// of the query heads that share it; a CTA's warps share its tokens.
-// The units of a launch, ordered by row, then head, then token, are cut into
-// equal runs, one for each CTA, whatever the rows' lengths: no CTA waits for a
-// long row. The beginning of a row counts as start_units more units (before
-// its first tile; a CTA whose run ends with them does nothing for the row),
-// since fetching queries and writing a result take as long as some tiles. A CTA whose run holds all of a row's tiles writes the result; one
-// that holds some writes a part (maximum, sum and weighted values) to the
-// workspace, and a second, small launch joins the parts of each split row in
-// their order, so that the result does not depend on timing. At most two of a
-// CTA's segments are parts (its first and its last), so the workspace does not
-// grow with the rows, and at most one row that is split begins in a CTA, so
-// neither does the list of them.
+// of the query heads that share it; a CTA's warps share its tokens. The units
+// of a launch, ordered by row, then head, then token, are cut into equal runs,
+// one for each CTA, whatever the rows' lengths: no CTA waits for a long row.
+// The beginning of a row counts as start_units more units (before its first
+// tile; a CTA whose run ends with them does nothing for the row), since
+// fetching queries and writing a result take as long as some tiles. A CTA
+// whose run holds all of a row's tiles writes the result; one that holds some
+// writes a part (maximum, sum and weighted values) to the workspace, and a
+// second, small launch joins the parts of each split row in their order, so
+// that the result does not depend on timing. At most two of a CTA's segments
+// are parts (its first and its last), so the workspace does not grow with the
+// rows, and at most one row that is split begins in a CTA, so neither does the
+// list of them.
 //
 // A few short rows are not worth that: there a cluster of CTAs (a team) takes
 // each row and group and joins its parts through distributed shared memory,
 // in the same launch and without the workspace.
-//
-// A few short rows are not worth that: there a cluster of CTAs (a team) takes
-// each row and group and joins its parts through distributed shared memory,
-// in the same launch and with no workspace.
 #pragma once
 
 #include <cooperative_groups.h>

@@ -44,7 +44,8 @@ struct Shape {
 };
 
 template <int DP, int GT>
-__global__ void __launch_bounds__(kWarps * 32, Shape<DP, GT>::kCtas) attend_f32_kernel(const __grid_constant__ AttendParams p) {
+__global__ void __launch_bounds__(kWarps * 32, Shape<DP, GT>::kCtas)
+    attend_f32_kernel(const __grid_constant__ AttendParams p) {
   using S = Shape<DP, GT>;
   using Ring = typename S::Ring;
   constexpr int kScores = 2 * GT;                      // of a lane's two tokens

@@ -88,7 +88,8 @@ struct Shape {
 };
 
 template <class T, int DP, int NT>
-__global__ void __launch_bounds__(kWarps * 32, Shape<T, DP, NT>::kCtas) attend_mma_kernel(const __grid_constant__ AttendParams p) {
+__global__ void __launch_bounds__(kWarps * 32, Shape<T, DP, NT>::kCtas)
+    attend_mma_kernel(const __grid_constant__ AttendParams p) {
   using S = Shape<T, DP, NT>;
   using Ring = typename S::Ring;
   constexpr int KS = DP / 16;

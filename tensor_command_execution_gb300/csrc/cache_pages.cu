@@ -340,7 +340,8 @@ __device__ __forceinline__ void move_pages(const L& pools, const int32_t* src, c
 constexpr int kMoveThreads = 256;
 
 template <class U, class L>
-__global__ void __launch_bounds__(kMoveThreads) select_apply_kernel(const __grid_constant__ SelectParams p, const __grid_constant__ L pools) {
+__global__ void __launch_bounds__(kMoveThreads)
+    select_apply_kernel(const __grid_constant__ SelectParams p, const __grid_constant__ L pools) {
   wait_for_previous();
   let_next_start();
   const int lane = threadIdx.x & 31, warps = gridDim.x * (kMoveThreads / 32);
@@ -404,7 +405,8 @@ __device__ __forceinline__ void compact_plan(const CompactParams& p) {
 }
 
 template <class U, class L>
-__global__ void __launch_bounds__(kMoveThreads) compact_apply_kernel(const __grid_constant__ CompactParams p, const __grid_constant__ L pools) {
+__global__ void __launch_bounds__(kMoveThreads)
+    compact_apply_kernel(const __grid_constant__ CompactParams p, const __grid_constant__ L pools) {
   wait_for_previous();
   let_next_start();
   const int lane = threadIdx.x & 31, warps = gridDim.x * (kMoveThreads / 32);

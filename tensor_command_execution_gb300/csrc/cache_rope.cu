@@ -259,7 +259,8 @@ __global__ void __launch_bounds__(512, 2) rope_kernel(const __grid_constant__ Ro
       int j = 0;
       while (h >= p.s[j].heads) h -= p.s[j++].heads;
       const RopeStream& s = p.s[j];
-      const T* src = static_cast<const T*>(s.in) + stride_of<VEC>(b, s.in_st[0]) + stride_of<VEC>(t, s.in_st[1]) + stride_of<VEC>(h, s.in_st[2]);
+      const T* src = static_cast<const T*>(s.in) + stride_of<VEC>(b, s.in_st[0]) + stride_of<VEC>(t, s.in_st[1]) +
+                     stride_of<VEC>(h, s.in_st[2]);
       if (s.cache) {
         if (page < 0) continue;
         dst[i] = static_cast<T*>(s.out) + stride_of<VEC>(page, s.out_st[0]) + stride_of<VEC>(page_slot, s.out_st[1]) +

@@ -116,7 +116,7 @@ struct Where {
 };
 
 void same_device(const Where& w, PyObject* o, const char* name) {
-  if (o != Py_None && THPVariable_Unpack(o).device() != w.guard.current_device())
+  if (o != Py_None && tensor(o, name).device() != w.guard.current_device())
     raise(PyExc_ValueError, std::string(name) + " is on another GPU");
 }
 
@@ -209,6 +209,7 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     x.rope = rope_spec(a[9], a[10], a[11], 0);
     x.status = status_word(a[12]);
+    same_device(w, a[12], "status");
     const char* names[] = {"k", "v", "k_cache", "v_cache", "tables", "positions", "rows", "q", "q_out", "turns"};
     for (int i = 0; i < 10; ++i) same_device(w, a[i], names[i]);
     check(cmd_cache_append(&x, w.stream), "cmd_cache_append");
@@ -252,6 +253,7 @@ PyObject* py_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
       x.workspace = workspace.get();
     }
     x.status = status_word(a[12]);
+    same_device(w, a[12], "status");
     const char* names[] = {"q", "k_cache", "v_cache", "tables", "lengths"};
     for (int i = 0; i < 5; ++i) same_device(w, a[i], names[i]);
     same_device(w, a[8], "out");
@@ -276,7 +278,8 @@ int pools(PyObject* list, int64_t pages, const Where& w, cmd_pool* out) {
     same_device(w, o, "a pool");
     const int64_t rank = t.dim();
     if (rank < 1 || t.size(0) != pages)
-      raise(PyExc_ValueError, "pool " + std::to_string(i) + " does not have " + std::to_string(pages) + " pages in its first dim");
+      raise(PyExc_ValueError,
+            "pool " + std::to_string(i) + " does not have " + std::to_string(pages) + " pages in its first dim");
     int64_t block = 1, dims = 0;
     for (int64_t d = 1; d < rank; ++d) {
       block *= t.size(d);
@@ -339,6 +342,7 @@ PyObject* py_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
     workspace = w.scratch(x.workspace_bytes);
     x.workspace = workspace.get();
     x.status = status_word(a[8]);
+    same_device(w, a[8], "status");
     const char* names[] = {"tables", "lengths", "refs", "parents"};
     for (int i = 0; i < 4; ++i) same_device(w, a[i], names[i]);
     same_device(w, a[6], "grow");
@@ -372,6 +376,7 @@ PyObject* py_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
     workspace = w.scratch(x.workspace_bytes);
     x.workspace = workspace.get();
     x.status = status_word(a[6]);
+    same_device(w, a[6], "status");
     const char* names[] = {"tables", "lengths", "refs"};
     for (int i = 0; i < 3; ++i) same_device(w, a[i], names[i]);
     check(cmd_cache_compact(&x, w.stream), "cmd_cache_compact");
@@ -406,9 +411,14 @@ constexpr PyMethodDef method(const char* name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(F)), METH_FASTCALL, nullptr};
 }
 
-PyMethodDef g_methods[] = {method<py_rope>("rope"),         method<py_append>("cache_append"), method<py_attend>("attention_decode"),
-                           method<py_select>("cache_select"), method<py_compact>("cache_compact"), method<py_status>("cache_status"),
-                           {"set_error", py_set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
+PyMethodDef g_methods[] = {method<py_rope>("rope"),
+                           method<py_append>("cache_append"),
+                           method<py_attend>("attention_decode"),
+                           method<py_select>("cache_select"),
+                           method<py_compact>("cache_compact"),
+                           method<py_status>("cache_status"),
+                           {"set_error", py_set_error, METH_O, nullptr},
+                           {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_cache_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

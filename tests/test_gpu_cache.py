@@ -599,6 +599,10 @@ def test_refusals_of_tensors():
             (lambda: T.attention_decode(x, c, c, t, i, workspace=torch.empty(64, device="cuda")), T.CmdError, "workspace"),
             (lambda: T.attention_decode(x, c, c, t, i, status=torch.zeros(2, dtype=torch.int32, device="cuda")), ValueError, "status"),
             (lambda: T.cache_append(x, x, c, c.clone(), t, i, q=x), T.CmdError, "rotates"),
+            (lambda: T.cache_append(x, x, c, c.clone(), t, i, q_out=5), TypeError, "q_out is no tensor"),
+            (lambda: T.attention_decode(x, c, c, t, i, status=3), TypeError, "status is no tensor"),
+            (lambda: T.attention_decode(x, c, c, t, i, window=1 << 40), ValueError, "window"),
+            (lambda: T.attention_decode(x, c, c, t, i, softcap="1"), TypeError, "real number"),
             (lambda: T.cache_select(t, i, i, i, [c], page_size=2), ValueError, "pages in its first dim"),
             (lambda: T.cache_select(t, i, torch.zeros(4, dtype=torch.int32, device="cuda"), i, [c[..., ::2]], page_size=2), ValueError, "dense"),
             (lambda: T.cache_select(t, i, torch.zeros(4, dtype=torch.int32, device="cuda"), i, c, page_size=2), TypeError, "list or tuple"),
