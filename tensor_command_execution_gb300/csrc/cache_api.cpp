@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <string>
 #include <utility>
 
@@ -206,18 +207,22 @@ void check_rope(const cmd_rope_spec& r, int64_t dim) {
   }
 }
 
-// Whether a view's rows are whole 16-byte vectors, and its strides below 2^31.
-bool rope_rows(const cmd_operand& o) {
-  for (int d = 0; d < o.rank; ++d)
-    if (o.sizes[d] > 1 && o.strides[d] > 0x7fffffff) return false;
-  return vector_rows(o, 16);
-}
-
-// Whether every chunk of 16 bytes of a head lies wholly in the rotated part
-// (in the half layout in one half of it) or past it.
-bool rope_vectors(const cmd_rope_spec& r, int64_t dim, int es) {
-  const int ve = 16 / es;
-  return dim % ve == 0 && (r.layout == CMD_ROPE_HALF ? r.n_pairs : 2 * r.n_pairs) % ve == 0;
+// The bytes of an access that suit a rotation of these tensors: 16, 8 or 4 (a
+// chunk lies wholly in the rotated part, in the half layout in one half of it,
+// or past it; strides are below 2^31), else 0.
+int rope_bytes(const cmd_rope_spec& r, int64_t dim, std::initializer_list<const cmd_operand*> views) {
+  const int es = elem_size((*views.begin())->dtype);
+  for (int bytes = 16; bytes > es; bytes /= 2) {
+    const int ve = bytes / es;
+    bool ok = dim % ve == 0 && (r.layout == CMD_ROPE_HALF ? r.n_pairs : 2 * r.n_pairs) % ve == 0;
+    for (const cmd_operand* o : views) {
+      if (!o->ptr) continue;
+      ok = ok && vector_rows(*o, bytes);
+      for (int d = 0; d < o->rank; ++d) ok = ok && (o->sizes[d] <= 1 || o->strides[d] <= 0x7fffffff);
+    }
+    if (ok) return bytes;
+  }
+  return 0;
 }
 
 // A stream of the rope kernel from operands [batch,] tokens, heads, dim.
@@ -311,7 +316,7 @@ extern "C" cmd_status cmd_rope(const cmd_operand* q, const cmd_operand* q_out, c
     const cmd_operand* outs[2] = {q_out, k_out};
     const char* names[2][2] = {{"q", "q_out"}, {"k", "k_out"}};
     const cmd_operand* like = nullptr;
-    bool vec = true, nothing = false;
+    bool nothing = false;
     for (int j = 0; j < 2; ++j) {
       if (!ins[j]) continue;
       const cmd_operand& in = *ins[j];
@@ -335,7 +340,6 @@ extern "C" cmd_status cmd_rope(const cmd_operand* q, const cmd_operand* q_out, c
       check_apart(out, names[j][1], *positions, "positions");
       check_heads(in.sizes[in.rank - 2]);
       nothing = nothing || in.sizes[in.rank - 3] == 0 || in.sizes[in.rank - 1] == 0 || in.sizes[0] == 0;
-      vec = vec && rope_rows(in) && rope_rows(out);
       p.s[p.n_streams++] = rope_stream(in, out, true, false);
     }
     NEED(like, CMD_ERR_NULL, "q and k are both absent");
@@ -365,8 +369,9 @@ extern "C" cmd_status cmd_rope(const cmd_operand* q, const cmd_operand* q_out, c
     p.columns = -1;  // no cache
     rope_common(p, *rope, dim);
     if (nothing || p.heads == 0) return CMD_OK;
-    vec = vec && rope_vectors(*rope, dim, elem_size(like->dtype));
-    return launched(cmdx::rope_launch(like->dtype, rope->layout, vec, p, static_cast<cudaStream_t>(cuda_stream)));
+    const cmd_operand none = {};
+    const int bytes = rope_bytes(*rope, dim, {like, q ? q : &none, q ? q_out : &none, k ? k : &none, k ? k_out : &none});
+    return launched(cmdx::rope_launch(like->dtype, rope->layout, bytes, p, static_cast<cudaStream_t>(cuda_stream)));
   });
 }
 
@@ -431,7 +436,6 @@ extern "C" cmd_status cmd_cache_append(const cmd_append_args* args, void* cuda_s
     check_apart(a.k_cache, "k_cache", a.v_cache, "v_cache");
     cmdx::RopeParams p;
     std::memset(&p, 0, sizeof p);
-    bool vec = rope_rows(a.k) && rope_rows(a.v) && rope_rows(a.k_cache) && rope_rows(a.v_cache);
     if (has_q) {
       check(a.q, "q", 3, true);
       check(a.q_out, "q_out", 3, true);
@@ -445,7 +449,6 @@ extern "C" cmd_status cmd_cache_append(const cmd_append_args* args, void* cuda_s
       for (const auto& r : reads) check_apart(a.q_out, "q_out", *r.o, r.name, r.o == &a.q);
       check_apart(a.q_out, "q_out", a.k_cache, "k_cache");
       check_apart(a.q_out, "q_out", a.v_cache, "v_cache");
-      vec = vec && rope_rows(a.q) && rope_rows(a.q_out);
       p.s[p.n_streams++] = rope_stream(a.q, a.q_out, true, false);
     }
     p.s[p.n_streams++] = rope_stream(a.k, a.k_cache, true, true);
@@ -467,8 +470,9 @@ extern "C" cmd_status cmd_cache_append(const cmd_append_args* args, void* cuda_s
     p.status = a.status;
     rope_common(p, a.rope, dim);
     if (tokens == 0 || dim == 0 || p.heads == 0) return CMD_OK;
-    vec = vec && rope_vectors(a.rope, dim, elem_size(a.k.dtype));
-    return launched(cmdx::rope_launch(a.k.dtype, a.rope.layout, vec, p, static_cast<cudaStream_t>(cuda_stream)));
+    const cmd_operand none = {};
+    const int bytes = rope_bytes(a.rope, dim, {&a.k, &a.v, &a.k_cache, &a.v_cache, &a.q, has_q ? &a.q_out : &none});
+    return launched(cmdx::rope_launch(a.k.dtype, a.rope.layout, bytes, p, static_cast<cudaStream_t>(cuda_stream)));
   });
 }
 

@@ -59,9 +59,9 @@ struct RopeParams {
   int32_t* status;
 };
 
-// vec: every row of every stream may be accessed in 16-byte vectors, and every
-// stride is below 2^31
-cudaError_t rope_launch(int dtype, int layout, bool vec, const RopeParams& p, cudaStream_t stream);
+// bytes: 16, 8 or 4 where every row of every stream may be accessed so many at
+// a time and every stride is below 2^31, else 0
+cudaError_t rope_launch(int dtype, int layout, int bytes, const RopeParams& p, cudaStream_t stream);
 
 // ---- attention of one token (cache_attend*.cu) --------------------------------
 constexpr int kAttendMaxCtas = 152 * 4;  // bounds the workspace

@@ -27,10 +27,15 @@ namespace cmdx {
 
 namespace {
 
-// Heads a thread has in flight. Measured on 4 x 4096 tokens of 40 heads of 128
-// (bf16, before divisions and strides were narrowed): 2, 56.2 us (half) and
-// 56.9 (interleaved); 3, 55.7 and 55.3; 4, 61.5 and 61.4.
-constexpr int kRopeLoads = 3;
+// Heads a thread has in flight, by the bytes of an access (0: an element) and
+// of an element. Measured on 4 x 4096 tokens of 40 bf16 heads: of 128 elements
+// (16 bytes, before divisions and strides were narrowed) 2, 56.2 us; 3, 55.7;
+// 4, 61.5; of 72 (8 bytes) 3, 54.3; 4, 44.3; 5, 40.9; of 72 with 36 rotated (4
+// bytes) 3, 72.1; 4, 69.8; 6, 63.3. f32 heads of 72 (8 bytes) 3, 76.4; 4, 73.4;
+// 5, 101.7 (spills).
+__host__ __device__ constexpr int rope_loads(int bytes, int element) {
+  return bytes == 16 ? 3 : bytes == 8 ? (element == 2 ? 5 : 4) : bytes == 4 ? 6 : 4;
+}
 
 // Two 16-bit numbers of a word, and back.
 template <class T>
@@ -80,8 +85,8 @@ struct Turns {
   __device__ __forceinline__ float2 one() const { return of_token[group]; }
 };
 
-// VE elements of a head: a 16-byte vector when VEC, else up to VE of them one
-// by one.
+// VE elements of a head: a vector of 16, 8 or 4 bytes when VEC, else up to VE
+// of them one by one.
 template <class T, int VE, bool VEC>
 struct Chunk {
   T x[VE];
@@ -110,30 +115,41 @@ struct Chunk {
 };
 template <class T, int VE>
 struct Chunk<T, VE, true> {
-  uint32_t w[4];
+  static constexpr int kWords = VE * (int)sizeof(T) / 4;
+  uint32_t w[kWords];
   __device__ __forceinline__ void load(const T* p, int) {
-    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
-    w[0] = v.x;
-    w[1] = v.y;
-    w[2] = v.z;
-    w[3] = v.w;
+    if constexpr (kWords == 4) {
+      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
+      w[0] = v.x;
+      w[1] = v.y;
+      w[2] = v.z;
+      w[3] = v.w;
+    } else if constexpr (kWords == 2) {
+      const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p));
+      w[0] = v.x;
+      w[1] = v.y;
+    } else {
+      w[0] = __ldcs(reinterpret_cast<const uint32_t*>(p));
+    }
   }
   __device__ __forceinline__ void store(T* p, int) const {
-    __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
+    if constexpr (kWords == 4) __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
+    else if constexpr (kWords == 2) __stcs(reinterpret_cast<uint2*>(p), make_uint2(w[0], w[1]));
+    else __stcs(reinterpret_cast<uint32_t*>(p), w[0]);
   }
   __device__ __forceinline__ void turn_with(Chunk& o, const Turns<VE>& t) {
+    // two pairs at a time: of one word, or of two
 #pragma unroll
-    for (int i = 0; i < 4; i += VE == 4 ? 2 : 1) {
-      if constexpr (VE == 4) {
-        const float4 c = t.two(i / 2);
-        const float2 y = turned(__uint_as_float(w[i]), __uint_as_float(o.w[i]), make_float2(c.x, c.y));
-        const float2 z = turned(__uint_as_float(w[i + 1]), __uint_as_float(o.w[i + 1]), make_float2(c.z, c.w));
-        w[i] = __float_as_uint(y.x);
-        o.w[i] = __float_as_uint(y.y);
-        w[i + 1] = __float_as_uint(z.x);
-        o.w[i + 1] = __float_as_uint(z.y);
+    for (int i = 0; i < VE / 2; ++i) {
+      const float4 c = t.two(i);
+      if constexpr (sizeof(T) == 4) {
+        const float2 y = turned(__uint_as_float(w[2 * i]), __uint_as_float(o.w[2 * i]), make_float2(c.x, c.y));
+        const float2 z = turned(__uint_as_float(w[2 * i + 1]), __uint_as_float(o.w[2 * i + 1]), make_float2(c.z, c.w));
+        w[2 * i] = __float_as_uint(y.x);
+        o.w[2 * i] = __float_as_uint(y.y);
+        w[2 * i + 1] = __float_as_uint(z.x);
+        o.w[2 * i + 1] = __float_as_uint(z.y);
       } else {
-        const float4 c = t.two(i);
         const float2 a = unpack<T>(w[i]), b = unpack<T>(o.w[i]);
         const float2 y = turned(a.x, b.x, make_float2(c.x, c.y)), z = turned(a.y, b.y, make_float2(c.z, c.w));
         w[i] = pack<T>(y.x, z.x);
@@ -141,21 +157,27 @@ struct Chunk<T, VE, true> {
       }
     }
   }
+  // pair i of this chunk turned
+  __device__ __forceinline__ void turn_pair(int i, float2 c) {
+    if constexpr (sizeof(T) == 4) {
+      const float2 y = turned(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]), c);
+      w[2 * i] = __float_as_uint(y.x);
+      w[2 * i + 1] = __float_as_uint(y.y);
+    } else {
+      const float2 a = unpack<T>(w[i]);
+      const float2 y = turned(a.x, a.y, c);
+      w[i] = pack<T>(y.x, y.y);
+    }
+  }
   __device__ __forceinline__ void turn(const Turns<VE / 2>& t) {
+    if constexpr (VE == 2) {
+      turn_pair(0, t.one());
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-      if constexpr (VE == 4) {
-        const float4 c = t.two(0);
-        const float2 y = turned(__uint_as_float(w[i]), __uint_as_float(w[i + 1]),
-                                i == 0 ? make_float2(c.x, c.y) : make_float2(c.z, c.w));
-        w[i] = __float_as_uint(y.x);
-        w[i + 1] = __float_as_uint(y.y);
-      } else {
-        const float4 c = t.two(i / 2);
-        const float2 a = unpack<T>(w[i]), b = unpack<T>(w[i + 1]);
-        const float2 y = turned(a.x, a.y, make_float2(c.x, c.y)), z = turned(b.x, b.y, make_float2(c.z, c.w));
-        w[i] = pack<T>(y.x, y.y);
-        w[i + 1] = pack<T>(z.x, z.y);
+      for (int i = 0; i < VE / 4; ++i) {
+        const float4 c = t.two(i);
+        turn_pair(2 * i, make_float2(c.x, c.y));
+        turn_pair(2 * i + 1, make_float2(c.z, c.w));
       }
     }
   }
@@ -178,6 +200,7 @@ __device__ __forceinline__ int64_t stride_of(int64_t index, int64_t stride) {
 template <class T, int VE, bool VEC, bool HALF>
 __global__ void __launch_bounds__(512, 2) rope_kernel(const __grid_constant__ RopeParams p, const RopeShape shape) {
   constexpr int NP = HALF ? VE : VE / 2;  // pairs of a thread's place
+  constexpr int kRopeLoads = rope_loads(VEC ? VE * (int)sizeof(T) : 0, sizeof(T));
   extern __shared__ __align__(16) float2 s_turn[];  // [tokens][n_pairs]: cosine and sine
   const int tid = threadIdx.x;
   const int column = (int)fast_div32(shape.by_units, tid), unit = tid - column * shape.units;
@@ -310,6 +333,7 @@ __global__ void __launch_bounds__(512, 2) rope_kernel(const __grid_constant__ Ro
 template <class T, int VE, bool VEC, bool HALF>
 cudaError_t launch(const RopeParams& p, cudaStream_t stream) {
   RopeShape s;
+  constexpr int kRopeLoads = rope_loads(VEC ? VE * (int)sizeof(T) : 0, sizeof(T));
   const int halves = HALF ? p.n_pairs / VE : 0, chunks = (p.dim - (HALF ? 2 * p.n_pairs : 0) + VE - 1) / VE;
   s.units = halves + (chunks + 1) / 2;
   // as many heads at once as leave every thread kRopeLoads of them, or fewer, within 512 threads
@@ -333,21 +357,33 @@ cudaError_t launch(const RopeParams& p, cudaStream_t stream) {
                     (size_t)s.tokens * p.n_pairs * sizeof(float2), stream, p, s);
 }
 
+template <class T, int VE, bool VEC>
+cudaError_t launch_layout(int layout, const RopeParams& p, cudaStream_t stream) {
+  constexpr int kHalf = VEC ? VE : 1;  // (one by one: single elements in the half layout, pairs in the other)
+  return layout == CMD_ROPE_HALF ? launch<T, kHalf, VEC, true>(p, stream) : launch<T, VE, VEC, false>(p, stream);
+}
+
+// The access: 16, 8 or (16-bit types) 4 bytes, else element by element.
+// Measured on 4 x 4096 tokens of 40 bf16 heads: of 80 elements, all rotated (16
+// bytes) 38.0 us; of 72 (8 bytes) 40.9, of 72 with 36 rotated (4 bytes) 63.3,
+// both 140 element by element.
 template <class T>
-cudaError_t launch_type(int layout, bool vec, const RopeParams& p, cudaStream_t stream) {
-  constexpr int VE = 16 / sizeof(T);
-  if (layout == CMD_ROPE_HALF)
-    return vec ? launch<T, VE, true, true>(p, stream) : launch<T, 1, false, true>(p, stream);
-  return vec ? launch<T, VE, true, false>(p, stream) : launch<T, 2, false, false>(p, stream);
+cudaError_t launch_type(int layout, int bytes, const RopeParams& p, cudaStream_t stream) {
+  constexpr int ES = sizeof(T);
+  if (bytes == 16) return launch_layout<T, 16 / ES, true>(layout, p, stream);
+  if (bytes == 8) return launch_layout<T, 8 / ES, true>(layout, p, stream);
+  if constexpr (ES == 2)
+    if (bytes == 4) return launch_layout<T, 2, true>(layout, p, stream);
+  return launch_layout<T, 2, false>(layout, p, stream);
 }
 
 }  // namespace
 
-cudaError_t rope_launch(int dtype, int layout, bool vec, const RopeParams& p, cudaStream_t stream) {
+cudaError_t rope_launch(int dtype, int layout, int bytes, const RopeParams& p, cudaStream_t stream) {
   switch (dtype) {
-    case CMD_F32: return launch_type<float>(layout, vec, p, stream);
-    case CMD_F16: return launch_type<__half>(layout, vec, p, stream);
-    case CMD_BF16: return launch_type<__nv_bfloat16>(layout, vec, p, stream);
+    case CMD_F32: return launch_type<float>(layout, bytes, p, stream);
+    case CMD_F16: return launch_type<__half>(layout, bytes, p, stream);
+    case CMD_BF16: return launch_type<__nv_bfloat16>(layout, bytes, p, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -36,6 +36,7 @@ ROPE_SHAPES = [  # batch, tokens, q heads, k heads, dim, rotated
     (2, 5, 4, 2, 128, 128), (1, 1, 1, 1, 64, 64), (3, 7, 3, 3, 80, 32), (1, 9, 5, 1, 72, 72), (2, 3, 2, 2, 256, 256),
     (1, 4, 130, 2, 64, 48), (1, 6, 2, 1, 10, 6), (2, 4, 3, 1, 33, 20), (1, 2, 1, 1, 2, 2), (1, 3, 2, 2, 16, 0),
     (2, 3001, 1, 1, 16, 8), (1, 5003, 2, 0, 32, 32),
+    (2, 9, 17, 3, 72, 36), (1, 7, 20, 20, 80, 40), (1, 5, 9, 2, 20, 12), (2, 3, 31, 1, 36, 36), (1, 8, 3, 3, 22, 10),
 ]
 
 
