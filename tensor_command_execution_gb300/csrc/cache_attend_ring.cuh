@@ -15,13 +15,13 @@ namespace cmdx {
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
-// N bytes to shared memory, or as many zeros where !take
+// The first `bytes` of N bytes to shared memory, and zeros for the others.
 template <int N>
-__device__ __forceinline__ void copy_bytes(uint32_t dst, const void* src, bool take) {
+__device__ __forceinline__ void copy_bytes(uint32_t dst, const void* src, int bytes) {
   if constexpr (N == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(take ? 4 : 0) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -57,8 +57,10 @@ struct AttendRing {
   const uint32_t at;     // the ring's shared address
   const int copy_row, chunk, chunks;
   const bool one_page;   // a tile lies in one page
-  // the tile to copy next: the page (-1: none) and slot of this lane's token,
-  // lane % TOKENS, and the head's keys and values
+  // the tile to copy next: whether this lane's token, lane % TOKENS, is in the
+  // row, its page and slot, and the head's keys and values. (The page is not
+  // looked at before the copy, so that its load may be on its way until then.)
+  bool inside = false;
   int page = -1, slot = 0;
   const T *k = nullptr, *v = nullptr;
   const int32_t* table = nullptr;
@@ -81,53 +83,74 @@ struct AttendRing {
   }
 
   __device__ __forceinline__ void look_up() {
-    page = -1;
+    inside = false;
     if (look_at < 0 || look_at == look.tiles) {
       if (look_at > 0) look = attend_next(p, rows, share, look, kTile);
       look_at = 0;
       if (look.tiles == 0) return;
       table = p.tables + look.row * p.table_st[0];
       const int head = look.group / p.blocks;
-      k = static_cast<const T*>(p.k) + chunk * kEach + head * p.k_st[2];
-      v = static_cast<const T*>(p.v) + chunk * kEach + head * p.v_st[2];
+      k = static_cast<const T*>(p.k) + head * p.k_st[2];
+      v = static_cast<const T*>(p.v) + head * p.v_st[2];
     }
     const int token = (look.tile0 + look_at) * kTile + warp * TOKENS + lane % TOKENS;
     const uint32_t column = fast_div32(p.page, (uint32_t)token);
     slot = token - (int)(column * p.page.d);
-    if (token >= look.lo && token < look.n) {
-      page = __ldg(table + column * p.table_st[1]);
-      if (page < 0 || page >= p.n_pages) {
-        report(p.status, CMD_CACHE_BAD_PAGE);
-        page = -1;
-      }
-    }
+    inside = token >= look.lo && token < look.n;
+    if (inside) page = __ldg(table + column * p.table_st[1]);
     ++look_at;
+  }
+
+  // One row's keys and values, or zeros where !take.
+  __device__ __forceinline__ void copy_row_of(uint32_t dst, const T* ks, const T* vs, bool take) {
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c) {
+      const int piece = chunk + 32 * c;  // (pieces past the head dim are zeros: they read the first one's address, no bytes)
+      const int bytes = take && piece < chunks ? COPY : 0, e = piece < chunks ? piece * kEach : 0;
+      copy_bytes<COPY>(dst + 32 * c * COPY, ks + e, bytes);
+      copy_bytes<COPY>(dst + 32 * c * COPY + kKeys, vs + e, bytes);
+    }
   }
 
   // Copies the next tile into a stage; returns which of its tokens have a page.
   __device__ __forceinline__ uint32_t copy(int into) {
-    const uint32_t has = __ballot_sync(~0u, page >= 0) & ((1u << TOKENS) - 1u);
+    constexpr uint32_t kAll = (1u << TOKENS) - 1u;
+    if (inside && (page < 0 || page >= p.n_pages)) {
+      report(p.status, CMD_CACHE_BAD_PAGE);
+      inside = false;
+    }
+    const uint32_t has = __ballot_sync(~0u, inside) & kAll;
     if (has) {
       const uint32_t dst = at + into * kStage + copy_row * PITCH + chunk * COPY;
-      const int64_t one = __shfl_sync(~0u, page, __ffs(has) - 1);
-      const int64_t first = __shfl_sync(~0u, slot, 0) + copy_row;
-      const T* k0 = k + one * p.k_st[0] + first * p.k_st[1];
-      const T* v0 = v + one * p.v_st[0] + first * p.v_st[1];
+      if (one_page) {
+        const int64_t one = __shfl_sync(~0u, page, __ffs(has) - 1);
+        const int64_t first = __shfl_sync(~0u, slot, 0) + copy_row;
+        const T* ks = k + one * p.k_st[0] + first * p.k_st[1];
+        const T* vs = v + one * p.v_st[0] + first * p.v_st[1];
+        const int64_t k_step = kRows * p.k_st[1], v_step = kRows * p.v_st[1];
+        if (has == kAll) {
 #pragma unroll
-      for (int r = 0; r < TOKENS; r += kRows) {
-        const bool in = has >> (r + copy_row) & 1;
-        const T *ks = k0 + r * p.k_st[1], *vs = v0 + r * p.v_st[1];
-        if (!one_page) {
-          const int64_t pg = __shfl_sync(~0u, page, r + copy_row), sl = __shfl_sync(~0u, slot, r + copy_row);
-          ks = k + pg * p.k_st[0] + sl * p.k_st[1];
-          vs = v + pg * p.v_st[0] + sl * p.v_st[1];
+          for (int r = 0; r < TOKENS; r += kRows) {
+            copy_row_of(dst + r * PITCH, ks, vs, true);
+            ks += k_step;
+            vs += v_step;
+          }
+        } else {
+#pragma unroll
+          for (int r = 0; r < TOKENS; r += kRows) {
+            const bool in = has >> (r + copy_row) & 1;
+            copy_row_of(dst + r * PITCH, in ? ks : k, in ? vs : v, in);
+            ks += k_step;
+            vs += v_step;
+          }
         }
+      } else {
 #pragma unroll
-        for (int c = 0; c < kPieces; ++c) {
-          const bool take = in && chunk + 32 * c < chunks;
-          const int e = 32 * c * kEach, to = r * PITCH + 32 * c * COPY;
-          copy_bytes<COPY>(dst + to, take ? static_cast<const void*>(ks + e) : p.k, take);
-          copy_bytes<COPY>(dst + to + kKeys, take ? static_cast<const void*>(vs + e) : p.v, take);
+        for (int r = 0; r < TOKENS; r += kRows) {
+          const int64_t pg = __shfl_sync(~0u, page, r + copy_row), sl = __shfl_sync(~0u, slot, r + copy_row);
+          const bool in = has >> (r + copy_row) & 1;
+          copy_row_of(dst + r * PITCH, in ? k + pg * p.k_st[0] + sl * p.k_st[1] : k,
+                      in ? v + pg * p.v_st[0] + sl * p.v_st[1] : v, in);
         }
       }
     }
