@@ -70,7 +70,7 @@ constexpr int kAttendLeastTile = 32;     // tokens of a CTA's tile, at least, an
 constexpr int kAttendMostStart = 4;      // units of a row's beginning, at most: they bound a launch's units
 
 // A row (for one kv head and block of query heads) whose tiles went to several
-// CTAs: part k lies at index `first` for k = 0, (first & ~1) + 2 k after.
+// CTAs: part k lies at index `first` for k = 0, (first & ~1) + 2 k sides after.
 struct AttendSplit {
   int32_t row, group, first;
   int32_t parts;  // 0: none
@@ -99,6 +99,7 @@ struct AttendParams {
   AttendSplit* splits; // one for each CTA, or for each row and group
   int32_t tasks;       // of the join
   int32_t start_units; // what the beginning of a row counts, in tiles
+  int32_t sides;       // groups whose CTAs work side by side: all of them, or 1: units of all groups are shared
   int32_t team;        // CTAs of a cluster that takes one row and group; 0: units are dealt out evenly
   uint8_t split_by_row;
   int32_t* status;
