@@ -15,7 +15,7 @@
 // Measured: 24 rows of 2999 tokens, 16 kv heads of 128, one query head each
 // 177 us, 6.65 TB/s, 98% of the copy peak; 8 query heads to each of 2 kv heads,
 // 96 rows, 118 us, 74%, bound by the multiply-adds and the reads of queries; 24
-// rows of 1 to 1100 tokens (16 heads of 80, capped, windowed) 20.2 us, 49%,
+// rows of 1 to 1100 tokens (16 heads of 80, capped, windowed) 19.5 us, 51%,
 // 8 of it the fixed part of two launches.
 #include "cache_attend_ring.cuh"
 

@@ -20,10 +20,10 @@
 // are copied, whatever their slots hold.
 //
 // Measured (bf16, 8 kv heads of 128, 64 query heads): 64 rows of 4096 tokens
-// 177 us, 6.08 TB/s, 90% of the copy peak (the launch alone 169; its slowest
-// SM ran 8% longer than the mean); 64 rows of 0 to 8192 tokens 47 us, 75%; two
-// rows of 393217 and 262147 tokens of 2 kv heads (f16) 112.5 us, 88%; one row
-// of 700, 6.5 us, the latency of one launch. Tensor units 14% busy, issue
+// 176.5 us, 6.10 TB/s, 90% of the copy peak (the launch alone 169; its slowest
+// SM ran 8% longer than the mean); 64 rows of 0 to 8192 tokens 48.4 us, 73%;
+// two rows of 393217 and 262147 tokens of 2 kv heads (f16) 113.7 us, 87%; one
+// row of 700, 6.7 us, the latency of one launch. Tensor units 14% busy, issue
 // slots 31%. Rows copied in pieces of 4 bytes: 64 rows of 4096 tokens of dim
 // 100, 263 us, 47%, bound by the number of copies.
 #include "cache_attend_ring.cuh"

@@ -11,11 +11,11 @@
 // tables and moves the pages: bound by memory, 16 bytes a thread and access
 // with four in flight.
 //
-// Measured: compaction moving 1703 pages of 4 x 64 KB among 7001, 142.4 us,
-// 6.27 TB/s, 92.5% of the copy peak (the moves alone 6.75 TB/s); selection of
+// Measured: compaction moving 1703 pages of 4 x 64 KB among 7001, 141.8 us,
+// 6.30 TB/s, 93% of the copy peak (the moves alone 6.75 TB/s); selection of
 // 509 rows among 6300 pages, 200 of 4 x 128 KB copied, 41.7 us, 75% (13 us of
-// it the plan, bound by the latency of its steps); 64 beams 8.5 us, 601 pages'
-// compaction 5.6 us, both fixed parts.
+// it the plan, bound by the latency of its steps); 64 beams 8.7 us, 601 pages'
+// compaction 5.8 us, both fixed parts.
 //
 // Only integer atomics are used where threads meet, so the results do not
 // depend on their order (the list of pages to copy has no order of its own:
