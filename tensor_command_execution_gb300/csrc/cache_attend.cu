@@ -10,8 +10,9 @@
 // butterfly that leaves each lane one finished score (31 shuffles for 32
 // scores rather than 5 each), where scaling, the cap, the mask and the
 // exponential are then done once. Bound by the latency of its loads, element
-// by element: 64 rows of 4096 tokens of 8 kv heads of 101 (bf16, 64 query
-// heads) 2060 us, 6% of the copy peak, which is what an odd head dim costs.
+// by element: 64 rows of 4096 tokens of 8 kv heads of 101 (bf16) 559 us with one
+// query head each, 22% of the copy peak, 1117 with eight, which is what an odd
+// head dim costs (2060 with each token's page looked up where it is read).
 #include "cache_attend.cuh"
 
 namespace cmdx {
@@ -64,35 +65,39 @@ __global__ void __launch_bounds__(kWarps * 32) attend_simt_kernel(const __grid_c
     // this lane's score is that of token lane / kDup / GT and head lane / kDup % GT of a step
     const int my_token = lane / kDup / GT;
     float m = -CUDART_INF_F, l = 0.0f;
+    // the page and slot of this lane's token of a tile (lane % 16), read a tile ahead
+    const int32_t* table = p.tables + g.row * p.table_st[0];
+    int page = 0, slot = 0;
+    bool inside = false;
+    const auto look_up = [&](int i) {
+      const int token = (g.tile0 + i) * tile + warp * kTokens + lane % kTokens;
+      inside = i < g.tiles && token >= g.lo && token < g.n;
+      const uint32_t column = fast_div32(p.page, (uint32_t)token);
+      slot = token - (int)(column * p.page.d);
+      if (inside) page = __ldg(table + column * p.table_st[1]);
+    };
+    look_up(0);
     for (int i = 0; i < g.tiles; ++i) {
-      const int t0 = (g.tile0 + i) * tile + warp * kTokens;
-      for (int t = max(t0, g.lo / kStep * kStep); t < min(t0 + kTokens, g.n); t += kStep) {
+      if (inside && (page < 0 || page >= p.n_pages)) {
+        report(p.status, CMD_CACHE_BAD_PAGE);
+        inside = false;
+      }
+      const uint32_t has = __ballot_sync(~0u, inside) & ((1u << kTokens) - 1u);
+      const int page_here = inside ? page : 0, slot_here = inside ? slot : 0;
+      look_up(i + 1);
+      for (int t = 0; t < kTokens; t += kStep) {
+        if ((has >> t & ((1u << kStep) - 1u)) == 0) continue;
         float k[kStep][VEC], v[kStep][VEC];
-        bool bad = false;
         bool seen[kStep];
 #pragma unroll
         for (int j = 0; j < kStep; ++j) {
-          const int token = t + j;
-          seen[j] = token >= g.lo && token < g.n;
-          const uint32_t column = fast_div32(p.page, (uint32_t)token);
-          int page = 0;
-          if (seen[j]) {
-            page = p.tables[g.row * p.table_st[0] + column * p.table_st[1]];
-            if (page < 0 || page >= p.n_pages) {
-              seen[j] = false;
-              bad = true;
-            }
-          }
-          if (seen[j]) {
-            const int64_t in_page = token - (int64_t)column * p.page.d;
-            load_row<T, VEC>(k[j], kp + page * p.k_st[0] + in_page * p.k_st[1] + heads.kv * p.k_st[2], lane, p.dim);
-            load_row<T, VEC>(v[j], vp + page * p.v_st[0] + in_page * p.v_st[1] + heads.kv * p.v_st[2], lane, p.dim);
-          } else {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) k[j][e] = v[j][e] = 0.0f;
-          }
+          seen[j] = has >> (t + j) & 1;
+          // (a token outside reads nothing: every element is past a dim of 0)
+          const int64_t pg = __shfl_sync(~0u, page_here, t + j), sl = __shfl_sync(~0u, slot_here, t + j);
+          const int dim = seen[j] ? p.dim : 0;
+          load_row<T, VEC>(k[j], kp + pg * p.k_st[0] + sl * p.k_st[1] + heads.kv * p.k_st[2], lane, dim);
+          load_row<T, VEC>(v[j], vp + pg * p.v_st[0] + sl * p.v_st[1] + heads.kv * p.v_st[2], lane, dim);
         }
-        if (bad && lane == 0) report(p.status, CMD_CACHE_BAD_PAGE);
         float s[NV];
 #pragma unroll
         for (int j = 0; j < kStep; ++j)
