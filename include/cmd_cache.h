@@ -28,8 +28,9 @@
  * element strides >= 0). Outputs must address distinct elements and must not
  * overlap an input, except where "in place" is allowed. Element types are
  * CMD_F32, CMD_F16 and CMD_BF16 for numbers (one type within a call; all
- * arithmetic is in 32 bits, rounded once to the output's type) and CMD_I32
- * for tables, lengths, positions and counts.
+ * arithmetic is in 32 bits, rounded once to the output's type, but for the
+ * softmax weights of 16-bit caches, see the attention) and CMD_I32 for tables,
+ * lengths, positions and counts.
  *
  * Every launch is asynchronous on cuda_stream (NULL = the legacy default
  * stream), on the current device, allocates nothing, may be captured, and
@@ -145,8 +146,13 @@ cmd_status cmd_cache_append(const cmd_append_args* args, void* cuda_stream);
  * through workspace: cmd_attention_workspace bytes of device memory, 16-byte
  * aligned, of any contents, used by one call at a time (streams that overlap
  * need one each). Results do not depend on the timing of the parts. columns *
- * page_size * kv_heads stays below 2^35. A 16-bit
- * value of infinity inside a row makes its element of out NaN or infinite. */
+ * page_size * kv_heads stays below 2^35.
+ *
+ * The weights of 16-bit caches are multiplied with the values as the sum of two
+ * 16-bit numbers each: to 2^-16 of itself in bf16 and 2^-22 in f16 (there no
+ * finer than 2^-40 of the largest weight); their sum, lse and everything else
+ * are in 32 bits. A 16-bit value of infinity inside a row makes its element of
+ * out NaN or infinite. */
 typedef struct cmd_attention_args {
   cmd_operand q, out;           /* [rows, q_heads, dim], dim <= CMD_CACHE_MAX_DIM */
   cmd_operand lse;              /* optional: f32 [rows, q_heads] */

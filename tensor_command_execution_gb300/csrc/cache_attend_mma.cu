@@ -16,8 +16,15 @@
 //
 // A weight p is held as the sum of two 16-bit numbers, hi + lo, multiplied
 // apart: rounding p itself to 16 bits would add an error as large as the
-// output's own rounding. Tokens outside the row are filled with zeros as they
-// are copied, whatever their slots hold.
+// output's own rounding. Together they hold p to 2^-16 of itself (bf16) or
+// 2^-22 (f16). binary16 has few exponents for that, and rows can be long: beside
+// one token that takes nearly all, 10^5 others of 2^-26 each still add up to
+// 2^-9. So an f16 weight is lifted by 2^15 first (the largest, 1, to half of the
+// largest number), which leaves an error of 2^-40 of the largest weight at most,
+// and o is lowered again when a row ends; the sum l takes p as it is. (Unlifted,
+// the output of 8192 tokens beside one e^17.5 times as heavy was 25% off.)
+// Tokens outside the row are filled with zeros as they are copied, whatever
+// their slots hold.
 //
 // Measured (bf16, 8 kv heads of 128, 64 query heads): 64 rows of 4096 tokens
 // 176.5 us, 6.10 TB/s, 90% of the copy peak (the launch alone 169; its slowest
@@ -64,6 +71,12 @@ __device__ __forceinline__ void mma<__nv_bfloat16>(float (&c)[4], const uint32_t
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+
+// What weights are multiplied by before they are rounded to T: a power of two.
+template <class T>
+constexpr float kLift = 1.0f;
+template <>
+constexpr float kLift<__half> = 32768.0f;
 
 // x and y rounded to T, and what the rounding leaves of each, rounded again.
 template <class T>
@@ -204,8 +217,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<T, DP, NT>::kCtas)
           x[e] = x[e] == -CUDART_INF_F ? 0.0f : power_of_two(x[e] - m[j][e & 1]);
           l[j][e & 1] += x[e];
         }
-        split<T>(x[0], x[1], &hi[j][0], &lo[j][0]);
-        split<T>(x[2], x[3], &hi[j][1], &lo[j][1]);
+        split<T>(x[0] * kLift<T>, x[1] * kLift<T>, &hi[j][0], &lo[j][0]);
+        split<T>(x[2] * kLift<T>, x[3] * kLift<T>, &hi[j][1], &lo[j][1]);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           hi[j][e] = transposed(hi[j][e]);
@@ -247,8 +260,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<T, DP, NT>::kCtas)
         }
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          x[16 * k + gr] = o[j][k][e];
-          x[16 * k + gr + 8] = o[j][k][2 + e];
+          x[16 * k + gr] = o[j][k][e] * (1.0f / kLift<T>);
+          x[16 * k + gr + 8] = o[j][k][2 + e] * (1.0f / kLift<T>);
         }
       }
     }
