@@ -93,12 +93,14 @@ typedef enum cmd_rope_scaling {
   CMD_ROPE_SCALING_BASE = 2,   /* base * factor^(d / (d - 2)), d = 2 n_pairs: the slowest frequency is divided by factor,
                                   the fastest kept */
   CMD_ROPE_SCALING_PARTS = 3   /* pairs that make at least beta_fast turns over original_length kept, those that make
-                                  at most beta_slow divided by factor, a linear ramp over the pair's index between */
+                                  at most beta_slow divided by factor, a linear ramp over the pair's index between: from
+                                  the index that makes beta_fast, rounded down and at least 0, to that which makes
+                                  beta_slow, rounded up and at most 2 n_pairs - 1 (the last pair's is n_pairs - 1) */
 } cmd_rope_scaling;
 
 /* turns[i] = 2^64 * base^(-i / n_pairs) / (2 pi), scaled as `scaling` says, rounded to an integer, for i < n_pairs;
  * turns is host memory. factor >= 1; original_length, beta_fast > beta_slow > 0 are read by CMD_ROPE_SCALING_PARTS
- * only. base > 1 (>= 1 for n_pairs = 1). Host only. */
+ * only. base > 1 (>= 1 for n_pairs = 1, but by parts). Host only. */
 cmd_status cmd_rope_turns(int32_t n_pairs, double base, int32_t scaling, double factor, double original_length,
                           double beta_fast, double beta_slow, uint64_t* turns);
 

@@ -284,12 +284,14 @@ extern "C" cmd_status cmd_rope_turns(int32_t n_pairs, double base, int32_t scali
       NEED(std::isfinite(original_length) && original_length > 0 && std::isfinite(beta_fast) && beta_slow > 0 &&
                beta_fast > beta_slow,
            CMD_ERR_ARG, "scaling by parts needs original_length > 0 and beta_fast > beta_slow > 0");
-      // the pair that makes `beta` turns over original_length: a real index
+      NEED(base > 1.0 || n_pairs == 0, CMD_ERR_ARG, "scaling by parts needs a base above 1");
+      // the pair that makes `beta` turns over original_length: a real index (past the last pair, where the slowest one
+      // makes more: the ramp then ends outside, at most at the rotated elements' number less one)
       auto pair_of = [&](double beta) {
         return n_pairs * std::log(original_length / (beta * two_pi)) / std::log(base);
       };
       lo = std::max(std::floor(pair_of(beta_fast)), 0.0);
-      hi = std::min(std::ceil(pair_of(beta_slow)), (double)n_pairs - 1);
+      hi = std::min(std::ceil(pair_of(beta_slow)), 2.0 * n_pairs - 1);
       if (hi <= lo) hi = lo + 0.001;
     }
     for (int i = 0; i < n_pairs; ++i) {
