@@ -70,7 +70,8 @@ bool empty(const cmd_operand& o) {
   return false;
 }
 
-// Checks that hold for every operand: rank, sizes, strides, pointer.
+// Checks that hold for every operand: rank, sizes, strides, pointer. They come
+// before anything else that walks an operand's dims.
 void check(const cmd_operand& o, const char* name, int rank, bool has_dim = false) {
   NEED(o.rank == rank, CMD_ERR_SHAPE, std::string(name) + " has rank " + std::to_string(o.rank) + ", not " +
                                           std::to_string(rank));
@@ -339,7 +340,6 @@ extern "C" cmd_status cmd_rope(const cmd_operand* q, const cmd_operand* q_out, c
       }
       like = &in;
       check_apart(out, names[j][1], in, names[j][0], true);
-      check_apart(out, names[j][1], *positions, "positions");
       check_heads(in.sizes[in.rank - 2]);
       nothing = nothing || in.sizes[in.rank - 3] == 0 || in.sizes[in.rank - 1] == 0 || in.sizes[0] == 0;
       p.s[p.n_streams++] = rope_stream(in, out, true, false);
@@ -354,6 +354,8 @@ extern "C" cmd_status cmd_rope(const cmd_operand* q, const cmd_operand* q_out, c
     check(*positions, "positions", lead);
     check_type(*positions, "positions", CMD_I32);
     check_sizes(*positions, "positions", like->sizes);
+    for (int j = 0; j < 2; ++j)
+      if (ins[j]) check_apart(*outs[j], names[j][1], *positions, "positions");
     const int64_t dim = like->sizes[like->rank - 1];
     NEED(dim <= CMD_CACHE_MAX_DIM, CMD_ERR_LIMIT, "a head dim above 256");
     check_rope(*rope, dim);
@@ -424,6 +426,10 @@ extern "C" cmd_status cmd_cache_append(const cmd_append_args* args, void* cuda_s
     } else {
       NEED(a.tables.sizes[0] == tokens, CMD_ERR_SHAPE, "rows may be absent only where each token has its own table row");
     }
+    if (has_q) {
+      check(a.q, "q", 3, true);
+      check(a.q_out, "q_out", 3, true);
+    }
     check_rope(a.rope, dim);
     check_distinct(a.k_cache, "k_cache");
     check_distinct(a.v_cache, "v_cache");
@@ -439,8 +445,6 @@ extern "C" cmd_status cmd_cache_append(const cmd_append_args* args, void* cuda_s
     cmdx::RopeParams p;
     std::memset(&p, 0, sizeof p);
     if (has_q) {
-      check(a.q, "q", 3, true);
-      check(a.q_out, "q_out", 3, true);
       NEED(a.rope.n_pairs > 0, CMD_ERR_ARG, "q is given and nothing rotates it");
       check_type(a.q, "q", a.k.dtype);
       check_type(a.q_out, "q_out", a.k.dtype);
