@@ -264,6 +264,10 @@ void rope_common(cmdx::RopeParams& p, const cmd_rope_spec& r, int64_t dim) {
   p.n_streams = n;
 }
 
+void check_status(const int32_t* status) {
+  NEED(reinterpret_cast<uintptr_t>(status) % sizeof(int32_t) == 0, CMD_ERR_ALIGN, "status is not 4-byte aligned");
+}
+
 void check_heads(int64_t heads) { NEED(heads <= 65536, CMD_ERR_LIMIT, "more than 65536 heads"); }
 
 }  // namespace
@@ -405,6 +409,7 @@ extern "C" cmd_status cmd_cache_append(const cmd_append_args* args, void* cuda_s
   return guarded([&]() -> cmd_status {
     NEED(args, CMD_ERR_NULL, "args is NULL");
     const cmd_append_args& a = *args;
+    check_status(a.status);
     check(a.k, "k", 3, true);
     check(a.v, "v", 3, true);
     check_cache(a.k_cache, a.v_cache, a.tables);
@@ -517,6 +522,7 @@ extern "C" cmd_status cmd_attention_decode(const cmd_attention_args* args, void*
   return guarded([&]() -> cmd_status {
     NEED(args, CMD_ERR_NULL, "args is NULL");
     const cmd_attention_args& a = *args;
+    check_status(a.status);
     check(a.q, "q", 3, true);
     check(a.out, "out", 3, true);
     check_cache(a.k_cache, a.v_cache, a.tables);
@@ -702,6 +708,7 @@ extern "C" cmd_status cmd_cache_select(const cmd_select_args* args, void* cuda_s
   return guarded([&]() -> cmd_status {
     NEED(args, CMD_ERR_NULL, "args is NULL");
     const cmd_select_args& a = *args;
+    check_status(a.status);
     check_ints(a.tables, "tables", 2);
     check_ints(a.tables_out, "tables_out", 2);
     const int64_t old_rows = a.tables.sizes[0], new_rows = a.tables_out.sizes[0], columns = a.tables.sizes[1];
@@ -782,6 +789,7 @@ extern "C" cmd_status cmd_cache_compact(const cmd_compact_args* args, void* cuda
   return guarded([&]() -> cmd_status {
     NEED(args, CMD_ERR_NULL, "args is NULL");
     const cmd_compact_args& a = *args;
+    check_status(a.status);
     check_ints(a.tables, "tables", 2);
     check_ints(a.tables_out, "tables_out", 2);
     check_sizes(a.tables_out, "tables_out", a.tables.sizes);
@@ -837,6 +845,7 @@ extern "C" cmd_status cmd_cache_compact(const cmd_compact_args* args, void* cuda
 extern "C" cmd_status cmd_cache_status(int32_t* status, int32_t* bits, void* cuda_stream) {
   return guarded([&]() -> cmd_status {
     NEED(status, CMD_ERR_NULL, "status is NULL");
+    check_status(status);
     const cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
     int32_t word = 0;
     cudaError_t e = cudaMemcpyAsync(&word, status, sizeof word, cudaMemcpyDeviceToHost, stream);

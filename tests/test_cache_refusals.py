@@ -66,3 +66,31 @@ def test_a_rank_is_checked_before_the_sizes_are_walked():
     a = _append()
     a.q_out.rank = 8
     refuses("cmd_cache_append", (ctypes.byref(a), None), "CMD_ERR_SHAPE", "q_out has rank 8")
+
+
+def _attention(**kw):
+    a = C.cmd_attention_args(q=op(3, 4, 16), out=op(3, 4, 16), k_cache=op(9, 4, 2, 16), v_cache=op(9, 4, 2, 16), tables=i32(3, 5),
+                             lengths=i32(3), scale=0.25, workspace=next(_at), workspace_bytes=1 << 30)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+def _pooled(kind, rows=4, **kw):
+    common = dict(tables=i32(rows, 0), lengths=i32(rows), refs=i32(20), refs_out=i32(20), page_size=8, workspace=next(_at), workspace_bytes=1 << 40)
+    if kind == "select":
+        a = C.cmd_select_args(parents=i32(5), tables_out=i32(5, 0), lengths_out=i32(5), **common)
+    else:
+        a = C.cmd_compact_args(tables_out=i32(rows, 0), page_map_out=i32(20), **common)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("name,make", [
+    ("cmd_cache_append", _append), ("cmd_attention_decode", _attention), ("cmd_cache_select", lambda **kw: _pooled("select", **kw)),
+    ("cmd_cache_compact", lambda **kw: _pooled("compact", **kw))])
+def test_a_status_word_off_its_alignment_is_refused(name, make):
+    """(The kernels set its bits with 4-byte atomics.)"""
+    refuses(name, (ctypes.byref(make(status=(1 << 39) + 2)), None), "CMD_ERR_ALIGN", "status")
+    refuses("cmd_cache_status", ((1 << 39) + 2, None, None), "CMD_ERR_ALIGN", "status")
