@@ -176,7 +176,9 @@ cmd_status cmd_attention_decode(const cmd_attention_args* args, void* cuda_strea
 
 /* ---- pages ---------------------------------------------------------------------- */
 
-/* The pools of a select or compact call: each n_pages pages of page_bytes
+/* Rows and pages of a select or compact call number at most 2^30 each.
+ *
+ * The pools of a call: each n_pages pages of page_bytes
  * bytes, page_stride bytes apart (>= page_bytes), the bytes of a page dense. */
 typedef struct cmd_pool {
   void* ptr;

@@ -675,6 +675,10 @@ void check_pools(const cmdx::PoolList& l, int64_t pages) {
     }
 }
 
+// Rows and pages of a select or compact call, whose kernels step through them
+// in 32 bits.
+constexpr int64_t kMostRows = 1 << 30, kMostPages = 1 << 30;
+
 constexpr int64_t kHeadWords = 16;
 int64_t padded(int64_t words) { return round_up(words, 4); }
 int64_t select_words(int64_t old_rows, int64_t new_rows, int64_t pages) {
@@ -713,6 +717,7 @@ extern "C" cmd_status cmd_cache_select(const cmd_select_args* args, void* cuda_s
     check_ints(a.tables_out, "tables_out", 2);
     const int64_t old_rows = a.tables.sizes[0], new_rows = a.tables_out.sizes[0], columns = a.tables.sizes[1];
     NEED(a.tables_out.sizes[1] == columns, CMD_ERR_SHAPE, "tables and tables_out differ in columns");
+    NEED(old_rows <= kMostRows && new_rows <= kMostRows, CMD_ERR_LIMIT, "more than 2^30 rows");
     check_distinct(a.tables_out, "tables_out");
     check_ints(a.lengths, "lengths", 1);
     check_sizes(a.lengths, "lengths", &old_rows);
@@ -728,7 +733,7 @@ extern "C" cmd_status cmd_cache_select(const cmd_select_args* args, void* cuda_s
     const int64_t pages = a.refs.sizes[0];
     check_ints(a.refs_out, "refs_out", 1);
     check_sizes(a.refs_out, "refs_out", &pages);
-    NEED(pages <= 0x40000000, CMD_ERR_LIMIT, "more than 2^30 pages");
+    NEED(pages <= kMostPages, CMD_ERR_LIMIT, "more than 2^30 pages");
     NEED(a.page_size >= 1, CMD_ERR_SHAPE, "a page holds no token");
     NEED((__int128)columns * a.page_size <= 0x7fff0000, CMD_ERR_LIMIT, "table rows that reach past 2^31 - 2^16 tokens");
     const cmdx::PoolList pools = pool_list(a.pools, a.n_pools, pages);
@@ -793,6 +798,7 @@ extern "C" cmd_status cmd_cache_compact(const cmd_compact_args* args, void* cuda
     check_ints(a.tables, "tables", 2);
     check_ints(a.tables_out, "tables_out", 2);
     check_sizes(a.tables_out, "tables_out", a.tables.sizes);
+    NEED(a.tables.sizes[0] <= kMostRows, CMD_ERR_LIMIT, "more than 2^30 rows");
     check_distinct(a.tables_out, "tables_out");
     check_ints(a.lengths, "lengths", 1);
     check_sizes(a.lengths, "lengths", &a.tables.sizes[0]);
@@ -802,7 +808,7 @@ extern "C" cmd_status cmd_cache_compact(const cmd_compact_args* args, void* cuda
     check_sizes(a.refs_out, "refs_out", &pages);
     check_ints(a.page_map_out, "page_map_out", 1);
     check_sizes(a.page_map_out, "page_map_out", &pages);
-    NEED(pages <= 0x40000000, CMD_ERR_LIMIT, "more than 2^30 pages");
+    NEED(pages <= kMostPages, CMD_ERR_LIMIT, "more than 2^30 pages");
     NEED(a.page_size >= 1, CMD_ERR_SHAPE, "a page holds no token");
     NEED((__int128)columns * a.page_size <= 0x7fff0000, CMD_ERR_LIMIT, "table rows that reach past 2^31 - 2^16 tokens");
     const cmdx::PoolList pools = pool_list(a.pools, a.n_pools, pages);

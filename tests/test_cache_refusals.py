@@ -94,3 +94,13 @@ def test_a_status_word_off_its_alignment_is_refused(name, make):
     """(The kernels set its bits with 4-byte atomics.)"""
     refuses(name, (ctypes.byref(make(status=(1 << 39) + 2)), None), "CMD_ERR_ALIGN", "status")
     refuses("cmd_cache_status", ((1 << 39) + 2, None, None), "CMD_ERR_ALIGN", "status")
+
+
+@pytest.mark.parametrize("kind", ["select", "compact"])
+def test_rows_that_pass_the_kernels_counters_are_refused(kind):
+    """The kernels step through rows in 32 bits, thousands at a time; a table of no columns may have any number."""
+    many, rows = (1 << 30) + 1, "rows"
+    refuses(f"cmd_cache_{kind}", (ctypes.byref(_pooled(kind, rows=many)), None), "CMD_ERR_LIMIT", rows)
+    if kind == "select":
+        a = _pooled(kind, parents=i32(many), tables_out=i32(many, 0), lengths_out=i32(many))
+        refuses("cmd_cache_select", (ctypes.byref(a), None), "CMD_ERR_LIMIT", rows)
