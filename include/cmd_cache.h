@@ -243,9 +243,11 @@ typedef struct cmd_compact_args {
 cmd_status cmd_compact_workspace(int64_t pages, int64_t* bytes);
 cmd_status cmd_cache_compact(const cmd_compact_args* args, void* cuda_stream);
 
-/* Wait for cuda_stream, read the status word and clear it: CMD_OK for 0, else
- * CMD_ERR_ARG for BAD_PAGE or BAD_INDEX and CMD_ERR_LIMIT otherwise, with the
- * bits in *bits (when non-NULL) and a message. */
+/* Wait for cuda_stream, read the status word and clear the bits that it held:
+ * CMD_OK for 0, else CMD_ERR_ARG for BAD_PAGE or BAD_INDEX and CMD_ERR_LIMIT
+ * otherwise, with the bits in *bits (when non-NULL) and a message. A word may
+ * serve several streams: bits that work on another one sets meanwhile stay for
+ * the next call. */
 cmd_status cmd_cache_status(int32_t* status, int32_t* bits, void* cuda_stream);
 
 #ifdef __cplusplus

@@ -857,7 +857,7 @@ extern "C" cmd_status cmd_cache_status(int32_t* status, int32_t* bits, void* cud
     cudaError_t e = cudaMemcpyAsync(&word, status, sizeof word, cudaMemcpyDeviceToHost, stream);
     if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
     if (e == cudaSuccess && word) {
-      e = cudaMemsetAsync(status, 0, sizeof word, stream);
+      e = cmdx::status_clear_launch(status, word, stream);
       if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
     }
     if (e != cudaSuccess) return launched(e);

@@ -154,6 +154,7 @@ struct CompactParams {
 };
 
 cudaError_t select_launch(const SelectParams& p, const PoolList& pools, cudaStream_t stream);
+cudaError_t status_clear_launch(int32_t* status, int32_t bits, cudaStream_t stream);
 cudaError_t compact_launch(const CompactParams& p, const PoolList& pools, cudaStream_t stream);
 
 }  // namespace cmdx

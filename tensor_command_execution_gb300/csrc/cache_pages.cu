@@ -453,6 +453,14 @@ __global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(kTeamThreads)
 // 14.8, 6000 pages 16.5 and 15.4; of 509 rows among 6300 pages 54.5 and 41.7.
 constexpr int kLargePool = 4096, kManyRows = 256;
 
+// Takes bits off the status word that were read from it, and no others: an
+// operator on another stream may have set some since.
+__global__ void status_clear_kernel(int32_t* status, int32_t bits) {
+  wait_for_previous();
+  let_next_start();
+  atomicAnd(status, ~bits);
+}
+
 template <class P, class L>
 cudaError_t run(void (*plan)(P), int ctas, void (*apply)(P, L), const P& p, const PoolList& pools, cudaStream_t stream) {
   cudaError_t e = launch_chained(plan, ctas, kTeamThreads, 0, stream, p);
@@ -491,6 +499,10 @@ cudaError_t select_launch(const SelectParams& p, const PoolList& pools, cudaStre
   return by_unit(pools, [&](auto u, auto l) {
     return run(plan, !few || large ? 8 : 1, select_apply_kernel<decltype(u), decltype(l)>, p, pools, stream);
   });
+}
+
+cudaError_t status_clear_launch(int32_t* status, int32_t bits, cudaStream_t stream) {
+  return launch_chained(status_clear_kernel, 1, 1, 0, stream, status, bits);
 }
 
 cudaError_t compact_launch(const CompactParams& p, const PoolList& pools, cudaStream_t stream) {
