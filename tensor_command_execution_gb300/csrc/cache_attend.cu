@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kWarps * 32) attend_simt_kernel(const __grid_c
       inside = i < g.tiles && token >= g.lo && token < g.n;
       const uint32_t column = fast_div32(p.page, (uint32_t)token);
       slot = token - (int)(column * p.page.d);
-      if (inside) page = __ldg(table + column * p.table_st[1]);
+      if (inside) page = table[column * p.table_st[1]];
     };
     look_up(0);
     for (int i = 0; i < g.tiles; ++i) {

@@ -97,7 +97,7 @@ struct AttendRing {
     const uint32_t column = fast_div32(p.page, (uint32_t)token);
     slot = token - (int)(column * p.page.d);
     inside = token >= look.lo && token < look.n;
-    if (inside) page = __ldg(table + column * p.table_st[1]);
+    if (inside) page = table[column * p.table_st[1]];
     ++look_at;
   }
 
