@@ -7,7 +7,8 @@ attention of one new token per sequence (``attention_decode``), the selection of
 A cache is a pair of tensors [pages, page_size, kv_heads, dim] of any strides with a unit stride along dim: pages
 stored with their heads outermost are passed as ``pool.transpose(1, 2)``. Tables, lengths, positions and counts are
 int32. Outputs are allocated where none are given. ``stream`` is a torch.cuda.Stream, a raw handle, or None for
-torch's current stream; inputs must be ready on it, and outputs and workspaces are allocated for it.
+torch's current stream; inputs must be ready on it, and outputs and workspaces are allocated for it. Tensors of other
+streams may be dropped as soon as a call returns.
 
 Tensors are described to the library by a small native module (csrc/cache_torch.cpp), built with it; the ``cmd_*``
 functions and structures here mirror the C entry points for callers with raw pointers.
@@ -144,12 +145,25 @@ def _native():
     return _module
 
 
-def _on(stream, like):
-    """A context in which `stream` is the current stream of `like`'s device."""
-    import torch
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), like.device)
-    return torch.cuda.stream(stream)
+class _On:
+    """`stream` as the current stream of `like`'s device while a call is made. Tensors that it uses and that belong to
+    another stream stay allocated until the work is done, however soon the caller drops them."""
+
+    def __init__(self, stream, like, *used):
+        import torch
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), like.device)
+        self.stream, self.current, self.used = stream, torch.cuda.stream(stream), (like, *used)
+
+    def __enter__(self):
+        self.current.__enter__()
+
+    def __exit__(self, kind, error, trace):
+        if kind is None:
+            for x in self.used:
+                if getattr(x, "is_cuda", False):
+                    x.record_stream(self.stream)
+        return self.current.__exit__(kind, error, trace)
 
 
 def _layout(layout):
@@ -176,7 +190,7 @@ def rope_turns(rotated: int, base: float = 10000.0, *, scaling: str = "none", fa
 def _rope(q, k, positions, turns, layout, scale, out, stream, backward):
     q_out, k_out = (None, None) if out is None else out
     if stream is not None:
-        with _on(stream, q if q is not None else k):
+        with _On(stream, q if q is not None else k, k, positions, turns, q_out, k_out):
             return _native().rope(q, k, positions, turns, _layout(layout), scale, q_out, k_out, backward)
     return (_module or _native()).rope(q, k, positions, turns, _layout(layout), scale, q_out, k_out, backward)
 
@@ -197,7 +211,7 @@ def cache_append(k, v, k_cache, v_cache, tables, positions, *, rows=None, q=None
     """Store each token's key, rotated where turns is given, and value in its page; returns q rotated (None without
     q). rows: each token's table row (None: token t has row t)."""
     if stream is not None:
-        with _on(stream, k):
+        with _On(stream, k, v, k_cache, v_cache, tables, positions, rows, q, q_out, turns, status):
             return cache_append(k, v, k_cache, v_cache, tables, positions, rows=rows, q=q, q_out=q_out, turns=turns,
                                 layout=layout, scale=scale, status=status)
     return (_module or _native()).cache_append(k, v, k_cache, v_cache, tables, positions, rows, q, q_out, turns,
@@ -211,7 +225,7 @@ def attention_decode(q, k_cache, v_cache, tables, lengths, *, scale: float | Non
     out, or (out, lse) with return_lse. scale: dim ** -0.5 unless given. workspace: cmd_attention_workspace bytes
     (allocated where None)."""
     if stream is not None:
-        with _on(stream, q):
+        with _On(stream, q, k_cache, v_cache, tables, lengths, out, lse, workspace, status):
             return attention_decode(q, k_cache, v_cache, tables, lengths, scale=scale, softcap=softcap, window=window,
                                     out=out, lse=lse, return_lse=return_lse, workspace=workspace, status=status)
     return (_module or _native()).attention_decode(q, k_cache, v_cache, tables, lengths, scale, softcap, window, out, lse,
@@ -224,7 +238,7 @@ def cache_select(tables, lengths, refs, parents, pools, *, page_size: int, grow=
     are copied in every pool for later children. pools: tensors [pages, ...] whose pages are dense. Returns (tables,
     lengths, refs); out: those three, to write to."""
     if stream is not None:
-        with _on(stream, tables):
+        with _On(stream, tables, lengths, refs, parents, *pools, grow, *(out or ()), status):
             return cache_select(tables, lengths, refs, parents, pools, page_size=page_size, grow=grow, out=out, status=status)
     return (_module or _native()).cache_select(tables, lengths, refs, parents, pools, page_size, grow, out, status)
 
@@ -232,7 +246,7 @@ def cache_select(tables, lengths, refs, parents, pools, *, page_size: int, grow=
 def cache_compact(tables, lengths, refs, pools, *, page_size: int, out=None, status=None, stream=None):
     """The pages in use moved to the front of every pool. Returns (tables, refs, page_map); out: those three."""
     if stream is not None:
-        with _on(stream, tables):
+        with _On(stream, tables, lengths, refs, *pools, *(out or ()), status):
             return cache_compact(tables, lengths, refs, pools, page_size=page_size, out=out, status=status)
     return (_module or _native()).cache_compact(tables, lengths, refs, pools, page_size, out, status)
 
@@ -241,6 +255,6 @@ def cache_status(status, stream=None) -> None:
     """Wait for the stream and raise CmdError if an operator given this status word met an invalid table or index, or
     had no room; the word is cleared."""
     if stream is not None:
-        with _on(stream, status):
+        with _On(stream, status):
             return cache_status(status)
     (_module or _native()).cache_status(status)
