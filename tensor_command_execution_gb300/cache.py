@@ -10,6 +10,9 @@ int32. Outputs are allocated where none are given. ``stream`` is a torch.cuda.St
 torch's current stream; inputs must be ready on it, and outputs and workspaces are allocated for it. Tensors of other
 streams may be dropped as soon as a call returns.
 
+The rotation is part of autograd. The operators on a cache are for serving: their results carry no gradient, whatever
+their inputs require. Autograd is told of every tensor that an operator writes.
+
 Tensors are described to the library by a small native module (csrc/cache_torch.cpp), built with it; the ``cmd_*``
 functions and structures here mirror the C entry points for callers with raw pointers.
 """
@@ -187,22 +190,63 @@ def rope_turns(rotated: int, base: float = 10000.0, *, scaling: str = "none", fa
     return torch.tensor([x - (1 << 64) if x >> 63 else x for x in w], dtype=torch.int64).to(device)
 
 
+_function = None
+
+
+def _recorded():
+    """The rotation as a function of autograd: linear, so that its gradient is the transposed rotation."""
+    global _function
+    if _function is None:
+        import torch
+
+        class Rope(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, q, k, positions, turns, layout, scale, backward):
+                ctx.save_for_backward(positions, turns)
+                ctx.call = layout, scale, backward
+                ctx.set_materialize_grads(False)
+                got = (_module or _native()).rope(q, k, positions, turns, _layout(layout), scale, None, None, backward)
+                ctx.mark_non_differentiable(*(y for y, needed in zip(got, ctx.needs_input_grad) if y is not None and not needed))
+                return got
+
+            @staticmethod
+            def backward(ctx, *grads):
+                # (the kernels read rows of unit stride: a sum's gradient has none)
+                grads = [None if g is None or not needed else g if g.stride(-1) == 1 or g.shape[-1] < 2 else g.contiguous()
+                         for g, needed in zip(grads, ctx.needs_input_grad)]
+                if all(g is None for g in grads):
+                    return (None,) * 7
+                positions, turns = ctx.saved_tensors
+                layout, scale, backward = ctx.call
+                return (*_rope(*grads, positions, turns, layout, scale, None, None, not backward), *(None,) * 5)
+        _function = Rope
+    return _function
+
+
 def _rope(q, k, positions, turns, layout, scale, out, stream, backward):
     q_out, k_out = (None, None) if out is None else out
     if stream is not None:
         with _On(stream, q if q is not None else k, k, positions, turns, q_out, k_out):
-            return _native().rope(q, k, positions, turns, _layout(layout), scale, q_out, k_out, backward)
+            return _rope(q, k, positions, turns, layout, scale, out, None, backward)
+    if getattr(q, "requires_grad", False) or getattr(k, "requires_grad", False):
+        import torch
+        if torch.is_grad_enabled():
+            if out is not None:
+                raise ValueError("out= records no gradient: q or k requires one")
+            return _recorded().apply(q, k, positions, turns, layout, scale, backward)
     return (_module or _native()).rope(q, k, positions, turns, _layout(layout), scale, q_out, k_out, backward)
 
 
 def rope(q, k, positions, turns, *, layout: str = "half", scale: float = 1.0, out=None, stream=None):
     """q and k ([batch,] tokens, heads, dim; either may be None) rotated by their positions, as (q, k). out: the pair
-    of outputs (the inputs themselves: in place)."""
+    of outputs (the inputs themselves: in place). Autograd records the call where an input requires a gradient (out= is
+    refused then)."""
     return _rope(q, k, positions, turns, layout, scale, out, stream, False)
 
 
 def rope_backward(dq, dk, positions, turns, *, layout: str = "half", scale: float = 1.0, out=None, stream=None):
-    """The gradients of rope's inputs from those of its outputs."""
+    """The gradients of rope's inputs from those of its outputs (for programs that keep their own graph; recorded by
+    autograd as rope is)."""
     return _rope(dq, dk, positions, turns, layout, scale, out, stream, True)
 
 

@@ -6,6 +6,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -120,6 +121,20 @@ void same_device(const Where& w, PyObject* o, const char* name) {
     raise(PyExc_ValueError, std::string(name) + " is on another GPU");
 }
 
+// A tensor that a call is to write, where one is given: autograd keeps no record
+// of it, so none may be asked for.
+void writable(PyObject* o, const char* name) {
+  if (o != Py_None && at::GradMode::is_enabled() && tensor(o, name).requires_grad())
+    raise(PyExc_ValueError, std::string(name) + " is written and requires a gradient: none would be recorded");
+}
+// Tells autograd that a tensor was written: gradients that need what it held are
+// refused.
+void written(PyObject* o) {
+  if (o == Py_None) return;
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 PyObject* wrap(const at::Tensor& t) {
   PyObject* o = THPVariable_Wrap(t);
   if (!o) throw Raised{};
@@ -181,9 +196,13 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const cmd_rope_spec r = rope_spec(a[3], a[4], a[5], PyObject_IsTrue(a[8]));
     same_device(w, a[3], "turns");
     const bool q = a[0] != Py_None, k = a[1] != Py_None;
+    if (q) writable(a[6], "out");
+    if (k) writable(a[7], "out");
     check(cmd_rope(q ? &in[0] : nullptr, q ? &out[0] : nullptr, k ? &in[1] : nullptr, k ? &out[1] : nullptr, &positions, &r,
                    w.stream),
           "cmd_rope");
+    if (q) written(a[6]);
+    if (k) written(a[7]);
     return pack({q ? result(a[6], made[0]) : none(), k ? result(a[7], made[1]) : none()});
   });
 }
@@ -212,7 +231,12 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     same_device(w, a[12], "status");
     const char* names[] = {"k", "v", "k_cache", "v_cache", "tables", "positions", "rows", "q", "q_out", "turns"};
     for (int i = 0; i < 10; ++i) same_device(w, a[i], names[i]);
+    const int outs[] = {2, 3, 8};
+    for (int i : outs)
+      if (i != 8 || a[7] != Py_None) writable(a[i], names[i]);
     check(cmd_cache_append(&x, w.stream), "cmd_cache_append");
+    for (int i : outs)
+      if (i != 8 || a[7] != Py_None) written(a[i]);
     return a[7] == Py_None ? none() : result(a[8], made);
   });
 }
@@ -259,7 +283,11 @@ PyObject* py_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     same_device(w, a[8], "out");
     same_device(w, a[9], "lse");
     same_device(w, a[11], "workspace");
+    writable(a[8], "out");
+    writable(a[9], "lse");
     check(cmd_attention_decode(&x, w.stream), "cmd_attention_decode");
+    written(a[8]);
+    written(a[9]);
     PyObject* o = result(a[8], out);
     return with_lse ? pack({o, result(a[9], lse)}) : o;
   });
@@ -276,6 +304,7 @@ int pools(PyObject* list, int64_t pages, const Where& w, cmd_pool* out) {
     PyObject* o = tuple ? PyTuple_GET_ITEM(list, i) : PyList_GET_ITEM(list, i);
     const at::Tensor& t = tensor(o, "a pool");
     same_device(w, o, "a pool");
+    writable(o, "a pool");
     const int64_t rank = t.dim();
     if (rank < 1 || t.size(0) != pages)
       raise(PyExc_ValueError,
@@ -298,6 +327,12 @@ int pools(PyObject* list, int64_t pages, const Where& w, cmd_pool* out) {
     out[i].page_stride = (pages > 1 ? t.stride(0) : block) * es;
   }
   return (int)n;
+}
+
+void pools_written(PyObject* list) {
+  const bool tuple = PyTuple_Check(list);
+  const Py_ssize_t n = tuple ? PyTuple_GET_SIZE(list) : PyList_GET_SIZE(list);
+  for (Py_ssize_t i = 0; i < n; ++i) written(tuple ? PyTuple_GET_ITEM(list, i) : PyList_GET_ITEM(list, i));
 }
 
 // Item i of a given tuple of outputs (None where none was given).
@@ -347,6 +382,8 @@ PyObject* py_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
     for (int i = 0; i < 4; ++i) same_device(w, a[i], names[i]);
     same_device(w, a[6], "grow");
     check(cmd_cache_select(&x, w.stream), "cmd_cache_select");
+    for (PyObject* o : out) written(o);
+    pools_written(a[4]);
     return pack({result(out[0], made[0]), result(out[1], made[1]), result(out[2], made[2])});
   });
 }
@@ -380,6 +417,8 @@ PyObject* py_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const char* names[] = {"tables", "lengths", "refs"};
     for (int i = 0; i < 3; ++i) same_device(w, a[i], names[i]);
     check(cmd_cache_compact(&x, w.stream), "cmd_cache_compact");
+    for (PyObject* o : out) written(o);
+    pools_written(a[3]);
     return pack({result(out[0], made[0]), result(out[1], made[1]), result(out[2], made[2])});
   });
 }
