@@ -212,8 +212,8 @@ def _recorded():
             @staticmethod
             def backward(ctx, *grads):
                 # (the kernels read rows of unit stride: a sum's gradient has none)
-                grads = [None if g is None or not needed else g if g.stride(-1) == 1 or g.shape[-1] < 2 else g.contiguous()
-                         for g, needed in zip(grads, ctx.needs_input_grad)]
+                grads = [g.resolve_neg() if g is not None and needed else None for g, needed in zip(grads, ctx.needs_input_grad)]
+                grads = [g if g is None or g.stride(-1) == 1 or g.shape[-1] < 2 else g.contiguous() for g in grads]
                 if all(g is None for g in grads):
                     return (None,) * 7
                 positions, turns = ctx.saved_tensors

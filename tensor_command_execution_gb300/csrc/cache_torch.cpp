@@ -71,6 +71,7 @@ cmd_operand describe(const at::Tensor& t, const char* name) {
     case at::kInt: x.dtype = CMD_I32; break;
     default: raise(PyExc_TypeError, std::string(name) + " is not float32, float16, bfloat16 or int32");
   }
+  if (t.is_neg()) raise(PyExc_ValueError, std::string(name) + " is a view of negated numbers (resolve_neg() makes them so)");
   const int64_t rank = t.dim();
   if (rank > CMD_MAX_RANK) raise(PyExc_ValueError, std::string(name) + " has more than 4 dims");
   x.rank = (int32_t)rank;

@@ -99,3 +99,9 @@ def test_autograd_hears_of_what_is_written():
     with torch.inference_mode():  # (tensors without a version)
         z = torch.zeros(2, 2, 16, device="cuda")
         assert T.rope(z, None, pos, turns, out=(z, None))[0] is z
+
+
+def test_views_that_hold_negated_numbers_are_refused():
+    x = torch._neg_view(_randn(4, 2, 16))
+    with pytest.raises(ValueError, match="negat"):
+        T.rope(x, None, POS[0].cuda(), T.rope_turns(16))
