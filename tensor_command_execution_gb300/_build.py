@@ -1,4 +1,4 @@
-"""Build the CUDA executor library (libcmdexec.so) in-tree, and the module that hands torch tensors to it.
+"""Build the CUDA executor library (libcmdexec.so) in-tree, and the module that hands torch tensors to its cache operators.
 
 Each executor source compiles once per tier and op-set variant
 (CMDX_TIER, CMDX_EXT; the tile executor also per view variant, CMDX_ND):
@@ -24,9 +24,19 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 OBJ_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libcmdexec.so")
-# (torch's C++ interface holds for one version of it; without torch the module is not built)
 TORCH = importlib.util.find_spec("torch") is not None
-TORCH_PATH = os.path.join(OUT_DIR, f"_cache_torch-{importlib.metadata.version('torch') if TORCH else 'none'}.so")
+
+
+def _torch_version() -> str:
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        return "unknown"
+
+
+# (torch's C++ interface holds for one version of it)
+TORCH_PATH = os.path.join(OUT_DIR, f"_cache_torch-{_torch_version() if TORCH else 'none'}.so")
+
 
 # (source, the defines of each object built from it), longest compiles first
 def _objs(tiers, nds=(None,)):
@@ -75,11 +85,55 @@ def _sources():
 
 
 def up_to_date() -> bool:
-    made = [LIB_PATH] + [TORCH_PATH] * TORCH
-    if not all(os.path.exists(m) for m in made):
+    if not os.path.exists(LIB_PATH):
         return False
-    t = min(os.path.getmtime(m) for m in made)
+    t = os.path.getmtime(LIB_PATH)
     return all(os.path.getmtime(s) <= t for s in _sources())
+
+
+def _module_compile() -> str:
+    """Compiles the module for torch tensors; returns its object file."""
+    obj = os.path.join(OBJ_DIR, TORCH_SOURCE + ".o")
+    torch_dir = _torch_dir()
+    os.makedirs(OBJ_DIR, exist_ok=True)
+    _step(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c", os.path.join(CSRC, TORCH_SOURCE), "-o", obj,
+           "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(torch_dir, "include"),
+           "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           "-I" + os.path.join(cuda_home(), "include"), "-I" + os.path.join(ROOT, "include")])
+    return obj
+
+
+def _module_link(obj: str) -> None:
+    tmp = TORCH_PATH + f".tmp{os.getpid()}"
+    _step(["g++", "-shared", "-o", tmp, obj, "-L" + os.path.join(_torch_dir(), "lib"), "-L" + OUT_DIR, "-ltorch_python",
+           "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-l:libcmdexec.so", "-Wl,-rpath,$ORIGIN"])
+    os.replace(tmp, TORCH_PATH)
+
+
+def _torch_dir() -> str:
+    return list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+
+
+def _step(cmd: list) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+
+
+def module_path() -> str:
+    """The module that hands torch tensors to the cache operators, built first where it is missing or stale. The
+    library does not depend on it: where it cannot be built (no headers of Python, a torch without CUDA), this is what
+    raises."""
+    build()
+    if not TORCH:
+        raise RuntimeError("the cache operators take torch tensors, and torch is not installed")
+    sources = [os.path.join(CSRC, TORCH_SOURCE), os.path.join(ROOT, "include", "cmd.h"), os.path.join(ROOT, "include", "cmd_cache.h")]
+    if not os.path.exists(TORCH_PATH) or os.path.getmtime(TORCH_PATH) < max(map(os.path.getmtime, sources)):
+        try:
+            _module_link(_module_compile())
+        except Exception as e:
+            raise RuntimeError(f"the cache operators' module for torch tensors could not be built: {e}") from e
+    return TORCH_PATH
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -111,13 +165,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
         cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-Wno-unused-parameter",
                "-c", os.path.join(CSRC, s), "-o", obj] + inc
         jobs.append((cmd, obj, None))
-    torch_obj = os.path.join(OBJ_DIR, TORCH_SOURCE + ".o")
-    if TORCH:
-        torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
-        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c", os.path.join(CSRC, TORCH_SOURCE), "-o",
-               torch_obj, "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(torch_dir, "include"),
-               "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include")] + inc
-        jobs.append((cmd, torch_obj, None))
 
     def run(job):
         cmd, obj, log = job
@@ -131,23 +178,23 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
-        objs = [o for o in ex.map(run, jobs) if o != torch_obj]
+    with ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 1))) as ex:
+        module = ex.submit(_module_compile) if TORCH else None
+        objs = list(ex.map(run, jobs))
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     link = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcudart_static", "-lrt", "-lpthread", "-ldl"]
     r = subprocess.run(link, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed: {' '.join(link)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
-    if not TORCH:
-        return LIB_PATH
-    tmp = TORCH_PATH + f".tmp{os.getpid()}"
-    link = (["g++", "-shared", "-o", tmp, torch_obj, "-L" + os.path.join(torch_dir, "lib"), "-L" + OUT_DIR]
-            + ["-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-l:libcmdexec.so", "-Wl,-rpath,$ORIGIN"])
-    r = subprocess.run(link, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed: {' '.join(link)}\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, TORCH_PATH)
+    if os.path.exists(TORCH_PATH):
+        os.remove(TORCH_PATH)  # (of an older build)
+    if module:
+        try:
+            _module_link(module.result())
+        except Exception as e:  # the first call that needs it tries again, and raises (module_path)
+            if verbose:
+                print(f"the module for torch tensors could not be built: {e}")
     return LIB_PATH
 
 

@@ -135,12 +135,12 @@ _module = None
 
 
 def _native():
-    """The native module, loaded on first use (with the library, which is built when it is missing or stale)."""
+    """The native module, loaded on first use (with the library; both are built when missing or stale)."""
     global _module
     if _module is None:
         import torch  # noqa: F401  (its libraries come first)
         lib()
-        loader = importlib.machinery.ExtensionFileLoader("_cache_torch", _build.TORCH_PATH)
+        loader = importlib.machinery.ExtensionFileLoader("_cache_torch", _build.module_path())
         m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_cache_torch", loader))
         loader.exec_module(m)
         m.set_error(CmdError)
