@@ -81,7 +81,7 @@ typedef enum cmd_rope_layout {
  * copied. turns: n_pairs 64-bit words in device memory, 8-byte aligned. */
 typedef struct cmd_rope_spec {
   const uint64_t* turns;
-  int32_t n_pairs;  /* 0: no rotation (cmd_cache_append only) */
+  int32_t n_pairs;  /* 0: no rotation, a copy (cmd_cache_append: without q) */
   int32_t layout;   /* cmd_rope_layout */
   float scale;
   int32_t backward; /* 1: turn by -t, the gradient of the same call with 0 */
@@ -146,9 +146,9 @@ cmd_status cmd_cache_append(const cmd_append_args* args, void* cuda_stream);
  *
  * The work is split over the sequences' lengths in equal parts and joined
  * through workspace: cmd_attention_workspace bytes of device memory, 16-byte
- * aligned, of any contents, used by one call at a time (streams that overlap
- * need one each). Results do not depend on the timing of the parts. columns *
- * page_size * kv_heads stays below 2^35.
+ * aligned, of any contents, apart from all else of the call, used by one call at
+ * a time (streams that overlap need one each). Results do not depend on the
+ * timing of the parts. columns * page_size * kv_heads stays below 2^35.
  *
  * The weights of 16-bit caches are multiplied with the values as the sum of two
  * 16-bit numbers each: to 2^-16 of itself in bf16 and 2^-22 in f16 (there no
@@ -170,7 +170,8 @@ typedef struct cmd_attention_args {
   int32_t* status;
 } cmd_attention_args;
 
-/* Workspace bytes for any call with at most these heads and this dim (whatever the rows and lengths). */
+/* Workspace bytes for any call with at most q_heads / kv_heads query heads to a kv head and at most this dim (whatever
+ * the number of heads, rows and lengths). */
 cmd_status cmd_attention_workspace(int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t* bytes);
 cmd_status cmd_attention_decode(const cmd_attention_args* args, void* cuda_stream);
 
@@ -178,8 +179,10 @@ cmd_status cmd_attention_decode(const cmd_attention_args* args, void* cuda_strea
 
 /* Rows and pages of a select or compact call number at most 2^30 each.
  *
- * The pools of a call: each n_pages pages of page_bytes
- * bytes, page_stride bytes apart (>= page_bytes), the bytes of a page dense. */
+ * The pools of a call: each as many pages of page_bytes bytes, page_stride bytes
+ * apart (>= page_bytes), the bytes of a page dense. A model with more than
+ * CMD_CACHE_MAX_POOLS of them makes a call for each so many, all with the same
+ * inputs: every call writes the same tables, lengths and counts. */
 typedef struct cmd_pool {
   void* ptr;
   int64_t page_bytes;
@@ -194,11 +197,16 @@ typedef struct cmd_pool {
  *     child whose table has room, and every other child gets a copy in a page
  *     of its own;
  *   - pages for the tokens to come are added up to length + grow[i].
- * New pages are the free ones in ascending order, where a page is free when
- * nothing holds it once the old rows are gone and the new ones hold what they
- * share. Then lengths_out[i] = length + grow[i]; table entries past it are -1.
- * A row that its table or the pool has no room for is dropped: length 0, no
- * pages (status bits FULL_TABLE, NO_PAGES). Counts may include holders outside the tables.
+ * New pages are the free ones in ascending order, dealt out in the order of i,
+ * where a page is free when nothing holds it once the old rows are gone and the
+ * new ones (those that will get none too) hold what they share. Then lengths_out[i] = length + grow[i]; table
+ * entries past it are -1. A row whose table is too short for it is dropped:
+ * length 0, no pages (status bit FULL_TABLE). So is a row whose new pages would
+ * lie past the last free one (NO_PAGES). It keeps its place in the order: rows
+ * after it get the pages after those that it asked for, so that every later row
+ * that needs a new page is dropped too, and those that need none go on. (The old
+ * tables, lengths and counts are as they were: a caller may free rows and select
+ * anew from them.) Counts may include holders outside the tables.
  * workspace: cmd_select_workspace bytes, 16-byte aligned, of any contents. */
 typedef struct cmd_select_args {
   cmd_operand tables;      /* i32 [old_rows, columns], each row dense */

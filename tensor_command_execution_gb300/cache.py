@@ -279,8 +279,9 @@ def attention_decode(q, k_cache, v_cache, tables, lengths, *, scale: float | Non
 def cache_select(tables, lengths, refs, parents, pools, *, page_size: int, grow=None, out=None, status=None,
                  stream=None):
     """New row i goes on from row parents[i] (-1: an empty row) with room for grow[i] more tokens; pages in progress
-    are copied in every pool for later children. pools: tensors [pages, ...] whose pages are dense. Returns (tables,
-    lengths, refs); out: those three, to write to."""
+    are copied in every pool for later children. pools: up to 64 tensors [pages, ...] whose pages are dense (for more,
+    a call for each 64, with the same inputs). Returns (tables, lengths, refs); out: those three, to write to. When the
+    pool runs out, the first row that gets no page is dropped, and every later one that needs any."""
     if stream is not None:
         with _On(stream, tables, lengths, refs, parents, *pools, grow, *(out or ()), status):
             return cache_select(tables, lengths, refs, parents, pools, page_size=page_size, grow=grow, out=out, status=status)
@@ -288,7 +289,8 @@ def cache_select(tables, lengths, refs, parents, pools, *, page_size: int, grow=
 
 
 def cache_compact(tables, lengths, refs, pools, *, page_size: int, out=None, status=None, stream=None):
-    """The pages in use moved to the front of every pool. Returns (tables, refs, page_map); out: those three."""
+    """The pages in use moved to the front of every pool (up to 64; for more, a call for each 64 with the same inputs).
+    Returns (tables, refs, page_map); out: those three."""
     if stream is not None:
         with _On(stream, tables, lengths, refs, *pools, *(out or ()), status):
             return cache_compact(tables, lengths, refs, pools, page_size=page_size, out=out, status=status)

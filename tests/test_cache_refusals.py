@@ -104,3 +104,12 @@ def test_rows_that_pass_the_kernels_counters_are_refused(kind):
     if kind == "select":
         a = _pooled(kind, parents=i32(many), tables_out=i32(many, 0), lengths_out=i32(many))
         refuses("cmd_cache_select", (ctypes.byref(a), None), "CMD_ERR_LIMIT", rows)
+
+
+def test_a_workspace_serves_what_the_header_says():
+    """Any call with at most as many query heads to a kv head, and at most the dim."""
+    for q, kv, dim in ((32, 8, 128), (32, 32, 64), (16, 1, 256), (48, 3, 80)):
+        mine = C.cmd_attention_workspace(q, kv, dim)
+        for q2, kv2, dim2 in ((64, 64, 16), (64, 16, 64), (32, 1, 200), (7, 7, 256), (4096, 512, 1), (16, 1, 80)):
+            if q2 * kv <= q * kv2 and dim2 <= dim:
+                assert C.cmd_attention_workspace(q2, kv2, dim2) <= mine
