@@ -2,8 +2,9 @@
 
 A one-layer attention model with random weights extends a few prompts of different lengths. The prompts' keys and
 values enter the cache at once; each step then forks, drops and grows the beams' rows (cache_select), stores the new
-tokens (cache_append) and attends to them (attention_decode). Halfway, requests that are done leave, and the pool is
-compacted. Tables, lengths and counts never leave the GPU.
+tokens (cache_append) and attends to them (attention_decode); what is elementwise between them, the beams' scores added
+to their tokens', is a Command on the same stream. Halfway, requests that are done leave, and the pool is compacted.
+Tables, lengths and counts never leave the GPU.
 
     python examples/beam_search.py
 """
@@ -37,6 +38,21 @@ class Model:
     def project(self, tokens):
         x = self.embedding[tokens]
         return ((x @ self.q).view(-1, HEADS, DIM), (x @ self.k).view(-1, KV_HEADS, DIM), (x @ self.v).view(-1, KV_HEADS, DIM))
+
+
+class Scores:
+    """Each beam's score added to those of its tokens: a Command over [beams, vocabulary], the beams' scores broadcast."""
+
+    def __init__(self):
+        c = T.Command()
+        self.tokens, self.beams = c.load_tensor("f32", 2), c.load_tensor("f32", 2)
+        self.out = c.store(c.execute([("add", self.tokens, self.beams)])[0], "f32", 2)
+        self.kernel = c.compile()
+
+    def __call__(self, tokens, beams):
+        out = torch.empty_like(tokens)
+        self.kernel.launch({self.tokens: tokens, self.beams: beams[:, None].expand_as(tokens), self.out: out})
+        return out
 
 
 class Cache:
@@ -75,6 +91,7 @@ def search(model, prompts, beams=4, steps=40, leave=None):
 
     longest = max(len(p) for p in prompts) + steps
     columns = -(-longest // PAGE)
+    add = Scores()
     cache = Cache(pages=len(prompts) * (columns + beams * (steps // PAGE + 2)), columns=columns)
     # the prompts, but their last tokens, enter the cache; then every request is its beams' first
     cache.select(i32([-1] * len(prompts)), i32([len(p) - 1 for p in prompts]))
@@ -95,7 +112,7 @@ def search(model, prompts, beams=4, steps=40, leave=None):
     for step in range(1, steps):
         cache.select(parents.int(), one[: len(parents)])
         history = torch.cat([history[parents] if step > 1 else history, token[:, None]], 1)
-        scores = cache.attend(model, token) + score[:, None]
+        scores = add(cache.attend(model, token), score)
         best = scores.view(len(alive), -1).topk(beams, -1)  # over a request's beams and the vocabulary
         score, token = best.values.flatten(), (best.indices % VOCABULARY).flatten()
         parents = (best.indices // VOCABULARY + beams * torch.arange(len(alive), device="cuda")[:, None]).flatten()
@@ -117,6 +134,7 @@ def search(model, prompts, beams=4, steps=40, leave=None):
     for i, r in enumerate(alive):
         done[r] = [(tokens[b].tolist(), float(score[b])) for b in range(i * beams, (i + 1) * beams)]
     T.cache_status(cache.status)
+    add.kernel.sync()
     return done, cache
 
 
