@@ -83,7 +83,7 @@ void check(const cmd_operand& o, const char* name, int rank, bool has_dim = fals
   NEED(reinterpret_cast<uintptr_t>(o.ptr) % elem_size(o.dtype) == 0, CMD_ERR_ALIGN,
        std::string(name) + " is not aligned to its element size");
   if (has_dim)
-    NEED(o.sizes[rank - 1] <= 1 || o.strides[rank - 1] == 1, CMD_ERR_SHAPE,
+    NEED(o.sizes[rank - 1] <= 1 || o.strides[rank - 1] == 1 || empty(o), CMD_ERR_SHAPE,
          std::string(name) + " needs a unit stride along its last dim");
   last_offset(o, name);
 }

@@ -113,3 +113,16 @@ def test_a_workspace_serves_what_the_header_says():
         for q2, kv2, dim2 in ((64, 64, 16), (64, 16, 64), (32, 1, 200), (7, 7, 256), (4096, 512, 1), (16, 1, 80)):
             if q2 * kv <= q * kv2 and dim2 <= dim:
                 assert C.cmd_attention_workspace(q2, kv2, dim2) <= mine
+
+
+def test_tensors_without_elements_have_any_strides():
+    """Empty views come with the strides of whatever they were cut from: nothing is read through them. (No token, row or
+    page: no launch, and so no GPU needed.)"""
+    q, positions, spec = op(0, 2, 8, strides=(16, 8, 2)), i32(0), _spec()
+    assert C.entry("cmd_rope")(ctypes.byref(q), ctypes.byref(op(0, 2, 8)), None, None, ctypes.byref(positions), ctypes.byref(spec), None) == 0
+    a = _append(k=op(0, 2, 16, strides=(64, 32, 2)), v=op(0, 2, 16, strides=(0, 0, 0)), positions=i32(0), rows=i32(0), q=op(0, 4, 16), q_out=op(0, 4, 16))
+    assert C.entry("cmd_cache_append")(ctypes.byref(a), None) == 0
+    a = _pooled("compact", rows=0, tables=i32(0, 5, strides=(0, 3)), tables_out=i32(0, 5, strides=(1, 2)), refs=i32(0, strides=(2,)), refs_out=i32(0),
+                page_map_out=i32(0))
+    assert C.entry("cmd_cache_compact")(ctypes.byref(a), None) == 0
+    refuses("cmd_cache_compact", (ctypes.byref(_pooled("compact", tables=i32(4, 5, strides=(10, 2)), tables_out=i32(4, 5))), None), "CMD_ERR_SHAPE", "unit stride")
