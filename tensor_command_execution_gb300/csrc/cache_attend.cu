@@ -10,8 +10,8 @@
 // butterfly that leaves each lane one finished score (31 shuffles for 32
 // scores rather than 5 each), where scaling, the cap, the mask and the
 // exponential are then done once. Bound by the latency of its loads, element
-// by element: 64 rows of 4096 tokens of 8 kv heads of 101 (bf16) 559 us with one
-// query head each, 22% of the copy peak, 1117 with eight, which is what an odd
+// by element: 64 rows of 4096 tokens of 8 kv heads of 101 (bf16) 568 us with one
+// query head each, 22% of the copy peak, 1116 with eight, which is what an odd
 // head dim costs (2060 with each token's page looked up where it is read).
 #include "cache_attend.cuh"
 

@@ -13,10 +13,12 @@
 // 4 tokens and 2 neighbouring pieces meet in no bank.
 //
 // Measured: 24 rows of 2999 tokens, 16 kv heads of 128, one query head each
-// 177 us, 6.65 TB/s, 98% of the copy peak; 8 query heads to each of 2 kv heads,
-// 96 rows, 118 us, 74%, bound by the multiply-adds and the reads of queries; 24
-// rows of 1 to 1100 tokens (16 heads of 80, capped, windowed) 19.5 us, 51%,
-// 8 of it the fixed part of two launches.
+// 174 us, 6.80 TB/s, the copy peak; 8 query heads to each of 2 kv heads, 96 rows,
+// 105 us, 83%, with no unit full (multiply-adds 36%, shared memory 46%, issue
+// slots 55%): its 168 registers leave two CTAs of four warps on an SM, too few to
+// cover a tile's dependent steps; 12 query heads, in two blocks that each copy
+// the cache, 198 us, 44%; 24 rows of 1 to 1100 tokens (16 heads of 80, capped,
+// windowed) 19.6 us, 50%, 6 of it the fixed part of two launches.
 #include "cache_attend_ring.cuh"
 
 #ifndef CMDX_COPY

@@ -26,13 +26,14 @@
 // Tokens outside the row are filled with zeros as they are copied, whatever
 // their slots hold.
 //
-// Measured (bf16, 8 kv heads of 128, 64 query heads): 64 rows of 4096 tokens
-// 176.5 us, 6.10 TB/s, 90% of the copy peak (the launch alone 169; its slowest
-// SM ran 8% longer than the mean); 64 rows of 0 to 8192 tokens 48.4 us, 73%;
-// two rows of 393217 and 262147 tokens of 2 kv heads (f16) 113.7 us, 87%; one
-// row of 700, 6.7 us, the latency of one launch. Tensor units 14% busy, issue
-// slots 31%. Rows copied in pieces of 4 bytes: 64 rows of 4096 tokens of dim
-// 100, 263 us, 47%, bound by the number of copies.
+// Measured (8 kv heads of 128, 64 query heads): 64 rows of 4096 tokens 181 us in
+// bf16 and in f16, 5.95 TB/s, 87% of the copy peak (the launch alone 177; its
+// slowest SM ran 10% longer than the mean); 64 rows of 0 to 8192 tokens 49.3 us,
+// 71%; two rows of 393217 and 262147 tokens of 2 kv heads (f16) 115.2 us, 86%; one
+// row of 700, 6.7 us, the latency of one launch. Tensor units 13% busy, issue
+// slots 26%. Dims 136 to 256 in the kernel of 256: 286 to 350 us, 59 to 90%. Rows
+// copied in pieces of 4 bytes: 64 rows of 4096 tokens of dim 100, 241 us, 51%,
+// bound by the number of copies.
 #include "cache_attend_ring.cuh"
 
 #ifndef CMDX_COPY

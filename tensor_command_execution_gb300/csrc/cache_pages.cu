@@ -11,11 +11,13 @@
 // tables and moves the pages: bound by memory, 16 bytes a thread and access
 // with four in flight.
 //
-// Measured: compaction moving 1703 pages of 4 x 64 KB among 7001, 141.8 us,
-// 6.30 TB/s, 93% of the copy peak (the moves alone 6.75 TB/s); selection of
-// 509 rows among 6300 pages, 200 of 4 x 128 KB copied, 41.7 us, 75% (13 us of
-// it the plan, bound by the latency of its steps); 64 beams 8.7 us, 601 pages'
-// compaction 5.8 us, both fixed parts.
+// Measured: compaction moving 1703 pages of 4 x 64 KB among 7001, 143.2 us,
+// 6.24 TB/s, 92% of the copy peak (the moves alone 6.75 TB/s), and 437 pages of
+// 64 x 64 KB, 563 us, 96%; selection of 509 rows among 6300 pages, 200 of 4 x 128
+// KB copied, 41.7 us, 75% (13 us of it the plan, bound by the latency of its
+// steps); 64 beams 8.6 us, 601 pages' compaction 5.7 us, both fixed parts. Pools
+// are gone over one after another: 64 beams on 64 pools of a few copies each take
+// 72.7 us.
 //
 // Only integer atomics are used where threads meet, so the results do not
 // depend on their order (the list of pages to copy has no order of its own:

@@ -15,12 +15,14 @@
 // within the head (in the half layout's rotated part, elements and their
 // partners n_pairs further) and goes over heads.
 //
-// Measured: 4 x 4096 tokens of 40 heads of 128 (bf16) 52.8 us, 6.36 TB/s, 94%
-// of the copy peak (a library copy of as many bytes: 54.0 us), with 70% of the
+// Measured: 4 x 4096 tokens of 40 heads of 128 (bf16) 52.8 us, 6.36 TB/s, 93%
+// of the copy peak (a library copy of as many bytes: 54.0 us), with 69% of the
 // issue slots taken; 3 x 1537 tokens of 24 heads of 80 (f32, 32 rotated) 13.6
 // us, 77%, 2.5 us of it a launch's fixed part; 7 prompts of 1171 tokens into a
-// cache (f16, 24 + 2 x 8 heads of 128) 29.9 us, 83%; one token of 16 rows 3.1
-// us, all of it fixed.
+// cache (f16, 24 + 2 x 8 heads of 128) 30.0 us, 82%; one token of 16 rows 3.1
+// us, all of it fixed. A head is accessed in pieces of one size, so heads of 72
+// take 40.9 us (68%) in 8-byte ones, and with 36 rotated 63.2 (44%) in 4-byte
+// ones, bound by their instructions.
 #include "cache_common.cuh"
 
 namespace cmdx {
