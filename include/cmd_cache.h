@@ -11,7 +11,19 @@
  *   cmd_cache_append      new tokens' keys (rotated) and values into the cache;
  *   cmd_attention_decode  attention of one new token per sequence;
  *   cmd_cache_select      which sequences go on: fork, free, grow, in one step;
- *   cmd_cache_compact     the pages in use moved to the front of the pool.
+ *   cmd_cache_compact     the pages in use moved to the front of the pool;
+ *
+ * where it drafts several tokens ahead and has them checked in one pass:
+ *
+ *   cmd_attention_drafts  attention of a tree of drafted tokens per sequence,
+ *                         and the weight that each cached token gets;
+ *   cmd_draft_path        the branch that agrees with the model's choices;
+ *   cmd_cache_accept      that branch's tokens moved together, the rest dropped;
+ *
+ * and where the cache has a budget:
+ *
+ *   cmd_cache_evict       the tokens of the least weight dropped, those kept
+ *                         moved together.
  *
  * The cache. Two pools of pages, keys and values, each a tensor of logical
  * sizes [pages, page_size, kv_heads, dim] and any strides with a unit stride
@@ -50,13 +62,16 @@ extern "C" {
 #endif
 
 #define CMD_CACHE_MAX_DIM 256  /* head dim of the attention and the rotation */
-#define CMD_CACHE_MAX_POOLS 64 /* pools of one select or compact call */
+#define CMD_CACHE_MAX_POOLS 64 /* pools of one select, compact or accept call */
+#define CMD_CACHE_MAX_LAYERS 32 /* layers of one evict call */
+#define CMD_CACHE_MAX_DRAFTS 256 /* drafted tokens of a sequence */
 
 /* Bits of the device status word. */
 #define CMD_CACHE_BAD_PAGE 1  /* a table entry names no page of the pool; its tokens were skipped */
 #define CMD_CACHE_BAD_INDEX 2 /* a row, parent, position or length outside its range; skipped */
 #define CMD_CACHE_FULL_TABLE 4 /* a row would need more columns than its table has; dropped */
 #define CMD_CACHE_NO_PAGES 8  /* the pool had no free page left for a row; dropped */
+#define CMD_CACHE_SHARED_PAGE 16 /* tokens would move into a page that others hold too; left as they are */
 
 typedef struct cmd_operand {
   void* ptr; /* NULL: absent, where an operand is optional */
@@ -175,6 +190,132 @@ typedef struct cmd_attention_args {
 cmd_status cmd_attention_workspace(int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t* bytes);
 cmd_status cmd_attention_decode(const cmd_attention_args* args, void* cuda_stream);
 
+/* ---- attention of drafted tokens -------------------------------------------------- */
+
+/* The last `drafts` tokens of row r's lengths[r] are guesses, stored in the
+ * cache behind the others in any order that puts a guess behind the one that it
+ * goes on from. parents[r][i] is the draft that draft i goes on from, below i;
+ * -1: the tokens before the drafts; less: draft i is padding. (So is one whose
+ * parent is; a parent of i or above is reported, and its draft padding.) Draft i
+ * sees the lengths[r] - drafts tokens before the drafts, its ancestors and
+ * itself, and with a window those at most window - 1 positions back, where a
+ * draft's position is lengths[r] - drafts + its number of ancestors. Over them,
+ * scores, out and lse are as in cmd_attention_decode, which this is for one
+ * draft. Nothing that a draft does not see enters its output. Padding, and rows
+ * of length 0, give out = 0 and lse = -infinity; so do rows whose length is out
+ * of range or below `drafts` (reported).
+ *
+ * weights, where given, gets the attention that each token of each row received:
+ *   weights[r][h][t] += sum over the drafts and the query heads that read kv
+ *                       head h of exp(s_t - lse),
+ * for the tokens t < lengths[r] that are seen, in 32 bits, in an order that does
+ * not depend on timing. It reaches at least columns * page_size tokens.
+ *
+ * workspace as for cmd_attention_decode, of cmd_drafts_workspace bytes. Limits:
+ * drafts <= CMD_CACHE_MAX_DRAFTS, drafts * q_heads <= 2^20. */
+typedef struct cmd_drafts_args {
+  cmd_operand q, out;           /* [rows, drafts, q_heads, dim], dim <= CMD_CACHE_MAX_DIM */
+  cmd_operand lse;              /* optional: f32 [rows, drafts, q_heads] */
+  cmd_operand k_cache, v_cache; /* [pages, page_size, kv_heads, dim]; kv_heads divides q_heads */
+  cmd_operand tables;           /* i32 [rows, columns] */
+  cmd_operand lengths;          /* i32 [rows], drafts included */
+  cmd_operand parents;          /* i32 [rows, drafts]; absent: each goes on from the one before */
+  cmd_operand weights;          /* optional: f32 [rows, kv_heads, tokens], unit stride along tokens; added to */
+  float scale;                  /* > 0 */
+  float softcap;                /* 0: none */
+  int32_t window;               /* 0: none */
+  int32_t reserved;             /* 0 */
+  void* workspace;
+  int64_t workspace_bytes;
+  int32_t* status;
+} cmd_drafts_args;
+
+/* Workspace bytes for a call with at most these rows, drafts and query heads, q_heads / kv_heads of them to a kv head,
+ * and at most this dim; tokens: columns * page_size where weights are given, else 0. */
+cmd_status cmd_drafts_workspace(int64_t rows, int32_t drafts, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t tokens,
+                                int64_t* bytes);
+cmd_status cmd_attention_drafts(const cmd_drafts_args* args, void* cuda_stream);
+
+/* ---- the accepted branch -------------------------------------------------------- */
+
+/* Walks each row's tree (parents as above) along the model's choices: from draft
+ * 0 (the model's own last choice, say, which needs no check) to the first draft
+ * that goes on from it and whose token is choices[r][0], what the model chooses
+ * after draft 0, and so on. path[r] lists the drafts passed, ascending, then -1;
+ * counts[r] says how many they are, and last[r] what the model chooses after the
+ * last of them. Where draft 0 is no root (parents[r][0] is not -1) nothing is
+ * passed: counts 0, last -1. All i32. */
+typedef struct cmd_path_args {
+  cmd_operand tokens, choices; /* [rows, drafts] */
+  cmd_operand parents;         /* [rows, drafts]; absent: each goes on from the one before */
+  cmd_operand path;            /* [rows, drafts] */
+  cmd_operand counts, last;    /* [rows] */
+  int32_t* status;
+} cmd_path_args;
+
+cmd_status cmd_draft_path(const cmd_path_args* args, void* cuda_stream);
+
+/* Of row r's last `drafts` tokens, keeps those listed in the first counts[r]
+ * entries of path[r] (ascending, each below `drafts`): in every pool the j-th one
+ * moves from its slot to slot lengths[r] - drafts + j, and lengths_out[r] =
+ * lengths[r] - drafts + counts[r]. Pages past that are released (refs_out). Rows
+ * of length 0 stay as they are. A row whose list is not as above, or whose moves
+ * would meet pages that do not exist or write to one that others hold too (refs
+ * above 1), keeps none of its drafts (reported); one shorter than `drafts` stays
+ * as it is (reported). Pools as tensors, since parts of a page move; the same
+ * sizes and element type in all of them; a model with more makes a call for each
+ * CMD_CACHE_MAX_POOLS, with the same inputs. */
+typedef struct cmd_accept_args {
+  cmd_operand tables;       /* i32 [rows, columns], each row dense */
+  cmd_operand lengths;      /* i32 [rows], drafts included; dense (as all vectors here) */
+  cmd_operand refs;         /* i32 [pages] */
+  cmd_operand path;         /* i32 [rows, drafts], each row dense */
+  cmd_operand counts;       /* i32 [rows] */
+  cmd_operand lengths_out;  /* i32 [rows] */
+  cmd_operand refs_out;     /* i32 [pages] */
+  const cmd_operand* pools; /* n_pools of [pages, page_size, kv_heads, dim] (host array, read during the call) */
+  int32_t n_pools;          /* at least 1 */
+  int32_t reserved;         /* 0 */
+  int32_t* status;
+} cmd_accept_args;
+
+cmd_status cmd_cache_accept(const cmd_accept_args* args, void* cuda_stream);
+
+/* ---- eviction --------------------------------------------------------------------- */
+
+/* Holds rows to a budget: of a row of n > budget tokens, each kv head of each
+ * layer keeps the last `recent` tokens and, of those before, the budget - recent
+ * of the largest weights (of equal ones the earliest; NaN counts as less than any
+ * number). They move to the row's first `budget` slots in their order, keys,
+ * values and weights; the weights past them, up to n, become 0. lengths_out[r] =
+ * budget, and pages past it are released (refs_out). Rows of at most budget
+ * tokens stay as they are; so does a row where a page does not exist, or one of
+ * those that it goes on with is held by others too (refs above 1) (reported).
+ * Positions are no longer slots then: keys keep the rotation they were stored
+ * with. All layers have the same sizes and element type; a model with more than
+ * CMD_CACHE_MAX_LAYERS makes a call for each so many, with the same inputs.
+ * workspace: cmd_evict_workspace bytes, 16-byte aligned, of any contents. */
+typedef struct cmd_evict_args {
+  cmd_operand tables;                    /* i32 [rows, columns], each row dense */
+  cmd_operand lengths;                   /* i32 [rows], dense (as all vectors here) */
+  cmd_operand refs;                      /* i32 [pages] */
+  cmd_operand lengths_out;               /* i32 [rows] */
+  cmd_operand refs_out;                  /* i32 [pages] */
+  const cmd_operand *k_caches, *v_caches; /* n_layers of [pages, page_size, kv_heads, dim] (host arrays, as the next) */
+  const cmd_operand* weights;            /* n_layers of f32 [rows, kv_heads, tokens], unit stride along tokens; tokens >=
+                                            columns * page_size */
+  int32_t n_layers;                      /* at least 1 */
+  int32_t budget;                        /* >= recent */
+  int32_t recent;                        /* >= 0 */
+  int32_t reserved;                      /* 0 */
+  void* workspace;
+  int64_t workspace_bytes;
+  int32_t* status;
+} cmd_evict_args;
+
+cmd_status cmd_evict_workspace(int64_t rows, int32_t layers, int32_t kv_heads, int32_t budget, int64_t* bytes);
+cmd_status cmd_cache_evict(const cmd_evict_args* args, void* cuda_stream);
+
 /* ---- pages ---------------------------------------------------------------------- */
 
 /* Rows and pages of a select or compact call number at most 2^30 each.
@@ -252,8 +393,8 @@ cmd_status cmd_compact_workspace(int64_t pages, int64_t* bytes);
 cmd_status cmd_cache_compact(const cmd_compact_args* args, void* cuda_stream);
 
 /* Wait for cuda_stream, read the status word and clear the bits that it held:
- * CMD_OK for 0, else CMD_ERR_ARG for BAD_PAGE or BAD_INDEX and CMD_ERR_LIMIT
- * otherwise, with the bits in *bits (when non-NULL) and a message. A word may
+ * CMD_OK for 0, else CMD_ERR_ARG for BAD_PAGE or BAD_INDEX, CMD_ERR_LIMIT for
+ * FULL_TABLE or NO_PAGES and CMD_ERR_ALIAS for SHARED_PAGE (the first that holds), with the bits in *bits (when non-NULL) and a message. A word may
  * serve several streams: bits that work on another one sets meanwhile stay for
  * the next call. */
 cmd_status cmd_cache_status(int32_t* status, int32_t* bits, void* cuda_stream);

@@ -473,5 +473,5 @@ def spec_scalars(spec: dict, tags: dict) -> dict:
 
 # ---- operators of a paged key-value cache (include/cmd_cache.h) ------------------
 
-from .cache import (attention_decode, cache_append, cache_compact, cache_select, cache_status,  # noqa: E402
-                    rope, rope_backward, rope_turns)
+from .cache import (attention_decode, attention_drafts, cache_accept, cache_append, cache_compact,  # noqa: E402
+                    cache_evict, cache_select, cache_status, draft_path, rope, rope_backward, rope_turns)

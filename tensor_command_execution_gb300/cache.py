@@ -2,7 +2,9 @@
 
 Rotary positions (``rope``, ``rope_backward``), the append of new tokens' keys and values (``cache_append``),
 attention of one new token per sequence (``attention_decode``), the selection of the sequences that go on
-(``cache_select``: fork, free, grow) and compaction (``cache_compact``). The header says what each computes.
+(``cache_select``: fork, free, grow) and compaction (``cache_compact``); attention of a tree of drafted tokens
+(``attention_drafts``, which also adds up the weight that each cached token gets), the branch that the model agrees with
+(``draft_path``) and its slots (``cache_accept``); eviction by weight (``cache_evict``). The header says what each computes.
 
 A cache is a pair of tensors [pages, page_size, kv_heads, dim] of any strides with a unit stride along dim: pages
 stored with their heads outermost are passed as ``pool.transpose(1, 2)``. Tables, lengths, positions and counts are
@@ -24,8 +26,8 @@ import importlib.util
 
 from . import CmdError, _build, _check, _P, lib
 
-CMD_CACHE_MAX_DIM, CMD_CACHE_MAX_POOLS = 256, 64
-BAD_PAGE, BAD_INDEX, FULL_TABLE, NO_PAGES = 1, 2, 4, 8  # bits of the status word
+CMD_CACHE_MAX_DIM, CMD_CACHE_MAX_POOLS, CMD_CACHE_MAX_LAYERS, CMD_CACHE_MAX_DRAFTS = 256, 64, 32, 256
+BAD_PAGE, BAD_INDEX, FULL_TABLE, NO_PAGES, SHARED_PAGE = 1, 2, 4, 8, 16  # bits of the status word
 LAYOUTS = {"half": 0, "interleaved": 1}
 SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
 
@@ -76,6 +78,29 @@ class cmd_compact_args(ctypes.Structure):
 
 _OP = ctypes.POINTER(cmd_operand)
 
+
+class cmd_drafts_args(ctypes.Structure):
+    _fields_ = [(n, cmd_operand) for n in ("q", "out", "lse", "k_cache", "v_cache", "tables", "lengths", "parents",
+                                           "weights")] + [
+        ("scale", _F32), ("softcap", _F32), ("window", _I32), ("reserved", _I32), ("workspace", _P),
+        ("workspace_bytes", _I64), ("status", _P)]
+
+
+class cmd_path_args(ctypes.Structure):
+    _fields_ = [(n, cmd_operand) for n in ("tokens", "choices", "parents", "path", "counts", "last")] + [("status", _P)]
+
+
+class cmd_accept_args(ctypes.Structure):
+    _fields_ = [(n, cmd_operand) for n in ("tables", "lengths", "refs", "path", "counts", "lengths_out", "refs_out")] + [
+        ("pools", _OP), ("n_pools", _I32), ("reserved", _I32), ("status", _P)]
+
+
+class cmd_evict_args(ctypes.Structure):
+    _fields_ = [(n, cmd_operand) for n in ("tables", "lengths", "refs", "lengths_out", "refs_out")] + [
+        ("k_caches", _OP), ("v_caches", _OP), ("weights", _OP), ("n_layers", _I32), ("budget", _I32), ("recent", _I32),
+        ("reserved", _I32), ("workspace", _P), ("workspace_bytes", _I64), ("status", _P)]
+
+
 # Every symbol include/cmd_cache.h declares, with (restype, argtypes).
 SIGNATURES = {
     "cmd_rope_turns": (_I, [_I32, ctypes.c_double, _I32] + [ctypes.c_double] * 4 + [ctypes.POINTER(ctypes.c_uint64)]),
@@ -87,6 +112,12 @@ SIGNATURES = {
     "cmd_cache_select": (_I, [ctypes.POINTER(cmd_select_args), _P]),
     "cmd_compact_workspace": (_I, [_I64, ctypes.POINTER(_I64)]),
     "cmd_cache_compact": (_I, [ctypes.POINTER(cmd_compact_args), _P]),
+    "cmd_drafts_workspace": (_I, [_I64] + [_I32] * 4 + [_I64, ctypes.POINTER(_I64)]),
+    "cmd_attention_drafts": (_I, [ctypes.POINTER(cmd_drafts_args), _P]),
+    "cmd_draft_path": (_I, [ctypes.POINTER(cmd_path_args), _P]),
+    "cmd_cache_accept": (_I, [ctypes.POINTER(cmd_accept_args), _P]),
+    "cmd_evict_workspace": (_I, [_I64] + [_I32] * 3 + [ctypes.POINTER(_I64)]),
+    "cmd_cache_evict": (_I, [ctypes.POINTER(cmd_evict_args), _P]),
     "cmd_cache_status": (_I, [_P, ctypes.POINTER(_I32), _P]),
 }
 
@@ -126,6 +157,19 @@ def cmd_select_workspace(old_rows: int, new_rows: int, pages: int) -> int:
 def cmd_compact_workspace(pages: int) -> int:
     n = _I64()
     _check(entry("cmd_compact_workspace")(pages, ctypes.byref(n)), "cmd_compact_workspace")
+    return n.value
+
+
+def cmd_drafts_workspace(rows: int, drafts: int, q_heads: int, kv_heads: int, dim: int, tokens: int = 0) -> int:
+    n = _I64()
+    _check(entry("cmd_drafts_workspace")(rows, drafts, q_heads, kv_heads, dim, tokens, ctypes.byref(n)),
+           "cmd_drafts_workspace")
+    return n.value
+
+
+def cmd_evict_workspace(rows: int, layers: int, kv_heads: int, budget: int) -> int:
+    n = _I64()
+    _check(entry("cmd_evict_workspace")(rows, layers, kv_heads, budget, ctypes.byref(n)), "cmd_evict_workspace")
     return n.value
 
 
@@ -295,6 +339,58 @@ def cache_compact(tables, lengths, refs, pools, *, page_size: int, out=None, sta
         with _On(stream, tables, lengths, refs, *pools, *(out or ()), status):
             return cache_compact(tables, lengths, refs, pools, page_size=page_size, out=out, status=status)
     return (_module or _native()).cache_compact(tables, lengths, refs, pools, page_size, out, status)
+
+
+def attention_drafts(q, k_cache, v_cache, tables, lengths, *, parents=None, scale: float | None = None,
+                     softcap: float = 0.0, window: int = 0, weights=None, out=None, lse=None, return_lse: bool = False,
+                     workspace=None, status=None, stream=None):
+    """Attention of each row's last drafts, a tree: q [rows, drafts, q_heads, dim], whose keys and values are the last
+    of the first lengths[r] tokens of row r. parents [rows, drafts]: the draft that each goes on from (below its own
+    index; -1: the tokens before the drafts; less: padding); None: each goes on from the one before. A draft sees the
+    tokens before the drafts, its ancestors and itself. weights [rows, kv_heads, tokens], float32: the attention that
+    each token got is added to it. Returns out, or (out, lse) with return_lse. scale: dim ** -0.5 unless given.
+    workspace: cmd_drafts_workspace bytes (allocated where None)."""
+    if stream is not None:
+        with _On(stream, q, k_cache, v_cache, tables, lengths, parents, weights, out, lse, workspace, status):
+            return attention_drafts(q, k_cache, v_cache, tables, lengths, parents=parents, scale=scale, softcap=softcap,
+                                    window=window, weights=weights, out=out, lse=lse, return_lse=return_lse,
+                                    workspace=workspace, status=status)
+    return (_module or _native()).attention_drafts(q, k_cache, v_cache, tables, lengths, parents, scale, softcap, window,
+                                                   weights, out, lse, return_lse, workspace, status)
+
+
+def draft_path(tokens, choices, *, parents=None, out=None, status=None, stream=None):
+    """The branch of each row's tree of drafts that agrees with the model: from draft 0 to the first draft that goes on
+    from it with the token choices[r][0], which the model chooses after draft 0, and so on. tokens, choices, parents:
+    [rows, drafts] (parents as in attention_drafts). Returns (path, counts, last): the drafts passed (then -1), their
+    number, and the choice after the last of them; out: those three, to write to."""
+    if stream is not None:
+        with _On(stream, tokens, choices, parents, *(out or ()), status):
+            return draft_path(tokens, choices, parents=parents, out=out, status=status)
+    return (_module or _native()).draft_path(tokens, choices, parents, out, status)
+
+
+def cache_accept(tables, lengths, refs, path, counts, pools, *, drafts: int | None = None, out=None, status=None,
+                 stream=None):
+    """Of each row's last drafts (as many as path has columns; drafts, where given, has to say the same) keeps the
+    first counts[r] of path[r]: their keys and values move together behind the tokens before the drafts, and pages past
+    them are released. pools: up to 64 tensors [pages, page_size, kv_heads, dim] (for more, a call for each 64, with
+    the same inputs). Returns (lengths, refs); out: those two, to write to."""
+    if stream is not None:
+        with _On(stream, tables, lengths, refs, path, counts, *pools, *(out or ()), status):
+            return cache_accept(tables, lengths, refs, path, counts, pools, drafts=drafts, out=out, status=status)
+    return (_module or _native()).cache_accept(tables, lengths, refs, path, counts, pools, drafts, out, status)
+
+
+def cache_evict(tables, lengths, refs, layers, *, budget: int, recent: int = 0, out=None, status=None, stream=None):
+    """Holds rows to a budget: in each layer, a (k_cache, v_cache, weights) triple, each kv head of a longer row keeps
+    the last `recent` tokens and the others of the largest weights, moved together in their order, weights too; pages
+    past them are released. Up to 32 layers (for more, a call for each 32, with the same inputs). Returns (lengths,
+    refs); out: those two, to write to."""
+    if stream is not None:
+        with _On(stream, tables, lengths, refs, *(x for layer in layers for x in layer), *(out or ()), status):
+            return cache_evict(tables, lengths, refs, layers, budget=budget, recent=recent, out=out, status=status)
+    return (_module or _native()).cache_evict(tables, lengths, refs, layers, budget, recent, out, status)
 
 
 def cache_status(status, stream=None) -> None:

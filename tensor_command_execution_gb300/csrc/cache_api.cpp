@@ -505,6 +505,27 @@ int64_t attention_workspace(int64_t q_heads, int64_t kv_heads, int64_t dim) {
   return kSplitBytes + 2 * (int64_t)cmdx::kAttendMaxCtas * heads * (round_up(dim, 4) + 4) * 4;
 }
 
+// The cache and the scores' scale, as the attentions' kernels take them.
+void attention_common(cmdx::AttendParams& p, const cmd_operand& k_cache, const cmd_operand& v_cache, const cmd_operand& tables,
+                      const cmd_operand& lengths, float scale, float softcap) {
+  p.dim = (int32_t)k_cache.sizes[3];
+  p.n_pages = (int32_t)k_cache.sizes[0];
+  p.columns = (int32_t)tables.sizes[1];
+  p.page = cmdx::fast_div_by((uint32_t)k_cache.sizes[1]);
+  const double log2e = 1.4426950408889634074;
+  p.scale_log2 = (float)(scale * log2e);
+  p.cap_in = softcap > 0.0f ? (float)((double)scale / softcap) : 0.0f;
+  p.cap_out = (float)(softcap * log2e);
+  for (int d = 0; d < 3; ++d) {
+    p.k_st[d] = k_cache.strides[d];
+    p.v_st[d] = v_cache.strides[d];
+  }
+  for (int d = 0; d < 2; ++d) p.table_st[d] = tables.strides[d];
+  p.len_st = lengths.strides[0];
+  p.k = k_cache.ptr;
+  p.v = v_cache.ptr;
+}
+
 }  // namespace
 
 extern "C" cmd_status cmd_attention_workspace(int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t* bytes) {
@@ -560,28 +581,13 @@ extern "C" cmd_status cmd_attention_decode(const cmd_attention_args* args, void*
     std::memset(&p, 0, sizeof p);
     p.kv_heads = (int32_t)kv;
     p.group = (int32_t)(heads / kv);
-    p.dim = (int32_t)dim;
-    p.n_pages = (int32_t)a.k_cache.sizes[0];
-    p.columns = (int32_t)a.tables.sizes[1];
-    p.page = cmdx::fast_div_by((uint32_t)a.k_cache.sizes[1]);
-    const double log2e = 1.4426950408889634074;
-    p.scale_log2 = (float)(a.scale * log2e);
-    p.cap_in = a.softcap > 0.0f ? (float)((double)a.scale / a.softcap) : 0.0f;
-    p.cap_out = (float)(a.softcap * log2e);
     p.window = a.window;
-    for (int d = 0; d < 3; ++d) {
-      p.k_st[d] = a.k_cache.strides[d];
-      p.v_st[d] = a.v_cache.strides[d];
-    }
+    attention_common(p, a.k_cache, a.v_cache, a.tables, a.lengths, a.scale, a.softcap);
     for (int d = 0; d < 2; ++d) {
       p.q_st[d] = a.q.strides[d];
       p.out_st[d] = a.out.strides[d];
       p.lse_st[d] = a.lse.ptr ? a.lse.strides[d] : 0;
-      p.table_st[d] = a.tables.strides[d];
     }
-    p.len_st = a.lengths.strides[0];
-    p.k = a.k_cache.ptr;
-    p.v = a.v_cache.ptr;
     p.splits = static_cast<cmdx::AttendSplit*>(a.workspace);
     p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kSplitBytes);
     p.status = a.status;
@@ -848,6 +854,405 @@ extern "C" cmd_status cmd_cache_compact(const cmd_compact_args* args, void* cuda
   });
 }
 
+// ---- attention of drafted tokens, and what is kept ----------------------------------
+
+namespace {
+
+constexpr int64_t kDraftHeads = 1 << 20;  // drafts * q_heads, at most
+
+int64_t drafts_parts(int64_t drafts, int64_t q_heads, int64_t kv_heads, int64_t dim) {
+  const int64_t rows = std::min<int64_t>(drafts * (q_heads / kv_heads), cmdx::kDraftRows);
+  return round_up(cmdx::kDraftCtas, 16) * (int64_t)sizeof(cmdx::AttendSplit) + 2 * (int64_t)cmdx::kDraftCtas * rows * (round_up(dim, 4) + 4) * 4;
+}
+int64_t drafts_workspace(int64_t rows, int64_t drafts, int64_t q_heads, int64_t kv_heads, int64_t dim, bool weights) {
+  return drafts_parts(drafts, q_heads, kv_heads, dim) + (weights ? round_up(rows * drafts * q_heads * 8, 16) : 0);
+}
+
+// A tensor that a call reads as i32 of these sizes, with any strides.
+void check_i32(const cmd_operand& o, const char* name, int rank, const int64_t* sizes) {
+  check(o, name, rank);
+  check_type(o, name, CMD_I32);
+  check_sizes(o, name, sizes);
+}
+
+}  // namespace
+
+extern "C" cmd_status cmd_drafts_workspace(int64_t rows, int32_t drafts, int32_t q_heads, int32_t kv_heads, int32_t dim,
+                                           int64_t tokens, int64_t* bytes) {
+  return guarded([&]() -> cmd_status {
+    NEED(bytes, CMD_ERR_NULL, "bytes is NULL");
+    NEED(rows >= 0 && rows <= 0x7fffffff && tokens >= 0, CMD_ERR_SHAPE, "negative rows or tokens, or rows above 2^31 - 1");
+    NEED(drafts >= 1 && drafts <= CMD_CACHE_MAX_DRAFTS, CMD_ERR_LIMIT, "drafts are 1 to 256");
+    NEED(kv_heads >= 1 && q_heads >= 1 && q_heads % kv_heads == 0, CMD_ERR_SHAPE, "kv_heads must divide q_heads");
+    check_heads(q_heads);
+    NEED((int64_t)drafts * q_heads <= kDraftHeads, CMD_ERR_LIMIT, "drafts times q_heads pass 2^20");
+    NEED(dim >= 0 && dim <= CMD_CACHE_MAX_DIM, CMD_ERR_LIMIT, "a head dim above 256");
+    *bytes = drafts_workspace(rows, drafts, q_heads, kv_heads, dim, tokens > 0);
+    return CMD_OK;
+  });
+}
+
+extern "C" cmd_status cmd_attention_drafts(const cmd_drafts_args* args, void* cuda_stream) {
+  return guarded([&]() -> cmd_status {
+    NEED(args, CMD_ERR_NULL, "args is NULL");
+    const cmd_drafts_args& a = *args;
+    check_status(a.status);
+    check(a.q, "q", 4, true);
+    check(a.out, "out", 4, true);
+    check_cache(a.k_cache, a.v_cache, a.tables);
+    check_type(a.q, "q", a.k_cache.dtype);
+    check_type(a.out, "out", a.k_cache.dtype);
+    check_sizes(a.out, "out", a.q.sizes);
+    check_distinct(a.out, "out");
+    const int64_t rows = a.q.sizes[0], drafts = a.q.sizes[1], heads = a.q.sizes[2], dim = a.q.sizes[3], kv = a.k_cache.sizes[2];
+    NEED(dim == a.k_cache.sizes[3], CMD_ERR_SHAPE, "q and k_cache differ in dim");
+    NEED(dim >= 1, CMD_ERR_SHAPE, "a head has no elements");
+    NEED(kv >= 1 ? heads % kv == 0 : heads == 0, CMD_ERR_SHAPE, "the cache's heads must divide q's");
+    check_heads(heads);
+    NEED(drafts >= 1 && drafts <= CMD_CACHE_MAX_DRAFTS, CMD_ERR_LIMIT, "drafts are 1 to 256");
+    NEED(drafts * heads <= kDraftHeads, CMD_ERR_LIMIT, "drafts times q_heads pass 2^20");
+    NEED(rows == a.tables.sizes[0], CMD_ERR_SHAPE, "q and tables differ in rows");
+    check_i32(a.lengths, "lengths", 1, &rows);
+    const cmd_operand* ins[] = {&a.q, &a.k_cache, &a.v_cache, &a.tables, &a.lengths, &a.parents};
+    const char* names[] = {"q", "k_cache", "v_cache", "tables", "lengths", "parents"};
+    const bool has_parents = a.parents.ptr != nullptr, has_weights = a.weights.ptr != nullptr;
+    if (has_parents) check_i32(a.parents, "parents", 2, a.q.sizes);
+    const cmd_operand* outs[] = {&a.out, &a.lse, &a.weights};
+    const char* out_names[] = {"out", "lse", "weights"};
+    if (a.lse.ptr) {
+      check(a.lse, "lse", 3);
+      check_type(a.lse, "lse", CMD_F32);
+      check_sizes(a.lse, "lse", a.q.sizes);
+      check_distinct(a.lse, "lse");
+    }
+    const int64_t tokens = a.tables.sizes[1] * a.k_cache.sizes[1];
+    if (has_weights) {
+      check(a.weights, "weights", 3, true);
+      check_type(a.weights, "weights", CMD_F32);
+      NEED(a.weights.sizes[0] == rows && a.weights.sizes[1] == kv, CMD_ERR_SHAPE, "weights and q differ in rows, or weights and k_cache in heads");
+      NEED(a.weights.sizes[2] >= tokens, CMD_ERR_SHAPE, "weights holds fewer tokens than a table row");
+      check_distinct(a.weights, "weights");
+    }
+    for (int o = 0; o < 3; ++o) {
+      if (!outs[o]->ptr) continue;
+      for (int i = 0; i < 6; ++i)
+        if (i != 5 || has_parents) check_apart(*outs[o], out_names[o], *ins[i], names[i]);
+      for (int j = 0; j < o; ++j)
+        if (outs[j]->ptr) check_apart(*outs[o], out_names[o], *outs[j], out_names[j]);
+    }
+    NEED(std::isfinite(a.scale) && a.scale > 0.0f, CMD_ERR_ARG, "scale must be positive");
+    NEED(std::isfinite(a.softcap) && a.softcap >= 0.0f, CMD_ERR_ARG, "softcap must be positive, or 0 for none");
+    NEED(a.window >= 0, CMD_ERR_ARG, "window must be positive, or 0 for none");
+    NEED(a.reserved == 0, CMD_ERR_ARG, "reserved must be 0");
+    if (rows == 0 || heads == 0) return CMD_OK;
+    check_workspace(a.workspace, a.workspace_bytes, drafts_workspace(rows, drafts, heads, kv, dim, has_weights));
+    cmdx::DraftParams p;
+    std::memset(&p, 0, sizeof p);
+    const int32_t per = (int32_t)(heads / kv);
+    p.kv_heads = (int32_t)kv;
+    p.group = (int32_t)drafts * per;
+    p.per = cmdx::fast_div_by((uint32_t)per);
+    p.drafts = (int32_t)drafts;
+    p.near = a.window;
+    p.window = a.window > 0 ? (int32_t)std::min<int64_t>(a.window + drafts - 1, 0x7fffffff) : 0;
+    attention_common(p, a.k_cache, a.v_cache, a.tables, a.lengths, a.scale, a.softcap);
+    p.q_st[0] = a.q.strides[0];
+    p.q_draft = a.q.strides[1];
+    p.q_st[1] = a.q.strides[2];
+    p.out_st[0] = a.out.strides[0];
+    p.out_draft = a.out.strides[1];
+    p.out_st[1] = a.out.strides[2];
+    if (a.lse.ptr) {
+      p.lse_st[0] = a.lse.strides[0];
+      p.lse_draft = a.lse.strides[1];
+      p.lse_st[1] = a.lse.strides[2];
+    }
+    if (has_parents)
+      for (int d = 0; d < 2; ++d) p.parent_st[d] = a.parents.strides[d];
+    if (has_weights)
+      for (int d = 0; d < 2; ++d) p.w_st[d] = a.weights.strides[d];
+    p.splits = static_cast<cmdx::AttendSplit*>(a.workspace);
+    p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + round_up(cmdx::kDraftCtas, 16) * sizeof(cmdx::AttendSplit));
+    float2* stats = has_weights ? reinterpret_cast<float2*>(static_cast<uint8_t*>(a.workspace) + drafts_parts(drafts, heads, kv, dim)) : nullptr;
+    p.status = a.status;
+    const int es = elem_size(a.q.dtype);
+    const auto pieces = [&](int n) { return dim * es % n == 0 && vector_rows(a.k_cache, n) && vector_rows(a.v_cache, n); };
+    const int copy = pieces(16) ? 16 : pieces(4) ? 4 : 0;
+    p.blocks = (p.group + cmdx::kDraftRows - 1) / cmdx::kDraftRows;
+    p.block_heads = (p.group + p.blocks - 1) / p.blocks;
+    p.q_pairs = dim % 2 == 0 && vector_rows(a.q, 4);
+    const int64_t row_units = (int64_t)p.kv_heads * p.blocks * (tokens / cmdx::kAttendLeastTile + 2 + cmdx::kAttendMostStart);
+    NEED(row_units < 0x7fffffff, CMD_ERR_LIMIT, "a table row's tokens times the heads pass 2^31 tiles of 32");
+    const int64_t at_once = std::min<int64_t>(cmdx::kAttendRows, 0x7fffffff / row_units);
+    for (int64_t r = 0; r < rows; r += at_once) {
+      p.rows = (int32_t)std::min<int64_t>(at_once, rows - r);
+      p.q = static_cast<const uint8_t*>(a.q.ptr) + r * a.q.strides[0] * es;
+      p.out = static_cast<uint8_t*>(a.out.ptr) + r * a.out.strides[0] * es;
+      p.lse = a.lse.ptr ? static_cast<float*>(a.lse.ptr) + r * a.lse.strides[0] : nullptr;
+      p.tables = static_cast<const int32_t*>(a.tables.ptr) + r * a.tables.strides[0];
+      p.lengths = static_cast<const int32_t*>(a.lengths.ptr) + r * a.lengths.strides[0];
+      p.parents = has_parents ? static_cast<const int32_t*>(a.parents.ptr) + r * a.parents.strides[0] : nullptr;
+      p.weights = has_weights ? static_cast<float*>(a.weights.ptr) + r * a.weights.strides[0] : nullptr;
+      p.stats = stats ? stats + r * drafts * heads : nullptr;
+      const cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+      const cudaError_t e = es == 4      ? (copy == 16 ? cmdx::drafts_f32_launch16 : cmdx::drafts_f32_launch4)(p, stream)
+                            : copy == 16 ? cmdx::drafts_mma_launch16(a.q.dtype, p, stream)
+                            : copy == 4  ? cmdx::drafts_mma_launch4(a.q.dtype, p, stream)
+                                         : cmdx::drafts_mma_launch0(a.q.dtype, p, stream);
+      if (e != cudaSuccess) return launched(e);
+    }
+    return CMD_OK;
+  });
+}
+
+extern "C" cmd_status cmd_draft_path(const cmd_path_args* args, void* cuda_stream) {
+  return guarded([&]() -> cmd_status {
+    NEED(args, CMD_ERR_NULL, "args is NULL");
+    const cmd_path_args& a = *args;
+    check_status(a.status);
+    check(a.tokens, "tokens", 2);
+    check_type(a.tokens, "tokens", CMD_I32);
+    const int64_t rows = a.tokens.sizes[0], drafts = a.tokens.sizes[1];
+    const cmd_operand* ins[] = {&a.tokens, &a.choices, &a.parents};
+    const char* names[] = {"tokens", "choices", "parents"};
+    check_i32(a.choices, "choices", 2, a.tokens.sizes);
+    const bool has_parents = a.parents.ptr != nullptr;
+    if (has_parents) check_i32(a.parents, "parents", 2, a.tokens.sizes);
+    const cmd_operand* outs[] = {&a.path, &a.counts, &a.last};
+    const char* out_names[] = {"path", "counts", "last"};
+    for (int o = 0; o < 3; ++o) {
+      check_i32(*outs[o], out_names[o], o == 0 ? 2 : 1, a.tokens.sizes);
+      check_distinct(*outs[o], out_names[o]);
+      for (int i = 0; i < 2 + has_parents; ++i) check_apart(*outs[o], out_names[o], *ins[i], names[i]);
+      for (int j = 0; j < o; ++j) check_apart(*outs[o], out_names[o], *outs[j], out_names[j]);
+    }
+    NEED(drafts >= 1 && drafts <= CMD_CACHE_MAX_DRAFTS, CMD_ERR_LIMIT, "drafts are 1 to 256");
+    NEED(rows <= kMostRows, CMD_ERR_LIMIT, "more than 2^30 rows");
+    if (rows == 0) return CMD_OK;
+    cmdx::PathParams p;
+    std::memset(&p, 0, sizeof p);
+    p.tokens = static_cast<const int32_t*>(a.tokens.ptr);
+    p.choices = static_cast<const int32_t*>(a.choices.ptr);
+    p.parents = static_cast<const int32_t*>(a.parents.ptr);
+    p.path = static_cast<int32_t*>(a.path.ptr);
+    p.counts = static_cast<int32_t*>(a.counts.ptr);
+    p.last = static_cast<int32_t*>(a.last.ptr);
+    for (int d = 0; d < 2; ++d) {
+      p.token_st[d] = a.tokens.strides[d];
+      p.choice_st[d] = a.choices.strides[d];
+      p.parent_st[d] = has_parents ? a.parents.strides[d] : 0;
+      p.path_st[d] = a.path.strides[d];
+    }
+    p.counts_st = a.counts.strides[0];
+    p.last_st = a.last.strides[0];
+    p.rows = (int32_t)rows;
+    p.drafts = (int32_t)drafts;
+    p.status = a.status;
+    return launched(cmdx::path_launch(p, static_cast<cudaStream_t>(cuda_stream)));
+  });
+}
+
+namespace {
+
+// The pools of an accept or evict call, written to: alike in sizes and type,
+// apart from one another.
+struct KeptPools {
+  const cmd_operand* pool[CMD_CACHE_MAX_POOLS];
+  Range range[CMD_CACHE_MAX_POOLS];
+  std::string name[CMD_CACHE_MAX_POOLS];
+  int n = 0;
+
+  void add(const cmd_operand& o, const std::string& what, int64_t pages) {
+    check(o, what.c_str(), 4, true);
+    NEED(is_float(o.dtype), CMD_ERR_TYPE, what + " is no float tensor");
+    NEED(o.sizes[0] == pages, CMD_ERR_SHAPE, what + " has another number of pages than refs");
+    if (n == 0) {
+      NEED(o.sizes[1] >= 1, CMD_ERR_SHAPE, "a page holds no token");
+      NEED(o.sizes[2] >= 1 && o.sizes[3] >= 1, CMD_ERR_SHAPE, "a token has no elements");
+      NEED(o.sizes[3] <= CMD_CACHE_MAX_DIM, CMD_ERR_LIMIT, "a head dim above 256");
+      check_heads(o.sizes[2]);
+    } else {
+      check_type(o, what.c_str(), pool[0]->dtype);
+      check_sizes(o, what.c_str(), pool[0]->sizes);
+    }
+    check_distinct(o, what.c_str());
+    apart(o, what.c_str());
+    pool[n] = &o;
+    range[n] = range_of(o);
+    name[n++] = what;
+  }
+  void apart(const cmd_operand& o, const char* what) const {
+    const Range r = range_of(o);
+    for (int i = 0; i < n; ++i)
+      if (meet(r, range[i])) check_apart(*pool[i], name[i].c_str(), o, what);
+  }
+  // the largest access that suits all of them
+  int unit() const {
+    const int es = elem_size(pool[0]->dtype);
+    for (int bytes = 16; bytes > es; bytes /= 2) {
+      bool ok = pool[0]->sizes[3] * es % bytes == 0;
+      for (int i = 0; i < n; ++i) ok = ok && vector_rows(*pool[i], bytes);
+      if (ok) return bytes;
+    }
+    return es;
+  }
+};
+
+cmdx::KeepPool keep_pool(const cmd_operand& o) {
+  cmdx::KeepPool p;
+  p.ptr = static_cast<uint8_t*>(o.ptr);
+  for (int d = 0; d < 3; ++d) p.st[d] = o.strides[d] * elem_size(o.dtype);
+  return p;
+}
+
+// What accept and evict share: tables, lengths, counts; the pools are in `pools`.
+template <class Args>
+cmdx::KeepParams keep_common(const Args& a, const KeptPools& pools) {
+  const int64_t rows = a.tables.sizes[0], pages = a.refs.sizes[0], columns = a.tables.sizes[1];
+  const cmd_operand& first = *pools.pool[0];
+  check_ints(a.lengths, "lengths", 1);
+  check_sizes(a.lengths, "lengths", &rows);
+  check_ints(a.lengths_out, "lengths_out", 1);
+  check_sizes(a.lengths_out, "lengths_out", &rows);
+  check_ints(a.refs_out, "refs_out", 1);
+  check_sizes(a.refs_out, "refs_out", &pages);
+  NEED(rows <= kMostRows, CMD_ERR_LIMIT, "more than 2^30 rows");
+  NEED(pages <= kMostPages, CMD_ERR_LIMIT, "more than 2^30 pages");
+  NEED((__int128)columns * first.sizes[1] <= 0x7fff0000, CMD_ERR_LIMIT, "table rows that reach past 2^31 - 2^16 tokens");
+  const cmd_operand* ins[] = {&a.tables, &a.lengths, &a.refs};
+  const char* names[] = {"tables", "lengths", "refs"};
+  const cmd_operand* outs[] = {&a.lengths_out, &a.refs_out};
+  const char* out_names[] = {"lengths_out", "refs_out"};
+  for (int i = 0; i < 3; ++i) {
+    for (int o = 0; o < 2; ++o) check_apart(*outs[o], out_names[o], *ins[i], names[i]);
+    pools.apart(*ins[i], names[i]);
+  }
+  for (int o = 0; o < 2; ++o) pools.apart(*outs[o], out_names[o]);
+  check_apart(a.refs_out, "refs_out", a.lengths_out, "lengths_out");
+  NEED(a.reserved == 0, CMD_ERR_ARG, "reserved must be 0");
+  cmdx::KeepParams p;
+  std::memset(&p, 0, sizeof p);
+  p.tables = static_cast<const int32_t*>(a.tables.ptr);
+  p.lengths = static_cast<const int32_t*>(a.lengths.ptr);
+  p.refs = static_cast<const int32_t*>(a.refs.ptr);
+  p.lengths_out = static_cast<int32_t*>(a.lengths_out.ptr);
+  p.refs_out = static_cast<int32_t*>(a.refs_out.ptr);
+  p.table_st = a.tables.strides[0];
+  p.rows = (int32_t)rows;
+  p.columns = (int32_t)columns;
+  p.pages = (int32_t)pages;
+  p.page = cmdx::fast_div_by((uint32_t)first.sizes[1]);
+  p.heads = (int32_t)first.sizes[2];
+  p.unit = pools.unit();
+  p.pieces = (int32_t)(first.sizes[3] * elem_size(first.dtype) / p.unit);
+  p.per_head = cmdx::fast_div_by((uint32_t)p.pieces);
+  p.status = a.status;
+  return p;
+}
+
+}  // namespace
+
+extern "C" cmd_status cmd_cache_accept(const cmd_accept_args* args, void* cuda_stream) {
+  return guarded([&]() -> cmd_status {
+    NEED(args, CMD_ERR_NULL, "args is NULL");
+    const cmd_accept_args& a = *args;
+    check_status(a.status);
+    check_ints(a.tables, "tables", 2);
+    check_ints(a.refs, "refs", 1);
+    NEED(a.n_pools >= 1 && a.n_pools <= CMD_CACHE_MAX_POOLS, CMD_ERR_LIMIT, "pools are 1 to 64");
+    NEED(a.pools, CMD_ERR_NULL, "pools is NULL");
+    KeptPools pools;
+    for (int i = 0; i < a.n_pools; ++i) pools.add(a.pools[i], "pool " + std::to_string(i), a.refs.sizes[0]);
+    cmdx::KeepParams p = keep_common(a, pools);
+    const int64_t rows = a.tables.sizes[0];
+    check_ints(a.path, "path", 2);
+    NEED(a.path.sizes[0] == rows, CMD_ERR_SHAPE, "path and tables differ in rows");
+    NEED(a.path.sizes[1] >= 1 && a.path.sizes[1] <= CMD_CACHE_MAX_DRAFTS, CMD_ERR_LIMIT, "drafts are 1 to 256");
+    check_ints(a.counts, "counts", 1);
+    check_sizes(a.counts, "counts", &rows);
+    const cmd_operand* more[] = {&a.path, &a.counts};
+    const char* names[] = {"path", "counts"};
+    for (int i = 0; i < 2; ++i) {
+      check_apart(a.lengths_out, "lengths_out", *more[i], names[i]);
+      check_apart(a.refs_out, "refs_out", *more[i], names[i]);
+      pools.apart(*more[i], names[i]);
+    }
+    p.path = static_cast<const int32_t*>(a.path.ptr);
+    p.path_st = a.path.strides[0];
+    p.counts = static_cast<const int32_t*>(a.counts.ptr);
+    p.drafts = (int32_t)a.path.sizes[1];
+    if (rows == 0 && p.pages == 0) return CMD_OK;
+    cmdx::KeepPools list;
+    std::memset(&list, 0, sizeof list);
+    for (int i = 0; i < pools.n; ++i) list.pool[i] = keep_pool(*pools.pool[i]);
+    list.n = pools.n;
+    return launched(cmdx::accept_launch(p, list, static_cast<cudaStream_t>(cuda_stream)));
+  });
+}
+
+namespace {
+
+int64_t evict_workspace(int64_t rows, int64_t layers, int64_t heads, int64_t budget) {
+  NEED((__int128)rows * layers * heads * 3 <= 0x7fffffff, CMD_ERR_LIMIT, "rows times layers times heads pass 2^31 / 3");
+  return std::max<int64_t>(round_up(rows * layers * heads * budget * 4, 16), 16);
+}
+
+}  // namespace
+
+extern "C" cmd_status cmd_evict_workspace(int64_t rows, int32_t layers, int32_t kv_heads, int32_t budget, int64_t* bytes) {
+  return guarded([&]() -> cmd_status {
+    NEED(bytes, CMD_ERR_NULL, "bytes is NULL");
+    NEED(rows >= 0 && rows <= 0x7fffffff && layers >= 1 && kv_heads >= 1 && budget >= 0, CMD_ERR_SHAPE, "negative size, or no layer or head");
+    *bytes = evict_workspace(rows, layers, kv_heads, budget);
+    return CMD_OK;
+  });
+}
+
+extern "C" cmd_status cmd_cache_evict(const cmd_evict_args* args, void* cuda_stream) {
+  return guarded([&]() -> cmd_status {
+    NEED(args, CMD_ERR_NULL, "args is NULL");
+    const cmd_evict_args& a = *args;
+    check_status(a.status);
+    check_ints(a.tables, "tables", 2);
+    check_ints(a.refs, "refs", 1);
+    NEED(a.n_layers >= 1 && a.n_layers <= CMD_CACHE_MAX_LAYERS, CMD_ERR_LIMIT, "layers are 1 to 32");
+    NEED(a.k_caches && a.v_caches && a.weights, CMD_ERR_NULL, "k_caches, v_caches or weights is NULL");
+    KeptPools pools;
+    for (int i = 0; i < a.n_layers; ++i) {
+      pools.add(a.k_caches[i], "k_cache " + std::to_string(i), a.refs.sizes[0]);
+      pools.add(a.v_caches[i], "v_cache " + std::to_string(i), a.refs.sizes[0]);
+    }
+    cmdx::KeepParams p = keep_common(a, pools);
+    cmdx::KeepLayers list;
+    std::memset(&list, 0, sizeof list);
+    for (int i = 0; i < a.n_layers; ++i) {
+      const cmd_operand& w = a.weights[i];
+      const std::string name = "weights " + std::to_string(i);
+      check(w, name.c_str(), 3, true);
+      check_type(w, name.c_str(), CMD_F32);
+      NEED(w.sizes[0] == p.rows && w.sizes[1] == p.heads, CMD_ERR_SHAPE, name + " and tables differ in rows, or it and the caches in heads");
+      NEED(w.sizes[2] >= (int64_t)p.columns * p.page.d, CMD_ERR_SHAPE, name + " holds fewer tokens than a table row");
+      check_distinct(w, name.c_str());
+      const cmd_operand* others[] = {&a.tables, &a.lengths, &a.refs, &a.lengths_out, &a.refs_out};
+      const char* names[] = {"tables", "lengths", "refs", "lengths_out", "refs_out"};
+      for (int o = 0; o < 5; ++o) check_apart(w, name.c_str(), *others[o], names[o]);
+      for (int j = 0; j < i; ++j) check_apart(w, name.c_str(), a.weights[j], "another layer's");
+      pools.apart(w, name.c_str());
+      for (int j = 0; j < 2; ++j) list.pool[i][j] = keep_pool(j == 0 ? a.k_caches[i] : a.v_caches[i]);
+      list.weights[i] = static_cast<float*>(w.ptr);
+      for (int d = 0; d < 2; ++d) list.w_st[i][d] = w.strides[d];
+    }
+    NEED(a.recent >= 0 && a.budget >= a.recent, CMD_ERR_ARG, "recent is 0 to budget");
+    if (p.rows == 0 && p.pages == 0) return CMD_OK;
+    check_workspace(a.workspace, a.workspace_bytes, evict_workspace(p.rows, a.n_layers, p.heads, a.budget));
+    p.layers = a.n_layers;
+    p.budget = a.budget;
+    p.recent = a.recent;
+    p.kept = static_cast<int32_t*>(a.workspace);
+    return launched(cmdx::evict_launch(p, list, static_cast<cudaStream_t>(cuda_stream)));
+  });
+}
+
 extern "C" cmd_status cmd_cache_status(int32_t* status, int32_t* bits, void* cuda_stream) {
   return guarded([&]() -> cmd_status {
     NEED(status, CMD_ERR_NULL, "status is NULL");
@@ -868,7 +1273,9 @@ extern "C" cmd_status cmd_cache_status(int32_t* status, int32_t* bits, void* cud
     if (word & CMD_CACHE_BAD_INDEX) msg += " a row, parent, position or length was out of its range;";
     if (word & CMD_CACHE_FULL_TABLE) msg += " a table row had no room;";
     if (word & CMD_CACHE_NO_PAGES) msg += " the pool had no free page;";
+    if (word & CMD_CACHE_SHARED_PAGE) msg += " tokens would have moved into a page that others hold;";
     msg.pop_back();
-    return host_fail(word & (CMD_CACHE_BAD_PAGE | CMD_CACHE_BAD_INDEX) ? CMD_ERR_ARG : CMD_ERR_LIMIT, msg);
+    if (word & (CMD_CACHE_BAD_PAGE | CMD_CACHE_BAD_INDEX)) return host_fail(CMD_ERR_ARG, msg);
+    return host_fail(word & (CMD_CACHE_FULL_TABLE | CMD_CACHE_NO_PAGES) ? CMD_ERR_LIMIT : CMD_ERR_ALIAS, msg);
   });
 }

@@ -54,7 +54,8 @@ __device__ __forceinline__ int attend_length(const AttendParams& p, int r) {
 // Fills s for tiles of `tile` tokens (aligned to the row's start); all
 // threads of the CTA call it. (The host sees to it that the units of a launch,
 // of all heads, are below 2^31.)
-__device__ __forceinline__ void attend_rows(const AttendParams& p, AttendRows& s, int tile) {
+template <class P>
+__device__ __forceinline__ void attend_rows(const P& p, AttendRows& s, int tile) {
   __shared__ int32_t s_warp[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int run = (p.rows + blockDim.x - 1) / blockDim.x;
@@ -191,17 +192,29 @@ __device__ __forceinline__ void scale_by(float4& o, float c) {
   o.w *= c;
 }
 
+// Where query head h of a row is written (elements from out and lse), and what
+// is kept of its maximum and sum.
+struct AttendPlace {
+  int64_t out, lse;
+};
+__device__ __forceinline__ AttendPlace attend_place(const AttendParams& p, int row, int h) {
+  return {row * p.out_st[0] + h * p.out_st[1], row * p.lse_st[0] + h * p.lse_st[1]};
+}
+__device__ __forceinline__ void attend_note(const AttendParams&, int, int, float, float) {}
+
 // Writes elements d .. d + 3 (those below dim) of a finished head.
-template <class T>
-__device__ __forceinline__ void attend_write(const AttendParams& p, int row, int h, int d, float top, float l, float4 o) {
-  T* out = static_cast<T*>(p.out) + row * p.out_st[0] + h * p.out_st[1] + d;
+template <class T, class P>
+__device__ __forceinline__ void attend_write(const P& p, int row, int h, int d, float top, float l, float4 o) {
+  const AttendPlace at = attend_place(p, row, h);
+  T* out = static_cast<T*>(p.out) + at.out + d;
   const float r = l == 0.0f ? 0.0f : 1.0f / l;
   if (l == 0.0f) o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   const float x[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (d + i < p.dim) out[i] = from_float<T>(x[i] * r);
-  if (d == 0 && p.lse) p.lse[row * p.lse_st[0] + h * p.lse_st[1]] = l == 0.0f ? -CUDART_INF_F : (top + log2f(l)) * CUDART_LN2_F;
+  if (d == 0 && p.lse) p.lse[at.lse] = l == 0.0f ? -CUDART_INF_F : (top + log2f(l)) * CUDART_LN2_F;
+  if (d == 0) attend_note(p, row, h, top, l);
 }
 
 // A segment's kv head and its query heads [head0, head0 + heads).
@@ -237,11 +250,11 @@ __device__ __forceinline__ float4 attend_merged(const float* s, int warp_pitch, 
 }
 
 // Ends a segment. The warps' states lie in shared memory, query head q of
-// warp w at state + w * warp_pitch + q * pitch (pitch = attend_pitch of
-// something at least dim). All threads call it, once their states are
-// written.
-template <class T, int WARPS>
-__device__ __forceinline__ void attend_finish(const AttendParams& p, const AttendShare& w, const AttendSegment& g,
+// warp w (of WARPS that hold states of the same heads) at state + w *
+// warp_pitch + q * pitch (pitch = attend_pitch of something at least dim). All
+// threads call it, once their states are written.
+template <class T, int WARPS, int THREADS = WARPS * 32, class P>
+__device__ __forceinline__ void attend_finish(const P& p, const AttendShare& w, const AttendSegment& g,
                                               const AttendHeads& h, const float* state, int warp_pitch, int pitch) {
   const int part_pitch = attend_pitch(p.dim), quads = part_pitch / 4 - 1;
   const int slot = 2 * blockIdx.x + (g.first <= w.begin ? 0 : 1);
@@ -254,7 +267,7 @@ __device__ __forceinline__ void attend_finish(const AttendParams& p, const Atten
     else if (part) p.splits[blockIdx.x] = split;
   }
   __syncthreads();  // the warps' states are complete
-  for (int i = threadIdx.x; i < h.heads * quads; i += WARPS * 32) {
+  for (int i = threadIdx.x; i < h.heads * quads; i += THREADS) {
     const int q = i / quads, d = 4 * (i - q * quads);
     float top, l;
     const float4 o = attend_merged<WARPS>(state + q * pitch, warp_pitch, pitch, d, &top, &l);
@@ -274,18 +287,18 @@ __device__ __forceinline__ void attend_finish(const AttendParams& p, const Atten
 
 // What a CTA does before its first segment: the rows, those of them that are
 // empty (zeros, and a log-sum of -infinity), and its share. False: no work.
-template <class T>
-__device__ __forceinline__ bool attend_begin(const AttendParams& p, AttendRows& s, int tile, AttendShare* w) {
+template <class T, class P>
+__device__ __forceinline__ bool attend_begin(const P& p, AttendRows& s, int tile, AttendShare* w) {
   attend_rows(p, s, tile);
   const int heads = p.kv_heads * p.group, groups = p.kv_heads * p.blocks;
   for (int r = blockIdx.x; r < p.rows; r += gridDim.x) {
     if (s.at[r + 1] != s.at[r]) continue;
     for (int i = threadIdx.x; i < heads * p.dim; i += blockDim.x) {
       const int h = i / p.dim;
-      static_cast<T*>(p.out)[r * p.out_st[0] + h * p.out_st[1] + (i - h * p.dim)] = from_float<T>(0.0f);
+      static_cast<T*>(p.out)[attend_place(p, r, h).out + (i - h * p.dim)] = from_float<T>(0.0f);
     }
     if (p.lse)
-      for (int h = threadIdx.x; h < heads; h += blockDim.x) p.lse[r * p.lse_st[0] + h * p.lse_st[1]] = -CUDART_INF_F;
+      for (int h = threadIdx.x; h < heads; h += blockDim.x) p.lse[attend_place(p, r, h).lse] = -CUDART_INF_F;
     if (p.split_by_row)
       for (int i = threadIdx.x; i < groups; i += blockDim.x) p.splits[r * groups + i].parts = 0;
   }
@@ -296,7 +309,8 @@ __device__ __forceinline__ bool attend_begin(const AttendParams& p, AttendRows& 
 
 // A team's CTA: its stretch of the team's row and group (no tiles where the row
 // is short), and a share that ends with it.
-__device__ __forceinline__ AttendSegment attend_team(const AttendParams& p, int tile, AttendShare* w) {
+template <class P>
+__device__ __forceinline__ AttendSegment attend_team(const P& p, int tile, AttendShare* w) {
   const int team = blockIdx.x / p.team, rank = blockIdx.x - team * p.team;
   w->groups = p.kv_heads * p.blocks;
   w->units = w->ctas = w->begin = w->end = w->index = w->group0 = 0;
@@ -317,14 +331,14 @@ __device__ __forceinline__ AttendSegment attend_team(const AttendParams& p, int 
 // Ends a team's row: the warps' states (as in attend_finish) go to `part` of
 // each CTA, and the CTAs of the team write the result, a run of elements each.
 // Every thread of the team calls it.
-template <class T, int WARPS>
-__device__ __forceinline__ void attend_finish_team(const AttendParams& p, const AttendSegment& g, const AttendHeads& h,
+template <class T, int WARPS, int THREADS = WARPS * 32, class P>
+__device__ __forceinline__ void attend_finish_team(const P& p, const AttendSegment& g, const AttendHeads& h,
                                                    const float* state, int warp_pitch, int pitch, float* part) {
   namespace cg = cooperative_groups;
   const cg::cluster_group team = cg::this_cluster();
   const int part_pitch = attend_pitch(p.dim), quads = part_pitch / 4 - 1;
   __syncthreads();  // the warps' states are complete
-  for (int i = threadIdx.x; i < h.heads * quads; i += WARPS * 32) {
+  for (int i = threadIdx.x; i < h.heads * quads; i += THREADS) {
     const int q = i / quads, d = 4 * (i - q * quads);
     float top, l;
     const float4 o = attend_merged<WARPS>(state + q * pitch, warp_pitch, pitch, d, &top, &l);
@@ -338,7 +352,7 @@ __device__ __forceinline__ void attend_finish_team(const AttendParams& p, const 
   team.sync();
   constexpr int kMost = 8;
   const int rank = blockIdx.x % p.team;
-  for (int i = rank * WARPS * 32 + threadIdx.x; i < h.heads * quads; i += p.team * WARPS * 32) {
+  for (int i = rank * THREADS + threadIdx.x; i < h.heads * quads; i += p.team * THREADS) {
     const int q = i / quads, d = 4 * (i - q * quads);
     float m[kMost], pl[kMost], top = -CUDART_INF_F, l = 0.0f;
     float4 po[kMost], o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -367,8 +381,8 @@ __device__ __forceinline__ void attend_finish_team(const AttendParams& p, const 
 
 // Joins the parts of query head q of a split row: WARPS warps take every
 // WARPS-th run of 8 parts, a lane 4 elements of the head (and 128 further).
-template <class T, int WARPS>
-__device__ __forceinline__ void attend_join(const AttendParams& p, int task, float (*s_state)[CMD_CACHE_MAX_DIM + 4]) {
+template <class T, int WARPS, class P>
+__device__ __forceinline__ void attend_join(const P& p, int task, float (*s_state)[CMD_CACHE_MAX_DIM + 4]) {
   constexpr int kAtOnce = 8;
   const int lane = threadIdx.x & 31, warp = WARPS == 1 ? 0 : threadIdx.x >> 5;
   const AttendSplit split = p.splits[task / p.block_heads];
@@ -440,8 +454,8 @@ __device__ __forceinline__ void attend_join(const AttendParams& p, int task, flo
   }
 }
 
-template <class T, int WARPS>
-__global__ void __launch_bounds__(WARPS == 1 ? 256 : WARPS * 32) attend_join_kernel(const __grid_constant__ AttendParams p) {
+template <class T, int WARPS, class P>
+__global__ void __launch_bounds__(WARPS == 1 ? 256 : WARPS * 32) attend_join_kernel(const __grid_constant__ P p) {
   __shared__ __align__(16) float s_state[WARPS == 1 ? 1 : WARPS][CMD_CACHE_MAX_DIM + 4];
   wait_for_previous();
   let_next_start();
@@ -475,8 +489,8 @@ inline int attend_team_size(const AttendParams& p, int ctas, int tile) {
 // Measured, one against 16, whole calls: one row of 393217 tokens and one kv
 // head (456 parts) 116 and 47.7 us; one of 32768 and 8 kv heads 39.3 and 30.2;
 // four of those 93.5 and 94.5; 64 rows of 4096 tokens 179 and 227.
-template <class T, class K>
-cudaError_t attend_launch(K kernel, AttendParams p, int start_units, int ctas, int threads, int smem, int tile,
+template <class T, class K, class P>
+cudaError_t attend_launch(K kernel, P p, int start_units, int ctas, int threads, int smem, int tile,
                           cudaStream_t stream, bool teams = true) {
   p.start_units = start_units;
   p.team = teams ? attend_team_size(p, ctas, tile) : 0;
@@ -496,8 +510,8 @@ cudaError_t attend_launch(K kernel, AttendParams p, int start_units, int ctas, i
   p.tasks = lists * p.block_heads;
   cudaError_t e = launch_chained(kernel, ctas, threads, (size_t)smem, stream, p);
   if (e != cudaSuccess || (int64_t)p.columns * p.page.d <= tile) return e;  // (a row of one tile is never split)
-  if (lists * 16 <= ctas) return launch_chained(attend_join_kernel<T, 16>, p.tasks, 512, 0, stream, p);
-  return launch_chained(attend_join_kernel<T, 1>, (p.tasks + 7) / 8, 256, 0, stream, p);
+  if (lists * 16 <= ctas) return launch_chained(attend_join_kernel<T, 16, P>, p.tasks, 512, 0, stream, p);
+  return launch_chained(attend_join_kernel<T, 1, P>, (p.tasks + 7) / 8, 256, 0, stream, p);
 }
 
 // A score in powers of two from a dot product.

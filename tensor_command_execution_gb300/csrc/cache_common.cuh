@@ -19,10 +19,10 @@ __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.
 
 // (with cluster > 1: in clusters of that many CTAs)
 template <class K, class... P>
-inline cudaError_t launch_clusters(K kernel, int cluster, int grid, int block, size_t smem, cudaStream_t stream,
+inline cudaError_t launch_clusters(K kernel, int cluster, dim3 grid, int block, size_t smem, cudaStream_t stream,
                                    const P&... params) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -37,8 +37,12 @@ inline cudaError_t launch_clusters(K kernel, int cluster, int grid, int block, s
   return cudaLaunchKernelEx(&cfg, kernel, params...);
 }
 template <class K, class... P>
-inline cudaError_t launch_chained(K kernel, int grid, int block, size_t smem, cudaStream_t stream, const P&... params) {
+inline cudaError_t launch_grid(K kernel, dim3 grid, int block, size_t smem, cudaStream_t stream, const P&... params) {
   return launch_clusters(kernel, 1, grid, block, smem, stream, params...);
+}
+template <class K, class... P>
+inline cudaError_t launch_chained(K kernel, int grid, int block, size_t smem, cudaStream_t stream, const P&... params) {
+  return launch_grid(kernel, dim3((unsigned)grid), block, smem, stream, params...);
 }
 
 // Whether something was done once for a device (relaxed atomics: a race only

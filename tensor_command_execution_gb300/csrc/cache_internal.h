@@ -120,6 +120,77 @@ cudaError_t attend_mma_launch16(int dtype, const AttendParams& p, cudaStream_t s
 cudaError_t attend_mma_launch4(int dtype, const AttendParams& p, cudaStream_t stream);
 constexpr int kAttendHeads = 8, kAttendMmaHeads = 16;
 
+// ---- attention of drafted tokens (cache_drafts*.cu) ----------------------------
+// The attention above with drafts * (query heads to a kv head) rows in the
+// place of a kv head's query heads: `group` counts them, draft outermost.
+// lengths include the drafts; `window` reaches from the last token back to the
+// first that any draft sees.
+struct DraftParams : AttendParams {
+  int32_t drafts;
+  FastDiv32 per;              // by query heads to a kv head
+  int64_t q_draft, out_draft, lse_draft;  // strides of the drafts
+  const int32_t* parents;     // NULL: each draft goes on from the one before
+  int64_t parent_st[2];
+  int32_t near;               // the caller's window, 0: none
+  float2* stats;              // optional: maximum and sum, [rows][kv heads][group]
+  float* weights;             // optional: [rows, kv heads, tokens], added to
+  int64_t w_st[2];
+};
+constexpr int kDraftCtas = 152 * 2;     // bounds the workspace
+constexpr int kDraftRows = 64;          // rows of a block, at most
+// copy: bytes of a copy that suits every row of the cache, 16 or 4, or 0
+cudaError_t drafts_mma_launch16(int dtype, const DraftParams& p, cudaStream_t stream);
+cudaError_t drafts_mma_launch4(int dtype, const DraftParams& p, cudaStream_t stream);
+cudaError_t drafts_mma_launch0(int dtype, const DraftParams& p, cudaStream_t stream);
+cudaError_t drafts_f32_launch16(const DraftParams& p, cudaStream_t stream);
+cudaError_t drafts_f32_launch4(const DraftParams& p, cudaStream_t stream);
+
+// ---- what is kept (cache_keep.cu) -----------------------------------------------
+struct PathParams {
+  const int32_t *tokens, *choices, *parents;  // (parents NULL: a chain)
+  int64_t token_st[2], choice_st[2], parent_st[2];
+  int32_t *path, *counts, *last;
+  int64_t path_st[2], counts_st, last_st;
+  int32_t rows, drafts;
+  int32_t* status;
+};
+cudaError_t path_launch(const PathParams& p, cudaStream_t stream);
+
+// What the accepted tokens' move and the eviction share: rows that are cut.
+struct KeepParams {
+  const int32_t *tables, *lengths, *refs;
+  int32_t *lengths_out, *refs_out;
+  int64_t table_st;
+  int32_t rows, columns, pages;
+  FastDiv32 page;
+  int32_t heads, pieces;      // a token's access units: heads times the pieces of one
+  int32_t unit;               // bytes of one
+  FastDiv32 per_head;         // by pieces
+  int32_t* status;
+  // accept
+  const int32_t *path, *counts;
+  int64_t path_st;            // rows; a row's entries are dense
+  int32_t drafts;
+  // evict
+  int32_t budget, recent, layers;
+  int32_t* kept;              // [rows][layers][heads][budget]
+};
+struct KeepPool {
+  uint8_t* ptr;
+  int64_t st[3];              // page, slot, head (bytes)
+};
+struct KeepPools {
+  KeepPool pool[CMD_CACHE_MAX_POOLS];
+  int32_t n;
+};
+struct KeepLayers {
+  KeepPool pool[CMD_CACHE_MAX_LAYERS][2];
+  float* weights[CMD_CACHE_MAX_LAYERS];
+  int64_t w_st[CMD_CACHE_MAX_LAYERS][2];
+};
+cudaError_t accept_launch(const KeepParams& p, const KeepPools& pools, cudaStream_t stream);
+cudaError_t evict_launch(const KeepParams& p, const KeepLayers& layers, cudaStream_t stream);
+
 // ---- pages (cache_pages.cu) -----------------------------------------------------
 // The pools of a call; MAX of them at most (a launch's parameters are copied
 // to the device with it, so few pools go in a short list).

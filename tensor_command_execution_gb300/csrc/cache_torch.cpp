@@ -424,6 +424,197 @@ PyObject* py_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// attention_drafts(q, k_cache, v_cache, tables, lengths, parents, scale, softcap, window, weights, out, lse, return_lse,
+// workspace, status) -> out or (out, lse)
+PyObject* py_drafts(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    expect(n, 15);
+    const at::Tensor& q = tensor(a[0], "q");
+    const Where w(q);
+    cmd_drafts_args x = {};
+    x.q = operand(a[0], "q");
+    x.k_cache = operand(a[1], "k_cache");
+    x.v_cache = operand(a[2], "v_cache");
+    x.tables = operand(a[3], "tables");
+    x.lengths = operand(a[4], "lengths");
+    x.parents = optional(a[5], "parents");
+    if (a[5] != Py_None && !x.parents.ptr && x.q.rank == 4 && x.q.sizes[0] > 0) raise(PyExc_ValueError, "parents is empty");
+    if (x.q.rank != 4 || x.k_cache.rank != 4 || x.tables.rank != 2)
+      raise(PyExc_ValueError, "q and the caches have rank 4 and tables has rank 2");
+    const int64_t dim = x.q.sizes[3];
+    x.scale = (float)(a[6] != Py_None ? number(a[6]) : dim > 0 ? 1.0 / std::sqrt((double)dim) : 1.0);
+    x.softcap = (float)number(a[7]);
+    x.window = integer(a[8], "window");
+    x.weights = optional(a[9], "weights");
+    at::Tensor out, lse;
+    c10::DataPtr workspace;
+    x.out = a[10] == Py_None ? describe(out = w.empty(q.sizes(), q.scalar_type()), "out") : operand(a[10], "out");
+    const bool with_lse = PyObject_IsTrue(a[12]);
+    if (a[11] != Py_None) x.lse = operand(a[11], "lse");
+    else if (with_lse) x.lse = describe(lse = w.empty({q.size(0), q.size(1), q.size(2)}, at::kFloat), "lse");
+    const int64_t drafts = x.q.sizes[1], heads = x.q.sizes[2], kv = x.k_cache.sizes[2];
+    if (a[13] != Py_None) {
+      const at::Tensor& t = tensor(a[13], "workspace");
+      if (!t.is_contiguous()) raise(PyExc_ValueError, "workspace is not contiguous");
+      x.workspace = t.data_ptr();
+      x.workspace_bytes = (int64_t)t.nbytes();
+    } else if (heads > 0 && kv > 0 && heads % kv == 0 && heads <= INT32_MAX && dim <= CMD_CACHE_MAX_DIM && drafts > 0 &&
+               drafts <= CMD_CACHE_MAX_DRAFTS) {
+      check(cmd_drafts_workspace(x.q.sizes[0], (int32_t)drafts, (int32_t)heads, (int32_t)kv, (int32_t)dim,
+                                 x.weights.ptr ? x.tables.sizes[1] * x.k_cache.sizes[1] : 0, &x.workspace_bytes),
+            "cmd_drafts_workspace");
+      workspace = w.scratch(x.workspace_bytes);
+      x.workspace = workspace.get();
+    }
+    x.status = status_word(a[14]);
+    same_device(w, a[14], "status");
+    const char* names[] = {"q", "k_cache", "v_cache", "tables", "lengths", "parents"};
+    for (int i = 0; i < 6; ++i) same_device(w, a[i], names[i]);
+    const int outs[] = {9, 10, 11};
+    const char* out_names[] = {"weights", "out", "lse"};
+    for (int i = 0; i < 3; ++i) {
+      same_device(w, a[outs[i]], out_names[i]);
+      writable(a[outs[i]], out_names[i]);
+    }
+    same_device(w, a[13], "workspace");
+    check(cmd_attention_drafts(&x, w.stream), "cmd_attention_drafts");
+    for (int i : outs) written(a[i]);
+    PyObject* o = result(a[10], out);
+    return with_lse ? pack({o, result(a[11], lse)}) : o;
+  });
+}
+
+// draft_path(tokens, choices, parents, out, status) -> (path, counts, last)
+PyObject* py_path(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    expect(n, 5);
+    const Where w(tensor(a[0], "tokens"));
+    cmd_path_args x = {};
+    x.tokens = operand(a[0], "tokens");
+    x.choices = operand(a[1], "choices");
+    x.parents = optional(a[2], "parents");
+    if (x.tokens.rank != 2) raise(PyExc_ValueError, "tokens has rank 2");
+    const int64_t rows = x.tokens.sizes[0];
+    at::Tensor made[3];
+    PyObject* out[3] = {item(a[3], 0, 3), item(a[3], 1, 3), item(a[3], 2, 3)};
+    x.path = output(out[0], w, {rows, x.tokens.sizes[1]}, &made[0], "path");
+    x.counts = output(out[1], w, {rows}, &made[1], "counts");
+    x.last = output(out[2], w, {rows}, &made[2], "last");
+    x.status = status_word(a[4]);
+    same_device(w, a[4], "status");
+    same_device(w, a[1], "choices");
+    same_device(w, a[2], "parents");
+    check(cmd_draft_path(&x, w.stream), "cmd_draft_path");
+    for (PyObject* o : out) written(o);
+    return pack({result(out[0], made[0]), result(out[1], made[1]), result(out[2], made[2])});
+  });
+}
+
+// The items of a list or tuple.
+struct Items {
+  PyObject* list;
+  bool tuple;
+  Py_ssize_t n;
+  Items(PyObject* o, const char* what) : list(o), tuple(PyTuple_Check(o)) {
+    if (!tuple && !PyList_Check(o)) raise(PyExc_TypeError, std::string(what) + " is no list or tuple");
+    n = tuple ? PyTuple_GET_SIZE(o) : PyList_GET_SIZE(o);
+  }
+  PyObject* operator[](Py_ssize_t i) const { return tuple ? PyTuple_GET_ITEM(list, i) : PyList_GET_ITEM(list, i); }
+};
+cmd_operand written_operand(PyObject* o, const Where& w, const char* name) {
+  const cmd_operand x = operand(o, name);
+  same_device(w, o, name);
+  writable(o, name);
+  return x;
+}
+
+// cache_accept(tables, lengths, refs, path, counts, pools, drafts, out, status) -> (lengths, refs)
+PyObject* py_accept(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    expect(n, 9);
+    const Where w(tensor(a[0], "tables"));
+    cmd_accept_args x = {};
+    x.tables = operand(a[0], "tables");
+    x.lengths = operand(a[1], "lengths");
+    x.refs = operand(a[2], "refs");
+    x.path = operand(a[3], "path");
+    x.counts = operand(a[4], "counts");
+    if (x.tables.rank != 2 || x.refs.rank != 1 || x.path.rank != 2)
+      raise(PyExc_ValueError, "tables and path have rank 2 and refs has rank 1");
+    if (a[6] != Py_None && integer(a[6], "drafts") != x.path.sizes[1])
+      raise(PyExc_ValueError, "path lists " + std::to_string(x.path.sizes[1]) + " drafts");
+    const Items pools(a[5], "pools");
+    if (pools.n < 1 || pools.n > CMD_CACHE_MAX_POOLS) raise(PyExc_ValueError, "pools are 1 to 64 tensors");
+    cmd_operand list[CMD_CACHE_MAX_POOLS];
+    for (Py_ssize_t i = 0; i < pools.n; ++i) list[i] = written_operand(pools[i], w, "a pool");
+    x.pools = list;
+    x.n_pools = (int32_t)pools.n;
+    at::Tensor made[2];
+    PyObject* out[2] = {item(a[7], 0, 2), item(a[7], 1, 2)};
+    x.lengths_out = output(out[0], w, {x.tables.sizes[0]}, &made[0], "lengths_out");
+    x.refs_out = output(out[1], w, {x.refs.sizes[0]}, &made[1], "refs_out");
+    x.status = status_word(a[8]);
+    same_device(w, a[8], "status");
+    const char* names[] = {"tables", "lengths", "refs", "path", "counts"};
+    for (int i = 0; i < 5; ++i) same_device(w, a[i], names[i]);
+    check(cmd_cache_accept(&x, w.stream), "cmd_cache_accept");
+    for (PyObject* o : out) written(o);
+    for (Py_ssize_t i = 0; i < pools.n; ++i) written(pools[i]);
+    return pack({result(out[0], made[0]), result(out[1], made[1])});
+  });
+}
+
+// cache_evict(tables, lengths, refs, layers, budget, recent, out, status) -> (lengths, refs)
+PyObject* py_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    expect(n, 8);
+    const Where w(tensor(a[0], "tables"));
+    cmd_evict_args x = {};
+    x.tables = operand(a[0], "tables");
+    x.lengths = operand(a[1], "lengths");
+    x.refs = operand(a[2], "refs");
+    if (x.tables.rank != 2 || x.refs.rank != 1) raise(PyExc_ValueError, "tables has rank 2 and refs has rank 1");
+    const Items layers(a[3], "layers");
+    if (layers.n < 1 || layers.n > CMD_CACHE_MAX_LAYERS) raise(PyExc_ValueError, "layers are 1 to 32 triples of tensors");
+    cmd_operand list[3][CMD_CACHE_MAX_LAYERS];
+    const char* parts[] = {"a k_cache", "a v_cache", "weights"};
+    for (Py_ssize_t i = 0; i < layers.n; ++i) {
+      const Items layer(layers[i], "a layer");
+      if (layer.n != 3) raise(PyExc_ValueError, "a layer is (k_cache, v_cache, weights)");
+      for (int j = 0; j < 3; ++j) list[j][i] = written_operand(layer[j], w, parts[j]);
+    }
+    if (list[0][0].rank != 4) raise(PyExc_ValueError, "a k_cache has rank 4");
+    x.k_caches = list[0];
+    x.v_caches = list[1];
+    x.weights = list[2];
+    x.n_layers = (int32_t)layers.n;
+    x.budget = integer(a[4], "budget");
+    x.recent = integer(a[5], "recent");
+    at::Tensor made[2];
+    c10::DataPtr workspace;
+    PyObject* out[2] = {item(a[6], 0, 2), item(a[6], 1, 2)};
+    x.lengths_out = output(out[0], w, {x.tables.sizes[0]}, &made[0], "lengths_out");
+    x.refs_out = output(out[1], w, {x.refs.sizes[0]}, &made[1], "refs_out");
+    const int64_t heads = list[0][0].sizes[2];
+    if (heads > 0 && heads <= INT32_MAX && x.budget >= 0) {
+      check(cmd_evict_workspace(x.tables.sizes[0], x.n_layers, (int32_t)heads, x.budget, &x.workspace_bytes), "cmd_evict_workspace");
+      workspace = w.scratch(x.workspace_bytes);
+      x.workspace = workspace.get();
+    }
+    x.status = status_word(a[7]);
+    same_device(w, a[7], "status");
+    const char* names[] = {"tables", "lengths", "refs"};
+    for (int i = 0; i < 3; ++i) same_device(w, a[i], names[i]);
+    check(cmd_cache_evict(&x, w.stream), "cmd_cache_evict");
+    for (PyObject* o : out) written(o);
+    for (Py_ssize_t i = 0; i < layers.n; ++i) {
+      const Items layer(layers[i], "a layer");
+      for (int j = 0; j < 3; ++j) written(layer[j]);
+    }
+    return pack({result(out[0], made[0]), result(out[1], made[1])});
+  });
+}
+
 // cache_status(status)
 PyObject* py_status(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
@@ -456,6 +647,10 @@ PyMethodDef g_methods[] = {method<py_rope>("rope"),
                            method<py_attend>("attention_decode"),
                            method<py_select>("cache_select"),
                            method<py_compact>("cache_compact"),
+                           method<py_drafts>("attention_drafts"),
+                           method<py_path>("draft_path"),
+                           method<py_accept>("cache_accept"),
+                           method<py_evict>("cache_evict"),
                            method<py_status>("cache_status"),
                            {"set_error", py_set_error, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
