@@ -72,6 +72,7 @@ extern "C" {
 #define CMD_CACHE_FULL_TABLE 4 /* a row would need more columns than its table has; dropped */
 #define CMD_CACHE_NO_PAGES 8  /* the pool had no free page left for a row; dropped */
 #define CMD_CACHE_SHARED_PAGE 16 /* tokens would move into a page that others hold too; left as they are */
+#define CMD_CACHE_TIMEOUT 32 /* a kernel's wait took too long (never expected): its outputs are not valid */
 
 typedef struct cmd_operand {
   void* ptr; /* NULL: absent, where an operand is optional */
@@ -393,7 +394,7 @@ cmd_status cmd_compact_workspace(int64_t pages, int64_t* bytes);
 cmd_status cmd_cache_compact(const cmd_compact_args* args, void* cuda_stream);
 
 /* Wait for cuda_stream, read the status word and clear the bits that it held:
- * CMD_OK for 0, else CMD_ERR_ARG for BAD_PAGE or BAD_INDEX, CMD_ERR_LIMIT for
+ * CMD_OK for 0, else CMD_ERR_DEVICE_TIMEOUT for TIMEOUT, CMD_ERR_ARG for BAD_PAGE or BAD_INDEX, CMD_ERR_LIMIT for
  * FULL_TABLE or NO_PAGES and CMD_ERR_ALIAS for SHARED_PAGE (the first that holds), with the bits in *bits (when non-NULL) and a message. A word may
  * serve several streams: bits that work on another one sets meanwhile stay for
  * the next call. */

@@ -27,7 +27,7 @@ import importlib.util
 from . import CmdError, _build, _check, _P, lib
 
 CMD_CACHE_MAX_DIM, CMD_CACHE_MAX_POOLS, CMD_CACHE_MAX_LAYERS, CMD_CACHE_MAX_DRAFTS = 256, 64, 32, 256
-BAD_PAGE, BAD_INDEX, FULL_TABLE, NO_PAGES, SHARED_PAGE = 1, 2, 4, 8, 16  # bits of the status word
+BAD_PAGE, BAD_INDEX, FULL_TABLE, NO_PAGES, SHARED_PAGE, TIMEOUT = 1, 2, 4, 8, 16, 32  # bits of the status word
 LAYOUTS = {"half": 0, "interleaved": 1}
 SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
 

@@ -861,8 +861,9 @@ namespace {
 constexpr int64_t kDraftHeads = 1 << 20;  // drafts * q_heads, at most
 
 int64_t drafts_parts(int64_t drafts, int64_t q_heads, int64_t kv_heads, int64_t dim) {
-  const int64_t rows = std::min<int64_t>(drafts * (q_heads / kv_heads), cmdx::kDraftRows);
-  return round_up(cmdx::kDraftCtas, 16) * (int64_t)sizeof(cmdx::AttendSplit) + 2 * (int64_t)cmdx::kDraftCtas * rows * (round_up(dim, 4) + 4) * 4;
+  const int64_t group = drafts * (q_heads / kv_heads);
+  const int64_t rows = std::max(std::min<int64_t>(group, cmdx::kDraftRows) * cmdx::kDraftCtas, std::min<int64_t>(group, cmdx::kDraftTcRows) * cmdx::kDraftTcCtas);
+  return round_up(cmdx::kDraftCtas, 16) * (int64_t)sizeof(cmdx::AttendSplit) + 2 * rows * (round_up(dim, 4) + 4) * 4;
 }
 int64_t drafts_workspace(int64_t rows, int64_t drafts, int64_t q_heads, int64_t kv_heads, int64_t dim, bool weights) {
   return drafts_parts(drafts, q_heads, kv_heads, dim) + (weights ? round_up(rows * drafts * q_heads * 8, 16) : 0);
@@ -978,9 +979,13 @@ extern "C" cmd_status cmd_attention_drafts(const cmd_drafts_args* args, void* cu
     const int es = elem_size(a.q.dtype);
     const auto pieces = [&](int n) { return dim * es % n == 0 && vector_rows(a.k_cache, n) && vector_rows(a.v_cache, n); };
     const int copy = pieces(16) ? 16 : pieces(4) ? 4 : 0;
-    p.blocks = (p.group + cmdx::kDraftRows - 1) / cmdx::kDraftRows;
+    const bool tc = copy == 16 && es == 2 && dim <= 128;
+    const int most = tc ? cmdx::kDraftTcRows : cmdx::kDraftRows;
+    p.blocks = (p.group + most - 1) / most;
     p.block_heads = (p.group + p.blocks - 1) / p.blocks;
     p.q_pairs = dim % 2 == 0 && vector_rows(a.q, 4);
+    p.q_vectors = vector_rows(a.q, 16);
+    p.out_vectors = vector_rows(a.out, 16);
     const int64_t row_units = (int64_t)p.kv_heads * p.blocks * (tokens / cmdx::kAttendLeastTile + 2 + cmdx::kAttendMostStart);
     NEED(row_units < 0x7fffffff, CMD_ERR_LIMIT, "a table row's tokens times the heads pass 2^31 tiles of 32");
     const int64_t at_once = std::min<int64_t>(cmdx::kAttendRows, 0x7fffffff / row_units);
@@ -995,10 +1000,16 @@ extern "C" cmd_status cmd_attention_drafts(const cmd_drafts_args* args, void* cu
       p.weights = has_weights ? static_cast<float*>(a.weights.ptr) + r * a.weights.strides[0] : nullptr;
       p.stats = stats ? stats + r * drafts * heads : nullptr;
       const cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
-      const cudaError_t e = es == 4      ? (copy == 16 ? cmdx::drafts_f32_launch16 : cmdx::drafts_f32_launch4)(p, stream)
-                            : copy == 16 ? cmdx::drafts_mma_launch16(a.q.dtype, p, stream)
-                            : copy == 4  ? cmdx::drafts_mma_launch4(a.q.dtype, p, stream)
-                                         : cmdx::drafts_mma_launch0(a.q.dtype, p, stream);
+      cudaError_t e = es == 4      ? (copy == 16 ? cmdx::drafts_f32_launch16 : cmdx::drafts_f32_launch4)(p, stream)
+                      : tc         ? cmdx::drafts_tc_launch(a.q.dtype, p, stream)
+                      : copy == 16 ? cmdx::drafts_mma_launch16(a.q.dtype, p, stream)
+                      : copy == 4  ? cmdx::drafts_mma_launch4(a.q.dtype, p, stream)
+                                   : cmdx::drafts_mma_launch0(a.q.dtype, p, stream);
+      if (e == cudaSuccess && has_weights)
+        e = es == 4      ? (copy == 16 ? cmdx::weigh_f32_launch16 : cmdx::weigh_f32_launch4)(p, stream)
+            : copy == 16 ? cmdx::weigh_mma_launch16(a.q.dtype, p, stream)
+            : copy == 4  ? cmdx::weigh_mma_launch4(a.q.dtype, p, stream)
+                         : cmdx::weigh_mma_launch0(a.q.dtype, p, stream);
       if (e != cudaSuccess) return launched(e);
     }
     return CMD_OK;
@@ -1274,7 +1285,9 @@ extern "C" cmd_status cmd_cache_status(int32_t* status, int32_t* bits, void* cud
     if (word & CMD_CACHE_FULL_TABLE) msg += " a table row had no room;";
     if (word & CMD_CACHE_NO_PAGES) msg += " the pool had no free page;";
     if (word & CMD_CACHE_SHARED_PAGE) msg += " tokens would have moved into a page that others hold;";
+    if (word & CMD_CACHE_TIMEOUT) msg += " a kernel's wait took too long, and it gave up;";
     msg.pop_back();
+    if (word & CMD_CACHE_TIMEOUT) return host_fail(CMD_ERR_DEVICE_TIMEOUT, msg);
     if (word & (CMD_CACHE_BAD_PAGE | CMD_CACHE_BAD_INDEX)) return host_fail(CMD_ERR_ARG, msg);
     return host_fail(word & (CMD_CACHE_FULL_TABLE | CMD_CACHE_NO_PAGES) ? CMD_ERR_LIMIT : CMD_ERR_ALIAS, msg);
   });

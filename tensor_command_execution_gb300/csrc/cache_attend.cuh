@@ -249,6 +249,21 @@ __device__ __forceinline__ float4 attend_merged(const float* s, int warp_pitch, 
   return o;
 }
 
+// Where a segment's part goes (NULL: the segment is all of its row and group);
+// one thread says in the list of splits where the parts of a row that begins
+// here are.
+__device__ __forceinline__ float* attend_part(const AttendParams& p, const AttendShare& w, const AttendSegment& g, bool one) {
+  const int slot = 2 * blockIdx.x + (g.first <= w.begin ? 0 : 1);
+  float* part = g.whole() ? nullptr : p.parts + (int64_t)slot * p.block_heads * attend_pitch(p.dim);
+  if (one && g.first >= w.begin) {
+    AttendSplit split = {g.row, g.group, slot, 0};
+    if (part) split.parts = w.owner(g.first + g.row_tiles - 1) - w.index + 1;
+    if (p.split_by_row) p.splits[g.row * p.kv_heads * p.blocks + g.group] = split;
+    else if (part) p.splits[blockIdx.x] = split;
+  }
+  return part;
+}
+
 // Ends a segment. The warps' states lie in shared memory, query head q of
 // warp w (of WARPS that hold states of the same heads) at state + w *
 // warp_pitch + q * pitch (pitch = attend_pitch of something at least dim). All
@@ -257,15 +272,7 @@ template <class T, int WARPS, int THREADS = WARPS * 32, class P>
 __device__ __forceinline__ void attend_finish(const P& p, const AttendShare& w, const AttendSegment& g,
                                               const AttendHeads& h, const float* state, int warp_pitch, int pitch) {
   const int part_pitch = attend_pitch(p.dim), quads = part_pitch / 4 - 1;
-  const int slot = 2 * blockIdx.x + (g.first <= w.begin ? 0 : 1);
-  float* part = g.whole() ? nullptr : p.parts + (int64_t)slot * p.block_heads * part_pitch;
-  if (threadIdx.x == 0 && g.first >= w.begin) {
-    // the row begins here: say where its parts are
-    AttendSplit split = {g.row, g.group, slot, 0};
-    if (part) split.parts = w.owner(g.first + g.row_tiles - 1) - w.index + 1;
-    if (p.split_by_row) p.splits[g.row * p.kv_heads * p.blocks + g.group] = split;
-    else if (part) p.splits[blockIdx.x] = split;
-  }
+  float* part = attend_part(p, w, g, threadIdx.x == 0);
   __syncthreads();  // the warps' states are complete
   for (int i = threadIdx.x; i < h.heads * quads; i += THREADS) {
     const int q = i / quads, d = 4 * (i - q * quads);

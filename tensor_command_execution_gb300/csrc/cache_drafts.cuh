@@ -51,16 +51,45 @@ struct DraftTree {
     const uint32_t j = (uint32_t)(t - base);
     return j < (uint32_t)p.drafts && (seen[i][j >> 5] >> (j & 31) & 1);
   }
+  // Which of the tokens t .. t + 31 draft i sees, a bit each.
+  __device__ __forceinline__ uint32_t sees_of_32(const DraftParams& p, int i, int t, int base) const {
+    const int first = max(from[i] - t, 0), last = min(base - t, 32);  // (context tokens: bits [first, last))
+    uint32_t bits = first < last ? (~0u >> (32 - (last - first))) << first : 0u;
+    const int j = t - base;  // bit k stands for draft j + k
+    if (j > -32 && from[i] != kNever) {
+      const int word = j >> 5;  // (rounded down: j may be negative)
+      const uint32_t lo = word >= 0 && word < kDraftWords && word * 32 < p.drafts ? seen[i][word] : 0u;
+      const uint32_t hi = word + 1 < kDraftWords && (word + 1) * 32 < p.drafts ? seen[i][word + 1] : 0u;
+      bits |= __funnelshift_r(lo, hi, j & 31);
+    }
+    return bits;
+  }
 };
 
-// Fills s for a row whose drafts begin at `base`; all THREADS threads of the
-// CTA call it. Ancestors are found by doubling: a draft's list takes in that
-// of the draft it points to, which then points where that one did.
-template <int THREADS>
+// A barrier of all threads of the CTA, and one of THREADS of them (whole warps).
+struct WholeCta {
+  static __device__ __forceinline__ void sync() { __syncthreads(); }
+  static __device__ __forceinline__ bool any(bool x) { return __syncthreads_or(x); }
+};
+template <int THREADS, int ID>
+struct SomeThreads {
+  static __device__ __forceinline__ void sync() { asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory"); }
+  static __device__ __forceinline__ bool any(bool x) {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+                 : "=r"(r) : "r"((uint32_t)x), "n"(ID), "n"(THREADS) : "memory");
+    return r != 0;
+  }
+};
+
+// Fills s for a row whose drafts begin at `base`; THREADS threads, the
+// CTA's first, call it. Ancestors are found by doubling: a draft's list takes in
+// that of the draft it points to, which then points where that one did.
+template <int THREADS, class B = WholeCta>
 __device__ __forceinline__ void draft_tree(const DraftParams& p, DraftTree& s, int row, int base) {
   constexpr int kEach = (CMD_CACHE_MAX_DRAFTS + THREADS - 1) / THREADS;
   const int words = (p.drafts + 31) >> 5;
-  __syncthreads();  // the tree before it is no longer read
+  B::sync();  // the tree before it is no longer read
   bool going = false;
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
@@ -81,7 +110,7 @@ __device__ __forceinline__ void draft_tree(const DraftParams& p, DraftTree& s, i
     s.from[i] = parent;
     going = going || parent >= 0;
   }
-  while (__syncthreads_or(going)) {
+  while (B::any(going)) {
     uint32_t add[kEach][kDraftWords];
     int next[kEach];
 #pragma unroll
@@ -95,7 +124,7 @@ __device__ __forceinline__ void draft_tree(const DraftParams& p, DraftTree& s, i
       for (int w = 0; w < kDraftWords; ++w) add[e][w] = at >= 0 && w < words ? s.seen[at][w] : 0u;
       if (at >= 0) next[e] = s.from[at];
     }
-    __syncthreads();
+    B::sync();
     going = false;
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
@@ -117,7 +146,7 @@ __device__ __forceinline__ void draft_tree(const DraftParams& p, DraftTree& s, i
     s.depth[i] = depth;
     s.from[i] = s.from[i] == -2 ? kNever : p.near ? max(0, base + depth + 1 - p.near) : 0;
   }
-  __syncthreads();
+  B::sync();
   if (p.near && p.near < p.drafts) {  // (a chain of ancestors may be longer than the window)
     for (int e = 0; e < kEach; ++e) {
       const int i = threadIdx.x + e * THREADS;
@@ -131,7 +160,7 @@ __device__ __forceinline__ void draft_tree(const DraftParams& p, DraftTree& s, i
         s.seen[i][w] = mine;
       }
     }
-    __syncthreads();
+    B::sync();
   }
 }
 

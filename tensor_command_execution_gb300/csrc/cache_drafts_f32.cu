@@ -296,32 +296,35 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_f32_kernel(const __grid_con
 }
 
 template <int DP, int R>
-cudaError_t launch(const DraftParams& p, cudaStream_t stream) {
+cudaError_t launch(bool weights, DraftParams p, cudaStream_t stream) {
   using S = Shape<DP, R>;
   static PerDevice ready, weigh_ready;  // (static storage: zero before first use)
-  cudaError_t e = allow_smem(drafts_f32_kernel<DP, R>, S::kSmem, ready);
-  if (e == cudaSuccess)
-    e = attend_launch<float>(drafts_f32_kernel<DP, R>, p, 2, 152 * S::kCtas, kThreads, S::kSmem, kTile, stream, false);
-  if (e != cudaSuccess || !p.weights) return e;
-  DraftParams w = p;
-  w.blocks = w.sides = 1;
-  w.start_units = 0;
+  if (!weights) {
+    const cudaError_t e = allow_smem(drafts_f32_kernel<DP, R>, S::kSmem, ready);
+    if (e != cudaSuccess) return e;
+    return attend_launch<float>(drafts_f32_kernel<DP, R>, p, 2, 152 * S::kCtas, kThreads, S::kSmem, kTile, stream, false);
+  }
+  p.blocks = p.sides = 1;
+  p.start_units = 0;
   constexpr int smem = (2 * S::kKeys + S::kRows * S::kPitch) * 4 + (S::kSmem - S::kRest);
-  e = allow_smem(weigh_f32_kernel<DP, R>, smem, weigh_ready);
+  const cudaError_t e = allow_smem(weigh_f32_kernel<DP, R>, smem, weigh_ready);
   if (e != cudaSuccess) return e;
-  return launch_chained(weigh_f32_kernel<DP, R>, 152 * 2, kThreads, (size_t)smem, stream, w);
+  return launch_chained(weigh_f32_kernel<DP, R>, 152 * 2, kThreads, (size_t)smem, stream, p);
 }
 
 template <int R>
-cudaError_t launch_dim(const DraftParams& p, cudaStream_t stream) {
-  if (p.dim <= 64) return launch<64, R>(p, stream);
-  return p.dim <= 128 ? launch<128, R>(p, stream) : launch<256, R>(p, stream);
+cudaError_t by_dim(bool weights, const DraftParams& p, cudaStream_t stream) {
+  if (p.dim <= 64) return launch<64, R>(weights, p, stream);
+  return p.dim <= 128 ? launch<128, R>(weights, p, stream) : launch<256, R>(weights, p, stream);
 }
 
 }  // namespace
 
 cudaError_t CMDX_COPY_NAME(drafts_f32_launch)(const DraftParams& p, cudaStream_t stream) {
-  return p.block_heads <= 16 ? launch_dim<2>(p, stream) : launch_dim<8>(p, stream);
+  return p.block_heads <= 16 ? by_dim<2>(false, p, stream) : by_dim<8>(false, p, stream);
+}
+cudaError_t CMDX_COPY_NAME(weigh_f32_launch)(const DraftParams& p, cudaStream_t stream) {
+  return p.group <= 16 ? by_dim<2>(true, p, stream) : by_dim<8>(true, p, stream);
 }
 
 }  // namespace cmdx

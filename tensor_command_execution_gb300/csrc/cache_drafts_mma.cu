@@ -408,36 +408,43 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_mma_kernel(const __grid_con
 template <class T, int DP, int MT>
 cudaError_t launch(const DraftParams& p, cudaStream_t stream) {
   using S = Shape<DP, MT>;
-  static PerDevice ready, weigh_ready;  // (static storage: zero before first use)
-  cudaError_t e = allow_smem(drafts_mma_kernel<T, DP, MT>, S::kSmem, ready);
-  if (e == cudaSuccess)
-    e = attend_launch<T>(drafts_mma_kernel<T, DP, MT>, p, 2, 152 * S::kCtas, kThreads, S::kSmem, kTile, stream, false);
-  if (e != cudaSuccess || !p.weights) return e;
-  DraftParams w = p;
-  w.blocks = w.sides = 1;
-  w.start_units = 0;
-  constexpr int smem = S::kSmem - 2 * S::kKeys;
-  e = allow_smem(weigh_mma_kernel<T, DP, MT>, smem, weigh_ready);
+  static PerDevice ready;  // (static storage: zero before first use)
+  const cudaError_t e = allow_smem(drafts_mma_kernel<T, DP, MT>, S::kSmem, ready);
   if (e != cudaSuccess) return e;
-  return launch_chained(weigh_mma_kernel<T, DP, MT>, 152 * 2, kThreads, (size_t)smem, stream, w);
+  return attend_launch<T>(drafts_mma_kernel<T, DP, MT>, p, 2, 152 * S::kCtas, kThreads, S::kSmem, kTile, stream, false);
+}
+template <class T, int DP, int MT>
+cudaError_t weigh(DraftParams p, cudaStream_t stream) {
+  p.blocks = p.sides = 1;
+  p.start_units = 0;
+  constexpr int smem = Shape<DP, MT>::kSmem - 2 * Shape<DP, MT>::kKeys;
+  static PerDevice ready;  // (static storage: zero before first use)
+  const cudaError_t e = allow_smem(weigh_mma_kernel<T, DP, MT>, smem, ready);
+  if (e != cudaSuccess) return e;
+  return launch_chained(weigh_mma_kernel<T, DP, MT>, 152 * 2, kThreads, (size_t)smem, stream, p);
 }
 
 template <class T, int DP>
-cudaError_t launch_rows(const DraftParams& p, cudaStream_t stream) {
-  if (p.block_heads <= 16) return launch<T, DP, 1>(p, stream);
-  if (CMDX_COPY == 16 && p.block_heads <= 32) return launch<T, DP, CMDX_COPY == 16 ? 2 : 4>(p, stream);
-  return launch<T, DP, 4>(p, stream);
+cudaError_t by_rows(bool weights, const DraftParams& p, cudaStream_t stream) {
+  const int rows = weights ? p.group : p.block_heads;
+  if (rows <= 16) return weights ? weigh<T, DP, 1>(p, stream) : launch<T, DP, 1>(p, stream);
+  constexpr int two = CMDX_COPY == 16 ? 2 : 4;
+  if (rows <= 16 * two) return weights ? weigh<T, DP, two>(p, stream) : launch<T, DP, two>(p, stream);
+  return weights ? weigh<T, DP, 4>(p, stream) : launch<T, DP, 4>(p, stream);
 }
 template <class T>
-cudaError_t launch_type(const DraftParams& p, cudaStream_t stream) {
-  if (p.dim <= 64) return launch_rows<T, 64>(p, stream);
-  return p.dim <= 128 ? launch_rows<T, 128>(p, stream) : launch_rows<T, 256>(p, stream);
+cudaError_t by_dim(bool weights, const DraftParams& p, cudaStream_t stream) {
+  if (p.dim <= 64) return by_rows<T, 64>(weights, p, stream);
+  return p.dim <= 128 ? by_rows<T, 128>(weights, p, stream) : by_rows<T, 256>(weights, p, stream);
 }
 
 }  // namespace
 
 cudaError_t CMDX_COPY_NAME(drafts_mma_launch)(int dtype, const DraftParams& p, cudaStream_t stream) {
-  return dtype == CMD_F16 ? launch_type<__half>(p, stream) : launch_type<__nv_bfloat16>(p, stream);
+  return dtype == CMD_F16 ? by_dim<__half>(false, p, stream) : by_dim<__nv_bfloat16>(false, p, stream);
+}
+cudaError_t CMDX_COPY_NAME(weigh_mma_launch)(int dtype, const DraftParams& p, cudaStream_t stream) {
+  return dtype == CMD_F16 ? by_dim<__half>(true, p, stream) : by_dim<__nv_bfloat16>(true, p, stream);
 }
 
 }  // namespace cmdx

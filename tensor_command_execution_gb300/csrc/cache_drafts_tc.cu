@@ -1,0 +1,620 @@
+// cache_drafts_tc.cu - attention of drafted tokens over a paged cache of
+// 16-bit numbers on the CTA-wide tensor instructions (tcgen05).
+//
+// A CTA takes 128 query rows (drafts times the query heads of a kv head) at a
+// time, or 256 as two sets of 128, against tiles of 128 tokens: S = Q K^T into
+// tensor memory, the softmax there, O += P V with P read from tensor memory. Two
+// groups of four softmax warps, a thread to a query row, take turns, so that the
+// tensor units work on one group's products while the other's exponentials are
+// worked out: with 256 rows a group has its own rows (and a key or value is read
+// once for both), with 128 its own tiles, and the two halves are joined at the
+// end of a segment. One warp issues the products, three copy keys and values
+// (16-byte asynchronous copies, zeros where a row has no token) into a ring in
+// the layout that the products read.
+//
+// A weight is held as the sum of two 16-bit numbers, as in cache_attend_mma.cu:
+// P takes exactly the columns of S that it came from. O is rescaled only when a
+// row's maximum has grown by more than kSlack (in powers of two) since it was
+// last taken: weights are up to 2^kSlack then, and f16 ones are lifted by so
+// much less (2^11): no finer than 2^-36 of the row's largest weight.
+#include "cache_drafts.cuh"
+#include "cache_attend_ring.cuh"
+#include "cache_mma.cuh"
+#include "exec_pipe.cuh"
+#include "tcgen05.cuh"
+
+namespace cmdx {
+
+namespace {
+
+constexpr int kGroup = 128;                   // threads of a softmax group, and query rows
+constexpr int kLoaders = 96;
+constexpr int kThreads = 2 * kGroup + 32 + kLoaders;
+constexpr int kTile = 128;                    // tokens
+constexpr uint64_t kPatience = 2000000000;    // ns: no wait takes longer
+
+template <class T>
+constexpr float kSlack = 8.0f;
+template <>
+constexpr float kSlack<__half> = 4.0f;
+template <class T>
+constexpr float kRaise = 1.0f;  // what weights are multiplied by
+template <>
+constexpr float kRaise<__half> = 2048.0f;
+
+template <int DP, bool WIDE>
+struct Shape {
+  static constexpr int kRows = WIDE ? 256 : 128;
+  static constexpr int kSlot = kTile * DP * 2;    // keys or values of a tile
+  static constexpr int kSlots = DP == 64 ? 8 : 4;
+  static constexpr int kQueries = kRows * DP * 2;
+  static constexpr int kRing = kQueries;
+  static constexpr int kRest = kRing + kSlots * kSlot;
+  static constexpr int kScores = 0;               // columns of tensor memory: S of each group, then O
+  static constexpr int kOut = 256;
+};
+
+constexpr int kHereTiles = 8;
+struct State {
+  uint64_t full[8], empty[8], scores[2], weights[2], done[2], queries, end;
+  uint32_t tmem;
+  uint32_t stop;                       // a wait ran out of time
+  uint32_t here[kHereTiles][4];        // which tokens of a tile have a page
+  uint32_t bad[kHereTiles];            // the last of these tiles (counted from 1) whose values are not all finite
+  float2 part[2][kGroup];              // maximum and sum of a group's rows
+  int64_t k[2][kTile], v[2][kTile];    // offsets of a tile's rows, -1: none
+};
+template <int DP, bool WIDE>
+constexpr int kSmem = Shape<DP, WIDE>::kRest + (int)(sizeof(State) + sizeof(DraftTree) + sizeof(AttendRows)) + 1024;
+
+// A wait that gives up (for the whole CTA) after kPatience.
+__device__ __forceinline__ void wait(State& s, uint32_t bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return;
+  volatile uint32_t* stop = &s.stop;
+  const uint64_t t0 = global_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*stop) return;
+    if (global_ns() - t0 > kPatience) {
+      *stop = 1;
+      return;
+    }
+  }
+}
+
+template <class T>
+constexpr uint32_t kExponent = 0x7f807f80u;
+template <>
+constexpr uint32_t kExponent<__half> = 0x7c007c00u;
+// The parts of x (two numbers of type T) that are infinite or NaN, as a mask.
+template <class T>
+__device__ __forceinline__ uint32_t not_finite(uint32_t x) {
+  constexpr uint32_t lo = kExponent<T> & 0xffffu, hi = kExponent<T> & 0xffff0000u;
+  return ((x & lo) == lo ? 0xffffu : 0u) | ((x & hi) == hi ? 0xffff0000u : 0u);
+}
+
+// ---- the copies -----------------------------------------------------------------
+template <class T, int DP, bool WIDE>
+struct Loader {
+  using S = Shape<DP, WIDE>;
+  static constexpr int kChunks = DP / 8, kOver = kLoaders / kChunks;
+  // (of the groups of copies on their way at most kBehind are left behind when
+  // another has been issued: the products of a tile wait for the keys of the
+  // next, and a slot's next copies for the products of the tile in it)
+  static constexpr int kBehind = 2;
+  const DraftParams& p;
+  State& s;
+  const uint32_t ring;
+  const int tid = threadIdx.x - 2 * kGroup - 32, chunk = tid % kChunks, row0 = tid / kChunks, chunks, used;
+  uint32_t issued = 0, arrived = 0;  // groups: keys and values in turn
+  uint32_t masked = 0;               // a bit for each group on its way, the newest lowest: values of a tile that not all see
+
+  __device__ __forceinline__ Loader(const DraftParams& p_, State& s_, uint32_t ring_)
+      : p(p_), s(s_), ring(ring_), chunks(p_.dim / 8), used((p_.dim + 15) / 16 * 2) {}
+
+  __device__ __forceinline__ void arrive() {
+    const int slot = arrived % S::kSlots;
+    if (masked >> (issued - 1 - arrived) & 1) clear(slot);
+    fence_async_smem();
+    mbar_arrive(smem_u32(&s.full[slot]));
+    ++arrived;
+  }
+  // Values that are not finite become zeros, whatever their weight, and the
+  // softmax group is told: it adds them where they are seen.
+  __device__ __forceinline__ void clear(int slot) {
+    if (chunk >= chunks) return;
+    const uint32_t at = ring + slot * S::kSlot + chunk / 8 * kTile * 128;
+    for (int r = row0; r < kTile; r += kOver) {
+      const uint32_t a = at + swizzled(r, chunk % 8);
+      uint4 x = lds128(a);
+      const uint4 bad = make_uint4(not_finite<T>(x.x), not_finite<T>(x.y), not_finite<T>(x.z), not_finite<T>(x.w));
+      if ((bad.x | bad.y | bad.z | bad.w) == 0) continue;
+      sts128(a, make_uint4(x.x & ~bad.x, x.y & ~bad.y, x.z & ~bad.z, x.w & ~bad.w));
+      *static_cast<volatile uint32_t*>(&s.bad[arrived / 2 % kHereTiles]) = arrived / 2 + 1;
+    }
+  }
+  __device__ __forceinline__ void copy(const T* from, const int64_t* offset, bool mask) {
+    const int slot = issued % S::kSlots;
+    const uint32_t bar = smem_u32(&s.empty[slot]), parity = (issued / S::kSlots + 1) & 1;
+    wait(s, bar, parity);
+    if (chunk < used) {
+      const bool inside = chunk < chunks;
+      const T* at = from + (inside ? chunk * 8 : 0);
+      const uint32_t dst = ring + slot * S::kSlot + chunk / 8 * kTile * 128;
+#pragma unroll 8
+      for (int r = row0; r < kTile; r += kOver) {
+        const int64_t o = offset[r];
+        copy_bytes<16>(dst + swizzled(r, chunk % 8), at + (o >= 0 ? o : 0), o >= 0 && inside ? 16 : 0);
+      }
+    }
+    copy_commit();
+    ++issued;
+    masked = masked << 1 | (mask ? 1u : 0u);
+    if (issued - arrived > kBehind) {
+      copy_wait<kBehind>();
+      arrive();
+    }
+  }
+  __device__ __forceinline__ void drain() {
+    copy_wait<0>();
+    while (arrived != issued) arrive();
+  }
+
+  __device__ __forceinline__ void run(const AttendRows& rows, const AttendShare& share) {
+    int tile = 0;
+    for (AttendSegment g = attend_first(p, rows, share, kTile); g.tiles; g = attend_next(p, rows, share, g, kTile)) {
+      const int kv = attend_heads(p, g.group).kv, base = g.n - p.drafts;
+      DraftLook look[2];
+      const auto look_up = [&](int i) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          look[e] = {0, 0, false};
+          const int t = (g.tile0 + i) * kTile + tid + e * kLoaders;
+          if (tid + e * kLoaders < kTile && i < g.tiles && t >= g.lo && t < g.n) {
+            const uint32_t column = fast_div32(p.page, (uint32_t)t);
+            look[e].inside = true;
+            look[e].slot = t - (int)(column * p.page.d);
+            look[e].page = p.tables[g.row * p.table_st[0] + column * p.table_st[1]];
+          }
+        }
+      };
+      look_up(0);
+      for (int i = 0; i < g.tiles; ++i, ++tile) {
+        const int b = tile & 1;
+        bool all = true;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = tid + e * kLoaders;
+          if (r >= kTile) break;  // (whole warps)
+          bool in = look[e].inside;
+          if (in && (look[e].page < 0 || look[e].page >= p.n_pages)) {
+            report(p.status, CMD_CACHE_BAD_PAGE);
+            in = false;
+          }
+          s.k[b][r] = in ? look[e].page * p.k_st[0] + look[e].slot * p.k_st[1] + kv * p.k_st[2] : -1;
+          s.v[b][r] = in ? look[e].page * p.v_st[0] + look[e].slot * p.v_st[1] + kv * p.v_st[2] : -1;
+          const uint32_t here = __ballot_sync(~0u, in);
+          if (threadIdx.x % 32 == 0) s.here[tile % kHereTiles][r / 32] = here;
+        }
+        look_up(i + 1);
+        SomeThreads<kLoaders, 2>::sync();
+        const uint32_t* here = s.here[tile % kHereTiles];
+        all = (here[0] & here[1] & here[2] & here[3]) == ~0u;
+        const int t0 = (g.tile0 + i) * kTile;
+        copy(static_cast<const T*>(p.k), s.k[b], false);
+        copy(static_cast<const T*>(p.v), s.v[b], !(all && draft_all_seen(p, t0, t0 + kTile, base)));
+      }
+    }
+    drain();
+  }
+};
+
+// ---- the products -----------------------------------------------------------------
+template <class T, int DP, bool WIDE>
+__device__ __forceinline__ void issue(const DraftParams& p, State& s, const AttendRows& rows, const AttendShare& share, uint32_t queries,
+                                      uint32_t ring, uint32_t tmem) {
+  using S = Shape<DP, WIDE>;
+  constexpr bool kBf16 = sizeof(T) == 2 && kSlack<T> == 8.0f;
+  const int steps = (p.dim + 15) / 16;
+  const uint32_t qk = tcgen05_shape(kBf16, kTile, false), pv = tcgen05_shape(kBf16, steps * 16, true);
+  uint32_t tile0 = 0, segments = 0, count[2] = {0, 0};
+  for (AttendSegment g = attend_first(p, rows, share, kTile); g.tiles; g = attend_next(p, rows, share, g, kTile)) {
+    wait(s, smem_u32(&s.queries), segments & 1);
+    ++segments;
+    tcgen05_after_sync();
+    const int items = WIDE ? 2 * g.tiles : g.tiles;
+    const auto scores = [&](int n) {
+      const uint32_t group = tile0 + (WIDE ? n >> 1 : n), at = 2 * group % S::kSlots, w = n & 1;
+      if (!WIDE || w == 0) wait(s, smem_u32(&s.full[at]), (2 * group / S::kSlots) & 1);
+      const uint32_t q = queries + (WIDE ? w * kGroup * 128 : 0), k = ring + at * S::kSlot;
+      for (int e = 0; e < steps; ++e) {
+        const uint32_t slab = e / 4, in = e % 4 * 32;
+        tcgen05_mma(tmem + S::kScores + w * kTile, smem_along_k(q + slab * S::kRows * 128 + in), smem_along_k(k + slab * kTile * 128 + in), qk, e > 0);
+      }
+      tcgen05_commit(smem_u32(&s.scores[w]));
+      if (!WIDE || w == 1) tcgen05_commit(smem_u32(&s.empty[at]));
+    };
+    scores(0);
+    if (items > 1) scores(1);
+    for (int n = 0; n < items; ++n) {
+      const uint32_t group = tile0 + (WIDE ? n >> 1 : n), at = (2 * group + 1) % S::kSlots, w = n & 1;
+      if (!WIDE || w == 0) wait(s, smem_u32(&s.full[at]), ((2 * group + 1) / S::kSlots) & 1);
+      wait(s, smem_u32(&s.weights[w]), count[w] & 1);
+      ++count[w];
+      tcgen05_after_sync();
+      const uint32_t v = ring + at * S::kSlot, weights = tmem + S::kScores + w * kTile, out = tmem + S::kOut + w * 128;
+#pragma unroll
+      for (int e = 0; e < kTile / 16; ++e) {
+        // (a chunk of 32 tokens: 16 columns of the weights' upper parts, 16 of the lower)
+        const uint32_t a = weights + e / 2 * 32 + e % 2 * 8;
+        const uint64_t b = smem_across_k(v + e * 2048, kTile * 128);
+        tcgen05_mma(out, a, b, pv, n > 1 || e > 0);
+        tcgen05_mma(out, a + 16, b, pv, true);
+      }
+      tcgen05_commit(smem_u32(&s.done[w]));
+      if (!WIDE || w == 1) tcgen05_commit(smem_u32(&s.empty[at]));
+      if (n + 2 < items) scores(n + 2);
+    }
+    tile0 += g.tiles;
+  }
+  tcgen05_commit(smem_u32(&s.end));
+  wait(s, smem_u32(&s.end), 0);
+}
+
+// ---- the softmax --------------------------------------------------------------------
+template <class T, int DP, bool WIDE>
+struct Softmax {
+  using S = Shape<DP, WIDE>;
+  const DraftParams& p;
+  State& s;
+  DraftTree& tree;
+  const uint32_t tmem;   // of this warp's lanes
+  const int w = threadIdx.x / kGroup, row = threadIdx.x % kGroup;
+  uint32_t count = 0;    // items so far
+  // of the row: its maximum when O was last rescaled, and the sum
+  float m, l;
+
+  __device__ __forceinline__ Softmax(const DraftParams& p_, State& s_, DraftTree& t, uint32_t tmem_)
+      : p(p_), s(s_), tree(t), tmem(tmem_ + ((threadIdx.x / 32 % 4 * 32) << 16)) {}
+
+  __device__ __forceinline__ void load_queries(unsigned char* to, int batch_row, int kv, int q0, int n) {
+    const int pieces = (p.dim + 15) / 16 * 2;
+    for (int i = threadIdx.x; i < S::kRows * pieces; i += 2 * kGroup) {
+      const int r = i / pieces, c = i - r * pieces;
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (r < n && c * 8 < p.dim) {
+        const T* q = draft_query<T>(p, batch_row, kv, q0 + r) + c * 8;
+        if (p.q_vectors) {
+          x = *reinterpret_cast<const uint4*>(q);
+        } else {
+          T e[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) e[k] = q[k];
+          x = *reinterpret_cast<uint4*>(e);
+        }
+      }
+      *reinterpret_cast<uint4*>(to + c / 8 * S::kRows * 128 + swizzled(r, c % 8)) = x;
+    }
+  }
+
+  // One tile of this group's: the weights of its 128 tokens into the place of
+  // their scores. t0: its first token; mask: not every draft sees all of it.
+  __device__ __forceinline__ void item(bool first, bool alive, int draft, int t0, int base, bool mask, const uint32_t* here) {
+    const uint32_t at = tmem + S::kScores + w * kTile;
+    tcgen05_after_sync();
+    if (__any_sync(~0u, alive)) {
+      float top = -CUDART_INF_F;
+      uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
+      if (mask) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) seen[c] = here[c] & tree.sees_of_32(p, draft, t0 + 32 * c, base);
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t x[32];
+        tmem_load(x, at + 32 * c);
+        tmem_wait_load(x);
+        if (p.cap_out != 0.0f) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(p.cap_out * tanhf(__uint_as_float(x[e]) * p.cap_in));
+          tmem_store(at + 32 * c, x);
+        }
+        if (mask) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (seen[c] >> e & 1) top = fmaxf(top, __uint_as_float(x[e]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(x[e]));
+        }
+      }
+      const float scale = p.cap_out != 0.0f ? 1.0f : p.scale_log2;
+      top = fmaxf(m, top * scale);
+      const bool grown = top > m + kSlack<T>;  // (also from -infinity)
+      if (__any_sync(~0u, grown)) {
+        const float c = grown ? attend_weight(m, top) : 1.0f;
+        if (grown) m = top;
+        if (!first && __any_sync(~0u, c != 1.0f)) {
+          wait(s, smem_u32(&s.done[w]), (count - 1) & 1);
+          tcgen05_after_sync();
+          rescale(c);
+        }
+        l *= c;
+      }
+      const float low = m == -CUDART_INF_F ? 0.0f : m;
+      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (p.cap_out != 0.0f) tmem_wait_store();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t x[32], y[32];
+        tmem_load(x, at + 32 * c);
+        tmem_wait_load(x);
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          float a = power_of_two(fmaf(__uint_as_float(x[e]), scale, -low)), b = power_of_two(fmaf(__uint_as_float(x[e + 1]), scale, -low));
+          if (mask) {
+            a = seen[c] >> e & 1 ? a : 0.0f;
+            b = seen[c] >> (e + 1) & 1 ? b : 0.0f;
+          }
+          sum[e & 2] += a;
+          sum[(e & 2) + 1] += b;
+          split<T>(a * kRaise<T>, b * kRaise<T>, &y[e / 2], &y[16 + e / 2]);
+        }
+        tmem_store(at + 32 * c, y);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_wait_store();
+    }
+    tcgen05_before_sync();
+    mbar_arrive(smem_u32(&s.weights[w]));
+    ++count;
+  }
+
+  __device__ __forceinline__ void rescale(float c) {
+    for (int d = 0; d < p.dim; d += 32) {
+      uint32_t x[32];
+      tmem_load(x, tmem + S::kOut + w * 128 + d);
+      tmem_wait_load(x);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * c);
+      tmem_store(tmem + S::kOut + w * 128 + d, x);
+    }
+    tmem_wait_store();
+  }
+
+  // What the copies left out of a tile's values because it is not finite, to
+  // the rows that see it (read again from where it lies).
+  __device__ __forceinline__ void add_infinite(const AttendSegment& g, int kv, int draft, bool alive, int t0, int base, const uint32_t* here) {
+    uint32_t seen[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) seen[c] = alive ? here[c] & tree.sees_of_32(p, draft, t0 + 32 * c, base) : 0u;
+    for (int d = 0; d < p.dim; d += 32) {
+      uint32_t x[32];
+      tmem_load(x, tmem + S::kOut + w * 128 + d);
+      tmem_wait_load(x);
+      for (int t = 0; t < kTile; ++t) {
+        if (!(here[t >> 5] >> (t & 31) & 1)) continue;
+        const uint32_t column = fast_div32(p.page, (uint32_t)(t0 + t));
+        const int slot = t0 + t - (int)(column * p.page.d), page = p.tables[g.row * p.table_st[0] + column * p.table_st[1]];
+        const T* v = static_cast<const T*>(p.v) + page * p.v_st[0] + slot * p.v_st[1] + kv * p.v_st[2] + d;
+        const bool sees = seen[t >> 5] >> (t & 31) & 1;
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (sees && d + e < p.dim) {
+            const float y = to_float(v[e]);
+            if (!(fabsf(y) < CUDART_INF_F)) x[e] = __float_as_uint(__uint_as_float(x[e]) + y);
+          }
+      }
+      tmem_store(tmem + S::kOut + w * 128 + d, x);
+    }
+    tmem_wait_store();
+  }
+
+  // Writes 32 elements of the row's (finished or a part's).
+  __device__ __forceinline__ void write(const float (&o)[32], float* part, T* out, int d) const {
+    if (part) {
+#pragma unroll
+      for (int e = 0; e < 32; e += 4)
+        if (d + e < p.dim) *reinterpret_cast<float4*>(part + d + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+    } else if (p.out_vectors) {
+#pragma unroll
+      for (int e = 0; e < 32; e += 8)
+        if (d + e < p.dim) {
+          T y[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) y[k] = from_float<T>(o[e + k]);
+          *reinterpret_cast<uint4*>(out + d + e) = *reinterpret_cast<uint4*>(y);
+        }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (d + e < p.dim) out[d + e] = from_float<T>(o[e]);
+    }
+  }
+
+  __device__ __forceinline__ void run(const AttendRows& rows, const AttendShare& share, unsigned char* queries) {
+    using Both = SomeThreads<2 * kGroup, 1>;
+    int tile = 0;
+    for (AttendSegment g = attend_first(p, rows, share, kTile); g.tiles; g = attend_next(p, rows, share, g, kTile)) {
+      const AttendHeads heads = attend_heads(p, g.group);
+      const int q0 = heads.head0 - heads.kv * p.group, base = g.n - p.drafts;
+      draft_tree<2 * kGroup, Both>(p, tree, g.row, base);
+      load_queries(queries, g.row, heads.kv, q0, heads.heads);
+      fence_async_smem();
+      mbar_arrive(smem_u32(&s.queries));
+
+      const int mine = row + (WIDE ? w * kGroup : 0);
+      const int draft = (int)fast_div32(p.per, (uint32_t)(q0 + min(mine, heads.heads - 1)));
+      const bool alive = mine < heads.heads, live = alive && tree.from[draft] != kNever;
+      m = -CUDART_INF_F;
+      l = 0.0f;
+      bool any = false;
+      for (int i = WIDE ? 0 : w; i < g.tiles; i += WIDE ? 1 : 2) {
+        const int t0 = (g.tile0 + i) * kTile;
+        // (the tile's scores are there: so is what the copies say of it)
+        wait(s, smem_u32(&s.scores[w]), count & 1);
+        const uint32_t* at = s.here[(tile + i) % kHereTiles];
+        const uint32_t here[4] = {at[0], at[1], at[2], at[3]};
+        const bool mask = (here[0] & here[1] & here[2] & here[3]) != ~0u || !draft_all_seen(p, t0, t0 + kTile, base);
+        item(!any, alive, draft, t0, base, mask, here);
+        any = true;
+        if (mask) {
+          wait(s, smem_u32(&s.done[w]), (count - 1) & 1);
+          tcgen05_after_sync();
+          if (*static_cast<volatile uint32_t*>(&s.bad[(tile + i) % kHereTiles]) == (uint32_t)(tile + i) + 1) {
+            add_infinite(g, heads.kv, draft, alive, t0, base, here);
+            tcgen05_before_sync();  // (the next product comes after this thread's next arrival)
+          }
+        }
+      }
+      if (any) wait(s, smem_u32(&s.done[w]), (count - 1) & 1);
+      tcgen05_after_sync();
+      tile += g.tiles;
+
+      const int part_pitch = attend_pitch(p.dim);
+      float* part = attend_part(p, share, g, threadIdx.x == 0);
+      const int h = heads.head0 + mine;
+      float top = m, total = l, c[2] = {1.0f, 1.0f};
+      bool has[2] = {any, any};
+      if (!WIDE) {
+        s.part[w][row] = make_float2(m, l);
+        Both::sync();  // (the other group's products are done as well)
+        tcgen05_after_sync();
+        has[0] = true;
+        has[1] = g.tiles > 1;
+        const float2 a = s.part[0][row], b = has[1] ? s.part[1][row] : make_float2(-CUDART_INF_F, 0.0f);
+        top = fmaxf(a.x, b.x);
+        c[0] = attend_weight(a.x, top);
+        c[1] = attend_weight(b.x, top);
+        total = a.y * c[0] + b.y * c[1];
+      }
+      if (!live) {
+        top = -CUDART_INF_F;
+        total = 0.0f;
+      }
+      T* out = nullptr;
+      float scale = 1.0f / kRaise<T>;
+      if (part) {
+        part += (h - heads.head0) * part_pitch;
+        if (alive && (WIDE || w == 0)) {
+          part[part_pitch - 4] = top;
+          part[part_pitch - 3] = total;
+        }
+      } else if (alive) {
+        const AttendPlace place = attend_place(p, g.row, h);
+        out = static_cast<T*>(p.out) + place.out;
+        if (WIDE || w == 0) {
+          if (p.lse) p.lse[place.lse] = total == 0.0f ? -CUDART_INF_F : (top + log2f(total)) * CUDART_LN2_F;
+          attend_note(p, g.row, h, top, total);
+        }
+        scale = total == 0.0f ? 0.0f : scale / total;
+      }
+      if (__any_sync(~0u, alive)) {
+        const int half = WIDE ? DP : DP / 2, d0 = WIDE ? 0 : w * half;
+        for (int d = d0; d < d0 + half && d < p.dim; d += 32) {
+          float o[32];
+          uint32_t x[32];
+          if (WIDE) {
+            tmem_load(x, tmem + S::kOut + w * 128 + d);
+            tmem_wait_load(x);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(x[e]) * scale;
+          } else {
+            tmem_load(x, tmem + S::kOut + d);
+            tmem_wait_load(x);
+            const float a = c[0] * scale, b = c[1] * scale;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = c[0] == 0.0f ? 0.0f : __uint_as_float(x[e]) * a;
+            if (has[1]) {
+              tmem_load(x, tmem + S::kOut + 128 + d);
+              tmem_wait_load(x);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] += c[1] == 0.0f ? 0.0f : __uint_as_float(x[e]) * b;
+            }
+          }
+          if (total == 0.0f) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+          }
+          if (alive) write(o, part, out, d);
+        }
+      }
+      tcgen05_before_sync();  // (what is next issued over O comes after a barrier of these threads)
+    }
+  }
+};
+
+template <class T, int DP, bool WIDE>
+__global__ void __launch_bounds__(kThreads, 1) drafts_tc_kernel(const __grid_constant__ DraftParams p) {
+  using S = Shape<DP, WIDE>;
+  extern __shared__ unsigned char s_raw[];
+  unsigned char* s_mem = s_raw + ((1024 - smem_u32(s_raw) % 1024) % 1024);
+  State& s = *reinterpret_cast<State*>(s_mem + S::kRest);
+  DraftTree& tree = *reinterpret_cast<DraftTree*>(&s + 1);
+  AttendRows& rows = *reinterpret_cast<AttendRows*>(&tree + 1);
+  const int warp = threadIdx.x / 32;
+
+  wait_for_previous();
+  let_next_start();
+  AttendShare share;
+  if (!attend_begin<T>(p, rows, kTile, &share)) return;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::kSlots; ++i) {
+      mbar_init(smem_u32(&s.full[i]), kLoaders);
+      mbar_init(smem_u32(&s.empty[i]), 1);
+    }
+    for (int i = 0; i < kHereTiles; ++i) s.bad[i] = 0;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s.scores[i]), 1);
+      mbar_init(smem_u32(&s.weights[i]), kGroup);
+      mbar_init(smem_u32(&s.done[i]), 1);
+    }
+    mbar_init(smem_u32(&s.queries), 2 * kGroup);
+    mbar_init(smem_u32(&s.end), 1);
+    s.stop = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 2 * kGroup / 32) tmem_alloc(smem_u32(&s.tmem), 512);
+  tcgen05_before_sync();
+  __syncthreads();
+  tcgen05_after_sync();
+  const uint32_t tmem = *static_cast<volatile uint32_t*>(&s.tmem);
+  const uint32_t queries = smem_u32(s_mem), ring = queries + S::kRing;
+  if (warp < 2 * kGroup / 32) {
+    Softmax<T, DP, WIDE> softmax(p, s, tree, tmem);
+    softmax.run(rows, share, s_mem);
+  } else if (warp == 2 * kGroup / 32) {
+    if (threadIdx.x % 32 == 0) issue<T, DP, WIDE>(p, s, rows, share, queries, ring, tmem);
+    __syncwarp();
+  } else {
+    Loader<T, DP, WIDE> loader(p, s, ring);
+    loader.run(rows, share);
+  }
+  tcgen05_before_sync();
+  __syncthreads();
+  tcgen05_after_sync();
+  if (warp == 2 * kGroup / 32) tmem_free(tmem, 512);
+  if (threadIdx.x == 0 && s.stop) report(p.status, CMD_CACHE_TIMEOUT);
+}
+
+template <class T, int DP, bool WIDE>
+cudaError_t launch(const DraftParams& p, cudaStream_t stream) {
+  static PerDevice ready;  // (static storage: zero before first use)
+  static_assert(kSmem<DP, WIDE> <= 227 * 1024, "the CTA fits an SM");
+  const cudaError_t e = allow_smem(drafts_tc_kernel<T, DP, WIDE>, kSmem<DP, WIDE>, ready);
+  if (e != cudaSuccess) return e;
+  return attend_launch<T>(drafts_tc_kernel<T, DP, WIDE>, p, 2, 152, kThreads, kSmem<DP, WIDE>, kTile, stream, false);
+}
+template <class T>
+cudaError_t launch_type(const DraftParams& p, cudaStream_t stream) {
+  const bool wide = p.block_heads > kGroup;
+  if (p.dim <= 64) return wide ? launch<T, 64, true>(p, stream) : launch<T, 64, false>(p, stream);
+  return wide ? launch<T, 128, true>(p, stream) : launch<T, 128, false>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t drafts_tc_launch(int dtype, const DraftParams& p, cudaStream_t stream) {
+  return dtype == CMD_F16 ? launch_type<__half>(p, stream) : launch_type<__nv_bfloat16>(p, stream);
+}
+
+}  // namespace cmdx

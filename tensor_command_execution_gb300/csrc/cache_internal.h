@@ -135,15 +135,25 @@ struct DraftParams : AttendParams {
   float2* stats;              // optional: maximum and sum, [rows][kv heads][group]
   float* weights;             // optional: [rows, kv heads, tokens], added to
   int64_t w_st[2];
+  uint8_t q_vectors, out_vectors;  // their rows may be accessed 16 bytes at a time
 };
-constexpr int kDraftCtas = 152 * 2;     // bounds the workspace
-constexpr int kDraftRows = 64;          // rows of a block, at most
+// CTAs of a launch and rows of a block, at most: they bound the workspace
+constexpr int kDraftCtas = 152 * 2, kDraftRows = 64;
+constexpr int kDraftTcCtas = 152, kDraftTcRows = 256;
 // copy: bytes of a copy that suits every row of the cache, 16 or 4, or 0
 cudaError_t drafts_mma_launch16(int dtype, const DraftParams& p, cudaStream_t stream);
 cudaError_t drafts_mma_launch4(int dtype, const DraftParams& p, cudaStream_t stream);
 cudaError_t drafts_mma_launch0(int dtype, const DraftParams& p, cudaStream_t stream);
+// 16-byte copies, dims up to 128
+cudaError_t drafts_tc_launch(int dtype, const DraftParams& p, cudaStream_t stream);
 cudaError_t drafts_f32_launch16(const DraftParams& p, cudaStream_t stream);
 cudaError_t drafts_f32_launch4(const DraftParams& p, cudaStream_t stream);
+// The weights, from the maxima and sums that the attention has left in p.stats.
+cudaError_t weigh_mma_launch16(int dtype, const DraftParams& p, cudaStream_t stream);
+cudaError_t weigh_mma_launch4(int dtype, const DraftParams& p, cudaStream_t stream);
+cudaError_t weigh_mma_launch0(int dtype, const DraftParams& p, cudaStream_t stream);
+cudaError_t weigh_f32_launch16(const DraftParams& p, cudaStream_t stream);
+cudaError_t weigh_f32_launch4(const DraftParams& p, cudaStream_t stream);
 
 // ---- what is kept (cache_keep.cu) -----------------------------------------------
 struct PathParams {
