@@ -212,7 +212,8 @@ cmd_status cmd_attention_decode(const cmd_attention_args* args, void* cuda_strea
  * for the tokens t < lengths[r] that are seen, in 32 bits, in an order that does
  * not depend on timing. It reaches at least columns * page_size tokens.
  *
- * workspace as for cmd_attention_decode, of cmd_drafts_workspace bytes. Limits:
+ * The softmax weights of 16-bit caches are held as there, in f16 no finer than
+ * 2^-36 of the largest. workspace as there, of cmd_drafts_workspace bytes. Limits:
  * drafts <= CMD_CACHE_MAX_DRAFTS, drafts * q_heads <= 2^20. */
 typedef struct cmd_drafts_args {
   cmd_operand q, out;           /* [rows, drafts, q_heads, dim], dim <= CMD_CACHE_MAX_DIM */

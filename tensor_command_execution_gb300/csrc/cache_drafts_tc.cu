@@ -15,8 +15,8 @@
 // A weight is held as the sum of two 16-bit numbers, as in cache_attend_mma.cu:
 // P takes exactly the columns of S that it came from. O is rescaled only when a
 // row's maximum has grown by more than kSlack (in powers of two) since it was
-// last taken: weights are up to 2^kSlack then, and f16 ones are lifted by so
-// much less (2^11): no finer than 2^-36 of the row's largest weight.
+// last taken: weights are up to 2^kSlack then, and f16 ones are lifted by 2^11
+// (rather than 2^15), which holds them to no finer than 2^-36 of the largest.
 #include "cache_drafts.cuh"
 #include "cache_attend_ring.cuh"
 #include "cache_mma.cuh"
@@ -33,14 +33,61 @@ constexpr int kThreads = 2 * kGroup + 32 + kLoaders;
 constexpr int kTile = 128;                    // tokens
 constexpr uint64_t kPatience = 2000000000;    // ns: no wait takes longer
 
+// Powers of two: how far a maximum may grow before O is rescaled, and how far
+// weights are lifted.
 template <class T>
 constexpr float kSlack = 8.0f;
 template <>
 constexpr float kSlack<__half> = 4.0f;
 template <class T>
-constexpr float kRaise = 1.0f;  // what weights are multiplied by
+constexpr float kRaise = 0.0f;
 template <>
-constexpr float kRaise<__half> = 2048.0f;
+constexpr float kRaise<__half> = 11.0f;
+template <class T>
+constexpr bool kBf16 = true;
+template <>
+constexpr bool kBf16<__half> = false;
+
+// ---- pairs of binary32 numbers in one instruction --------------------------------
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// x and y rounded to 16 bits, and what that leaves of each, rounded again
+template <class T>
+__device__ __forceinline__ void split2(float x, float y, uint32_t* hi, uint32_t* lo) {
+  if constexpr (kBf16<T>) {
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(*hi) : "f"(y), "f"(x));
+    const float2 rest = unpair(add2(pair(x, y), pair(-__uint_as_float(*hi << 16), -__uint_as_float(*hi & 0xffff0000u))));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(*lo) : "f"(rest.y), "f"(rest.x));
+  } else {
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(*hi) : "f"(y), "f"(x));
+    const float2 h = __half22float2(*reinterpret_cast<const __half2*>(hi));
+    const float2 rest = unpair(add2(pair(x, y), pair(-h.x, -h.y)));
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(*lo) : "f"(rest.y), "f"(rest.x));
+  }
+}
 
 template <int DP, bool WIDE>
 struct Shape {
@@ -213,9 +260,8 @@ template <class T, int DP, bool WIDE>
 __device__ __forceinline__ void issue(const DraftParams& p, State& s, const AttendRows& rows, const AttendShare& share, uint32_t queries,
                                       uint32_t ring, uint32_t tmem) {
   using S = Shape<DP, WIDE>;
-  constexpr bool kBf16 = sizeof(T) == 2 && kSlack<T> == 8.0f;
   const int steps = (p.dim + 15) / 16;
-  const uint32_t qk = tcgen05_shape(kBf16, kTile, false), pv = tcgen05_shape(kBf16, steps * 16, true);
+  const uint32_t qk = tcgen05_shape(kBf16<T>, kTile, false), pv = tcgen05_shape(kBf16<T>, steps * 16, true);
   uint32_t tile0 = 0, segments = 0, count[2] = {0, 0};
   for (AttendSegment g = attend_first(p, rows, share, kTile); g.tiles; g = attend_next(p, rows, share, g, kTile)) {
     wait(s, smem_u32(&s.queries), segments & 1);
@@ -270,7 +316,8 @@ struct Softmax {
   const uint32_t tmem;   // of this warp's lanes
   const int w = threadIdx.x / kGroup, row = threadIdx.x % kGroup;
   uint32_t count = 0;    // items so far
-  // of the row: its maximum when O was last rescaled, and the sum
+  // of the row: the power of two that its weights are counted from (its maximum
+  // when O was last rescaled, less kRaise), and their sum
   float m, l;
 
   __device__ __forceinline__ Softmax(const DraftParams& p_, State& s_, DraftTree& t, uint32_t tmem_)
@@ -296,77 +343,86 @@ struct Softmax {
     }
   }
 
-  // One tile of this group's: the weights of its 128 tokens into the place of
-  // their scores. t0: its first token; mask: not every draft sees all of it.
-  __device__ __forceinline__ void item(bool first, bool alive, int draft, int t0, int base, bool mask, const uint32_t* here) {
+  // Scores that the cap changes, and those of tokens that the row does not see,
+  // which become -infinity (whatever they are).
+  __device__ __noinline__ void prepare(int draft, int t0, int base, bool mask, const uint32_t* here) {
     const uint32_t at = tmem + S::kScores + w * kTile;
-    tcgen05_after_sync();
-    if (__any_sync(~0u, alive)) {
-      float top = -CUDART_INF_F;
-      uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
-      if (mask) {
+#pragma unroll 1
+    for (int c = 0; c < kTile / 32; ++c) {
+      uint32_t x[32];
+      tmem_load(x, at + 32 * c);
+      const uint32_t seen = mask ? here[c] & tree.sees_of_32(p, draft, t0 + 32 * c, base) : ~0u;
+      tmem_wait_load(x);
+      if (p.cap_out != 0.0f) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) seen[c] = here[c] & tree.sees_of_32(p, draft, t0 + 32 * c, base);
+        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(p.cap_out * tanhf(__uint_as_float(x[e]) * p.cap_in));
       }
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t x[32];
-        tmem_load(x, at + 32 * c);
-        tmem_wait_load(x);
-        if (p.cap_out != 0.0f) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(p.cap_out * tanhf(__uint_as_float(x[e]) * p.cap_in));
-          tmem_store(at + 32 * c, x);
-        }
-        if (mask) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (seen[c] >> e & 1) top = fmaxf(top, __uint_as_float(x[e]));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(x[e]));
-        }
-      }
-      const float scale = p.cap_out != 0.0f ? 1.0f : p.scale_log2;
-      top = fmaxf(m, top * scale);
-      const bool grown = top > m + kSlack<T>;  // (also from -infinity)
-      if (__any_sync(~0u, grown)) {
-        const float c = grown ? attend_weight(m, top) : 1.0f;
-        if (grown) m = top;
-        if (!first && __any_sync(~0u, c != 1.0f)) {
-          wait(s, smem_u32(&s.done[w]), (count - 1) & 1);
-          tcgen05_after_sync();
-          rescale(c);
-        }
-        l *= c;
-      }
-      const float low = m == -CUDART_INF_F ? 0.0f : m;
-      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (p.cap_out != 0.0f) tmem_wait_store();
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int e = 0; e < 32; ++e) x[e] = seen >> e & 1 ? x[e] : __float_as_uint(-CUDART_INF_F);
+      tmem_store(at + 32 * c, x);
+    }
+    tmem_wait_store();
+  }
+
+  // One tile of this group's: the weights of its 128 tokens into the place of
+  // their scores.
+  __device__ __forceinline__ void item(bool first) {
+    const uint32_t at = tmem + S::kScores + w * kTile;
+    const float scale = p.cap_out != 0.0f ? 1.0f : p.scale_log2;
+    float top = -CUDART_INF_F;
+    {
+      float up[4] = {top, top, top, top};
+#pragma unroll 1
+      for (int c = 0; c < kTile; c += 64) {
         uint32_t x[32], y[32];
-        tmem_load(x, at + 32 * c);
+        tmem_load(x, at + c);
+        tmem_load(y, at + c + 32);
         tmem_wait_load(x);
+        tmem_wait_load(y);
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) up[k] = max3(up[k], __uint_as_float(x[e + k]), __uint_as_float(y[e + k]));
+        }
+      }
+      top = fmaxf(max3(up[0], up[1], up[2]), up[3]) * scale;
+    }
+    const bool grown = top > m + (kSlack<T> + kRaise<T>);  // (also from -infinity)
+    if (__any_sync(~0u, grown)) {
+      const float now = top - kRaise<T>, c = grown ? attend_weight(m, now) : 1.0f;
+      if (grown) m = now;
+      if (!first && __any_sync(~0u, c != 1.0f)) {
+        wait(s, smem_u32(&s.done[w]), (count - 1) & 1);
+        tcgen05_after_sync();
+        rescale(c);
+      }
+      l *= c;
+    }
+    const float low = m == -CUDART_INF_F ? 0.0f : -m;
+    const uint64_t scale2 = pair(scale, scale), low2 = pair(low, low);
+    uint64_t sum[2] = {0, 0};
+    uint32_t x[2][32];
+    tmem_load(x[0], at);
+#pragma unroll 1
+    for (int c = 0; c < kTile; c += 64) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        tmem_wait_load(x[b]);
+        if (c + 32 * b + 32 < kTile) tmem_load(x[b ^ 1], at + c + 32 * b + 32);
+        uint32_t y[32];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-          float a = power_of_two(fmaf(__uint_as_float(x[e]), scale, -low)), b = power_of_two(fmaf(__uint_as_float(x[e + 1]), scale, -low));
-          if (mask) {
-            a = seen[c] >> e & 1 ? a : 0.0f;
-            b = seen[c] >> (e + 1) & 1 ? b : 0.0f;
-          }
-          sum[e & 2] += a;
-          sum[(e & 2) + 1] += b;
-          split<T>(a * kRaise<T>, b * kRaise<T>, &y[e / 2], &y[16 + e / 2]);
+          const float2 z = unpair(fma2(pair(__uint_as_float(x[b][e]), __uint_as_float(x[b][e + 1])), scale2, low2));
+          const float u = power_of_two(z.x), v = power_of_two(z.y);
+          sum[e / 2 & 1] = add2(sum[e / 2 & 1], pair(u, v));
+          split2<T>(u, v, &y[e / 2], &y[16 + e / 2]);
         }
-        tmem_store(at + 32 * c, y);
+        tmem_store(at + c + 32 * b, y);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_wait_store();
     }
-    tcgen05_before_sync();
-    mbar_arrive(smem_u32(&s.weights[w]));
-    ++count;
+    const float2 all = unpair(add2(sum[0], sum[1]));
+    l += all.x + all.y;
+    tmem_wait_store();
   }
 
   __device__ __forceinline__ void rescale(float c) {
@@ -383,7 +439,7 @@ struct Softmax {
 
   // What the copies left out of a tile's values because it is not finite, to
   // the rows that see it (read again from where it lies).
-  __device__ __forceinline__ void add_infinite(const AttendSegment& g, int kv, int draft, bool alive, int t0, int base, const uint32_t* here) {
+  __device__ __noinline__ void add_infinite(const AttendSegment& g, int kv, int draft, bool alive, int t0, int base, const uint32_t* here) {
     uint32_t seen[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) seen[c] = alive ? here[c] & tree.sees_of_32(p, draft, t0 + 32 * c, base) : 0u;
@@ -455,7 +511,14 @@ struct Softmax {
         const uint32_t* at = s.here[(tile + i) % kHereTiles];
         const uint32_t here[4] = {at[0], at[1], at[2], at[3]};
         const bool mask = (here[0] & here[1] & here[2] & here[3]) != ~0u || !draft_all_seen(p, t0, t0 + kTile, base);
-        item(!any, alive, draft, t0, base, mask, here);
+        tcgen05_after_sync();
+        if (__any_sync(~0u, alive)) {
+          if (mask || p.cap_out != 0.0f) prepare(draft, t0, base, mask, here);
+          item(!any);
+        }
+        tcgen05_before_sync();
+        mbar_arrive(smem_u32(&s.weights[w]));
+        ++count;
         any = true;
         if (mask) {
           wait(s, smem_u32(&s.done[w]), (count - 1) & 1);
@@ -492,7 +555,7 @@ struct Softmax {
         total = 0.0f;
       }
       T* out = nullptr;
-      float scale = 1.0f / kRaise<T>;
+      float scale = 1.0f;
       if (part) {
         part += (h - heads.head0) * part_pitch;
         if (alive && (WIDE || w == 0)) {
@@ -506,7 +569,7 @@ struct Softmax {
           if (p.lse) p.lse[place.lse] = total == 0.0f ? -CUDART_INF_F : (top + log2f(total)) * CUDART_LN2_F;
           attend_note(p, g.row, h, top, total);
         }
-        scale = total == 0.0f ? 0.0f : scale / total;
+        scale = total == 0.0f ? 0.0f : 1.0f / total;
       }
       if (__any_sync(~0u, alive)) {
         const int half = WIDE ? DP : DP / 2, d0 = WIDE ? 0 : w * half;
