@@ -201,6 +201,8 @@ __device__ __forceinline__ AttendPlace attend_place(const AttendParams& p, int r
   return {row * p.out_st[0] + h * p.out_st[1], row * p.lse_st[0] + h * p.lse_st[1]};
 }
 __device__ __forceinline__ void attend_note(const AttendParams&, int, int, float, float) {}
+// Whether a part with this maximum says that its row is empty, whatever the others hold.
+__device__ __forceinline__ bool attend_void(const AttendParams&, float) { return false; }
 
 // Writes elements d .. d + 3 (those below dim) of a finished head.
 template <class T, class P>
@@ -404,6 +406,7 @@ __device__ __forceinline__ void attend_join(const P& p, int task, float (*s_stat
     if (WARPS > 1 && d - 4 * lane >= pitch - 4) break;  // (the same for all of the CTA)
     const bool mine = d < pitch - 4;
     float top = -CUDART_INF_F, l = 0.0f;
+    bool empty = false;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int c = warp * kAtOnce; c < split.parts; c += WARPS * kAtOnce) {
       float m[kAtOnce], pl[kAtOnce];
@@ -420,7 +423,10 @@ __device__ __forceinline__ void attend_join(const P& p, int task, float (*s_stat
       }
       float up = top;
 #pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) up = fmaxf(up, m[k]);
+      for (int k = 0; k < kAtOnce; ++k) {
+        up = fmaxf(up, m[k]);
+        empty = empty || attend_void(p, m[k]);
+      }
       const float a = attend_weight(top, up);
       l *= a;
       scale_by(o, a);
@@ -433,6 +439,7 @@ __device__ __forceinline__ void attend_join(const P& p, int task, float (*s_stat
           add_scaled(o, po[k], b);
         }
     }
+    if (empty) top = CUDART_NAN_F;  // (a maximum is never that)
     if constexpr (WARPS > 1) {
       if (mine) {
         *reinterpret_cast<float4*>(&s_state[warp][d]) = o;
@@ -445,7 +452,11 @@ __device__ __forceinline__ void attend_join(const P& p, int task, float (*s_stat
       if (warp == 0 && mine) {
         top = -CUDART_INF_F;
 #pragma unroll
-        for (int t = 0; t < WARPS; ++t) top = fmaxf(top, s_state[t][CMD_CACHE_MAX_DIM]);
+        for (int t = 0; t < WARPS; ++t) {
+          const float x = s_state[t][CMD_CACHE_MAX_DIM];
+          top = fmaxf(top, x);
+          empty = empty || x != x;
+        }
         l = 0.0f;
         o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
@@ -457,6 +468,7 @@ __device__ __forceinline__ void attend_join(const P& p, int task, float (*s_stat
       }
       // (a second run of dims reads the m and l that the first wrote, unchanged)
     }
+    if (empty) l = 0.0f;
     if (warp == 0 && mine) attend_write<T>(p, split.row, h.head0 + q, d, top, l, o);
   }
 }

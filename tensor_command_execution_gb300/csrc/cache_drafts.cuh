@@ -37,6 +37,11 @@ __device__ __forceinline__ AttendPlace attend_place(const DraftParams& p, int ro
 __device__ __forceinline__ void attend_note(const DraftParams& p, int row, int h, float top, float l) {
   if (p.stats) p.stats[(int64_t)row * p.kv_heads * p.group + h] = make_float2(top, l);
 }
+// The maximum that a part of padding is given (with a sum of zero): the parts
+// of tokens that every draft sees are worked out without the tree, as if it
+// were none.
+constexpr float kPadding = 3e38f;
+__device__ __forceinline__ bool attend_void(const DraftParams&, float m) { return m == kPadding; }
 
 // The drafts of a row: which each sees (a bit each; itself among them), its
 // first token (kNever: the draft is padding and sees nothing).

@@ -144,27 +144,15 @@ template <class T, int DP, bool WIDE>
 struct Loader {
   using S = Shape<DP, WIDE>;
   static constexpr int kChunks = DP / 8, kOver = kLoaders / kChunks;
-  // (of the groups of copies on their way at most kBehind are left behind when
-  // another has been issued: the products of a tile wait for the keys of the
-  // next, and a slot's next copies for the products of the tile in it)
-  static constexpr int kBehind = 2;
   const DraftParams& p;
   State& s;
   const uint32_t ring;
   const int tid = threadIdx.x - 2 * kGroup - 32, chunk = tid % kChunks, row0 = tid / kChunks, chunks, used;
-  uint32_t issued = 0, arrived = 0;  // groups: keys and values in turn
-  uint32_t masked = 0;               // a bit for each group on its way, the newest lowest: values of a tile that not all see
+  uint32_t issued = 0;  // keys and values in turn
 
   __device__ __forceinline__ Loader(const DraftParams& p_, State& s_, uint32_t ring_)
       : p(p_), s(s_), ring(ring_), chunks(p_.dim / 8), used((p_.dim + 15) / 16 * 2) {}
 
-  __device__ __forceinline__ void arrive() {
-    const int slot = arrived % S::kSlots;
-    if (masked >> (issued - 1 - arrived) & 1) clear(slot);
-    fence_async_smem();
-    mbar_arrive(smem_u32(&s.full[slot]));
-    ++arrived;
-  }
   // Values that are not finite become zeros, whatever their weight, and the
   // softmax group is told: it adds them where they are seen.
   __device__ __forceinline__ void clear(int slot) {
@@ -176,7 +164,7 @@ struct Loader {
       const uint4 bad = make_uint4(not_finite<T>(x.x), not_finite<T>(x.y), not_finite<T>(x.z), not_finite<T>(x.w));
       if ((bad.x | bad.y | bad.z | bad.w) == 0) continue;
       sts128(a, make_uint4(x.x & ~bad.x, x.y & ~bad.y, x.z & ~bad.z, x.w & ~bad.w));
-      *static_cast<volatile uint32_t*>(&s.bad[arrived / 2 % kHereTiles]) = arrived / 2 + 1;
+      *static_cast<volatile uint32_t*>(&s.bad[issued / 2 % kHereTiles]) = issued / 2 + 1;
     }
   }
   __device__ __forceinline__ void copy(const T* from, const int64_t* offset, bool mask) {
@@ -193,17 +181,20 @@ struct Loader {
         copy_bytes<16>(dst + swizzled(r, chunk % 8), at + (o >= 0 ? o : 0), o >= 0 && inside ? 16 : 0);
       }
     }
-    copy_commit();
-    ++issued;
-    masked = masked << 1 | (mask ? 1u : 0u);
-    if (issued - arrived > kBehind) {
-      copy_wait<kBehind>();
-      arrive();
+    // The arrival comes with the data; the thread that issues the products, not
+    // this one, orders them for the products' reads: the fence waits for all of
+    // a thread's copies on their way (here it cost 5 to 10 thousand cycles a
+    // tile, 219 us for 125 of 4 x 64 drafts over 16384 tokens).
+    const uint32_t full = smem_u32(&s.full[slot]);
+    if (mask) {
+      copy_commit();
+      copy_wait<0>();
+      clear(slot);
+      mbar_arrive(full);
+    } else {
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
     }
-  }
-  __device__ __forceinline__ void drain() {
-    copy_wait<0>();
-    while (arrived != issued) arrive();
+    ++issued;
   }
 
   __device__ __forceinline__ void run(const AttendRows& rows, const AttendShare& share) {
@@ -251,7 +242,8 @@ struct Loader {
         copy(static_cast<const T*>(p.v), s.v[b], !(all && draft_all_seen(p, t0, t0 + kTile, base)));
       }
     }
-    drain();
+    copy_commit();
+    copy_wait<0>();
   }
 };
 
@@ -268,9 +260,13 @@ __device__ __forceinline__ void issue(const DraftParams& p, State& s, const Atte
     ++segments;
     tcgen05_after_sync();
     const int items = WIDE ? 2 * g.tiles : g.tiles;
+    const auto wait_full = [&](uint32_t at, uint32_t copies) {
+      wait(s, smem_u32(&s.full[at]), (copies / S::kSlots) & 1);
+      fence_async_smem();
+    };
     const auto scores = [&](int n) {
       const uint32_t group = tile0 + (WIDE ? n >> 1 : n), at = 2 * group % S::kSlots, w = n & 1;
-      if (!WIDE || w == 0) wait(s, smem_u32(&s.full[at]), (2 * group / S::kSlots) & 1);
+      if (!WIDE || w == 0) wait_full(at, 2 * group);
       const uint32_t q = queries + (WIDE ? w * kGroup * 128 : 0), k = ring + at * S::kSlot;
       for (int e = 0; e < steps; ++e) {
         const uint32_t slab = e / 4, in = e % 4 * 32;
@@ -283,7 +279,7 @@ __device__ __forceinline__ void issue(const DraftParams& p, State& s, const Atte
     if (items > 1) scores(1);
     for (int n = 0; n < items; ++n) {
       const uint32_t group = tile0 + (WIDE ? n >> 1 : n), at = (2 * group + 1) % S::kSlots, w = n & 1;
-      if (!WIDE || w == 0) wait(s, smem_u32(&s.full[at]), ((2 * group + 1) / S::kSlots) & 1);
+      if (!WIDE || w == 0) wait_full(at, 2 * group + 1);
       wait(s, smem_u32(&s.weights[w]), count[w] & 1);
       ++count[w];
       tcgen05_after_sync();
@@ -324,34 +320,46 @@ struct Softmax {
       : p(p_), s(s_), tree(t), tmem(tmem_ + ((threadIdx.x / 32 % 4 * 32) << 16)) {}
 
   __device__ __forceinline__ void load_queries(unsigned char* to, int batch_row, int kv, int q0, int n) {
-    const int pieces = (p.dim + 15) / 16 * 2;
-    for (int i = threadIdx.x; i < S::kRows * pieces; i += 2 * kGroup) {
-      const int r = i / pieces, c = i - r * pieces;
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (r < n && c * 8 < p.dim) {
-        const T* q = draft_query<T>(p, batch_row, kv, q0 + r) + c * 8;
-        if (p.q_vectors) {
-          x = *reinterpret_cast<const uint4*>(q);
-        } else {
-          T e[8];
+    constexpr int kPieces = DP / 8, kOver = 2 * kGroup / kPieces, kAtOnce = 8;
+    const int c = threadIdx.x % kPieces, r0 = threadIdx.x / kPieces;
+    if (c >= (p.dim + 15) / 16 * 2) return;
+    unsigned char* slab = to + c / 8 * S::kRows * 128;
+#pragma unroll 1
+    for (int i = 0; i < S::kRows; i += kOver * kAtOnce) {
+      uint4 x[kAtOnce];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) e[k] = q[k];
-          x = *reinterpret_cast<uint4*>(e);
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int r = r0 + i + k * kOver;
+        x[k] = make_uint4(0, 0, 0, 0);
+        if (r < n && c * 8 < p.dim) {
+          const T* q = draft_query<T>(p, batch_row, kv, q0 + r) + c * 8;
+          if (p.q_vectors) {
+            x[k] = *reinterpret_cast<const uint4*>(q);
+          } else {
+            T e[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) e[j] = q[j];
+            x[k] = *reinterpret_cast<uint4*>(e);
+          }
         }
       }
-      *reinterpret_cast<uint4*>(to + c / 8 * S::kRows * 128 + swizzled(r, c % 8)) = x;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int r = r0 + i + k * kOver;
+        if (r < S::kRows) *reinterpret_cast<uint4*>(slab + swizzled(r, c % 8)) = x[k];
+      }
     }
   }
 
   // Scores that the cap changes, and those of tokens that the row does not see,
   // which become -infinity (whatever they are).
-  __device__ __noinline__ void prepare(int draft, int t0, int base, bool mask, const uint32_t* here) {
+  __device__ __noinline__ void prepare(int draft, int t0, int base, bool all, const uint32_t* here) {
     const uint32_t at = tmem + S::kScores + w * kTile;
 #pragma unroll 1
     for (int c = 0; c < kTile / 32; ++c) {
       uint32_t x[32];
       tmem_load(x, at + 32 * c);
-      const uint32_t seen = mask ? here[c] & tree.sees_of_32(p, draft, t0 + 32 * c, base) : ~0u;
+      const uint32_t seen = here[c] & (all ? ~0u : tree.sees_of_32(p, draft, t0 + 32 * c, base));
       tmem_wait_load(x);
       if (p.cap_out != 0.0f) {
 #pragma unroll
@@ -439,10 +447,11 @@ struct Softmax {
 
   // What the copies left out of a tile's values because it is not finite, to
   // the rows that see it (read again from where it lies).
-  __device__ __noinline__ void add_infinite(const AttendSegment& g, int kv, int draft, bool alive, int t0, int base, const uint32_t* here) {
+  __device__ __noinline__ void add_infinite(const AttendSegment& g, int kv, int draft, bool alive, int t0, int base, bool all,
+                                            const uint32_t* here) {
     uint32_t seen[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) seen[c] = alive ? here[c] & tree.sees_of_32(p, draft, t0 + 32 * c, base) : 0u;
+    for (int c = 0; c < 4; ++c) seen[c] = !alive ? 0u : here[c] & (all ? ~0u : tree.sees_of_32(p, draft, t0 + 32 * c, base));
     for (int d = 0; d < p.dim; d += 32) {
       uint32_t x[32];
       tmem_load(x, tmem + S::kOut + w * 128 + d);
@@ -493,14 +502,18 @@ struct Softmax {
     for (AttendSegment g = attend_first(p, rows, share, kTile); g.tiles; g = attend_next(p, rows, share, g, kTile)) {
       const AttendHeads heads = attend_heads(p, g.group);
       const int q0 = heads.head0 - heads.kv * p.group, base = g.n - p.drafts;
-      draft_tree<2 * kGroup, Both>(p, tree, g.row, base);
+      // (where every draft sees all of the segment's tokens, the tree is not asked)
+      const int t_begin = g.tile0 * kTile, t_end = t_begin + g.tiles * kTile;
+      const bool planted = !draft_all_seen(p, t_begin, t_end, base);
+      if (planted) draft_tree<2 * kGroup, Both>(p, tree, g.row, base);
+      else Both::sync();
       load_queries(queries, g.row, heads.kv, q0, heads.heads);
       fence_async_smem();
       mbar_arrive(smem_u32(&s.queries));
 
       const int mine = row + (WIDE ? w * kGroup : 0);
       const int draft = (int)fast_div32(p.per, (uint32_t)(q0 + min(mine, heads.heads - 1)));
-      const bool alive = mine < heads.heads, live = alive && tree.from[draft] != kNever;
+      const bool alive = mine < heads.heads, live = alive && !(planted && tree.from[draft] == kNever);
       m = -CUDART_INF_F;
       l = 0.0f;
       bool any = false;
@@ -510,10 +523,10 @@ struct Softmax {
         wait(s, smem_u32(&s.scores[w]), count & 1);
         const uint32_t* at = s.here[(tile + i) % kHereTiles];
         const uint32_t here[4] = {at[0], at[1], at[2], at[3]};
-        const bool mask = (here[0] & here[1] & here[2] & here[3]) != ~0u || !draft_all_seen(p, t0, t0 + kTile, base);
+        const bool all = draft_all_seen(p, t0, t0 + kTile, base), mask = !all || (here[0] & here[1] & here[2] & here[3]) != ~0u;
         tcgen05_after_sync();
         if (__any_sync(~0u, alive)) {
-          if (mask || p.cap_out != 0.0f) prepare(draft, t0, base, mask, here);
+          if (mask || p.cap_out != 0.0f) prepare(draft, t0, base, all, here);
           item(!any);
         }
         tcgen05_before_sync();
@@ -524,7 +537,7 @@ struct Softmax {
           wait(s, smem_u32(&s.done[w]), (count - 1) & 1);
           tcgen05_after_sync();
           if (*static_cast<volatile uint32_t*>(&s.bad[(tile + i) % kHereTiles]) == (uint32_t)(tile + i) + 1) {
-            add_infinite(g, heads.kv, draft, alive, t0, base, here);
+            add_infinite(g, heads.kv, draft, alive, t0, base, all, here);
             tcgen05_before_sync();  // (the next product comes after this thread's next arrival)
           }
         }
@@ -551,7 +564,7 @@ struct Softmax {
         total = a.y * c[0] + b.y * c[1];
       }
       if (!live) {
-        top = -CUDART_INF_F;
+        top = kPadding;
         total = 0.0f;
       }
       T* out = nullptr;

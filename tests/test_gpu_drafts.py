@@ -366,3 +366,28 @@ def test_captured_and_replayed():
         call()
         torch.cuda.synchronize()
         assert torch.equal(out, got) and torch.equal(weights, w), seed
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("drafts,dim", [(5, 64), (40, 128), (40, 200)])
+@pytest.mark.parametrize("junk", [math.nan, math.inf])
+def test_padding_may_hold_anything(kind, drafts, dim, junk):
+    """Queries, keys and values of padding are not finite, in rows that are split over many CTAs."""
+    lengths = [9000 + drafts, 70 + drafts]
+    c = U.Cache(kind, lengths, 2, dim, 16)
+    q = _randn(2, drafts, 4, dim, kind=kind, seed=6)
+    parents = D.trees(2, drafts, "tree", 6)
+    for r in range(2):
+        parents[r][drafts // 2] = -2
+    want, want_lse = T.attention_drafts(q, c.k, c.v, c.tables, c.lengths, parents=_i32(parents), return_lse=True)
+    w0, w1 = (torch.zeros(2, 2, c.tables.shape[1] * 16, device="cuda") for _ in range(2))
+    T.attention_drafts(q, c.k, c.v, c.tables, c.lengths, parents=_i32(parents), weights=w0)
+    for r, n in enumerate(lengths):
+        page, slot = D.slots(c, r, n)
+        for i, path in enumerate(D.seen_by(parents[r])):
+            if path is None:
+                at = n - drafts + i
+                q[r, i], c.k[page[at], slot[at]], c.v[page[at], slot[at]] = junk, junk, junk
+                assert bool((want[r, i] == 0).all()) and bool((want_lse[r, i] == -math.inf).all())
+    got, lse = T.attention_drafts(q, c.k, c.v, c.tables, c.lengths, parents=_i32(parents), return_lse=True, weights=w1)
+    assert torch.equal(got, want) and torch.equal(lse, want_lse) and torch.equal(w0, w1)
