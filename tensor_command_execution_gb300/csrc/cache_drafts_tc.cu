@@ -175,10 +175,16 @@ struct Loader {
       const bool inside = chunk < chunks;
       const T* at = from + (inside ? chunk * 8 : 0);
       const uint32_t dst = ring + slot * S::kSlot + chunk / 8 * kTile * 128;
-#pragma unroll 8
-      for (int r = row0; r < kTile; r += kOver) {
-        const int64_t o = offset[r];
-        copy_bytes<16>(dst + swizzled(r, chunk % 8), at + (o >= 0 ? o : 0), o >= 0 && inside ? 16 : 0);
+      constexpr int kAtOnce = 8;  // (offsets read before the copies that need them)
+#pragma unroll 1
+      for (int r0 = row0; r0 < kTile; r0 += kOver * kAtOnce) {
+        int64_t o[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) o[k] = r0 + k * kOver < kTile ? offset[r0 + k * kOver] : -1;
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k)
+          if (r0 + k * kOver < kTile)
+            copy_bytes<16>(dst + swizzled(r0 + k * kOver, chunk % 8), at + (o[k] >= 0 ? o[k] : 0), o[k] >= 0 && inside ? 16 : 0);
       }
     }
     // The arrival comes with the data; the thread that issues the products, not
@@ -629,10 +635,6 @@ __global__ void __launch_bounds__(kThreads, 1) drafts_tc_kernel(const __grid_con
   AttendRows& rows = *reinterpret_cast<AttendRows*>(&tree + 1);
   const int warp = threadIdx.x / 32;
 
-  wait_for_previous();
-  let_next_start();
-  AttendShare share;
-  if (!attend_begin<T>(p, rows, kTile, &share)) return;
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kSlots; ++i) {
       mbar_init(smem_u32(&s.full[i]), kLoaders);
@@ -650,12 +652,17 @@ __global__ void __launch_bounds__(kThreads, 1) drafts_tc_kernel(const __grid_con
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 2 * kGroup / 32) tmem_alloc(smem_u32(&s.tmem), 512);
+  wait_for_previous();
+  let_next_start();
+  AttendShare share;
+  const bool work = attend_begin<T>(p, rows, kTile, &share);  // (without work there is no segment below)
   tcgen05_before_sync();
   __syncthreads();
   tcgen05_after_sync();
   const uint32_t tmem = *static_cast<volatile uint32_t*>(&s.tmem);
   const uint32_t queries = smem_u32(s_mem), ring = queries + S::kRing;
-  if (warp < 2 * kGroup / 32) {
+  if (!work) {
+  } else if (warp < 2 * kGroup / 32) {
     Softmax<T, DP, WIDE> softmax(p, s, tree, tmem);
     softmax.run(rows, share, s_mem);
   } else if (warp == 2 * kGroup / 32) {
