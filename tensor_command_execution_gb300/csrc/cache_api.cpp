@@ -869,6 +869,14 @@ int64_t drafts_workspace(int64_t rows, int64_t drafts, int64_t q_heads, int64_t 
   return drafts_parts(drafts, q_heads, kv_heads, dim) + (weights ? round_up(rows * drafts * q_heads * 8, 16) : 0);
 }
 
+// (TMA copies are issued on device memory only)
+bool in_device_memory(const void* ptr) {
+  cudaPointerAttributes a;
+  if (cudaPointerGetAttributes(&a, ptr) == cudaSuccess) return a.type == cudaMemoryTypeDevice;
+  cudaGetLastError();
+  return false;
+}
+
 // A tensor that a call reads as i32 of these sizes, with any strides.
 void check_i32(const cmd_operand& o, const char* name, int rank, const int64_t* sizes) {
   check(o, name, rank);
@@ -980,6 +988,8 @@ extern "C" cmd_status cmd_attention_drafts(const cmd_drafts_args* args, void* cu
     const auto pieces = [&](int n) { return dim * es % n == 0 && vector_rows(a.k_cache, n) && vector_rows(a.v_cache, n); };
     const int copy = pieces(16) ? 16 : pieces(4) ? 4 : 0;
     const bool tc = copy == 16 && es == 2 && dim <= 128;
+    const bool tma = tc && cmdx::drafts_tma_fits(a.k_cache.sizes[1], a.k_cache.sizes, a.k_cache.strides, a.v_cache.strides) &&
+                     in_device_memory(a.k_cache.ptr) && in_device_memory(a.v_cache.ptr);
     const int most = tc ? cmdx::kDraftTcRows : cmdx::kDraftRows;
     p.blocks = (p.group + most - 1) / most;
     p.block_heads = (p.group + p.blocks - 1) / p.blocks;
@@ -1001,7 +1011,7 @@ extern "C" cmd_status cmd_attention_drafts(const cmd_drafts_args* args, void* cu
       p.stats = stats ? stats + r * drafts * heads : nullptr;
       const cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
       cudaError_t e = es == 4      ? (copy == 16 ? cmdx::drafts_f32_launch16 : cmdx::drafts_f32_launch4)(p, stream)
-                      : tc         ? cmdx::drafts_tc_launch(a.q.dtype, p, stream)
+                      : tc         ? (tma ? cmdx::drafts_tma_launch : cmdx::drafts_tc_launch)(a.q.dtype, p, stream)
                       : copy == 16 ? cmdx::drafts_mma_launch16(a.q.dtype, p, stream)
                       : copy == 4  ? cmdx::drafts_mma_launch4(a.q.dtype, p, stream)
                                    : cmdx::drafts_mma_launch0(a.q.dtype, p, stream);

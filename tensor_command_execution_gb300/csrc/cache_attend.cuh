@@ -294,23 +294,29 @@ __device__ __forceinline__ void attend_finish(const P& p, const AttendShare& w, 
   __syncthreads();  // the states may be overwritten
 }
 
-// What a CTA does before its first segment: the rows, those of them that are
-// empty (zeros, and a log-sum of -infinity), and its share. False: no work.
-template <class T, class P>
-__device__ __forceinline__ bool attend_begin(const P& p, AttendRows& s, int tile, AttendShare* w) {
-  attend_rows(p, s, tile);
+// Zeros, and a log-sum of -infinity, for the rows without a token: a row to a CTA.
+template <class T>
+__device__ __forceinline__ void attend_empty_rows(const AttendParams& p, const AttendRows& s) {
   const int heads = p.kv_heads * p.group, groups = p.kv_heads * p.blocks;
   for (int r = blockIdx.x; r < p.rows; r += gridDim.x) {
     if (s.at[r + 1] != s.at[r]) continue;
     for (int i = threadIdx.x; i < heads * p.dim; i += blockDim.x) {
       const int h = i / p.dim;
-      static_cast<T*>(p.out)[attend_place(p, r, h).out + (i - h * p.dim)] = from_float<T>(0.0f);
+      static_cast<T*>(p.out)[r * p.out_st[0] + h * p.out_st[1] + (i - h * p.dim)] = from_float<T>(0.0f);
     }
     if (p.lse)
-      for (int h = threadIdx.x; h < heads; h += blockDim.x) p.lse[attend_place(p, r, h).lse] = -CUDART_INF_F;
+      for (int h = threadIdx.x; h < heads; h += blockDim.x) p.lse[r * p.lse_st[0] + h * p.lse_st[1]] = -CUDART_INF_F;
     if (p.split_by_row)
       for (int i = threadIdx.x; i < groups; i += blockDim.x) p.splits[r * groups + i].parts = 0;
   }
+}
+
+// What a CTA does before its first segment: the rows, those of them that are
+// empty (zeros, and a log-sum of -infinity), and its share. False: no work.
+template <class T, class P>
+__device__ __forceinline__ bool attend_begin(const P& p, AttendRows& s, int tile, AttendShare* w) {
+  attend_rows(p, s, tile);
+  attend_empty_rows<T>(p, s);
   *w = attend_share(p, s);
   if (!p.split_by_row && threadIdx.x == 0) p.splits[blockIdx.x].parts = 0;  // (unless a row is split here, below)
   return w->begin != w->end;

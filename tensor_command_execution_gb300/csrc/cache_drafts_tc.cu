@@ -8,9 +8,10 @@
 // tensor units work on one group's products while the other's exponentials are
 // worked out: with 256 rows a group has its own rows (and a key or value is read
 // once for both), with 128 its own tiles, and the two halves are joined at the
-// end of a segment. One warp issues the products, three copy keys and values
-// (16-byte asynchronous copies, zeros where a row has no token) into a ring in
-// the layout that the products read.
+// end of a segment. One warp issues the products, another copies keys and values
+// into a ring in the layout that the products read: TMA boxes of the tokens that
+// a page and a tile share, where those are 8 or a multiple, else three warps
+// with 16-byte asynchronous copies.
 //
 // A weight is held as the sum of two 16-bit numbers, as in cache_attend_mma.cu:
 // P takes exactly the columns of S that it came from. O is rescaled only when a
@@ -23,12 +24,27 @@
 #include "exec_pipe.cuh"
 #include "tcgen05.cuh"
 
+#include <cudaTypedefs.h>
+
+#ifndef CMDX_TMA
+#error "cache_drafts_tc.cu is compiled for both kinds of copies, with -DCMDX_TMA=<1|0>"
+#endif
+
 namespace cmdx {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // (exec_host.cpp)
 
 namespace {
 
+struct TcParams : DraftParams {
+#if CMDX_TMA
+  CUtensorMap maps[2];  // keys, values: [page][kv head][slot][dim]
+  int32_t box;          // tokens of a copy: a power of two, 8 to 128
+#endif
+};
+
 constexpr int kGroup = 128;                   // threads of a softmax group, and query rows
-constexpr int kLoaders = 96;
+constexpr int kLoaders = CMDX_TMA ? 32 : 96;
 constexpr int kThreads = 2 * kGroup + 32 + kLoaders;
 constexpr int kTile = 128;                    // tokens
 constexpr uint64_t kPatience = 2000000000;    // ns: no wait takes longer
@@ -103,25 +119,30 @@ struct Shape {
 
 constexpr int kHereTiles = 8;
 struct State {
-  uint64_t full[8], empty[8], scores[2], weights[2], done[2], queries, end;
+  uint64_t full[8], empty[8], scores[2], weights[2], done[2], landed, queries, end;
   uint32_t tmem;
   uint32_t stop;                       // a wait ran out of time
   uint32_t here[kHereTiles][4];        // which tokens of a tile have a page
   uint32_t bad[kHereTiles];            // the last of these tiles (counted from 1) whose values are not all finite
   float2 part[2][kGroup];              // maximum and sum of a group's rows
+#if !CMDX_TMA
   int64_t k[2][kTile], v[2][kTile];    // offsets of a tile's rows, -1: none
+#endif
 };
 template <int DP, bool WIDE>
 constexpr int kSmem = Shape<DP, WIDE>::kRest + (int)(sizeof(State) + sizeof(DraftTree) + sizeof(AttendRows)) + 1024;
 
-// A wait that gives up (for the whole CTA) after kPatience.
+// A wait that gives up (for the whole CTA) after kPatience. (The clock is read
+// now and then only: a read takes about as long as a wait should.)
 __device__ __forceinline__ void wait(State& s, uint32_t bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return;
   volatile uint32_t* stop = &s.stop;
-  const uint64_t t0 = global_ns();
-  while (!mbar_try_wait(bar, parity)) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+    if (n % 256) continue;
     if (*stop) return;
-    if (global_ns() - t0 > kPatience) {
+    const uint64_t now = global_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kPatience) {
       *stop = 1;
       return;
     }
@@ -140,17 +161,117 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t x) {
 }
 
 // ---- the copies -----------------------------------------------------------------
+#if CMDX_TMA
+template <class T, int DP, bool WIDE>
+struct Loader {
+  using S = Shape<DP, WIDE>;
+  static constexpr int kPieces = DP / 8, kOver = 32 / kPieces;
+  const TcParams& p;
+  State& s;
+  const uint32_t ring;
+  // this lane's box of a tile, and the slab of 64 dims that it copies of it
+  const int lane = threadIdx.x % 32, boxes, box, slab, slabs;
+  uint32_t issued = 0, cleared = 0;  // keys and values in turn; tiles that were
+
+  __device__ __forceinline__ Loader(const TcParams& p_, State& s_, uint32_t ring_)
+      : p(p_), s(s_), ring(ring_), boxes(kTile / p_.box), box(lane % boxes), slab(lane / boxes), slabs((p_.dim + 63) / 64) {}
+
+  // Rows of no token become zeros, and so do values that are not finite,
+  // whatever their weight: the softmax group is told, and adds them where they
+  // are seen.
+  __device__ __forceinline__ void clear(uint32_t slot, const uint32_t* here) {
+    constexpr int kAtOnce = 8;
+    const int c = lane % kPieces;
+    if (c < (p.dim + 15) / 16 * 2) {
+      const uint32_t at = slot + c / 8 * kTile * 128;
+#pragma unroll 1
+      for (int r0 = lane / kPieces; r0 < kTile; r0 += kOver * kAtOnce) {
+        uint4 x[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) x[k] = lds128(at + swizzled(r0 + k * kOver, c % 8));
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          const int r = r0 + k * kOver;
+          const uint4 bad = make_uint4(not_finite<T>(x[k].x), not_finite<T>(x[k].y), not_finite<T>(x[k].z), not_finite<T>(x[k].w));
+          const bool in = here[r >> 5] >> (r & 31) & 1;
+          if (in && (bad.x | bad.y | bad.z | bad.w) == 0) continue;
+          sts128(at + swizzled(r, c % 8), in ? make_uint4(x[k].x & ~bad.x, x[k].y & ~bad.y, x[k].z & ~bad.z, x[k].w & ~bad.w) : make_uint4(0, 0, 0, 0));
+          if (in) *static_cast<volatile uint32_t*>(&s.bad[issued / 2 % kHereTiles]) = issued / 2 + 1;
+        }
+      }
+    }
+    fence_async_smem();
+    __syncwarp();
+  }
+
+  __device__ __forceinline__ void copy(const CUtensorMap& map, bool take, int n, int page, int first, int kv, const uint32_t* mask) {
+    const uint32_t at = issued % S::kSlots, slot = ring + at * S::kSlot, full = smem_u32(&s.full[at]);
+    const uint32_t bar = mask ? smem_u32(&s.landed) : full;
+    wait(s, smem_u32(&s.empty[at]), (issued / S::kSlots + 1) & 1);
+    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(n * slabs * p.box * 128));
+    __syncwarp();
+    if (take && slab < slabs)
+      asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+                       slot + slab * kTile * 128 + box * p.box * 128),
+                   "l"(&map), "r"(64 * slab), "r"(first), "r"(kv), "r"(page), "r"(bar)
+                   : "memory");
+    if (mask) {
+      wait(s, bar, cleared++ & 1);
+      clear(slot, mask);
+      if (lane == 0) mbar_arrive(full);
+    }
+    ++issued;
+  }
+
+  __device__ __forceinline__ void run(const AttendRows& rows, const AttendShare& share) {
+    int tile = 0;
+    for (AttendSegment g = attend_first(p, rows, share, kTile); g.tiles; g = attend_next(p, rows, share, g, kTile)) {
+      const int kv = attend_heads(p, g.group).kv, base = g.n - p.drafts;
+      int page = 0, slot = 0;
+      bool in = false;
+      const auto look_up = [&](int i) {  // (a tile ahead of the copies that need it)
+        const int t = (g.tile0 + i) * kTile + box * p.box;
+        in = i < g.tiles && t < g.n && t + p.box > g.lo;
+        const uint32_t column = fast_div32(p.page, (uint32_t)t);
+        slot = t - (int)(column * p.page.d);
+        if (in) page = p.tables[g.row * p.table_st[0] + column * p.table_st[1]];
+      };
+      look_up(0);
+      for (int i = 0; i < g.tiles; ++i, ++tile) {
+        if (in && (page < 0 || page >= p.n_pages)) {
+          report(p.status, CMD_CACHE_BAD_PAGE);
+          in = false;
+        }
+        const bool take = in;
+        const int from = page, first = slot;
+        const uint32_t taken = __ballot_sync(~0u, take && slab == 0);
+        look_up(i + 1);
+        // which tokens there are: a word to each of the first four lanes
+        const int t0 = (g.tile0 + i) * kTile, t = t0 + 32 * lane, begin = max(g.lo - t, 0), end = min(g.n - t, 32);
+        uint32_t word = begin < end ? (~0u >> (32 - (end - begin))) << begin : 0u;
+        for (int k = 0; k < 32; k += min(p.box, 32))
+          if (lane < 4 && !(taken >> ((32 * lane + k) / p.box) & 1)) word &= ~((p.box < 32 ? (1u << p.box) - 1u : ~0u) << k);
+        uint32_t* here = s.here[tile % kHereTiles];
+        if (lane < 4) here[lane] = word;
+        const bool all = __all_sync(~0u, lane >= 4 || word == ~0u) && draft_all_seen(p, t0, t0 + kTile, base);
+        copy(p.maps[0], take, __popc(taken), from, first, kv, nullptr);
+        copy(p.maps[1], take, __popc(taken), from, first, kv, all ? nullptr : here);
+      }
+    }
+  }
+};
+#else
 template <class T, int DP, bool WIDE>
 struct Loader {
   using S = Shape<DP, WIDE>;
   static constexpr int kChunks = DP / 8, kOver = kLoaders / kChunks;
-  const DraftParams& p;
+  const TcParams& p;
   State& s;
   const uint32_t ring;
   const int tid = threadIdx.x - 2 * kGroup - 32, chunk = tid % kChunks, row0 = tid / kChunks, chunks, used;
   uint32_t issued = 0;  // keys and values in turn
 
-  __device__ __forceinline__ Loader(const DraftParams& p_, State& s_, uint32_t ring_)
+  __device__ __forceinline__ Loader(const TcParams& p_, State& s_, uint32_t ring_)
       : p(p_), s(s_), ring(ring_), chunks(p_.dim / 8), used((p_.dim + 15) / 16 * 2) {}
 
   // Values that are not finite become zeros, whatever their weight, and the
@@ -253,6 +374,8 @@ struct Loader {
   }
 };
 
+#endif
+
 // ---- the products -----------------------------------------------------------------
 template <class T, int DP, bool WIDE>
 __device__ __forceinline__ void issue(const DraftParams& p, State& s, const AttendRows& rows, const AttendShare& share, uint32_t queries,
@@ -268,7 +391,7 @@ __device__ __forceinline__ void issue(const DraftParams& p, State& s, const Atte
     const int items = WIDE ? 2 * g.tiles : g.tiles;
     const auto wait_full = [&](uint32_t at, uint32_t copies) {
       wait(s, smem_u32(&s.full[at]), (copies / S::kSlots) & 1);
-      fence_async_smem();
+      if (!CMDX_TMA) fence_async_smem();
     };
     const auto scores = [&](int n) {
       const uint32_t group = tile0 + (WIDE ? n >> 1 : n), at = 2 * group % S::kSlots, w = n & 1;
@@ -626,7 +749,7 @@ struct Softmax {
 };
 
 template <class T, int DP, bool WIDE>
-__global__ void __launch_bounds__(kThreads, 1) drafts_tc_kernel(const __grid_constant__ DraftParams p) {
+__global__ void __launch_bounds__(kThreads, 1) drafts_tc_kernel(const __grid_constant__ TcParams p) {
   using S = Shape<DP, WIDE>;
   extern __shared__ unsigned char s_raw[];
   unsigned char* s_mem = s_raw + ((1024 - smem_u32(s_raw) % 1024) % 1024);
@@ -637,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1) drafts_tc_kernel(const __grid_con
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kSlots; ++i) {
-      mbar_init(smem_u32(&s.full[i]), kLoaders);
+      mbar_init(smem_u32(&s.full[i]), CMDX_TMA ? 1 : kLoaders);
       mbar_init(smem_u32(&s.empty[i]), 1);
     }
     for (int i = 0; i < kHereTiles; ++i) s.bad[i] = 0;
@@ -646,6 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1) drafts_tc_kernel(const __grid_con
       mbar_init(smem_u32(&s.weights[i]), kGroup);
       mbar_init(smem_u32(&s.done[i]), 1);
     }
+    mbar_init(smem_u32(&s.landed), 1);
     mbar_init(smem_u32(&s.queries), 2 * kGroup);
     mbar_init(smem_u32(&s.end), 1);
     s.stop = 0;
@@ -680,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1) drafts_tc_kernel(const __grid_con
 }
 
 template <class T, int DP, bool WIDE>
-cudaError_t launch(const DraftParams& p, cudaStream_t stream) {
+cudaError_t launch(const TcParams& p, cudaStream_t stream) {
   static PerDevice ready;  // (static storage: zero before first use)
   static_assert(kSmem<DP, WIDE> <= 227 * 1024, "the CTA fits an SM");
   const cudaError_t e = allow_smem(drafts_tc_kernel<T, DP, WIDE>, kSmem<DP, WIDE>, ready);
@@ -688,7 +812,7 @@ cudaError_t launch(const DraftParams& p, cudaStream_t stream) {
   return attend_launch<T>(drafts_tc_kernel<T, DP, WIDE>, p, 2, 152, kThreads, kSmem<DP, WIDE>, kTile, stream, false);
 }
 template <class T>
-cudaError_t launch_type(const DraftParams& p, cudaStream_t stream) {
+cudaError_t launch_type(const TcParams& p, cudaStream_t stream) {
   const bool wide = p.block_heads > kGroup;
   if (p.dim <= 64) return wide ? launch<T, 64, true>(p, stream) : launch<T, 64, false>(p, stream);
   return wide ? launch<T, 128, true>(p, stream) : launch<T, 128, false>(p, stream);
@@ -696,8 +820,41 @@ cudaError_t launch_type(const DraftParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t drafts_tc_launch(int dtype, const DraftParams& p, cudaStream_t stream) {
+#if CMDX_TMA
+bool drafts_tma_fits(int64_t page_size, const int64_t (&sizes)[4], const int64_t (&k_st)[4], const int64_t (&v_st)[4]) {
+  if (page_size % 8 || sizes[0] < 1) return false;
+  for (int d = 0; d < 3; ++d)
+    for (const int64_t st : {k_st[d], v_st[d]})
+      if (sizes[d] > 1 && (st == 0 || st >= (int64_t(1) << 38))) return false;
+  return tensor_map_encoder() != nullptr;
+}
+
+cudaError_t drafts_tma_launch(int dtype, const DraftParams& d, cudaStream_t stream) {
+  TcParams p;
+  static_cast<DraftParams&>(p) = d;
+  p.box = kTile;
+  while (p.page.d % p.box) p.box /= 2;
+  for (int i = 0; i < 2; ++i) {
+    const int64_t* st = i == 0 ? p.k_st : p.v_st;  // page, slot, head
+    // (a stride of a dim of one element may be anything)
+    const auto bytes = [&](int64_t n, int64_t stride) { return (cuuint64_t)(n > 1 ? 2 * stride : 16); };
+    const cuuint64_t sizes[4] = {(cuuint64_t)p.dim, p.page.d, (cuuint64_t)p.kv_heads, (cuuint64_t)p.n_pages};
+    const cuuint64_t strides[3] = {bytes(p.page.d, st[1]), bytes(p.kv_heads, st[2]), bytes(p.n_pages, st[0])};
+    const cuuint32_t box[4] = {64, (cuuint32_t)p.box, 1, 1}, step[4] = {1, 1, 1, 1};
+    const CUresult r = tensor_map_encoder()(
+        &p.maps[i], dtype == CMD_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+        const_cast<void*>(i == 0 ? p.k : p.v), sizes, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+  }
   return dtype == CMD_F16 ? launch_type<__half>(p, stream) : launch_type<__nv_bfloat16>(p, stream);
 }
+#else
+cudaError_t drafts_tc_launch(int dtype, const DraftParams& d, cudaStream_t stream) {
+  TcParams p;
+  static_cast<DraftParams&>(p) = d;
+  return dtype == CMD_F16 ? launch_type<__half>(p, stream) : launch_type<__nv_bfloat16>(p, stream);
+}
+#endif
 
 }  // namespace cmdx

@@ -144,8 +144,11 @@ constexpr int kDraftTcCtas = 152, kDraftTcRows = 256;
 cudaError_t drafts_mma_launch16(int dtype, const DraftParams& p, cudaStream_t stream);
 cudaError_t drafts_mma_launch4(int dtype, const DraftParams& p, cudaStream_t stream);
 cudaError_t drafts_mma_launch0(int dtype, const DraftParams& p, cudaStream_t stream);
-// 16-byte copies, dims up to 128
+// 16-byte copies, dims up to 128; by TMA, where pages of `sizes` and these
+// strides (page, slot, head, dim; elements) in device memory suit it
 cudaError_t drafts_tc_launch(int dtype, const DraftParams& p, cudaStream_t stream);
+cudaError_t drafts_tma_launch(int dtype, const DraftParams& p, cudaStream_t stream);
+bool drafts_tma_fits(int64_t page_size, const int64_t (&sizes)[4], const int64_t (&k_st)[4], const int64_t (&v_st)[4]);
 cudaError_t drafts_f32_launch16(const DraftParams& p, cudaStream_t stream);
 cudaError_t drafts_f32_launch4(const DraftParams& p, cudaStream_t stream);
 // The weights, from the maxima and sums that the attention has left in p.stats.

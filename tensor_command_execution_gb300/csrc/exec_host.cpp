@@ -78,7 +78,7 @@ cudaError_t generic_launch(int tier, bool ext, const GenericParams& p, cudaStrea
   return kGenericLaunch[ext][tier](p, stream);
 }
 
-static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   if (!fn) {
     void* f = nullptr;
