@@ -377,57 +377,68 @@ struct Loader {
 #endif
 
 // ---- the products -----------------------------------------------------------------
+// (What comes from shared memory passes through a shuffle, so that it is known
+// to be the same in all lanes.)
 template <class T, int DP, bool WIDE>
 __device__ __forceinline__ void issue(const DraftParams& p, State& s, const AttendRows& rows, const AttendShare& share, uint32_t queries,
                                       uint32_t ring, uint32_t tmem) {
   using S = Shape<DP, WIDE>;
   const int steps = (p.dim + 15) / 16;
-  const uint32_t qk = tcgen05_shape(kBf16<T>, kTile, false), pv = tcgen05_shape(kBf16<T>, steps * 16, true);
-  uint32_t tile0 = 0, segments = 0, count[2] = {0, 0};
+  const uint32_t qk = tcgen05_shape(kBf16<T>, kTile, false), pv = tcgen05_shape(kBf16<T>, steps * 16, true), one = elected();
+  // the copies (keys and values in turn) that the next products read, modulo
+  // twice the ring, and how often the groups' weights were waited for
+  uint32_t keys = 0, values = 1, segments = 0, count = 0;
+  const auto wait_full = [&](uint32_t copy) {
+    wait(s, smem_u32(&s.full[copy % S::kSlots]), copy / S::kSlots & 1);
+    if (!CMDX_TMA) fence_async_smem();
+  };
   for (AttendSegment g = attend_first(p, rows, share, kTile); g.tiles; g = attend_next(p, rows, share, g, kTile)) {
     wait(s, smem_u32(&s.queries), segments & 1);
     ++segments;
     tcgen05_after_sync();
-    const int items = WIDE ? 2 * g.tiles : g.tiles;
-    const auto wait_full = [&](uint32_t at, uint32_t copies) {
-      wait(s, smem_u32(&s.full[at]), (copies / S::kSlots) & 1);
-      if (!CMDX_TMA) fence_async_smem();
-    };
-    const auto scores = [&](int n) {
-      const uint32_t group = tile0 + (WIDE ? n >> 1 : n), at = 2 * group % S::kSlots, w = n & 1;
-      if (!WIDE || w == 0) wait_full(at, 2 * group);
-      const uint32_t q = queries + (WIDE ? w * kGroup * 128 : 0), k = ring + at * S::kSlot;
-      for (int e = 0; e < steps; ++e) {
-        const uint32_t slab = e / 4, in = e % 4 * 32;
-        tcgen05_mma(tmem + S::kScores + w * kTile, smem_along_k(q + slab * S::kRows * 128 + in), smem_along_k(k + slab * kTile * 128 + in), qk, e > 0);
+    const int items = __shfl_sync(~0u, WIDE ? 2 * g.tiles : g.tiles, 0);
+    const auto scores = [&](uint32_t w) {
+      if (!WIDE || w == 0) wait_full(keys);
+      const uint32_t q = queries + (WIDE ? w * kGroup * 128 : 0), at = keys % S::kSlots;
+      const uint64_t a = smem_along_k(q), b = smem_along_k(ring + at * S::kSlot);
+#pragma unroll
+      for (int e = 0; e < DP / 16; ++e)
+        if (e < steps)
+          tcgen05_mma(one, tmem + S::kScores + w * kTile, a + (e / 4 * S::kRows * 128 + e % 4 * 32) / 16, b + (e / 4 * kTile * 128 + e % 4 * 32) / 16,
+                      qk, e > 0);
+      tcgen05_commit(one, smem_u32(&s.scores[w]));
+      if (!WIDE || w == 1) {
+        tcgen05_commit(one, smem_u32(&s.empty[at]));
+        keys = (keys + 2) % (2 * S::kSlots);
       }
-      tcgen05_commit(smem_u32(&s.scores[w]));
-      if (!WIDE || w == 1) tcgen05_commit(smem_u32(&s.empty[at]));
     };
     scores(0);
     if (items > 1) scores(1);
+#pragma unroll 1
     for (int n = 0; n < items; ++n) {
-      const uint32_t group = tile0 + (WIDE ? n >> 1 : n), at = (2 * group + 1) % S::kSlots, w = n & 1;
-      if (!WIDE || w == 0) wait_full(at, 2 * group + 1);
-      wait(s, smem_u32(&s.weights[w]), count[w] & 1);
-      ++count[w];
+      const uint32_t w = n & 1;
+      if (!WIDE || w == 0) wait_full(values);
+      wait(s, smem_u32(&s.weights[w]), count >> w & 1);
+      count ^= 1u << w;
       tcgen05_after_sync();
-      const uint32_t v = ring + at * S::kSlot, weights = tmem + S::kScores + w * kTile, out = tmem + S::kOut + w * 128;
+      const uint32_t at = values % S::kSlots, weights = tmem + S::kScores + w * kTile, out = tmem + S::kOut + w * 128;
+      const uint64_t b = smem_across_k(ring + at * S::kSlot, kTile * 128);
 #pragma unroll
       for (int e = 0; e < kTile / 16; ++e) {
         // (a chunk of 32 tokens: 16 columns of the weights' upper parts, 16 of the lower)
         const uint32_t a = weights + e / 2 * 32 + e % 2 * 8;
-        const uint64_t b = smem_across_k(v + e * 2048, kTile * 128);
-        tcgen05_mma(out, a, b, pv, n > 1 || e > 0);
-        tcgen05_mma(out, a + 16, b, pv, true);
+        tcgen05_mma(one, out, a, b + e * 2048 / 16, pv, n > 1 || e > 0);
+        tcgen05_mma(one, out, a + 16, b + e * 2048 / 16, pv, true);
       }
-      tcgen05_commit(smem_u32(&s.done[w]));
-      if (!WIDE || w == 1) tcgen05_commit(smem_u32(&s.empty[at]));
-      if (n + 2 < items) scores(n + 2);
+      tcgen05_commit(one, smem_u32(&s.done[w]));
+      if (!WIDE || w == 1) {
+        tcgen05_commit(one, smem_u32(&s.empty[at]));
+        values = (values + 2) % (2 * S::kSlots);
+      }
+      if (n + 2 < items) scores(w);
     }
-    tile0 += g.tiles;
   }
-  tcgen05_commit(smem_u32(&s.end));
+  tcgen05_commit(one, smem_u32(&s.end));
   wait(s, smem_u32(&s.end), 0);
 }
 
@@ -790,8 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1) drafts_tc_kernel(const __grid_con
     Softmax<T, DP, WIDE> softmax(p, s, tree, tmem);
     softmax.run(rows, share, s_mem);
   } else if (warp == 2 * kGroup / 32) {
-    if (threadIdx.x % 32 == 0) issue<T, DP, WIDE>(p, s, rows, share, queries, ring, tmem);
-    __syncwarp();
+    issue<T, DP, WIDE>(p, s, rows, share, queries, ring, __shfl_sync(~0u, tmem, 0));
   } else {
     Loader<T, DP, WIDE> loader(p, s, ring);
     loader.run(rows, share);
@@ -809,7 +819,7 @@ cudaError_t launch(const TcParams& p, cudaStream_t stream) {
   static_assert(kSmem<DP, WIDE> <= 227 * 1024, "the CTA fits an SM");
   const cudaError_t e = allow_smem(drafts_tc_kernel<T, DP, WIDE>, kSmem<DP, WIDE>, ready);
   if (e != cudaSuccess) return e;
-  return attend_launch<T>(drafts_tc_kernel<T, DP, WIDE>, p, 2, 152, kThreads, kSmem<DP, WIDE>, kTile, stream, false);
+  return attend_launch<T>(drafts_tc_kernel<T, DP, WIDE>, p, 4, 152, kThreads, kSmem<DP, WIDE>, kTile, stream, false);
 }
 template <class T>
 cudaError_t launch_type(const TcParams& p, cudaStream_t stream) {

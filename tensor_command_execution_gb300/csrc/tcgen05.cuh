@@ -70,21 +70,35 @@ __device__ __forceinline__ uint32_t swizzled(uint32_t r, uint32_t c) { return r 
 __device__ __forceinline__ uint32_t tcgen05_shape(bool bf16, int n, bool b_across) {
   return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_across ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
 }
-// d (+)= a * b, one step of 16 in K; one thread issues it
-__device__ __forceinline__ void tcgen05_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {
-  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a),
-               "l"(b), "r"(shape), "r"((uint32_t)add)
-               : "memory");
+// One lane of the warp (the same one each time).
+__device__ __forceinline__ uint32_t elected() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r;
+}
+// d (+)= a * b, one step of 16 in K, issued by the elected lane. (A predicate,
+// not a branch: all lanes work out the addresses, which stay in the warp's
+// uniform registers, where the instruction takes them from. Issued from a branch
+// of one lane, a product took 95 cycles, of any size.)
+__device__ __forceinline__ void tcgen05_mma(uint32_t lane, uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(shape), "r"((uint32_t)add), "r"(lane)
+      : "memory");
 }
 // ... with a in tensor memory (two 16-bit numbers to a column)
-__device__ __forceinline__ void tcgen05_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool add) {
-  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a),
-               "l"(b), "r"(shape), "r"((uint32_t)add)
-               : "memory");
+__device__ __forceinline__ void tcgen05_mma(uint32_t lane, uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool add) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(shape), "r"((uint32_t)add), "r"(lane)
+      : "memory");
 }
-// An arrival on the mbarrier once everything that this thread has issued is done.
-__device__ __forceinline__ void tcgen05_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+// An arrival on the mbarrier once everything that the elected lane has issued is done.
+__device__ __forceinline__ void tcgen05_commit(uint32_t lane, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.u32 q, %1, 0;\n @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+      "r"(lane)
+      : "memory");
 }
 
 }  // namespace cmdx
