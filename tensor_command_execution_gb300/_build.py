@@ -60,7 +60,7 @@ CU_SOURCES = [("exec_tile2d.cu", _objs((2,), (0, 1))), ("exec_generic.cu", _objs
               ("static_scratch.cu", [{}]),
               ("cache_attend.cu", [{}]),
               ("cache_attend_mma.cu", [dict(CMDX_COPY=16), dict(CMDX_COPY=4)]),
-              ("cache_drafts_tc.cu", [dict(CMDX_TMA=1), dict(CMDX_TMA=0)]), ("cache_drafts_mma.cu", [dict(CMDX_COPY=16), dict(CMDX_COPY=4), dict(CMDX_COPY=0)]),
+              ("cache_drafts_tc.cu", [dict(CMDX_TMA=1), dict(CMDX_TMA=0)]), ("cache_weigh_tc.cu", [{}]), ("cache_drafts_mma.cu", [dict(CMDX_COPY=16), dict(CMDX_COPY=4), dict(CMDX_COPY=0)]),
               ("cache_attend_f32.cu", [dict(CMDX_COPY=16), dict(CMDX_COPY=4)]),
               ("cache_drafts_f32.cu", [dict(CMDX_COPY=16), dict(CMDX_COPY=4)]), ("cache_rope.cu", [{}]), ("cache_pages.cu", [{}]),
               ("cache_keep.cu", [{}])]
@@ -68,7 +68,7 @@ CPP_SOURCES = ["cmd_api.cpp", "cmd_yaml.cpp", "exec_host.cpp", "cache_api.cpp"]
 TORCH_SOURCE = "cache_torch.cpp"
 HEADERS = ["cmd_internal.h", "exec_common.cuh", "exec_pipe.cuh", "exec_tile2d.h", "interp_asm.cuh",
            "gen_interp.py", "cache_internal.h", "cache_common.cuh", "cache_attend.cuh",
-           "cache_attend_ring.cuh", "cache_drafts.cuh", "cache_mma.cuh", "tcgen05.cuh"]
+           "cache_attend_ring.cuh", "cache_drafts.cuh", "cache_mma.cuh", "cache_tc.cuh", "tcgen05.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -526,6 +526,18 @@ void attention_common(cmdx::AttendParams& p, const cmd_operand& k_cache, const c
   p.v = v_cache.ptr;
 }
 
+// The blocks of query heads of the one-token attention's kernels, and their launch.
+void attend_blocks(cmdx::AttendParams& p, int es, int copy) {
+  const int most = copy && es == 2 ? cmdx::kAttendMmaHeads : cmdx::kAttendHeads;
+  p.blocks = (p.group + most - 1) / most;
+  p.block_heads = (p.group + p.blocks - 1) / p.blocks;
+}
+cudaError_t attend_one(int dtype, int copy, const cmdx::AttendParams& p, cudaStream_t stream) {
+  if (!copy) return cmdx::attend_simt_launch(dtype, p, stream);
+  if (elem_size(dtype) == 4) return (copy == 16 ? cmdx::attend_f32_launch16 : cmdx::attend_f32_launch4)(p, stream);
+  return (copy == 16 ? cmdx::attend_mma_launch16 : cmdx::attend_mma_launch4)(dtype, p, stream);
+}
+
 }  // namespace
 
 extern "C" cmd_status cmd_attention_workspace(int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t* bytes) {
@@ -596,9 +608,7 @@ extern "C" cmd_status cmd_attention_decode(const cmd_attention_args* args, void*
     // heads of 128: bf16 180 us with 16, 217 with 4; 24 f32 ones of 2999 tokens and 16 kv heads 180 and 226.)
     const auto pieces = [&](int n) { return dim * es % n == 0 && vector_rows(a.k_cache, n) && vector_rows(a.v_cache, n); };
     const int copy = pieces(16) ? 16 : pieces(4) ? 4 : 0;
-    const int most = copy && es == 2 ? cmdx::kAttendMmaHeads : cmdx::kAttendHeads;
-    p.blocks = (p.group + most - 1) / most;
-    p.block_heads = (p.group + p.blocks - 1) / p.blocks;
+    attend_blocks(p, es, copy);
     p.q_pairs = vector_rows(a.q, 4);
     // a launch's units (tiles of rows that fill their tables, for each head) stay below 2^31
     const int64_t row_units = (int64_t)p.kv_heads * p.blocks *
@@ -612,11 +622,7 @@ extern "C" cmd_status cmd_attention_decode(const cmd_attention_args* args, void*
       p.lse = a.lse.ptr ? static_cast<float*>(a.lse.ptr) + r * a.lse.strides[0] : nullptr;
       p.tables = static_cast<const int32_t*>(a.tables.ptr) + r * a.tables.strides[0];
       p.lengths = static_cast<const int32_t*>(a.lengths.ptr) + r * a.lengths.strides[0];
-      const cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
-      const cudaError_t e = !copy       ? cmdx::attend_simt_launch(a.q.dtype, p, stream)
-                            : es == 4   ? (copy == 16 ? cmdx::attend_f32_launch16 : cmdx::attend_f32_launch4)(p, stream)
-                                        : (copy == 16 ? cmdx::attend_mma_launch16
-                                                      : cmdx::attend_mma_launch4)(a.q.dtype, p, stream);
+      const cudaError_t e = attend_one(a.q.dtype, copy, p, static_cast<cudaStream_t>(cuda_stream));
       if (e != cudaSuccess) return launched(e);
     }
     return CMD_OK;
@@ -863,7 +869,7 @@ constexpr int64_t kDraftHeads = 1 << 20;  // drafts * q_heads, at most
 int64_t drafts_parts(int64_t drafts, int64_t q_heads, int64_t kv_heads, int64_t dim) {
   const int64_t group = drafts * (q_heads / kv_heads);
   const int64_t rows = std::max(std::min<int64_t>(group, cmdx::kDraftRows) * cmdx::kDraftCtas, std::min<int64_t>(group, cmdx::kDraftTcRows) * cmdx::kDraftTcCtas);
-  return round_up(cmdx::kDraftCtas, 16) * (int64_t)sizeof(cmdx::AttendSplit) + 2 * rows * (round_up(dim, 4) + 4) * 4;
+  return std::max(attention_workspace(q_heads, kv_heads, dim), kSplitBytes + 2 * rows * (round_up(dim, 4) + 4) * 4);
 }
 int64_t drafts_workspace(int64_t rows, int64_t drafts, int64_t q_heads, int64_t kv_heads, int64_t dim, bool weights) {
   return drafts_parts(drafts, q_heads, kv_heads, dim) + (weights ? round_up(rows * drafts * q_heads * 8, 16) : 0);
@@ -981,18 +987,22 @@ extern "C" cmd_status cmd_attention_drafts(const cmd_drafts_args* args, void* cu
     if (has_weights)
       for (int d = 0; d < 2; ++d) p.w_st[d] = a.weights.strides[d];
     p.splits = static_cast<cmdx::AttendSplit*>(a.workspace);
-    p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + round_up(cmdx::kDraftCtas, 16) * sizeof(cmdx::AttendSplit));
+    p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kSplitBytes);
     float2* stats = has_weights ? reinterpret_cast<float2*>(static_cast<uint8_t*>(a.workspace) + drafts_parts(drafts, heads, kv, dim)) : nullptr;
     p.status = a.status;
     const int es = elem_size(a.q.dtype);
     const auto pieces = [&](int n) { return dim * es % n == 0 && vector_rows(a.k_cache, n) && vector_rows(a.v_cache, n); };
     const int copy = pieces(16) ? 16 : pieces(4) ? 4 : 0;
-    const bool tc = copy == 16 && es == 2 && dim <= 128;
-    const bool tma = tc && cmdx::drafts_tma_fits(a.k_cache.sizes[1], a.k_cache.sizes, a.k_cache.strides, a.v_cache.strides) &&
+    const bool one = drafts == 1 && !has_parents, tc = copy == 16 && es == 2 && dim <= 128;
+    const bool tma = tc && (!one || has_weights) && cmdx::drafts_tma_fits(a.k_cache.sizes[1], a.k_cache.sizes, a.k_cache.strides, a.v_cache.strides) &&
                      in_device_memory(a.k_cache.ptr) && in_device_memory(a.v_cache.ptr);
-    const int most = tc ? cmdx::kDraftTcRows : cmdx::kDraftRows;
-    p.blocks = (p.group + most - 1) / most;
-    p.block_heads = (p.group + p.blocks - 1) / p.blocks;
+    if (one) {
+      attend_blocks(p, es, copy);
+    } else {
+      const int most = tc ? cmdx::kDraftTcRows : cmdx::kDraftRows;
+      p.blocks = (p.group + most - 1) / most;
+      p.block_heads = (p.group + p.blocks - 1) / p.blocks;
+    }
     p.q_pairs = dim % 2 == 0 && vector_rows(a.q, 4);
     p.q_vectors = vector_rows(a.q, 16);
     p.out_vectors = vector_rows(a.out, 16);
@@ -1010,13 +1020,15 @@ extern "C" cmd_status cmd_attention_drafts(const cmd_drafts_args* args, void* cu
       p.weights = has_weights ? static_cast<float*>(a.weights.ptr) + r * a.weights.strides[0] : nullptr;
       p.stats = stats ? stats + r * drafts * heads : nullptr;
       const cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
-      cudaError_t e = es == 4      ? (copy == 16 ? cmdx::drafts_f32_launch16 : cmdx::drafts_f32_launch4)(p, stream)
+      cudaError_t e = one          ? attend_one(a.q.dtype, copy, p, stream)
+                      : es == 4    ? (copy == 16 ? cmdx::drafts_f32_launch16 : cmdx::drafts_f32_launch4)(p, stream)
                       : tc         ? (tma ? cmdx::drafts_tma_launch : cmdx::drafts_tc_launch)(a.q.dtype, p, stream)
                       : copy == 16 ? cmdx::drafts_mma_launch16(a.q.dtype, p, stream)
                       : copy == 4  ? cmdx::drafts_mma_launch4(a.q.dtype, p, stream)
                                    : cmdx::drafts_mma_launch0(a.q.dtype, p, stream);
       if (e == cudaSuccess && has_weights)
         e = es == 4      ? (copy == 16 ? cmdx::weigh_f32_launch16 : cmdx::weigh_f32_launch4)(p, stream)
+            : tma        ? cmdx::weigh_tma_launch(a.q.dtype, p, stream)
             : copy == 16 ? cmdx::weigh_mma_launch16(a.q.dtype, p, stream)
             : copy == 4  ? cmdx::weigh_mma_launch4(a.q.dtype, p, stream)
                          : cmdx::weigh_mma_launch0(a.q.dtype, p, stream);

@@ -200,7 +200,9 @@ struct AttendPlace {
 __device__ __forceinline__ AttendPlace attend_place(const AttendParams& p, int row, int h) {
   return {row * p.out_st[0] + h * p.out_st[1], row * p.lse_st[0] + h * p.lse_st[1]};
 }
-__device__ __forceinline__ void attend_note(const AttendParams&, int, int, float, float) {}
+__device__ __forceinline__ void attend_note(const AttendParams& p, int row, int h, float top, float l) {
+  if (p.stats) p.stats[(int64_t)row * p.kv_heads * p.group + h] = make_float2(top, l);
+}
 // Whether a part with this maximum says that its row is empty, whatever the others hold.
 __device__ __forceinline__ bool attend_void(const AttendParams&, float) { return false; }
 

@@ -34,9 +34,6 @@ __device__ __forceinline__ AttendPlace attend_place(const DraftParams& p, int ro
   return {row * p.out_st[0] + draft * p.out_draft + head * p.out_st[1],
           row * p.lse_st[0] + draft * p.lse_draft + head * p.lse_st[1]};
 }
-__device__ __forceinline__ void attend_note(const DraftParams& p, int row, int h, float top, float l) {
-  if (p.stats) p.stats[(int64_t)row * p.kv_heads * p.group + h] = make_float2(top, l);
-}
 // The maximum that a part of padding is given (with a sum of zero): the parts
 // of tokens that every draft sees are worked out without the tree, as if it
 // were none.

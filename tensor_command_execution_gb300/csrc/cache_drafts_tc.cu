@@ -21,10 +21,7 @@
 #include "cache_drafts.cuh"
 #include "cache_attend_ring.cuh"
 #include "cache_mma.cuh"
-#include "exec_pipe.cuh"
-#include "tcgen05.cuh"
-
-#include <cudaTypedefs.h>
+#include "cache_tc.cuh"
 
 #ifndef CMDX_TMA
 #error "cache_drafts_tc.cu is compiled for both kinds of copies, with -DCMDX_TMA=<1|0>"
@@ -32,22 +29,12 @@
 
 namespace cmdx {
 
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // (exec_host.cpp)
-
 namespace {
-
-struct TcParams : DraftParams {
-#if CMDX_TMA
-  CUtensorMap maps[2];  // keys, values: [page][kv head][slot][dim]
-  int32_t box;          // tokens of a copy: a power of two, 8 to 128
-#endif
-};
 
 constexpr int kGroup = 128;                   // threads of a softmax group, and query rows
 constexpr int kLoaders = CMDX_TMA ? 32 : 96;
 constexpr int kThreads = 2 * kGroup + 32 + kLoaders;
 constexpr int kTile = 128;                    // tokens
-constexpr uint64_t kPatience = 2000000000;    // ns: no wait takes longer
 
 // Powers of two: how far a maximum may grow before O is rescaled, and how far
 // weights are lifted.
@@ -64,32 +51,6 @@ constexpr bool kBf16 = true;
 template <>
 constexpr bool kBf16<__half> = false;
 
-// ---- pairs of binary32 numbers in one instruction --------------------------------
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t x) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
 // x and y rounded to 16 bits, and what that leaves of each, rounded again
 template <class T>
 __device__ __forceinline__ void split2(float x, float y, uint32_t* hi, uint32_t* lo) {
@@ -131,23 +92,6 @@ struct State {
 };
 template <int DP, bool WIDE>
 constexpr int kSmem = Shape<DP, WIDE>::kRest + (int)(sizeof(State) + sizeof(DraftTree) + sizeof(AttendRows)) + 1024;
-
-// A wait that gives up (for the whole CTA) after kPatience. (The clock is read
-// now and then only: a read takes about as long as a wait should.)
-__device__ __forceinline__ void wait(State& s, uint32_t bar, uint32_t parity) {
-  volatile uint32_t* stop = &s.stop;
-  uint64_t t0 = 0;
-  for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
-    if (n % 256) continue;
-    if (*stop) return;
-    const uint64_t now = global_ns();
-    if (t0 == 0) t0 = now;
-    if (now - t0 > kPatience) {
-      *stop = 1;
-      return;
-    }
-  }
-}
 
 template <class T>
 constexpr uint32_t kExponent = 0x7f807f80u;
@@ -207,7 +151,7 @@ struct Loader {
   __device__ __forceinline__ void copy(const CUtensorMap& map, bool take, int n, int page, int first, int kv, const uint32_t* mask) {
     const uint32_t at = issued % S::kSlots, slot = ring + at * S::kSlot, full = smem_u32(&s.full[at]);
     const uint32_t bar = mask ? smem_u32(&s.landed) : full;
-    wait(s, smem_u32(&s.empty[at]), (issued / S::kSlots + 1) & 1);
+    wait(s.stop, smem_u32(&s.empty[at]), (issued / S::kSlots + 1) & 1);
     if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(n * slabs * p.box * 128));
     __syncwarp();
     if (take && slab < slabs)
@@ -216,7 +160,7 @@ struct Loader {
                    "l"(&map), "r"(64 * slab), "r"(first), "r"(kv), "r"(page), "r"(bar)
                    : "memory");
     if (mask) {
-      wait(s, bar, cleared++ & 1);
+      wait(s.stop, bar, cleared++ & 1);
       clear(slot, mask);
       if (lane == 0) mbar_arrive(full);
     }
@@ -291,7 +235,7 @@ struct Loader {
   __device__ __forceinline__ void copy(const T* from, const int64_t* offset, bool mask) {
     const int slot = issued % S::kSlots;
     const uint32_t bar = smem_u32(&s.empty[slot]), parity = (issued / S::kSlots + 1) & 1;
-    wait(s, bar, parity);
+    wait(s.stop, bar, parity);
     if (chunk < used) {
       const bool inside = chunk < chunks;
       const T* at = from + (inside ? chunk * 8 : 0);
@@ -389,11 +333,11 @@ __device__ __forceinline__ void issue(const DraftParams& p, State& s, const Atte
   // twice the ring, and how often the groups' weights were waited for
   uint32_t keys = 0, values = 1, segments = 0, count = 0;
   const auto wait_full = [&](uint32_t copy) {
-    wait(s, smem_u32(&s.full[copy % S::kSlots]), copy / S::kSlots & 1);
+    wait(s.stop, smem_u32(&s.full[copy % S::kSlots]), copy / S::kSlots & 1);
     if (!CMDX_TMA) fence_async_smem();
   };
   for (AttendSegment g = attend_first(p, rows, share, kTile); g.tiles; g = attend_next(p, rows, share, g, kTile)) {
-    wait(s, smem_u32(&s.queries), segments & 1);
+    wait(s.stop, smem_u32(&s.queries), segments & 1);
     ++segments;
     tcgen05_after_sync();
     const int items = __shfl_sync(~0u, WIDE ? 2 * g.tiles : g.tiles, 0);
@@ -418,7 +362,7 @@ __device__ __forceinline__ void issue(const DraftParams& p, State& s, const Atte
     for (int n = 0; n < items; ++n) {
       const uint32_t w = n & 1;
       if (!WIDE || w == 0) wait_full(values);
-      wait(s, smem_u32(&s.weights[w]), count >> w & 1);
+      wait(s.stop, smem_u32(&s.weights[w]), count >> w & 1);
       count ^= 1u << w;
       tcgen05_after_sync();
       const uint32_t at = values % S::kSlots, weights = tmem + S::kScores + w * kTile, out = tmem + S::kOut + w * 128;
@@ -439,7 +383,7 @@ __device__ __forceinline__ void issue(const DraftParams& p, State& s, const Atte
     }
   }
   tcgen05_commit(one, smem_u32(&s.end));
-  wait(s, smem_u32(&s.end), 0);
+  wait(s.stop, smem_u32(&s.end), 0);
 }
 
 // ---- the softmax --------------------------------------------------------------------
@@ -540,7 +484,7 @@ struct Softmax {
       const float now = top - kRaise<T>, c = grown ? attend_weight(m, now) : 1.0f;
       if (grown) m = now;
       if (!first && __any_sync(~0u, c != 1.0f)) {
-        wait(s, smem_u32(&s.done[w]), (count - 1) & 1);
+        wait(s.stop, smem_u32(&s.done[w]), (count - 1) & 1);
         tcgen05_after_sync();
         rescale(c);
       }
@@ -660,7 +604,7 @@ struct Softmax {
       for (int i = WIDE ? 0 : w; i < g.tiles; i += WIDE ? 1 : 2) {
         const int t0 = (g.tile0 + i) * kTile;
         // (the tile's scores are there: so is what the copies say of it)
-        wait(s, smem_u32(&s.scores[w]), count & 1);
+        wait(s.stop, smem_u32(&s.scores[w]), count & 1);
         const uint32_t* at = s.here[(tile + i) % kHereTiles];
         const uint32_t here[4] = {at[0], at[1], at[2], at[3]};
         const bool all = draft_all_seen(p, t0, t0 + kTile, base), mask = !all || (here[0] & here[1] & here[2] & here[3]) != ~0u;
@@ -674,7 +618,7 @@ struct Softmax {
         ++count;
         any = true;
         if (mask) {
-          wait(s, smem_u32(&s.done[w]), (count - 1) & 1);
+          wait(s.stop, smem_u32(&s.done[w]), (count - 1) & 1);
           tcgen05_after_sync();
           if (*static_cast<volatile uint32_t*>(&s.bad[(tile + i) % kHereTiles]) == (uint32_t)(tile + i) + 1) {
             add_infinite(g, heads.kv, draft, alive, t0, base, all, here);
@@ -682,7 +626,7 @@ struct Softmax {
           }
         }
       }
-      if (any) wait(s, smem_u32(&s.done[w]), (count - 1) & 1);
+      if (any) wait(s.stop, smem_u32(&s.done[w]), (count - 1) & 1);
       tcgen05_after_sync();
       tile += g.tiles;
 
@@ -841,27 +785,13 @@ bool drafts_tma_fits(int64_t page_size, const int64_t (&sizes)[4], const int64_t
 
 cudaError_t drafts_tma_launch(int dtype, const DraftParams& d, cudaStream_t stream) {
   TcParams p;
-  static_cast<DraftParams&>(p) = d;
-  p.box = kTile;
-  while (p.page.d % p.box) p.box /= 2;
-  for (int i = 0; i < 2; ++i) {
-    const int64_t* st = i == 0 ? p.k_st : p.v_st;  // page, slot, head
-    // (a stride of a dim of one element may be anything)
-    const auto bytes = [&](int64_t n, int64_t stride) { return (cuuint64_t)(n > 1 ? 2 * stride : 16); };
-    const cuuint64_t sizes[4] = {(cuuint64_t)p.dim, p.page.d, (cuuint64_t)p.kv_heads, (cuuint64_t)p.n_pages};
-    const cuuint64_t strides[3] = {bytes(p.page.d, st[1]), bytes(p.kv_heads, st[2]), bytes(p.n_pages, st[0])};
-    const cuuint32_t box[4] = {64, (cuuint32_t)p.box, 1, 1}, step[4] = {1, 1, 1, 1};
-    const CUresult r = tensor_map_encoder()(
-        &p.maps[i], dtype == CMD_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-        const_cast<void*>(i == 0 ? p.k : p.v), sizes, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
-  }
+  const cudaError_t e = pool_maps(dtype, d, &p);
+  if (e != cudaSuccess) return e;
   return dtype == CMD_F16 ? launch_type<__half>(p, stream) : launch_type<__nv_bfloat16>(p, stream);
 }
 #else
 cudaError_t drafts_tc_launch(int dtype, const DraftParams& d, cudaStream_t stream) {
-  TcParams p;
+  TcParams p = {};
   static_cast<DraftParams&>(p) = d;
   return dtype == CMD_F16 ? launch_type<__half>(p, stream) : launch_type<__nv_bfloat16>(p, stream);
 }

@@ -103,6 +103,7 @@ struct AttendParams {
   int32_t team;        // CTAs of a cluster that takes one row and group; 0: units are dealt out evenly
   uint8_t split_by_row;
   int32_t* status;
+  float2* stats;       // optional: a row's maximum and sum for each head, [rows][kv_heads * group]
   uint8_t q_pairs;     // q rows may be read two 16-bit elements at a time
 };
 
@@ -132,7 +133,6 @@ struct DraftParams : AttendParams {
   const int32_t* parents;     // NULL: each draft goes on from the one before
   int64_t parent_st[2];
   int32_t near;               // the caller's window, 0: none
-  float2* stats;              // optional: maximum and sum, [rows][kv heads][group]
   float* weights;             // optional: [rows, kv heads, tokens], added to
   int64_t w_st[2];
   uint8_t q_vectors, out_vectors;  // their rows may be accessed 16 bytes at a time
@@ -155,6 +155,7 @@ cudaError_t drafts_f32_launch4(const DraftParams& p, cudaStream_t stream);
 cudaError_t weigh_mma_launch16(int dtype, const DraftParams& p, cudaStream_t stream);
 cudaError_t weigh_mma_launch4(int dtype, const DraftParams& p, cudaStream_t stream);
 cudaError_t weigh_mma_launch0(int dtype, const DraftParams& p, cudaStream_t stream);
+cudaError_t weigh_tma_launch(int dtype, const DraftParams& p, cudaStream_t stream);  // (where drafts_tma_launch may be)
 cudaError_t weigh_f32_launch16(const DraftParams& p, cudaStream_t stream);
 cudaError_t weigh_f32_launch4(const DraftParams& p, cudaStream_t stream);
 
