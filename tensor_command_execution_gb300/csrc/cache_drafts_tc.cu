@@ -113,19 +113,17 @@ struct Loader {
   const TcParams& p;
   State& s;
   const uint32_t ring;
-  // this lane's box of a tile, and the slab of 64 dims that it copies of it
-  const int lane = threadIdx.x % 32, boxes, box, slab, slabs;
+  TmaTiles tiles;
   uint32_t issued = 0, cleared = 0;  // keys and values in turn; tiles that were
 
-  __device__ __forceinline__ Loader(const TcParams& p_, State& s_, uint32_t ring_)
-      : p(p_), s(s_), ring(ring_), boxes(kTile / p_.box), box(lane % boxes), slab(lane / boxes), slabs((p_.dim + 63) / 64) {}
+  __device__ __forceinline__ Loader(const TcParams& p_, State& s_, uint32_t ring_) : p(p_), s(s_), ring(ring_), tiles(p_) {}
 
   // Rows of no token become zeros, and so do values that are not finite,
   // whatever their weight: the softmax group is told, and adds them where they
   // are seen.
   __device__ __forceinline__ void clear(uint32_t slot, const uint32_t* here) {
     constexpr int kAtOnce = 8;
-    const int c = lane % kPieces;
+    const int lane = tiles.lane, c = lane % kPieces;
     if (c < (p.dim + 15) / 16 * 2) {
       const uint32_t at = slot + c / 8 * kTile * 128;
 #pragma unroll 1
@@ -148,21 +146,14 @@ struct Loader {
     __syncwarp();
   }
 
-  __device__ __forceinline__ void copy(const CUtensorMap& map, bool take, int n, int page, int first, int kv, const uint32_t* mask) {
+  __device__ __forceinline__ void copy(const CUtensorMap& map, int kv, const uint32_t* mask) {
     const uint32_t at = issued % S::kSlots, slot = ring + at * S::kSlot, full = smem_u32(&s.full[at]);
-    const uint32_t bar = mask ? smem_u32(&s.landed) : full;
     wait(s.stop, smem_u32(&s.empty[at]), (issued / S::kSlots + 1) & 1);
-    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(n * slabs * p.box * 128));
-    __syncwarp();
-    if (take && slab < slabs)
-      asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
-                       slot + slab * kTile * 128 + box * p.box * 128),
-                   "l"(&map), "r"(64 * slab), "r"(first), "r"(kv), "r"(page), "r"(bar)
-                   : "memory");
+    tiles.copy(map, kv, slot, mask ? smem_u32(&s.landed) : full);
     if (mask) {
-      wait(s.stop, bar, cleared++ & 1);
+      wait(s.stop, smem_u32(&s.landed), cleared++ & 1);
       clear(slot, mask);
-      if (lane == 0) mbar_arrive(full);
+      if (tiles.lane == 0) mbar_arrive(full);
     }
     ++issued;
   }
@@ -171,35 +162,15 @@ struct Loader {
     int tile = 0;
     for (AttendSegment g = attend_first(p, rows, share, kTile); g.tiles; g = attend_next(p, rows, share, g, kTile)) {
       const int kv = attend_heads(p, g.group).kv, base = g.n - p.drafts;
-      int page = 0, slot = 0;
-      bool in = false;
-      const auto look_up = [&](int i) {  // (a tile ahead of the copies that need it)
-        const int t = (g.tile0 + i) * kTile + box * p.box;
-        in = i < g.tiles && t < g.n && t + p.box > g.lo;
-        const uint32_t column = fast_div32(p.page, (uint32_t)t);
-        slot = t - (int)(column * p.page.d);
-        if (in) page = p.tables[g.row * p.table_st[0] + column * p.table_st[1]];
-      };
-      look_up(0);
+      tiles.begin(g);
       for (int i = 0; i < g.tiles; ++i, ++tile) {
-        if (in && (page < 0 || page >= p.n_pages)) {
-          report(p.status, CMD_CACHE_BAD_PAGE);
-          in = false;
-        }
-        const bool take = in;
-        const int from = page, first = slot;
-        const uint32_t taken = __ballot_sync(~0u, take && slab == 0);
-        look_up(i + 1);
-        // which tokens there are: a word to each of the first four lanes
-        const int t0 = (g.tile0 + i) * kTile, t = t0 + 32 * lane, begin = max(g.lo - t, 0), end = min(g.n - t, 32);
-        uint32_t word = begin < end ? (~0u >> (32 - (end - begin))) << begin : 0u;
-        for (int k = 0; k < 32; k += min(p.box, 32))
-          if (lane < 4 && !(taken >> ((32 * lane + k) / p.box) & 1)) word &= ~((p.box < 32 ? (1u << p.box) - 1u : ~0u) << k);
+        tiles.look<true>(i);
+        const int t0 = (g.tile0 + i) * kTile;
         uint32_t* here = s.here[tile % kHereTiles];
-        if (lane < 4) here[lane] = word;
-        const bool all = __all_sync(~0u, lane >= 4 || word == ~0u) && draft_all_seen(p, t0, t0 + kTile, base);
-        copy(p.maps[0], take, __popc(taken), from, first, kv, nullptr);
-        copy(p.maps[1], take, __popc(taken), from, first, kv, all ? nullptr : here);
+        if (tiles.lane < 4) here[tiles.lane] = tiles.here;
+        const bool all = __all_sync(~0u, tiles.lane >= 4 || tiles.here == ~0u) && draft_all_seen(p, t0, t0 + kTile, base);
+        copy(p.maps[0], kv, nullptr);
+        copy(p.maps[1], kv, all ? nullptr : here);
       }
     }
   }

@@ -61,6 +61,70 @@ __device__ __forceinline__ void wait(uint32_t& stop_word, uint32_t bar, uint32_t
   }
 }
 
+// What a warp needs to copy the tiles of a segment by TMA: a lane to a box of
+// tokens (and a slab of 64 dims of it). Table entries are read for as many
+// tiles at once as the lanes hold, and so many again ahead of the copies.
+struct TmaTiles {
+  const TcParams& p;
+  const int lane, boxes, box, slab, each;  // each: tiles to a batch of entries
+  AttendSegment g;
+  int page = 0, next = 0;  // of this lane's box in its tile of the batch, and of the next batch
+  // the tile at hand: this lane's box is there, its page and first slot; which
+  // boxes are; which of tokens 32 * lane .. + 31 are (lanes 0 to 3)
+  bool take = false;
+  int from = 0, first = 0;
+  uint32_t taken = 0, here = 0;
+
+  __device__ __forceinline__ TmaTiles(const TcParams& p_)
+      : p(p_), lane(threadIdx.x % 32), boxes(kTcTile / p_.box), box(lane % boxes), slab(lane / boxes), each(32 / boxes) {}
+
+  __device__ __forceinline__ bool inside(int t) const { return t < g.n && t + p.box > g.lo; }
+  __device__ __forceinline__ int entry(int batch) const {
+    const int i = batch * each + slab, t = (g.tile0 + i) * kTcTile + box * p.box;
+    if (i >= g.tiles || !inside(t)) return 0;
+    return p.tables[g.row * p.table_st[0] + fast_div32(p.page, (uint32_t)t) * p.table_st[1]];
+  }
+  __device__ __forceinline__ void begin(const AttendSegment& segment) {
+    g = segment;
+    next = entry(0);
+  }
+  // Tile i of the segment (in order). REPORT: of entries that name no page.
+  template <bool REPORT>
+  __device__ __forceinline__ void look(int i) {
+    const int sub = i % each;
+    if (sub == 0) {
+      page = next;
+      next = entry(i / each + 1);
+    }
+    const int t0 = (g.tile0 + i) * kTcTile, t = t0 + box * p.box;
+    from = __shfl_sync(~0u, page, sub * boxes + box);
+    const uint32_t column = fast_div32(p.page, (uint32_t)t);
+    first = t - (int)(column * p.page.d);
+    take = inside(t);
+    if (take && (from < 0 || from >= p.n_pages)) {
+      if (REPORT) report(p.status, CMD_CACHE_BAD_PAGE);
+      take = false;
+    }
+    taken = __ballot_sync(~0u, take && slab == 0);
+    const int mine = t0 + 32 * lane, begin = max(g.lo - mine, 0), end = min(g.n - mine, 32);
+    here = begin < end ? (~0u >> (32 - (end - begin))) << begin : 0u;
+    if (taken != (boxes == 32 ? ~0u : (1u << boxes) - 1u))
+      for (int k = 0; k < 32; k += min(p.box, 32))
+        if (lane < 4 && !(taken >> ((32 * lane + k) / p.box) & 1)) here &= ~((p.box < 32 ? (1u << p.box) - 1u : ~0u) << k);
+  }
+  // Copies one kv head's tile into a slot, completing on the mbarrier `bar`.
+  __device__ __forceinline__ void copy(const CUtensorMap& map, int kv, uint32_t slot, uint32_t bar) const {
+    const int slabs = (p.dim + 63) / 64;
+    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(__popc(taken) * slabs * p.box * 128));
+    __syncwarp();
+    if (take && slab < slabs)
+      asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+                       slot + slab * kTcTile * 128 + box * p.box * 128),
+                   "l"(&map), "r"(64 * slab), "r"(first), "r"(kv), "r"(from), "r"(bar)
+                   : "memory");
+  }
+};
+
 // ---- pairs of binary32 numbers in one instruction --------------------------------
 __device__ __forceinline__ uint64_t pair(float a, float b) {
   uint64_t r;

@@ -50,38 +50,17 @@ constexpr int kSmem = Shape<DP>::kRest + (int)(sizeof(State) + sizeof(DraftTree)
 template <int DP>
 __device__ __forceinline__ void copy_keys(const Params& p, State& s, uint32_t ring, const AttendRows& rows, const AttendShare& share) {
   using S = Shape<DP>;
-  const int lane = threadIdx.x % 32, boxes = kTile / p.box, box = lane % boxes, slab = lane / boxes, slabs = (p.dim + 63) / 64;
+  TmaTiles tiles(p);
   uint32_t issued = 0;
   for (AttendSegment g = attend_first(p, rows, share, kTile); g.tiles; g = attend_next(p, rows, share, g, kTile)) {
-    int page = 0, slot = 0;
-    bool in = false;
-    const auto look_up = [&](int i) {  // (a tile ahead of the copies that need it)
-      const int t = (g.tile0 + i) * kTile + box * p.box;
-      in = i < g.tiles && t < g.n && t + p.box > g.lo;
-      const uint32_t column = fast_div32(p.page, (uint32_t)t);
-      slot = t - (int)(column * p.page.d);
-      if (in) page = p.tables[g.row * p.table_st[0] + column * p.table_st[1]];
-    };
-    look_up(0);
+    tiles.begin(g);
     for (int i = 0; i < g.tiles; ++i, ++issued) {
-      const bool take = in && page >= 0 && page < p.n_pages;  // (what is wrong has been reported by the attention)
-      const int from = page, first = slot;
-      const uint32_t taken = __ballot_sync(~0u, take && slab == 0), at = issued % S::kSlots, full = smem_u32(&s.full[at]);
-      look_up(i + 1);
-      const int t = (g.tile0 + i) * kTile + 32 * lane, begin = max(g.lo - t, 0), end = min(g.n - t, 32);
-      uint32_t word = begin < end ? (~0u >> (32 - (end - begin))) << begin : 0u;
-      for (int k = 0; k < 32; k += min(p.box, 32))
-        if (lane < 4 && !(taken >> ((32 * lane + k) / p.box) & 1)) word &= ~((p.box < 32 ? (1u << p.box) - 1u : ~0u) << k);
+      tiles.look<false>(i);  // (what is wrong has been reported by the attention)
+      const uint32_t at = issued % S::kSlots;
       wait(s.stop, smem_u32(&s.empty[at]), (issued / S::kSlots + 1) & 1);
-      if (lane < 4) s.here[issued % kHereTiles][lane] = word;
+      if (tiles.lane < 4) s.here[issued % kHereTiles][tiles.lane] = tiles.here;
       __syncwarp();
-      if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(__popc(taken) * slabs * p.box * 128));
-      __syncwarp();
-      if (take && slab < slabs)
-        asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
-                         ring + at * S::kSlot + slab * kTile * 128 + box * p.box * 128),
-                     "l"(&p.maps[0]), "r"(64 * slab), "r"(first), "r"(g.group), "r"(from), "r"(full)
-                     : "memory");
+      tiles.copy(p.maps[0], g.group, ring + at * S::kSlot, smem_u32(&s.full[at]));
     }
   }
 }
@@ -120,28 +99,68 @@ __device__ __forceinline__ void issue(const Params& p, State& s, const AttendRow
   wait(s.stop, smem_u32(&s.end), 0);
 }
 
-// The sum of a tile that not every draft sees, or whose scores are capped.
-__device__ __noinline__ float sum_masked(const Params& p, const State& s, const DraftTree& tree, uint32_t at, int n, int t, int base, bool all) {
-  float sum = 0.0f;
+// Scores that the cap changes, and those of query rows that do not see the
+// token, which become -infinity (whatever they are).
+__device__ __noinline__ void prepare(const Params& p, const DraftTree& tree, uint32_t at, int columns, int t, int base, bool all) {
+  const int per = (int)p.per.d;
+  int draft = (int)fast_div32(p.per, (uint32_t)p.row0), head = p.row0 - draft * per;
 #pragma unroll 1
-  for (int c = 0; c < n; c += 32) {
+  for (int c = 0; c < columns; c += 32) {
     uint32_t x[32];
     tmem_load(x, at + c);
     tmem_wait_load(x);
-#pragma unroll 1
-    for (int k = 0; k < 32; k += 8) {
+    if (p.cap_out != 0.0f) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(p.cap_out * tanhf(__uint_as_float(x[e]) * p.cap_in));
+    }
+    if (!all) {
+      bool sees = tree.sees(p, min(draft, p.drafts - 1), t, base);
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
-        if (e / 8 * 8 != k || c + e >= n) continue;
-        const float4 st = s.stats[(c + e) / 2];
-        const float m = e & 1 ? st.y : st.x, r = e & 1 ? st.w : st.z;
-        const int draft = (int)fast_div32(p.per, (uint32_t)(p.row0 + c + e));
-        const float y = attend_score(p, __uint_as_float(x[e]));
-        if ((all || tree.sees(p, draft, t, base)) && r != 0.0f && y != -CUDART_INF_F) sum += power_of_two(y + m) * r;
+        if (!sees) x[e] = __float_as_uint(-CUDART_INF_F);
+        if (++head == per) {
+          head = 0;
+          ++draft;
+          sees = tree.sees(p, min(draft, p.drafts - 1), t, base);
+        }
+      }
+    }
+    tmem_store(at + c, x);
+  }
+  tmem_wait_store();
+}
+
+// What a token gets from the query rows. HIDDEN: scores of -infinity count
+// nothing, whatever their row's statistics.
+template <bool HIDDEN>
+__device__ __forceinline__ float token_sum(const State& s, uint32_t at, int columns, float to_log2) {
+  const uint64_t scale = pair(to_log2, to_log2);
+  uint64_t part[2] = {0, 0};
+#pragma unroll 1
+  for (int c = 0; c < columns; c += 32) {
+    uint32_t x[32];
+    tmem_load(x, at + c);
+    tmem_wait_load(x);
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      if (e % 16 == 0 && c + e >= columns) break;  // (columns are a multiple of 16)
+      const float4 st = s.stats[(c + e) / 2];
+      float2 z = unpair(fma2(pair(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), scale, pair(st.x, st.y)));
+      // (a score that is not a number: its row's 1 / l is none either, or the row
+      // is zeros beside an infinite key, and 1 / l is 0)
+      z.x = fmaxf(z.x, -200.0f);
+      z.y = fmaxf(z.y, -200.0f);
+      if (HIDDEN) {
+        const float a = __uint_as_float(x[e]) == -CUDART_INF_F ? 0.0f : power_of_two(z.x) * st.z;
+        const float b = __uint_as_float(x[e + 1]) == -CUDART_INF_F ? 0.0f : power_of_two(z.y) * st.w;
+        part[e / 2 & 1] = add2(part[e / 2 & 1], pair(a, b));
+      } else {
+        part[e / 2 & 1] = fma2(pair(power_of_two(z.x), power_of_two(z.y)), pair(st.z, st.w), part[e / 2 & 1]);
       }
     }
   }
-  return sum;
+  const float2 both = unpair(add2(part[0], part[1]));
+  return both.x + both.y;
 }
 
 template <class T, int DP>
@@ -206,27 +225,12 @@ __device__ __forceinline__ void sums(const Params& p, State& s, DraftTree& tree,
       tcgen05_after_sync();
       const uint32_t here = s.here[items % kHereTiles][token / 32];
       const bool all = draft_all_seen(p, t0, t0 + kTile, base);
-      float sum = 0.0f;
+      float sum;
       if (!all || p.cap_out != 0.0f) {
-        sum = sum_masked(p, s, tree, at, n, t, base, all);
+        prepare(p, tree, at, columns, t, base, all);
+        sum = token_sum<true>(s, at, columns, p.cap_out != 0.0f ? 1.0f : p.scale_log2);
       } else {
-        const uint64_t scale = pair(p.scale_log2, p.scale_log2);
-        uint64_t part[2] = {0, 0};
-#pragma unroll 1
-        for (int c = 0; c < columns; c += 32) {
-          uint32_t x[32];
-          tmem_load(x, at + c);
-          tmem_wait_load(x);
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            if (e % 16 == 0 && c + e >= columns) break;  // (columns are a multiple of 16)
-            const float4 st = s.stats[(c + e) / 2];
-            const float2 z = unpair(fma2(pair(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), scale, pair(st.x, st.y)));
-            part[e / 2 & 1] = fma2(pair(power_of_two(z.x), power_of_two(z.y)), pair(st.z, st.w), part[e / 2 & 1]);
-          }
-        }
-        const float2 both = unpair(add2(part[0], part[1]));
-        sum = both.x + both.y;
+        sum = token_sum<false>(s, at, columns, p.scale_log2);
       }
       tcgen05_before_sync();
       mbar_arrive(smem_u32(&s.taken[w]));
@@ -306,7 +310,7 @@ cudaError_t weigh_tma_launch(int dtype, const DraftParams& d, cudaStream_t strea
   const cudaError_t e = pool_maps(dtype, d, &p);
   if (e != cudaSuccess) return e;
   p.blocks = p.sides = 1;
-  p.start_units = 1;
+  p.start_units = 4;
   return dtype == CMD_F16 ? by_dim<__half>(p, stream) : by_dim<__nv_bfloat16>(p, stream);
 }
 
