@@ -509,6 +509,17 @@ inline int attend_team_size(const AttendParams& p, int ctas, int tile) {
   return tiles <= team * kTeamTiles && (int64_t)p.rows * p.kv_heads * p.blocks * team * 3 <= ctas * 2 ? team : 0;
 }
 
+// The CTAs of a launch of at most `ctas`, and how many groups work side by side:
+// all groups, where that leaves at most a twentieth of the places
+// empty. Measured on 64 rows of 4096 tokens, 8 kv heads (bf16, heads side by
+// side in a page), against units of all groups in one order: dim 72 (144-byte
+// rows) 119 and 159 us, 96 138 and 165, 128 176.5 and 179.5, f32 of 72 189 and
+// 233; heads outermost, dim 128, 180 and 182.5; 64 ragged rows 48.5 and 48.5.
+inline int attend_sides(int groups, int ctas, int32_t* sides) {
+  *sides = ctas / groups * groups * 20 >= ctas * 19 ? groups : 1;
+  return *sides > 1 ? ctas / groups * groups : ctas;
+}
+
 // Launches a kernel of `ctas` CTAs of `threads` threads that splits its work
 // as above in tiles of `tile` tokens (teams: it can also work in teams), and
 // the join. The joining warps: 16 to a
@@ -525,13 +536,7 @@ cudaError_t attend_launch(K kernel, P p, int start_units, int ctas, int threads,
     return launch_clusters(kernel, p.team, p.rows * p.kv_heads * p.blocks * p.team, threads, (size_t)smem, stream, p);
   const int groups = p.kv_heads * p.blocks;
   const int64_t rows = (int64_t)p.rows * groups;
-  // groups side by side, where that leaves at most a twentieth of the places
-  // empty. Measured on 64 rows of 4096 tokens, 8 kv heads (bf16, heads side by
-  // side in a page), against units of all groups in one order: dim 72 (144-byte
-  // rows) 119 and 159 us, 96 138 and 165, 128 176.5 and 179.5, f32 of 72 189 and
-  // 233; heads outermost, dim 128, 180 and 182.5; 64 ragged rows 48.5 and 48.5.
-  p.sides = ctas / groups * groups * 20 >= ctas * 19 ? groups : 1;
-  if (p.sides > 1) ctas = ctas / groups * groups;
+  ctas = attend_sides(groups, ctas, &p.sides);
   p.split_by_row = rows <= ctas;
   const int lists = p.split_by_row ? (int)rows : ctas;
   p.tasks = lists * p.block_heads;

@@ -220,6 +220,8 @@ __device__ __forceinline__ void sums(const Params& p, State& s, DraftTree& tree,
     for (int i = 0; i < g.tiles; ++i, ++items) {
       if ((items & 1) != w) continue;
       const int t0 = (g.tile0 + i) * kTile, t = t0 + token;
+      float before = 0.0f;
+      if (t >= g.lo && t < g.n) before = weights[t];  // (on its way while the scores are worked out)
       wait(s.stop, smem_u32(&s.scores[w]), count & 1);
       ++count;
       tcgen05_after_sync();
@@ -234,7 +236,7 @@ __device__ __forceinline__ void sums(const Params& p, State& s, DraftTree& tree,
       }
       tcgen05_before_sync();
       mbar_arrive(smem_u32(&s.taken[w]));
-      if (here >> (token % 32) & 1) weights[t] += sum;
+      if (here >> (token % 32) & 1) weights[t] = before + sum;
     }
   }
 }
@@ -294,8 +296,9 @@ cudaError_t launch(const Params& p, cudaStream_t stream) {
   static_assert(kSmem<DP> <= 227 * 1024, "the CTA fits an SM");
   cudaError_t e = allow_smem(weigh_tc_kernel<T, DP>, kSmem<DP>, ready);
   Params q = p;
+  const int ctas = attend_sides(p.kv_heads, 152, &q.sides);
   for (q.row0 = 0; e == cudaSuccess && q.row0 < q.group; q.row0 += kMostRows)
-    e = launch_chained(weigh_tc_kernel<T, DP>, 152, kThreads, (size_t)kSmem<DP>, stream, q);
+    e = launch_chained(weigh_tc_kernel<T, DP>, ctas, kThreads, (size_t)kSmem<DP>, stream, q);
   return e;
 }
 template <class T>
@@ -309,7 +312,7 @@ cudaError_t weigh_tma_launch(int dtype, const DraftParams& d, cudaStream_t strea
   Params p;
   const cudaError_t e = pool_maps(dtype, d, &p);
   if (e != cudaSuccess) return e;
-  p.blocks = p.sides = 1;
+  p.blocks = 1;
   p.start_units = 4;
   return dtype == CMD_F16 ? by_dim<__half>(p, stream) : by_dim<__nv_bfloat16>(p, stream);
 }
