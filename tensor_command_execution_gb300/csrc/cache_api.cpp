@@ -1282,6 +1282,9 @@ extern "C" cmd_status cmd_cache_evict(const cmd_evict_args* args, void* cuda_str
     p.budget = a.budget;
     p.recent = a.recent;
     p.kept = static_cast<int32_t*>(a.workspace);
+    // at least 4 pieces (64 bytes) to a CTA, and no more CTAs than fill the device about four times
+    p.slices = 1;
+    while (p.slices * 8 <= p.pieces && (int64_t)p.rows * p.layers * p.heads * p.slices < 152 * 8) p.slices *= 2;
     return launched(cmdx::evict_launch(p, list, static_cast<cudaStream_t>(cuda_stream)));
   });
 }

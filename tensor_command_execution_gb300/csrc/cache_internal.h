@@ -187,6 +187,7 @@ struct KeepParams {
   int32_t drafts;
   // evict
   int32_t budget, recent, layers;
+  int32_t slices;             // a token's pieces go to so many CTAs
   int32_t* kept;              // [rows][layers][heads][budget]
 };
 struct KeepPool {

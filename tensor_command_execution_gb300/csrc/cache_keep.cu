@@ -164,13 +164,15 @@ __device__ __forceinline__ void release_pages(const KeepParams& p, int row, int 
 }
 
 // ---- the accepted branch's tokens ----------------------------------------------------
-// A thread takes one piece of a token (16 bytes where all rows allow it) in
-// one pool, and moves it for all tokens of a row, in order.
+// A CTA takes some pieces of a token (16 bytes each where all rows allow it) of
+// one row in one pool, a thread one piece of every accepted token, in order.
+// Where the tokens lie is worked out once for the CTA, all at the same time.
 constexpr int kAcceptThreads = 128;
 
 template <class U>
 __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const __grid_constant__ KeepParams p, const __grid_constant__ KeepPools pools) {
-  constexpr int kAtOnce = 4;
+  constexpr int kAtOnce = 8;
+  __shared__ int64_t s_from[CMD_CACHE_MAX_DRAFTS], s_to[CMD_CACHE_MAX_DRAFTS];  // (from -1: it stays)
   wait_for_previous();
   let_next_start();
   const uint32_t at = blockIdx.x * kAcceptThreads + threadIdx.x;
@@ -181,37 +183,46 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const __grid_con
     const int before = keep_length(p, row), base = before - p.drafts, now = p.lengths_out[row];
     if (base < 0) continue;
     if (blockIdx.x == 0 && blockIdx.y == 0) release_pages(p, row, now, before);
-    if (at >= (uint32_t)(p.heads * p.pieces)) continue;
+    const int count = now - base;
     const int32_t* path = p.path + row * p.path_st;
     const int32_t* table = p.tables + row * p.table_st;
     const auto slot = [&](int t) {
       const uint32_t column = fast_div32(p.page, (uint32_t)t);
-      return reinterpret_cast<U*>(base_ptr + table[column] * pool.st[0] + (int64_t)(t - column * p.page.d) * pool.st[1]);
+      return table[column] * pool.st[0] + (int64_t)(t - column * p.page.d) * pool.st[1];
     };
-    for (int j = 0; j < now - base; j += kAtOnce) {
-      U x[kAtOnce];
-      bool moves[kAtOnce];
-#pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) {
-        const int of = j + k < now - base ? path[j + k] : j + k;
-        moves[k] = of != j + k;
-        if (moves[k]) x[k] = *slot(base + of);
-      }
-#pragma unroll
-      for (int k = 0; k < kAtOnce; ++k)
-        if (moves[k]) *slot(base + j + k) = x[k];
+    for (int j = threadIdx.x; j < count; j += kAcceptThreads) {
+      const int of = path[j];
+      s_from[j] = of == j ? -1 : slot(base + of);
+      s_to[j] = of == j ? 0 : slot(base + j);
     }
+    __syncthreads();
+    if (at < (uint32_t)(p.heads * p.pieces)) {
+      for (int j = 0; j < count; j += kAtOnce) {
+        U x[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k)
+          if (j + k < count && s_from[j + k] >= 0) x[k] = *reinterpret_cast<const U*>(base_ptr + s_from[j + k]);
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k)
+          if (j + k < count && s_from[j + k] >= 0) *reinterpret_cast<U*>(base_ptr + s_to[j + k]) = x[k];
+      }
+    }
+    __syncthreads();
   }
 }
 
 // ---- eviction --------------------------------------------------------------------------
 // Which tokens one kv head of one layer and row keeps: those whose key (the
 // weight's bits, in the order of the numbers) is above the threshold, and of
-// those at it the first. The threshold is found digit by digit from a
-// histogram. Weights are read once where they fit in shared memory.
-constexpr int kSelectThreads = 512, kSelectWarps = kSelectThreads / 32;
+// those at it the first. The threshold's first 11 bits come from a histogram of
+// all keys; the few with the same first bits are then gathered, and its others
+// come from histograms of them. Keys are read once where they fit in shared
+// memory; in the last pass each warp writes the kept ones of its run of tokens
+// behind those of the runs before.
+constexpr int kSelectThreads = 1024, kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kCached = 48 * 1024;  // keys
+constexpr int kCached = 44 * 1024;  // keys
+constexpr int kGathered = 1024;     // of equal first bits, at most: more are gone over where they lie
 
 __device__ __forceinline__ uint32_t order_of(float x) {
   if (x != x) return 0;  // below all numbers
@@ -219,12 +230,67 @@ __device__ __forceinline__ uint32_t order_of(float x) {
   return b >> 31 ? ~b : b | 0x80000000u;
 }
 
+struct SelectState {
+  uint32_t bins[kBins];
+  uint32_t warp[kSelectWarps], more[kSelectWarps], equal[kSelectWarps];
+  uint32_t digit, above, gathered;
+  uint32_t key[kGathered];
+  int32_t token[kGathered];
+};
+
+// Counts a warp's keys' digits (those with `mine`).
+__device__ __forceinline__ void count_digit(SelectState& s, uint32_t digit, bool mine) {
+  const uint32_t who = __ballot_sync(~0u, mine);
+  if (!mine) return;
+  int same;
+  __match_all_sync(who, digit, &same);  // (equal weights would meet in one counter)
+  if (!same) atomicAdd(&s.bins[digit], 1u);
+  else if ((threadIdx.x & 31) == __ffs(who) - 1) atomicAdd(&s.bins[digit], (uint32_t)__popc(who));
+}
+// The digit at which the counts from the largest down reach `left`; *left then
+// counts on among the keys of that digit. Every thread calls it.
+__device__ __forceinline__ uint32_t find_digit(SelectState& s, uint32_t* left) {
+  constexpr int kEach = kBins / kSelectThreads;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __syncthreads();
+  const int first = kBins - 1 - (int)threadIdx.x * kEach;
+  uint32_t sum = 0;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) sum += s.bins[first - k];
+  uint32_t incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(~0u, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) s.warp[warp] = incl;
+  __syncthreads();
+  uint32_t w = lane < warp ? s.warp[lane] : 0u;
+  uint32_t above = __reduce_add_sync(~0u, w) + incl - sum;
+  if (above < *left && above + sum >= *left) {  // (one thread)
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const uint32_t here = s.bins[first - k];
+      if (above < *left && above + here >= *left) {
+        s.digit = first - k;
+        s.above = above;
+        break;
+      }
+      above += here;
+    }
+  }
+  __syncthreads();
+  *left -= s.above;
+  const uint32_t digit = s.digit;
+  for (int i = threadIdx.x; i < kBins; i += kSelectThreads) s.bins[i] = 0;
+  __syncthreads();
+  return digit;
+}
+
 __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __grid_constant__ KeepParams p,
                                                                        const __grid_constant__ KeepLayers layers, int cached) {
   extern __shared__ uint32_t s_keys[];
-  __shared__ uint32_t s_bins[kBins];
-  __shared__ uint32_t s_warp[kSelectWarps], s_more[kSelectWarps];
-  __shared__ uint32_t s_digit, s_above;
+  __shared__ SelectState s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   wait_for_previous();
   let_next_start();
@@ -235,87 +301,73 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
   int32_t* kept = p.kept + (int64_t)blockIdx.x * p.budget;
   const int count = n - p.recent, want = p.budget - p.recent;
   const bool in_shared = count <= cached;
-  if (in_shared)
-    for (int t = threadIdx.x; t < count; t += kSelectThreads) s_keys[t] = order_of(weights[t]);
+  for (int i = threadIdx.x; i < kBins; i += kSelectThreads) s.bins[i] = 0;
+  if (threadIdx.x < kSelectWarps) s.more[threadIdx.x] = s.equal[threadIdx.x] = 0;
+  if (threadIdx.x == 0) s.gathered = 0;
   __syncthreads();
   const auto key_of = [&](int t) { return in_shared ? s_keys[t] : order_of(weights[t]); };
-  uint32_t top = 0, left = want;  // the threshold's digits so far; how many are still to be taken among its equals
+  // runs of tokens for the warps of the last pass, whole 32s each
+  const int run = (count + kSelectThreads - 1) / kSelectThreads * 32;
+  uint32_t top = 0, left = want;  // the threshold; how many are still to be taken among its equals
   if (want > 0) {
-#pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
-      for (int i = threadIdx.x; i < kBins; i += kSelectThreads) s_bins[i] = 0;
-      __syncthreads();
-      for (int t0 = warp * 32; t0 < count; t0 += kSelectThreads) {
-        const int t = t0 + lane;
-        const uint32_t key = t < count ? key_of(t) : 0u;
-        const bool mine = t < count && (pass == 0 || key >> (shift + width) == top);
-        const uint32_t digit = key >> shift & ((1u << width) - 1);
-        const uint32_t who = __ballot_sync(~0u, mine);
-        if (!mine) continue;
-        int same;
-        __match_all_sync(who, digit, &same);  // (equal weights would meet in one counter)
-        if (!same) atomicAdd(&s_bins[digit], 1u);
-        else if (lane == __ffs(who) - 1) atomicAdd(&s_bins[digit], (uint32_t)__popc(who));
+    constexpr int kAtOnce = 8;
+    for (int t0 = 0; t0 < count; t0 += kSelectThreads * kAtOnce) {
+      float x[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int t = t0 + k * kSelectThreads + (int)threadIdx.x;
+        if (t < count) x[k] = weights[t];
       }
-      __syncthreads();
-      // this thread's 4 bins, the largest first
-      constexpr int kEach = kBins / kSelectThreads;
-      const int first = kBins - 1 - (int)threadIdx.x * kEach;
-      uint32_t sum = 0;
 #pragma unroll
-      for (int k = 0; k < kEach; ++k) sum += s_bins[first - k];
-      uint32_t incl = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(~0u, incl, o);
-        if (lane >= o) incl += y;
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int t = t0 + k * kSelectThreads + (int)threadIdx.x;
+        const uint32_t key = t < count ? order_of(x[k]) : 0u;
+        if (in_shared && t < count) s_keys[t] = key;
+        count_digit(s, key >> 21, t < count);
       }
-      if (lane == 31) s_warp[warp] = incl;
-      __syncthreads();
-      uint32_t above = incl - sum;
-      for (int w = 0; w < warp; ++w) above += s_warp[w];
-      if (above < left && above + sum >= left) {  // (one thread)
-#pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-          const uint32_t here = s_bins[first - k];
-          if (above < left && above + here >= left) {
-            s_digit = first - k;
-            s_above = above;
-            break;
-          }
-          above += here;
+    }
+    top = find_digit(s, &left);
+    // those with its first bits, gathered; those above counted, for each run
+    for (int t0 = 0; t0 < count; t0 += kSelectThreads) {
+      const int t = t0 + (int)threadIdx.x;
+      const uint32_t key = t < count ? key_of(t) : 0u;
+      const bool more = t < count && key >> 21 > top, same = t < count && key >> 21 == top;
+      const uint32_t is_more = __ballot_sync(~0u, more);
+      if (lane == 0 && is_more) atomicAdd(&s.more[(t0 + warp * 32) / run], (uint32_t)__popc(is_more));  // (a run is whole 32s)
+      if (same) {
+        const uint32_t at = atomicAdd(&s.gathered, 1u);
+        if (at < kGathered) {
+          s.key[at] = key;
+          s.token[at] = t;
         }
       }
-      __syncthreads();
-      top = top << width | s_digit;
-      left -= s_above;
-      __syncthreads();  // (the next pass clears the bins)
     }
-  }
-  // the kept ones in order: warps take runs, and count before they write
-  const int run = (count + kSelectThreads - 1) / kSelectThreads * 32;
-  const int from = min(warp * run, count), to = min(from + run, count);
-  uint32_t more = 0, equal = 0;
-  if (want > 0)
-    for (int t = from + lane; t < to; t += 32) {
-      const uint32_t key = key_of(t);
-      more += key > top;
-      equal += key == top;
+    __syncthreads();
+    const uint32_t gathered = s.gathered;
+    const bool few = gathered <= kGathered;
+    const int items = few ? (int)gathered : count;
+    const auto item_key = [&](int i) { return few ? s.key[i] : key_of(i); };
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+      const int shift = pass == 0 ? 10 : 0, width = pass == 0 ? 11 : 10;
+      for (int i0 = 0; i0 < items; i0 += kSelectThreads) {
+        const int i = i0 + (int)threadIdx.x;
+        const uint32_t key = i < items ? item_key(i) : 0u;
+        count_digit(s, key >> shift & ((1u << width) - 1), i < items && key >> (shift + width) == top);
+      }
+      top = top << width | find_digit(s, &left);
     }
-  more = __reduce_add_sync(~0u, more);
-  equal = __reduce_add_sync(~0u, equal);
-  if (lane == 0) {
-    s_more[warp] = more;
-    s_warp[warp] = equal;
-  }
-  __syncthreads();
-  more = equal = 0;
-  for (int w = 0; w < warp; ++w) {
-    more += s_more[w];
-    equal += s_warp[w];
-  }
-  if (want > 0)
+    for (int i = threadIdx.x; i < items; i += kSelectThreads) {
+      const uint32_t key = item_key(i);
+      if (key >> 21 != top >> 21) continue;
+      const int t = few ? s.token[i] : i;
+      if (key > top) atomicAdd(&s.more[t / run], 1u);
+      if (key == top) atomicAdd(&s.equal[t / run], 1u);
+    }
+    __syncthreads();
+    uint32_t more = __reduce_add_sync(~0u, lane < warp ? s.more[lane] : 0u);
+    uint32_t equal = __reduce_add_sync(~0u, lane < warp ? s.equal[lane] : 0u);
+    const int from = min(warp * run, count), to = min(from + run, count);
     for (int t0 = from; t0 < to; t0 += 32) {
       const int t = t0 + lane;
       const uint32_t key = t < to ? key_of(t) : 0u, below = (1u << lane) - 1u;
@@ -326,66 +378,84 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
       more += __popc(is_more);
       equal += __popc(is_equal);
     }
+  }
   for (int i = threadIdx.x; i < p.recent; i += kSelectThreads) kept[want + i] = count + i;
 }
 
-// A CTA moves the kept keys, values or weights of one kv head of one layer and
-// row, chunks of tokens in order: the next chunk is read before this one is
-// written, and the barrier between stands for its reads by all threads.
+// A CTA moves the kept keys or values of one kv head of one layer and row (some
+// of each token's pieces), or its weights, chunks of tokens in order. While a
+// chunk's data is on its way, the next one's places are looked up; it is read
+// before this one is written, and the barrier between stands for its reads by
+// all threads.
 constexpr int kMoveThreads = 256, kMoveAtOnce = 8;
 
-template <class U, class A>
-__device__ __forceinline__ void move_kept(const int32_t* kept, int n, int pieces, const A& address) {
+// tokens: of a chunk (threads / pieces * kMoveAtOnce); from, to: their places,
+// two chunks of each
+template <class U, class F>
+__device__ __forceinline__ void move_kept(int n, int pieces, int64_t* from, int64_t* to, uint8_t* base, const F& place) {
   const int over = kMoveThreads / pieces;  // tokens side by side
   const int mine = threadIdx.x / pieces, piece = threadIdx.x - mine * pieces;
   const int chunk = over * kMoveAtOnce;
   const bool busy = mine < over;
+  base += (int64_t)piece * sizeof(U);
   U x[kMoveAtOnce];
-  const auto read = [&](int j0) {
+  const auto look = [&](int j0) {
+    for (int i = threadIdx.x; i < chunk && j0 + i < n; i += kMoveThreads) place(j0 + i, &from[i], &to[i]);
+  };
+  look(0);
+  __syncthreads();
+  for (int j0 = 0; j0 < n; j0 += chunk) {
+    int64_t d[kMoveAtOnce];
 #pragma unroll
     for (int k = 0; k < kMoveAtOnce; ++k) {
-      const int j = j0 + k * over + mine;
-      if (busy && j < n) x[k] = *address(kept[j], piece);
+      const int i = k * over + mine;
+      if (busy && j0 + i < n) {
+        x[k] = *reinterpret_cast<const U*>(base + from[i]);
+        d[k] = to[i];
+      }
     }
-  };
-  read(0);
-  for (int j0 = 0; j0 < n; j0 += chunk) {
-    U y[kMoveAtOnce];
-#pragma unroll
-    for (int k = 0; k < kMoveAtOnce; ++k) y[k] = x[k];
-    read(j0 + chunk);
+    __syncthreads();  // (the places have been read; so has, after the next barrier, the data)
+    look(j0 + chunk);
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kMoveAtOnce; ++k) {
-      const int j = j0 + k * over + mine;
-      if (busy && j < n) *address(j, piece) = y[k];
-    }
+    for (int k = 0; k < kMoveAtOnce; ++k)
+      if (busy && j0 + k * over + mine < n) *reinterpret_cast<U*>(base + d[k]) = x[k];
   }
 }
 
 template <class U>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ KeepParams p, const __grid_constant__ KeepLayers layers) {
+  __shared__ int64_t s_from[kMoveThreads * kMoveAtOnce], s_to[kMoveThreads * kMoveAtOnce];
   wait_for_previous();
   let_next_start();
-  const int what = blockIdx.x % 3, list = blockIdx.x / 3;
+  // the slices of a list: keys, values, and at the end the weights
+  const int slices = 2 * p.slices + 1, what = blockIdx.x % slices, list = blockIdx.x / slices;
   const int head = list % p.heads, task = list / p.heads, layer = task % p.layers, row = task / p.layers;
   const int n = keep_length(p, row), now = p.lengths_out[row];
   if (n <= p.budget || now != p.budget) return;
   const int32_t* kept = p.kept + (int64_t)list * p.budget;
-  if (what == 2) {
+  if (what == slices - 1) {
     float* weights = layers.weights[layer] + row * layers.w_st[layer][0] + head * layers.w_st[layer][1];
-    move_kept<float>(kept, now, 1, [&](int t, int) { return weights + t; });
+    move_kept<float>(now, 1, s_from, s_to, reinterpret_cast<uint8_t*>(weights), [&](int j, int64_t* from, int64_t* to) {
+      *from = 4 * (int64_t)kept[j];
+      *to = 4 * (int64_t)j;
+    });
     __syncthreads();
     for (int t = now + threadIdx.x; t < n; t += kMoveThreads) weights[t] = 0.0f;
     if (layer == 0 && head == 0) release_pages(p, row, now, n);
     return;
   }
-  const KeepPool& pool = layers.pool[layer][what];
-  uint8_t* base = pool.ptr + head * pool.st[2];
+  const int each = (p.pieces + p.slices - 1) / p.slices, piece0 = what / 2 * each, pieces = min(each, p.pieces - piece0);
+  if (pieces <= 0) return;
+  const KeepPool& pool = layers.pool[layer][what & 1];
   const int32_t* table = p.tables + row * p.table_st;
-  move_kept<U>(kept, now, p.pieces, [&](int t, int piece) {
+  const auto slot = [&](int t) {
     const uint32_t column = fast_div32(p.page, (uint32_t)t);
-    return reinterpret_cast<U*>(base + table[column] * pool.st[0] + (int64_t)(t - column * p.page.d) * pool.st[1]) + piece;
+    return table[column] * pool.st[0] + (int64_t)(t - column * p.page.d) * pool.st[1];
+  };
+  move_kept<U>(now, pieces, s_from, s_to, pool.ptr + head * pool.st[2] + (int64_t)piece0 * sizeof(U), [&](int j, int64_t* from, int64_t* to) {
+    *from = slot(kept[j]);
+    *to = slot(j);
   });
 }
 
@@ -435,7 +505,9 @@ cudaError_t evict_launch(const KeepParams& p, const KeepLayers& layers, cudaStre
     if (e == cudaSuccess) e = launch_chained(evict_select_kernel, lists, kSelectThreads, (size_t)cached * 4, stream, p, layers, cached);
   }
   if (e != cudaSuccess) return e;
-  return by_unit(p.unit, [&](auto u) { return launch_chained(evict_move_kernel<decltype(u)>, 3 * lists, kMoveThreads, 0, stream, p, layers); });
+  return by_unit(p.unit, [&](auto u) {
+    return launch_chained(evict_move_kernel<decltype(u)>, (2 * p.slices + 1) * lists, kMoveThreads, 0, stream, p, layers);
+  });
 }
 
 }  // namespace cmdx
