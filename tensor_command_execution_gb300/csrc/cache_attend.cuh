@@ -345,27 +345,14 @@ __device__ __forceinline__ AttendSegment attend_team(const P& p, int tile, Atten
   return g;
 }
 
-// Ends a team's row: the warps' states (as in attend_finish) go to `part` of
-// each CTA, and the CTAs of the team write the result, a run of elements each.
-// Every thread of the team calls it.
-template <class T, int WARPS, int THREADS = WARPS * 32, class P>
-__device__ __forceinline__ void attend_finish_team(const P& p, const AttendSegment& g, const AttendHeads& h,
-                                                   const float* state, int warp_pitch, int pitch, float* part) {
+// Joins a team's row: every CTA's `part` holds its states of the heads, and the
+// CTAs of the team write the result, a run of elements each. Every thread of
+// the team calls it.
+template <class T, int THREADS, class P>
+__device__ __forceinline__ void attend_join_team(const P& p, const AttendSegment& g, const AttendHeads& h, float* part) {
   namespace cg = cooperative_groups;
   const cg::cluster_group team = cg::this_cluster();
   const int part_pitch = attend_pitch(p.dim), quads = part_pitch / 4 - 1;
-  __syncthreads();  // the warps' states are complete
-  for (int i = threadIdx.x; i < h.heads * quads; i += THREADS) {
-    const int q = i / quads, d = 4 * (i - q * quads);
-    float top, l;
-    const float4 o = attend_merged<WARPS>(state + q * pitch, warp_pitch, pitch, d, &top, &l);
-    float* x = part + q * part_pitch;
-    if (d == 0) {
-      x[part_pitch - 4] = top;
-      x[part_pitch - 3] = l;
-    }
-    *reinterpret_cast<float4*>(x + d) = o;
-  }
   team.sync();
   constexpr int kMost = 8;
   const int rank = blockIdx.x % p.team;
@@ -373,6 +360,7 @@ __device__ __forceinline__ void attend_finish_team(const P& p, const AttendSegme
     const int q = i / quads, d = 4 * (i - q * quads);
     float m[kMost], pl[kMost], top = -CUDART_INF_F, l = 0.0f;
     float4 po[kMost], o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    bool empty = false;
 #pragma unroll
     for (int k = 0; k < kMost; ++k) {
       m[k] = -CUDART_INF_F;
@@ -383,6 +371,7 @@ __device__ __forceinline__ void attend_finish_team(const P& p, const AttendSegme
         po[k] = *reinterpret_cast<const float4*>(x + d);
       }
       top = fmaxf(top, m[k]);
+      empty = empty || attend_void(p, m[k]);
     }
 #pragma unroll
     for (int k = 0; k < kMost; ++k)
@@ -391,9 +380,31 @@ __device__ __forceinline__ void attend_finish_team(const P& p, const AttendSegme
         l = fmaf(pl[k], c, l);
         add_scaled(o, po[k], c);
       }
+    if (empty) l = 0.0f;
     attend_write<T>(p, g.row, h.head0 + q, d, top, l, o);
   }
   team.sync();  // nobody leaves while its part is read
+}
+
+// Ends a team's row: the warps' states (as in attend_finish) go to `part` of
+// each CTA, and are joined. Every thread of the team calls it.
+template <class T, int WARPS>
+__device__ __forceinline__ void attend_finish_team(const AttendParams& p, const AttendSegment& g, const AttendHeads& h,
+                                                   const float* state, int warp_pitch, int pitch, float* part) {
+  const int part_pitch = attend_pitch(p.dim), quads = part_pitch / 4 - 1;
+  __syncthreads();  // the warps' states are complete
+  for (int i = threadIdx.x; i < h.heads * quads; i += WARPS * 32) {
+    const int q = i / quads, d = 4 * (i - q * quads);
+    float top, l;
+    const float4 o = attend_merged<WARPS>(state + q * pitch, warp_pitch, pitch, d, &top, &l);
+    float* x = part + q * part_pitch;
+    if (d == 0) {
+      x[part_pitch - 4] = top;
+      x[part_pitch - 3] = l;
+    }
+    *reinterpret_cast<float4*>(x + d) = o;
+  }
+  attend_join_team<T, WARPS * 32>(p, g, h, part);
 }
 
 // Joins the parts of query head q of a split row: WARPS warps take every

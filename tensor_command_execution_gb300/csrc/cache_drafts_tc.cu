@@ -158,9 +158,9 @@ struct Loader {
     ++issued;
   }
 
-  __device__ __forceinline__ void run(const AttendRows& rows, const AttendShare& share) {
+  __device__ __forceinline__ void run(const AttendRows& rows, const AttendShare& share, const AttendSegment& head) {
     int tile = 0;
-    for (AttendSegment g = attend_first(p, rows, share, kTile); g.tiles; g = attend_next(p, rows, share, g, kTile)) {
+    for (AttendSegment g = head; g.tiles; g = attend_next(p, rows, share, g, kTile)) {
       const int kv = attend_heads(p, g.group).kv, base = g.n - p.drafts;
       tiles.begin(g);
       for (int i = 0; i < g.tiles; ++i, ++tile) {
@@ -239,9 +239,9 @@ struct Loader {
     ++issued;
   }
 
-  __device__ __forceinline__ void run(const AttendRows& rows, const AttendShare& share) {
+  __device__ __forceinline__ void run(const AttendRows& rows, const AttendShare& share, const AttendSegment& head) {
     int tile = 0;
-    for (AttendSegment g = attend_first(p, rows, share, kTile); g.tiles; g = attend_next(p, rows, share, g, kTile)) {
+    for (AttendSegment g = head; g.tiles; g = attend_next(p, rows, share, g, kTile)) {
       const int kv = attend_heads(p, g.group).kv, base = g.n - p.drafts;
       DraftLook look[2];
       const auto look_up = [&](int i) {
@@ -295,8 +295,8 @@ struct Loader {
 // (What comes from shared memory passes through a shuffle, so that it is known
 // to be the same in all lanes.)
 template <class T, int DP, bool WIDE>
-__device__ __forceinline__ void issue(const DraftParams& p, State& s, const AttendRows& rows, const AttendShare& share, uint32_t queries,
-                                      uint32_t ring, uint32_t tmem) {
+__device__ __forceinline__ void issue(const DraftParams& p, State& s, const AttendRows& rows, const AttendShare& share,
+                                      const AttendSegment& head, uint32_t queries, uint32_t ring, uint32_t tmem) {
   using S = Shape<DP, WIDE>;
   const int steps = (p.dim + 15) / 16;
   const uint32_t qk = tcgen05_shape(kBf16<T>, kTile, false), pv = tcgen05_shape(kBf16<T>, steps * 16, true), one = elected();
@@ -307,7 +307,7 @@ __device__ __forceinline__ void issue(const DraftParams& p, State& s, const Atte
     wait(s.stop, smem_u32(&s.full[copy % S::kSlots]), copy / S::kSlots & 1);
     if (!CMDX_TMA) fence_async_smem();
   };
-  for (AttendSegment g = attend_first(p, rows, share, kTile); g.tiles; g = attend_next(p, rows, share, g, kTile)) {
+  for (AttendSegment g = head; g.tiles; g = attend_next(p, rows, share, g, kTile)) {
     wait(s.stop, smem_u32(&s.queries), segments & 1);
     ++segments;
     tcgen05_after_sync();
@@ -551,10 +551,17 @@ struct Softmax {
     }
   }
 
-  __device__ __forceinline__ void run(const AttendRows& rows, const AttendShare& share, unsigned char* queries) {
+  // team_part: where a team's part goes
+  __device__ __forceinline__ void run(const AttendRows& rows, const AttendShare& share, const AttendSegment& head, unsigned char* queries,
+                                      float* team_part) {
     using Both = SomeThreads<2 * kGroup, 1>;
     int tile = 0;
-    for (AttendSegment g = attend_first(p, rows, share, kTile); g.tiles; g = attend_next(p, rows, share, g, kTile)) {
+    if (p.team && head.tiles == 0) {
+      const AttendHeads heads = attend_heads(p, head.group);
+      const int pitch = attend_pitch(p.dim);
+      for (int i = threadIdx.x; i < heads.heads * pitch; i += 2 * kGroup) team_part[i] = i % pitch == pitch - 4 ? -CUDART_INF_F : 0.0f;
+    }
+    for (AttendSegment g = head; g.tiles; g = attend_next(p, rows, share, g, kTile)) {
       const AttendHeads heads = attend_heads(p, g.group);
       const int q0 = heads.head0 - heads.kv * p.group, base = g.n - p.drafts;
       // (where every draft sees all of the segment's tokens, the tree is not asked)
@@ -602,7 +609,7 @@ struct Softmax {
       tile += g.tiles;
 
       const int part_pitch = attend_pitch(p.dim);
-      float* part = attend_part(p, share, g, threadIdx.x == 0);
+      float* part = p.team ? team_part : attend_part(p, share, g, threadIdx.x == 0);
       const int h = heads.head0 + mine;
       float top = m, total = l, c[2] = {1.0f, 1.0f};
       bool has[2] = {any, any};
@@ -617,6 +624,8 @@ struct Softmax {
         c[0] = attend_weight(a.x, top);
         c[1] = attend_weight(b.x, top);
         total = a.y * c[0] + b.y * c[1];
+      } else if (p.team) {
+        Both::sync();  // (the other group's products have read what the part overwrites)
       }
       if (!live) {
         top = kPadding;
@@ -705,36 +714,44 @@ __global__ void __launch_bounds__(kThreads, 1) drafts_tc_kernel(const __grid_con
   wait_for_previous();
   let_next_start();
   AttendShare share;
-  const bool work = attend_begin<T>(p, rows, kTile, &share);  // (without work there is no segment below)
+  AttendSegment head;
+  if (p.team) {
+    head = attend_team(p, kTile, &share);
+  } else {
+    head.tiles = 0;  // (without work)
+    if (attend_begin<T>(p, rows, kTile, &share)) head = attend_first(p, rows, share, kTile);
+  }
   tcgen05_before_sync();
   __syncthreads();
   tcgen05_after_sync();
   const uint32_t tmem = *static_cast<volatile uint32_t*>(&s.tmem);
   const uint32_t queries = smem_u32(s_mem), ring = queries + S::kRing;
-  if (!work) {
-  } else if (warp < 2 * kGroup / 32) {
+  float* team_part = reinterpret_cast<float*>(s_mem);  // (the queries and the ring have been read by then)
+  if (warp < 2 * kGroup / 32) {
     Softmax<T, DP, WIDE> softmax(p, s, tree, tmem);
-    softmax.run(rows, share, s_mem);
+    softmax.run(rows, share, head, s_mem, team_part);
   } else if (warp == 2 * kGroup / 32) {
-    issue<T, DP, WIDE>(p, s, rows, share, queries, ring, __shfl_sync(~0u, tmem, 0));
+    issue<T, DP, WIDE>(p, s, rows, share, head, queries, ring, __shfl_sync(~0u, tmem, 0));
   } else {
     Loader<T, DP, WIDE> loader(p, s, ring);
-    loader.run(rows, share);
+    loader.run(rows, share, head);
   }
   tcgen05_before_sync();
   __syncthreads();
   tcgen05_after_sync();
   if (warp == 2 * kGroup / 32) tmem_free(tmem, 512);
   if (threadIdx.x == 0 && s.stop) report(p.status, CMD_CACHE_TIMEOUT);
+  if (p.team) attend_join_team<T, kThreads>(p, head, attend_heads(p, head.group), team_part);
 }
 
 template <class T, int DP, bool WIDE>
 cudaError_t launch(const TcParams& p, cudaStream_t stream) {
   static PerDevice ready;  // (static storage: zero before first use)
   static_assert(kSmem<DP, WIDE> <= 227 * 1024, "the CTA fits an SM");
+  static_assert(Shape<DP, WIDE>::kRows * attend_pitch(DP) * 4 <= Shape<DP, WIDE>::kRest, "a team's part fits the queries and the ring");
   const cudaError_t e = allow_smem(drafts_tc_kernel<T, DP, WIDE>, kSmem<DP, WIDE>, ready);
   if (e != cudaSuccess) return e;
-  return attend_launch<T>(drafts_tc_kernel<T, DP, WIDE>, p, 4, 152, kThreads, kSmem<DP, WIDE>, kTile, stream, false);
+  return attend_launch<T>(drafts_tc_kernel<T, DP, WIDE>, p, 4, 152, kThreads, kSmem<DP, WIDE>, kTile, stream);
 }
 template <class T>
 cudaError_t launch_type(const TcParams& p, cudaStream_t stream) {
