@@ -232,8 +232,9 @@ typedef struct cmd_drafts_args {
   int32_t* status;
 } cmd_drafts_args;
 
-/* Workspace bytes for a call with at most these rows, drafts and query heads, q_heads / kv_heads of them to a kv head,
- * and at most this dim; tokens: columns * page_size where weights are given, else 0. */
+/* Workspace bytes for a call of as many drafts with at most these rows and query heads, q_heads / kv_heads of them to a
+ * kv head, this dim and these tokens: columns * page_size where weights are given, else 0. (For one draft with weights
+ * that is up to a GiB, which its scores are kept in: 4 bytes for each query head, token and row.) */
 cmd_status cmd_drafts_workspace(int64_t rows, int32_t drafts, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t tokens,
                                 int64_t* bytes);
 cmd_status cmd_attention_drafts(const cmd_drafts_args* args, void* cuda_stream);

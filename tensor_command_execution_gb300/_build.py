@@ -60,7 +60,7 @@ CU_SOURCES = [("exec_tile2d.cu", _objs((2,), (0, 1))), ("exec_generic.cu", _objs
               ("static_scratch.cu", [{}]),
               ("cache_attend.cu", [{}]),
               ("cache_attend_mma.cu", [dict(CMDX_COPY=16), dict(CMDX_COPY=4)]),
-              ("cache_drafts_tc.cu", [dict(CMDX_TMA=1), dict(CMDX_TMA=0)]), ("cache_weigh_tc.cu", [{}]), ("cache_drafts_mma.cu", [dict(CMDX_COPY=16), dict(CMDX_COPY=4), dict(CMDX_COPY=0)]),
+              ("cache_drafts_tc.cu", [dict(CMDX_TMA=1), dict(CMDX_TMA=0)]), ("cache_weigh_tc.cu", [{}]), ("cache_weigh.cu", [{}]), ("cache_drafts_mma.cu", [dict(CMDX_COPY=16), dict(CMDX_COPY=4), dict(CMDX_COPY=0)]),
               ("cache_attend_f32.cu", [dict(CMDX_COPY=16), dict(CMDX_COPY=4)]),
               ("cache_drafts_f32.cu", [dict(CMDX_COPY=16), dict(CMDX_COPY=4)]), ("cache_rope.cu", [{}]), ("cache_pages.cu", [{}]),
               ("cache_keep.cu", [{}])]

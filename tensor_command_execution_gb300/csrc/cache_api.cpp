@@ -871,8 +871,18 @@ int64_t drafts_parts(int64_t drafts, int64_t q_heads, int64_t kv_heads, int64_t 
   const int64_t rows = std::max(std::min<int64_t>(group, cmdx::kDraftRows) * cmdx::kDraftCtas, std::min<int64_t>(group, cmdx::kDraftTcRows) * cmdx::kDraftTcCtas);
   return std::max(attention_workspace(q_heads, kv_heads, dim), kSplitBytes + 2 * rows * (round_up(dim, 4) + 4) * 4);
 }
-int64_t drafts_workspace(int64_t rows, int64_t drafts, int64_t q_heads, int64_t kv_heads, int64_t dim, bool weights) {
-  return drafts_parts(drafts, q_heads, kv_heads, dim) + (weights ? round_up(rows * drafts * q_heads * 8, 16) : 0);
+// What one new token's weights need beside the maxima and sums: its scores,
+// where they take no more than a GiB (else they are worked out again).
+constexpr int64_t kMostScores = 1 << 30;
+int64_t score_bytes(int64_t rows, int64_t q_heads, int64_t tokens) {
+  const __int128 n = (__int128)rows * q_heads * tokens * 4;
+  return (int64_t)std::min<__int128>(n, kMostScores);
+}
+int64_t drafts_workspace(int64_t rows, int64_t drafts, int64_t q_heads, int64_t kv_heads, int64_t dim, int64_t tokens) {
+  int64_t n = drafts_parts(drafts, q_heads, kv_heads, dim);
+  if (tokens > 0) n += round_up(rows * drafts * q_heads * 8, 16);
+  if (tokens > 0 && drafts == 1) n += round_up(score_bytes(rows, q_heads, tokens), 16);
+  return n;
 }
 
 // (TMA copies are issued on device memory only)
@@ -902,7 +912,7 @@ extern "C" cmd_status cmd_drafts_workspace(int64_t rows, int32_t drafts, int32_t
     check_heads(q_heads);
     NEED((int64_t)drafts * q_heads <= kDraftHeads, CMD_ERR_LIMIT, "drafts times q_heads pass 2^20");
     NEED(dim >= 0 && dim <= CMD_CACHE_MAX_DIM, CMD_ERR_LIMIT, "a head dim above 256");
-    *bytes = drafts_workspace(rows, drafts, q_heads, kv_heads, dim, tokens > 0);
+    *bytes = drafts_workspace(rows, drafts, q_heads, kv_heads, dim, tokens);
     return CMD_OK;
   });
 }
@@ -960,7 +970,7 @@ extern "C" cmd_status cmd_attention_drafts(const cmd_drafts_args* args, void* cu
     NEED(a.window >= 0, CMD_ERR_ARG, "window must be positive, or 0 for none");
     NEED(a.reserved == 0, CMD_ERR_ARG, "reserved must be 0");
     if (rows == 0 || heads == 0) return CMD_OK;
-    check_workspace(a.workspace, a.workspace_bytes, drafts_workspace(rows, drafts, heads, kv, dim, has_weights));
+    check_workspace(a.workspace, a.workspace_bytes, drafts_workspace(rows, drafts, heads, kv, dim, has_weights ? tokens : 0));
     cmdx::DraftParams p;
     std::memset(&p, 0, sizeof p);
     const int32_t per = (int32_t)(heads / kv);
@@ -994,7 +1004,10 @@ extern "C" cmd_status cmd_attention_drafts(const cmd_drafts_args* args, void* cu
     const auto pieces = [&](int n) { return dim * es % n == 0 && vector_rows(a.k_cache, n) && vector_rows(a.v_cache, n); };
     const int copy = pieces(16) ? 16 : pieces(4) ? 4 : 0;
     const bool one = drafts == 1 && !has_parents, tc = copy == 16 && es == 2 && dim <= 128;
-    const bool tma = tc && (!one || has_weights) && cmdx::drafts_tma_fits(a.k_cache.sizes[1], a.k_cache.sizes, a.k_cache.strides, a.v_cache.strides) &&
+    const bool kept = one && has_weights && tokens > 0 && copy == 16 && es == 2 && (__int128)rows * heads * tokens * 4 <= kMostScores;
+    float* scores = kept ? reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(stats) + round_up(rows * heads * 8, 16)) : nullptr;
+    p.scores_tokens = tokens;
+    const bool tma = tc && !(one && (kept || !has_weights)) && cmdx::drafts_tma_fits(a.k_cache.sizes[1], a.k_cache.sizes, a.k_cache.strides, a.v_cache.strides) &&
                      in_device_memory(a.k_cache.ptr) && in_device_memory(a.v_cache.ptr);
     if (one) {
       attend_blocks(p, es, copy);
@@ -1019,6 +1032,7 @@ extern "C" cmd_status cmd_attention_drafts(const cmd_drafts_args* args, void* cu
       p.parents = has_parents ? static_cast<const int32_t*>(a.parents.ptr) + r * a.parents.strides[0] : nullptr;
       p.weights = has_weights ? static_cast<float*>(a.weights.ptr) + r * a.weights.strides[0] : nullptr;
       p.stats = stats ? stats + r * drafts * heads : nullptr;
+      p.scores = scores ? scores + r * heads * tokens : nullptr;
       const cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
       cudaError_t e = one          ? attend_one(a.q.dtype, copy, p, stream)
                       : es == 4    ? (copy == 16 ? cmdx::drafts_f32_launch16 : cmdx::drafts_f32_launch4)(p, stream)
@@ -1027,7 +1041,8 @@ extern "C" cmd_status cmd_attention_drafts(const cmd_drafts_args* args, void* cu
                       : copy == 4  ? cmdx::drafts_mma_launch4(a.q.dtype, p, stream)
                                    : cmdx::drafts_mma_launch0(a.q.dtype, p, stream);
       if (e == cudaSuccess && has_weights)
-        e = es == 4      ? (copy == 16 ? cmdx::weigh_f32_launch16 : cmdx::weigh_f32_launch4)(p, stream)
+        e = kept         ? cmdx::weigh_scores_launch(p, stream)
+            : es == 4    ? (copy == 16 ? cmdx::weigh_f32_launch16 : cmdx::weigh_f32_launch4)(p, stream)
             : tma        ? cmdx::weigh_tma_launch(a.q.dtype, p, stream)
             : copy == 16 ? cmdx::weigh_mma_launch16(a.q.dtype, p, stream)
             : copy == 4  ? cmdx::weigh_mma_launch4(a.q.dtype, p, stream)

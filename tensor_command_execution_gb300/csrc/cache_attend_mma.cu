@@ -58,7 +58,9 @@ struct Shape {
   static constexpr int kSmem = kWarps * Ring::kBytes + (int)sizeof(AttendRows);
 };
 
-template <class T, int DP, int NT>
+// KEEP: the scores are written to p.scores as well, for the weights that the
+// tokens get.
+template <class T, int DP, int NT, bool KEEP>
 __global__ void __launch_bounds__(kWarps * 32, Shape<T, DP, NT>::kCtas)
     attend_mma_kernel(const __grid_constant__ AttendParams p) {
   using S = Shape<T, DP, NT>;
@@ -147,6 +149,13 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<T, DP, NT>::kCtas)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           x[e] = (e < 2 ? in0 : in1) ? attend_score(p, s[j][0][e] + s[j][1][e]) : -CUDART_INF_F;
+        if constexpr (KEEP) {
+          const int t = (g.tile0 + i) * Ring::kTile + warp * kTokens + gr, h = j * 8 + tc;
+          float* to = p.scores + (((int64_t)g.row * p.kv_heads + heads.kv) * p.scores_tokens + t) * p.group + heads.head0 - heads.kv * p.group + h;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if ((e < 2 ? in0 : in1) && h + (e & 1) < heads.heads) to[(e < 2 ? 0 : 8 * p.group) + (e & 1)] = x[e];
+        }
         float up[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
 #pragma unroll
         for (int b = 4; b < 32; b <<= 1) {
@@ -232,18 +241,25 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<T, DP, NT>::kCtas)
   }
 }
 
-template <class T, int DP, int NT>
-cudaError_t launch(const AttendParams& p, cudaStream_t stream) {
+template <class T, int DP, int NT, bool KEEP>
+cudaError_t launch_kept(const AttendParams& p, cudaStream_t stream) {
   using S = Shape<T, DP, NT>;
   static_assert(NT * 8 * attend_pitch(DP) * 4 <= S::Ring::kStage, "a warp's state fits a stage");
   static PerDevice ready;  // (static storage: zero before first use)
-  const cudaError_t e = allow_smem(attend_mma_kernel<T, DP, NT>, S::kSmem, ready);
+  const cudaError_t e = allow_smem(attend_mma_kernel<T, DP, NT, KEEP>, S::kSmem, ready);
   if (e != cudaSuccess) return e;
   // The beginning of a row as two tiles of 64 tokens. Measured on 64 rows of 0
   // to 8192 tokens (their logarithms even; bf16, dim 128): counted as 0, 66.6
   // us; 1, 49.9; 2, 48.9; 3, 48.6; with 16 query heads to a kv head 120, 74,
   // 58 and 59. On 64 rows of 4096 tokens it costs nothing beyond the noise.
-  return attend_launch<T>(attend_mma_kernel<T, DP, NT>, p, 2, 152 * S::kCtas, kWarps * 32, S::kSmem, S::Ring::kTile, stream);
+  return attend_launch<T>(attend_mma_kernel<T, DP, NT, KEEP>, p, 2, 152 * S::kCtas, kWarps * 32, S::kSmem, S::Ring::kTile, stream);
+}
+
+template <class T, int DP, int NT>
+cudaError_t launch(const AttendParams& p, cudaStream_t stream) {
+  if constexpr (CMDX_COPY == 16)
+    if (p.scores) return launch_kept<T, DP, NT, true>(p, stream);
+  return launch_kept<T, DP, NT, false>(p, stream);
 }
 
 template <class T>

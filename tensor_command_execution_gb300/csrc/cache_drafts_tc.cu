@@ -564,14 +564,14 @@ struct Softmax {
     for (AttendSegment g = head; g.tiles; g = attend_next(p, rows, share, g, kTile)) {
       const AttendHeads heads = attend_heads(p, g.group);
       const int q0 = heads.head0 - heads.kv * p.group, base = g.n - p.drafts;
+      Both::sync();  // (the queries before these, and what they gave, are no longer read)
+      load_queries(queries, g.row, heads.kv, q0, heads.heads);
+      fence_async_smem();
+      mbar_arrive(smem_u32(&s.queries));
       // (where every draft sees all of the segment's tokens, the tree is not asked)
       const int t_begin = g.tile0 * kTile, t_end = t_begin + g.tiles * kTile;
       const bool planted = !draft_all_seen(p, t_begin, t_end, base);
       if (planted) draft_tree<2 * kGroup, Both>(p, tree, g.row, base);
-      else Both::sync();
-      load_queries(queries, g.row, heads.kv, q0, heads.heads);
-      fence_async_smem();
-      mbar_arrive(smem_u32(&s.queries));
 
       const int mine = row + (WIDE ? w * kGroup : 0);
       const int draft = (int)fast_div32(p.per, (uint32_t)(q0 + min(mine, heads.heads - 1)));

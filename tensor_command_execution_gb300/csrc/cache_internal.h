@@ -104,6 +104,8 @@ struct AttendParams {
   uint8_t split_by_row;
   int32_t* status;
   float2* stats;       // optional: a row's maximum and sum for each head, [rows][kv_heads * group]
+  float* scores;       // optional (16-bit types, copies of 16 bytes): every token's, [rows][kv_heads][scores_tokens][group]
+  int64_t scores_tokens;
   uint8_t q_pairs;     // q rows may be read two 16-bit elements at a time
 };
 
@@ -155,6 +157,7 @@ cudaError_t drafts_f32_launch4(const DraftParams& p, cudaStream_t stream);
 cudaError_t weigh_mma_launch16(int dtype, const DraftParams& p, cudaStream_t stream);
 cudaError_t weigh_mma_launch4(int dtype, const DraftParams& p, cudaStream_t stream);
 cudaError_t weigh_mma_launch0(int dtype, const DraftParams& p, cudaStream_t stream);
+cudaError_t weigh_scores_launch(const DraftParams& p, cudaStream_t stream);  // (from p.scores)
 cudaError_t weigh_tma_launch(int dtype, const DraftParams& p, cudaStream_t stream);  // (where drafts_tma_launch may be)
 cudaError_t weigh_f32_launch16(const DraftParams& p, cudaStream_t stream);
 cudaError_t weigh_f32_launch4(const DraftParams& p, cudaStream_t stream);

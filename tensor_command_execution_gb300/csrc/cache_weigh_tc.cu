@@ -173,8 +173,7 @@ __device__ __forceinline__ void sums(const Params& p, State& s, DraftTree& tree,
   for (AttendSegment g = attend_first(p, rows, share, kTile); g.tiles; g = attend_next(p, rows, share, g, kTile)) {
     const int kv = g.group, base = g.n - p.drafts;
     const bool planted = !draft_all_seen(p, g.tile0 * kTile, (g.tile0 + g.tiles) * kTile, base);
-    if (planted) draft_tree<2 * kGroup, Both>(p, tree, g.row, base);
-    else Both::sync();
+    Both::sync();  // (the queries before these are no longer read)
     // rows, and what the attention has left of them; padding (a sum of zero) is zeros, whatever it holds
     const float2* stats = p.stats + ((int64_t)g.row * p.kv_heads + kv) * p.group + p.row0;
     for (int q = threadIdx.x; q < columns; q += 2 * kGroup) {
@@ -215,7 +214,8 @@ __device__ __forceinline__ void sums(const Params& p, State& s, DraftTree& tree,
     }
     fence_async_smem();
     mbar_arrive(smem_u32(&s.queries));
-    Both::sync();  // (the statistics are complete)
+    if (planted) draft_tree<2 * kGroup, Both>(p, tree, g.row, base);
+    else Both::sync();  // (the statistics are complete)
     float* weights = p.weights + g.row * p.w_st[0] + kv * p.w_st[1];
     for (int i = 0; i < g.tiles; ++i, ++items) {
       if ((items & 1) != w) continue;

@@ -208,12 +208,13 @@ def test_workspaces():
         C.cmd_evict_workspace(-1, 1, 1, 1)
     with pytest.raises(T.CmdError, match="2.31"):
         C.cmd_evict_workspace(1 << 20, 32, 64, 1)
-    # any call with at most as many rows, drafts and heads, query heads to a kv head, and at most the dim
+    # any call of as many drafts with at most as many rows and heads, query heads to a kv head, tokens, and at most the dim
     for rows, d, q, kv, dim, t in ((4, 24, 32, 8, 128, 900), (1, 256, 8, 8, 64, 0), (700, 1, 16, 1, 256, 64)):
         mine = C.cmd_drafts_workspace(rows, d, q, kv, dim, t)
-        for rows2, d2, q2, kv2, dim2 in ((1, 24, 32, 8, 128), (1, 1, 8, 8, 64), (4, 24, 8, 2, 20), (700, 1, 4, 1, 1)):
-            if rows2 <= rows and d2 <= d and q2 <= q and q2 * kv <= q * kv2 and dim2 <= dim:
-                assert C.cmd_drafts_workspace(rows2, d2, q2, kv2, dim2, t) <= mine
+        for rows2, q2, kv2, dim2, t2 in ((1, 32, 8, 128, 900), (1, 8, 8, 64, 1), (4, 8, 2, 20, 0), (700, 4, 1, 1, 64), (2, 16, 4, 64, 2)):
+            if rows2 <= rows and q2 <= q and q2 * kv <= q * kv2 and dim2 <= dim and t2 <= t:
+                assert C.cmd_drafts_workspace(rows2, d, q2, kv2, dim2, t2) <= mine
+    assert C.cmd_drafts_workspace(512, 1, 64, 8, 128, 1 << 30) < C.cmd_drafts_workspace(512, 1, 64, 8, 128, 0) + (1 << 30) + (1 << 20)
 
 
 def test_the_module_refuses():
