@@ -8,10 +8,10 @@
 // tensor units work on one group's products while the other's exponentials are
 // worked out: with 256 rows a group has its own rows (and a key or value is read
 // once for both), with 128 its own tiles, and the two halves are joined at the
-// end of a segment. One warp issues the products, another copies keys and values
+// end of a segment. One warp issues the products, others copy keys and values
 // into a ring in the layout that the products read: TMA boxes of the tokens that
-// a page and a tile share, where those are 8 or a multiple, else three warps
-// with 16-byte asynchronous copies.
+// a page and a tile share, where those are 8 or a multiple (a warp for keys, one
+// for values), else three warps with 16-byte asynchronous copies.
 //
 // A weight is held as the sum of two 16-bit numbers, as in cache_attend_mma.cu:
 // P takes exactly the columns of S that it came from. O is rescaled only when a
@@ -32,7 +32,7 @@ namespace cmdx {
 namespace {
 
 constexpr int kGroup = 128;                   // threads of a softmax group, and query rows
-constexpr int kLoaders = CMDX_TMA ? 32 : 96;
+constexpr int kLoaders = CMDX_TMA ? 64 : 96;
 constexpr int kThreads = 2 * kGroup + 32 + kLoaders;
 constexpr int kTile = 128;                    // tokens
 
@@ -114,15 +114,23 @@ struct Loader {
   State& s;
   const uint32_t ring;
   TmaTiles tiles;
-  uint32_t issued = 0, cleared = 0;  // keys and values in turn; tiles that were
+  const bool values;             // of the two warps one copies keys, one values: each slot is one warp's, which waits for all
+                                 // of its turns (a parity says nothing about a barrier that is two turns away)
+  uint32_t copies, cleared = 0;  // keys and values in turn; tiles that were
 
-  __device__ __forceinline__ Loader(const TcParams& p_, State& s_, uint32_t ring_) : p(p_), s(s_), ring(ring_), tiles(p_) {}
+  __device__ __forceinline__ Loader(const TcParams& p_, State& s_, uint32_t ring_)
+      : p(p_), s(s_), ring(ring_), tiles(p_), values(threadIdx.x >= 2 * kGroup + 64), copies(values) {
+    static_assert(S::kSlots % 2 == 0, "a slot is of keys or of values");
+  }
 
   // Rows of no token become zeros, and so do values that are not finite,
   // whatever their weight: the softmax group is told, and adds them where they
   // are seen.
-  __device__ __forceinline__ void clear(uint32_t slot, const uint32_t* here) {
+  __device__ __forceinline__ void clear(uint32_t slot) {
     constexpr int kAtOnce = 8;
+    uint32_t here[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) here[k] = __shfl_sync(~0u, tiles.here, k);
     const int lane = tiles.lane, c = lane % kPieces;
     if (c < (p.dim + 15) / 16 * 2) {
       const uint32_t at = slot + c / 8 * kTile * 128;
@@ -135,10 +143,11 @@ struct Loader {
         for (int k = 0; k < kAtOnce; ++k) {
           const int r = r0 + k * kOver;
           const uint4 bad = make_uint4(not_finite<T>(x[k].x), not_finite<T>(x[k].y), not_finite<T>(x[k].z), not_finite<T>(x[k].w));
-          const bool in = here[r >> 5] >> (r & 31) & 1;
+          const uint32_t word = r < 64 ? (r < 32 ? here[0] : here[1]) : (r < 96 ? here[2] : here[3]);
+          const bool in = word >> (r & 31) & 1;
           if (in && (bad.x | bad.y | bad.z | bad.w) == 0) continue;
           sts128(at + swizzled(r, c % 8), in ? make_uint4(x[k].x & ~bad.x, x[k].y & ~bad.y, x[k].z & ~bad.z, x[k].w & ~bad.w) : make_uint4(0, 0, 0, 0));
-          if (in) *static_cast<volatile uint32_t*>(&s.bad[issued / 2 % kHereTiles]) = issued / 2 + 1;
+          if (in) *static_cast<volatile uint32_t*>(&s.bad[copies / 2 % kHereTiles]) = copies / 2 + 1;
         }
       }
     }
@@ -146,31 +155,27 @@ struct Loader {
     __syncwarp();
   }
 
-  __device__ __forceinline__ void copy(const CUtensorMap& map, int kv, const uint32_t* mask) {
-    const uint32_t at = issued % S::kSlots, slot = ring + at * S::kSlot, full = smem_u32(&s.full[at]);
-    wait(s.stop, smem_u32(&s.empty[at]), (issued / S::kSlots + 1) & 1);
-    tiles.copy(map, kv, slot, mask ? smem_u32(&s.landed) : full);
-    if (mask) {
-      wait(s.stop, smem_u32(&s.landed), cleared++ & 1);
-      clear(slot, mask);
-      if (tiles.lane == 0) mbar_arrive(full);
-    }
-    ++issued;
-  }
-
   __device__ __forceinline__ void run(const AttendRows& rows, const AttendShare& share, const AttendSegment& head) {
-    int tile = 0;
     for (AttendSegment g = head; g.tiles; g = attend_next(p, rows, share, g, kTile)) {
       const int kv = attend_heads(p, g.group).kv, base = g.n - p.drafts;
       tiles.begin(g);
-      for (int i = 0; i < g.tiles; ++i, ++tile) {
+      for (int i = 0; i < g.tiles; ++i, copies += 2) {
         tiles.look<true>(i);
-        const int t0 = (g.tile0 + i) * kTile;
-        uint32_t* here = s.here[tile % kHereTiles];
-        if (tiles.lane < 4) here[tiles.lane] = tiles.here;
-        const bool all = __all_sync(~0u, tiles.lane >= 4 || tiles.here == ~0u) && draft_all_seen(p, t0, t0 + kTile, base);
-        copy(p.maps[0], kv, nullptr);
-        copy(p.maps[1], kv, all ? nullptr : here);
+        const uint32_t at = copies % S::kSlots, slot = ring + at * S::kSlot, full = smem_u32(&s.full[at]);
+        wait(s.stop, smem_u32(&s.empty[at]), (copies / S::kSlots + 1) & 1);
+        if (!values) {
+          if (tiles.lane < 4) s.here[copies / 2 % kHereTiles][tiles.lane] = tiles.here;
+          __syncwarp();
+          tiles.copy(p.maps[0], kv, slot, full);
+          continue;
+        }
+        const bool all = __all_sync(~0u, tiles.lane >= 4 || tiles.here == ~0u) && draft_all_seen(p, tiles.t0, tiles.t0 + kTile, base);
+        tiles.copy(p.maps[1], kv, slot, all ? full : smem_u32(&s.landed));
+        if (!all) {
+          wait(s.stop, smem_u32(&s.landed), cleared++ & 1);
+          clear(slot);
+          if (tiles.one) mbar_arrive(full);
+        }
       }
     }
   }

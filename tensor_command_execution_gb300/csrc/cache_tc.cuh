@@ -61,67 +61,71 @@ __device__ __forceinline__ void wait(uint32_t& stop_word, uint32_t bar, uint32_t
   }
 }
 
-// What a warp needs to copy the tiles of a segment by TMA: a lane to a box of
-// tokens (and a slab of 64 dims of it). Table entries are read for as many
-// tiles at once as the lanes hold, and so many again ahead of the copies.
+// What a warp needs to copy the tiles of a segment by TMA. Table entries are
+// read for as many tiles at once as there are lanes (one to each box of tokens),
+// and so many again ahead of the copies. (A copy takes 80 cycles to issue,
+// whether by a lane each or by one lane in a loop.)
 struct TmaTiles {
   const TcParams& p;
-  const int lane, boxes, box, slab, each;  // each: tiles to a batch of entries
+  const int lane, boxes, each, slabs;  // each: tiles to a batch of entries
+  const uint32_t one;
   AttendSegment g;
-  int page = 0, next = 0;  // of this lane's box in its tile of the batch, and of the next batch
-  // the tile at hand: this lane's box is there, its page and first slot; which
-  // boxes are; which of tokens 32 * lane .. + 31 are (lanes 0 to 3)
-  bool take = false;
-  int from = 0, first = 0;
+  int page = 0, next = 0;              // of this lane's tile of the batch and box, and of the next batch
+  uint32_t good = 0;                   // which lanes' boxes are there
+  int batch = 0, sub = 0;
+  // the tile at hand: its first token, which boxes are there, which of tokens
+  // 32 * lane .. + 31 are (lanes 0 to 3)
+  int t0 = 0;
   uint32_t taken = 0, here = 0;
 
   __device__ __forceinline__ TmaTiles(const TcParams& p_)
-      : p(p_), lane(threadIdx.x % 32), boxes(kTcTile / p_.box), box(lane % boxes), slab(lane / boxes), each(32 / boxes) {}
+      : p(p_), lane(threadIdx.x % 32), boxes(kTcTile / p_.box), each(32 / boxes), slabs((p_.dim + 63) / 64), one(elected()) {}
 
-  __device__ __forceinline__ bool inside(int t) const { return t < g.n && t + p.box > g.lo; }
-  __device__ __forceinline__ int entry(int batch) const {
-    const int i = batch * each + slab, t = (g.tile0 + i) * kTcTile + box * p.box;
-    if (i >= g.tiles || !inside(t)) return 0;
-    return p.tables[g.row * p.table_st[0] + fast_div32(p.page, (uint32_t)t) * p.table_st[1]];
+  // this lane's entry of a batch; -1: it has none
+  __device__ __forceinline__ int entry(int b) const {
+    const int i = b * each + lane / boxes, t = (g.tile0 + i) * kTcTile + lane % boxes * p.box;
+    if (i >= g.tiles || t >= g.n || t + p.box <= g.lo) return -1;
+    return max(p.tables[g.row * p.table_st[0] + fast_div32(p.page, (uint32_t)t) * p.table_st[1]], -2);
   }
   __device__ __forceinline__ void begin(const AttendSegment& segment) {
     g = segment;
+    batch = -1;
     next = entry(0);
   }
-  // Tile i of the segment (in order). REPORT: of entries that name no page.
+  // Tile i of the segment (in order). REPORT: entries that name no page.
   template <bool REPORT>
   __device__ __forceinline__ void look(int i) {
-    const int sub = i % each;
-    if (sub == 0) {
+    sub = i & (each - 1);
+    if (i - sub != batch * each) {
       page = next;
-      next = entry(i / each + 1);
+      next = entry(++batch + 1);
+      if (REPORT && (page < -1 || page >= p.n_pages)) report(p.status, CMD_CACHE_BAD_PAGE);
+      good = __ballot_sync(~0u, page >= 0 && page < p.n_pages);
     }
-    const int t0 = (g.tile0 + i) * kTcTile, t = t0 + box * p.box;
-    from = __shfl_sync(~0u, page, sub * boxes + box);
-    const uint32_t column = fast_div32(p.page, (uint32_t)t);
-    first = t - (int)(column * p.page.d);
-    take = inside(t);
-    if (take && (from < 0 || from >= p.n_pages)) {
-      if (REPORT) report(p.status, CMD_CACHE_BAD_PAGE);
-      take = false;
-    }
-    taken = __ballot_sync(~0u, take && slab == 0);
-    const int mine = t0 + 32 * lane, begin = max(g.lo - mine, 0), end = min(g.n - mine, 32);
-    here = begin < end ? (~0u >> (32 - (end - begin))) << begin : 0u;
-    if (taken != (boxes == 32 ? ~0u : (1u << boxes) - 1u))
+    t0 = (g.tile0 + i) * kTcTile;
+    const uint32_t all = (1u << boxes) - 1u;  // (at most 16)
+    taken = good >> (sub * boxes) & all;
+    here = ~0u;
+    if (taken != all || t0 < g.lo || t0 + kTcTile > g.n) {
+      const int mine = t0 + 32 * lane, begin = max(g.lo - mine, 0), end = min(g.n - mine, 32);
+      here = begin < end ? (~0u >> (32 - (end - begin))) << begin : 0u;
       for (int k = 0; k < 32; k += min(p.box, 32))
         if (lane < 4 && !(taken >> ((32 * lane + k) / p.box) & 1)) here &= ~((p.box < 32 ? (1u << p.box) - 1u : ~0u) << k);
+    }
   }
-  // Copies one kv head's tile into a slot, completing on the mbarrier `bar`.
+  // Copies one kv head's tile into a slot, completing on the mbarrier `bar`: a
+  // lane to each box and slab of 64 dims.
   __device__ __forceinline__ void copy(const CUtensorMap& map, int kv, uint32_t slot, uint32_t bar) const {
-    const int slabs = (p.dim + 63) / 64;
-    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(__popc(taken) * slabs * p.box * 128));
+    if (one) mbar_arrive_expect_tx(bar, (uint32_t)(__popc(taken) * slabs * p.box * 128));
     __syncwarp();
-    if (take && slab < slabs)
+    const int box = lane & (boxes - 1), slab = lane / boxes, t = t0 + box * p.box;
+    const int from = __shfl_sync(~0u, page, sub * boxes + box), first = t - (int)(fast_div32(p.page, (uint32_t)t) * p.page.d);
+    if (slab < slabs && (taken >> box & 1))
       asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
                        slot + slab * kTcTile * 128 + box * p.box * 128),
                    "l"(&map), "r"(64 * slab), "r"(first), "r"(kv), "r"(from), "r"(bar)
                    : "memory");
+    __syncwarp();
   }
 };
 
