@@ -241,11 +241,11 @@ struct SelectState {
 // Counts a warp's keys' digits (those with `mine`).
 __device__ __forceinline__ void count_digit(SelectState& s, uint32_t digit, bool mine) {
   const uint32_t who = __ballot_sync(~0u, mine);
-  if (!mine) return;
-  int same;
-  __match_all_sync(who, digit, &same);  // (equal weights would meet in one counter)
-  if (!same) atomicAdd(&s.bins[digit], 1u);
-  else if ((threadIdx.x & 31) == __ffs(who) - 1) atomicAdd(&s.bins[digit], (uint32_t)__popc(who));
+  const int first = __ffs(who) - 1;
+  // (equal weights would meet in one counter)
+  const uint32_t lead = __shfl_sync(~0u, digit, first & 31);
+  const bool same = __all_sync(~0u, !mine || digit == lead);
+  if (mine && (!same || (int)(threadIdx.x & 31) == first)) atomicAdd(&s.bins[digit], same ? (uint32_t)__popc(who) : 1u);
 }
 // The digit at which the counts from the largest down reach `left`; *left then
 // counts on among the keys of that digit. Every thread calls it.
@@ -328,17 +328,25 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
     }
     top = find_digit(s, &left);
     // those with its first bits, gathered; those above counted, for each run
-    for (int t0 = 0; t0 < count; t0 += kSelectThreads) {
-      const int t = t0 + (int)threadIdx.x;
-      const uint32_t key = t < count ? key_of(t) : 0u;
-      const bool more = t < count && key >> 21 > top, same = t < count && key >> 21 == top;
-      const uint32_t is_more = __ballot_sync(~0u, more);
-      if (lane == 0 && is_more) atomicAdd(&s.more[(t0 + warp * 32) / run], (uint32_t)__popc(is_more));  // (a run is whole 32s)
-      if (same) {
-        const uint32_t at = atomicAdd(&s.gathered, 1u);
-        if (at < kGathered) {
-          s.key[at] = key;
-          s.token[at] = t;
+    for (int t0 = 0; t0 < count; t0 += kSelectThreads * kAtOnce) {
+      uint32_t key[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int t = t0 + k * kSelectThreads + (int)threadIdx.x;
+        key[k] = t < count ? key_of(t) : 0u;
+      }
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int t = t0 + k * kSelectThreads + (int)threadIdx.x;
+        const bool more = t < count && key[k] >> 21 > top, same = t < count && key[k] >> 21 == top;
+        const uint32_t is_more = __ballot_sync(~0u, more);
+        if (lane == 0 && is_more) atomicAdd(&s.more[t / run], (uint32_t)__popc(is_more));  // (a run is whole 32s)
+        if (same) {
+          const uint32_t at = atomicAdd(&s.gathered, 1u);
+          if (at < kGathered) {
+            s.key[at] = key[k];
+            s.token[at] = t;
+          }
         }
       }
     }
@@ -368,15 +376,24 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
     uint32_t more = __reduce_add_sync(~0u, lane < warp ? s.more[lane] : 0u);
     uint32_t equal = __reduce_add_sync(~0u, lane < warp ? s.equal[lane] : 0u);
     const int from = min(warp * run, count), to = min(from + run, count);
-    for (int t0 = from; t0 < to; t0 += 32) {
-      const int t = t0 + lane;
-      const uint32_t key = t < to ? key_of(t) : 0u, below = (1u << lane) - 1u;
-      const uint32_t is_more = __ballot_sync(~0u, t < to && key > top), is_equal = __ballot_sync(~0u, t < to && key == top);
-      const uint32_t m = more + __popc(is_more & below), e = equal + __popc(is_equal & below);
-      if (is_more >> lane & 1) kept[m + min(e, left)] = t;
-      else if ((is_equal >> lane & 1) && e < left) kept[m + e] = t;
-      more += __popc(is_more);
-      equal += __popc(is_equal);
+    const uint32_t below = (1u << lane) - 1u;
+    for (int t0 = from; t0 < to; t0 += 32 * kAtOnce) {
+      uint32_t key[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int t = t0 + 32 * k + lane;
+        key[k] = t < to ? key_of(t) : 0u;
+      }
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int t = t0 + 32 * k + lane;
+        const uint32_t is_more = __ballot_sync(~0u, t < to && key[k] > top), is_equal = __ballot_sync(~0u, t < to && key[k] == top);
+        const uint32_t m = more + __popc(is_more & below), e = equal + __popc(is_equal & below);
+        if (is_more >> lane & 1) kept[m + min(e, left)] = t;
+        else if ((is_equal >> lane & 1) && e < left) kept[m + e] = t;
+        more += __popc(is_more);
+        equal += __popc(is_equal);
+      }
     }
   }
   for (int i = threadIdx.x; i < p.recent; i += kSelectThreads) kept[want + i] = count + i;

@@ -104,20 +104,16 @@ __device__ __forceinline__ void issue(const Params& p, State& s, const AttendRow
 __device__ __noinline__ void prepare(const Params& p, const DraftTree& tree, uint32_t at, int columns, int t, int base, bool all) {
   const int per = (int)p.per.d;
   int draft = (int)fast_div32(p.per, (uint32_t)p.row0), head = p.row0 - draft * per;
+  bool sees = true;
+  if (!all) sees = tree.sees(p, min(draft, p.drafts - 1), t, base);
 #pragma unroll 1
   for (int c = 0; c < columns; c += 32) {
-    uint32_t x[32];
+    uint32_t x[32], seen = ~0u;
     tmem_load(x, at + c);
-    tmem_wait_load(x);
-    if (p.cap_out != 0.0f) {
-#pragma unroll
-      for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(p.cap_out * tanhf(__uint_as_float(x[e]) * p.cap_in));
-    }
     if (!all) {
-      bool sees = tree.sees(p, min(draft, p.drafts - 1), t, base);
-#pragma unroll
+#pragma unroll 1
       for (int e = 0; e < 32; ++e) {
-        if (!sees) x[e] = __float_as_uint(-CUDART_INF_F);
+        if (!sees) seen &= ~(1u << e);
         if (++head == per) {
           head = 0;
           ++draft;
@@ -125,6 +121,13 @@ __device__ __noinline__ void prepare(const Params& p, const DraftTree& tree, uin
         }
       }
     }
+    tmem_wait_load(x);
+    if (p.cap_out != 0.0f) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(p.cap_out * tanhf(__uint_as_float(x[e]) * p.cap_in));
+    }
+#pragma unroll
+    for (int e = 0; e < 32; ++e) x[e] = seen >> e & 1 ? x[e] : __float_as_uint(-CUDART_INF_F);
     tmem_store(at + c, x);
   }
   tmem_wait_store();
