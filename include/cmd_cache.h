@@ -316,6 +316,7 @@ typedef struct cmd_evict_args {
   int32_t* status;
 } cmd_evict_args;
 
+/* For a call with at most these rows, layers, heads and budget (or columns * page_size, where that is less). */
 cmd_status cmd_evict_workspace(int64_t rows, int32_t layers, int32_t kv_heads, int32_t budget, int64_t* bytes);
 cmd_status cmd_cache_evict(const cmd_evict_args* args, void* cuda_stream);
 

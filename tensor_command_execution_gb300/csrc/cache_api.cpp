@@ -1007,7 +1007,8 @@ extern "C" cmd_status cmd_attention_drafts(const cmd_drafts_args* args, void* cu
     const bool kept = one && has_weights && tokens > 0 && copy == 16 && es == 2 && (__int128)rows * heads * tokens * 4 <= kMostScores;
     float* scores = kept ? reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(stats) + round_up(rows * heads * 8, 16)) : nullptr;
     p.scores_tokens = tokens;
-    const bool tma = tc && !(one && (kept || !has_weights)) && cmdx::drafts_tma_fits(a.k_cache.sizes[1], a.k_cache.sizes, a.k_cache.strides, a.v_cache.strides) &&
+    // (the weights' kernel takes heads of up to 256 dims, the attention's of up to 128)
+    const bool tma = copy == 16 && es == 2 && (tc || has_weights) && !(one && (kept || !has_weights)) && cmdx::drafts_tma_fits(a.k_cache.sizes[1], a.k_cache.sizes, a.k_cache.strides, a.v_cache.strides) &&
                      in_device_memory(a.k_cache.ptr) && in_device_memory(a.v_cache.ptr);
     if (one) {
       attend_blocks(p, es, copy);
@@ -1292,10 +1293,12 @@ extern "C" cmd_status cmd_cache_evict(const cmd_evict_args* args, void* cuda_str
     }
     NEED(a.recent >= 0 && a.budget >= a.recent, CMD_ERR_ARG, "recent is 0 to budget");
     if (p.rows == 0 && p.pages == 0) return CMD_OK;
-    check_workspace(a.workspace, a.workspace_bytes, evict_workspace(p.rows, a.n_layers, p.heads, a.budget));
+    // (no row is longer than the table: nothing is kept of a list that would be)
+    const int32_t budget = (int32_t)std::min<int64_t>(a.budget, (int64_t)p.columns * p.page.d);
+    check_workspace(a.workspace, a.workspace_bytes, evict_workspace(p.rows, a.n_layers, p.heads, budget));
     p.layers = a.n_layers;
-    p.budget = a.budget;
-    p.recent = a.recent;
+    p.budget = budget;
+    p.recent = std::min(a.recent, budget);
     p.kept = static_cast<int32_t*>(a.workspace);
     // at least 4 pieces (64 bytes) to a CTA, and no more CTAs than fill the device about four times
     p.slices = 1;

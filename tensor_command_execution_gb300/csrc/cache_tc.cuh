@@ -118,13 +118,16 @@ struct TmaTiles {
   __device__ __forceinline__ void copy(const CUtensorMap& map, int kv, uint32_t slot, uint32_t bar) const {
     if (one) mbar_arrive_expect_tx(bar, (uint32_t)(__popc(taken) * slabs * p.box * 128));
     __syncwarp();
-    const int box = lane & (boxes - 1), slab = lane / boxes, t = t0 + box * p.box;
+    const int box = lane & (boxes - 1), t = t0 + box * p.box;
     const int from = __shfl_sync(~0u, page, sub * boxes + box), first = t - (int)(fast_div32(p.page, (uint32_t)t) * p.page.d);
-    if (slab < slabs && (taken >> box & 1))
-      asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
-                       slot + slab * kTcTile * 128 + box * p.box * 128),
-                   "l"(&map), "r"(64 * slab), "r"(first), "r"(kv), "r"(from), "r"(bar)
-                   : "memory");
+    if (taken >> box & 1) {
+#pragma unroll 1
+      for (int slab = lane / boxes; slab < slabs; slab += 32 / boxes)  // (once, up to 128 dims)
+        asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+                         slot + slab * kTcTile * 128 + box * p.box * 128),
+                     "l"(&map), "r"(64 * slab), "r"(first), "r"(kv), "r"(from), "r"(bar)
+                     : "memory");
+    }
     __syncwarp();
   }
 };

@@ -13,6 +13,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
 #include <exception>
 #include <string>
@@ -597,7 +598,9 @@ PyObject* py_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
     x.refs_out = output(out[1], w, {x.refs.sizes[0]}, &made[1], "refs_out");
     const int64_t heads = list[0][0].sizes[2];
     if (heads > 0 && heads <= INT32_MAX && x.budget >= 0) {
-      check(cmd_evict_workspace(x.tables.sizes[0], x.n_layers, (int32_t)heads, x.budget, &x.workspace_bytes), "cmd_evict_workspace");
+      const int64_t most = std::min<int64_t>(x.tables.sizes[1] * list[0][0].sizes[1], INT32_MAX);  // (of a row's tokens)
+      check(cmd_evict_workspace(x.tables.sizes[0], x.n_layers, (int32_t)heads, std::min(x.budget, (int32_t)most), &x.workspace_bytes),
+            "cmd_evict_workspace");
       workspace = w.scratch(x.workspace_bytes);
       x.workspace = workspace.get();
     }

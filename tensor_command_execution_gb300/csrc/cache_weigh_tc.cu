@@ -4,11 +4,11 @@
 // weights[t] += sum over the query rows q of a kv head of exp2(s_qt - m_q) / l_q,
 // with the maxima m and sums l that the attention has left. The scores are
 // worked out again from the keys alone, transposed: 128 tokens by up to 256
-// query rows, so that a thread holds all of a token's scores and its sum needs
+// query rows (128 of heads above 128 dims), so that a thread holds all of a token's scores and its sum needs
 // no other thread. (Keeping the scores instead would cost 8 bytes for each token
 // and query row, more than the keys' 2 dim bytes from dim / 4 rows on.) Two
 // groups of four warps take turns, as in cache_drafts_tc.cu. Where a kv head has
-// more than 256 query rows, each 256 of them are a launch, one after another.
+// more query rows, so many each are a launch, one after another.
 #include <type_traits>
 
 #include "cache_tc.cuh"
@@ -20,18 +20,18 @@ namespace {
 
 constexpr int kGroup = 128;                // threads of a group, and tokens of a tile
 constexpr int kThreads = 2 * kGroup + 64;  // and a warp that issues the products, and one that copies
-constexpr int kMostRows = 256;
 constexpr int kTile = kTcTile;
 static_assert(kTile == kGroup, "a token to a thread");
 
 struct Params : TcParams {
-  int32_t row0;  // the query rows of this launch: row0 .. row0 + 255
+  int32_t row0;  // the first query row of this launch
 };
 
 template <int DP>
 struct Shape {
+  static constexpr int kMostRows = DP == 256 ? 128 : 256;  // of a launch
   static constexpr int kSlot = kTile * DP * 2;
-  static constexpr int kSlots = DP == 64 ? 8 : 4;
+  static constexpr int kSlots = DP == 64 ? 8 : DP == 128 ? 4 : 2;
   static constexpr int kQueries = kMostRows * DP * 2;
   static constexpr int kRest = kQueries + kSlots * kSlot;
 };
@@ -42,7 +42,7 @@ struct State {
   uint32_t tmem;
   uint32_t stop;                    // a wait ran out of time
   uint32_t here[kHereTiles][4];     // which tokens of a tile have a page
-  float4 stats[kMostRows / 2];      // of two rows: -m, -m, 1 / l, 1 / l
+  float4 stats[128];                // of two rows: -m, -m, 1 / l, 1 / l
 };
 template <int DP>
 constexpr int kSmem = Shape<DP>::kRest + (int)(sizeof(State) + sizeof(DraftTree) + sizeof(AttendRows)) + 1024;
@@ -89,7 +89,7 @@ __device__ __forceinline__ void issue(const Params& p, State& s, const AttendRow
 #pragma unroll
       for (int e = 0; e < DP / 16; ++e)
         if (e < steps)
-          tcgen05_mma(one, tmem + w * 256, a + (e / 4 * kTile * 128 + e % 4 * 32) / 16, b + (e / 4 * kMostRows * 128 + e % 4 * 32) / 16, shape, e > 0);
+          tcgen05_mma(one, tmem + w * 256, a + (e / 4 * kTile * 128 + e % 4 * 32) / 16, b + (e / 4 * S::kMostRows * 128 + e % 4 * 32) / 16, shape, e > 0);
       tcgen05_commit(one, smem_u32(&s.scores[w]));
       tcgen05_commit(one, smem_u32(&s.empty[at]));
       keys = (keys + 1) % (2 * S::kSlots);
@@ -189,7 +189,7 @@ __device__ __forceinline__ void sums(const Params& p, State& s, DraftTree& tree,
       constexpr int kPieces = DP / 8, kOver = 2 * kGroup / kPieces, kAtOnce = 4;
       const int c = threadIdx.x % kPieces;
       if (c < (p.dim + 15) / 16 * 2) {
-        unsigned char* slab = queries + c / 8 * kMostRows * 128;
+        unsigned char* slab = queries + c / 8 * S::kMostRows * 128;
 #pragma unroll 1
         for (int r0 = threadIdx.x / kPieces; r0 < columns; r0 += kOver * kAtOnce) {
           uint4 x[kAtOnce];
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
   tcgen05_after_sync();
   const uint32_t tmem = *static_cast<volatile uint32_t*>(&s.tmem);
   const uint32_t queries = smem_u32(s_mem), ring = queries + S::kQueries;
-  const int n = min(p.group - p.row0, kMostRows), columns = (n + 15) / 16 * 16;
+  const int n = min(p.group - p.row0, S::kMostRows), columns = (n + 15) / 16 * 16;
   if (share.begin == share.end) {
   } else if (warp < 8) {
     sums<T, DP>(p, s, tree, rows, share, s_mem, tmem, n, columns);
@@ -300,13 +300,14 @@ cudaError_t launch(const Params& p, cudaStream_t stream) {
   cudaError_t e = allow_smem(weigh_tc_kernel<T, DP>, kSmem<DP>, ready);
   Params q = p;
   const int ctas = attend_sides(p.kv_heads, 152, &q.sides);
-  for (q.row0 = 0; e == cudaSuccess && q.row0 < q.group; q.row0 += kMostRows)
+  for (q.row0 = 0; e == cudaSuccess && q.row0 < q.group; q.row0 += Shape<DP>::kMostRows)
     e = launch_chained(weigh_tc_kernel<T, DP>, ctas, kThreads, (size_t)kSmem<DP>, stream, q);
   return e;
 }
 template <class T>
 cudaError_t by_dim(const Params& p, cudaStream_t stream) {
-  return p.dim <= 64 ? launch<T, 64>(p, stream) : launch<T, 128>(p, stream);
+  if (p.dim <= 64) return launch<T, 64>(p, stream);
+  return p.dim <= 128 ? launch<T, 128>(p, stream) : launch<T, 256>(p, stream);
 }
 
 }  // namespace

@@ -391,3 +391,132 @@ def test_padding_may_hold_anything(kind, drafts, dim, junk):
                 assert bool((want[r, i] == 0).all()) and bool((want_lse[r, i] == -math.inf).all())
     got, lse = T.attention_drafts(q, c.k, c.v, c.tables, c.lengths, parents=_i32(parents), return_lse=True, weights=w1)
     assert torch.equal(got, want) and torch.equal(lse, want_lse) and torch.equal(w0, w1)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("hq,hk,dim,page", [(8, 8, 64, 16), (32, 4, 128, 16), (7, 1, 64, 3), (24, 2, 256, 1), (33, 1, 72, 16), (48, 3, 100, 8),
+                                            (4, 2, 33, 16), (130, 1, 64, 32)])
+def test_weights_of_one_token(kind, hq, hk, dim, page):
+    """One new token's scores are kept (16-bit rows of whole 16-byte vectors), or worked out again."""
+    _check(kind, [0, 1, 15, 130, -1, 1500], 1, hq, hk, dim, page, tree=None)
+    _check(kind, [0, 40, 200], 1, hq, hk, dim, page, tree=None, softcap=5.0, window=30)
+    _check(kind, [0, 40, 200], 1, hq, hk, dim, page, tree="padded", seed=2)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("drafts,hq,hk,dim,page", [(16, 28, 2, 192, 8), (5, 8, 2, 256, 16), (40, 8, 1, 136, 64), (2, 4, 4, 200, 24), (9, 30, 1, 256, 8)])
+def test_weights_of_wide_heads(kind, drafts, hq, hk, dim, page):
+    """Heads of more than 128 dims, with more query rows to a head than a launch takes."""
+    _check(kind, [0, 1, 100, 700, -1], drafts, hq, hk, dim, page, tree="padded")
+    _check(kind, [300, 20], drafts, hq, hk, dim, page, tree="tree", softcap=5.0, window=60)
+
+
+@pytest.mark.parametrize("drafts", [1, 3])
+def test_weights_of_tables_with_room_for_millions(drafts):
+    """Scores that would take more than a GiB are not kept; tables, weights and lengths of rows far apart."""
+    lengths, columns = [700, 3, 2100], 100_000
+    totals = [n + drafts for n in lengths]
+    c = U.Cache("bf16", totals, 8, 64, 16, columns=columns)
+    q = _randn(3, drafts, 64, 64, kind="bf16", seed=1)
+    weights = torch.zeros(3, 8, columns * 16, device="cuda")
+    out, lse = T.attention_drafts(q, c.k, c.v, c.tables, c.lengths, weights=weights, return_lse=True)
+    _, _, want, _, _, bound = D.drafted(q, c, totals, D.trees(3, drafts, "chain"), 0.125)
+    for r, n in enumerate(totals):
+        _near(weights[r, :, :n], want[r], bound[r] + 2.0 ** -24 * want[r], "weights")
+        assert not bool(weights[r, :, n:].any())
+
+
+def test_two_streams_at_once():
+    """Calls on two streams over one cache, each with its own workspace and outputs, again and again."""
+    c = U.Cache("bf16", [3000, 40, 900, 260], 2, 128, 16)
+    calls = []
+    for seed in range(2):
+        q, parents = _randn(4, 10, 8, 128, kind="bf16", seed=seed), _i32(D.trees(4, 10, "tree", seed))
+        calls.append((q, parents, T.attention_drafts(q, c.k, c.v, c.tables, c.lengths, parents=parents)))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            w = torch.zeros(4, 2, c.tables.shape[1] * 16, device="cuda")
+            s.wait_stream(torch.cuda.current_stream())
+            got[i].append((T.attention_drafts(calls[i][0], c.k, c.v, c.tables, c.lengths, parents=calls[i][1], weights=w, stream=s), w))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, calls[i][2]) and torch.equal(w, got[i][0][1]) for x, w in got[i])
+
+
+def test_a_step_with_drafts():
+    """Room for the drafts, their keys at their own positions, attention, the accepted branch and its slots: the cache is
+    what it would be had the accepted tokens come one by one; captured in a graph too."""
+    drafts, tree = 7, [-1, 0, 0, 1, 1, 3, 2]
+    depth = _i32([0, 1, 1, 2, 2, 3, 2])
+    turns = T.rope_turns(64)
+    gen = torch.Generator(device="cuda").manual_seed(0)
+
+    def start():
+        c = U.Cache("bf16", [33, 16, 5], 2, 64, 16, spare=12, columns=6)
+        return c, D.counts(c)
+    tokens = _i32([[3, 5, 6, 7, 8, 9, 4], [1, 2, 2, 4, 4, 4, 4], [9, 8, 7, 6, 5, 4, 3]])
+    choices = _i32([[5, 8, 0, 0, 0, 0, 0], [2, 4, 0, 4, 0, 0, 0], [0, 0, 0, 0, 0, 0, 0]])
+    want_path = [[0, 1, 4], [0, 1, 3, 5], [0]]
+    parents = _i32([tree] * 3)
+    q, k, v = (torch.randn(3, drafts, h, 64, generator=gen, device="cuda").bfloat16() for h in (8, 2, 2))
+    same, grow = _i32([0, 1, 2]), _i32([drafts] * 3)
+    rows = same.repeat_interleave(drafts)
+
+    def step(c, refs):
+        t, n, r = T.cache_select(c.tables, c.lengths, refs, same, [c.k, c.v], page_size=16, grow=grow)
+        positions = n[:, None] - drafts + depth
+        x, y = T.rope(q, k, positions, turns)
+        slots = (n[:, None] - drafts + torch.arange(drafts, dtype=torch.int32, device="cuda")).flatten()
+        T.cache_append(y.flatten(0, 1), v.flatten(0, 1), c.k, c.v, t, slots, rows=rows)
+        out = T.attention_drafts(x, c.k, c.v, t, n, parents=parents)
+        path, counts, last = T.draft_path(tokens, choices, parents=parents)
+        n, r = T.cache_accept(t, n, r, path, counts, [c.k, c.v], drafts=drafts)
+        return out, t, n, r, path, counts, last, c.k, c.v
+
+    c, refs = start()
+    got = [x.clone() for x in step(c, refs)]
+    out, t, n, r, path, counts, last = got[:7]
+    assert [p[:k] for p, k in zip(path.tolist(), counts.tolist())] == want_path
+    assert n.tolist() == [33 + 3, 16 + 4, 5 + 1]
+    # the same tokens, one at a time
+    one, refs1 = start()
+    t1, n1, r1 = one.tables, one.lengths, refs1
+    for step_ in range(4):
+        alive = [step_ < len(w) for w in want_path]
+        node = [w[min(step_, len(w) - 1)] for w in want_path]
+        t1, n1, r1 = T.cache_select(t1, n1, r1, same, [one.k, one.v], page_size=16, grow=_i32([int(a) for a in alive]))
+        pick = torch.tensor(node, device="cuda")
+        kk, vv, qq = (x[torch.arange(3, device="cuda"), pick] for x in (k, v, q))
+        pos = torch.where(torch.tensor(alive, device="cuda"), n1 - 1, -1)
+        turned = T.cache_append(kk, vv, one.k, one.v, t1, pos.int(), q=qq, turns=turns)
+        single = T.attention_decode(turned, one.k, one.v, t1, n1)
+        for row in range(3):
+            if alive[row]:
+                # (the same function: two roundings of values below 4)
+                assert float((single[row].float() - out[row, node[row]].float()).abs().max()) < 8 * U.ROUND["bf16"]
+    assert torch.equal(n1, n)
+    for row, length in enumerate(n.tolist()):
+        at = torch.arange(length, device="cuda")
+        for x, y in ((got[7], one.k), (got[8], one.v)):
+            assert torch.equal(x[t[row].long()[at // 16], at % 16], y[t1[row].long()[at // 16], at % 16])
+    assert int(r.sum()) == int(r1.sum()) == sum(-(-x // 16) for x in n.tolist())
+    # captured
+    c, refs = start()
+    kc, vc = c.k.clone(), c.v.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(c, refs)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        again = step(c, refs)
+    for _ in range(2):
+        c.k.copy_(kc)
+        c.v.copy_(vc)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(again, got))

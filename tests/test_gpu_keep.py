@@ -363,3 +363,37 @@ def test_captured_and_replayed(which):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_a_budget_beyond_the_table():
+    """... keeps every row as it is, with no more workspace than the table's tokens ask for."""
+    c = U.Cache("bf16", [60, 30], 2, 32, 8)
+    refs, w = D.counts(c), torch.rand(2, 2, 64, device="cuda")
+    before = [x.clone() for x in (c.k, c.v, w)]
+    lengths, out = T.cache_evict(c.tables, c.lengths, refs, [(c.k, c.v, w)], budget=2 ** 31 - 1, recent=2 ** 31 - 1)
+    assert torch.equal(lengths, c.lengths) and torch.equal(out, refs)
+    assert all(torch.equal(a, b) for a, b in zip(before, (c.k, c.v, w)))
+
+
+def test_evicted_rows_go_on():
+    """Rows are held to their budget, grow again, and are attended to: what is left is a cache like any other."""
+    c = U.Cache("f32", [50, 20, 90], 2, 64, 8, spare=6, columns=14)
+    w = torch.rand(3, 2, 14 * 8, device="cuda")
+    refs = D.counts(c)
+    kept = [D.evicted(w[r, h].tolist(), n, 32, 5) if n > 32 else list(range(n)) for r, n in enumerate((50, 20, 90)) for h in range(2)]
+    keys, values = ([[x[D.slots(c, r, n)][:, h].clone() for h in range(2)] for r, n in enumerate((50, 20, 90))] for x in (c.k, c.v))
+    lengths, refs = T.cache_evict(c.tables, c.lengths, refs, [(c.k, c.v, w)], budget=32, recent=5)
+    tables, lengths, refs = T.cache_select(c.tables, lengths, refs, _i32([0, 1, 2]), [c.k, c.v], page_size=8, grow=_i32([1, 1, 1]))
+    assert lengths.tolist() == [33, 21, 33]
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    q, k, v = (torch.randn(3, h, 64, generator=gen, device="cuda") for h in (4, 2, 2))
+    T.cache_append(k, v, c.k, c.v, tables, lengths - 1)
+    out = T.attention_decode(q, c.k, c.v, tables, lengths)
+    for r in range(3):
+        for h in range(2):
+            kk = torch.cat([keys[r][h][kept[2 * r + h]], k[r, h][None]]).double()
+            vv = torch.cat([values[r][h][kept[2 * r + h]], v[r, h][None]]).double()
+            for i in (2 * h, 2 * h + 1):
+                want = torch.softmax(kk @ q[r, i].double() / 8, 0) @ vv
+                # (33 terms of values below 5 and scores below 8 in 32 bits)
+                assert float((out[r, i].double() - want).abs().max()) < 64 * 2.0 ** -24 * 5 * 8
