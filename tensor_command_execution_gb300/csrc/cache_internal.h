@@ -174,6 +174,7 @@ struct PathParams {
 cudaError_t path_launch(const PathParams& p, cudaStream_t stream);
 
 // What the accepted tokens' move and the eviction share: rows that are cut.
+constexpr int kEvictMoveThreads = 256, kEvictMoveAtOnce = 8;  // of a CTA that moves what an eviction keeps
 struct KeepParams {
   const int32_t *tables, *lengths, *refs;
   int32_t *lengths_out, *refs_out;
@@ -190,7 +191,7 @@ struct KeepParams {
   int32_t drafts;
   // evict
   int32_t budget, recent, layers;
-  int32_t slices;             // a token's pieces go to so many CTAs
+  int32_t slices, team;       // a token's pieces go to so many clusters of so many CTAs
   int32_t* kept;              // [rows][layers][heads][budget]
 };
 struct KeepPool {

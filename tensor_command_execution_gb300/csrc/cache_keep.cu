@@ -7,6 +7,7 @@
 // far ahead as it likes: what it writes lies before everything that it has yet
 // to read. A plan (a warp to a row) says first which rows are cut, and copies
 // the counts; pages past a row's new end are released by the move.
+#include <cooperative_groups.h>
 #include <math_constants.h>
 
 #include "cache_common.cuh"
@@ -14,6 +15,8 @@
 namespace cmdx {
 
 namespace {
+
+namespace cg = cooperative_groups;
 
 __device__ __forceinline__ int pages_of(const KeepParams& p, int n) { return (int)fast_div32(p.page, (uint32_t)n + p.page.d - 1); }
 
@@ -399,29 +402,33 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
   for (int i = threadIdx.x; i < p.recent; i += kSelectThreads) kept[want + i] = count + i;
 }
 
-// A CTA moves the kept keys or values of one kv head of one layer and row (some
-// of each token's pieces), or its weights, chunks of tokens in order. While a
-// chunk's data is on its way, the next one's places are looked up; it is read
-// before this one is written, and the barrier between stands for its reads by
-// all threads.
-constexpr int kMoveThreads = 256, kMoveAtOnce = 8;
+// A team (a cluster of CTAs) moves the kept keys or values of one kv head of one
+// layer and row (some of each token's pieces), or its weights: chunks of tokens
+// in order, one to each CTA at a time. No token moves up, so that what a chunk is
+// written over lies in its own place or before it, and all that is left to see to
+// is that the team has read its chunks before any of them is written: a barrier
+// of the team. While a chunk's data is on its way, the next one's places are
+// looked up. (A lone CTA takes 2 us for 256 tokens; CTAs without a row to cut cost
+// as much as they are many, so that teams stand where the lists are few.)
+constexpr int kMoveThreads = kEvictMoveThreads, kMoveAtOnce = kEvictMoveAtOnce;
 
 // tokens: of a chunk (threads / pieces * kMoveAtOnce); from, to: their places,
 // two chunks of each
 template <class U, class F>
-__device__ __forceinline__ void move_kept(int n, int pieces, int64_t* from, int64_t* to, uint8_t* base, const F& place) {
+__device__ __forceinline__ void move_kept(int n, int team, int pieces, int64_t* from, int64_t* to, uint8_t* base, const F& place) {
   const int over = kMoveThreads / pieces;  // tokens side by side
   const int mine = threadIdx.x / pieces, piece = threadIdx.x - mine * pieces;
-  const int chunk = over * kMoveAtOnce;
+  const int chunk = over * kMoveAtOnce, first = blockIdx.x % team * chunk;
   const bool busy = mine < over;
   base += (int64_t)piece * sizeof(U);
   U x[kMoveAtOnce];
   const auto look = [&](int j0) {
     for (int i = threadIdx.x; i < chunk && j0 + i < n; i += kMoveThreads) place(j0 + i, &from[i], &to[i]);
   };
-  look(0);
+  look(first);
   __syncthreads();
-  for (int j0 = 0; j0 < n; j0 += chunk) {
+  for (int all0 = 0; all0 < n; all0 += team * chunk) {
+    const int j0 = all0 + first;
     int64_t d[kMoveAtOnce];
 #pragma unroll
     for (int k = 0; k < kMoveAtOnce; ++k) {
@@ -432,8 +439,9 @@ __device__ __forceinline__ void move_kept(int n, int pieces, int64_t* from, int6
       }
     }
     __syncthreads();  // (the places have been read; so has, after the next barrier, the data)
-    look(j0 + chunk);
-    __syncthreads();
+    look(j0 + team * chunk);
+    if (team > 1) cg::this_cluster().sync();
+    else __syncthreads();
 #pragma unroll
     for (int k = 0; k < kMoveAtOnce; ++k)
       if (busy && j0 + k * over + mine < n) *reinterpret_cast<U*>(base + d[k]) = x[k];
@@ -446,20 +454,21 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
   wait_for_previous();
   let_next_start();
   // the slices of a list: keys, values, and at the end the weights
-  const int slices = 2 * p.slices + 1, what = blockIdx.x % slices, list = blockIdx.x / slices;
+  const int slices = 2 * p.slices + 1, what = blockIdx.x / p.team % slices, list = blockIdx.x / p.team / slices;
   const int head = list % p.heads, task = list / p.heads, layer = task % p.layers, row = task / p.layers;
   const int n = keep_length(p, row), now = p.lengths_out[row];
   if (n <= p.budget || now != p.budget) return;
   const int32_t* kept = p.kept + (int64_t)list * p.budget;
   if (what == slices - 1) {
     float* weights = layers.weights[layer] + row * layers.w_st[layer][0] + head * layers.w_st[layer][1];
-    move_kept<float>(now, 1, s_from, s_to, reinterpret_cast<uint8_t*>(weights), [&](int j, int64_t* from, int64_t* to) {
+    move_kept<float>(now, p.team, 1, s_from, s_to, reinterpret_cast<uint8_t*>(weights), [&](int j, int64_t* from, int64_t* to) {
       *from = 4 * (int64_t)kept[j];
       *to = 4 * (int64_t)j;
     });
-    __syncthreads();
-    for (int t = now + threadIdx.x; t < n; t += kMoveThreads) weights[t] = 0.0f;
-    if (layer == 0 && head == 0) release_pages(p, row, now, n);
+    // (the team has read all that it will, now that its last chunks are written)
+    const int rank = blockIdx.x % p.team;
+    for (int t = now + rank * kMoveThreads + (int)threadIdx.x; t < n; t += p.team * kMoveThreads) weights[t] = 0.0f;
+    if (layer == 0 && head == 0 && rank == 0) release_pages(p, row, now, n);
     return;
   }
   const int each = (p.pieces + p.slices - 1) / p.slices, piece0 = what / 2 * each, pieces = min(each, p.pieces - piece0);
@@ -470,7 +479,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     const uint32_t column = fast_div32(p.page, (uint32_t)t);
     return table[column] * pool.st[0] + (int64_t)(t - column * p.page.d) * pool.st[1];
   };
-  move_kept<U>(now, pieces, s_from, s_to, pool.ptr + head * pool.st[2] + (int64_t)piece0 * sizeof(U), [&](int j, int64_t* from, int64_t* to) {
+  move_kept<U>(now, p.team, pieces, s_from, s_to, pool.ptr + head * pool.st[2] + (int64_t)piece0 * sizeof(U), [&](int j, int64_t* from, int64_t* to) {
     *from = slot(kept[j]);
     *to = slot(j);
   });
@@ -523,7 +532,7 @@ cudaError_t evict_launch(const KeepParams& p, const KeepLayers& layers, cudaStre
   }
   if (e != cudaSuccess) return e;
   return by_unit(p.unit, [&](auto u) {
-    return launch_chained(evict_move_kernel<decltype(u)>, (2 * p.slices + 1) * lists, kMoveThreads, 0, stream, p, layers);
+    return launch_clusters(evict_move_kernel<decltype(u)>, p.team, (unsigned)((2 * p.slices + 1) * lists * p.team), kMoveThreads, 0, stream, p, layers);
   });
 }
 

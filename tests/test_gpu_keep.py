@@ -397,3 +397,11 @@ def test_evicted_rows_go_on():
                 want = torch.softmax(kk @ q[r, i].double() / 8, 0) @ vv
                 # (33 terms of values below 5 and scores below 8 in 32 bits)
                 assert float((out[r, i].double() - want).abs().max()) < 64 * 2.0 ** -24 * 5 * 8
+
+
+@pytest.mark.parametrize("kind,heads,dim,order,pad", [("bf16", 2, 64, "slots", 0), ("f32", 3, 33, "heads", 0), ("f16", 1, 256, "slots", 0),
+                                                      ("bf16", 8, 128, "heads", 0), ("bf16", 2, 96, "both", 1), ("f32", 20, 40, "slots", 0)])
+@pytest.mark.parametrize("budget,recent", [(3001, 100), (513, 512), (4999, 4999)])
+def test_evict_long_lists(kind, heads, dim, order, pad, budget, recent):
+    """Lists that several CTAs move side by side, most tokens by a few slots, or by thousands."""
+    _evict(kind, [5000, 3002, 40], heads, dim, 16, budget, recent, order, pad=pad)
