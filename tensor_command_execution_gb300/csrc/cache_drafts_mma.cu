@@ -70,21 +70,32 @@ __device__ __forceinline__ void copy_tile(const DraftParams& p, const DraftTile<
 // Query rows [q0, q0 + n) of a kv head, zeros past them and past the head dim.
 template <class T, int DP, int ROWS>
 __device__ __forceinline__ void load_queries(const DraftParams& p, unsigned char* to, int row, int kv, int q0, int n, int steps) {
-  constexpr int kPitch = DP * 2 + 16;
-  const int pairs = steps * 8;
-  for (int i = threadIdx.x; i < ROWS * pairs; i += kThreads) {
-    const int r = i / pairs, d = 2 * (i - r * pairs);
-    uint32_t x = 0;
-    if (r < n && d < p.dim) {
-      const T* q = draft_query<T>(p, row, kv, q0 + r) + d;
-      if (p.q_pairs) {
-        x = *reinterpret_cast<const uint32_t*>(q);
-      } else {
-        T e[2] = {q[0], d + 1 < p.dim ? q[1] : from_float<T>(0.0f)};
-        x = *reinterpret_cast<uint32_t*>(e);
+  constexpr int kPitch = DP * 2 + 16, kAtOnce = 4;
+  const int pieces = steps * 2;  // of 8 numbers
+#pragma unroll 1
+  for (int i0 = threadIdx.x; i0 < ROWS * pieces; i0 += kThreads * kAtOnce) {
+    uint4 x[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int i = i0 + k * kThreads, r = i / pieces, d = 8 * (i - r * pieces);
+      x[k] = make_uint4(0, 0, 0, 0);
+      if (r < n && d < p.dim) {
+        const T* q = draft_query<T>(p, row, kv, q0 + r) + d;
+        if (p.q_vectors && p.dim % 8 == 0) {
+          x[k] = *reinterpret_cast<const uint4*>(q);
+        } else {
+          T e[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) e[j] = d + j < p.dim ? q[j] : from_float<T>(0.0f);
+          x[k] = *reinterpret_cast<uint4*>(e);
+        }
       }
     }
-    *reinterpret_cast<uint32_t*>(to + r * kPitch + 2 * d) = x;
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int i = i0 + k * kThreads, r = i / pieces;
+      if (r < ROWS) *reinterpret_cast<uint4*>(to + r * kPitch + 16 * (i - r * pieces)) = x[k];
+    }
   }
 }
 
@@ -178,9 +189,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, MT>::kCtas)) drafts_mma_k
       bool infinite = false;  // a value that a masked weight of zero would turn to NaN
       if (masked) {
         bool found = false;
-        for (int j = threadIdx.x; j < kTile * steps * 8; j += kThreads) {
-          const int r = j / (steps * 8), c = j - r * steps * 8;
-          found |= not_finite<T>(*reinterpret_cast<const uint32_t*>(s_mem + buffer * S::kStage + S::kKeys + r * S::kPitch + 4 * c)) != 0;
+        static_assert(kThreads == 2 * kTile, "two threads to a row");
+        const unsigned char* v = s_mem + buffer * S::kStage + S::kKeys + threadIdx.x / 2 * S::kPitch + threadIdx.x % 2 * 16;
+#pragma unroll 4
+        for (int j = 0; j < steps; ++j) {
+          const uint4 x = *reinterpret_cast<const uint4*>(v + 32 * j);
+          found |= (not_finite<T>(x.x) | not_finite<T>(x.y) | not_finite<T>(x.z) | not_finite<T>(x.w)) != 0;
         }
         infinite = __syncthreads_or(found);
       }
