@@ -12,15 +12,16 @@ namespace cmdx {
 
 namespace {
 
-constexpr int kThreads = 128;
 constexpr int kTile = 64;  // tokens of a tile
 
 // Query rows come in MT tiles of 16, one for each MT-th warp; where there are
-// fewer than 4 of those, the others take other tokens of a tile.
+// fewer of those than warps, the others take other tokens of a tile. (Wide heads
+// leave room for one CTA on an SM: it has eight warps rather than four.)
 template <int DP, int MT>
 struct Shape {
+  static constexpr int kWarps = DP == 256 && MT > 1 ? 8 : 4, kThreads = 32 * kWarps;
   static constexpr int kRows = 16 * MT;
-  static constexpr int kSets = 4 / MT;             // warps that hold states of the same rows
+  static constexpr int kSets = kWarps / MT;        // warps that hold states of the same rows
   static constexpr int kMine = kTile / kSets;      // tokens of a warp
   static constexpr int kChunk = kMine < 32 ? kMine : 32;
   static constexpr int kPitch = DP * 2 + 16;       // bytes of a row: an odd number of 16
@@ -30,14 +31,14 @@ struct Shape {
   static constexpr int kRest = kQueries + kRows * kPitch;
   static constexpr int kSmem = kRest + (int)(2 * sizeof(DraftTile<kTile>) + sizeof(DraftTree) + sizeof(AttendRows));
   static constexpr int kStatePitch = attend_pitch(DP);
-  static_assert(4 / MT * kRows * kStatePitch * 4 <= kStage, "the states fit a stage");
+  static_assert(kSets * kRows * kStatePitch * 4 <= 2 * kStage, "the states fit the stages");
   static constexpr int kCtas = kSmem <= 113 * 1024 ? 2 : 1;  // of an SM
 };
 
 // The rows of a tile (keys only, or keys and values) into a stage, elements
 // past the head dim up to a multiple of 16 as zeros, as the rows of tokens
 // that have no page.
-template <class T, int DP, bool VALUES>
+template <class T, int DP, int kThreads, bool VALUES>
 __device__ __forceinline__ void copy_tile(const DraftParams& p, const DraftTile<kTile>& tile, unsigned char* stage, int steps) {
   constexpr int kPitch = DP * 2 + 16, kKeys = kTile * kPitch;
   const T* k = static_cast<const T*>(p.k);
@@ -68,7 +69,7 @@ __device__ __forceinline__ void copy_tile(const DraftParams& p, const DraftTile<
 }
 
 // Query rows [q0, q0 + n) of a kv head, zeros past them and past the head dim.
-template <class T, int DP, int ROWS>
+template <class T, int DP, int kThreads, int ROWS>
 __device__ __forceinline__ void load_queries(const DraftParams& p, unsigned char* to, int row, int kv, int q0, int n, int steps) {
   constexpr int kPitch = DP * 2 + 16, kAtOnce = 4;
   const int pieces = steps * 2;  // of 8 numbers
@@ -134,9 +135,9 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t x) {
 }
 
 template <class T, int DP, int MT>
-__global__ void __launch_bounds__(kThreads, (Shape<DP, MT>::kCtas)) drafts_mma_kernel(const __grid_constant__ DraftParams p) {
+__global__ void __launch_bounds__((Shape<DP, MT>::kThreads), (Shape<DP, MT>::kCtas)) drafts_mma_kernel(const __grid_constant__ DraftParams p) {
   using S = Shape<DP, MT>;
-  constexpr int KS = DP / 16, NC = S::kChunk / 8;
+  constexpr int KS = DP / 16, NC = S::kChunk / 8, kThreads = S::kThreads;
   extern __shared__ __align__(16) unsigned char s_mem[];
   DraftTile<kTile>* s_tile = reinterpret_cast<DraftTile<kTile>*>(s_mem + S::kRest);
   DraftTree& s_tree = *reinterpret_cast<DraftTree*>(s_tile + 2);
@@ -157,9 +158,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, MT>::kCtas)) drafts_mma_k
     const int q0 = heads.head0 - heads.kv * p.group, base = g.n - p.drafts;
     draft_place(p, s_tile[0], draft_look(p, g, g.tile0, kTile, true), heads.kv);
     draft_place(p, s_tile[1], draft_look(p, g, g.tile0 + 1, kTile, g.tiles > 1), heads.kv);
-    load_queries<T, DP, S::kRows>(p, s_mem + S::kQueries, g.row, heads.kv, q0, heads.heads, steps);
+    load_queries<T, DP, kThreads, S::kRows>(p, s_mem + S::kQueries, g.row, heads.kv, q0, heads.heads, steps);
     draft_tree<kThreads>(p, s_tree, g.row, base);  // (with barriers: the tiles' places are complete)
-    copy_tile<T, DP, true>(p, s_tile[0], s_mem, steps);
+    copy_tile<T, DP, kThreads, true>(p, s_tile[0], s_mem, steps);
 
     // this thread's two query rows
     int draft[2];
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, MT>::kCtas)) drafts_mma_k
 
     for (int i = 0; i < g.tiles; ++i) {
       const int buffer = i & 1;
-      if (i + 1 < g.tiles) copy_tile<T, DP, true>(p, s_tile[buffer ^ 1], s_mem + (buffer ^ 1) * S::kStage, steps);
+      if (i + 1 < g.tiles) copy_tile<T, DP, kThreads, true>(p, s_tile[buffer ^ 1], s_mem + (buffer ^ 1) * S::kStage, steps);
       const DraftLook look = draft_look(p, g, g.tile0 + i + 2, kTile, i + 2 < g.tiles);
       if (i + 1 < g.tiles) copy_wait<1>();
       else copy_wait<0>();
@@ -189,11 +190,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, MT>::kCtas)) drafts_mma_k
       bool infinite = false;  // a value that a masked weight of zero would turn to NaN
       if (masked) {
         bool found = false;
-        static_assert(kThreads == 2 * kTile, "two threads to a row");
-        const unsigned char* v = s_mem + buffer * S::kStage + S::kKeys + threadIdx.x / 2 * S::kPitch + threadIdx.x % 2 * 16;
+        constexpr int kEach = kThreads / kTile;  // threads to a row
+        const unsigned char* v = s_mem + buffer * S::kStage + S::kKeys + threadIdx.x / kEach * S::kPitch;
 #pragma unroll 4
-        for (int j = 0; j < steps; ++j) {
-          const uint4 x = *reinterpret_cast<const uint4*>(v + 32 * j);
+        for (int j = threadIdx.x % kEach; j < 2 * steps; j += kEach) {
+          const uint4 x = *reinterpret_cast<const uint4*>(v + 16 * j);
           found |= (not_finite<T>(x.x) | not_finite<T>(x.y) | not_finite<T>(x.z) | not_finite<T>(x.w)) != 0;
         }
         infinite = __syncthreads_or(found);
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, MT>::kCtas)) drafts_mma_k
       __syncthreads();
     }
 
-    // the states into the first stage, which is copied to again only after attend_finish
+    // the states into the stages, which are copied to again only after attend_finish
     float* state = reinterpret_cast<float*>(s_mem) + (set * S::kRows + rows_of * 16) * S::kStatePitch;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -325,9 +326,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, MT>::kCtas)) drafts_mma_k
 // and sums that the attention has kept: each tile's scores are worked out
 // again, and one CTA sums a tile over all of its query rows in their order.
 template <class T, int DP, int MT>
-__global__ void __launch_bounds__(kThreads, 2) weigh_mma_kernel(const __grid_constant__ DraftParams p) {
+__global__ void __launch_bounds__((Shape<DP, MT>::kThreads), 2) weigh_mma_kernel(const __grid_constant__ DraftParams p) {
   using S = Shape<DP, MT>;
-  constexpr int NC = S::kMine / 8;
+  constexpr int NC = S::kMine / 8, kThreads = S::kThreads;
   extern __shared__ __align__(16) unsigned char s_mem[];
   // (two stages of keys alone)
   constexpr int kQueries = 2 * S::kKeys, kRest = kQueries + S::kRows * S::kPitch;
@@ -353,10 +354,10 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_mma_kernel(const __grid_con
     draft_place(p, s_tile[0], draft_look(p, g, g.tile0, kTile, true), kv);
     draft_place(p, s_tile[1], draft_look(p, g, g.tile0 + 1, kTile, g.tiles > 1), kv);
     draft_tree<kThreads>(p, s_tree, g.row, base);  // (with barriers: the tiles' places are complete)
-    copy_tile<T, DP, false>(p, s_tile[0], s_mem, steps);
+    copy_tile<T, DP, kThreads, false>(p, s_tile[0], s_mem, steps);
     for (int i = 0; i < g.tiles; ++i) {
       const int buffer = i & 1;
-      if (i + 1 < g.tiles) copy_tile<T, DP, false>(p, s_tile[buffer ^ 1], s_mem + (buffer ^ 1) * S::kKeys, steps);
+      if (i + 1 < g.tiles) copy_tile<T, DP, kThreads, false>(p, s_tile[buffer ^ 1], s_mem + (buffer ^ 1) * S::kKeys, steps);
       const DraftLook look = draft_look(p, g, g.tile0 + i + 2, kTile, i + 2 < g.tiles);
       if (i + 1 < g.tiles) copy_wait<1>();
       else copy_wait<0>();
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_mma_kernel(const __grid_con
         const int n = min(S::kRows, p.group - q0);
         if (i == 0 || p.group > S::kRows) {  // (one block stays where it is)
           __syncthreads();
-          load_queries<T, DP, S::kRows>(p, s_mem + kQueries, g.row, kv, q0, n, steps);
+          load_queries<T, DP, kThreads, S::kRows>(p, s_mem + kQueries, g.row, kv, q0, n, steps);
         }
         __syncthreads();
         int draft[2];
@@ -425,7 +426,7 @@ cudaError_t launch(const DraftParams& p, cudaStream_t stream) {
   static PerDevice ready;  // (static storage: zero before first use)
   const cudaError_t e = allow_smem(drafts_mma_kernel<T, DP, MT>, S::kSmem, ready);
   if (e != cudaSuccess) return e;
-  return attend_launch<T>(drafts_mma_kernel<T, DP, MT>, p, 2, 152 * S::kCtas, kThreads, S::kSmem, kTile, stream, false);
+  return attend_launch<T>(drafts_mma_kernel<T, DP, MT>, p, 2, 152 * S::kCtas, S::kThreads, S::kSmem, kTile, stream, false);
 }
 template <class T, int DP, int MT>
 cudaError_t weigh(DraftParams p, cudaStream_t stream) {
@@ -435,7 +436,7 @@ cudaError_t weigh(DraftParams p, cudaStream_t stream) {
   static PerDevice ready;  // (static storage: zero before first use)
   const cudaError_t e = allow_smem(weigh_mma_kernel<T, DP, MT>, smem, ready);
   if (e != cudaSuccess) return e;
-  return launch_chained(weigh_mma_kernel<T, DP, MT>, 152 * 2, kThreads, (size_t)smem, stream, p);
+  return launch_chained(weigh_mma_kernel<T, DP, MT>, 152 * 2, Shape<DP, MT>::kThreads, (size_t)smem, stream, p);
 }
 
 template <class T, int DP>

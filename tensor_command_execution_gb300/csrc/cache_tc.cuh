@@ -35,10 +35,16 @@ inline cudaError_t pool_maps(int dtype, const DraftParams& d, TcParams* out) {
     const cuuint64_t sizes[4] = {(cuuint64_t)p.dim, p.page.d, (cuuint64_t)p.kv_heads, (cuuint64_t)p.n_pages};
     const cuuint64_t strides[3] = {bytes(p.page.d, st[1]), bytes(p.kv_heads, st[2]), bytes(p.n_pages, st[0])};
     const cuuint32_t box[4] = {64, (cuuint32_t)p.box, 1, 1}, step[4] = {1, 1, 1, 1};
+    // (bytes that L2 fetches at once: no more than lie together. Of rows of 128 bytes between other heads' 256 would be
+    // half theirs.)
+    const cuuint64_t run = (st[1] == p.dim ? p.page.d : 1) * (cuuint64_t)p.dim * 2;
+    const CUtensorMapL2promotion fetch = run % 256 == 0   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                         : run % 128 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                          : CU_TENSOR_MAP_L2_PROMOTION_NONE;
     const CUresult r = tensor_map_encoder()(
         &p.maps[i], dtype == CMD_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
         const_cast<void*>(i == 0 ? p.k : p.v), sizes, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        fetch, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
   }
   return cudaSuccess;
