@@ -29,6 +29,8 @@
 #include <cooperative_groups.h>
 #include <math_constants.h>
 
+#include <type_traits>
+
 #include "cache_common.cuh"
 
 namespace cmdx {
@@ -206,8 +208,9 @@ __device__ __forceinline__ void attend_note(const AttendParams& p, int row, int 
 // Whether a part with this maximum says that its row is empty, whatever the others hold.
 __device__ __forceinline__ bool attend_void(const AttendParams&, float) { return false; }
 
-// Writes elements d .. d + 3 (those below dim) of a finished head.
-template <class T, class P>
+// Writes elements d .. d + 3 (those below dim) of a finished head. NOTE: its
+// maximum and sum may be asked for.
+template <class T, bool NOTE = true, class P>
 __device__ __forceinline__ void attend_write(const P& p, int row, int h, int d, float top, float l, float4 o) {
   const AttendPlace at = attend_place(p, row, h);
   T* out = static_cast<T*>(p.out) + at.out + d;
@@ -218,7 +221,7 @@ __device__ __forceinline__ void attend_write(const P& p, int row, int h, int d, 
   for (int i = 0; i < 4; ++i)
     if (d + i < p.dim) out[i] = from_float<T>(x[i] * r);
   if (d == 0 && p.lse) p.lse[at.lse] = l == 0.0f ? -CUDART_INF_F : (top + log2f(l)) * CUDART_LN2_F;
-  if (d == 0) attend_note(p, row, h, top, l);
+  if (NOTE && d == 0) attend_note(p, row, h, top, l);
 }
 
 // A segment's kv head and its query heads [head0, head0 + heads).
@@ -409,9 +412,10 @@ __device__ __forceinline__ void attend_finish_team(const AttendParams& p, const 
 
 // Joins the parts of query head q of a split row: WARPS warps take every
 // WARPS-th run of 8 parts, a lane 4 elements of the head (and 128 further).
-template <class T, int WARPS, class P>
+template <class T, int WARPS, bool NOTE, class P>
 __device__ __forceinline__ void attend_join(const P& p, int task, float (*s_state)[CMD_CACHE_MAX_DIM + 4]) {
   constexpr int kAtOnce = 8;
+  constexpr bool kVoid = !std::is_same<P, AttendParams>::value;  // (attend_void may be true)
   const int lane = threadIdx.x & 31, warp = WARPS == 1 ? 0 : threadIdx.x >> 5;
   const AttendSplit split = p.splits[task / p.block_heads];
   const int q = task % p.block_heads;
@@ -458,7 +462,7 @@ __device__ __forceinline__ void attend_join(const P& p, int task, float (*s_stat
           add_scaled(o, po[k], b);
         }
     }
-    if (empty) top = CUDART_NAN_F;  // (a maximum is never that)
+    if (kVoid && empty) top = CUDART_NAN_F;  // (a maximum is never that)
     if constexpr (WARPS > 1) {
       if (mine) {
         *reinterpret_cast<float4*>(&s_state[warp][d]) = o;
@@ -474,7 +478,7 @@ __device__ __forceinline__ void attend_join(const P& p, int task, float (*s_stat
         for (int t = 0; t < WARPS; ++t) {
           const float x = s_state[t][CMD_CACHE_MAX_DIM];
           top = fmaxf(top, x);
-          empty = empty || x != x;
+          if (kVoid) empty = empty || x != x;
         }
         l = 0.0f;
         o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -488,17 +492,17 @@ __device__ __forceinline__ void attend_join(const P& p, int task, float (*s_stat
       // (a second run of dims reads the m and l that the first wrote, unchanged)
     }
     if (empty) l = 0.0f;
-    if (warp == 0 && mine) attend_write<T>(p, split.row, h.head0 + q, d, top, l, o);
+    if (warp == 0 && mine) attend_write<T, NOTE>(p, split.row, h.head0 + q, d, top, l, o);
   }
 }
 
-template <class T, int WARPS, class P>
+template <class T, int WARPS, bool NOTE, class P>
 __global__ void __launch_bounds__(WARPS == 1 ? 256 : WARPS * 32) attend_join_kernel(const __grid_constant__ P p) {
   __shared__ __align__(16) float s_state[WARPS == 1 ? 1 : WARPS][CMD_CACHE_MAX_DIM + 4];
   wait_for_previous();
   let_next_start();
   const int task = WARPS == 1 ? blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
-  if (task < p.tasks) attend_join<T, WARPS>(p, task, s_state);
+  if (task < p.tasks) attend_join<T, WARPS, NOTE>(p, task, s_state);
 }
 
 // CTAs of the teams of a launch of tiles of `tile` tokens, 0 for none: up to 8
@@ -553,8 +557,13 @@ cudaError_t attend_launch(K kernel, P p, int start_units, int ctas, int threads,
   p.tasks = lists * p.block_heads;
   cudaError_t e = launch_chained(kernel, ctas, threads, (size_t)smem, stream, p);
   if (e != cudaSuccess || (int64_t)p.columns * p.page.d <= tile) return e;  // (a row of one tile is never split)
-  if (lists * 16 <= ctas) return launch_chained(attend_join_kernel<T, 16, P>, p.tasks, 512, 0, stream, p);
-  return launch_chained(attend_join_kernel<T, 1, P>, (p.tasks + 7) / 8, 256, 0, stream, p);
+  const auto join = [&](auto note) {
+    if (lists * 16 <= ctas) return launch_chained(attend_join_kernel<T, 16, note, P>, p.tasks, 512, 0, stream, p);
+    return launch_chained(attend_join_kernel<T, 1, note, P>, (p.tasks + 7) / 8, 256, 0, stream, p);
+  };
+  // (of one token's attention the maxima and sums are seldom wanted, and the join that may note them spills registers)
+  if (std::is_same<P, AttendParams>::value && !p.stats) return join(std::integral_constant<bool, !std::is_same<P, AttendParams>::value>());
+  return join(std::true_type());
 }
 
 // A score in powers of two from a dot product.
