@@ -4,9 +4,12 @@
 // A thread holds R query rows by 2 tokens of the scores, and R rows by 4 dims
 // (and every 64th further) of the output; 16 threads share a row, and the two
 // halves of a warp 2 R rows, so that a row's maximum, sum and weights stay in
-// its warp. Products are binary32 multiply-adds: the tensor units take 32-bit
-// numbers at three products of 11 bits each, which is no more than the
-// multiply-adds' rate at the warp level.
+// its warp. Products are binary32 multiply-adds: the tensor units would take a
+// 32-bit number as a sum of ones of 11 bits, whose products leave 2^-21 of a
+// score, and scores come to weights as powers. 12 rows of 13 drafts, up to 2999
+// tokens, window 1100, 16 heads of 80: 33 us of the call's 39 (its bytes: 5.5),
+// bound by the latency between a tile's steps (issue slots 44%, 16 warps on an
+// SM: registers and stages are full).
 #include "cache_attend_ring.cuh"
 #include "cache_drafts.cuh"
 

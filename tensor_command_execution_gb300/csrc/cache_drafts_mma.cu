@@ -1,5 +1,16 @@
 // cache_drafts_mma.cu - attention of drafted tokens over a paged cache of
-// 16-bit numbers on the warp-level tensor instructions.
+// 16-bit numbers on the warp-level tensor instructions: for heads of more than
+// 128 dims, whose scores and output do not fit tensor memory beside each other,
+// and for rows that are not whole 16-byte vectors. (cache_drafts_tc.cu has the
+// others.)
+//
+// A tile of 64 tokens lies in shared memory, keys and values, the next one on
+// its way; a warp has 16 query rows by some of the tile's tokens, its scores and
+// its output in registers, and the online softmax of its rows; warps of the same
+// rows are joined at a segment's end. Weights are sums of two 16-bit numbers, as
+// in cache_attend_mma.cu. Bound by latency: 24 rows of 16 drafts of up to 374
+// tokens, 112 query heads on 16 kv heads of 192 dims take 130 us (its bytes 9),
+// with 8 warps on an SM, whose registers are full.
 #include "cache_attend_ring.cuh"
 #include "cache_drafts.cuh"
 #include "cache_mma.cuh"

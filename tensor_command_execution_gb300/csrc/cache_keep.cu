@@ -23,7 +23,8 @@ __device__ __forceinline__ int pages_of(const KeepParams& p, int n) { return (in
 // ---- the accepted branch ---------------------------------------------------------
 // A warp walks a row's tree: each lane holds every 32nd draft, and a step is a
 // minimum over the drafts that go on from the present one with the token that
-// the model chose there. Bound by the steps' latency.
+// the model chose there. Bound by the steps' latency, one after another (16 rows
+// of 24 drafts 2.1 us, 512 of 256 3.8).
 constexpr int kPathRows = 4;
 
 __global__ void __launch_bounds__(kPathRows * 32) path_kernel(const __grid_constant__ PathParams p) {
@@ -170,6 +171,9 @@ __device__ __forceinline__ void release_pages(const KeepParams& p, int row, int 
 // A CTA takes some pieces of a token (16 bytes each where all rows allow it) of
 // one row in one pool, a thread one piece of every accepted token, in order.
 // Where the tokens lie is worked out once for the CTA, all at the same time.
+// 61 rows of 64 drafts in 32 pools of 8 heads of 128 dims: 14 us with the plan
+// (18.8 MB read and as many written: 5.6), the chain of plan, path, tables and
+// data; from Python 52, of which 24 are the caller's 32 views of its pools.
 constexpr int kAcceptThreads = 128;
 
 template <class U>
@@ -221,7 +225,8 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const __grid_con
 // all keys; the few with the same first bits are then gathered, and its others
 // come from histograms of them. Keys are read once where they fit in shared
 // memory; in the last pass each warp writes the kept ones of its run of tokens
-// behind those of the runs before.
+// behind those of the runs before. Bound by instructions (issue slots 65%) and by
+// lists to a CTA: 256 lists of 20011 to 32768 weights 49 us, their 27 MB 4.
 constexpr int kSelectThreads = 1024, kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kCached = 44 * 1024;  // keys
@@ -409,7 +414,9 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
 // is that the team has read its chunks before any of them is written: a barrier
 // of the team. While a chunk's data is on its way, the next one's places are
 // looked up. (A lone CTA takes 2 us for 256 tokens; CTAs without a row to cut cost
-// as much as they are many, so that teams stand where the lists are few.)
+// as much as they are many, so that teams stand where the lists are few.) 4 rows'
+// 4096 of up to 32768 tokens in 8 layers of 8 heads of 128 dims: 192 us, 1.08 GB
+// read and written, 84% of the copy peak.
 constexpr int kMoveThreads = kEvictMoveThreads, kMoveAtOnce = kEvictMoveAtOnce;
 
 // tokens: of a chunk (threads / pieces * kMoveAtOnce); from, to: their places,

@@ -50,8 +50,9 @@ inline cudaError_t pool_maps(int dtype, const DraftParams& d, TcParams* out) {
   return cudaSuccess;
 }
 
-// A wait that gives up (for the whole CTA, whose word it sets) after kPatience. (The clock is read
-// now and then only: a read takes about as long as a wait should.)
+// A wait that gives up (for the whole CTA, whose word it sets) after kPatience.
+// (The clock is read now and then only: a read takes about as long as a wait
+// should.)
 __device__ __forceinline__ void wait(uint32_t& stop_word, uint32_t bar, uint32_t parity) {
   volatile uint32_t* stop = &stop_word;
   uint64_t t0 = 0;

@@ -8,7 +8,11 @@
 // no other thread. (Keeping the scores instead would cost 8 bytes for each token
 // and query row, more than the keys' 2 dim bytes from dim / 4 rows on.) Two
 // groups of four warps take turns, as in cache_drafts_tc.cu. Where a kv head has
-// more query rows, so many each are a launch, one after another.
+// more query rows, so many each are a launch, one after another. No unit
+// is full (issue slots 40%, tensor units 14%): a group's loads of scores, its
+// exponentials and its turn follow one another, and the slowest CTA counts. Two
+// rows of 65536 and 30011 tokens, 32 drafts, 32 query heads on 8 kv heads of 64
+// dims: 47 us, for 98 MB of keys 15.
 #include <type_traits>
 
 #include "cache_tc.cuh"
