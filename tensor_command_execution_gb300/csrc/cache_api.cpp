@@ -1003,12 +1003,23 @@ extern "C" cmd_status cmd_attention_drafts(const cmd_drafts_args* args, void* cu
     const int es = elem_size(a.q.dtype);
     const auto pieces = [&](int n) { return dim * es % n == 0 && vector_rows(a.k_cache, n) && vector_rows(a.v_cache, n); };
     const int copy = pieces(16) ? 16 : pieces(4) ? 4 : 0;
-    const bool one = drafts == 1 && !has_parents, tc = copy == 16 && es == 2 && dim <= 128;
-    const bool kept = one && has_weights && tokens > 0 && copy == 16 && es == 2 && (__int128)rows * heads * tokens * 4 <= kMostScores;
+    const bool one = drafts == 1;
+    // Many short rows of few queries take the warp-level instructions: a segment of the CTA-wide ones costs 7 us, however
+    // short. 16-bit, 8 kv heads of 128 dims, rows of 1 to so many tokens, CTA-wide and warp-level:
+    //   200 rows, 16 query rows to a kv head:  30 tokens 90 and 59 us, 120 90 and 67, 500 112 and 87
+    //    40 rows, 16 query rows:              120 tokens 28 and 24,    500 34 and 30, 1500 40 and 40
+    //   200 rows, 32 query rows:               30 tokens 93 and 81,    120 100 and 93, 500 116 and 127
+    //   200 rows, 64 query rows:               30 tokens 97 and 130;   64 rows of 4096 tokens, 16 query rows 186 and 265
+    const int64_t queries = kv > 0 ? drafts * (heads / kv) : 0;
+    const auto few = [&](int64_t most16, int64_t most32) { return tokens <= (queries <= 16 ? most16 : queries <= 32 ? most32 : 0); };
+    const bool vectors = copy == 16 && es == 2, tc = !one && vectors && dim <= 128 && !few(1024, 256);
+    const bool kept = one && has_weights && tokens > 0 && vectors && (__int128)rows * heads * tokens * 4 <= kMostScores;
     float* scores = kept ? reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(stats) + round_up(rows * heads * 8, 16)) : nullptr;
     p.scores_tokens = tokens;
-    // (the weights' kernel takes heads of up to 256 dims, the attention's of up to 128)
-    const bool tma = copy == 16 && es == 2 && (tc || has_weights) && !(one && (kept || !has_weights)) && cmdx::drafts_tma_fits(a.k_cache.sizes[1], a.k_cache.sizes, a.k_cache.strides, a.v_cache.strides) &&
+    // The weights of those, with the attention: 200 rows, 16 query rows, 120 tokens 143 and 111 us, 500 175 and 174; 40 rows
+    // 53 and 50, of 1000 tokens 58 and 65. (Their CTA-wide kernel takes heads of up to 256 dims, the attention's of up to 128.)
+    const bool weigh_tc = vectors && has_weights && !kept && !(dim <= 128 && few(512, 256));
+    const bool tma = (tc || weigh_tc) && cmdx::drafts_tma_fits(a.k_cache.sizes[1], a.k_cache.sizes, a.k_cache.strides, a.v_cache.strides) &&
                      in_device_memory(a.k_cache.ptr) && in_device_memory(a.v_cache.ptr);
     if (one) {
       attend_blocks(p, es, copy);
@@ -1034,6 +1045,7 @@ extern "C" cmd_status cmd_attention_drafts(const cmd_drafts_args* args, void* cu
       p.weights = has_weights ? static_cast<float*>(a.weights.ptr) + r * a.weights.strides[0] : nullptr;
       p.stats = stats ? stats + r * drafts * heads : nullptr;
       p.scores = scores ? scores + r * heads * tokens : nullptr;
+      if (one) p.roots = p.parents, p.root_st = p.parent_st[0];
       const cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
       cudaError_t e = one          ? attend_one(a.q.dtype, copy, p, stream)
                       : es == 4    ? (copy == 16 ? cmdx::drafts_f32_launch16 : cmdx::drafts_f32_launch4)(p, stream)
@@ -1044,7 +1056,7 @@ extern "C" cmd_status cmd_attention_drafts(const cmd_drafts_args* args, void* cu
       if (e == cudaSuccess && has_weights)
         e = kept         ? cmdx::weigh_scores_launch(p, stream)
             : es == 4    ? (copy == 16 ? cmdx::weigh_f32_launch16 : cmdx::weigh_f32_launch4)(p, stream)
-            : tma        ? cmdx::weigh_tma_launch(a.q.dtype, p, stream)
+            : weigh_tc && tma ? cmdx::weigh_tma_launch(a.q.dtype, p, stream)
             : copy == 16 ? cmdx::weigh_mma_launch16(a.q.dtype, p, stream)
             : copy == 4  ? cmdx::weigh_mma_launch4(a.q.dtype, p, stream)
                          : cmdx::weigh_mma_launch0(a.q.dtype, p, stream);

@@ -45,12 +45,20 @@ struct AttendRows {
   }
 };
 
-// Row r's length, held to its table.
+// Row r's length, held to its table; none where its one draft is padding.
 __device__ __forceinline__ int attend_length(const AttendParams& p, int r) {
-  const int n = p.lengths[r * p.len_st], most = p.columns * (int)p.page.d;
-  if (n >= 0 && n <= most) return n;
-  report(p.status, CMD_CACHE_BAD_INDEX);
-  return n < 0 ? 0 : most;
+  int n = p.lengths[r * p.len_st];
+  const int most = p.columns * (int)p.page.d;
+  if (n < 0 || n > most) {
+    report(p.status, CMD_CACHE_BAD_INDEX);
+    n = n < 0 ? 0 : most;
+  }
+  if (p.roots && n > 0) {
+    const int parent = p.roots[r * p.root_st];
+    if (parent >= 0) report(p.status, CMD_CACHE_BAD_INDEX);
+    if (parent != -1) n = 0;
+  }
+  return n;
 }
 
 // Fills s for tiles of `tile` tokens (aligned to the row's start); all

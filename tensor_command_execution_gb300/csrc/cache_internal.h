@@ -106,6 +106,8 @@ struct AttendParams {
   float2* stats;       // optional: a row's maximum and sum for each head, [rows][kv_heads * group]
   float* scores;       // optional (16-bit types, copies of 16 bytes): every token's, [rows][kv_heads][scores_tokens][group]
   int64_t scores_tokens;
+  const int32_t* roots;  // optional: a row where this is not -1 is as one without a token
+  int64_t root_st;
   uint8_t q_pairs;     // q rows may be read two 16-bit elements at a time
 };
 
@@ -127,7 +129,8 @@ constexpr int kAttendHeads = 8, kAttendMmaHeads = 16;
 // The attention above with drafts * (query heads to a kv head) rows in the
 // place of a kv head's query heads: `group` counts them, draft outermost.
 // lengths include the drafts; `window` reaches from the last token back to the
-// first that any draft sees.
+// first that any draft sees. One draft is one token's attention, of the rows
+// where its parent is -1 (roots).
 struct DraftParams : AttendParams {
   int32_t drafts;
   FastDiv32 per;              // by query heads to a kv head

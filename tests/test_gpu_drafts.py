@@ -404,6 +404,40 @@ def test_weights_of_one_token(kind, hq, hk, dim, page):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("drafts,hq,hk,dim,page", [(2, 4, 4, 64, 16), (8, 4, 2, 128, 8), (5, 3, 1, 72, 3), (16, 4, 2, 128, 16), (3, 16, 2, 80, 24),
+                                                   (31, 1, 1, 64, 128)])
+def test_few_queries_of_long_tables(kind, drafts, hq, hk, dim, page):
+    """Up to 32 query rows to a kv head, in tables long enough for the CTA-wide instructions, and in shorter ones."""
+    _check(kind, [0, 1, 100, 700, -1, 1300], drafts, hq, hk, dim, page, tree="padded")
+    _check(kind, [1300, 20], drafts, hq, hk, dim, page, tree="tree", softcap=5.0, window=60, junk=float("nan"))
+    _check(kind, [0, 1, 100, -1, 200], drafts, hq, hk, dim, page, tree="padded")
+    _check(kind, [200, 20], drafts, hq, hk, dim, page, tree="tree", softcap=5.0, window=60, junk=float("nan"))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("hq,hk,dim,page", [(8, 2, 128, 16), (3, 3, 33, 8), (20, 1, 256, 1)])
+def test_one_draft_with_parents(kind, hq, hk, dim, page):
+    """-1 is one token's attention, exactly; less, or a parent that does not exist (reported), is a row without any."""
+    totals = [700, 20, 1, 0, 40, 300]
+    c = U.Cache(kind, totals, hk, dim, page)
+    q = _randn(6, 1, hq, dim, kind=kind, seed=1)
+    parents, status = _i32([[-1], [-2], [-1], [-1], [0], [-2147483648]]), torch.zeros(1, dtype=torch.int32, device="cuda")
+    tokens = c.tables.shape[1] * page
+    w, plain = (torch.rand(6, hk, tokens, generator=torch.Generator(device="cuda").manual_seed(0), device="cuda") for _ in range(2))
+    start = w.clone()
+    out, lse = T.attention_drafts(q, c.k, c.v, c.tables, c.lengths, parents=parents, weights=w, return_lse=True, status=status)
+    with pytest.raises(T.CmdError):
+        T.cache_status(status)
+    want, want_lse = T.attention_drafts(q, c.k, c.v, c.tables, c.lengths, weights=plain, return_lse=True)
+    assert torch.equal(want[:, 0], T.attention_decode(q[:, 0], c.k, c.v, c.tables, c.lengths))
+    for r in range(6):
+        if r in (0, 2):
+            assert torch.equal(out[r], want[r]) and torch.equal(lse[r], want_lse[r]) and torch.equal(w[r], plain[r])
+        else:
+            assert not bool(out[r].any()) and bool((lse[r] == -math.inf).all()) and torch.equal(w[r], start[r])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
 @pytest.mark.parametrize("drafts,hq,hk,dim,page", [(16, 28, 2, 192, 8), (5, 8, 2, 256, 16), (40, 8, 1, 136, 64), (2, 4, 4, 200, 24), (9, 30, 1, 256, 8)])
 def test_weights_of_wide_heads(kind, drafts, hq, hk, dim, page):
     """Heads of more than 128 dims, with more query rows to a head than a launch takes."""
