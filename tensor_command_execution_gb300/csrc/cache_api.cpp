@@ -1024,7 +1024,10 @@ extern "C" cmd_status cmd_attention_drafts(const cmd_drafts_args* args, void* cu
     if (one) {
       attend_blocks(p, es, copy);
     } else {
-      const int most = tc ? cmdx::kDraftTcRows : cmdx::kDraftRows;
+      // 32-bit rows: blocks of 16 take two sevenths of the time of blocks of 64, full or not (12 rows of up to 2999 tokens, 16
+      // heads of 80: 75 and 261 us), and go over the keys as often as there are blocks.
+      const bool small = es == 4 && (p.group + 15) / 16 * 2 < (p.group + 63) / 64 * 7;
+      const int most = tc ? cmdx::kDraftTcRows : small ? 16 : cmdx::kDraftRows;
       p.blocks = (p.group + most - 1) / most;
       p.block_heads = (p.group + p.blocks - 1) / p.blocks;
     }

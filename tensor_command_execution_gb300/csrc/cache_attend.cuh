@@ -399,12 +399,12 @@ __device__ __forceinline__ void attend_join_team(const P& p, const AttendSegment
 
 // Ends a team's row: the warps' states (as in attend_finish) go to `part` of
 // each CTA, and are joined. Every thread of the team calls it.
-template <class T, int WARPS>
-__device__ __forceinline__ void attend_finish_team(const AttendParams& p, const AttendSegment& g, const AttendHeads& h,
-                                                   const float* state, int warp_pitch, int pitch, float* part) {
+template <class T, int WARPS, int THREADS = WARPS * 32, class P>
+__device__ __forceinline__ void attend_finish_team(const P& p, const AttendSegment& g, const AttendHeads& h, const float* state,
+                                                   int warp_pitch, int pitch, float* part) {
   const int part_pitch = attend_pitch(p.dim), quads = part_pitch / 4 - 1;
   __syncthreads();  // the warps' states are complete
-  for (int i = threadIdx.x; i < h.heads * quads; i += WARPS * 32) {
+  for (int i = threadIdx.x; i < h.heads * quads; i += THREADS) {
     const int q = i / quads, d = 4 * (i - q * quads);
     float top, l;
     const float4 o = attend_merged<WARPS>(state + q * pitch, warp_pitch, pitch, d, &top, &l);
@@ -415,7 +415,7 @@ __device__ __forceinline__ void attend_finish_team(const AttendParams& p, const 
     }
     *reinterpret_cast<float4*>(x + d) = o;
   }
-  attend_join_team<T, WARPS * 32>(p, g, h, part);
+  attend_join_team<T, THREADS>(p, g, h, part);
 }
 
 // Joins the parts of query head q of a split row: WARPS warps take every

@@ -40,7 +40,7 @@ struct Shape {
   static constexpr int kRest = (kWeights + kRows * kWeightPitch) * 4;  // bytes (the sets' weights side by side)
   static constexpr int kSmem = kRest + (int)(2 * sizeof(DraftTile<kTile>) + sizeof(DraftTree) + sizeof(AttendRows));
   static constexpr int kStatePitch = attend_pitch(DP);
-  static_assert(kSets * kRows * kStatePitch <= 2 * kStage, "the states fit the stages");
+  static_assert((kSets + 1) * kRows * kStatePitch <= 2 * kStage, "the states and a team's part fit the stages");
   static constexpr int kCtas = kSmem <= 113 * 1024 ? 2 : 1;  // of an SM
 };
 
@@ -167,15 +167,23 @@ __global__ void __launch_bounds__((Shape<DP, R>::kThreads), (Shape<DP, R>::kCtas
   wait_for_previous();
   let_next_start();
   AttendShare share;
-  if (!attend_begin<float>(p, s_rows, kTile, &share)) return;
-  for (AttendSegment g = attend_first(p, s_rows, share, kTile); g.tiles; g = attend_next(p, s_rows, share, g, kTile)) {
+  AttendSegment g;
+  if (p.team) {
+    g = attend_team(p, kTile, &share);
+  } else {
+    if (!attend_begin<float>(p, s_rows, kTile, &share)) return;
+    g = attend_first(p, s_rows, share, kTile);
+  }
+  for (; p.team || g.tiles; g = attend_next(p, s_rows, share, g, kTile)) {
     const AttendHeads heads = attend_heads(p, g.group);
     const int q0 = heads.head0 - heads.kv * p.group, base = g.n - p.drafts;
-    draft_place(p, s_tile[0], draft_look(p, g, g.tile0, kTile, true), heads.kv);
-    draft_place(p, s_tile[1], draft_look(p, g, g.tile0 + 1, kTile, g.tiles > 1), heads.kv);
-    load_queries<DP, kThreads, S::kRows>(p, s_mem + S::kQueries, g.row, heads.kv, q0, heads.heads, steps);
-    draft_tree<kThreads>(p, s_tree, g.row, base);  // (with barriers: the tiles' places are complete)
-    copy_tile<DP, kThreads, true>(p, s_tile[0], s_mem, steps);
+    if (g.tiles) {  // (none: a team's CTA that has none of a short row)
+      draft_place(p, s_tile[0], draft_look(p, g, g.tile0, kTile, true), heads.kv);
+      draft_place(p, s_tile[1], draft_look(p, g, g.tile0 + 1, kTile, g.tiles > 1), heads.kv);
+      load_queries<DP, kThreads, S::kRows>(p, s_mem + S::kQueries, g.row, heads.kv, q0, heads.heads, steps);
+      draft_tree<kThreads>(p, s_tree, g.row, base);  // (with barriers: the tiles' places are complete)
+      copy_tile<DP, kThreads, true>(p, s_tile[0], s_mem, steps);
+    }
 
     int draft[R];
     float o[R][NJ][4], m[R], l[R];
@@ -245,7 +253,7 @@ __global__ void __launch_bounds__((Shape<DP, R>::kThreads), (Shape<DP, R>::kCtas
     for (int r = 0; r < R; ++r) {
 #pragma unroll
       for (int b = 1; b < 16; b <<= 1) l[r] += __shfl_xor_sync(~0u, l[r], b);
-      const bool live = r0 + r < heads.heads && s_tree.from[draft[r]] != kNever;
+      const bool live = g.tiles && r0 + r < heads.heads && s_tree.from[draft[r]] != kNever;
       float* x = s_mem + (set * S::kRows + r0 + r) * S::kStatePitch;
       if (tx == 0) {
         x[S::kStatePitch - 4] = live ? m[r] : -CUDART_INF_F;
@@ -256,6 +264,11 @@ __global__ void __launch_bounds__((Shape<DP, R>::kThreads), (Shape<DP, R>::kCtas
         const float4 y = live ? make_float4(o[r][j][0], o[r][j][1], o[r][j][2], o[r][j][3]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         *reinterpret_cast<float4*>(x + 4 * tx + 64 * j) = y;
       }
+    }
+    if (p.team) {
+      attend_finish_team<float, S::kSets, kThreads>(p, g, heads, s_mem, S::kRows * S::kStatePitch, S::kStatePitch,
+                                                    s_mem + S::kSets * S::kRows * S::kStatePitch);
+      return;
     }
     attend_finish<float, S::kSets, kThreads>(p, share, g, heads, s_mem, S::kRows * S::kStatePitch, S::kStatePitch);
   }
@@ -346,7 +359,7 @@ cudaError_t launch(bool weights, DraftParams p, cudaStream_t stream) {
   if (!weights) {
     const cudaError_t e = allow_smem(drafts_f32_kernel<DP, R>, S::kSmem, ready);
     if (e != cudaSuccess) return e;
-    return attend_launch<float>(drafts_f32_kernel<DP, R>, p, 2, 152 * S::kCtas, S::kThreads, S::kSmem, kTile, stream, false);
+    return attend_launch<float>(drafts_f32_kernel<DP, R>, p, 2, 152 * S::kCtas, S::kThreads, S::kSmem, kTile, stream);
   }
   p.blocks = p.sides = 1;
   p.start_units = 0;

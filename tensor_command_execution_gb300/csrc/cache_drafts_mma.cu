@@ -42,7 +42,8 @@ struct Shape {
   static constexpr int kRest = kQueries + kRows * kPitch;
   static constexpr int kSmem = kRest + (int)(2 * sizeof(DraftTile<kTile>) + sizeof(DraftTree) + sizeof(AttendRows));
   static constexpr int kStatePitch = attend_pitch(DP);
-  static_assert(kSets * kRows * kStatePitch * 4 <= 2 * kStage, "the states fit the stages");
+  static constexpr bool kTeams = kWarps == 4;      // (a team's part needs room beside the states)
+  static_assert((kSets + (kTeams ? 1 : 0)) * kRows * kStatePitch * 4 <= 2 * kStage, "the states fit the stages");
   static constexpr int kCtas = kSmem <= 113 * 1024 ? 2 : 1;  // of an SM
 };
 
@@ -163,15 +164,23 @@ __global__ void __launch_bounds__((Shape<DP, MT>::kThreads), (Shape<DP, MT>::kCt
   wait_for_previous();
   let_next_start();
   AttendShare share;
-  if (!attend_begin<T>(p, s_rows, kTile, &share)) return;
-  for (AttendSegment g = attend_first(p, s_rows, share, kTile); g.tiles; g = attend_next(p, s_rows, share, g, kTile)) {
+  AttendSegment g;
+  if (S::kTeams && p.team) {
+    g = attend_team(p, kTile, &share);
+  } else {
+    if (!attend_begin<T>(p, s_rows, kTile, &share)) return;
+    g = attend_first(p, s_rows, share, kTile);
+  }
+  for (; (S::kTeams && p.team) || g.tiles; g = attend_next(p, s_rows, share, g, kTile)) {
     const AttendHeads heads = attend_heads(p, g.group);
     const int q0 = heads.head0 - heads.kv * p.group, base = g.n - p.drafts;
-    draft_place(p, s_tile[0], draft_look(p, g, g.tile0, kTile, true), heads.kv);
-    draft_place(p, s_tile[1], draft_look(p, g, g.tile0 + 1, kTile, g.tiles > 1), heads.kv);
-    load_queries<T, DP, kThreads, S::kRows>(p, s_mem + S::kQueries, g.row, heads.kv, q0, heads.heads, steps);
-    draft_tree<kThreads>(p, s_tree, g.row, base);  // (with barriers: the tiles' places are complete)
-    copy_tile<T, DP, kThreads, true>(p, s_tile[0], s_mem, steps);
+    if (g.tiles) {  // (none: a team's CTA that has none of a short row)
+      draft_place(p, s_tile[0], draft_look(p, g, g.tile0, kTile, true), heads.kv);
+      draft_place(p, s_tile[1], draft_look(p, g, g.tile0 + 1, kTile, g.tiles > 1), heads.kv);
+      load_queries<T, DP, kThreads, S::kRows>(p, s_mem + S::kQueries, g.row, heads.kv, q0, heads.heads, steps);
+      draft_tree<kThreads>(p, s_tree, g.row, base);  // (with barriers: the tiles' places are complete)
+      copy_tile<T, DP, kThreads, true>(p, s_tile[0], s_mem, steps);
+    }
 
     // this thread's two query rows
     int draft[2];
@@ -180,7 +189,7 @@ __global__ void __launch_bounds__((Shape<DP, MT>::kThreads), (Shape<DP, MT>::kCt
     for (int e = 0; e < 2; ++e) {
       const int r = rows_of * 16 + gr + 8 * e;
       draft[e] = (int)fast_div32(p.per, (uint32_t)(q0 + min(r, heads.heads - 1)));
-      live[e] = r < heads.heads && s_tree.from[draft[e]] != kNever;
+      live[e] = g.tiles && r < heads.heads && s_tree.from[draft[e]] != kNever;
     }
     float o[KS][2][4], m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -328,6 +337,11 @@ __global__ void __launch_bounds__((Shape<DP, MT>::kThreads), (Shape<DP, MT>::kCt
           *reinterpret_cast<float2*>(x + 16 * k + 8 * b + tc) = y;
         }
     }
+    if (S::kTeams && p.team) {
+      attend_finish_team<T, S::kSets, kThreads>(p, g, heads, reinterpret_cast<float*>(s_mem), S::kRows * S::kStatePitch, S::kStatePitch,
+                                                reinterpret_cast<float*>(s_mem) + S::kSets * S::kRows * S::kStatePitch);
+      return;
+    }
     attend_finish<T, S::kSets, kThreads>(p, share, g, heads, reinterpret_cast<float*>(s_mem), S::kRows * S::kStatePitch,
                                          S::kStatePitch);
   }
@@ -437,7 +451,7 @@ cudaError_t launch(const DraftParams& p, cudaStream_t stream) {
   static PerDevice ready;  // (static storage: zero before first use)
   const cudaError_t e = allow_smem(drafts_mma_kernel<T, DP, MT>, S::kSmem, ready);
   if (e != cudaSuccess) return e;
-  return attend_launch<T>(drafts_mma_kernel<T, DP, MT>, p, 2, 152 * S::kCtas, S::kThreads, S::kSmem, kTile, stream, false);
+  return attend_launch<T>(drafts_mma_kernel<T, DP, MT>, p, 2, 152 * S::kCtas, S::kThreads, S::kSmem, kTile, stream, S::kTeams);
 }
 template <class T, int DP, int MT>
 cudaError_t weigh(DraftParams p, cudaStream_t stream) {
