@@ -1016,7 +1016,7 @@ extern "C" cmd_status cmd_attention_drafts(const cmd_drafts_args* args, void* cu
     const bool kept = one && has_weights && tokens > 0 && vectors && (__int128)rows * heads * tokens * 4 <= kMostScores;
     float* scores = kept ? reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(stats) + round_up(rows * heads * 8, 16)) : nullptr;
     p.scores_tokens = tokens;
-    // The weights of those, with the attention: 200 rows, 16 query rows, 120 tokens 143 and 111 us, 500 175 and 174; 40 rows
+    // The weights of those, with the attention: 200 rows, 16 query rows, 120 tokens 143 and 109 us, 500 175 and 151; 40 rows
     // 53 and 50, of 1000 tokens 58 and 65. (Their CTA-wide kernel takes heads of up to 256 dims, the attention's of up to 128.)
     const bool weigh_tc = vectors && has_weights && !kept && !(dim <= 128 && few(512, 256));
     const bool tma = (tc || weigh_tc) && cmdx::drafts_tma_fits(a.k_cache.sizes[1], a.k_cache.sizes, a.k_cache.strides, a.v_cache.strides) &&

@@ -307,9 +307,14 @@ __global__ void __launch_bounds__((Shape<DP, R>::kThreads), 2) weigh_f32_kernel(
       if (i + 1 < g.tiles) copy_wait<1>();
       else copy_wait<0>();
       const int t0 = (g.tile0 + i) * kTile;
+      const bool mine = threadIdx.x < kTile && s_tile[buffer].k[threadIdx.x] >= 0;
+      const float before = mine ? weights[t0 + threadIdx.x] : 0.0f;  // (on its way while the scores are worked out)
       float sum[N] = {};
       for (int q0 = 0; q0 < p.group; q0 += S::kRows) {
         const int n = min(S::kRows, p.group - q0);
+        float2 of_row[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) of_row[r] = r0 + r < n ? stats[q0 + r0 + r] : make_float2(0.0f, 0.0f);
         if (i == 0 || p.group > S::kRows) {  // (one block stays where it is)
           __syncthreads();
           load_queries<DP, kThreads, S::kRows>(p, s_mem + kQueries, g.row, kv, q0, n, steps);
@@ -321,7 +326,7 @@ __global__ void __launch_bounds__((Shape<DP, R>::kThreads), 2) weigh_f32_kernel(
         scores<DP, R, N>(s, s_mem + kQueries + r0 * S::kPitch, s_mem + buffer * S::kKeys + (set * kTokens + tx) * S::kPitch, steps);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          const float2 x = r0 + r < n ? stats[q0 + r0 + r] : make_float2(0.0f, 0.0f);
+          const float2 x = of_row[r];
           const float w = x.y == 0.0f ? 0.0f : 1.0f / x.y;
           const int draft = (int)fast_div32(p.per, (uint32_t)(q0 + min(r0 + r, n - 1)));
 #pragma unroll
@@ -339,11 +344,11 @@ __global__ void __launch_bounds__((Shape<DP, R>::kThreads), 2) weigh_f32_kernel(
         if ((threadIdx.x & 16) == 0) s_sum[(threadIdx.x >> 5) % 4][set * kTokens + tx + 16 * e] = sum[e];
       }
       __syncthreads();  // (the tile is read, and the sums are complete)
-      if (threadIdx.x < kTile && s_tile[buffer].k[threadIdx.x] >= 0) {
+      if (mine) {
         float x = s_sum[0][threadIdx.x];
 #pragma unroll
         for (int j = 1; j < 4; ++j) x += s_sum[j][threadIdx.x];
-        weights[t0 + threadIdx.x] += x;
+        weights[t0 + threadIdx.x] = before + x;
       }
       __syncwarp();
       draft_place(p, s_tile[buffer], look, kv);
@@ -361,12 +366,13 @@ cudaError_t launch(bool weights, DraftParams p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     return attend_launch<float>(drafts_f32_kernel<DP, R>, p, 2, 152 * S::kCtas, S::kThreads, S::kSmem, kTile, stream);
   }
-  p.blocks = p.sides = 1;
-  p.start_units = 0;
+  p.blocks = 1;
+  p.start_units = 2;
+  const int ctas = attend_sides(p.kv_heads, 152 * 2, &p.sides);
   constexpr int smem = (2 * S::kKeys + S::kRows * S::kPitch) * 4 + (S::kSmem - S::kRest);
   const cudaError_t e = allow_smem(weigh_f32_kernel<DP, R>, smem, weigh_ready);
   if (e != cudaSuccess) return e;
-  return launch_chained(weigh_f32_kernel<DP, R>, 152 * 2, S::kThreads, (size_t)smem, stream, p);
+  return launch_chained(weigh_f32_kernel<DP, R>, ctas, S::kThreads, (size_t)smem, stream, p);
 }
 
 template <int R>

@@ -387,6 +387,8 @@ __global__ void __launch_bounds__((Shape<DP, MT>::kThreads), 2) weigh_mma_kernel
       if (i + 1 < g.tiles) copy_wait<1>();
       else copy_wait<0>();
       const int t0 = (g.tile0 + i) * kTile;
+      const bool mine = threadIdx.x < kTile && s_tile[buffer].k[threadIdx.x] >= 0;
+      const float before = mine ? weights[t0 + threadIdx.x] : 0.0f;  // (on its way while the scores are worked out)
       float sum[NC][2];
 #pragma unroll
       for (int j = 0; j < NC; ++j) sum[j][0] = sum[j][1] = 0.0f;
@@ -432,11 +434,11 @@ __global__ void __launch_bounds__((Shape<DP, MT>::kThreads), 2) weigh_mma_kernel
           if (gr == 0) s_sum[rows_of][set * S::kMine + 8 * j + tc + e] = sum[j][e];
         }
       __syncthreads();  // (the tile is read, and the sums are complete)
-      if (threadIdx.x < kTile && s_tile[buffer].k[threadIdx.x] >= 0) {
+      if (mine) {
         float x = s_sum[0][threadIdx.x];
 #pragma unroll
         for (int j = 1; j < MT; ++j) x += s_sum[j][threadIdx.x];
-        weights[t0 + threadIdx.x] += x;
+        weights[t0 + threadIdx.x] = before + x;
       }
       __syncwarp();
       draft_place(p, s_tile[buffer], look, kv);
@@ -455,13 +457,14 @@ cudaError_t launch(const DraftParams& p, cudaStream_t stream) {
 }
 template <class T, int DP, int MT>
 cudaError_t weigh(DraftParams p, cudaStream_t stream) {
-  p.blocks = p.sides = 1;
-  p.start_units = 0;
+  p.blocks = 1;
+  p.start_units = 2;
+  const int ctas = attend_sides(p.kv_heads, 152 * 2, &p.sides);
   constexpr int smem = Shape<DP, MT>::kSmem - 2 * Shape<DP, MT>::kKeys;
   static PerDevice ready;  // (static storage: zero before first use)
   const cudaError_t e = allow_smem(weigh_mma_kernel<T, DP, MT>, smem, ready);
   if (e != cudaSuccess) return e;
-  return launch_chained(weigh_mma_kernel<T, DP, MT>, 152 * 2, Shape<DP, MT>::kThreads, (size_t)smem, stream, p);
+  return launch_chained(weigh_mma_kernel<T, DP, MT>, ctas, Shape<DP, MT>::kThreads, (size_t)smem, stream, p);
 }
 
 template <class T, int DP>
