@@ -26,6 +26,8 @@ struct TcParams : DraftParams {
 inline cudaError_t pool_maps(int dtype, const DraftParams& d, TcParams* out) {
   TcParams& p = *out;
   static_cast<DraftParams&>(p) = d;
+  const auto encode = tensor_map_encoder();
+  if (!encode) return cudaErrorNotSupported;
   p.box = kTcTile;
   while (p.page.d % p.box) p.box /= 2;
   for (int i = 0; i < 2; ++i) {
@@ -41,7 +43,7 @@ inline cudaError_t pool_maps(int dtype, const DraftParams& d, TcParams* out) {
     const CUtensorMapL2promotion fetch = run % 256 == 0   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
                                          : run % 128 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
                                                           : CU_TENSOR_MAP_L2_PROMOTION_NONE;
-    const CUresult r = tensor_map_encoder()(
+    const CUresult r = encode(
         &p.maps[i], dtype == CMD_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
         const_cast<void*>(i == 0 ? p.k : p.v), sizes, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
         fetch, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
