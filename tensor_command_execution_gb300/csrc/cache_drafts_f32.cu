@@ -204,9 +204,10 @@ __global__ void __launch_bounds__((Shape<DP, R>::kThreads), (Shape<DP, R>::kCtas
       const DraftLook look = draft_look(p, g, g.tile0 + i + 2, kTile, i + 2 < g.tiles);
       if (i + 1 < g.tiles) copy_wait<1>();
       else copy_wait<0>();
+      // (before the barrier: draft_place writes it anew below)
+      const uint32_t here = s_tile[buffer].here[0];
       __syncthreads();
       const int t0 = (g.tile0 + i) * kTile;
-      const uint32_t here = s_tile[buffer].here[0];
       const bool masked = here != ~0u || !draft_all_seen(p, t0, t0 + kTile, base);
       const float* stage = s_mem + buffer * S::kStage;
       float s[R][N];

@@ -203,9 +203,10 @@ __global__ void __launch_bounds__((Shape<DP, MT>::kThreads), (Shape<DP, MT>::kCt
       const DraftLook look = draft_look(p, g, g.tile0 + i + 2, kTile, i + 2 < g.tiles);
       if (i + 1 < g.tiles) copy_wait<1>();
       else copy_wait<0>();
+      // (before the barrier: draft_place writes them anew below)
+      const uint32_t here0 = s_tile[buffer].here[0], here1 = s_tile[buffer].here[1];
       __syncthreads();
       const int t0 = (g.tile0 + i) * kTile;
-      const uint32_t here0 = s_tile[buffer].here[0], here1 = s_tile[buffer].here[1];
       const bool masked = (here0 & here1) != ~0u || !draft_all_seen(p, t0, t0 + kTile, base);
       bool infinite = false;  // a value that a masked weight of zero would turn to NaN
       if (masked) {
