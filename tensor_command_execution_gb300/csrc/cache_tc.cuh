@@ -90,11 +90,12 @@ struct TmaTiles {
   __device__ __forceinline__ TmaTiles(const TcParams& p_)
       : p(p_), lane(threadIdx.x % 32), boxes(kTcTile / p_.box), each(32 / boxes), slabs((p_.dim + 63) / 64), one(elected()) {}
 
-  // this lane's entry of a batch; -1: it has none
+  // this lane's entry of a batch; -1: it has none, and -2: it has one that is negative
   __device__ __forceinline__ int entry(int b) const {
     const int i = b * each + lane / boxes, t = (g.tile0 + i) * kTcTile + lane % boxes * p.box;
     if (i >= g.tiles || t >= g.n || t + p.box <= g.lo) return -1;
-    return max(p.tables[g.row * p.table_st[0] + fast_div32(p.page, (uint32_t)t) * p.table_st[1]], -2);
+    const int e = p.tables[g.row * p.table_st[0] + fast_div32(p.page, (uint32_t)t) * p.table_st[1]];
+    return e < 0 ? -2 : e;
   }
   __device__ __forceinline__ void begin(const AttendSegment& segment) {
     g = segment;

@@ -63,3 +63,13 @@ def test_masks_that_change_from_tile_to_tile(kernel):
     """Long rows whose tiles have other tokens missing each: whoever took a tile by another one's mask would be seen."""
     _check(*kernel[:1], [1900, 700, 40], *kernel[1:6], lambda j: (j * j) % 7 in (2, 4), lambda c: [-5, c.pages, 0x7fffffff, -(1 << 31)],
            columns=kernel[6], repeats=8)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_entries_of_minus_one_are_reported(kernel):
+    """... what a table holds where there is no page is no page inside a row's length either: alone, beside other bad
+    entries, as a row's first and as its last before the drafts."""
+    for where in (lambda j: j == 1, lambda j: j in (0, 4), lambda j: j % 3 == 0):
+        _check(*kernel[:1], [700, 130, 40], *kernel[1:6], where, lambda c: [-1], columns=kernel[6])
+    _check(*kernel[:1], [700, 130, 40], *kernel[1:6], lambda j: j % 4 == 0, lambda c: [-1, c.pages], columns=kernel[6])
+    _check(*kernel[:1], [700, 130, 40], *kernel[1:6], lambda j: False, lambda c: [-1], columns=kernel[6])
