@@ -30,11 +30,12 @@
  * along dim (slots outermost in a page, heads outermost, or interleaved with
  * another tensor). A sequence is a row of a page table, i32 [rows, columns]:
  * entry j is the page that holds its tokens j * page_size and on. Entries
- * past the sequence's length are never read. A page that several rows list
- * is shared; refs, i32 [pages], counts how many hold it, and a count of zero
- * makes a page free. Tables, lengths and counts live on the device and every
- * operator works on them there, so a whole generation step can be captured in
- * a CUDA graph.
+ * past the sequence's length are never read. A length is 0 to columns *
+ * page_size: one outside is reported and held to that range. A page that
+ * several rows list is shared; refs, i32 [pages], counts how many hold it, and
+ * a count of zero makes a page free. Tables, lengths and counts live on the
+ * device and every operator works on them there, so a whole generation step can
+ * be captured in a CUDA graph.
  *
  * Tensors are given as cmd_operand (a pointer the GPU can address, sizes and
  * element strides >= 0). Outputs must address distinct elements and must not
@@ -68,7 +69,7 @@ extern "C" {
 
 /* Bits of the device status word. */
 #define CMD_CACHE_BAD_PAGE 1  /* a table entry names no page of the pool; its tokens were skipped */
-#define CMD_CACHE_BAD_INDEX 2 /* a row, parent, position or length outside its range; skipped */
+#define CMD_CACHE_BAD_INDEX 2 /* a row, parent or position outside its range, skipped; a length, held to its range */
 #define CMD_CACHE_FULL_TABLE 4 /* a row would need more columns than its table has; dropped */
 #define CMD_CACHE_NO_PAGES 8  /* the pool had no free page left for a row; dropped */
 #define CMD_CACHE_SHARED_PAGE 16 /* tokens would move into a page that others hold too; left as they are */
@@ -203,8 +204,8 @@ cmd_status cmd_attention_decode(const cmd_attention_args* args, void* cuda_strea
  * draft's position is lengths[r] - drafts + its number of ancestors. Over them,
  * scores, out and lse are as in cmd_attention_decode, which this is for one
  * draft. Nothing that a draft does not see enters its output. Padding, and rows
- * of length 0, give out = 0 and lse = -infinity; so do rows whose length is out
- * of range or below `drafts` (reported).
+ * of length 0, give out = 0 and lse = -infinity; so do rows whose length is
+ * negative or below `drafts` (reported).
  *
  * weights, where given, gets the attention that each token of each row received:
  *   weights[r][h][t] += sum over the drafts and the query heads that read kv
@@ -262,12 +263,13 @@ cmd_status cmd_draft_path(const cmd_path_args* args, void* cuda_stream);
  * entries of path[r] (ascending, each below `drafts`): in every pool the j-th one
  * moves from its slot to slot lengths[r] - drafts + j, and lengths_out[r] =
  * lengths[r] - drafts + counts[r]. Pages past that are released (refs_out). Rows
- * of length 0 stay as they are. A row whose list is not as above, or whose moves
- * would meet pages that do not exist or write to one that others hold too (refs
- * above 1), keeps none of its drafts (reported); one shorter than `drafts` stays
- * as it is (reported). Pools as tensors, since parts of a page move; the same
- * sizes and element type in all of them; a model with more makes a call for each
- * CMD_CACHE_MAX_POOLS, with the same inputs. */
+ * of length 0 stay as they are. (Of a length beyond the table, which is held to it
+ * and reported, the drafts are the table's last tokens.) A row whose list is not
+ * as above, or whose moves would meet pages that do not exist or write to one
+ * that others hold too (refs above 1), keeps none of its drafts (reported); one
+ * shorter than `drafts` stays as it is (reported). Pools as tensors, since parts
+ * of a page move; the same sizes and element type in all of them; a model with
+ * more makes a call for each CMD_CACHE_MAX_POOLS, with the same inputs. */
 typedef struct cmd_accept_args {
   cmd_operand tables;       /* i32 [rows, columns], each row dense */
   cmd_operand lengths;      /* i32 [rows], drafts included; dense (as all vectors here) */
@@ -292,8 +294,9 @@ cmd_status cmd_cache_accept(const cmd_accept_args* args, void* cuda_stream);
  * number). They move to the row's first `budget` slots in their order, keys,
  * values and weights; the weights past them, up to n, become 0. lengths_out[r] =
  * budget, and pages past it are released (refs_out). Rows of at most budget
- * tokens stay as they are; so does a row where a page does not exist, or one of
- * those that it goes on with is held by others too (refs above 1) (reported).
+ * tokens stay as they are; so does a row whose length is beyond its table, where
+ * a page does not exist, or one of those that it goes on with is held by others
+ * too (refs above 1) (reported; lengths_out is then the length, held to the table).
  * Positions are no longer slots then: keys keep the rotation they were stored
  * with. All layers have the same sizes and element type; a model with more than
  * CMD_CACHE_MAX_LAYERS makes a call for each so many, with the same inputs.

@@ -139,7 +139,8 @@ __device__ __forceinline__ int accepted_length(const KeepParams& p, int row) {
 // ... and when it is held to the budget.
 __device__ __forceinline__ int evicted_length(const KeepParams& p, int row) {
   const int n = keep_length(p, row);
-  if (n <= p.budget) return n;
+  // (a length beyond the table names no tokens that are known to be the last ones: nothing is dropped by it)
+  if (n <= p.budget || p.lengths[row] != n) return n;
   const int to = pages_of(p, p.budget);
   bool ok = pages_usable(p, row, 0, to, true);
   ok = pages_usable(p, row, to, pages_of(p, n), false) && ok;

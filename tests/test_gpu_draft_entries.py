@@ -73,3 +73,21 @@ def test_entries_of_minus_one_are_reported(kernel):
         _check(*kernel[:1], [700, 130, 40], *kernel[1:6], where, lambda c: [-1], columns=kernel[6])
     _check(*kernel[:1], [700, 130, 40], *kernel[1:6], lambda j: j % 4 == 0, lambda c: [-1, c.pages], columns=kernel[6])
     _check(*kernel[:1], [700, 130, 40], *kernel[1:6], lambda j: False, lambda c: [-1], columns=kernel[6])
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("beyond", [1, 10 ** 6, None])
+def test_a_length_beyond_the_table_is_held_to_it(kernel, beyond):
+    kind, drafts, hq, hk, dim, page, columns = kernel
+    c = U.Cache(kind, [64 + drafts, 30 + drafts], hk, dim, page, columns=columns or None)
+    c.tables.clamp_(max=c.pages - 1)
+    most = c.tables.shape[1] * page
+    q, given, held = _randn(2, drafts, hq, dim, kind=kind), c.lengths.clone(), c.lengths.clone()
+    given[0], held[0] = 2 ** 31 - 1 if beyond is None else most + beyond, most
+    got = []
+    for lengths in (given, held):
+        status, weights = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(2, hk, most, device="cuda")
+        out, lse = T.attention_drafts(q, c.k, c.v, c.tables, lengths, weights=weights, return_lse=True, status=status)
+        assert int(status) == (T.cache.BAD_INDEX if lengths is given else 0)
+        got.append((out, lse, weights))
+    assert all(torch.equal(a, b) for a, b in zip(*got))

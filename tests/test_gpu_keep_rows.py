@@ -1,0 +1,37 @@
+"""What the accepted drafts' move and the eviction do with rows whose lengths, counts or pages are not as they should be, or only
+look so."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import cacheutil as U
+import draftutil as D
+import tensor_command_execution_gb300 as T
+
+pytestmark = pytest.mark.gpu
+
+
+def _i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def _status():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("length", [65, 10 ** 6, 2 ** 31 - 1])
+@pytest.mark.parametrize("budget,recent", [(30, 4), (0, 0), (63, 63)])
+def test_evict_leaves_a_row_longer_than_its_table_alone(length, budget, recent):
+    """Nothing of it is moved, zeroed or released; its length is held to the table's 64 tokens."""
+    c = U.Cache("bf16", [64, 64], 2, 32, 8)
+    w, lengths, refs = torch.rand(2, 2, 64, device="cuda"), c.lengths.clone(), D.counts(c)
+    lengths[1] = length
+    k, v, w2, status = c.k.clone(), c.v.clone(), w.clone(), _status()
+    got, out_refs = T.cache_evict(c.tables, lengths, refs, [(k, v, w2)], budget=budget, recent=recent, status=status)
+    assert int(status) == T.cache.BAD_INDEX and got.tolist() == [budget, 64]
+    page, slot = D.slots(c, 1, 64)
+    assert torch.equal(k[page, slot], c.k[page, slot]) and torch.equal(v[page, slot], c.v[page, slot]) and torch.equal(w2[1], w[1])
+    assert torch.equal(out_refs[page.unique()], refs[page.unique()])
+    assert int(out_refs.sum()) == 8 + -(-budget // 8)
