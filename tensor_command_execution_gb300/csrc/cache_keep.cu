@@ -87,7 +87,7 @@ __device__ __forceinline__ bool pages_usable(const KeepParams& p, int row, int f
     if (page < 0 || page >= p.pages) {
       report(p.status, CMD_CACHE_BAD_PAGE);
       ok = false;
-    } else if (shared && p.refs[page] != 1) {
+    } else if (shared && p.refs[page] > 1) {
       report(p.status, CMD_CACHE_SHARED_PAGE);
       ok = false;
     }

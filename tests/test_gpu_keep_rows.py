@@ -35,3 +35,32 @@ def test_evict_leaves_a_row_longer_than_its_table_alone(length, budget, recent):
     assert torch.equal(k[page, slot], c.k[page, slot]) and torch.equal(v[page, slot], c.v[page, slot]) and torch.equal(w2[1], w[1])
     assert torch.equal(out_refs[page.unique()], refs[page.unique()])
     assert int(out_refs.sum()) == 8 + -(-budget // 8)
+
+
+@pytest.mark.parametrize("count", [0, -1])
+def test_only_counts_above_one_say_that_others_hold_a_page(count):
+    """A caller that keeps no counts (or wrong ones) is not told of other holders."""
+    c = U.Cache("bf16", [26, 26], 2, 32, 8)
+    refs, status = D.counts(c), _status()
+    refs[c.tables[1, :4].long()] = count
+    path = _i32([[0, 2, 3, 5, -1, -1]] * 2)
+    k, v = c.k.clone(), c.v.clone()
+    got, out_refs = T.cache_accept(c.tables, c.lengths, refs, path, _i32([4, 4]), [k, v], status=status)
+    T.cache_status(status)
+    assert got.tolist() == [24, 24] and out_refs[c.tables[1, :3].long()].tolist() == [count] * 3
+    for r in range(2):
+        page, slot = D.slots(c, r, 26)
+        for x, y in ((k, c.k), (v, c.v)):
+            want = y[page, slot].clone()
+            want[20:24] = want[[20, 22, 23, 25]]
+            assert torch.equal(x[page, slot], want)
+    w = torch.rand(2, 2, 32, device="cuda")
+    k, v, mine = c.k.clone(), c.v.clone(), w.clone()
+    got, out_refs = T.cache_evict(c.tables, c.lengths, refs, [(k, v, mine)], budget=9, recent=2, status=status)
+    T.cache_status(status)
+    assert got.tolist() == [9, 9] and out_refs[c.tables[1, :2].long()].tolist() == [count] * 2
+    for r in range(2):
+        page, slot = D.slots(c, r, 26)
+        for h in range(2):
+            of = torch.tensor(D.evicted(w[r, h].tolist(), 26, 9, 2), device="cuda")
+            assert torch.equal(k[page[:9], slot[:9], h], c.k[page[of], slot[of], h]) and torch.equal(mine[r, h, :9], w[r, h, of])
