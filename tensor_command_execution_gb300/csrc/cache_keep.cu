@@ -77,21 +77,24 @@ __global__ void __launch_bounds__(kPathRows * 32) path_kernel(const __grid_const
 // ---- the plan ----------------------------------------------------------------------
 constexpr int kPlanThreads = 256;
 
-// Whether the row's pages [from, to) exist and only it holds them (`shared`
-// asks for the latter); every lane of a warp calls it.
-__device__ __forceinline__ bool pages_usable(const KeepParams& p, int row, int from, int to, bool shared) {
-  const int lane = threadIdx.x & 31;
-  bool ok = true;
-  for (int c = from + lane; c < to; c += 32) {
-    const int page = p.tables[row * p.table_st + c];
-    if (page < 0 || page >= p.pages) {
-      report(p.status, CMD_CACHE_BAD_PAGE);
-      ok = false;
-    } else if (shared && p.refs[page] > 1) {
-      report(p.status, CMD_CACHE_SHARED_PAGE);
-      ok = false;
-    }
+// Whether the page in column c of a row exists and only it holds it (`shared`
+// asks for the latter); what is wrong is reported.
+__device__ __forceinline__ bool page_usable(const KeepParams& p, int row, int c, bool shared) {
+  const int page = p.tables[row * p.table_st + c];
+  if (page < 0 || page >= p.pages) {
+    report(p.status, CMD_CACHE_BAD_PAGE);
+    return false;
   }
+  if (shared && p.refs[page] > 1) {
+    report(p.status, CMD_CACHE_SHARED_PAGE);
+    return false;
+  }
+  return true;
+}
+// ... all of columns [from, to); every lane of a warp calls it.
+__device__ __forceinline__ bool pages_usable(const KeepParams& p, int row, int from, int to, bool shared) {
+  bool ok = true;
+  for (int c = from + (int)(threadIdx.x & 31); c < to; c += 32) ok = page_usable(p, row, c, shared) && ok;
   return __all_sync(~0u, ok);
 }
 
@@ -115,25 +118,23 @@ __device__ __forceinline__ int accepted_length(const KeepParams& p, int row) {
   int count = p.counts[row];
   bool ok = count >= 0 && count <= p.drafts;
   if (!ok) count = 0;
-  bool moves = false;
-  int furthest = 0;
   for (int j = lane; j < count; j += 32) {
     const int of = path[j];
     ok = ok && of >= j && of < p.drafts && (j == 0 || path[j - 1] < of);
-    moves = moves || of != j;
-    furthest = max(furthest, of);
   }
   ok = __all_sync(~0u, ok);
   if (!ok) {
     report(p.status, CMD_CACHE_BAD_INDEX);
     return base;
   }
-  if (!__any_sync(~0u, moves)) return base + count;
-  furthest = __reduce_max_sync(~0u, furthest);
-  const int from = (int)fast_div32(p.page, (uint32_t)base), to = pages_of(p, base + count);
-  ok = pages_usable(p, row, from, to, true);
-  ok = pages_usable(p, row, to, pages_of(p, base + furthest + 1), false) && ok;
-  return ok ? base + count : base;
+  // the pages that the moves meet, and no others
+  for (int j = lane; j < count; j += 32) {
+    const int of = path[j];
+    if (of == j) continue;
+    ok = page_usable(p, row, (int)fast_div32(p.page, (uint32_t)(base + j)), true) && ok;
+    ok = page_usable(p, row, (int)fast_div32(p.page, (uint32_t)(base + of)), false) && ok;
+  }
+  return __all_sync(~0u, ok) ? base + count : base;
 }
 
 // ... and when it is held to the budget.

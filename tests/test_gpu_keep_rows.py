@@ -64,3 +64,30 @@ def test_only_counts_above_one_say_that_others_hold_a_page(count):
         for h in range(2):
             of = torch.tensor(D.evicted(w[r, h].tolist(), 26, 9, 2), device="cuda")
             assert torch.equal(k[page[:9], slot[:9], h], c.k[page[of], slot[of], h]) and torch.equal(mine[r, h, :9], w[r, h, of])
+
+
+def test_accept_asks_only_for_the_pages_that_its_moves_meet():
+    """Drafts that stay in their slots may lie in a page that another row holds too, and a page that no accepted draft comes
+    from or goes to need not exist."""
+    drafts, page = 10, 4  # drafts in slots 8 to 17: columns 2, 3 and 4
+    c = U.Cache("bf16", [18, 18, 18], 2, 32, page)
+    refs, tables, status = D.counts(c), c.tables.clone(), _status()
+    refs[tables[0, 2].long()] = 2
+    tables[1, 3] = -1
+    refs[tables[2, 3].long()] = 2  # (written to)
+    path = _i32([[0, 1, 2, 3, 5, 7, -1, -1, -1, -1], [0, 9] + [-1] * 8, [0, 1, 2, 3, 5] + [-1] * 5])
+    counts, moved = [6, 2, 5], [[0, 1, 2, 3, 5, 7], [0, 9], []]
+    k, v = c.k.clone(), c.v.clone()
+    got, out_refs = T.cache_accept(tables, c.lengths, refs, path, _i32(counts), [k, v], drafts=drafts, status=status)
+    # (the second row's missing page was to be released)
+    assert int(status) == T.cache.SHARED_PAGE | T.cache.BAD_PAGE
+    assert got.tolist() == [14, 10, 8]
+    for r in range(3):
+        at, slot = D.slots(c, r, 18)
+        there = torch.ones(18, dtype=torch.bool, device="cuda")
+        there[12:16] = r != 1
+        for x, y in ((k, c.k), (v, c.v)):
+            want = y[at, slot].clone()
+            want[8:8 + len(moved[r])] = want[[8 + i for i in moved[r]]]
+            assert torch.equal(x[at, slot][there], want[there])
+    assert out_refs[tables[0].long()].tolist() == [1, 1, 2, 1, 0]
