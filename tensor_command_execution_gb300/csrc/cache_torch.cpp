@@ -84,7 +84,14 @@ cmd_operand describe(const at::Tensor& t, const char* name) {
   return x;
 }
 cmd_operand operand(PyObject* o, const char* name) { return describe(tensor(o, name), name); }
-cmd_operand optional(PyObject* o, const char* name) { return o == Py_None ? cmd_operand{} : operand(o, name); }
+// An operand that may be absent. A tensor without elements has no address, but is not absent: it gets one (that nothing
+// reads), so that its sizes are checked.
+cmd_operand optional(PyObject* o, const char* name) {
+  if (o == Py_None) return cmd_operand{};
+  cmd_operand x = operand(o, name);
+  if (!x.ptr) x.ptr = reinterpret_cast<void*>(uintptr_t{256});
+  return x;
+}
 
 int32_t* status_word(PyObject* o) {
   if (o == Py_None) return nullptr;
@@ -222,7 +229,7 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     x.tables = operand(a[4], "tables");
     x.positions = operand(a[5], "positions");
     x.rows = optional(a[6], "rows");
-    x.q = optional(a[7], "q");
+    if (a[7] != Py_None) x.q = operand(a[7], "q");
     at::Tensor made;
     if (a[7] != Py_None) {
       const at::Tensor& q = THPVariable_Unpack(a[7]);
@@ -265,7 +272,7 @@ PyObject* py_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     c10::DataPtr workspace;
     x.out = a[8] == Py_None ? describe(out = w.empty(q.sizes(), q.scalar_type()), "out") : operand(a[8], "out");
     const bool with_lse = PyObject_IsTrue(a[10]);
-    if (a[9] != Py_None) x.lse = operand(a[9], "lse");
+    if (a[9] != Py_None) x.lse = optional(a[9], "lse");
     else if (with_lse) x.lse = describe(lse = w.empty({q.size(0), q.size(1)}, at::kFloat), "lse");
     const int64_t heads = x.q.sizes[1], kv = x.k_cache.sizes[2];
     if (a[11] != Py_None) {
@@ -439,7 +446,6 @@ PyObject* py_drafts(PyObject*, PyObject* const* a, Py_ssize_t n) {
     x.tables = operand(a[3], "tables");
     x.lengths = operand(a[4], "lengths");
     x.parents = optional(a[5], "parents");
-    if (a[5] != Py_None && !x.parents.ptr && x.q.rank == 4 && x.q.sizes[0] > 0) raise(PyExc_ValueError, "parents is empty");
     if (x.q.rank != 4 || x.k_cache.rank != 4 || x.tables.rank != 2)
       raise(PyExc_ValueError, "q and the caches have rank 4 and tables has rank 2");
     const int64_t dim = x.q.sizes[3];
@@ -451,7 +457,7 @@ PyObject* py_drafts(PyObject*, PyObject* const* a, Py_ssize_t n) {
     c10::DataPtr workspace;
     x.out = a[10] == Py_None ? describe(out = w.empty(q.sizes(), q.scalar_type()), "out") : operand(a[10], "out");
     const bool with_lse = PyObject_IsTrue(a[12]);
-    if (a[11] != Py_None) x.lse = operand(a[11], "lse");
+    if (a[11] != Py_None) x.lse = optional(a[11], "lse");
     else if (with_lse) x.lse = describe(lse = w.empty({q.size(0), q.size(1), q.size(2)}, at::kFloat), "lse");
     const int64_t drafts = x.q.sizes[1], heads = x.q.sizes[2], kv = x.k_cache.sizes[2];
     if (a[13] != Py_None) {
