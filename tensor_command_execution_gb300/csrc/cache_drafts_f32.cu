@@ -122,7 +122,8 @@ __device__ __forceinline__ void scores(float (&s)[R][N], const float* queries, c
 }
 
 // A tile's values, weighted, to R rows by 4 of every 64 dims (`dims` are left
-// from this thread's first). MASKED: weights of zero, whatever is weighted.
+// from this thread's first). MASKED: a weight of -1 says that the row does not
+// see the token, whatever its value (a weight of zero enters: times infinity).
 template <int DP, int R, int TOKENS, bool MASKED>
 __device__ __forceinline__ void add_values(float (&o)[R][DP / 64][4], const float* weights, const float* values, int dims) {
   constexpr int kPitch = DP + 4, kWeightPitch = kTile + 4;
@@ -140,7 +141,7 @@ __device__ __forceinline__ void add_values(float (&o)[R][DP / 64][4], const floa
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             const float x = w[r][e];
-            const bool none = MASKED && x == 0.0f;
+            const bool none = MASKED && x < 0.0f;
             o[r][j][0] = fmaf(x, none ? 0.0f : v.x, o[r][j][0]);
             o[r][j][1] = fmaf(x, none ? 0.0f : v.y, o[r][j][1]);
             o[r][j][2] = fmaf(x, none ? 0.0f : v.z, o[r][j][2]);
@@ -215,11 +216,13 @@ __global__ void __launch_bounds__((Shape<DP, R>::kThreads), (Shape<DP, R>::kCtas
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         float up = m[r];
+        bool hidden[N];
 #pragma unroll
         for (int e = 0; e < N; ++e) {
           const int t = set * kTokens + tx + 16 * e;
           float x = attend_score(p, s[r][e]);
-          if (masked && !((here >> t & 1) && s_tree.sees(p, draft[r], t0 + t, base))) x = -CUDART_INF_F;
+          hidden[e] = masked && !((here >> t & 1) && s_tree.sees(p, draft[r], t0 + t, base));
+          if (hidden[e]) x = -CUDART_INF_F;
           s[r][e] = x;
           up = fmaxf(up, x);
         }
@@ -238,7 +241,7 @@ __global__ void __launch_bounds__((Shape<DP, R>::kThreads), (Shape<DP, R>::kCtas
         for (int e = 0; e < N; ++e) {
           const float w = s[r][e] == -CUDART_INF_F ? 0.0f : exp2f(s[r][e] - m[r]);
           l[r] += w;
-          my_weights[r * S::kWeightPitch + tx + 16 * e] = w;
+          my_weights[r * S::kWeightPitch + tx + 16 * e] = hidden[e] ? -1.0f : w;
         }
       }
       __syncwarp();
