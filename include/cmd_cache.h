@@ -238,6 +238,9 @@ typedef struct cmd_drafts_args {
  * that is up to a GiB, which its scores are kept in: 4 bytes for each query head, token and row.) */
 cmd_status cmd_drafts_workspace(int64_t rows, int32_t drafts, int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t tokens,
                                 int64_t* bytes);
+/* ... for this very call, whose arguments are checked but for the workspace: no more than the above, and without room for
+ * scores where none are kept (32-bit caches, rows that are no whole 16-byte vectors, scores of more than a GiB). Host only. */
+cmd_status cmd_attention_drafts_workspace(const cmd_drafts_args* args, int64_t* bytes);
 cmd_status cmd_attention_drafts(const cmd_drafts_args* args, void* cuda_stream);
 
 /* ---- the accepted branch -------------------------------------------------------- */

@@ -114,6 +114,7 @@ SIGNATURES = {
     "cmd_cache_compact": (_I, [ctypes.POINTER(cmd_compact_args), _P]),
     "cmd_drafts_workspace": (_I, [_I64] + [_I32] * 4 + [_I64, ctypes.POINTER(_I64)]),
     "cmd_attention_drafts": (_I, [ctypes.POINTER(cmd_drafts_args), _P]),
+    "cmd_attention_drafts_workspace": (_I, [ctypes.POINTER(cmd_drafts_args), ctypes.POINTER(_I64)]),
     "cmd_draft_path": (_I, [ctypes.POINTER(cmd_path_args), _P]),
     "cmd_cache_accept": (_I, [ctypes.POINTER(cmd_accept_args), _P]),
     "cmd_evict_workspace": (_I, [_I64] + [_I32] * 3 + [ctypes.POINTER(_I64)]),
@@ -349,7 +350,7 @@ def attention_drafts(q, k_cache, v_cache, tables, lengths, *, parents=None, scal
     index; -1: the tokens before the drafts; less: padding); None: each goes on from the one before. A draft sees the
     tokens before the drafts, its ancestors and itself. weights [rows, kv_heads, tokens], float32: the attention that
     each token got is added to it. Returns out, or (out, lse) with return_lse. scale: dim ** -0.5 unless given.
-    workspace: cmd_drafts_workspace bytes (allocated where None)."""
+    workspace: at most cmd_drafts_workspace bytes (allocated where None)."""
     if stream is not None:
         with _On(stream, q, k_cache, v_cache, tables, lengths, parents, weights, out, lse, workspace, status):
             return attention_drafts(q, k_cache, v_cache, tables, lengths, parents=parents, scale=scale, softcap=softcap,

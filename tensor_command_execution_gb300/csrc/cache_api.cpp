@@ -878,10 +878,11 @@ int64_t score_bytes(int64_t rows, int64_t q_heads, int64_t tokens) {
   const __int128 n = (__int128)rows * q_heads * tokens * 4;
   return (int64_t)std::min<__int128>(n, kMostScores);
 }
-int64_t drafts_workspace(int64_t rows, int64_t drafts, int64_t q_heads, int64_t kv_heads, int64_t dim, int64_t tokens) {
+// tokens: 0 without weights; scores: they are kept
+int64_t drafts_workspace(int64_t rows, int64_t drafts, int64_t q_heads, int64_t kv_heads, int64_t dim, int64_t tokens, bool scores) {
   int64_t n = drafts_parts(drafts, q_heads, kv_heads, dim);
   if (tokens > 0) n += round_up(rows * drafts * q_heads * 8, 16);
-  if (tokens > 0 && drafts == 1) n += round_up(score_bytes(rows, q_heads, tokens), 16);
+  if (tokens > 0 && scores) n += round_up(score_bytes(rows, q_heads, tokens), 16);
   return n;
 }
 
@@ -912,12 +913,15 @@ extern "C" cmd_status cmd_drafts_workspace(int64_t rows, int32_t drafts, int32_t
     check_heads(q_heads);
     NEED((int64_t)drafts * q_heads <= kDraftHeads, CMD_ERR_LIMIT, "drafts times q_heads pass 2^20");
     NEED(dim >= 0 && dim <= CMD_CACHE_MAX_DIM, CMD_ERR_LIMIT, "a head dim above 256");
-    *bytes = drafts_workspace(rows, drafts, q_heads, kv_heads, dim, tokens);
+    *bytes = drafts_workspace(rows, drafts, q_heads, kv_heads, dim, tokens, drafts == 1);
     return CMD_OK;
   });
 }
 
-extern "C" cmd_status cmd_attention_drafts(const cmd_drafts_args* args, void* cuda_stream) {
+namespace {
+
+// cmd_attention_drafts, or (bytes given) the workspace that it would need.
+cmd_status drafts_call(const cmd_drafts_args* args, int64_t* bytes, void* cuda_stream) {
   return guarded([&]() -> cmd_status {
     NEED(args, CMD_ERR_NULL, "args is NULL");
     const cmd_drafts_args& a = *args;
@@ -969,8 +973,19 @@ extern "C" cmd_status cmd_attention_drafts(const cmd_drafts_args* args, void* cu
     NEED(std::isfinite(a.softcap) && a.softcap >= 0.0f, CMD_ERR_ARG, "softcap must be positive, or 0 for none");
     NEED(a.window >= 0, CMD_ERR_ARG, "window must be positive, or 0 for none");
     NEED(a.reserved == 0, CMD_ERR_ARG, "reserved must be 0");
+    if (bytes) *bytes = 0;
     if (rows == 0 || heads == 0) return CMD_OK;
-    check_workspace(a.workspace, a.workspace_bytes, drafts_workspace(rows, drafts, heads, kv, dim, has_weights ? tokens : 0));
+    const int es = elem_size(a.q.dtype);
+    const auto pieces = [&](int n) { return dim * es % n == 0 && vector_rows(a.k_cache, n) && vector_rows(a.v_cache, n); };
+    const int copy = pieces(16) ? 16 : pieces(4) ? 4 : 0;
+    const bool one = drafts == 1, vectors = copy == 16 && es == 2;
+    const bool kept = one && has_weights && tokens > 0 && vectors && (__int128)rows * heads * tokens * 4 <= kMostScores;
+    const int64_t need = drafts_workspace(rows, drafts, heads, kv, dim, has_weights ? tokens : 0, kept);
+    if (bytes) {
+      *bytes = need;
+      return CMD_OK;
+    }
+    check_workspace(a.workspace, a.workspace_bytes, need);
     cmdx::DraftParams p;
     std::memset(&p, 0, sizeof p);
     const int32_t per = (int32_t)(heads / kv);
@@ -1000,10 +1015,6 @@ extern "C" cmd_status cmd_attention_drafts(const cmd_drafts_args* args, void* cu
     p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kSplitBytes);
     float2* stats = has_weights ? reinterpret_cast<float2*>(static_cast<uint8_t*>(a.workspace) + drafts_parts(drafts, heads, kv, dim)) : nullptr;
     p.status = a.status;
-    const int es = elem_size(a.q.dtype);
-    const auto pieces = [&](int n) { return dim * es % n == 0 && vector_rows(a.k_cache, n) && vector_rows(a.v_cache, n); };
-    const int copy = pieces(16) ? 16 : pieces(4) ? 4 : 0;
-    const bool one = drafts == 1;
     // Many short rows of few queries take the warp-level instructions: a segment of the CTA-wide ones costs 7 us, however
     // short. 16-bit, 8 kv heads of 128 dims, rows of 1 to so many tokens, CTA-wide and warp-level:
     //   200 rows, 16 query rows to a kv head:  30 tokens 90 and 59 us, 120 90 and 67, 500 112 and 87
@@ -1012,8 +1023,7 @@ extern "C" cmd_status cmd_attention_drafts(const cmd_drafts_args* args, void* cu
     //   200 rows, 64 query rows:               30 tokens 97 and 130;   64 rows of 4096 tokens, 16 query rows 186 and 265
     const int64_t queries = kv > 0 ? drafts * (heads / kv) : 0;
     const auto few = [&](int64_t most16, int64_t most32) { return tokens <= (queries <= 16 ? most16 : queries <= 32 ? most32 : 0); };
-    const bool vectors = copy == 16 && es == 2, tc = !one && vectors && dim <= 128 && !few(1024, 256);
-    const bool kept = one && has_weights && tokens > 0 && vectors && (__int128)rows * heads * tokens * 4 <= kMostScores;
+    const bool tc = !one && vectors && dim <= 128 && !few(1024, 256);
     float* scores = kept ? reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(stats) + round_up(rows * heads * 8, 16)) : nullptr;
     p.scores_tokens = tokens;
     // The weights of those, with the attention: 200 rows, 16 query rows, 120 tokens 143 and 109 us, 500 175 and 151; 40 rows
@@ -1066,6 +1076,17 @@ extern "C" cmd_status cmd_attention_drafts(const cmd_drafts_args* args, void* cu
       if (e != cudaSuccess) return launched(e);
     }
     return CMD_OK;
+  });
+}
+
+}  // namespace
+
+extern "C" cmd_status cmd_attention_drafts(const cmd_drafts_args* args, void* cuda_stream) { return drafts_call(args, nullptr, cuda_stream); }
+
+extern "C" cmd_status cmd_attention_drafts_workspace(const cmd_drafts_args* args, int64_t* bytes) {
+  return guarded([&]() -> cmd_status {
+    NEED(bytes, CMD_ERR_NULL, "bytes is NULL");
+    return drafts_call(args, bytes, nullptr);
   });
 }
 

@@ -467,9 +467,13 @@ PyObject* py_drafts(PyObject*, PyObject* const* a, Py_ssize_t n) {
       x.workspace_bytes = (int64_t)t.nbytes();
     } else if (heads > 0 && kv > 0 && heads % kv == 0 && heads <= INT32_MAX && dim <= CMD_CACHE_MAX_DIM && drafts > 0 &&
                drafts <= CMD_CACHE_MAX_DRAFTS) {
-      check(cmd_drafts_workspace(x.q.sizes[0], (int32_t)drafts, (int32_t)heads, (int32_t)kv, (int32_t)dim,
-                                 x.weights.ptr ? x.tables.sizes[1] * x.k_cache.sizes[1] : 0, &x.workspace_bytes),
-            "cmd_drafts_workspace");
+      // (only one draft's weights need less for some types, strides and sizes than for others)
+      if (drafts == 1 && x.weights.ptr)
+        check(cmd_attention_drafts_workspace(&x, &x.workspace_bytes), "cmd_attention_drafts");
+      else
+        check(cmd_drafts_workspace(x.q.sizes[0], (int32_t)drafts, (int32_t)heads, (int32_t)kv, (int32_t)dim,
+                                   x.weights.ptr ? x.tables.sizes[1] * x.k_cache.sizes[1] : 0, &x.workspace_bytes),
+              "cmd_drafts_workspace");
       workspace = w.scratch(x.workspace_bytes);
       x.workspace = workspace.get();
     }
