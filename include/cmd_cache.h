@@ -73,7 +73,7 @@ extern "C" {
 #define CMD_CACHE_FULL_TABLE 4 /* a row would need more columns than its table has; dropped */
 #define CMD_CACHE_NO_PAGES 8  /* the pool had no free page left for a row; dropped */
 #define CMD_CACHE_SHARED_PAGE 16 /* tokens would move into a page that others hold too; left as they are */
-#define CMD_CACHE_TIMEOUT 32 /* a kernel's wait took too long (never expected): its outputs are not valid */
+#define CMD_CACHE_TIMEOUT 32 /* a kernel's wait took too long (never expected): its outputs are not valid, and NaN where it gave up */
 
 typedef struct cmd_operand {
   void* ptr; /* NULL: absent, where an operand is optional */

@@ -68,7 +68,7 @@ CPP_SOURCES = ["cmd_api.cpp", "cmd_yaml.cpp", "exec_host.cpp", "cache_api.cpp"]
 TORCH_SOURCE = "cache_torch.cpp"
 HEADERS = ["cmd_internal.h", "exec_common.cuh", "exec_pipe.cuh", "exec_tile2d.h", "interp_asm.cuh",
            "gen_interp.py", "cache_internal.h", "cache_common.cuh", "cache_attend.cuh",
-           "cache_attend_ring.cuh", "cache_drafts.cuh", "cache_mma.cuh", "cache_tc.cuh", "tcgen05.cuh"]
+           "cache_attend_ring.cuh", "cache_drafts.cuh", "cache_mma.cuh", "cache_tc.cuh", "cache_wait.cuh", "tcgen05.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -165,13 +165,19 @@ struct Loader {
   }
 
   __device__ __forceinline__ void run(const AttendRows& rows, const AttendShare& share, const AttendSegment& head) {
+    issue(rows, share, head);
+    // (none is on its way when the CTA ends)
+    for (uint32_t c = copies - min(copies - values, (uint32_t)S::kSlots); c < copies; c += 2)
+      wait_own(s.stop, smem_u32(&s.full[c % S::kSlots]), c / S::kSlots & 1);
+  }
+  __device__ __forceinline__ void issue(const AttendRows& rows, const AttendShare& share, const AttendSegment& head) {
     for (AttendSegment g = head; g.tiles; g = attend_next(p, rows, share, g, kTile)) {
       const int kv = attend_heads(p, g.group).kv, base = g.n - p.drafts;
       tiles.begin(g);
       for (int i = 0; i < g.tiles; ++i, copies += 2) {
         tiles.look<true>(i);
         const uint32_t at = copies % S::kSlots, slot = ring + at * S::kSlot, full = smem_u32(&s.full[at]);
-        wait(s.stop, smem_u32(&s.empty[at]), (copies / S::kSlots + 1) & 1);
+        if (!warp_wait(s.stop, smem_u32(&s.empty[at]), (copies / S::kSlots + 1) & 1)) return;
         if (!values) {
           if (tiles.lane < 4) s.here[copies / 2 % kHereTiles][tiles.lane] = tiles.here;
           __syncwarp();
@@ -181,7 +187,11 @@ struct Loader {
         const bool all = __all_sync(~0u, tiles.lane >= 4 || tiles.here == ~0u) && draft_all_seen(p, tiles.t0, tiles.t0 + kTile, base);
         tiles.copy(p.maps[1], kv, slot, all ? full : smem_u32(&s.landed));
         if (!all) {
-          wait(s.stop, smem_u32(&s.landed), cleared++ & 1);
+          const uint32_t turn = cleared++ & 1;
+          if (!warp_wait(s.stop, smem_u32(&s.landed), turn)) {
+            wait_own(s.stop, smem_u32(&s.landed), turn);
+            return;
+          }
           clear(slot);
           if (tiles.one) mbar_arrive(full);
         }
@@ -368,7 +378,7 @@ __device__ __forceinline__ void issue(const DraftParams& p, State& s, const Atte
     }
   }
   tcgen05_commit(one, smem_u32(&s.end));
-  wait(s.stop, smem_u32(&s.end), 0);
+  wait_own(s.stop, smem_u32(&s.end), 0);
 }
 
 // ---- the softmax --------------------------------------------------------------------
@@ -589,7 +599,7 @@ struct Softmax {
 
       const int mine = row + (WIDE ? w * kGroup : 0);
       const int draft = (int)fast_div32(p.per, (uint32_t)(q0 + min(mine, heads.heads - 1)));
-      const bool alive = mine < heads.heads, live = alive && !(planted && tree.from[draft] == kNever);
+      const bool alive = mine < heads.heads, live = alive && !(planted && tree.from[draft] == kNever), busy = __any_sync(~0u, alive);
       m = -CUDART_INF_F;
       l = 0.0f;
       bool any = false;
@@ -599,9 +609,10 @@ struct Softmax {
         wait(s.stop, smem_u32(&s.scores[w]), count & 1);
         const uint32_t* at = s.here[(tile + i) % kHereTiles];
         const uint32_t here[4] = {at[0], at[1], at[2], at[3]};
-        const bool all = draft_all_seen(p, t0, t0 + kTile, base), mask = !all || (here[0] & here[1] & here[2] & here[3]) != ~0u;
+        // (the whole warp's, also where a wait gave up and the words are being written)
+        const bool all = draft_all_seen(p, t0, t0 + kTile, base), mask = __any_sync(~0u, !all || (here[0] & here[1] & here[2] & here[3]) != ~0u);
         tcgen05_after_sync();
-        if (__any_sync(~0u, alive)) {
+        if (busy) {
           if (mask || p.cap_out != 0.0f) prepare(draft, t0, base, all, here);
           item(!any);
         }
@@ -612,7 +623,8 @@ struct Softmax {
         if (mask) {
           wait(s.stop, smem_u32(&s.done[w]), (count - 1) & 1);
           tcgen05_after_sync();
-          if (*static_cast<volatile uint32_t*>(&s.bad[(tile + i) % kHereTiles]) == (uint32_t)(tile + i) + 1) {
+          const bool bad = *static_cast<volatile uint32_t*>(&s.bad[(tile + i) % kHereTiles]) == (uint32_t)(tile + i) + 1;
+          if (__all_sync(~0u, bad && !gave_up(s.stop))) {
             add_infinite(g, heads.kv, draft, alive, t0, base, all, here);
             tcgen05_before_sync();  // (the next product comes after this thread's next arrival)
           }
@@ -620,6 +632,7 @@ struct Softmax {
       }
       if (any) wait(s.stop, smem_u32(&s.done[w]), (count - 1) & 1);
       tcgen05_after_sync();
+      if (gave_up(s.stop)) l = CUDART_NAN_F;
       tile += g.tiles;
 
       const int part_pitch = attend_pitch(p.dim);
@@ -662,7 +675,7 @@ struct Softmax {
         }
         scale = total == 0.0f ? 0.0f : 1.0f / total;
       }
-      if (__any_sync(~0u, alive)) {
+      if (busy) {
         const int half = WIDE ? DP : DP / 2, d0 = WIDE ? 0 : w * half;
         for (int d = d0; d < d0 + half && d < p.dim; d += 32) {
           float o[32];
@@ -685,9 +698,9 @@ struct Softmax {
               for (int e = 0; e < 32; ++e) o[e] += c[1] == 0.0f ? 0.0f : __uint_as_float(x[e]) * b;
             }
           }
-          if (total == 0.0f) {
+          if (!(total > 0.0f)) {  // (no token, or a wait gave up)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+            for (int e = 0; e < 32; ++e) o[e] = total;
           }
           if (alive) write(o, part, out, d);
         }

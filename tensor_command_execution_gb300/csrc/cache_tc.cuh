@@ -7,6 +7,7 @@
 #include <cstring>
 
 #include "cache_drafts.cuh"
+#include "cache_wait.cuh"
 #include "exec_pipe.cuh"
 #include "tcgen05.cuh"
 
@@ -14,8 +15,7 @@ namespace cmdx {
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // (exec_host.cpp)
 
-constexpr int kTcTile = 128;                // tokens
-constexpr uint64_t kPatience = 2000000000;  // ns: no wait takes longer
+constexpr int kTcTile = 128;  // tokens
 
 struct TcParams : DraftParams {
   CUtensorMap maps[2];  // keys, values: [page][kv head][slot][dim] (by TMA only)
@@ -52,22 +52,22 @@ inline cudaError_t pool_maps(int dtype, const DraftParams& d, TcParams* out) {
   return cudaSuccess;
 }
 
-// A wait that gives up (for the whole CTA, whose word it sets) after kPatience.
-// (The clock is read now and then only: a read takes about as long as a wait
-// should.)
-__device__ __forceinline__ void wait(uint32_t& stop_word, uint32_t bar, uint32_t parity) {
-  volatile uint32_t* stop = &stop_word;
-  uint64_t t0 = 0;
-  for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
-    if (n % 256) continue;
-    if (*stop) return;
-    const uint64_t now = global_ns();
-    if (t0 == 0) t0 = now;
-    if (now - t0 > kPatience) {
-      *stop = 1;
-      return;
-    }
-  }
+// Waits of a thread (cache_wait.cuh). One that gives up sets the CTA's word before
+// it does anything else. Whoever then goes on without what it waited for may tell
+// others that something is there which is not, but they hear of it after the word
+// was set: so a thread that finds the word clear after the last of its waits has
+// had all that its results rest on. (Going on keeps warps in step at their
+// barriers; who copies by TMA stops, since no barrier may be armed twice.)
+__device__ __forceinline__ bool wait(uint32_t& stop, uint32_t bar, uint32_t parity) {
+  return wait_until(&stop, [&] { return mbar_try_wait(bar, parity); }, [] { return global_ns(); });
+}
+__device__ __forceinline__ bool gave_up(const uint32_t& stop) { return *static_cast<const volatile uint32_t*>(&stop) != 0; }
+// ... of a whole warp, which is told one thing.
+__device__ __forceinline__ bool warp_wait(uint32_t& stop, uint32_t bar, uint32_t parity) { return __all_sync(~0u, wait(stop, bar, parity)); }
+// ... for what this warp has on its way, whatever the word says.
+__device__ __forceinline__ void wait_own(uint32_t& stop, uint32_t bar, uint32_t parity) {
+  wait_anyway(&stop, [&] { return mbar_try_wait(bar, parity); }, [] { return global_ns(); });
+  __syncwarp();
 }
 
 // What a warp needs to copy the tiles of a segment by TMA. Table entries are

@@ -56,17 +56,20 @@ __device__ __forceinline__ void copy_keys(const Params& p, State& s, uint32_t ri
   using S = Shape<DP>;
   TmaTiles tiles(p);
   uint32_t issued = 0;
-  for (AttendSegment g = attend_first(p, rows, share, kTile); g.tiles; g = attend_next(p, rows, share, g, kTile)) {
+  bool going = true;
+  for (AttendSegment g = attend_first(p, rows, share, kTile); g.tiles && going; g = attend_next(p, rows, share, g, kTile)) {
     tiles.begin(g);
     for (int i = 0; i < g.tiles; ++i, ++issued) {
       tiles.look<false>(i);  // (what is wrong has been reported by the attention)
       const uint32_t at = issued % S::kSlots;
-      wait(s.stop, smem_u32(&s.empty[at]), (issued / S::kSlots + 1) & 1);
+      if (!(going = warp_wait(s.stop, smem_u32(&s.empty[at]), (issued / S::kSlots + 1) & 1))) break;
       if (tiles.lane < 4) s.here[issued % kHereTiles][tiles.lane] = tiles.here;
       __syncwarp();
       tiles.copy(p.maps[0], g.group, ring + at * S::kSlot, smem_u32(&s.full[at]));
     }
   }
+  for (uint32_t c = issued - min(issued, (uint32_t)S::kSlots); c < issued; ++c)  // (none is on its way when the CTA ends)
+    wait_own(s.stop, smem_u32(&s.full[c % S::kSlots]), c / S::kSlots & 1);
 }
 
 template <class T, int DP>
@@ -100,7 +103,7 @@ __device__ __forceinline__ void issue(const Params& p, State& s, const AttendRow
     }
   }
   tcgen05_commit(one, smem_u32(&s.end));
-  wait(s.stop, smem_u32(&s.end), 0);
+  wait_own(s.stop, smem_u32(&s.end), 0);
 }
 
 // Scores that the cap changes, and those of query rows that do not see the
@@ -243,7 +246,11 @@ __device__ __forceinline__ void sums(const Params& p, State& s, DraftTree& tree,
       }
       tcgen05_before_sync();
       mbar_arrive(smem_u32(&s.taken[w]));
-      if (here >> (token % 32) & 1) weights[t] = before + sum;
+      if (gave_up(s.stop)) {  // (nor is what `here` says known to be the tile's)
+        if (t >= g.lo && t < g.n) weights[t] = CUDART_NAN_F;
+      } else if (here >> (token % 32) & 1) {
+        weights[t] = before + sum;
+      }
     }
   }
 }
