@@ -7,7 +7,7 @@
 // its warp. Products are binary32 multiply-adds: the tensor units would take a
 // 32-bit number as a sum of ones of 11 bits, whose products leave 2^-21 of a
 // score, and scores come to weights as powers. 12 rows of 13 drafts, up to 2999
-// tokens, window 1100, 16 heads of 80: 33 us of the call's 39 (its bytes: 5.5),
+// tokens, window 1100, 16 heads of 80: 33 us of the call's 40 (its bytes: 5.5),
 // bound by the latency between a tile's steps (issue slots 44%, 16 warps on an
 // SM: registers and stages are full).
 #include "cache_attend_ring.cuh"

@@ -1,8 +1,8 @@
 // cache_drafts_mma.cu - attention of drafted tokens over a paged cache of
 // 16-bit numbers on the warp-level tensor instructions: for heads of more than
-// 128 dims, whose scores and output do not fit tensor memory beside each other,
-// for rows that are not whole 16-byte vectors, and for few queries in short
-// tables (cmd_attention_drafts says which). cache_drafts_tc.cu has the others.
+// 128 dims (cache_drafts_tc.cu has no form for them), for rows that are not whole
+// 16-byte vectors, and for few queries in short tables (cmd_attention_drafts says
+// which). cache_drafts_tc.cu has the others.
 //
 // A tile of 64 tokens lies in shared memory, keys and values, the next one on
 // its way; a warp has 16 query rows by some of the tile's tokens, its scores and

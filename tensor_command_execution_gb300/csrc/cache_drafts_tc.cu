@@ -20,7 +20,7 @@
 // (rather than 2^15), which holds them to no finer than 2^-36 of the largest.
 //
 // Measured: 4 rows of 64 drafts, up to 16384 tokens, 64 query heads on 8 kv heads
-// of 128 dims (512 query rows to a kv head): 135 us with the join, 746 TFLOP/s of
+// of 128 dims (512 query rows to a kv head): 136 us with the join, 739 TFLOP/s of
 // the attention's products, and with the weights' second halves 1.5 times as many
 // on the tensor units, which are busy 56% of the time; the rest is a group's wait
 // for its turn at them and segments' beginnings. 16 rows of 24 drafts, 0 to 8192
